@@ -1,0 +1,334 @@
+// Product of two microscaled 4-bit matrices, C = bf16(ga·gb · A·Bᵀ), for sm_103a.
+//
+//   C[i,j] = bf16_rne( ga·gb · Σ_b SA[i,b]·SB[j,b] · Σ_{k in block b} A[i,k]·B[j,k] )
+//
+// with E2M1 codes, two per byte, and a scale per 32 (UE8M0, MXFP4) or 16
+// (E4M3, NVFP4) values of a row, laid out as fp4_quant.cuh describes. The
+// tensor core multiplies codes and scales itself (tcgen05.mma kind::mxf4 with
+// two scales, kind::mxf4nvf4 with four scales per row and 64 columns of K) and
+// sums in fp32; products of two codes and their scales are exact.
+//
+// A K stage is one 128-byte swizzle atom of codes (256 columns): four MMAs of
+// K = 64. Its scales are 2 (MXFP4) or 4 (NVFP4) tiles of 512 bytes per 128
+// rows, contiguous in memory: one untiled bulk copy into shared memory, then
+// tcgen05.cp into Tensor Memory, where tile q takes four columns.
+#pragma once
+
+#include <cuda.h>
+#include <cstdint>
+
+#include "bounded_wait.cuh"
+#include "fp4_quant.cuh"
+#include "ptx.cuh"
+
+namespace hk {
+namespace fp4 {
+
+constexpr int kStageCols = 256;        // K per stage
+constexpr int kMmaCols = 64;           // K per MMA
+constexpr int kMmasPerStage = kStageCols / kMmaCols;
+constexpr int kStageRowBytes = 128;    // codes of a row and stage
+constexpr int kSmemLimit = 232448;
+
+constexpr uint32_t kFlagDropArrive = 0x1u;
+
+// Scale tiles (512 bytes, 128 rows × 4 blocks) of 128 rows and one stage.
+__host__ __device__ constexpr int scale_tiles(int fmt) { return kStageCols / block_cols(fmt) / 4; }
+
+struct Fp4Params {
+    int32_t M, N;                      // rows of A (tokens) and of B (features)
+    int32_t k_stages;                  // ceil(K / 256)
+    int32_t tiles_m, tiles_n;
+    const uint8_t* sfa;                // scale tiles of A and B
+    const uint8_t* sfb;
+    const float* ga;                   // global scales, or null (1)
+    const float* gb;
+    uint16_t* c;
+    int64_t ldc;
+    int32_t vec_c;                     // C's rows are 16-byte aligned
+    uint32_t flags;
+    WaitCtx wait;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Instruction descriptor, kind::mxf4 and kind::mxf4nvf4: A and B in E2M1
+// (format code 1 in bits 7-9 and 10-11), both K-major, N >> 3 in bits 17-22,
+// scale type in bit 23 (1: UE8M0, 0: E4M3), M >> 7 in bits 27-28; the
+// scale-factor ids (bits 4-5 for B, 29-30 for A) are or-ed in per MMA.
+__host__ __device__ constexpr uint32_t idesc_fp4_f32(uint32_t m, uint32_t n, int fmt) {
+    return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((fmt == kMxfp4 ? 1u : 0u) << 23) | ((m >> 7) << 27);
+}
+
+// D[tmem] (+)= (A·sfa)[smem] · (B·sfb)[smem]ᵀ for one CTA or a CTA pair.
+template <int kCG, int kFmt>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    if constexpr (kCG == 1 && kFmt == kMxfp4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            : "memory");
+    else if constexpr (kCG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            : "memory");
+    else if constexpr (kFmt == kMxfp4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            : "memory");
+}
+
+// Which scale tile MMA k of a stage reads, and the scale-factor id inside it:
+// MXFP4 uses two of a tile's four blocks per MMA, NVFP4 all four.
+template <int kFmt> __device__ __forceinline__ constexpr uint32_t mma_scale_tile(int k) {
+    return kFmt == kMxfp4 ? static_cast<uint32_t>(k >> 1) : static_cast<uint32_t>(k);
+}
+template <int kFmt> __device__ __forceinline__ constexpr uint32_t mma_scale_id(int k) {
+    return kFmt == kMxfp4 ? static_cast<uint32_t>(k & 1) * 2u : 0u;
+}
+
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float global_alpha(const Fp4Params& p) {
+    return (p.ga != nullptr ? *p.ga : 1.0f) * (p.gb != nullptr ? *p.gb : 1.0f);
+}
+
+// ---------------------------------------------------- one-CTA tile kernel --
+//
+// For few tokens (rows of A): a tile is 128 features × kTok tokens and the
+// MMA's M side takes the features (rows of B), so that its N side need only be
+// as wide as the tokens are many. The tile's K range may be cut over the CTAs
+// of a cluster (one CTA per part); each leaves its fp32 sums in its shared
+// memory, and the CTAs then each add up and store a share of the tile's
+// tokens, in the order of the parts (the result does not depend on timing).
+// Two CTAs fit on an SM, so a tile's start and end overlap another's stream.
+template <int kTok, int kFmt>
+struct SingleGeometry {
+    static_assert(kTok == 16 || kTok == 32 || kTok == 64 || kTok == 128, "tokens per tile");
+    static constexpr int kTileF = 128;                                      // features per tile
+    static constexpr int kSfTiles = scale_tiles(kFmt);
+    static constexpr int kSfBytes = 512 * kSfTiles;                         // scales of one operand and stage
+    static constexpr int kWBytes = kTileF * kStageRowBytes;
+    static constexpr int kTBytes = kTok * kStageRowBytes;
+    static constexpr int kStageBytes = kWBytes + kTBytes + 2 * kSfBytes;
+    static constexpr int kBudget = 113 * 1024 - 2048;                       // two CTAs per SM
+    static constexpr int kSfCols = 8 * kSfTiles;                            // TMEM columns of a stage's scales
+    static constexpr int kFitSmem = kBudget / kStageBytes;
+    static constexpr int kFitTmem = (256 - kTok) / kSfCols;
+    static constexpr int kStages = kFitSmem < kFitTmem ? kFitSmem : kFitTmem;
+    static_assert(kStages >= 3, "pipeline too shallow");
+    static constexpr int kOffW = 0;
+    static constexpr int kOffT = kOffW + kStages * kWBytes;
+    static constexpr int kOffSf = kOffT + kStages * kTBytes;
+    static constexpr int kOffBars = kOffSf + kStages * 2 * kSfBytes;        // full[S], empty[S], acc
+    static constexpr int kOffHolder = kOffBars + (2 * kStages + 1) * 8;
+    static constexpr int kSmemBytes = kOffHolder + 16 + 1024;
+    static constexpr int kSumBytes = kTok * kTileF * 4;                     // fp32 sums, in the ring's place
+    static_assert(kSumBytes <= kOffBars, "the sums fit the ring");
+    static constexpr int kColSf = kTok;
+    static constexpr int kTmemCols = kColSf + kStages * kSfCols > 128 ? 256 : 128;
+    static constexpr uint32_t kIdesc = idesc_fp4_f32(kTileF, kTok, kFmt);
+    static constexpr int kThreads = 192;
+};
+
+template <int kTok, int kFmt>
+__global__ void __launch_bounds__(192, 2)
+gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                       const Fp4Params p, const int splits) {
+    using G = SingleGeometry<kTok, kFmt>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw);
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t lane = lane_id();
+    const int part = static_cast<int>(blockIdx.x) % splits;        // the CTA's rank in its cluster
+    const int tile = static_cast<int>(blockIdx.x) / splits;
+    const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
+    const int ks_begin = static_cast<int>(static_cast<int64_t>(part) * p.k_stages / splits);
+    const int ks_end = static_cast<int>(static_cast<int64_t>(part + 1) * p.k_stages / splits);
+
+    auto full_bar = [&](int s) { return base + G::kOffBars + 8u * s; };
+    auto empty_bar = [&](int s) { return base + G::kOffBars + 8u * (G::kStages + s); };
+    const uint32_t acc_bar = base + G::kOffBars + 8u * (2 * G::kStages);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(acc_bar, 1);
+        fence_mbar_init_cluster();
+    }
+    if (warp == 1) {
+        tmem_alloc_one(base + G::kOffHolder, G::kTmemCols);
+        tmem_relinquish_one();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + G::kOffHolder);
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint8_t* const sft = p.sfa + (static_cast<int64_t>(tm) * kTok / 128) * p.k_stages * G::kSfBytes;
+            const uint8_t* const sfw = p.sfb + static_cast<int64_t>(tn) * p.k_stages * G::kSfBytes;
+            int fills = 0, dropped = -1;
+            for (int ks = ks_begin; ks < ks_end; ++ks, ++fills) {
+                const int s = fills % G::kStages;
+                if (!wait_mbar(p.wait, empty_bar(s), ((fills / G::kStages) & 1) ^ 1u, kErrWaitRing)) {
+                    ok = false;
+                    break;
+                }
+                if ((p.flags & kFlagDropArrive) && fills == 0) {   // test only: this stage is never filled
+                    dropped = 0;
+                    continue;
+                }
+                mbar_arrive_expect_tx(full_bar(s), G::kStageBytes);
+                tma_load_2d(base + G::kOffW + s * G::kWBytes, &tmap_b, ks * kStageRowBytes, tn * G::kTileF, full_bar(s));
+                tma_load_2d(base + G::kOffT + s * G::kTBytes, &tmap_a, ks * kStageRowBytes, tm * kTok, full_bar(s));
+                const uint32_t sf = base + G::kOffSf + s * 2 * G::kSfBytes;
+                bulk_load(sf, sfw + static_cast<int64_t>(ks) * G::kSfBytes, G::kSfBytes, full_bar(s));
+                bulk_load(sf + G::kSfBytes, sft + static_cast<int64_t>(ks) * G::kSfBytes, G::kSfBytes, full_bar(s));
+            }
+            // abort: the copies in flight land before the CTA ends
+            if (!ok || wait_aborted(p.wait))
+                for (int f = fills > G::kStages ? fills - G::kStages : 0; f < fills; ++f)
+                    if (f != dropped) wait_mbar_drain(full_bar(f % G::kStages), (f / G::kStages) & 1);
+        }
+    } else if (warp == 1) {
+        int it = 0;
+        for (int ks = ks_begin; ks < ks_end; ++ks, ++it) {
+            const int s = it % G::kStages;
+            if (!wait_mbar(p.wait, full_bar(s), (it / G::kStages) & 1, kErrWaitData)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            if (lane == 0) {
+                const uint32_t sf = base + G::kOffSf + s * 2 * G::kSfBytes;
+                const uint32_t sf_tmem = tmem_base + G::kColSf + s * G::kSfCols;
+#pragma unroll
+                for (int q = 0; q < 2 * G::kSfTiles; ++q)
+                    tmem_cp_128x16b(sf_tmem + 4 * q, smem_desc_plain(sf + 512 * q, 16, 128));
+                const uint64_t wd = smem_desc_kmajor_sw128(base + G::kOffW + s * G::kWBytes);
+                const uint64_t td = smem_desc_kmajor_sw128(base + G::kOffT + s * G::kTBytes);
+#pragma unroll
+                for (int k = 0; k < kMmasPerStage; ++k) {
+                    const uint32_t id = mma_scale_id<kFmt>(k);
+                    const uint32_t col = 4 * mma_scale_tile<kFmt>(k);
+                    mma_fp4<1, kFmt>(tmem_base, wd + 2u * k, td + 2u * k, G::kIdesc | (id << 4) | (id << 29),
+                                     sf_tmem + col, sf_tmem + 4 * G::kSfTiles + col, (it > 0 || k > 0) ? 1u : 0u);
+                }
+                mma_commit_one(empty_bar(s));
+            }
+            __syncwarp();
+        }
+        // also on the abort path: everything issued completes before TMEM is freed
+        if (lane == 0) {
+            mma_commit_one(acc_bar);
+            if (!ok) wait_mbar_drain(acc_bar, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ epilogue --
+        ok = wait_mbar(p.wait, acc_bar, 0, kErrWaitAcc) && !wait_aborted(p.wait);
+        tc_fence_after_sync();
+        const uint32_t q = warp & 3u;
+        const int f_local = static_cast<int>(q * 32 + lane);
+        const int feature = tn * G::kTileF + f_local;
+        const uint32_t t_row = tmem_base + ((q * 32u) << 16);
+        const float alpha = global_alpha(p);
+        if (splits == 1) {
+#pragma unroll 1
+            for (int c = 0; c < kTok; c += 16) {
+                const int token0 = tm * kTok + c;
+                if (token0 >= p.M) break;
+                uint32_t v[16];
+                tmem_load_16cols(t_row + c, v);
+                tmem_wait_ld();
+                if (ok && feature < p.N) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (token0 + e < p.M)
+                            p.c[static_cast<int64_t>(token0 + e) * p.ldc + feature] =
+                                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[e]) * alpha));
+                }
+            }
+        } else {
+            // this part's sums: [token][feature] fp32 in the ring's place (every MMA has
+            // read its operands, and no copy is in flight)
+            float* const sums = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+            for (int c = 0; c < kTok; c += 16) {
+                uint32_t v[16];
+                tmem_load_16cols(t_row + c, v);
+                tmem_wait_ld();
+                if (ok) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sums[(c + e) * G::kTileF + f_local] = __uint_as_float(v[e]);
+                }
+            }
+        }
+        tc_fence_before_sync();
+    }
+    __syncwarp();
+    if (splits > 1) {
+        cluster_sync();
+        if (warp >= 2) {
+            const int f_local = static_cast<int>((warp & 3u) * 32 + lane);
+            const int feature = tn * G::kTileF + f_local;
+            const float alpha = global_alpha(p);
+            for (int t = part; t < kTok; t += splits) {
+                const int token = tm * kTok + t;
+                if (token >= p.M) break;
+                const uint32_t at = base + static_cast<uint32_t>(t * G::kTileF + f_local) * 4u;
+                float sum = 0.0f;
+                for (int r = 0; r < splits; ++r) sum += ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(r)));
+                if (ok && feature < p.N)
+                    p.c[static_cast<int64_t>(token) * p.ldc + feature] =
+                        __bfloat16_as_ushort(__float2bfloat16_rn(sum * alpha));
+            }
+        }
+        cluster_sync();    // no CTA leaves while another reads its sums
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_one(tmem_base, G::kTmemCols);
+    }
+}
+
+}  // namespace fp4
+}  // namespace hk

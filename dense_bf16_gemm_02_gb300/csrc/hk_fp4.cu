@@ -1,0 +1,307 @@
+// Host side of the microscaled 4-bit entry points (include/hk_gemm.h):
+// hk_fp4_quantize, hk_fp4_dequantize and hk_gemm_fp4: argument checks, tensor
+// maps, the choice of tile and K split, and the launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+#include <mutex>
+
+#include "../../include/hk_gemm.h"
+#include "fp4_gemm.cuh"
+#include "fp4_quant.cuh"
+#include "host_internal.h"
+
+namespace {
+
+using namespace hk::fp4;
+
+hk_status fail(hk_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+hk_status fail(hk_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return hk_host::set_error(s, buf);
+}
+
+hk_status cuda_fail(hk_status s, const char* what, cudaError_t e) {
+    return fail(s, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;   // 1 s per bounded wait
+constexpr int kMaxDevices = 64;
+constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+int type_bytes(int32_t t) { return t == HK_TYPE_FP32 ? 4 : 2; }
+
+hk_status check_format(int32_t format) {
+    if (format != HK_FP4_MXFP4 && format != HK_FP4_NVFP4) return fail(HK_ERR_INVALID_ARG, "unknown 4-bit format %d", (int)format);
+    return HK_OK;
+}
+
+// Sizes, codes and scales of one quantised matrix (pointers only when it has elements).
+hk_status check_matrix(const char* name, const void* codes, int64_t ld, const void* scales, int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return fail(HK_ERR_INVALID_ARG, "negative size");
+    if (rows > kLimit || cols > kLimit) return fail(HK_ERR_INVALID_ARG, "size of 2^31 or more");
+    if (rows == 0 || cols == 0) return HK_OK;
+    if (ld < ceil_div(cols, 32) * 16)
+        return fail(HK_ERR_INVALID_ARG, "%s: leading dimension %lld below the %lld bytes of a row's codes", name,
+                    (long long)ld, (long long)(ceil_div(cols, 32) * 16));
+    if (!codes || !scales) return fail(HK_ERR_INVALID_ARG, "%s: null pointer", name);
+    if (ld % 16 || !aligned(codes, 16) || !aligned(scales, 16))
+        return fail(HK_ERR_MISALIGNED, "%s: codes and scales must be 16-byte aligned, the leading dimension a multiple of 16", name);
+    return HK_OK;
+}
+
+hk_status current_device(int* device, int* sm_count) {
+    cudaError_t e = cudaGetDevice(device);
+    if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "cudaGetDevice", e);
+    if (*device < 0 || *device >= kMaxDevices) return fail(HK_ERR_INVALID_ARG, "device %d out of range", *device);
+    return hk_host::check_device(*device, sm_count);
+}
+
+// ------------------------------------------------ quantise and dequantise --
+
+// Warps of a block that share a row: a warp takes 1024 columns at a time, and
+// a narrow row leaves the block's other warps to other rows.
+int warps_per_row(int64_t cols) {
+    const int64_t spans = ceil_div(cols, kChunkCols * kSpanChunks);
+    int w = 1;
+    while (w < kQuantWarps && w < spans) w *= 2;
+    return w;
+}
+
+template <typename T, int kFmt>
+void launch_quantize(const void* x, int64_t rows, int64_t cols, int64_t ldx, void* codes, int64_t ld, void* scales,
+                     const float* g, cudaStream_t st) {
+    const int wpr = warps_per_row(cols);
+    const int64_t blocks = ceil_div(ceil_div(rows, 128) * 128, kQuantWarps / wpr);
+    const int64_t spans = ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr);
+    const int vec = aligned(x, 16) && (ldx * sizeof(T)) % 16 == 0;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20)),
+                    static_cast<unsigned>(std::min<int64_t>(spans, 4096)));
+    quantize_kernel<T, kFmt><<<grid, dim3(32, kQuantWarps), 0, st>>>(
+        static_cast<const T*>(x), rows, cols, ldx, static_cast<uint8_t*>(codes), ld, static_cast<uint8_t*>(scales), g, wpr, vec);
+}
+
+template <typename T, int kFmt>
+void launch_dequantize(const void* codes, int64_t ld, const void* scales, const float* g, int64_t rows, int64_t cols,
+                       void* y, int64_t ldy, cudaStream_t st) {
+    const int wpr = warps_per_row(cols);
+    const int64_t blocks = ceil_div(rows, kQuantWarps / wpr);
+    const int64_t spans = ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr);
+    const int vec = aligned(y, 16) && (ldy * sizeof(T)) % 16 == 0;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20)),
+                    static_cast<unsigned>(std::min<int64_t>(spans, 4096)));
+    dequantize_kernel<T, kFmt><<<grid, dim3(32, kQuantWarps), 0, st>>>(
+        static_cast<const uint8_t*>(codes), ld, static_cast<const uint8_t*>(scales), g, rows, cols, static_cast<T*>(y), ldy, wpr, vec);
+}
+
+// ------------------------------------------------------------- the product --
+
+using SingleFn = void (*)(CUtensorMap, CUtensorMap, Fp4Params, int);
+
+struct SingleVariant {
+    int tok;
+    SingleFn fn;
+    int smem, threads;
+};
+
+template <int kTok, int kFmt>
+constexpr SingleVariant single_variant() {
+    using G = SingleGeometry<kTok, kFmt>;
+    return {kTok, &gemm_fp4_single_kernel<kTok, kFmt>, G::kSmemBytes, G::kThreads};
+}
+
+const SingleVariant kSingle[2][4] = {
+    {single_variant<16, kMxfp4>(), single_variant<32, kMxfp4>(), single_variant<64, kMxfp4>(), single_variant<128, kMxfp4>()},
+    {single_variant<16, kNvfp4>(), single_variant<32, kNvfp4>(), single_variant<64, kNvfp4>(), single_variant<128, kNvfp4>()},
+};
+
+std::mutex g_setup_mutex;
+bool g_setup[kMaxDevices] = {};
+
+hk_status setup(int device) {
+    std::lock_guard<std::mutex> lock(g_setup_mutex);
+    if (g_setup[device]) return HK_OK;
+    for (const auto& row : kSingle)
+        for (const SingleVariant& v : row) {
+            cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(v.fn),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+            if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring a 4-bit product kernel", e);
+        }
+    g_setup[device] = true;
+    return HK_OK;
+}
+
+// Codes as rows of bytes in boxes of 128 bytes × box_rows, 128-byte swizzled;
+// rows and bytes past the matrix read as 0.
+hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, int64_t rows,
+                       int64_t cols, int64_t ld, uint32_t box_rows, const char* name) {
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(ceil_div(cols, 32) * 16), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(kStageRowBytes), box_rows};
+    cuuint32_t elem_strides[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, elem_strides,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of %s failed (CUresult %d)", name, (int)r);
+    return HK_OK;
+}
+
+// K parts of a tile: the most that keep the launch within one round of
+// resident CTAs (two per SM) and each part at least four stages long.
+int choose_splits(int64_t tiles, int64_t k_stages, int sm_count) {
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= 2 * int64_t(sm_count) && k_stages >= 4 * s * 2) s *= 2;
+    return s;
+}
+
+}  // namespace
+
+extern "C" size_t hk_fp4_scales_size(int64_t rows, int64_t cols, int32_t format) {
+    if (rows <= 0 || cols <= 0 || rows > kLimit || cols > kLimit ||
+        (format != HK_FP4_MXFP4 && format != HK_FP4_NVFP4))
+        return 0;
+    return static_cast<size_t>(ceil_div(rows, 128) * 128 * padded_blocks(cols, format));
+}
+
+extern "C" hk_status hk_fp4_quantize(const void* X, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx, void* codes,
+                                     int64_t ld_codes, void* scales, int32_t format, const float* global_scale,
+                                     void* stream) {
+    hk_status s = check_format(format);
+    if (s != HK_OK) return s;
+    if (x_type < HK_TYPE_BF16 || x_type > HK_TYPE_FP32) return fail(HK_ERR_INVALID_ARG, "unknown element type %d", (int)x_type);
+    if ((s = check_matrix("quantised matrix", codes, ld_codes, scales, rows, cols)) != HK_OK) return s;
+    if (ldx < cols) return fail(HK_ERR_INVALID_ARG, "leading dimension %lld below the %lld columns", (long long)ldx, (long long)cols);
+    if (format == HK_FP4_MXFP4 && global_scale) return fail(HK_ERR_INVALID_ARG, "MXFP4 has no global scale");
+    if (rows == 0 || cols == 0) return HK_OK;
+    if (!X) return fail(HK_ERR_INVALID_ARG, "null input pointer");
+    if (!aligned(X, type_bytes(x_type)) || !aligned(global_scale, 4)) return fail(HK_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    int device = 0, sms = 0;
+    if ((s = current_device(&device, &sms)) != HK_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool nv = format == HK_FP4_NVFP4;
+    auto go = [&](auto mx_fn, auto nv_fn) { (nv ? nv_fn : mx_fn)(X, rows, cols, ldx, codes, ld_codes, scales, global_scale, st); };
+    switch (x_type) {
+        case HK_TYPE_BF16: go(&launch_quantize<__nv_bfloat16, kMxfp4>, &launch_quantize<__nv_bfloat16, kNvfp4>); break;
+        case HK_TYPE_FP16: go(&launch_quantize<__half, kMxfp4>, &launch_quantize<__half, kNvfp4>); break;
+        default: go(&launch_quantize<float, kMxfp4>, &launch_quantize<float, kNvfp4>); break;
+    }
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the quantisation", e);
+}
+
+extern "C" hk_status hk_fp4_dequantize(const void* codes, int64_t ld_codes, const void* scales, int32_t format,
+                                       const float* global_scale, int64_t rows, int64_t cols, void* Y, int32_t y_type,
+                                       int64_t ldy, void* stream) {
+    hk_status s = check_format(format);
+    if (s != HK_OK) return s;
+    if (y_type < HK_TYPE_BF16 || y_type > HK_TYPE_FP32) return fail(HK_ERR_INVALID_ARG, "unknown element type %d", (int)y_type);
+    if ((s = check_matrix("quantised matrix", codes, ld_codes, scales, rows, cols)) != HK_OK) return s;
+    if (ldy < cols) return fail(HK_ERR_INVALID_ARG, "leading dimension %lld below the %lld columns", (long long)ldy, (long long)cols);
+    if (format == HK_FP4_MXFP4 && global_scale) return fail(HK_ERR_INVALID_ARG, "MXFP4 has no global scale");
+    if (rows == 0 || cols == 0) return HK_OK;
+    if (!Y) return fail(HK_ERR_INVALID_ARG, "null output pointer");
+    if (!aligned(Y, type_bytes(y_type)) || !aligned(global_scale, 4)) return fail(HK_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    int device = 0, sms = 0;
+    if ((s = current_device(&device, &sms)) != HK_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool nv = format == HK_FP4_NVFP4;
+    auto go = [&](auto mx_fn, auto nv_fn) { (nv ? nv_fn : mx_fn)(codes, ld_codes, scales, global_scale, rows, cols, Y, ldy, st); };
+    switch (y_type) {
+        case HK_TYPE_BF16: go(&launch_dequantize<__nv_bfloat16, kMxfp4>, &launch_dequantize<__nv_bfloat16, kNvfp4>); break;
+        case HK_TYPE_FP16: go(&launch_dequantize<__half, kMxfp4>, &launch_dequantize<__half, kNvfp4>); break;
+        default: go(&launch_dequantize<float, kMxfp4>, &launch_dequantize<float, kNvfp4>); break;
+    }
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the dequantisation", e);
+}
+
+extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* B, const void* SFB, void* C, int64_t M,
+                                    int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc, int32_t format,
+                                    const float* global_a, const float* global_b, uint32_t flags, uint64_t timeout_ns,
+                                    void* stream) {
+    hk_status s = check_format(format);
+    if (s != HK_OK) return s;
+    if (flags & ~HK_FLAG_FAULT_DROP_ARRIVE) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if (M < 0 || N < 0 || K < 0) return fail(HK_ERR_INVALID_ARG, "negative size");
+    if (ldc < N) return fail(HK_ERR_INVALID_ARG, "leading dimension of C below N");
+    if (M == 0 || N == 0) return HK_OK;
+    if ((s = check_matrix("A", A, lda, SFA, M, K)) != HK_OK) return s;
+    if ((s = check_matrix("B", B, ldb, SFB, N, K)) != HK_OK) return s;
+    if (format == HK_FP4_MXFP4 && (global_a || global_b)) return fail(HK_ERR_INVALID_ARG, "MXFP4 has no global scale");
+    if (!C) return fail(HK_ERR_INVALID_ARG, "null output pointer");
+    if (!aligned(C, 2) || !aligned(global_a, 4) || !aligned(global_b, 4))
+        return fail(HK_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    if (ceil_div(M, 16) * ceil_div(N, 128) > (int64_t(1) << 26)) return fail(HK_ERR_INVALID_ARG, "too many output tiles");
+    int device = 0, sms = 0;
+    if ((s = current_device(&device, &sms)) != HK_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (K == 0) {
+        e = cudaMemset2DAsync(C, static_cast<size_t>(ldc) * 2, 0, static_cast<size_t>(N) * 2, static_cast<size_t>(M), st);
+        return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "clearing C", e);
+    }
+    if ((s = setup(device)) != HK_OK) return s;
+    uint32_t* status = nullptr;
+    if ((s = hk_host::status_word(device, &status)) != HK_OK) return s;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    if ((s = hk_host::tensor_map_encoder(&enc)) != HK_OK) return s;
+
+    Fp4Params p = {};
+    p.M = static_cast<int32_t>(M);
+    p.N = static_cast<int32_t>(N);
+    p.k_stages = static_cast<int32_t>(ceil_div(K, kStageCols));
+    p.sfa = static_cast<const uint8_t*>(SFA);
+    p.sfb = static_cast<const uint8_t*>(SFB);
+    p.ga = global_a;
+    p.gb = global_b;
+    p.c = static_cast<uint16_t*>(C);
+    p.ldc = ldc;
+    p.vec_c = aligned(C, 16) && ldc % 8 == 0;
+    p.flags = flags;
+    p.wait.status = status;
+    p.wait.launch_id = hk_host::next_launch_id();
+    p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
+
+    // the narrowest tile that holds every token: the MMA's time and a stage's shared memory grow with it
+    const SingleVariant* v = &kSingle[format == HK_FP4_NVFP4][3];
+    for (int i = 2; i >= 0; --i)
+        if (M <= kSingle[format == HK_FP4_NVFP4][i].tok) v = &kSingle[format == HK_FP4_NVFP4][i];
+    p.tiles_m = static_cast<int32_t>(ceil_div(M, v->tok));
+    p.tiles_n = static_cast<int32_t>(ceil_div(N, 128));
+    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
+    const int splits = choose_splits(tiles, p.k_stages, sms);
+    CUtensorMap ta, tb;
+    if ((s = encode_codes(enc, &ta, A, M, K, lda, static_cast<uint32_t>(v->tok), "A")) != HK_OK) return s;
+    if ((s = encode_codes(enc, &tb, B, N, K, ldb, 128, "B")) != HK_OK) return s;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+    cfg.blockDim = dim3(static_cast<unsigned>(v->threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(v->smem);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, v->fn, ta, tb, p, splits);
+    return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the 4-bit product", e);
+}
+
+extern "C" hk_status hk_gemm_fp4(const void* A, const void* SFA, const void* B, const void* SFB, void* C, int64_t M,
+                                 int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc, int32_t format,
+                                 const float* global_a, const float* global_b, void* stream) {
+    return hk_gemm_fp4_ex(A, SFA, B, SFB, C, M, N, K, lda, ldb, ldc, format, global_a, global_b, 0u, 0u, stream);
+}

@@ -42,6 +42,13 @@ HK_ACT_SILU = 3
 HK_INPUT_BF16 = 0
 HK_INPUT_E4M3 = 1
 
+HK_FP4_MXFP4 = 0
+HK_FP4_NVFP4 = 1
+
+HK_TYPE_BF16 = 0
+HK_TYPE_FP16 = 1
+HK_TYPE_FP32 = 2
+
 HK_FLAG_NONE = 0x0
 HK_FLAG_FAULT_DROP_ARRIVE = 0x1
 HK_FLAG_NO_TAIL_SPLIT = 0x2
@@ -53,6 +60,7 @@ EXPORTED = (
     "hk_gemm_bf16_epilogue", "hk_gemm_plan_run_epilogue", "hk_gemm_bf16_fused", "hk_gemm_plan_run_fused",
     "hk_gemm_fp8_e4m3",
     "hk_attention_fwd", "hk_attention_fwd_ex", "hk_gemm_mxfp8", "hk_gemm_mxfp8_ex", "hk_gemm_mxfp8_workspace_size",
+    "hk_fp4_scales_size", "hk_fp4_quantize", "hk_fp4_dequantize", "hk_gemm_fp4", "hk_gemm_fp4_ex",
 )
 
 
@@ -145,6 +153,17 @@ def load() -> ctypes.CDLL:
         lib.hk_attention_fwd_ex.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I32, ctypes.c_uint32,
                                             ctypes.c_uint64, P]
         lib.hk_attention_fwd_ex.restype = I32
+        U32, U64, SZ = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t
+        lib.hk_fp4_scales_size.argtypes = [I64, I64, I32]
+        lib.hk_fp4_scales_size.restype = SZ
+        lib.hk_fp4_quantize.argtypes = [P, I32, I64, I64, I64, P, I64, P, I32, P, P]
+        lib.hk_fp4_quantize.restype = I32
+        lib.hk_fp4_dequantize.argtypes = [P, I64, P, I32, P, I64, I64, P, I32, I64, P]
+        lib.hk_fp4_dequantize.restype = I32
+        lib.hk_gemm_fp4.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, P, P]
+        lib.hk_gemm_fp4.restype = I32
+        lib.hk_gemm_fp4_ex.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, P, U32, U64, P]
+        lib.hk_gemm_fp4_ex.restype = I32
         _lib = lib
         return lib
 
@@ -209,6 +228,38 @@ def hk_attention_fwd_ex(Q: int, K: int, V: int, O: int, lse: int, B: int, Hq: in
                         causal: int = 0, flags: int = 0, timeout_ns: int = 0, stream: int = 0) -> int:
     return load().hk_attention_fwd_ex(Q, K, V, O, lse or None, B, Hq, Hkv, S, D, int(causal), flags,
                                       timeout_ns, stream)
+
+
+def hk_fp4_scales_size(rows: int, cols: int, format: int) -> int:
+    return int(load().hk_fp4_scales_size(rows, cols, format))
+
+
+def hk_fp4_quantize(X: int, x_type: int, rows: int, cols: int, ldx: int, codes: int, ld_codes: int, scales: int,
+                    format: int, global_scale: int = 0, stream: int = 0) -> int:
+    """X (rows × cols) to E2M1 codes (ld_codes bytes a row) and tiled block scales."""
+    return load().hk_fp4_quantize(X, x_type, rows, cols, ldx, codes, ld_codes, scales, format, global_scale or None,
+                                  stream)
+
+
+def hk_fp4_dequantize(codes: int, ld_codes: int, scales: int, format: int, global_scale: int, rows: int, cols: int,
+                      Y: int, y_type: int, ldy: int, stream: int = 0) -> int:
+    """The values of a quantised matrix, rounded to y_type."""
+    return load().hk_fp4_dequantize(codes, ld_codes, scales, format, global_scale or None, rows, cols, Y, y_type, ldy,
+                                    stream)
+
+
+def hk_gemm_fp4(A: int, SFA: int, B: int, SFB: int, C: int, M: int, N: int, K: int, lda: int, ldb: int, ldc: int,
+                format: int, global_a: int = 0, global_b: int = 0, stream: int = 0) -> int:
+    """C (bf16) = A·Bᵀ of two quantised matrices A (M×K) and B (N×K) (lda, ldb in bytes)."""
+    return load().hk_gemm_fp4(A, SFA, B, SFB, C, M, N, K, lda, ldb, ldc, format, global_a or None, global_b or None,
+                              stream)
+
+
+def hk_gemm_fp4_ex(A: int, SFA: int, B: int, SFB: int, C: int, M: int, N: int, K: int, lda: int, ldb: int, ldc: int,
+                   format: int, global_a: int = 0, global_b: int = 0, flags: int = 0, timeout_ns: int = 0,
+                   stream: int = 0) -> int:
+    return load().hk_gemm_fp4_ex(A, SFA, B, SFB, C, M, N, K, lda, ldb, ldc, format, global_a or None,
+                                 global_b or None, flags, timeout_ns, stream)
 
 
 def hk_gemm_last_device_status(device: int) -> int:

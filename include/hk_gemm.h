@@ -279,7 +279,7 @@ hk_status hk_gemm_plan_device_status(hk_gemm_plan* plan);
 
 /* The same for the calls of the one-shot entry points (hk_gemm_bf16,
  * hk_gemm_bf16_epilogue, hk_gemm_bf16_fused, hk_gemm_fp8_e4m3, hk_gemm_mxfp8(_ex),
- * hk_attention_fwd(_ex), hk_gemm_bf16_noalloc) on `device`. */
+ * hk_attention_fwd(_ex), hk_gemm_bf16_noalloc, hk_gemm_fp4(_ex)) on `device`. */
 hk_status hk_gemm_last_device_status(int device);
 
 void hk_gemm_plan_destroy(hk_gemm_plan* plan);
@@ -346,6 +346,81 @@ hk_status hk_attention_fwd(const void* Q, const void* K, const void* V, void* O,
 hk_status hk_attention_fwd_ex(const void* Q, const void* K, const void* V, void* O, float* lse,
                               int64_t B, int64_t Hq, int64_t Hkv, int64_t S, int64_t D,
                               int32_t causal, uint32_t flags, uint64_t timeout_ns, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4, NVFP4): quantisation and product.
+ *
+ * Values are E2M1 codes (1 sign, 2 exponent, 1 fraction bit; magnitudes 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6), with one scale per block of a row's columns:
+ *
+ *   HK_FP4_MXFP4  blocks of 32; scale 2^E, kept as the UE8M0 byte E + 127 (255:
+ *                 NaN), E = floor(log2 amax) - 2 of the block's largest magnitude
+ *                 (at least -127; 0 for a block of zeros: byte 0);
+ *                 code = e2m1(x / 2^E).
+ *   HK_FP4_NVFP4  blocks of 16; scale s in E4M3, s = e4m3(amax / (6·g)) with a
+ *                 global scale g > 0 of the whole matrix (one float in DEVICE
+ *                 memory, NULL: 1); code = e2m1(x · (1 / (s·g))); a value is
+ *                 code · s · g. g = amax of the matrix / 2688 uses the whole range.
+ *
+ * e2m1 and e4m3 round to nearest, halves to even; magnitudes above the
+ * largest become the largest (6 and 448). A block with a NaN or an infinity
+ * gets a NaN scale (255, 0x7F) and codes 0: its values are NaN.
+ *
+ * A quantised matrix of rows × cols is two device arrays, 16-byte aligned:
+ *   codes   two per byte, the even column in the low half; rows of `ld` BYTES, a
+ *           multiple of 16 and at least ceil(cols / 32) · 16; columns past the
+ *           matrix up to the next multiple of 32 hold code 0;
+ *   scales  hk_fp4_scales_size bytes in tiles of 128 rows × 4 blocks (512
+ *           bytes), row groups outermost: the scale of row r, block b is at
+ *             ((r / 128) · (nb / 4) + b / 4) · 512 + (r % 32) · 16 + (r % 128 / 32) · 4 + b % 4
+ *           with nb the blocks of a row padded to whole 256-column chunks
+ *           (nb = ceil(cols / 256) · 8 or · 16). Blocks past the matrix hold 0.
+ * hk_fp4_quantize writes both, padding included; the product reads them as
+ * they are (nothing is rearranged at call time). */
+#define HK_FP4_MXFP4 0
+#define HK_FP4_NVFP4 1
+
+/* Element types of the arrays that quantisation reads and writes. */
+#define HK_TYPE_BF16 0
+#define HK_TYPE_FP16 1
+#define HK_TYPE_FP32 2
+
+/* Bytes of the scales of a rows × cols matrix (0 for an empty one or an unknown format). */
+size_t hk_fp4_scales_size(int64_t rows, int64_t cols, int32_t format);
+
+/* Quantise X (rows × cols, row-major, element type x_type, leading dimension
+ * ldx in elements, any alignment of its element type; 16-byte aligned rows are
+ * read in 16-byte pieces). `global_scale` is NULL for MXFP4. rows or cols 0:
+ * HK_OK, nothing written. Asynchronous on `stream`, allocates nothing. */
+hk_status hk_fp4_quantize(const void* X, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
+                          void* codes, int64_t ld_codes, void* scales, int32_t format,
+                          const float* global_scale, void* stream);
+
+/* The values of a quantised matrix, code · (scale · g), rounded once to y_type. */
+hk_status hk_fp4_dequantize(const void* codes, int64_t ld_codes, const void* scales, int32_t format,
+                            const float* global_scale, int64_t rows, int64_t cols,
+                            void* Y, int32_t y_type, int64_t ldy, void* stream);
+
+/* Product of two quantised matrices of one format:
+ *     C[i,j] = bf16_rne( ga·gb · Σ_b SA[i,b]·SB[j,b] · Σ_{k in block b} A[i,k]·B[j,k] )
+ * A (M × K) and B (N × K) as above, lda and ldb in BYTES; C is M × N bf16,
+ * row-major, ldc ≥ N in elements, any 2-byte alignment. global_a and global_b
+ * are the operands' global scales (device memory, NULL: 1; NULL for MXFP4).
+ * The products run on the tensor cores with fp32 sums (tcgen05.mma kind::mxf4
+ * and kind::mxf4nvf4); a NaN scale gives NaN in its row or column of C. K = 0
+ * fills C with +0. Asynchronous on `stream`, needs no workspace; a bounded
+ * wait that runs out is reported by hk_gemm_last_device_status. */
+hk_status hk_gemm_fp4(const void* A, const void* SFA, const void* B, const void* SFB, void* C,
+                      int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
+                      int32_t format, const float* global_a, const float* global_b, void* stream);
+
+/* The same with test controls: `flags` takes HK_FLAG_FAULT_DROP_ARRIVE (the
+ * first stage is never filled, so a bounded wait runs out), `timeout_ns`
+ * bounds each wait (0: 1 s). */
+hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* B, const void* SFB, void* C,
+                         int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
+                         int32_t format, const float* global_a, const float* global_b,
+                         uint32_t flags, uint64_t timeout_ns, void* stream);
 
 /* Static description of a status code. */
 const char* hk_status_string(hk_status status);
