@@ -13,8 +13,9 @@ from .hk_gemm import (HK_ACT_GELU, HK_ACT_NONE, HK_ACT_RELU, HK_ACT_SILU, HK_ERR
                       hk_gemm_bf16_noalloc, hk_gemm_fp8_e4m3, hk_gemm_last_device_status, hk_gemm_last_error_string,
                       hk_gemm_mxfp8, hk_gemm_mxfp8_ex, hk_gemm_mxfp8_workspace_size, hk_status_string, load,
                       HK_FP4_MXFP4, HK_FP4_NVFP4, HK_TYPE_BF16, HK_TYPE_FP16, HK_TYPE_FP32, hk_fp4_dequantize,
-                      hk_fp4_quantize, hk_fp4_scales_size, hk_gemm_fp4, hk_gemm_fp4_ex)
-from .low_precision import Fp4Matrix, dequantize_fp4, gemm_fp4, quantize_fp4
+                      hk_attention_kv8, hk_attention_kv8_workspace_size, hk_fp4_quantize, hk_fp4_scales_size,
+                      hk_gemm_fp4, hk_gemm_fp4_ex, hk_kv8_append, hk_kv8_cache)
+from .low_precision import (Fp4Matrix, Kv8Cache, attention_kv8, dequantize_fp4, gemm_fp4, kv8_append, quantize_fp4)
 
 __all__ = ["attention", "gemm", "Plan", "HKError", "load",
            "hk_gemm_bf16", "hk_gemm_bf16_epilogue", "hk_gemm_bf16_fused", "hk_gemm_bf16_noalloc", "hk_gemm_fp8_e4m3",
@@ -23,6 +24,7 @@ __all__ = ["attention", "gemm", "Plan", "HKError", "load",
            "HK_ACT_NONE", "HK_ACT_RELU", "HK_ACT_GELU", "HK_ACT_SILU", "HK_INPUT_BF16", "HK_INPUT_E4M3",
            "HK_OK", "HK_ERR_INVALID_ARG", "HK_ERR_MISALIGNED", "HK_ERR_TIMEOUT", "HK_ERR_WORKSPACE",
            "HK_ERR_UNSUPPORTED_DEVICE", "HK_FLAG_FAULT_DROP_ARRIVE", "HK_FLAG_NO_TAIL_SPLIT",
-           "Fp4Matrix", "quantize_fp4", "dequantize_fp4", "gemm_fp4",
+           "Fp4Matrix", "quantize_fp4", "dequantize_fp4", "gemm_fp4", "Kv8Cache", "kv8_append", "attention_kv8",
+           "hk_kv8_cache", "hk_kv8_append", "hk_attention_kv8", "hk_attention_kv8_workspace_size",
            "hk_fp4_quantize", "hk_fp4_dequantize", "hk_fp4_scales_size", "hk_gemm_fp4", "hk_gemm_fp4_ex",
            "HK_FP4_MXFP4", "HK_FP4_NVFP4", "HK_TYPE_BF16", "HK_TYPE_FP16", "HK_TYPE_FP32"]

@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libhk_gemm.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("hk_gemm.cu", "hk_attention.cu", "hk_fp4.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("hk_gemm.cu", "hk_attention.cu", "hk_fp4.cu", "hk_kv8.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "hk_gemm.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

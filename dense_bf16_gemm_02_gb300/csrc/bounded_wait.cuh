@@ -25,7 +25,7 @@ __device__ __forceinline__ bool wait_aborted(WaitCtx c) {
     return *reinterpret_cast<volatile uint32_t*>(c.status + 1) == c.launch_id;
 }
 
-__device__ __noinline__ bool wait_mbar_slow(WaitCtx c, uint32_t bar, uint32_t parity, uint32_t code) {
+static __device__ __noinline__ bool wait_mbar_slow(WaitCtx c, uint32_t bar, uint32_t parity, uint32_t code) {
     const uint64_t t0 = global_timer_ns();
     for (;;) {
         if (mbar_try_wait_suspend(bar, parity, 20000)) return true;

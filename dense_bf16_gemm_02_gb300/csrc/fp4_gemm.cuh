@@ -230,7 +230,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
         int it = 0;
         for (int ks = ks_begin; ks < ks_end; ++ks, ++it) {
             const int s = it % G::kStages;
-            if (!wait_mbar(p.wait, full_bar(s), (it / G::kStages) & 1, kErrWaitData)) {
+            if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(s), (it / G::kStages) & 1, kErrWaitData))) {
                 ok = false;
                 break;
             }
@@ -262,7 +262,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue --
-        ok = wait_mbar(p.wait, acc_bar, 0, kErrWaitAcc) && !wait_aborted(p.wait);
+        ok = __all_sync(0xffffffffu, wait_mbar(p.wait, acc_bar, 0, kErrWaitAcc) && !wait_aborted(p.wait));
         tc_fence_after_sync();
         const uint32_t q = warp & 3u;
         const int f_local = static_cast<int>(q * 32 + lane);

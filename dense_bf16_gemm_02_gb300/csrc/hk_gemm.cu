@@ -18,6 +18,7 @@
 #include <string>
 
 #include "../../include/hk_gemm.h"
+#include "bounded_wait.cuh"
 #include "gemm_kernel.cuh"
 #include "host_internal.h"
 
@@ -267,8 +268,9 @@ hk_status read_status(StatusWord* w, int device) {
     if (e == cudaSuccess && h[0] != 0) e = cudaMemset(w->dev, 0, sizeof(uint32_t));
     if (prev >= 0 && prev != device) cudaSetDevice(prev);
     if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "reading the device status word", e);
-    if (h[0] != 0)
+    if (h[0] & ~hk::kErrPage)
         return fail(HK_ERR_TIMEOUT, "a bounded wait in the GEMM kernel ran out (error bits 0x%x)", h[0]);
+    if (h[0] != 0) return fail(HK_ERR_INVALID_ARG, "a page index or a length of a paged cache was out of range");
     return HK_OK;
 }
 

@@ -1,0 +1,316 @@
+// Host side of the paged 8-bit key/value cache (include/hk_gemm.h):
+// hk_kv8_append and hk_attention_kv8: argument checks, tensor maps, workspace
+// and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <mutex>
+
+#include "../../include/hk_gemm.h"
+#include "host_internal.h"
+#include "kv8_append.cuh"
+#include "kv8_decode.cuh"
+
+namespace {
+
+using namespace hk::kv8;
+
+hk_status fail(hk_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+hk_status fail(hk_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return hk_host::set_error(s, buf);
+}
+
+hk_status cuda_fail(hk_status s, const char* what, cudaError_t e) {
+    return fail(s, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;   // 1 s per bounded wait
+constexpr int kMaxDevices = 64;
+constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
+constexpr int kSms = 152;                               // the device's SMs: the workspace is sized without a device
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+hk_status check_cache(const hk_kv8_cache* c) {
+    if (!c) return fail(HK_ERR_INVALID_ARG, "null cache");
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return fail(HK_ERR_INVALID_ARG, "head dimension %d (supported: 64, 128)", (int)c->head_dim);
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return fail(HK_ERR_INVALID_ARG, "page size %d (supported: 16, 32, 64, 128)", (int)c->page_size);
+    if (c->heads < 1 || c->num_pages < 1 || c->num_pages > kLimit / c->heads)
+        return fail(HK_ERR_INVALID_ARG, "%lld pages of %d heads", (long long)c->num_pages, (int)c->heads);
+    if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return fail(HK_ERR_INVALID_ARG, "null cache pointer");
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return fail(HK_ERR_MISALIGNED, "cache codes must be 16-byte aligned, scales 4-byte aligned");
+    return HK_OK;
+}
+
+hk_status check_table(const int32_t* table, int64_t stride, int64_t max_pages, int64_t B, const int32_t* lengths,
+                      const int32_t* counts, int32_t page_size) {
+    if (max_pages < 1 || max_pages * page_size > kLimit)
+        return fail(HK_ERR_INVALID_ARG, "a block table of %lld pages per sequence", (long long)max_pages);
+    if (stride < max_pages && B > 1) return fail(HK_ERR_INVALID_ARG, "block table rows overlap");
+    if (!table || !lengths) return fail(HK_ERR_INVALID_ARG, "null block table or lengths");
+    if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(counts, 4))
+        return fail(HK_ERR_MISALIGNED, "block table, lengths and counts must be 4-byte aligned");
+    return HK_OK;
+}
+
+hk_status current_device(int* device, int* sm_count) {
+    cudaError_t e = cudaGetDevice(device);
+    if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "cudaGetDevice", e);
+    if (*device < 0 || *device >= kMaxDevices) return fail(HK_ERR_INVALID_ARG, "device %d out of range", *device);
+    return hk_host::check_device(*device, sm_count);
+}
+
+template <int kWarps>
+void launch_append(const AppendParams& p, int32_t type, unsigned blocks, cudaStream_t st) {
+    switch (type) {
+        case HK_TYPE_BF16: kv8_append_kernel<__nv_bfloat16, kWarps><<<blocks, 256, 0, st>>>(p); break;
+        case HK_TYPE_FP16: kv8_append_kernel<__half, kWarps><<<blocks, 256, 0, st>>>(p); break;
+        default: kv8_append_kernel<float, kWarps><<<blocks, 256, 0, st>>>(p); break;
+    }
+}
+
+// Codes of keys or values as [pages · heads, page_size, D] in boxes of up to 32 tokens of one head.
+hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, const hk_kv8_cache* c) {
+    const cuuint64_t D = static_cast<cuuint64_t>(c->head_dim);
+    cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->num_pages) * c->heads};
+    cuuint64_t strides[2] = {D, D * c->page_size};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(std::min(c->page_size, kTileKeys)), 1};
+    cuuint32_t elem_strides[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, elem_strides,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of the cache failed (CUresult %d)", (int)r);
+    return HK_OK;
+}
+
+std::mutex g_setup_mutex;
+bool g_setup[kMaxDevices] = {};
+
+template <int kD, typename T>
+cudaError_t setup_decode() {
+    return cudaFuncSetAttribute(kv8_decode_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeGeometry<kD>::kSmemBytes);
+}
+
+hk_status setup(int device) {
+    std::lock_guard<std::mutex> lock(g_setup_mutex);
+    if (g_setup[device]) return HK_OK;
+    cudaError_t e = setup_decode<64, __nv_bfloat16>();
+    if (e == cudaSuccess) e = setup_decode<64, __half>();
+    if (e == cudaSuccess) e = setup_decode<128, __nv_bfloat16>();
+    if (e == cudaSuccess) e = setup_decode<128, __half>();
+    if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring the cache attention kernels", e);
+    g_setup[device] = true;
+    return HK_OK;
+}
+
+// Workspace of the split kernel: partial sums and their maxima and sums for two
+// units per warp, and a record per warp.
+struct DecodeWorkspace {
+    size_t ml, info, total;
+};
+
+DecodeWorkspace decode_workspace(int64_t D) {
+    const size_t warps = static_cast<size_t>(2 * kSms) * kDecodeWarps;
+    DecodeWorkspace w;
+    w.ml = 2 * warps * kRows * static_cast<size_t>(D) * 4;
+    w.info = w.ml + 2 * warps * kRows * 2 * 4;
+    w.total = w.info + warps * sizeof(int4);
+    return w;
+}
+
+template <int kD, typename T>
+cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, cudaStream_t st) {
+    kv8_decode_kernel<kD, T><<<static_cast<unsigned>(blocks), 32 * kDecodeWarps, DecodeGeometry<kD>::kSmemBytes, st>>>(tk, tv, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    const int warps_per_row = 4;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks * kDecodeWarps), static_cast<unsigned>(kRows / (8 / warps_per_row)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv8_combine_kernel<kD, T>, p, warps_per_row);
+}
+
+}  // namespace
+
+extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, const void* V, int32_t type, int64_t B,
+                                   int64_t T, const int64_t k_strides[3], const int64_t v_strides[3],
+                                   const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                                   const int32_t* starts, const int32_t* counts, void* stream) {
+    hk_status s = check_cache(cache);
+    if (s != HK_OK) return s;
+    if (type < HK_TYPE_BF16 || type > HK_TYPE_FP32) return fail(HK_ERR_INVALID_ARG, "unknown element type %d", (int)type);
+    if (B < 0 || T < 0 || B > kLimit || T > kLimit) return fail(HK_ERR_INVALID_ARG, "invalid size");
+    if (B == 0 || T == 0) return HK_OK;
+    if ((s = check_table(block_table, table_stride, max_pages, B, starts, counts, cache->page_size)) != HK_OK) return s;
+    if (!K || !V || !k_strides || !v_strides) return fail(HK_ERR_INVALID_ARG, "null keys, values or strides");
+    const int size = type == HK_TYPE_FP32 ? 4 : 2;
+    if (!aligned(K, size) || !aligned(V, size)) return fail(HK_ERR_MISALIGNED, "keys or values not aligned to their elements");
+    int device = 0, sms = 0;
+    if ((s = current_device(&device, &sms)) != HK_OK) return s;
+    uint32_t* status = nullptr;
+    if ((s = hk_host::status_word(device, &status)) != HK_OK) return s;
+
+    AppendParams p = {};
+    const void* src[2] = {K, V};
+    const int64_t* strides[2] = {k_strides, v_strides};
+    for (int i = 0; i < 2; ++i) {
+        p.src[i] = src[i];
+        p.stride_b[i] = strides[i][0];
+        p.stride_t[i] = strides[i][1];
+        p.stride_h[i] = strides[i][2];
+        p.vec[i] = aligned(src[i], 16);
+        for (int k = 0; k < 3; ++k) p.vec[i] = p.vec[i] && (strides[i][k] * size) % 16 == 0;
+    }
+    p.codes[0] = static_cast<uint8_t*>(cache->k_codes);
+    p.codes[1] = static_cast<uint8_t*>(cache->v_codes);
+    p.scale[0] = cache->k_scale;
+    p.scale[1] = cache->v_scale;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.starts = starts;
+    p.counts = counts;
+    p.B = static_cast<int32_t>(B);
+    p.T = static_cast<int32_t>(T);
+    p.Hkv = cache->heads;
+    p.D = cache->head_dim;
+    p.page_size = cache->page_size;
+    p.max_pages = static_cast<int32_t>(max_pages);
+    p.num_pages = cache->num_pages;
+    p.slots = static_cast<int32_t>((T + p.page_size - 2) / p.page_size + 1);
+    p.status = status;
+    if (B > (int64_t(1) << 40) / p.slots / p.Hkv) return fail(HK_ERR_INVALID_ARG, "problem too large");
+    p.items = B * p.slots * p.Hkv * 2;
+    // one warp holds the new tokens of a page as long as they fit its registers (8 steps of 256 elements)
+    const bool one_warp = std::min<int64_t>(T, p.page_size) * p.D <= kAppendSteps * 256;
+    const int64_t blocks = one_warp ? ceil_div(p.items, 8) : p.items;
+    if (blocks > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (one_warp) launch_append<1>(p, type, static_cast<unsigned>(blocks), st);
+    else launch_append<8>(p, type, static_cast<unsigned>(blocks), st);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the cache append", e);
+}
+
+extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
+                                                  int64_t max_pages) {
+    (void)max_pages;
+    if (!cache || B <= 0 || T <= 0 || Hq <= 0) return 0;
+    return decode_workspace(cache->head_dim).total;
+}
+
+extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                                         const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                                         const int32_t* lengths, const int32_t* counts, void* O,
+                                         const int64_t o_strides[3], float* lse, int64_t B, int64_t T, int64_t Hq,
+                                         int32_t causal, float scale, void* workspace, size_t workspace_bytes,
+                                         uint32_t flags, uint64_t timeout_ns, void* stream) {
+    hk_status s = check_cache(cache);
+    if (s != HK_OK) return s;
+    if (flags) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if (type != HK_TYPE_BF16 && type != HK_TYPE_FP16) return fail(HK_ERR_INVALID_ARG, "element type %d (bf16 or fp16)", (int)type);
+    if (B < 0 || T < 0 || Hq < 0 || B > kLimit || T > kLimit || Hq > kLimit) return fail(HK_ERR_INVALID_ARG, "invalid size");
+    if (Hq % cache->heads) return fail(HK_ERR_INVALID_ARG, "Hq=%lld is not a multiple of the cache's %d heads", (long long)Hq, (int)cache->heads);
+    if (!std::isfinite(scale)) return fail(HK_ERR_INVALID_ARG, "the scale must be finite");
+    if (B == 0 || T == 0 || Hq == 0) return HK_OK;
+    if ((s = check_table(block_table, table_stride, max_pages, B, lengths, counts, cache->page_size)) != HK_OK) return s;
+    if (!Q || !O || !q_strides || !o_strides) return fail(HK_ERR_INVALID_ARG, "null queries, output or strides");
+    if (!aligned(Q, 2) || !aligned(O, 2) || !aligned(lse, 4)) return fail(HK_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    const int64_t group = Hq / cache->heads;
+    if (T > kLimit / 16 / group || ceil_div(T * group, kRows) * (ceil_div(max_pages * cache->page_size, kTileKeys) + 1) > kLimit)
+        return fail(HK_ERR_INVALID_ARG, "problem too large");
+    const DecodeWorkspace ws = decode_workspace(cache->head_dim);
+    if (!workspace || workspace_bytes < ws.total)
+        return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", ws.total, workspace ? workspace_bytes : size_t(0));
+    if (!aligned(workspace, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
+    int device = 0, sms = 0;
+    if ((s = current_device(&device, &sms)) != HK_OK) return s;
+    if ((s = setup(device)) != HK_OK) return s;
+    uint32_t* status = nullptr;
+    if ((s = hk_host::status_word(device, &status)) != HK_OK) return s;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    if ((s = hk_host::tensor_map_encoder(&enc)) != HK_OK) return s;
+    CUtensorMap tk, tv;
+    if ((s = encode_codes(enc, &tk, cache->k_codes, cache)) != HK_OK) return s;
+    if ((s = encode_codes(enc, &tv, cache->v_codes, cache)) != HK_OK) return s;
+
+    DecodeParams p = {};
+    p.q_stride_b = q_strides[0];
+    p.q_stride_t = q_strides[1];
+    p.q_stride_h = q_strides[2];
+    p.o_stride_b = o_strides[0];
+    p.o_stride_t = o_strides[1];
+    p.o_stride_h = o_strides[2];
+    p.vec_q = aligned(Q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
+    p.vec_o = aligned(O, 16) && o_strides[0] % 8 == 0 && o_strides[1] % 8 == 0 && o_strides[2] % 8 == 0;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.table_stride = table_stride;
+    p.T = static_cast<int32_t>(T);
+    p.Hq = static_cast<int32_t>(Hq);
+    p.Hkv = cache->heads;
+    p.group = static_cast<int32_t>(group);
+    p.row_tiles = static_cast<int32_t>(ceil_div(T * group, kRows));
+    p.page_size = cache->page_size;
+    p.page_shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
+    p.max_pages = static_cast<int32_t>(max_pages);
+    p.num_pages = cache->num_pages;
+    p.causal = causal ? 1 : 0;
+    p.scale_log2 = static_cast<float>(1.4426950408889634 * (scale != 0.0f ? static_cast<double>(scale)
+                                                                          : 1.0 / std::sqrt(static_cast<double>(cache->head_dim))));
+    p.min_tiles = 2;
+    char* const w = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(w);
+    p.part_ml = reinterpret_cast<float*>(w + ws.ml);
+    p.info = reinterpret_cast<int4*>(w + ws.info);
+    p.wait.status = status;
+    p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int blocks = 2 * std::min(sms, kSms);
+    for (int64_t b0 = 0; b0 < B; b0 += kMaxBatch) {       // (launches of one stream: they may share the workspace)
+        p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, kMaxBatch));
+        p.q = static_cast<const uint16_t*>(Q) + b0 * p.q_stride_b;
+        p.o = static_cast<uint16_t*>(O) + b0 * p.o_stride_b;
+        p.lse = lse ? lse + b0 * T * Hq : nullptr;
+        p.table = block_table + b0 * table_stride;
+        p.lengths = lengths + b0;
+        p.counts = counts ? counts + b0 : nullptr;
+        p.wait.launch_id = hk_host::next_launch_id();
+        cudaError_t e;
+        const bool half = type == HK_TYPE_FP16;
+        if (cache->head_dim == 64)
+            e = half ? launch_decode<64, __half>(tk, tv, p, blocks, st) : launch_decode<64, __nv_bfloat16>(tk, tv, p, blocks, st);
+        else
+            e = half ? launch_decode<128, __half>(tk, tv, p, blocks, st) : launch_decode<128, __nv_bfloat16>(tk, tv, p, blocks, st);
+        if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache attention", e);
+    }
+    return HK_OK;
+}
+
+extern "C" hk_status hk_attention_kv8(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                                      const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                                      const int32_t* lengths, const int32_t* counts, void* O, const int64_t o_strides[3],
+                                      float* lse, int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+    return hk_attention_kv8_ex(Q, type, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides,
+                               lse, B, T, Hq, causal, scale, workspace, workspace_bytes, 0u, 0u, stream);
+}

@@ -1,0 +1,174 @@
+// Appending keys and values to a paged cache held in E4M3 with one scale per
+// page and head.
+//
+// A page holds `page_size` tokens of every KV head: codes [page, head, token,
+// D], one fp32 scale per (page, head), always a power of two, so that a value
+// is code · scale and changing the scale moves only the exponent. The tokens
+// that arrive in a page need the scale 2^e with the smallest e for which their
+// largest finite magnitude is at most 448 · 2^e (E4M3's largest number); a page
+// that holds earlier tokens keeps its scale if that is larger, else its codes
+// are rounded once more to the new scale (exact unless they fall below E4M3's
+// smallest normal number).
+//
+// One item is a (sequence, touched page, head) of keys or of values: one warp
+// when few tokens arrive per page, else eight warps. The new tokens of an item
+// stay in registers between the maximum and the rounding, so that they are read
+// once; for one token per sequence the kernel is a launch and two dependent
+// reads (the page's index, then its scale beside the token).
+#pragma once
+
+#include <cstdint>
+
+#include "bounded_wait.cuh"
+#include "elements.cuh"
+
+namespace hk {
+namespace kv8 {
+
+struct AppendParams {
+    const void* src[2];            // new keys, new values
+    int64_t stride_b[2], stride_t[2], stride_h[2];   // in elements
+    uint8_t* codes[2];             // [pages, Hkv, page_size, D]
+    float* scale[2];               // [pages, Hkv]
+    const int32_t* table;          // [B, max_pages]
+    int64_t table_stride;
+    const int32_t* starts;         // tokens of each sequence before the append
+    const int32_t* counts;         // new tokens of each sequence, or null (T)
+    int64_t items;                 // B * slots * Hkv * 2
+    int32_t B, T, Hkv, D, page_size, max_pages;
+    int64_t num_pages;
+    int32_t slots;                 // pages a sequence can touch
+    int32_t vec[2];                // 16-byte loads
+    uint32_t* status;
+};
+
+constexpr int kAppendSteps = 8;    // steps of a group of warps: 8 elements per lane and step
+
+// The exponent field of the page scale for a largest magnitude (its bits).
+__device__ __forceinline__ uint32_t scale_field(uint32_t amax_bits) {
+    const int field = static_cast<int>(amax_bits >> 23);                   // 127 + floor(log2 amax)
+    const int e = field - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u);       // 448 = 1.75 · 2^8
+    return static_cast<uint32_t>(e < 1 ? 1 : e);
+}
+
+// Sixteen codes times a power of two, rounded to E4M3 again.
+__device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = (w >> (8 * i)) & 0xFFu;
+        out |= e4m3_of(e4m3_value(b) * ratio) << (8 * i);
+    }
+    return out;
+}
+
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(256)
+kv8_append_kernel(const AppendParams p) {
+    __shared__ uint32_t warp_top[8];
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t member = kWarps == 1 ? 0 : warp;          // this warp's place in its item
+    const int64_t item = kWarps == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : static_cast<int64_t>(blockIdx.x);
+    if (item >= p.items) return;
+    const int kv = static_cast<int>(item & 1);
+    int64_t rest = item >> 1;
+    const int h = static_cast<int>(rest % p.Hkv);
+    rest /= p.Hkv;
+    const int b = static_cast<int>(rest / p.slots);
+    const int nth = static_cast<int>(rest % p.slots);
+
+    const int32_t start = p.starts[b];
+    const int32_t count = p.counts != nullptr ? p.counts[b] : p.T;
+    const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+    const bool bad = start < 0 || count < 0 || count > p.T || start + static_cast<int64_t>(count) > room;
+    if (bad) {
+        if (lane == 0 && nth == 0) atomicOr(p.status, kErrPage);
+        return;
+    }
+    const int64_t slot = start / p.page_size + nth;
+    const int64_t lo = max(static_cast<int64_t>(start), slot * p.page_size);              // new tokens of this page
+    const int64_t hi = min(static_cast<int64_t>(start) + count, (slot + 1) * p.page_size);
+    if (lo >= hi) return;
+    const int64_t page = p.table[b * p.table_stride + slot];
+    if (page < 0 || page >= p.num_pages) {
+        if (lane == 0) atomicOr(p.status, kErrPage);
+        return;
+    }
+    const int64_t ph = page * p.Hkv + h;
+    const int old_tokens = static_cast<int>(lo - slot * p.page_size);
+    const float had = old_tokens > 0 ? p.scale[kv][ph] : 0.0f;
+
+    const int lanes_per_token = p.D >> 3;
+    const int per_step = kWarps * (32 / lanes_per_token);
+    const int sub = static_cast<int>(member) * (32 / lanes_per_token) + static_cast<int>(lane) / lanes_per_token;
+    const int d = static_cast<int>(lane) % lanes_per_token * 8;
+    const int n = static_cast<int>(hi - lo);
+    const T* const src = static_cast<const T*>(p.src[kv]) + b * p.stride_b[kv] + (lo - start) * p.stride_t[kv] +
+                         h * p.stride_h[kv];
+    Raw8<T> raw[kAppendSteps];
+#pragma unroll
+    for (int i = 0; i < kAppendSteps; ++i) {
+        const int t = i * per_step + sub;
+        if (i * per_step < n)
+            raw[i] = load8<T>(src + t * p.stride_t[kv], d, t < n ? p.D : 0, p.vec[kv] != 0);
+    }
+    uint32_t top = 0;       // largest finite magnitude, as bits
+#pragma unroll
+    for (int i = 0; i < kAppendSteps; ++i) {
+        if (i * per_step < n) {
+            float v[8];
+            widen8<T>(raw[i], v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t m = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+                top = max(top, m < 0x7F800000u ? m : 0u);
+            }
+        }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if constexpr (kWarps > 1) {
+        if (lane == 0) warp_top[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = max(top, warp_top[w]);
+    }
+    const float need = __uint_as_float(scale_field(top) << 23);
+    const float scale = old_tokens > 0 ? fmaxf(need, had) : need;
+
+    uint8_t* const dst = p.codes[kv] + ph * p.page_size * p.D;
+    if (old_tokens > 0 && scale > had) {
+        const float ratio = had / scale;
+        uint4* const old = reinterpret_cast<uint4*>(dst);
+        for (int i = static_cast<int>(member * 32 + lane); i < old_tokens * p.D / 16; i += 32 * kWarps) {
+            uint4 w = old[i];
+            w.x = rescale_codes(w.x, ratio);
+            w.y = rescale_codes(w.y, ratio);
+            w.z = rescale_codes(w.z, ratio);
+            w.w = rescale_codes(w.w, ratio);
+            old[i] = w;
+        }
+    }
+    const float inv = 1.0f / scale;      // exact: a power of two
+#pragma unroll
+    for (int i = 0; i < kAppendSteps; ++i) {
+        const int t = i * per_step + sub;
+        if (t < n) {
+            float v[8];
+            widen8<T>(raw[i], v);
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint16_t c0, c1;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c0) : "f"(v[4 * k + 1] * inv), "f"(v[4 * k] * inv));
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c1) : "f"(v[4 * k + 3] * inv), "f"(v[4 * k + 2] * inv));
+                w[k] = static_cast<uint32_t>(c0) | static_cast<uint32_t>(c1) << 16;
+            }
+            *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(old_tokens + t) * p.D + d) = make_uint2(w[0], w[1]);
+        }
+    }
+    if (member == 0 && lane == 0) p.scale[kv][ph] = scale;
+}
+
+}  // namespace kv8
+}  // namespace hk

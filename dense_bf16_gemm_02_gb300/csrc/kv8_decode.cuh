@@ -1,0 +1,669 @@
+// Attention of a few query rows over a paged cache held in E4M3 (see
+// kv8_append.cuh for the cache), for decoding: one or a few new tokens per
+// sequence, every cached token read once.
+//
+//   O[r] = Σ_j P[r,j]·V[j] / Σ_j P[r,j],  P[r,j] = exp(scale · q_r·K[j] - m_r)
+//
+// What bounds it is reading the cache: 2·D bytes per token and KV head. A unit
+// is 16 query rows (tokens × the query heads of one KV head, padded) of one
+// sequence and KV head; a tile is 32 cached tokens of a unit. All tiles of all
+// units, in order, are cut into equal runs, one per WARP of a grid that fills
+// the GPU once, whatever the lengths of the sequences are. A warp streams its
+// run through a ring of its own (TMA loads of code rows, swizzled so that the
+// reads below meet no bank twice) and needs no other warp: no block-wide
+// barrier, no imbalance between short and long sequences. A unit that lies
+// inside one run is finished by its warp; the others leave unnormalised sums
+// per run, which a second kernel adds up in order (no atomics: the result does
+// not depend on timing).
+//
+// Arithmetic. mma.sync m16n8k16 with f16 operands and fp32 sums: the tensor
+// work is a few per cent of its rate here, so the fragments' layout in
+// registers (no staging through Tensor Memory) counts for more than the faster
+// unit. Codes become f16 exactly, two per conversion. A query row is scaled by
+// a power of two so that its largest magnitude lies in [2^10, 2^11): exact for
+// every element down to 2^-24 of that, and the others err by at most 2^-35 of
+// it. P is rounded to f16 (11 bits), its sum is kept unrounded in fp32. The
+// page's scale multiplies the scores of its tokens and, for V, the sums of each
+// tile's products before they join the running output, all in fp32.
+//
+// Column orders. A thread's fragment registers need pairs along K: the columns
+// of an operand may be in any order as long as both operands agree, so a
+// thread takes 16 consecutive codes of a row at a time (one 16-byte read).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "bounded_wait.cuh"
+#include "elements.cuh"
+#include "ptx.cuh"
+
+namespace hk {
+namespace kv8 {
+
+constexpr int kRows = 16;              // query rows of a unit
+constexpr int kTileKeys = 32;
+constexpr int kDecodeWarps = 4;        // warps of a block, each on its own
+constexpr int kMaxBatch = 1024;        // sequences of one launch
+
+template <int kD>
+struct DecodeGeometry {
+    static_assert(kD == 64 || kD == 128, "head dimension 64 or 128");
+    static constexpr int kHalfBytes = kTileKeys * kD;                 // K or V of a tile
+    static constexpr int kStageBytes = 2 * kHalfBytes;
+    static constexpr int kStages = kD == 128 ? 3 : 6;                 // 24 KB per warp
+    static constexpr int kWarpBytes = kStages * kStageBytes;
+    static constexpr int kOffPrefix = kDecodeWarps * kWarpBytes;      // tiles of the sequences up to each one
+    static constexpr int kOffBars = kOffPrefix + (kMaxBatch + 1) * 8;
+    static constexpr int kSmemBytes = kOffBars + kDecodeWarps * kStages * 8 + 1024;
+    static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two blocks per SM");
+};
+
+struct DecodeParams {
+    const void* q;
+    int64_t q_stride_b, q_stride_t, q_stride_h;     // in elements
+    void* o;
+    int64_t o_stride_b, o_stride_t, o_stride_h;
+    float* lse;                                     // [B, T, Hq] or null
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* lengths;
+    const int32_t* counts;                          // query tokens of each sequence, or null (T)
+    int32_t B, T, Hq, Hkv, group;                   // group = Hq / Hkv
+    int32_t row_tiles;                              // ceil(T * group / 16)
+    int32_t page_size, page_shift, max_pages;
+    int64_t num_pages;
+    int32_t causal, vec_q, vec_o;
+    float scale_log2;                               // softmax scale · log2(e)
+    int32_t min_tiles;                              // least tiles of a run
+    float* part_o;                                  // [2 · warps][16][D]
+    float* part_ml;                                 // [2 · warps][16][2]
+    int4* info;                                     // [warps]: the unit whose partial sums begin with this warp's run
+    WaitCtx wait;
+};
+
+// Visible tokens of a sequence and its queries, with what is out of range clamped.
+struct Sequence {
+    int len, count;
+};
+
+__device__ __forceinline__ Sequence sequence(const DecodeParams& p, int b) {
+    Sequence s;
+    s.len = p.lengths[b];
+    s.count = p.counts != nullptr ? p.counts[b] : p.T;
+    const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+    if (s.len < 0 || s.len > room || s.count < 0 || s.count > p.T) {
+        atomicOr(p.wait.status, kErrPage);
+        s.len = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(s.len), room)));
+        s.count = max(0, min(s.count, p.T));
+    }
+    return s;
+}
+
+// Tokens that the last row of row tile `rt` sees: the tile's runs end there.
+__device__ __forceinline__ int row_tile_end(const DecodeParams& p, const Sequence& s, int rt) {
+    const int t_first = rt * kRows / p.group;
+    if (t_first >= s.count) return 0;
+    if (!p.causal) return s.len;
+    const int t_last = min((rt * kRows + kRows - 1) / p.group, s.count - 1);
+    return max(0, s.len - s.count + t_last + 1);
+}
+
+__device__ __forceinline__ int tiles_of(int end) { return max(1, (end + kTileKeys - 1) / kTileKeys); }
+
+__device__ __forceinline__ int sequence_tiles(const DecodeParams& p, const Sequence& s) {
+    int n = 0;
+    for (int rt = 0; rt < p.row_tiles; ++rt) n += tiles_of(row_tile_end(p, s, rt));
+    return n;       // of one KV head
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(pair)));
+    return h;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+// Byte offset of 16-byte chunk `c` of row `r` in a tile that TMA wrote with
+// 128-byte (D = 128) or 64-byte (D = 64) swizzling.
+template <int kD>
+__device__ __forceinline__ uint32_t chunk_offset(uint32_t r, uint32_t c) {
+    return kD == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_out(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack_out<__nv_bfloat16>(float a, float b) {
+    return pack_bf16x2_rn(__float_as_uint(a), __float_as_uint(b));
+}
+template <>
+__device__ __forceinline__ uint32_t pack_out<__half>(float a, float b) { return pack_f16x2(a, b); }
+
+// kCols consecutive values of an output row, 16-byte stores where `vec`.
+template <typename T, int kCols>
+__device__ __forceinline__ void store_row(T* dst, const float (&v)[kCols], bool vec) {
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i)
+            reinterpret_cast<uint4*>(dst)[i] =
+                make_uint4(pack_out<T>(v[8 * i], v[8 * i + 1]), pack_out<T>(v[8 * i + 2], v[8 * i + 3]),
+                           pack_out<T>(v[8 * i + 4], v[8 * i + 5]), pack_out<T>(v[8 * i + 6], v[8 * i + 7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) dst[i] = from_float<T>(v[i]);
+    }
+}
+
+template <int kD, typename T>
+__global__ void __launch_bounds__(32 * kDecodeWarps, 2)
+kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                  const DecodeParams p) {
+    using G = DecodeGeometry<kD>;
+    constexpr int kWords = kD / 16;          // 4-code words of a row that a thread holds (one K step each)
+    constexpr int kNTiles = kD / 8;          // 8-column tiles of the output
+    constexpr int kOwn = kD / 4;             // output columns of a thread
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw);
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    const uint32_t g = lane >> 2, c = lane & 3u;
+    const int warps = static_cast<int>(gridDim.x) * kDecodeWarps;
+    const int self = static_cast<int>(blockIdx.x) * kDecodeWarps + static_cast<int>(warp);
+
+    griddep_launch_dependents();             // the combining kernel may be scheduled; it waits for this grid's end
+
+    const uint32_t ring = base + warp * G::kWarpBytes;
+    auto full_bar = [&](int s) { return base + G::kOffBars + 8u * (warp * G::kStages + s); };
+    if (lane == 0) {
+        for (int s = 0; s < G::kStages; ++s) mbar_init(full_bar(s), 1);
+        fence_mbar_init_cluster();
+    }
+    // prefix[b]: tiles of the sequences before b, all KV heads
+    int64_t* const prefix = reinterpret_cast<int64_t*>(smem + G::kOffPrefix);
+    if (warp == 0) {
+        int64_t sum = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + static_cast<int>(lane);
+            int64_t n = 0;
+            if (b < p.B) n = static_cast<int64_t>(sequence_tiles(p, sequence(p, b))) * p.Hkv;
+            int64_t inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (static_cast<int>(lane) >= d) inc += o;
+            }
+            if (b < p.B) prefix[b] = sum + inc - n;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) prefix[p.B] = sum;
+    }
+    __syncthreads();
+
+    const int64_t total = prefix[p.B];
+    const int64_t per = max(static_cast<int64_t>(p.min_tiles), (total + warps - 1) / warps);
+    const int64_t begin = min(total, self * per), end = min(total, begin + per);
+    int4 info = make_int4(0, 0, 0, 0);
+    bool ok = true;
+    int fills = 0, uses = 0;                 // ring stages filled and consumed so far
+
+    // the sequence of the run's first tile
+    int b = 0;
+    {
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= begin) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+    }
+    int64_t at = begin;
+    while (at < end && ok) {
+        while (at >= prefix[b + 1]) ++b;
+        const Sequence seq = sequence(p, b);
+        const int head_tiles = sequence_tiles(p, seq);
+        const int64_t local = at - prefix[b];
+        const int h = static_cast<int>(local / head_tiles);
+        int first = static_cast<int>(local - static_cast<int64_t>(h) * head_tiles);
+        int rt = 0, key_end = row_tile_end(p, seq, 0);
+        while (first >= tiles_of(key_end)) {
+            first -= tiles_of(key_end);
+            key_end = row_tile_end(p, seq, ++rt);
+        }
+        const int unit_tiles = tiles_of(key_end);
+        const int last = static_cast<int>(min(static_cast<int64_t>(unit_tiles), first + (end - at)));   // tiles [first, last)
+
+        // ---- query rows g and g + 8 of the unit: f16 fragments and the factor of their scores
+        uint32_t qf[kWords][4];
+        float factor[2];
+        int limit[2];                        // tokens the row sees
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = rt * kRows + static_cast<int>(g) + 8 * i;
+            const int t = row / p.group;
+            const bool live = t < seq.count;
+            // (rows past T are never stored and need no mask)
+            limit[i] = t >= p.T ? 0x7FFFFFFF : !live ? 0 : p.causal ? max(0, seq.len - seq.count + t + 1) : seq.len;
+            const T* const src = static_cast<const T*>(p.q) + b * p.q_stride_b + t * p.q_stride_t +
+                                 static_cast<int64_t>(h * p.group + row % p.group) * p.q_stride_h;
+            Raw8<T> rawq[kD / 32];
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < kD / 32; ++k) {
+                rawq[k] = load8<T>(src, static_cast<int64_t>(c) * kOwn + 8 * k, live ? kD : 0, p.vec_q != 0);
+                float v[8];
+                widen8<T>(rawq[k], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(10 - floor(log2 top)), kept a normal number; 1 for rows of zeros and rows with an infinity or NaN
+            int field = 127 + 10 - (static_cast<int>(top >> 23) - 127);
+            if (top == 0 || top >= 0x7F800000u) field = 127;
+            field = min(max(field, 1), 253);
+            const float mul = __uint_as_float(static_cast<uint32_t>(field) << 23);
+            factor[i] = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * p.scale_log2;
+#pragma unroll
+            for (int k = 0; k < kD / 32; ++k) {
+                float v[8];
+                widen8<T>(rawq[k], v);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    qf[2 * k + w][i] = pack_f16x2(v[4 * w] * mul, v[4 * w + 1] * mul);
+                    qf[2 * k + w][2 + i] = pack_f16x2(v[4 * w + 2] * mul, v[4 * w + 3] * mul);
+                }
+            }
+        }
+        int all_see = min(limit[0], limit[1]);      // tokens that every row sees: no mask needed below
+        all_see = __reduce_min_sync(0xffffffffu, all_see);
+
+        float o[kNTiles][4];
+#pragma unroll
+        for (int j = 0; j < kNTiles; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+        // Pages of the next 32 tiles, one tile per lane (two pages where a page is 16 tokens); -1: not a page
+        int page0 = 0, page1 = 0;
+        float ks0 = 0, ks1 = 0, vs0 = 0, vs1 = 0;
+        auto look_up = [&](int tile0) {
+            auto page_of = [&](int key) {
+                if (key >= key_end) return -1;
+                const int32_t pg = p.table[b * p.table_stride + (key >> p.page_shift)];
+                if (pg < 0 || pg >= p.num_pages) {
+                    atomicOr(p.wait.status, kErrPage);
+                    return -1;
+                }
+                return static_cast<int>(pg);
+            };
+            const int key = (tile0 + static_cast<int>(lane)) * kTileKeys;
+            page0 = page_of(key);
+            page1 = p.page_size < kTileKeys ? page_of(key + 16) : page0;
+            // (no page: scale 0, so that nothing of page 0, read in its place, comes through)
+            auto scale_of = [&](const float* scale, int pg) {
+                return pg >= 0 ? scale[static_cast<int64_t>(pg) * p.Hkv + h] : 0.0f;
+            };
+            ks0 = scale_of(p.k_scale, page0);
+            vs0 = scale_of(p.v_scale, page0);
+            ks1 = p.page_size < kTileKeys ? scale_of(p.k_scale, page1) : ks0;
+            vs1 = p.page_size < kTileKeys ? scale_of(p.v_scale, page1) : vs0;
+        };
+        // (a page that is not one is read as page 0 and masked)
+        auto load_tile = [&](int tile, int pg0, int pg1) {
+            const int s = fills % G::kStages;
+            if (lane == 0) {
+                const uint32_t dst = ring + s * G::kStageBytes;
+                mbar_arrive_expect_tx(full_bar(s), G::kStageBytes);
+                const int row = (tile * kTileKeys) & (p.page_size - 1);
+                const int z0 = max(pg0, 0) * p.Hkv + h, z1 = max(pg1, 0) * p.Hkv + h;
+                if (p.page_size >= kTileKeys) {
+                    tma_load_3d(dst, &tmap_k, 0, row, z0, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, row, z0, full_bar(s));
+                } else {
+                    tma_load_3d(dst, &tmap_k, 0, 0, z0, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes / 2, &tmap_k, 0, 0, z1, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, 0, z0, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes * 3 / 2, &tmap_v, 0, 0, z1, full_bar(s));
+                }
+            }
+            ++fills;
+        };
+
+        int looked = first;                  // tiles [looked, looked + 32) are in the lanes
+        int next = first;                    // next tile to load
+        if (key_end > 0) look_up(first);
+        const int seen = key_end > 0 ? last : first;      // a unit that sees nothing has no tile to read
+        // the scales of the tiles in the ring, by place
+        float rks0[G::kStages], rks1[G::kStages], rvs0[G::kStages], rvs1[G::kStages];
+        int rbad[G::kStages];
+        auto feed = [&](int place) {
+            if (next - looked == 32) {
+                looked = next;
+                look_up(next);
+            }
+            const int src = next - looked;
+            const int pg0 = __shfl_sync(0xffffffffu, page0, src), pg1 = __shfl_sync(0xffffffffu, page1, src);
+            const float a = __shfl_sync(0xffffffffu, ks0, src), bq = __shfl_sync(0xffffffffu, ks1, src);
+            const float cq = __shfl_sync(0xffffffffu, vs0, src), dq = __shfl_sync(0xffffffffu, vs1, src);
+#pragma unroll
+            for (int s = 0; s < G::kStages; ++s)
+                if (s == place) {
+                    rks0[s] = a;
+                    rks1[s] = bq;
+                    rvs0[s] = cq;
+                    rvs1[s] = dq;
+                    rbad[s] = (pg0 < 0 ? 1 : 0) | (pg1 < 0 ? 2 : 0);
+                }
+            load_tile(next, pg0, pg1);
+            ++next;
+        };
+        for (int i = 0; i < G::kStages && next < seen; ++i) feed(fills % G::kStages);
+
+        for (int tile = first; tile < seen; ++tile) {
+            const int s = uses % G::kStages;
+            if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(s), (uses / G::kStages) & 1, kErrWaitData))) {
+                ok = false;
+                break;
+            }
+            ++uses;
+            float tks0 = 0, tks1 = 0, tvs0 = 0, tvs1 = 0;
+            int bad = 0;
+#pragma unroll
+            for (int q = 0; q < G::kStages; ++q)
+                if (q == s) {
+                    tks0 = rks0[q];
+                    tks1 = rks1[q];
+                    tvs0 = rvs0[q];
+                    tvs1 = rvs1[q];
+                    bad = rbad[q];
+                }
+            const uint32_t kb = ring + s * G::kStageBytes, vb = kb + G::kHalfBytes;
+            const int key0 = tile * kTileKeys;
+            if (key0 + kTileKeys > key_end) {
+                // rows past the end hold whatever the page holds there, perhaps NaN codes that
+                // a weight of 0 would not silence: V's are cleared
+                const int from = key_end - key0;
+                for (int i = static_cast<int>(lane); i < (kTileKeys - from) * (kD / 16); i += 32)
+                    st_shared_v4(vb + static_cast<uint32_t>(from * kD + 16 * i), 0, 0, 0, 0);   // (whole rows: any order inside)
+                __syncwarp();
+            }
+
+            // ---- scores of 32 tokens: key tiles of 8, column g of tile j is token 8 j + g
+            float sc[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
+                uint32_t w[kWords];
+#pragma unroll
+                for (int i = 0; i < kWords / 4; ++i) {
+                    const uint4 x = ld_shared_v4(kb + chunk_offset<kD>(8u * j + g, (kWords / 4) * c + i));
+                    w[4 * i] = x.x;
+                    w[4 * i + 1] = x.y;
+                    w[4 * i + 2] = x.z;
+                    w[4 * i + 3] = x.w;
+                }
+#pragma unroll
+                for (int k = 0; k < kWords; ++k)
+                    mma_f16(sc[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], e4m3x2_to_f16x2(w[k] & 0xFFFFu),
+                            e4m3x2_to_f16x2(w[k] >> 16));
+            }
+            // ---- softmax of rows g (elements 0, 1) and g + 8 (2, 3); columns 2 c, 2 c + 1 of each tile
+            float mx[2] = {-INFINITY, -INFINITY};
+            const bool masked = key0 + kTileKeys > all_see || bad != 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float ks = j < 2 ? tks0 : tks1;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = sc[j][e] * (factor[e >> 1] * ks);
+                    if (masked) {
+                        const int key = key0 + 8 * j + static_cast<int>(2 * c) + (e & 1);
+                        if (key >= limit[e >> 1] || (bad & (j < 2 ? 1 : 2))) x = -INFINITY;
+                    }
+                    sc[j][e] = x;
+                    mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                }
+            }
+            float alpha[2];
+            bool moved = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                const float now = fmaxf(m[i], mx[i]);
+                alpha[i] = now > m[i] ? ex2_approx(m[i] - now) : 1.0f;
+                moved = moved || now > m[i];
+                m[i] = now;
+                l[i] *= alpha[i];
+            }
+            const float sub0 = m[0] == -INFINITY ? 0.0f : m[0], sub1 = m[1] == -INFINITY ? 0.0f : m[1];
+            uint32_t pf[4][2];               // P of tile j, rows g and g + 8, as f16 pairs
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p0 = ex2_approx(sc[j][0] - sub0), p1 = ex2_approx(sc[j][1] - sub0);
+                const float p2 = ex2_approx(sc[j][2] - sub1), p3 = ex2_approx(sc[j][3] - sub1);
+                l[0] += p0 + p1;
+                l[1] += p2 + p3;
+                pf[j][0] = pack_f16x2(p0, p1);
+                pf[j][1] = pack_f16x2(p2, p3);
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int j = 0; j < kNTiles; ++j) {
+                    o[j][0] *= alpha[0];
+                    o[j][1] *= alpha[0];
+                    o[j][2] *= alpha[1];
+                    o[j][3] *= alpha[1];
+                }
+            }
+            // ---- O += (P·V) · scale: tokens in two steps of 16; column g of output tile j is
+            // dimension g · (D / 8) + j, so a thread reads D / 8 consecutive codes of four rows
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const float vs = st == 0 ? tvs0 : tvs1;
+                uint32_t r[4][kD / 32];      // rows 16 st + 2 c, + 1, + 8, + 9
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t row = 16u * st + 2u * c + (i & 1) + (i >> 1) * 8u;
+                    if constexpr (kD == 128) {
+                        const uint4 x = ld_shared_v4(vb + chunk_offset<kD>(row, g));
+                        r[i][0] = x.x;
+                        r[i][1] = x.y;
+                        r[i][2] = x.z;
+                        r[i][3] = x.w;
+                    } else {
+                        const uint2 x = ld_shared_v2(vb + chunk_offset<kD>(row, g >> 1) + (g & 1u) * 8u);
+                        r[i][0] = x.x;
+                        r[i][1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < kD / 32; ++w) {
+                    const uint32_t a0 = __byte_perm(r[0][w], r[1][w], 0x5140), a1 = __byte_perm(r[0][w], r[1][w], 0x7362);
+                    const uint32_t b0 = __byte_perm(r[2][w], r[3][w], 0x5140), b1 = __byte_perm(r[2][w], r[3][w], 0x7362);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = e < 2 ? a0 : a1, hi = e < 2 ? b0 : b1;
+                        const uint32_t v0 = e & 1 ? lo >> 16 : lo & 0xFFFFu, v1 = e & 1 ? hi >> 16 : hi & 0xFFFFu;
+                        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma_f16(t, pf[2 * st][0], pf[2 * st][1], pf[2 * st + 1][0], pf[2 * st + 1][1], e4m3x2_to_f16x2(v0),
+                                e4m3x2_to_f16x2(v1));
+                        const int j = 4 * w + e;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) o[j][q] = fmaf(t[q], vs, o[j][q]);
+                    }
+                }
+            }
+            if (key0 + kTileKeys > key_end) fence_proxy_async_smem();   // the cleared rows, before a load may follow
+            __syncwarp();                    // every lane has read the stage
+            if (next < seen) feed(s);
+        }
+        if (!ok) break;
+
+        // ---- the rows' sums over their four threads; finish the unit or leave its partial sums
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        }
+        const bool whole = first == 0 && last == unit_tiles;
+        const int slot = 2 * self + (at == begin ? 0 : 1);
+        if (!whole && first == 0) {          // this run holds the unit's first tile: it leads the sum
+            const int64_t unit_begin = at, unit_end = at + unit_tiles;
+            const int parts = static_cast<int>((unit_end - 1) / per - unit_begin / per + 1);
+            info = make_int4(parts, slot, b, h * p.row_tiles + rt);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = rt * kRows + static_cast<int>(g) + 8 * i;
+            const int t = row / p.group;
+            const int head = h * p.group + row % p.group;
+            float v[kOwn];
+            // columns 2 c and 2 c + 1 of output tile j: dimensions 2 c (D / 8) + j and (2 c + 1)(D / 8) + j
+            const float mul = !whole ? 1.0f : l[i] > 0.0f || l[i] != l[i] ? 1.0f / l[i] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kNTiles; ++j) {
+                v[j] = o[j][2 * i] * mul;
+                v[kNTiles + j] = o[j][2 * i + 1] * mul;
+            }
+            if (whole) {
+                if (t < p.T) {
+                    T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + c * kOwn;
+                    store_row<T, kOwn>(dst, v, p.vec_o != 0);
+                    if (p.lse != nullptr && c == 0)
+                        p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] =
+                            l[i] > 0.0f || l[i] != l[i] ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+                }
+            } else if (t < p.T) {
+                const int64_t at_row = static_cast<int64_t>(slot) * kRows + g + 8 * i;
+                float4* const dst = reinterpret_cast<float4*>(p.part_o + at_row * kD + c * kOwn);
+#pragma unroll
+                for (int k = 0; k < kOwn / 4; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                if (c == 0) {
+                    p.part_ml[2 * at_row] = m[i];
+                    p.part_ml[2 * at_row + 1] = l[i];
+                }
+            }
+        }
+        at += last - first;
+    }
+    if (lane == 0) p.info[self] = info;
+    // abort: the copies in flight land before the block ends
+    if (!ok)
+        for (; uses < fills; ++uses) wait_mbar_drain(full_bar(uses % G::kStages), (uses / G::kStages) & 1);
+}
+
+// Adds up the partial sums of the units that several warps' runs share. Block
+// (x: the warp whose run such a unit begins in, y: which rows); the parts of a
+// row are shared out over `kSplit` of its warps and joined through shared
+// memory in order.
+template <int kD, typename T>
+__global__ void __launch_bounds__(256)
+kv8_combine_kernel(const DecodeParams p, const int warps_per_row) {
+    constexpr int kVec = kD / 32;            // floats of a lane
+    __shared__ float joined[8][kD + 2];
+    griddep_wait();
+    const int4 info = __ldcg(p.info + blockIdx.x);   // (past L1: this grid may have started before the writes)
+    const int parts = info.x;
+    if (parts == 0) return;
+    const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+    const int rows_per_block = 8 / warps_per_row;
+    const int b = info.z, h = info.w / p.row_tiles, rt = info.w % p.row_tiles;
+    for (int r0 = static_cast<int>(blockIdx.y) * rows_per_block; r0 < kRows; r0 += static_cast<int>(gridDim.y) * rows_per_block) {
+        const int r = r0 + warp / warps_per_row;
+        const int share = warp % warps_per_row;
+        const int row = rt * kRows + r;
+        const int t = row / p.group, head = h * p.group + row % p.group;
+        const bool live = t < p.T;
+        float m = -INFINITY, l = 0.0f, acc[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) acc[k] = 0.0f;
+        if (live) {
+            // part i of the unit: the leader's slot, then the first slot of each warp that follows
+            auto row_of = [&](int i) {
+                const int64_t slot = i == 0 ? info.y : 2 * (static_cast<int64_t>(blockIdx.x) + i);
+                return slot * kRows + r;
+            };
+#pragma unroll 4
+            for (int i = share; i < parts; i += warps_per_row) {
+                const int64_t a = row_of(i);
+                const float pm = __ldcg(p.part_ml + 2 * a), pl = __ldcg(p.part_ml + 2 * a + 1);
+                float x[kVec];
+                if constexpr (kVec == 4) {
+                    const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * kD) + lane);
+                    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+                } else {
+                    const float2 f = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * kD) + lane);
+                    x[0] = f.x; x[1] = f.y;
+                }
+                const float now = fmaxf(m, pm);
+                const float ws = now == -INFINITY ? 0.0f : ex2_approx(m - now), wp = now == -INFINITY ? 0.0f : ex2_approx(pm - now);
+                m = now;
+                l = l * ws + pl * wp;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) acc[k] = acc[k] * ws + x[k] * wp;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) joined[warp][lane * kVec + k] = acc[k];
+        if (lane == 0) {
+            joined[warp][kD] = m;
+            joined[warp][kD + 1] = l;
+        }
+        __syncthreads();
+        if (share == 0 && live) {
+            for (int w = 1; w < warps_per_row; ++w) {
+                const float pm = joined[warp + w][kD], pl = joined[warp + w][kD + 1];
+                const float now = fmaxf(m, pm);
+                const float ws = now == -INFINITY ? 0.0f : ex2_approx(m - now), wp = now == -INFINITY ? 0.0f : ex2_approx(pm - now);
+                m = now;
+                l = l * ws + pl * wp;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) acc[k] = acc[k] * ws + joined[warp + w][lane * kVec + k] * wp;
+            }
+            const bool any = l > 0.0f || l != l;
+            const float mul = any ? 1.0f / l : 0.0f;
+            T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + lane * kVec;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) dst[k] = from_float<T>(acc[k] * mul);
+            if (p.lse != nullptr && lane == 0)
+                p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] =
+                    any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+    }
+}
+
+}  // namespace kv8
+}  // namespace hk

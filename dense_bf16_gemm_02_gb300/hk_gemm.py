@@ -61,6 +61,7 @@ EXPORTED = (
     "hk_gemm_fp8_e4m3",
     "hk_attention_fwd", "hk_attention_fwd_ex", "hk_gemm_mxfp8", "hk_gemm_mxfp8_ex", "hk_gemm_mxfp8_workspace_size",
     "hk_fp4_scales_size", "hk_fp4_quantize", "hk_fp4_dequantize", "hk_gemm_fp4", "hk_gemm_fp4_ex",
+    "hk_kv8_append", "hk_attention_kv8", "hk_attention_kv8_ex", "hk_attention_kv8_workspace_size",
 )
 
 
@@ -83,6 +84,12 @@ class hk_gemm_plan_info(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class hk_kv8_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class HKError(RuntimeError):
@@ -164,6 +171,16 @@ def load() -> ctypes.CDLL:
         lib.hk_gemm_fp4.restype = I32
         lib.hk_gemm_fp4_ex.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, P, U32, U64, P]
         lib.hk_gemm_fp4_ex.restype = I32
+        CP, F = ctypes.POINTER(hk_kv8_cache), ctypes.c_float
+        lib.hk_kv8_append.argtypes = [CP, P, P, I32, I64, I64, P, P, P, I64, I64, P, P, P]
+        lib.hk_kv8_append.restype = I32
+        lib.hk_attention_kv8.argtypes = [P, I32, P, CP, P, I64, I64, P, P, P, P, P, I64, I64, I64, I32, F, P, SZ, P]
+        lib.hk_attention_kv8.restype = I32
+        lib.hk_attention_kv8_ex.argtypes = [P, I32, P, CP, P, I64, I64, P, P, P, P, P, I64, I64, I64, I32, F, P, SZ,
+                                            U32, U64, P]
+        lib.hk_attention_kv8_ex.restype = I32
+        lib.hk_attention_kv8_workspace_size.argtypes = [CP, I64, I64, I64, I64]
+        lib.hk_attention_kv8_workspace_size.restype = SZ
         _lib = lib
         return lib
 
@@ -260,6 +277,30 @@ def hk_gemm_fp4_ex(A: int, SFA: int, B: int, SFB: int, C: int, M: int, N: int, K
                    stream: int = 0) -> int:
     return load().hk_gemm_fp4_ex(A, SFA, B, SFB, C, M, N, K, lda, ldb, ldc, format, global_a or None,
                                  global_b or None, flags, timeout_ns, stream)
+
+
+def hk_kv8_append(cache: hk_kv8_cache, K: int, V: int, type: int, B: int, T: int, k_strides, v_strides,
+                  block_table: int, table_stride: int, max_pages: int, starts: int, counts: int = 0,
+                  stream: int = 0) -> int:
+    """Append T tokens to each of B sequences of a paged 8-bit cache (strides: sequences of three element strides)."""
+    I3 = ctypes.c_int64 * 3
+    return load().hk_kv8_append(ctypes.byref(cache), K, V, type, B, T, I3(*k_strides), I3(*v_strides), block_table,
+                                table_stride, max_pages, starts, counts or None, stream)
+
+
+def hk_attention_kv8(Q: int, type: int, q_strides, cache: hk_kv8_cache, block_table: int, table_stride: int,
+                     max_pages: int, lengths: int, counts: int, O: int, o_strides, lse: int, B: int, T: int, Hq: int,
+                     causal: int = 1, scale: float = 0.0, workspace: int = 0, workspace_bytes: int = 0,
+                     stream: int = 0) -> int:
+    """Attention of T query tokens per sequence over a paged 8-bit cache."""
+    I3 = ctypes.c_int64 * 3
+    return load().hk_attention_kv8(Q, type, I3(*q_strides), ctypes.byref(cache), block_table, table_stride, max_pages,
+                                   lengths, counts or None, O, I3(*o_strides), lse or None, B, T, Hq, int(causal), scale,
+                                   workspace or None, workspace_bytes, stream)
+
+
+def hk_attention_kv8_workspace_size(cache: hk_kv8_cache, B: int, T: int, Hq: int, max_pages: int) -> int:
+    return int(load().hk_attention_kv8_workspace_size(ctypes.byref(cache), B, T, Hq, max_pages))
 
 
 def hk_gemm_last_device_status(device: int) -> int:

@@ -1,6 +1,7 @@
 """Torch conveniences over the low-precision serving entry points of
 ``include/hk_gemm.h``: matrices in microscaled 4-bit floating point
-(``quantize_fp4``, ``dequantize_fp4``, ``gemm_fp4``).
+(``quantize_fp4``, ``dequantize_fp4``, ``gemm_fp4``), and a paged key/value
+cache in 8 bits (``Kv8Cache``, ``kv8_append``, ``attention_kv8``).
 
 As in ``hk_gemm``, this is argument marshalling: every step runs in the CUDA
 library, on ``stream`` (default: torch's current stream). What a call
@@ -165,3 +166,119 @@ def gemm_fp4(a: Fp4Matrix, b: Fp4Matrix, out=None, stream=None):
                            _stream_handle(stream)),
            "hk_gemm_fp4")
     return out
+
+
+class Kv8Cache:
+    """A paged key/value cache in E4M3 with a power-of-two scale per page and head.
+
+    ``k``, ``v``: uint8 [pages, heads, page_size, head_dim]; ``k_scale``,
+    ``v_scale``: float32 [pages, heads]; all contiguous CUDA tensors.
+    ``Kv8Cache.empty`` makes them."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "_c")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        for t, name, dtype, dims in ((k, "k", torch.uint8, 4), (v, "v", torch.uint8, 4),
+                                     (k_scale, "k_scale", torch.float32, 2), (v_scale, "v_scale", torch.float32, 2)):
+            if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.dim() != dims:
+                raise TypeError(f"{name} must be a {dims}-D {dtype} CUDA tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if v.shape != k.shape or k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+            raise ValueError("v must have k's shape, the scales [pages, heads]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        pages, heads, page_size, head_dim = k.shape
+        self._c = _hk.hk_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads,
+                                   page_size, head_dim, 0)
+
+    @classmethod
+    def empty(cls, pages, heads, head_dim, page_size=64, device="cuda"):
+        """A cache of `pages` pages; nothing needs to be initialised."""
+        import torch
+        shape = (pages, heads, page_size, head_dim)
+        return cls(torch.empty(shape, dtype=torch.uint8, device=device), torch.empty(shape, dtype=torch.uint8, device=device),
+                   torch.empty(shape[:2], dtype=torch.float32, device=device),
+                   torch.empty(shape[:2], dtype=torch.float32, device=device))
+
+    pages = property(lambda self: self.k.size(0))
+    heads = property(lambda self: self.k.size(1))
+    page_size = property(lambda self: self.k.size(2))
+    head_dim = property(lambda self: self.k.size(3))
+
+
+def _check_tokens(t, name, cache, heads):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+        raise TypeError(f"{name} must be a CUDA tensor [B, T, heads, head_dim]")
+    if t.size(3) != cache.head_dim or (heads and t.size(2) != heads):
+        raise ValueError(f"{name} {tuple(t.shape)} does not fit the cache ({cache.heads} heads of {cache.head_dim})")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _check_index(t, name, shape_dims, B):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != shape_dims:
+        raise TypeError(f"{name} must be a {shape_dims}-D int32 CUDA tensor")
+    if t.size(0) != B:
+        raise ValueError(f"{name} has {t.size(0)} entries for {B} sequences")
+    if t.size(-1) > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def kv8_append(cache: Kv8Cache, k, v, block_table, starts, counts=None, stream=None) -> None:
+    """Append k, v [B, T, heads, head_dim] (bf16, fp16 or fp32) to B sequences
+    that hold ``starts`` tokens; ``counts``: of each sequence's T tokens the first
+    so many (None: all). ``block_table`` [B, max_pages], ``starts``, ``counts``
+    [B]: int32. See hk_kv8_append for the scales."""
+    _check_tokens(k, "k", cache, cache.heads)
+    _check_tokens(v, "v", cache, cache.heads)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("v must have k's shape and type")
+    B, T = k.shape[:2]
+    _check_index(block_table, "block_table", 2, B)
+    _check_index(starts, "starts", 1, B)
+    if counts is not None:
+        _check_index(counts, "counts", 1, B)
+    _check(_hk.hk_kv8_append(cache._c, k.data_ptr(), v.data_ptr(), _type_code(k.dtype), B, T, k.stride()[:3],
+                             v.stride()[:3], block_table.data_ptr(), block_table.stride(0), block_table.size(1),
+                             starts.data_ptr(), _ptr(counts), _stream_handle(stream)),
+           "hk_kv8_append")
+
+
+def attention_kv8(q, cache: Kv8Cache, block_table, lengths, counts=None, causal=True, scale=None, return_lse=False,
+                  out=None, stream=None):
+    """softmax(scale · q·Kᵀ)·V over the cached tokens of each sequence.
+
+    q [B, T, Hq, head_dim] (bf16 or fp16, any strides with contiguous rows),
+    ``lengths`` [B] int32: cached tokens, the queries' own among them; with
+    ``causal`` query t stands at position lengths - counts + t (``counts`` [B]
+    int32: valid queries of each sequence, None: T). Queries that see no token,
+    or lie past ``counts``, give zeros. Returns o [B, T, Hq, head_dim] (and the
+    fp32 log-sum-exp [B, T, Hq] with ``return_lse``). ``scale``: 1/sqrt(head_dim)."""
+    import torch
+    _check_tokens(q, "q", cache, 0)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("q must be bfloat16 or float16")
+    if scale is not None and not scale:
+        raise ValueError("scale must not be 0")
+    B, T, Hq = q.shape[:3]
+    _check_index(block_table, "block_table", 2, B)
+    _check_index(lengths, "lengths", 1, B)
+    if counts is not None:
+        _check_index(counts, "counts", 1, B)
+    size = _hk.hk_attention_kv8_workspace_size(cache._c, B, T, Hq, block_table.size(1))
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, T, Hq, cache.head_dim), dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or out.stride(3) != 1:
+            raise ValueError("out must have q's shape and type, rows contiguous")
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    _check(_hk.hk_attention_kv8(q.data_ptr(), _type_code(q.dtype), q.stride()[:3], cache._c, block_table.data_ptr(),
+                                block_table.stride(0), block_table.size(1), lengths.data_ptr(), _ptr(counts),
+                                out.data_ptr(), out.stride()[:3], _ptr(lse), B, T, Hq, int(causal),
+                                0.0 if scale is None else scale, workspace.data_ptr(), size, _stream_handle(stream)),
+           "hk_attention_kv8")
+    return (out, lse) if return_lse else out

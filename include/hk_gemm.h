@@ -279,7 +279,9 @@ hk_status hk_gemm_plan_device_status(hk_gemm_plan* plan);
 
 /* The same for the calls of the one-shot entry points (hk_gemm_bf16,
  * hk_gemm_bf16_epilogue, hk_gemm_bf16_fused, hk_gemm_fp8_e4m3, hk_gemm_mxfp8(_ex),
- * hk_attention_fwd(_ex), hk_gemm_bf16_noalloc, hk_gemm_fp4(_ex)) on `device`. */
+ * hk_attention_fwd(_ex), hk_gemm_bf16_noalloc, hk_gemm_fp4(_ex), hk_kv8_append,
+ * hk_attention_kv8(_ex)) on `device`; HK_ERR_INVALID_ARG if a page index or a length
+ * of a paged cache was out of range (and no wait ran out). */
 hk_status hk_gemm_last_device_status(int device);
 
 void hk_gemm_plan_destroy(hk_gemm_plan* plan);
@@ -421,6 +423,87 @@ hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* B, const vo
                          int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
                          int32_t format, const float* global_a, const float* global_b,
                          uint32_t flags, uint64_t timeout_ns, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged key/value cache held in 8 bits, the append to it and attention over it.
+ *
+ * Pages of `page_size` tokens (16, 32, 64 or 128) hold E4M3 codes of every KV
+ * head, with one fp32 scale per page and head, always a power of two: a cached
+ * value is code · scale. All four arrays are caller-owned device memory,
+ * contiguous:
+ *   k_codes, v_codes   [num_pages, heads, page_size, head_dim] bytes, 16-byte aligned
+ *   k_scale, v_scale   [num_pages, heads]
+ * head_dim is 64 or 128. A fresh cache needs no initialisation: the append
+ * that puts the first token into a page sets its scale.
+ *
+ * Which pages a sequence owns is said by a block table of int32, [B, max_pages]
+ * with `table_stride` elements between rows: token j of sequence b lies in page
+ * block_table[b][j / page_size] at place j % page_size. Entries past a
+ * sequence's tokens are not read. A page index outside [0, num_pages) or a
+ * length outside the table is never followed: those tokens are not written or
+ * not attended to, and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG. */
+typedef struct hk_kv8_cache {
+    void* k_codes;
+    void* v_codes;
+    float* k_scale;
+    float* v_scale;
+    int64_t num_pages;
+    int32_t heads;
+    int32_t page_size;
+    int32_t head_dim;
+    int32_t reserved;
+} hk_kv8_cache;
+
+/* Append T tokens (or counts[b] <= T of them, its first) to each of B
+ * sequences, which hold starts[b] tokens before: token t goes to position
+ * starts[b] + t. K and V are [B, T, heads, head_dim] arrays of `type` (bf16,
+ * fp16 or fp32) with strides (b, t, head) in elements and contiguous rows of
+ * head_dim (16-byte aligned rows are read in 16-byte pieces).
+ * The new tokens of a page need the scale 2^e, e >= -126 the smallest with
+ * amax <= 448 · 2^e over their finite values. A page that already holds tokens
+ * of the sequence keeps its scale where that is larger; else its codes are
+ * rounded again to the new scale. Rounding is to nearest, halves to even;
+ * infinities become ±448 · scale, NaN stays NaN. Calling it again with the
+ * same arguments changes nothing. Pages must not be shared between sequences
+ * that are appended to. Asynchronous on `stream`, allocates nothing (but the
+ * status word, once). */
+hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, const void* V, int32_t type,
+                        int64_t B, int64_t T, const int64_t k_strides[3], const int64_t v_strides[3],
+                        const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                        const int32_t* starts, const int32_t* counts, void* stream);
+
+/* Attention of T query tokens per sequence over its lengths[b] cached tokens:
+ *     O[b,t,h,:] = Σ_j P_j · V_j,  P = softmax_j( scale · Q[b,t,h,:]·K_j ),
+ * K_j and V_j the cached values of head h / (Hq / heads). With `causal` query t
+ * stands at position lengths[b] - n + t, n = counts[b] (NULL: T), and sees the
+ * tokens up to it (the queries' own keys are in the cache); else it sees all
+ * lengths[b]. A query that sees no token, and queries t >= counts[b], give a row
+ * of zeros and a log-sum-exp of -inf. `scale` 0: 1/sqrt(head_dim).
+ * Q and O are [B, T, Hq, head_dim] of `type` (bf16 or fp16), strides (b, t, head)
+ * in elements, contiguous rows. lse, when not NULL: fp32 [B, T, Hq], natural
+ * log of the sum of exp(scale · q·k).
+ * `workspace`: device memory of hk_attention_kv8_workspace_size bytes, 256-byte
+ * aligned, scratch of this call (calls that overlap on the GPU must not share
+ * it). Asynchronous on `stream`; a bounded wait that runs out is reported by
+ * hk_gemm_last_device_status. */
+hk_status hk_attention_kv8(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                           const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                           const int32_t* lengths, const int32_t* counts,
+                           void* O, const int64_t o_strides[3], float* lse,
+                           int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with test controls: no flag is defined, `timeout_ns` bounds each wait (0: 1 s). */
+hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                              const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                              const int32_t* lengths, const int32_t* counts,
+                              void* O, const int64_t o_strides[3], float* lse,
+                              int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale,
+                              void* workspace, size_t workspace_bytes, uint32_t flags, uint64_t timeout_ns,
+                              void* stream);
+
+/* Bytes of workspace hk_attention_kv8 needs (0 for an empty problem). */
+size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq, int64_t max_pages);
 
 /* Static description of a status code. */
 const char* hk_status_string(hk_status status);
