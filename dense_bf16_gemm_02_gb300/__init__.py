@@ -15,7 +15,18 @@ from .hk_gemm import (HK_ACT_GELU, HK_ACT_NONE, HK_ACT_RELU, HK_ACT_SILU, HK_ERR
                       HK_FP4_MXFP4, HK_FP4_NVFP4, HK_TYPE_BF16, HK_TYPE_FP16, HK_TYPE_FP32, hk_fp4_dequantize,
                       hk_attention_kv8, hk_attention_kv8_workspace_size, hk_fp4_quantize, hk_fp4_scales_size,
                       hk_gemm_fp4, hk_gemm_fp4_ex, hk_kv8_append, hk_kv8_cache)
-from .low_precision import (Fp4Matrix, Kv8Cache, attention_kv8, dequantize_fp4, gemm_fp4, kv8_append, quantize_fp4)
+
+_LOW_PRECISION = ("Fp4Matrix", "quantize_fp4", "dequantize_fp4", "gemm_fp4", "Kv8Cache", "kv8_append", "attention_kv8")
+
+
+def __getattr__(name):
+    # the module that imports torch loads with the first use of one of its names
+    if name in _LOW_PRECISION:
+        from . import low_precision
+        globals().update({n: getattr(low_precision, n) for n in _LOW_PRECISION})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 __all__ = ["attention", "gemm", "Plan", "HKError", "load",
            "hk_gemm_bf16", "hk_gemm_bf16_epilogue", "hk_gemm_bf16_fused", "hk_gemm_bf16_noalloc", "hk_gemm_fp8_e4m3",

@@ -107,6 +107,8 @@ _lock = threading.Lock()
 def load() -> ctypes.CDLL:
     """Load the compiled library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
