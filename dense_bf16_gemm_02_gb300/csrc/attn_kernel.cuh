@@ -161,7 +161,7 @@ enum class Wait { kPoll, kSuspend };
 
 // Returns true when the wait must give up (this launch was aborted, or the
 // time limit ran out; then it records `code` and aborts the launch).
-__device__ __noinline__ bool attn_wait_expired(const AttnParams& p, uint64_t waited_ns, uint32_t code) {
+static __device__ __noinline__ bool attn_wait_expired(const AttnParams& p, uint64_t waited_ns, uint32_t code) {
     if (attn_aborted(p)) return true;
     if (waited_ns <= p.timeout_ns) return false;
     atomicOr(p.status, code);
@@ -197,42 +197,76 @@ __device__ __forceinline__ bool attn_wait_warp(const AttnParams& p, uint32_t bar
     return ok != 0;
 }
 
-// K/V blocks query tile `row0` needs: all of them, or (causal) those up to
-// the block holding the tile's last row. 0 for a tile entirely past S.
-__device__ __forceinline__ int tile_blocks(const AttnParams& p, int row0) {
-    if (row0 >= p.S) return 0;
-    if (!p.causal) return p.kv_blocks;
-    const int last = row0 / kBlockKV + 1;
-    return last < p.kv_blocks ? last : p.kv_blocks;
-}
-
-// One work item: two query tiles (256 rows) of one (batch, query head).
-// Items are numbered head-fastest, so the query heads of one KV group run
-// side by side; causal: the longest rows first.
+// One work item: two query tiles (256 rows) of one (batch, query head), or of
+// what the items' policy makes a row of.
 struct AttnItem {
     int bh, kvh, q0, n_t0, n_t1, n_all;
 };
 
-__device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int w) {
-    AttnItem it;
-    const int bh_count = p.B * p.Hq;
-    const int slot_q = w / bh_count;
-    it.bh = w - slot_q * bh_count;
-    const int qp = p.causal ? p.q_pairs - 1 - slot_q : slot_q;
-    const int b = it.bh / p.Hq;
-    const int h = it.bh - b * p.Hq;
-    it.kvh = b * p.Hkv + h / (p.Hq / p.Hkv);
-    it.q0 = qp * (kTiles * kTileQ);
-    it.n_t0 = tile_blocks(p, it.q0);
-    it.n_t1 = tile_blocks(p, it.q0 + kTileQ);
-    it.n_all = it.n_t0 > it.n_t1 ? it.n_t0 : it.n_t1;
-    return it;
-}
+// What the kernel works on. A policy says what item w is, how its query tiles
+// are loaded, which keys a row sees and where its output goes; the kernel's
+// schedule is the same for all. This one: contiguous Q, K, V and O of one
+// sequence length. Items are numbered head-fastest, so the query heads of one
+// KV group run side by side; causal: the longest rows first.
+struct ContiguousItems {
+    using Params = AttnParams;
+    static constexpr bool kEmptyRows = false;   // may a row see no key at all
 
-template <int kD>
+    // K/V blocks query tile `row0` needs: all of them, or (causal) those up to
+    // the block holding the tile's last row. 0 for a tile entirely past S.
+    static __device__ __forceinline__ int tile_blocks(const AttnParams& p, int row0) {
+        if (row0 >= p.S) return 0;
+        if (!p.causal) return p.kv_blocks;
+        const int last = row0 / kBlockKV + 1;
+        return last < p.kv_blocks ? last : p.kv_blocks;
+    }
+
+    static __device__ __forceinline__ AttnItem item(const AttnParams& p, int w) {
+        AttnItem it;
+        const int bh_count = p.B * p.Hq;
+        const int slot_q = w / bh_count;
+        it.bh = w - slot_q * bh_count;
+        const int qp = p.causal ? p.q_pairs - 1 - slot_q : slot_q;
+        const int b = it.bh / p.Hq;
+        const int h = it.bh - b * p.Hq;
+        it.kvh = b * p.Hkv + h / (p.Hq / p.Hkv);
+        it.q0 = qp * (kTiles * kTileQ);
+        it.n_t0 = tile_blocks(p, it.q0);
+        it.n_t1 = tile_blocks(p, it.q0 + kTileQ);
+        it.n_all = it.n_t0 > it.n_t1 ? it.n_t0 : it.n_t1;
+        return it;
+    }
+
+    // columns [64 c, 64 c + 64) of query tile t
+    static __device__ __forceinline__ void load_q(const AttnParams&, uint32_t dst, const void* tmap, const AttnItem& it,
+                                                  int t, int c, uint32_t bar) {
+        tma_load_3d(dst, tmap, c * 64, it.q0 + t * kTileQ, it.bh, bar);
+    }
+
+    // keys [0, key_end) are visible to row r of tile t
+    static __device__ __forceinline__ int key_end(const AttnParams& p, const AttnItem& it, int t, int r) {
+        const int q = it.q0 + t * kTileQ + r;
+        return p.causal ? (q + 1 < p.S ? q + 1 : p.S) : p.S;
+    }
+
+    // where row r of tile t goes: its output and log-sum-exp, or nowhere (a row past S)
+    struct Row {
+        bool live;
+        uint16_t* out;
+        float* lse;
+    };
+    template <int kD>
+    static __device__ __forceinline__ Row row(const AttnParams& p, const AttnItem& it, int t, int r) {
+        const int q = it.q0 + t * kTileQ + r;
+        const int64_t at = static_cast<int64_t>(it.bh) * p.S + q;
+        return Row{q < p.S, p.O + at * kD, p.lse != nullptr ? p.lse + at : nullptr};
+    }
+};
+
+template <int kD, class Items = ContiguousItems>
 __global__ void __launch_bounds__(AttnGeometry<kD>::kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
+                const __grid_constant__ CUtensorMap tmap_v, const typename Items::Params p) {
     using G = AttnGeometry<kD>;
     constexpr int kWarpTma = G::kWarpTma;
     constexpr int kWarpMma = G::kWarpMma;
@@ -303,7 +337,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             uint32_t ring_ph = 0;  // its phase: flips each time the ring wraps
             int li = 0;      // items done by this CTA
             for (int w = first_item; w < p.n_items && !abort_seen; w += item_step, ++li) {
-                const AttnItem it = attn_item(p, w);
+                const AttnItem it = Items::item(p, w);
                 // Q of this item once both issuers have finished the previous item's S
                 if (li > 0 && !attn_wait(p, q_empty, (li - 1) & 1, kErrTmaEmpty, Wait::kSuspend)) {
                     abort_seen = true;
@@ -313,8 +347,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * G::kTileBytes));
                 for (int t = 0; t < tiles; ++t)
                     for (int c = 0; c < G::kChunks; ++c)
-                        tma_load_3d(base + G::kOffQ + t * G::kTileBytes + c * G::kChunkBytes, &tmap_q, c * 64,
-                                    it.q0 + t * kTileQ, it.bh, q_full);
+                        Items::load_q(p, base + G::kOffQ + t * G::kTileBytes + c * G::kChunkBytes, &tmap_q, it, t, c, q_full);
                 for (int u = 0; u < 2 * it.n_all && !abort_seen; ++u) {
                     const int s = slot;
                     const uint32_t parity = ring_ph ^ 1u;
@@ -375,7 +408,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             bool any_block = false;  // has this tile had a block before (then S waits for s_free)
             int li = 0;
             for (int w = first_item; w < p.n_items && !abort_seen; w += item_step, ++li) {
-                const AttnItem it = attn_item(p, w);
+                const AttnItem it = Items::item(p, w);
                 const int n = t ? it.n_t1 : it.n_t0;
                 const int n_all = it.n_all;
                 if (!wait(q_full, li & 1, kErrMmaKv)) break;
@@ -483,10 +516,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         for (int w = first_item; w < p.n_items && !abort_seen; w += item_step) {
             int n, key_end;
             {
-                const AttnItem it = attn_item(p, w);
+                const AttnItem it = Items::item(p, w);
                 n = t ? it.n_t1 : it.n_t0;
-                const int q = it.q0 + t * kTileQ + r;       // this thread's query row
-                key_end = p.causal ? (q + 1 < p.S ? q + 1 : p.S) : p.S;   // keys [0, key_end) are visible
+                key_end = Items::key_end(p, it, t, r);   // this thread's query row sees keys [0, key_end)
             }
             float m = 0.0f;   // running max of the scaled scores (log2 units) used for P
             float l = 0.0f;   // running sum of P (of this thread's columns)
@@ -539,7 +571,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     }
                     mx = fmaxf(mx, other);
                 }
-                const float m_blk = mx * c;
+                float m_blk = mx * c;
+                // (a row that sees no key: any finite maximum makes its weights 0)
+                if constexpr (Items::kEmptyRows)
+                    if (m_blk == -INFINITY) m_blk = j == 0 ? 0.0f : m;
                 float alpha = 1.0f;
                 if (j == 0) {
                     m = m_blk;
@@ -656,10 +691,11 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     float l_other = 0.0f;
                     if constexpr (kSplit > 1) abort_seen = !exchange(l, l_other);   // the row sum over both halves
                     l += l_other;
-                    const AttnItem it = attn_item(p, w);
-                    const int q = abort_seen ? p.S : it.q0 + t * kTileQ + r;   // no stores after a failed exchange
-                    const float inv_l = 1.0f / l;
-                    uint16_t* out = p.O + (static_cast<int64_t>(it.bh) * p.S + q) * kD;
+                    const AttnItem it = Items::item(p, w);
+                    const auto row = Items::template row<kD>(p, it, t, r);
+                    const bool live = row.live && !abort_seen;   // no stores after a failed exchange
+                    const float inv_l = Items::kEmptyRows && l == 0.0f ? 0.0f : 1.0f / l;
+                    uint16_t* const out = row.out;
 #pragma unroll
                     for (int cc = 0; cc < kD / 32 / kSplit; ++cc) {
                         const int col = 32 * (cc + half * (kD / 32 / kSplit));
@@ -671,16 +707,25 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         for (int e = 0; e < 16; ++e)
                             pk[e] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(o[2 * e]) * inv_l),
                                                    __float_as_uint(__uint_as_float(o[2 * e + 1]) * inv_l));
-                        if (q < p.S) {
+                        if (live) {
 #pragma unroll
                             for (int w4 = 0; w4 < 4; ++w4)
                                 st_global_v4(out + col + 8 * w4, pk[4 * w4], pk[4 * w4 + 1], pk[4 * w4 + 2],
                                              pk[4 * w4 + 3]);
                         }
                     }
-                    if (p.lse != nullptr && q < p.S && half == 0)
-                        p.lse[static_cast<int64_t>(it.bh) * p.S + q] = (m + log2f(l)) * 0.69314718055994531f;
+                    if (row.lse != nullptr && live && half == 0) *row.lse = (m + log2f(l)) * 0.69314718055994531f;
                     tc_fence_before_sync();
+                }
+            }
+            if constexpr (Items::kEmptyRows) {
+                if (!abort_seen && n == 0) {   // no row of the tile sees a key
+                    const AttnItem it = Items::item(p, w);
+                    const auto row = Items::template row<kD>(p, it, t, r);
+                    if (row.live) {
+                        for (int col = 0; col < kD; col += 8) st_global_v4(row.out + col, 0, 0, 0, 0);
+                        if (row.lse != nullptr) *row.lse = -INFINITY;
+                    }
                 }
             }
             jp ^= static_cast<uint32_t>(n & 1);

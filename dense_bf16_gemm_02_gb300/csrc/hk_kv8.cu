@@ -15,6 +15,7 @@
 #include "host_internal.h"
 #include "kv8_append.cuh"
 #include "kv8_decode.cuh"
+#include "kv8_prefill.cuh"
 
 namespace {
 
@@ -105,6 +106,12 @@ cudaError_t setup_decode() {
     return cudaFuncSetAttribute(kv8_decode_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeGeometry<kD>::kSmemBytes);
 }
 
+template <int kD>
+cudaError_t setup_prefill() {
+    return cudaFuncSetAttribute(hk::attn::attn_fwd_kernel<kD, CachedItems>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                hk::attn::AttnGeometry<kD>::kSmemBytes);
+}
+
 hk_status setup(int device) {
     std::lock_guard<std::mutex> lock(g_setup_mutex);
     if (g_setup[device]) return HK_OK;
@@ -112,6 +119,8 @@ hk_status setup(int device) {
     if (e == cudaSuccess) e = setup_decode<64, __half>();
     if (e == cudaSuccess) e = setup_decode<128, __nv_bfloat16>();
     if (e == cudaSuccess) e = setup_decode<128, __half>();
+    if (e == cudaSuccess) e = setup_prefill<64>();
+    if (e == cudaSuccess) e = setup_prefill<128>();
     if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring the cache attention kernels", e);
     g_setup[device] = true;
     return HK_OK;
@@ -132,6 +141,69 @@ DecodeWorkspace decode_workspace(int64_t D) {
     return w;
 }
 
+// Rows of a KV head (query tokens times heads) from which the tensor-core
+// kernel takes the work: below it the keys and values are read once or a few
+// times as codes, above it they are brought to bf16 first.
+constexpr int64_t kPrefillRows = 64;
+
+// Sequences that are brought to bf16 at a time: as many as fit 512 MB, one at least.
+constexpr int64_t kWidenBytes = int64_t(512) << 20;
+
+struct PrefillWorkspace {
+    int64_t rows, seqs;      // rows of a head, sequences at a time
+    size_t half, total;      // bytes of the keys (the values follow), of both
+};
+
+PrefillWorkspace prefill_workspace(const hk_kv8_cache* c, int64_t B, int64_t max_pages) {
+    PrefillWorkspace w;
+    w.rows = max_pages * c->page_size;
+    const int64_t one = 2 * w.rows * c->heads * c->head_dim * 2;
+    w.seqs = std::max<int64_t>(1, std::min<int64_t>(B, kWidenBytes / one));
+    w.seqs = std::min<int64_t>(w.seqs, 65535);
+    w.half = static_cast<size_t>(w.seqs * one / 2);
+    w.total = 2 * w.half;
+    return w;
+}
+
+// Queries as [B, T, heads, D] in boxes of 64 columns × `pack` heads × 128 / pack tokens.
+hk_status encode_queries(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* q, const int64_t strides[3],
+                         int64_t B, int64_t T, int64_t Hq, int64_t D, int pack) {
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(T),
+                          static_cast<cuuint64_t>(B)};
+    // (the stride of a dimension of one is never used, but has to be a valid one)
+    cuuint64_t st[3] = {static_cast<cuuint64_t>(Hq > 1 ? strides[2] * 2 : 16), static_cast<cuuint64_t>(T > 1 ? strides[1] * 2 : 16),
+                        static_cast<cuuint64_t>(B > 1 ? strides[0] * 2 : 16)};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(pack), static_cast<cuuint32_t>(hk::attn::kTileQ / pack), 1};
+    cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, st, box, elem_strides,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of the queries failed (CUresult %d)", (int)r);
+    return HK_OK;
+}
+
+// bf16 keys or values as [heads, rows, D] in boxes of 64 columns × 128 rows.
+hk_status encode_wide(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, int64_t heads, int64_t rows,
+                      int64_t D) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(rows * D) * 2};
+    cuuint32_t box[3] = {64, 128, 1};
+    cuuint32_t elem_strides[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, elem_strides,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of the workspace failed (CUresult %d)", (int)r);
+    return HK_OK;
+}
+
+template <int kD>
+void launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillParams& p, int sms,
+                    cudaStream_t st) {
+    using G = hk::attn::AttnGeometry<kD>;
+    hk::attn::attn_fwd_kernel<kD, CachedItems>
+        <<<static_cast<unsigned>(std::min(p.n_items, sms)), G::kThreads, G::kSmemBytes, st>>>(tq, tk, tv, p);
+}
+
 template <int kD, typename T>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, cudaStream_t st) {
     kv8_decode_kernel<kD, T><<<static_cast<unsigned>(blocks), 32 * kDecodeWarps, DecodeGeometry<kD>::kSmemBytes, st>>>(tk, tv, p);
@@ -148,6 +220,83 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kv8_combine_kernel<kD, T>, p, warps_per_row);
+}
+
+// Many query rows per KV head: the sequences' keys and values to bf16, then the
+// attention-forward kernel, for as many sequences at a time as the workspace holds.
+hk_status prefill(const void* Q, const int64_t q_strides[3], const hk_kv8_cache* c, const int32_t* table, int64_t table_stride,
+                  int64_t max_pages, const int32_t* lengths, const int32_t* counts, void* O, const int64_t o_strides[3],
+                  float* lse, int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale_log2, void* workspace,
+                  uint32_t* status, uint64_t timeout_ns, PFN_cuTensorMapEncodeTiled_v12000 enc, int sms, cudaStream_t st) {
+    const PrefillWorkspace ws = prefill_workspace(c, B, max_pages);
+    char* const wide[2] = {static_cast<char*>(workspace), static_cast<char*>(workspace) + ws.half};
+    const int64_t group = Hq / c->heads;
+    int pack_shift = 0;                            // all heads of a KV head share a tile, where they divide it evenly
+    while (pack_shift < 7 && group % (int64_t(2) << pack_shift) == 0) ++pack_shift;
+    hk_status s;
+    for (int64_t b0 = 0; b0 < B; b0 += ws.seqs) {
+        const int64_t n = std::min(ws.seqs, B - b0);
+        WidenParams w = {};
+        w.codes[0] = static_cast<const uint8_t*>(c->k_codes);
+        w.codes[1] = static_cast<const uint8_t*>(c->v_codes);
+        w.scale[0] = c->k_scale;
+        w.scale[1] = c->v_scale;
+        w.out[0] = reinterpret_cast<uint16_t*>(wide[0]);
+        w.out[1] = reinterpret_cast<uint16_t*>(wide[1]);
+        w.table = table + b0 * table_stride;
+        w.table_stride = table_stride;
+        w.lengths = lengths + b0;
+        w.counts = counts ? counts + b0 : nullptr;
+        w.rows = ws.rows;
+        w.num_pages = c->num_pages;
+        w.T = static_cast<int32_t>(T);
+        w.Hkv = c->heads;
+        w.D = c->head_dim;
+        w.page_size = c->page_size;
+        w.max_pages = static_cast<int32_t>(max_pages);
+        w.status = status;
+
+        const int64_t tokens_per_pair = (hk::attn::kTiles * hk::attn::kTileQ) >> pack_shift;
+        const int64_t q_pairs = ceil_div(T, tokens_per_pair);
+        const int64_t items = n * (Hq >> pack_shift) * q_pairs;
+        if (items > kLimit || n * c->heads > kLimit || c->heads > 65535) return fail(HK_ERR_INVALID_ARG, "problem too large");
+        PrefillParams p = {};
+        p.B = static_cast<int32_t>(n);
+        p.Hq = static_cast<int32_t>(Hq);
+        p.Hkv = c->heads;
+        p.causal = causal ? 1 : 0;
+        p.q_pairs = static_cast<int32_t>(q_pairs);
+        p.n_items = static_cast<int32_t>(items);
+        p.scale_log2 = scale_log2;
+        p.O = static_cast<uint16_t*>(O) + b0 * o_strides[0];
+        p.lse = lse ? lse + b0 * T * Hq : nullptr;
+        p.status = status;
+        p.launch_id = hk_host::next_launch_id();
+        p.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
+        p.lengths = w.lengths;
+        p.counts = w.counts;
+        p.T = static_cast<int32_t>(T);
+        p.room = static_cast<int32_t>(ws.rows);
+        p.group = static_cast<int32_t>(group);
+        p.pack_shift = pack_shift;
+        p.o_stride_b = o_strides[0];
+        p.o_stride_t = o_strides[1];
+        p.o_stride_h = o_strides[2];
+        CUtensorMap tq, tk, tv;
+        if ((s = encode_queries(enc, &tq, static_cast<const uint16_t*>(Q) + b0 * q_strides[0], q_strides, n, T, Hq, c->head_dim,
+                                1 << pack_shift)) != HK_OK) return s;
+        if ((s = encode_wide(enc, &tk, wide[0], n * c->heads, ws.rows, c->head_dim)) != HK_OK) return s;
+        if ((s = encode_wide(enc, &tv, wide[1], n * c->heads, ws.rows, c->head_dim)) != HK_OK) return s;
+        const dim3 grid(static_cast<unsigned>(max_pages), static_cast<unsigned>(c->heads), static_cast<unsigned>(n));
+        kv8_widen_kernel<<<grid, 256, 0, st>>>(w);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache's conversion", e);
+        if (c->head_dim == 64) launch_prefill<64>(tq, tk, tv, p, sms, st);
+        else launch_prefill<128>(tq, tk, tv, p, sms, st);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache attention", e);
+    }
+    return HK_OK;
 }
 
 }  // namespace
@@ -213,9 +362,12 @@ extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, con
 
 extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                   int64_t max_pages) {
-    (void)max_pages;
-    if (!cache || B <= 0 || T <= 0 || Hq <= 0) return 0;
-    return decode_workspace(cache->head_dim).total;
+    if (!cache || cache->heads < 1 || cache->page_size < 1 || cache->head_dim < 1 || B <= 0 || T <= 0 || Hq <= 0 ||
+        max_pages <= 0 || max_pages > kLimit / cache->page_size)
+        return 0;
+    const size_t split = decode_workspace(cache->head_dim).total;
+    if (T <= kPrefillRows * cache->heads / Hq) return split;
+    return std::max(split, prefill_workspace(cache, B, max_pages).total);
 }
 
 extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
@@ -230,7 +382,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if (type != HK_TYPE_BF16 && type != HK_TYPE_FP16) return fail(HK_ERR_INVALID_ARG, "element type %d (bf16 or fp16)", (int)type);
     if (B < 0 || T < 0 || Hq < 0 || B > kLimit || T > kLimit || Hq > kLimit) return fail(HK_ERR_INVALID_ARG, "invalid size");
     if (Hq % cache->heads) return fail(HK_ERR_INVALID_ARG, "Hq=%lld is not a multiple of the cache's %d heads", (long long)Hq, (int)cache->heads);
-    if (!std::isfinite(scale)) return fail(HK_ERR_INVALID_ARG, "the scale must be finite");
+    if (!std::isfinite(scale) || scale < 0.0f) return fail(HK_ERR_INVALID_ARG, "the scale must be finite and not negative");
     if (B == 0 || T == 0 || Hq == 0) return HK_OK;
     if ((s = check_table(block_table, table_stride, max_pages, B, lengths, counts, cache->page_size)) != HK_OK) return s;
     if (!Q || !O || !q_strides || !o_strides) return fail(HK_ERR_INVALID_ARG, "null queries, output or strides");
@@ -239,8 +391,9 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if (T > kLimit / 16 / group || ceil_div(T * group, kRows) * (ceil_div(max_pages * cache->page_size, kTileKeys) + 1) > kLimit)
         return fail(HK_ERR_INVALID_ARG, "problem too large");
     const DecodeWorkspace ws = decode_workspace(cache->head_dim);
-    if (!workspace || workspace_bytes < ws.total)
-        return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", ws.total, workspace ? workspace_bytes : size_t(0));
+    const size_t need = hk_attention_kv8_workspace_size(cache, B, T, Hq, max_pages);
+    if (!workspace || workspace_bytes < need)
+        return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
     if (!aligned(workspace, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
     int device = 0, sms = 0;
     if ((s = current_device(&device, &sms)) != HK_OK) return s;
@@ -249,6 +402,16 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if ((s = hk_host::status_word(device, &status)) != HK_OK) return s;
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     if ((s = hk_host::tensor_map_encoder(&enc)) != HK_OK) return s;
+    const bool vec_q = aligned(Q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
+    const bool vec_o = aligned(O, 16) && o_strides[0] % 8 == 0 && o_strides[1] % 8 == 0 && o_strides[2] % 8 == 0;
+    const float scale_log2 = static_cast<float>(
+        1.4426950408889634 * (scale != 0.0f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->head_dim))));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // (the tensor-core kernel takes bf16 rows that TMA can read: aligned, and not one row for several places)
+    const bool spread = (B == 1 || q_strides[0] > 0) && (T == 1 || q_strides[1] > 0) && (Hq == 1 || q_strides[2] > 0);
+    if (T > kPrefillRows * cache->heads / Hq && type == HK_TYPE_BF16 && vec_q && vec_o && spread)
+        return prefill(Q, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse, B, T, Hq,
+                       causal, scale_log2, workspace, status, timeout_ns, enc, sms, st);
     CUtensorMap tk, tv;
     if ((s = encode_codes(enc, &tk, cache->k_codes, cache)) != HK_OK) return s;
     if ((s = encode_codes(enc, &tv, cache->v_codes, cache)) != HK_OK) return s;
@@ -260,8 +423,8 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.o_stride_b = o_strides[0];
     p.o_stride_t = o_strides[1];
     p.o_stride_h = o_strides[2];
-    p.vec_q = aligned(Q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
-    p.vec_o = aligned(O, 16) && o_strides[0] % 8 == 0 && o_strides[1] % 8 == 0 && o_strides[2] % 8 == 0;
+    p.vec_q = vec_q;
+    p.vec_o = vec_o;
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
     p.table_stride = table_stride;
@@ -275,8 +438,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.max_pages = static_cast<int32_t>(max_pages);
     p.num_pages = cache->num_pages;
     p.causal = causal ? 1 : 0;
-    p.scale_log2 = static_cast<float>(1.4426950408889634 * (scale != 0.0f ? static_cast<double>(scale)
-                                                                          : 1.0 / std::sqrt(static_cast<double>(cache->head_dim))));
+    p.scale_log2 = scale_log2;
     p.min_tiles = 2;
     char* const w = static_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(w);
@@ -284,7 +446,6 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.info = reinterpret_cast<int4*>(w + ws.info);
     p.wait.status = status;
     p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int blocks = 2 * std::min(sms, kSms);
     for (int64_t b0 = 0; b0 < B; b0 += kMaxBatch) {       // (launches of one stream: they may share the workspace)
         p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, kMaxBatch));

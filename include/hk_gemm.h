@@ -440,8 +440,9 @@ hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* B, const vo
  * with `table_stride` elements between rows: token j of sequence b lies in page
  * block_table[b][j / page_size] at place j % page_size. Entries past a
  * sequence's tokens are not read. A page index outside [0, num_pages) or a
- * length outside the table is never followed: those tokens are not written or
- * not attended to, and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG. */
+ * length outside the table is never followed: such tokens are not written, the
+ * output of such a sequence is unspecified (the others' is not), and
+ * hk_gemm_last_device_status reports HK_ERR_INVALID_ARG. */
 typedef struct hk_kv8_cache {
     void* k_codes;
     void* v_codes;
@@ -478,7 +479,8 @@ hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, const void* V,
  * stands at position lengths[b] - n + t, n = counts[b] (NULL: T), and sees the
  * tokens up to it (the queries' own keys are in the cache); else it sees all
  * lengths[b]. A query that sees no token, and queries t >= counts[b], give a row
- * of zeros and a log-sum-exp of -inf. `scale` 0: 1/sqrt(head_dim).
+ * of zeros and a log-sum-exp of -inf. `scale` must not be
+ * negative; 0: 1/sqrt(head_dim).
  * Q and O are [B, T, Hq, head_dim] of `type` (bf16 or fp16), strides (b, t, head)
  * in elements, contiguous rows. lse, when not NULL: fp32 [B, T, Hq], natural
  * log of the sum of exp(scale · q·k).
