@@ -203,6 +203,12 @@ struct AttnItem {
     int bh, kvh, q0, n_t0, n_t1, n_all;
 };
 
+// Where a row's output and log-sum-exp go (elements of O and of lse).
+struct AttnRow {
+    bool live;
+    int64_t out, lse;
+};
+
 // What the kernel works on. A policy says what item w is, how its query tiles
 // are loaded, which keys a row sees and where its output goes; the kernel's
 // schedule is the same for all. This one: contiguous Q, K, V and O of one
@@ -249,17 +255,12 @@ struct ContiguousItems {
         return p.causal ? (q + 1 < p.S ? q + 1 : p.S) : p.S;
     }
 
-    // where row r of tile t goes: its output and log-sum-exp, or nowhere (a row past S)
-    struct Row {
-        bool live;
-        uint16_t* out;
-        float* lse;
-    };
+    // where row r of tile t goes, if it is a row (not past S)
     template <int kD>
-    static __device__ __forceinline__ Row row(const AttnParams& p, const AttnItem& it, int t, int r) {
+    static __device__ __forceinline__ AttnRow row(const AttnParams& p, const AttnItem& it, int t, int r) {
         const int q = it.q0 + t * kTileQ + r;
         const int64_t at = static_cast<int64_t>(it.bh) * p.S + q;
-        return Row{q < p.S, p.O + at * kD, p.lse != nullptr ? p.lse + at : nullptr};
+        return AttnRow{q < p.S, at * kD, at};
     }
 };
 
@@ -692,10 +693,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                     if constexpr (kSplit > 1) abort_seen = !exchange(l, l_other);   // the row sum over both halves
                     l += l_other;
                     const AttnItem it = Items::item(p, w);
-                    const auto row = Items::template row<kD>(p, it, t, r);
-                    const bool live = row.live && !abort_seen;   // no stores after a failed exchange
+                    AttnRow row = Items::template row<kD>(p, it, t, r);
+                    if (abort_seen) row.live = false;   // no stores after a failed exchange
                     const float inv_l = Items::kEmptyRows && l == 0.0f ? 0.0f : 1.0f / l;
-                    uint16_t* const out = row.out;
+                    uint16_t* const out = p.O + row.out;
 #pragma unroll
                     for (int cc = 0; cc < kD / 32 / kSplit; ++cc) {
                         const int col = 32 * (cc + half * (kD / 32 / kSplit));
@@ -707,24 +708,24 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         for (int e = 0; e < 16; ++e)
                             pk[e] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(o[2 * e]) * inv_l),
                                                    __float_as_uint(__uint_as_float(o[2 * e + 1]) * inv_l));
-                        if (live) {
+                        if (row.live) {
 #pragma unroll
                             for (int w4 = 0; w4 < 4; ++w4)
                                 st_global_v4(out + col + 8 * w4, pk[4 * w4], pk[4 * w4 + 1], pk[4 * w4 + 2],
                                              pk[4 * w4 + 3]);
                         }
                     }
-                    if (row.lse != nullptr && live && half == 0) *row.lse = (m + log2f(l)) * 0.69314718055994531f;
+                    if (p.lse != nullptr && row.live && half == 0) p.lse[row.lse] = (m + log2f(l)) * 0.69314718055994531f;
                     tc_fence_before_sync();
                 }
             }
             if constexpr (Items::kEmptyRows) {
                 if (!abort_seen && n == 0) {   // no row of the tile sees a key
                     const AttnItem it = Items::item(p, w);
-                    const auto row = Items::template row<kD>(p, it, t, r);
+                    const AttnRow row = Items::template row<kD>(p, it, t, r);
                     if (row.live) {
-                        for (int col = 0; col < kD; col += 8) st_global_v4(row.out + col, 0, 0, 0, 0);
-                        if (row.lse != nullptr) *row.lse = -INFINITY;
+                        for (int col = 0; col < kD; col += 8) st_global_v4(p.O + row.out + col, 0, 0, 0, 0);
+                        if (p.lse != nullptr) p.lse[row.lse] = -INFINITY;
                     }
                 }
             }

@@ -86,19 +86,14 @@ struct CachedItems {
         return p.causal ? max(0, s.len - s.count + tok + 1) : s.len;
     }
 
-    struct Row {
-        bool live;
-        uint16_t* out;
-        float* lse;
-    };
     template <int kD>
-    static __device__ __forceinline__ Row row(const Params& p, const attn::AttnItem& it, int t, int r) {
+    static __device__ __forceinline__ attn::AttnRow row(const Params& p, const attn::AttnItem& it, int t, int r) {
         const int heads = p.Hq >> p.pack_shift;
         const int b = it.bh / heads;
         const int tok = (it.q0 + t * attn::kTileQ + r) >> p.pack_shift;
         const int head = ((it.bh - b * heads) << p.pack_shift) + (r & ((1 << p.pack_shift) - 1));
-        return Row{tok < p.T, p.O + b * p.o_stride_b + tok * p.o_stride_t + head * p.o_stride_h,
-                   p.lse != nullptr ? p.lse + (static_cast<int64_t>(b) * p.T + tok) * p.Hq + head : nullptr};
+        return attn::AttnRow{tok < p.T, b * p.o_stride_b + tok * p.o_stride_t + head * p.o_stride_h,
+                             (static_cast<int64_t>(b) * p.T + tok) * p.Hq + head};
     }
 };
 
