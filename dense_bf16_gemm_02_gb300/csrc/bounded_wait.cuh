@@ -46,6 +46,29 @@ __device__ __forceinline__ bool wait_mbar(WaitCtx c, uint32_t bar, uint32_t pari
     return wait_mbar_slow(c, bar, parity, code);
 }
 
+// For barriers that the peer CTA's threads arrive on with
+// mbar_arrive_cluster_relaxed (they order tcgen05 operations only).
+static __device__ __noinline__ bool wait_mbar_cluster_slow(WaitCtx c, uint32_t bar, uint32_t parity, uint32_t code) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_cluster_relaxed(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (wait_aborted(c)) return false;
+            if (global_timer_ns() - t0 > c.timeout_ns) {
+                atomicOr(c.status, code);
+                atomicExch(c.status + 1, c.launch_id);
+                __threadfence();
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_mbar_cluster(WaitCtx c, uint32_t bar, uint32_t parity, uint32_t code) {
+    if (mbar_try_wait_cluster_relaxed(bar, parity)) return true;
+    return wait_mbar_cluster_slow(c, bar, parity, code);
+}
+
 // A wait on the abort path (a copy or MMA that was issued signals `bar` when
 // it completes); gives up after 2 ms.
 __device__ __forceinline__ void wait_mbar_drain(uint32_t bar, uint32_t parity) {

@@ -39,6 +39,8 @@ struct Fp4Params {
     int32_t M, N;                      // rows of A (tokens) and of B (features)
     int32_t k_stages;                  // ceil(K / 256)
     int32_t tiles_m, tiles_n;
+    int32_t group_m;                   // pair kernel: tile rows that are swept together
+    int32_t total_units, tail_start;   // pair kernel: work units; tiles from here on run as two halves
     const uint8_t* sfa;                // scale tiles of A and B
     const uint8_t* sfb;
     const float* ga;                   // global scales, or null (1)
@@ -327,6 +329,338 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_one(tmem_base, G::kTmemCols);
+    }
+}
+
+// --------------------------------------------------- CTA-pair tile kernel --
+//
+// For many tokens: 256 × 256 tiles on a pair of CTAs (cta_group::2), a
+// persistent grid, roles by warp: 0 loads, 1 issues the MMAs (leader CTA), 2-5
+// store, 6 copies each stage's scales into Tensor Memory (leader CTA), so that
+// no copy stands between two MMAs in the issuing thread's stream.
+//
+// Tensor Memory holds two accumulators of 256 columns and a ring of scale
+// slots, which together need more than its 512 columns: the accumulators
+// OVERLAP by what is missing. The epilogue reads the overlapping columns of its
+// tile first and then lets the next tile's MMAs begin, so that they wait for a
+// few reads instead of a whole epilogue.
+template <int kFmt>
+struct PairGeometry {
+    static constexpr int kTile = 256;                                       // rows of A and of B per tile
+    static constexpr int kSfTiles = scale_tiles(kFmt);
+    static constexpr int kSfBytes = 512 * kSfTiles;                         // scales of 128 rows and a stage
+    static constexpr int kOpBytes = 128 * kStageRowBytes;                   // A or B rows of one CTA and stage
+    static constexpr int kStageSf = 3 * kSfBytes;                           // own A rows, both halves of B
+    static constexpr int kStageBytes = 2 * kOpBytes + kStageSf;
+    static constexpr int kStages = (kSmemLimit - 2048) / kStageBytes > 6 ? 6 : (kSmemLimit - 2048) / kStageBytes;
+    static_assert(kStages >= 4, "pipeline too shallow");
+    static constexpr int kSfCols = 12 * kSfTiles;                           // TMEM columns of a stage's scales
+    static constexpr int kSlots = kFmt == kMxfp4 ? 4 : 3;                   // scale slots
+    static constexpr int kColSf = 512 - kSlots * kSfCols;
+    static constexpr int kOverlap = 512 - kColSf;                           // columns that both accumulators use
+    static constexpr int kCol1 = 256 - kOverlap;                            // where accumulator 1 begins
+    static constexpr int kFirstChunks = (kOverlap + 31) / 32;               // 32-column chunks read before the hand-over
+    static constexpr int kOffA = 0;
+    static constexpr int kOffB = kStages * kOpBytes;
+    static constexpr int kOffSf = 2 * kStages * kOpBytes;
+    // full[S], empty[S], sf_full[slots], acc_full[2], acc_free, drain[2]
+    static constexpr int kOffBars = kOffSf + kStages * kStageSf;
+    static constexpr int kNumBars = 2 * kStages + kSlots + 5;
+    static constexpr int kOffHolder = kOffBars + kNumBars * 8;              // TMEM address, two flags
+    static constexpr int kSmemBytes = kOffHolder + 16 + 1024;
+    static_assert(kSmemBytes <= kSmemLimit, "shared memory");
+    static constexpr uint32_t kIdesc = idesc_fp4_f32(256, 256, kFmt);
+    static constexpr uint32_t kIdescHalf = idesc_fp4_f32(256, 128, kFmt);
+    static constexpr int kThreads = 224;
+};
+
+// Work unit u -> tile and half (-1: the whole tile).
+__device__ __forceinline__ void pair_unit(const Fp4Params& p, int u, int& tm, int& tn, int& half) {
+    int t = u;
+    half = -1;
+    if (u >= p.tail_start) {
+        t = p.tail_start + ((u - p.tail_start) >> 1);
+        half = (u - p.tail_start) & 1;
+    }
+    const int per_group = p.group_m * p.tiles_n;
+    const int g = t / per_group;
+    const int first_m = g * p.group_m;
+    const int rows = min(p.tiles_m - first_m, p.group_m);
+    const int local = t - g * per_group;
+    tm = first_m + local % rows;
+    tn = local / rows;
+}
+
+// 32 sums of one row to bf16, stored at columns [col, col + 32).
+__device__ __forceinline__ void store_sums(const Fp4Params& p, const uint32_t (&v)[32], float alpha, int row, int col) {
+    if (row >= p.M || col >= p.N) return;
+    uint16_t* const dst = p.c + static_cast<int64_t>(row) * p.ldc + col;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        w[i] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(v[2 * i]) * alpha), __float_as_uint(__uint_as_float(v[2 * i + 1]) * alpha));
+    if (p.vec_c && col + 32 <= p.N) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st_global_v4(dst + 8 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (col + e < p.N) dst[e] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
+    }
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(224, 1)
+gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                     const __grid_constant__ CUtensorMap tmap_b_half, const __grid_constant__ CUtensorMap tmap_sfa,
+                     const __grid_constant__ CUtensorMap tmap_sfb, const Fp4Params p) {
+    using G = PairGeometry<kFmt>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw);
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t lane = lane_id();
+    const uint32_t rank = cluster_cta_rank();
+    const int unit = blockIdx.x / 2, num_units = gridDim.x / 2;
+
+    auto full_bar = [&](int s) { return base + G::kOffBars + 8u * s; };
+    auto empty_bar = [&](int s) { return base + G::kOffBars + 8u * (G::kStages + s); };
+    auto sf_full_bar = [&](int j) { return base + G::kOffBars + 8u * (2 * G::kStages + j); };
+    auto acc_full_bar = [&](int b) { return base + G::kOffBars + 8u * (2 * G::kStages + G::kSlots + b); };
+    const uint32_t acc_free_bar = base + G::kOffBars + 8u * (2 * G::kStages + G::kSlots + 2);
+    auto drain_bar = [&](int i) { return base + G::kOffBars + 8u * (2 * G::kStages + G::kSlots + 3 + i); };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int j = 0; j < G::kSlots; ++j) mbar_init(sf_full_bar(j), 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full_bar(b), 1);
+            mbar_init(drain_bar(b), 1);
+        }
+        mbar_init(acc_free_bar, 8);            // four storing warps of each CTA
+        fence_mbar_init_cluster();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensor_map(&tmap_a);
+        prefetch_tensor_map(&tmap_b);
+        prefetch_tensor_map(&tmap_sfa);
+        prefetch_tensor_map(&tmap_sfb);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(base + G::kOffHolder, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    cluster_sync();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + G::kOffHolder);
+    bool ok = true;
+
+    if (warp == 0) {
+        // ------------------------------------------------------- loads --
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t fills = 0, dropped = -1;
+            for (int u = unit; u < p.total_units && ok; u += num_units) {
+                int tm, tn, half;
+                pair_unit(p, u, tm, tn, half);
+                const int a_row = tm * 256 + static_cast<int>(rank) * 128;
+                const int b_row = half < 0 ? tn * 256 + static_cast<int>(rank) * 128
+                                           : tn * 256 + half * 128 + static_cast<int>(rank) * 64;
+                const void* const b_map = half < 0 ? static_cast<const void*>(&tmap_b) : static_cast<const void*>(&tmap_b_half);
+                // rows of 256 bytes of the scale tiles: kSfBytes per 128 rows and stage
+                constexpr int kSfRows = G::kSfBytes / 256;
+                const int sfa_row = (tm * 2 + static_cast<int>(rank)) * p.k_stages * kSfRows;
+                const int sfb_row = (tn * 2 + (half > 0 ? 1 : 0)) * p.k_stages * kSfRows;
+                // (groups of rows past the matrix read as 0)
+                const uint32_t bytes = half < 0 ? 2u * (2 * G::kOpBytes + 3 * G::kSfBytes)
+                                                : 2u * (G::kOpBytes + G::kOpBytes / 2 + 2 * G::kSfBytes);
+                for (int ks = 0; ks < p.k_stages; ++ks) {
+                    if (!wait_mbar(p.wait, empty_bar(stage), phase ^ 1u, kErrWaitRing)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) {
+                        if ((p.flags & kFlagDropArrive) && dropped < 0) dropped = fills;   // test only: never armed
+                        else mbar_arrive_expect_tx(full_bar(stage), bytes);
+                    }
+                    const uint32_t full = map_to_cta(full_bar(stage), 0);
+                    const uint32_t sf = base + G::kOffSf + stage * G::kStageSf;
+                    tma_load_2d_pair(sf, &tmap_sfa, 0, sfa_row + ks * kSfRows, full);
+                    tma_load_2d_pair(sf + G::kSfBytes, &tmap_sfb, 0, sfb_row + ks * kSfRows, full);
+                    if (half < 0) tma_load_2d_pair(sf + 2 * G::kSfBytes, &tmap_sfb, 0, sfb_row + (p.k_stages + ks) * kSfRows, full);
+                    tma_load_2d_pair(base + G::kOffA + stage * G::kOpBytes, &tmap_a, ks * kStageRowBytes, a_row, full);
+                    tma_load_2d_pair(base + G::kOffB + stage * G::kOpBytes, b_map, ks * kStageRowBytes, b_row, full);
+                    ++fills;
+                    if (++stage == G::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (rank == 0 && (!ok || wait_aborted(p.wait)))     // the copies in flight land before the block ends
+                for (int64_t f = fills > G::kStages ? fills - G::kStages : 0; f < fills; ++f)
+                    if (f != dropped)
+                        wait_mbar_drain(full_bar(static_cast<int>(f % G::kStages)), static_cast<uint32_t>((f / G::kStages) & 1));
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------- MMAs --
+        if (rank == 0) {
+            int stage = 0, slot = 0, local = 0;
+            uint32_t phase = 0, slot_phase = 0;
+            for (int u = unit; u < p.total_units && ok; u += num_units, ++local) {
+                int tm, tn, half;
+                pair_unit(p, u, tm, tn, half);
+                const uint32_t idesc = half < 0 ? G::kIdesc : G::kIdescHalf;
+                const uint32_t d_tmem = tmem_base + (local & 1 ? G::kCol1 : 0);
+                // the previous tile's epilogue has read the columns this accumulator shares with it
+                if (local > 0 && !__all_sync(0xffffffffu, wait_mbar_cluster(p.wait, acc_free_bar, (local - 1) & 1, kErrWaitAcc))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                for (int ks = 0; ks < p.k_stages; ++ks) {
+                    if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(stage), phase, kErrWaitData) &&
+                                                     wait_mbar(p.wait, sf_full_bar(slot), slot_phase, kErrWaitData))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t ad = smem_desc_kmajor_sw128(base + G::kOffA + stage * G::kOpBytes);
+                    const uint64_t bd = smem_desc_kmajor_sw128(base + G::kOffB + stage * G::kOpBytes);
+                    const uint32_t sf = tmem_base + G::kColSf + slot * G::kSfCols;
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 0; k < kMmasPerStage; ++k) {
+                            const uint32_t id = mma_scale_id<kFmt>(k);
+                            // slot: a stage's tiles in order, of each first A's, then B's two groups
+                            const uint32_t at = sf + 12 * mma_scale_tile<kFmt>(k);
+                            mma_fp4<2, kFmt>(d_tmem, ad + 2u * k, bd + 2u * k, idesc | (id << 4) | (id << 29), at, at + 4,
+                                             (ks > 0 || k > 0) ? 1u : 0u);
+                        }
+                        mma_commit_pair_mask(empty_bar(stage), 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == G::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++slot == G::kSlots) {
+                        slot = 0;
+                        slot_phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (lane == 0) mma_commit_pair_mask(acc_full_bar(local & 1), 0x3);
+                __syncwarp();
+            }
+            if (!ok || wait_aborted(p.wait)) {      // everything issued completes before TMEM is freed
+                if (lane == 0) {
+                    mma_commit_pair_mask(drain_bar(0), 0x1);
+                    wait_mbar_drain(drain_bar(0), 0);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------ scale copies --
+        if (rank == 0 && lane == 0) {
+            int stage = 0, slot = 0;
+            uint32_t phase = 0;
+            int64_t it = 0;
+            for (int u = unit; u < p.total_units && ok; u += num_units) {
+                int tm, tn, half;
+                pair_unit(p, u, tm, tn, half);
+                for (int ks = 0; ks < p.k_stages; ++ks, ++it) {
+                    // the slot is free once the MMAs of the stage kSlots before have completed: the phase
+                    // of that stage's empty barrier (it cannot run on past it, since the MMAs need this copy)
+                    const int64_t old = it - G::kSlots;
+                    if (!wait_mbar(p.wait, full_bar(stage), phase, kErrWaitData) ||
+                        (old >= 0 && !wait_mbar(p.wait, empty_bar(static_cast<int>(old % G::kStages)),
+                                                static_cast<uint32_t>((old / G::kStages) & 1), kErrWaitRing))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t src = base + G::kOffSf + stage * G::kStageSf;
+                    const uint32_t dst = tmem_base + G::kColSf + slot * G::kSfCols;
+                    const int groups = half < 0 ? 3 : 2;
+#pragma unroll
+                    for (int q = 0; q < G::kSfTiles; ++q)
+                        for (int j = 0; j < groups; ++j)
+                            tmem_cp_128x16b_pair(dst + 12 * q + 4 * j, smem_desc_plain(src + j * G::kSfBytes + 512 * q, 16, 128));
+                    mma_commit_pair_mask(sf_full_bar(slot), 0x1);
+                    if (++stage == G::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++slot == G::kSlots) slot = 0;
+                }
+            }
+            if (!ok || wait_aborted(p.wait)) {
+                mma_commit_pair_mask(drain_bar(1), 0x1);
+                wait_mbar_drain(drain_bar(1), 0);
+            }
+        }
+    } else {
+        // ----------------------------------------------------- epilogue --
+        const uint32_t q = warp & 3u;                 // TMEM lanes 32 q .. 32 q + 31
+        const float alpha = global_alpha(p);
+        int local = 0;
+        for (int u = unit; u < p.total_units; u += num_units, ++local) {
+            int tm, tn, half;
+            pair_unit(p, u, tm, tn, half);
+            const int buf = local & 1;
+            {
+                // one thread waits, suspended; the four warps meet at a named barrier (a flag per parity)
+                volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(smem + G::kOffHolder + 4) + buf;
+                if (warp == 2 && lane == 0)
+                    *flag = wait_mbar(p.wait, acc_full_bar(buf), (local >> 1) & 1, kErrWaitAcc) ? 1u : 0u;
+                __syncwarp();
+                named_barrier_sync(1, 128);
+                if (*flag == 0u) {
+                    ok = false;
+                    break;
+                }
+            }
+            tc_fence_after_sync();
+            const int row = tm * 256 + static_cast<int>(rank * 128 + q * 32 + lane);
+            const int col0 = tn * 256 + (half > 0 ? 128 : 0);
+            const int chunks = half < 0 ? 8 : 4;
+            const uint32_t t_row = tmem_base + ((q * 32u) << 16) + (buf ? G::kCol1 : 0);
+            // accumulator 0 shares its last columns, accumulator 1 its first: those are read first
+            auto chunk_of = [&](int i) { return buf ? i : chunks - 1 - i; };
+            uint32_t v[G::kFirstChunks][32];
+#pragma unroll
+            for (int i = 0; i < G::kFirstChunks; ++i)
+                if (i < chunks) tmem_load_32cols(t_row + 32 * chunk_of(i), v[i]);
+            tmem_wait_ld();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(map_to_cta(acc_free_bar, 0));
+#pragma unroll
+            for (int i = 0; i < G::kFirstChunks; ++i)
+                if (i < chunks) store_sums(p, v[i], alpha, row, col0 + 32 * chunk_of(i));
+#pragma unroll 1
+            for (int i = G::kFirstChunks; i < chunks; ++i) {
+                tmem_load_32cols(t_row + 32 * chunk_of(i), v[0]);
+                tmem_wait_ld();
+                store_sums(p, v[0], alpha, row, col0 + 32 * chunk_of(i));
+            }
+            tc_fence_before_sync();
+        }
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, 512);
     }
 }
 

@@ -125,6 +125,18 @@ const SingleVariant kSingle[2][4] = {
     {single_variant<16, kNvfp4>(), single_variant<32, kNvfp4>(), single_variant<64, kNvfp4>(), single_variant<128, kNvfp4>()},
 };
 
+using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Fp4Params);
+
+struct PairVariant {
+    PairFn fn;
+    int smem, threads;
+};
+
+const PairVariant kPair[2] = {
+    {&gemm_fp4_pair_kernel<kMxfp4>, PairGeometry<kMxfp4>::kSmemBytes, PairGeometry<kMxfp4>::kThreads},
+    {&gemm_fp4_pair_kernel<kNvfp4>, PairGeometry<kNvfp4>::kSmemBytes, PairGeometry<kNvfp4>::kThreads},
+};
+
 std::mutex g_setup_mutex;
 bool g_setup[kMaxDevices] = {};
 
@@ -137,6 +149,11 @@ hk_status setup(int device) {
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
             if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring a 4-bit product kernel", e);
         }
+    for (const PairVariant& v : kPair) {
+        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(v.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             v.smem);
+        if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring a 4-bit product kernel", e);
+    }
     g_setup[device] = true;
     return HK_OK;
 }
@@ -155,6 +172,59 @@ hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, 
     if (r != CUDA_SUCCESS)
         return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of %s failed (CUresult %d)", name, (int)r);
     return HK_OK;
+}
+
+// Scale tiles as rows of 256 bytes, in boxes of one stage's tiles of 128 matrix rows.
+hk_status encode_scales(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
+                        int32_t format, const char* name) {
+    const int64_t bytes = static_cast<int64_t>(hk_fp4_scales_size(rows, cols, format));
+    cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(bytes / 256)};
+    cuuint64_t strides[1] = {256};
+    cuuint32_t box[2] = {256, static_cast<cuuint32_t>(2 * scale_tiles(format))};
+    cuuint32_t elem_strides[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, elem_strides,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of %s failed (CUresult %d)", name, (int)r);
+    return HK_OK;
+}
+
+// Many tokens: 256 × 256 tiles on CTA pairs.
+hk_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 enc, Fp4Params p, const void* A, const void* B, int64_t K, int64_t lda,
+                      int64_t ldb, int32_t format, int sm_count, cudaStream_t st) {
+    hk_status s;
+    p.tiles_m = static_cast<int32_t>(ceil_div(p.M, 256));
+    p.tiles_n = static_cast<int32_t>(ceil_div(p.N, 256));
+    p.group_m = 8;
+    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
+    const int64_t units = sm_count / 2;
+    // the last round's tiles, when they fill at most half of the pairs, run as two halves each
+    const int64_t last = tiles - (ceil_div(tiles, units) - 1) * units;
+    const bool halves = 2 * last <= units;
+    p.tail_start = static_cast<int32_t>(halves ? tiles - last : tiles);
+    p.total_units = static_cast<int32_t>(halves ? tiles + last : tiles);
+    CUtensorMap ta, tb, tbh, tsa, tsb;
+    if ((s = encode_codes(enc, &ta, A, p.M, K, lda, 128, "A")) != HK_OK) return s;
+    if ((s = encode_codes(enc, &tb, B, p.N, K, ldb, 128, "B")) != HK_OK) return s;
+    if ((s = encode_codes(enc, &tbh, B, p.N, K, ldb, 64, "B")) != HK_OK) return s;
+    if ((s = encode_scales(enc, &tsa, p.sfa, p.M, K, format, "A's scales")) != HK_OK) return s;
+    if ((s = encode_scales(enc, &tsb, p.sfb, p.N, K, format, "B's scales")) != HK_OK) return s;
+    const PairVariant& v = kPair[format == HK_FP4_NVFP4];
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, p.total_units)));
+    cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, ta, tb, tbh, tsa, tsb, p);
+    return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the 4-bit product", e);
 }
 
 // K parts of a tile: the most that keep the launch within one round of
@@ -228,11 +298,15 @@ extern "C" hk_status hk_fp4_dequantize(const void* codes, int64_t ld_codes, cons
 
 extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* B, const void* SFB, void* C, int64_t M,
                                     int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc, int32_t format,
-                                    const float* global_a, const float* global_b, uint32_t flags, uint64_t timeout_ns,
-                                    void* stream) {
+                                    const float* global_a, const float* global_b, int32_t kernel, int32_t split_k,
+                                    uint32_t flags, uint64_t timeout_ns, void* stream) {
     hk_status s = check_format(format);
     if (s != HK_OK) return s;
     if (flags & ~HK_FLAG_FAULT_DROP_ARRIVE) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if (kernel != HK_KERNEL_AUTO && kernel != HK_KERNEL_PAIR_256x256 && kernel != HK_KERNEL_SINGLE_128x128)
+        return fail(HK_ERR_INVALID_ARG, "unknown kernel id %d", (int)kernel);
+    if (split_k != 0 && split_k != 1 && split_k != 2 && split_k != 4 && split_k != 8)
+        return fail(HK_ERR_INVALID_ARG, "split_k %d (0, 1, 2, 4 or 8)", (int)split_k);
     if (M < 0 || N < 0 || K < 0) return fail(HK_ERR_INVALID_ARG, "negative size");
     if (ldc < N) return fail(HK_ERR_INVALID_ARG, "leading dimension of C below N");
     if (M == 0 || N == 0) return HK_OK;
@@ -243,6 +317,7 @@ extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* 
     if (!aligned(C, 2) || !aligned(global_a, 4) || !aligned(global_b, 4))
         return fail(HK_ERR_MISALIGNED, "a pointer is not aligned to its elements");
     if (ceil_div(M, 16) * ceil_div(N, 128) > (int64_t(1) << 26)) return fail(HK_ERR_INVALID_ARG, "too many output tiles");
+    if ((std::max(M, N) + 512) * (K + 256) > (int64_t(1) << 42)) return fail(HK_ERR_INVALID_ARG, "matrix of 2^42 elements or more");
     int device = 0, sms = 0;
     if ((s = current_device(&device, &sms)) != HK_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -273,6 +348,8 @@ extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* 
     p.wait.launch_id = hk_host::next_launch_id();
     p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
 
+    if (kernel == HK_KERNEL_PAIR_256x256 || (kernel == HK_KERNEL_AUTO && M > 128))
+        return launch_pair(enc, p, A, B, K, lda, ldb, format, sms, st);
     // the narrowest tile that holds every token: the MMA's time and a stage's shared memory grow with it
     const SingleVariant* v = &kSingle[format == HK_FP4_NVFP4][3];
     for (int i = 2; i >= 0; --i)
@@ -280,7 +357,8 @@ extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* 
     p.tiles_m = static_cast<int32_t>(ceil_div(M, v->tok));
     p.tiles_n = static_cast<int32_t>(ceil_div(N, 128));
     const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
-    const int splits = choose_splits(tiles, p.k_stages, sms);
+    int splits = split_k ? split_k : choose_splits(tiles, p.k_stages, sms);
+    while (splits > p.k_stages) splits /= 2;     // every part owns at least one stage
     CUtensorMap ta, tb;
     if ((s = encode_codes(enc, &ta, A, M, K, lda, static_cast<uint32_t>(v->tok), "A")) != HK_OK) return s;
     if ((s = encode_codes(enc, &tb, B, N, K, ldb, 128, "B")) != HK_OK) return s;
@@ -303,5 +381,6 @@ extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* 
 extern "C" hk_status hk_gemm_fp4(const void* A, const void* SFA, const void* B, const void* SFB, void* C, int64_t M,
                                  int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc, int32_t format,
                                  const float* global_a, const float* global_b, void* stream) {
-    return hk_gemm_fp4_ex(A, SFA, B, SFB, C, M, N, K, lda, ldb, ldc, format, global_a, global_b, 0u, 0u, stream);
+    return hk_gemm_fp4_ex(A, SFA, B, SFB, C, M, N, K, lda, ldb, ldc, format, global_a, global_b, HK_KERNEL_AUTO, 0, 0u, 0u,
+                          stream);
 }

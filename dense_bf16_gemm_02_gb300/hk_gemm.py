@@ -171,7 +171,7 @@ def load() -> ctypes.CDLL:
         lib.hk_fp4_dequantize.restype = I32
         lib.hk_gemm_fp4.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, P, P]
         lib.hk_gemm_fp4.restype = I32
-        lib.hk_gemm_fp4_ex.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, P, U32, U64, P]
+        lib.hk_gemm_fp4_ex.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, P, I32, I32, U32, U64, P]
         lib.hk_gemm_fp4_ex.restype = I32
         CP, F = ctypes.POINTER(hk_kv8_cache), ctypes.c_float
         lib.hk_kv8_append.argtypes = [CP, P, P, I32, I64, I64, P, P, P, I64, I64, P, P, P]
@@ -275,10 +275,10 @@ def hk_gemm_fp4(A: int, SFA: int, B: int, SFB: int, C: int, M: int, N: int, K: i
 
 
 def hk_gemm_fp4_ex(A: int, SFA: int, B: int, SFB: int, C: int, M: int, N: int, K: int, lda: int, ldb: int, ldc: int,
-                   format: int, global_a: int = 0, global_b: int = 0, flags: int = 0, timeout_ns: int = 0,
-                   stream: int = 0) -> int:
+                   format: int, global_a: int = 0, global_b: int = 0, kernel: int = 0, split_k: int = 0,
+                   flags: int = 0, timeout_ns: int = 0, stream: int = 0) -> int:
     return load().hk_gemm_fp4_ex(A, SFA, B, SFB, C, M, N, K, lda, ldb, ldc, format, global_a or None,
-                                 global_b or None, flags, timeout_ns, stream)
+                                 global_b or None, kernel, split_k, flags, timeout_ns, stream)
 
 
 def hk_kv8_append(cache: hk_kv8_cache, K: int, V: int, type: int, B: int, T: int, k_strides, v_strides,

@@ -416,13 +416,16 @@ hk_status hk_gemm_fp4(const void* A, const void* SFA, const void* B, const void*
                       int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
                       int32_t format, const float* global_a, const float* global_b, void* stream);
 
-/* The same with test controls: `flags` takes HK_FLAG_FAULT_DROP_ARRIVE (the
- * first stage is never filled, so a bounded wait runs out), `timeout_ns`
- * bounds each wait (0: 1 s). */
+/* The same with tuning and test controls: `kernel` is HK_KERNEL_AUTO (chosen by
+ * shape), HK_KERNEL_PAIR_256x256 (CTA pairs) or HK_KERNEL_SINGLE_128x128 (one
+ * CTA, tiles of 128 rows of B × 16 to 128 rows of A, K cut into `split_k` parts
+ * of a cluster: 0 chosen, 1, 2, 4 or 8); `flags` takes
+ * HK_FLAG_FAULT_DROP_ARRIVE (the first stage is never filled, so a bounded wait
+ * runs out), `timeout_ns` bounds each wait (0: 1 s). */
 hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* B, const void* SFB, void* C,
                          int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc,
                          int32_t format, const float* global_a, const float* global_b,
-                         uint32_t flags, uint64_t timeout_ns, void* stream);
+                         int32_t kernel, int32_t split_k, uint32_t flags, uint64_t timeout_ns, void* stream);
 
 /* ---------------------------------------------------------------------------
  * A paged key/value cache held in 8 bits, the append to it and attention over it.

@@ -41,15 +41,16 @@ def test_product_refusals(lib):
     from dense_bf16_gemm_02_gb300 import hk_gemm as h
     INV, MIS = h.HK_ERR_INVALID_ARG, h.HK_ERR_MISALIGNED
 
-    def g(A=P, SA=P, B=P, SB=P, C=P, M=8, N=8, K=64, lda=32, ldb=32, ldc=8, fmt=1, ga=None, gb=None, flags=0):
-        return lib.hk_gemm_fp4_ex(A, SA, B, SB, C, M, N, K, lda, ldb, ldc, fmt, ga, gb, flags, 0, None)
+    def g(A=P, SA=P, B=P, SB=P, C=P, M=8, N=8, K=64, lda=32, ldb=32, ldc=8, fmt=1, ga=None, gb=None, flags=0,
+          kernel=0, split=0):
+        return lib.hk_gemm_fp4_ex(A, SA, B, SB, C, M, N, K, lda, ldb, ldc, fmt, ga, gb, kernel, split, flags, 0, None)
     assert g(M=0, A=None) == h.HK_OK and g(N=0, ldc=0, B=None) == h.HK_OK
     assert g(M=-1) == INV and g(K=-1) == INV and g(K=1 << 31) == INV and g(ldc=7) == INV
     assert g(lda=16) == INV and g(ldb=16) == INV and g(lda=40) == MIS and g(ldb=40) == MIS
     assert g(A=None) == INV and g(SA=None) == INV and g(B=None) == INV and g(SB=None) == INV and g(C=None) == INV
     assert g(A=P + 8) == MIS and g(SA=P + 8) == MIS and g(B=P + 8) == MIS and g(SB=P + 8) == MIS and g(C=P + 1) == MIS
     assert g(fmt=0, ga=P) == INV and g(fmt=0, gb=P) == INV and g(ga=P + 1) == MIS and g(fmt=5) == INV
-    assert g(flags=2) == INV
+    assert g(flags=2) == INV and g(kernel=2) == INV and g(kernel=9) == INV and g(split=3) == INV and g(split=16) == INV
     assert lib.hk_gemm_fp4(P, P, P, P, P, 8, 8, 64, 32, 32, 7, 0, None, None, None) == INV
 
 

@@ -170,6 +170,43 @@ def test_product(hk, fmt, M, N, K):
     _assert_product(C, av, bv, K)
 
 
+def _forced(hk, a, b, kernel, split):
+    import torch
+    M, N, K = a.rows, b.rows, a.cols
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    st = hk.hk_gemm_fp4_ex(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
+                           out.data_ptr(), M, N, K, a.codes.stride(0), b.codes.stride(0), N,
+                           hk.HK_FP4_MXFP4 if a.format == "mxfp4" else hk.HK_FP4_NVFP4, ptr(a.global_scale),
+                           ptr(b.global_scale), kernel=kernel, split_k=split,
+                           stream=torch.cuda.current_stream().cuda_stream)
+    assert st == hk.HK_OK, hk.hk_gemm_last_error_string()
+    return out
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 2304), (17, 130, 2048), (50, 129, 3000), (100, 640, 2100), (260, 513, 4096),
+                                   (777, 1000, 1536)])
+def test_every_kernel_and_split(hk, fmt, M, N, K):
+    """4 = HK_KERNEL_SINGLE_128x128 with each K split, 1 = HK_KERNEL_PAIR_256x256."""
+    a, av = _random_matrix(hk, M, K, fmt, M + N)
+    b, bv = _random_matrix(hk, N, K, fmt, M + K)
+    for kernel, split in ((4, 1), (4, 2), (4, 4), (4, 8), (1, 0)):
+        _assert_product(_forced(hk, a, b, kernel, split), av, bv, K)
+    _status_ok(hk)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(2560, 2100, 256), (5000, 2900, 320), (2304, 4352, 512)])
+def test_product_of_several_rounds(hk, fmt, M, N, K):
+    """More tiles than CTA pairs: accumulators take turns, the last round runs in halves."""
+    a, av = _random_matrix(hk, M, K, fmt, 5)
+    b, bv = _random_matrix(hk, N, K, fmt, 6)
+    for _ in range(2):
+        _assert_product(hk.gemm_fp4(a, b), av, bv, K)
+    _status_ok(hk)
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_product_scales_reach_their_rows_and_blocks(hk, fmt, M):
