@@ -46,6 +46,21 @@ __device__ __forceinline__ bool wait_mbar(WaitCtx c, uint32_t bar, uint32_t pari
     return wait_mbar_slow(c, bar, parity, code);
 }
 
+// The same for a wait on a pipeline's critical path: polls without suspending
+// (a suspended wait was measured to resume several hundred cycles after its
+// phase completed). The clock is read every 4096 probes.
+__device__ __forceinline__ bool wait_mbar_poll(WaitCtx c, uint32_t bar, uint32_t parity, uint32_t code) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_test_wait(bar, parity)) return true;
+        if ((it & 4095u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 >= 20000) return wait_mbar_slow(c, bar, parity, code);
+        }
+    }
+}
+
 // For barriers that the peer CTA's threads arrive on with
 // mbar_arrive_cluster_relaxed (they order tcgen05 operations only).
 static __device__ __noinline__ bool wait_mbar_cluster_slow(WaitCtx c, uint32_t bar, uint32_t parity, uint32_t code) {

@@ -12,6 +12,14 @@
 // K = 64. Its scales are 2 (MXFP4) or 4 (NVFP4) tiles of 512 bytes per 128
 // rows, contiguous in memory: one untiled bulk copy into shared memory, then
 // tcgen05.cp into Tensor Memory, where tile q takes four columns.
+//
+// The MMA warp issues a stage's scale copies just before its MMAs, in one
+// instruction stream (a copy is ordered before the MMAs that follow it). What
+// that costs is the issuing: each of these instructions takes its operands from
+// uniform registers. Measured per stage of 4 MMAs of a 256 × 256 tile, operands
+// stepping through a ring: 517 cycles with 12 copies issued under elect.sync,
+// 1049 to 1304 under a test of the lane id, where every operand is moved to a
+// uniform register on its own; the MMAs alone take 515.
 #pragma once
 
 #include <cuda.h>
@@ -171,7 +179,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const smem = smem_raw + (base - raw);
-    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be the same in every lane
     const uint32_t lane = lane_id();
     const int part = static_cast<int>(blockIdx.x) % splits;        // the CTA's rank in its cluster
     const int tile = static_cast<int>(blockIdx.x) / splits;
@@ -208,7 +216,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             int fills = 0, dropped = -1;
             for (int ks = ks_begin; ks < ks_end; ++ks, ++fills) {
                 const int s = fills % G::kStages;
-                if (!wait_mbar(p.wait, empty_bar(s), ((fills / G::kStages) & 1) ^ 1u, kErrWaitRing)) {
+                if (!wait_mbar_poll(p.wait, empty_bar(s), ((fills / G::kStages) & 1) ^ 1u, kErrWaitRing)) {
                     ok = false;
                     break;
                 }
@@ -229,32 +237,37 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     if (f != dropped) wait_mbar_drain(full_bar(f % G::kStages), (f / G::kStages) & 1);
         }
     } else if (warp == 1) {
-        int it = 0;
-        for (int ks = ks_begin; ks < ks_end; ++ks, ++it) {
-            const int s = it % G::kStages;
-            if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(s), (it / G::kStages) & 1, kErrWaitData))) {
-                ok = false;
-                break;
-            }
+        int stage = 0;
+        uint32_t phase = 0;
+        // (after a wait that gave up the loop runs on without issuing: its exit depends on no wait, so that the
+        // compiler sees every index as the same in all lanes)
+        for (int ks = ks_begin; ks < ks_end; ++ks) {
+            if (ok) ok = wait_mbar_poll(p.wait, full_bar(stage), phase, kErrWaitData);
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after_sync();
-            if (lane == 0) {
-                const uint32_t sf = base + G::kOffSf + s * 2 * G::kSfBytes;
-                const uint32_t sf_tmem = tmem_base + G::kColSf + s * G::kSfCols;
+            const uint32_t sf = desc_low(base + G::kOffSf + stage * 2 * G::kSfBytes, 16);
+            const uint32_t sf_tmem = tmem_base + G::kColSf + stage * G::kSfCols;
+            const uint32_t wd = desc_low(base + G::kOffW + stage * G::kWBytes, 16);
+            const uint32_t td = desc_low(base + G::kOffT + stage * G::kTBytes, 16);
+            if (ok && elect_one()) {
 #pragma unroll
                 for (int q = 0; q < 2 * G::kSfTiles; ++q)
-                    tmem_cp_128x16b(sf_tmem + 4 * q, smem_desc_plain(sf + 512 * q, 16, 128));
-                const uint64_t wd = smem_desc_kmajor_sw128(base + G::kOffW + s * G::kWBytes);
-                const uint64_t td = smem_desc_kmajor_sw128(base + G::kOffT + s * G::kTBytes);
+                    tmem_cp_128x16b(sf_tmem + 4 * q, smem_desc(sf + ((512 * q) >> 4), desc_high_plain(128)));
 #pragma unroll
                 for (int k = 0; k < kMmasPerStage; ++k) {
                     const uint32_t id = mma_scale_id<kFmt>(k);
                     const uint32_t col = 4 * mma_scale_tile<kFmt>(k);
-                    mma_fp4<1, kFmt>(tmem_base, wd + 2u * k, td + 2u * k, G::kIdesc | (id << 4) | (id << 29),
-                                     sf_tmem + col, sf_tmem + 4 * G::kSfTiles + col, (it > 0 || k > 0) ? 1u : 0u);
+                    mma_fp4<1, kFmt>(tmem_base, smem_desc(wd + 2 * k, kDescHighKmajorSw128),
+                                     smem_desc(td + 2 * k, kDescHighKmajorSw128), G::kIdesc | (id << 4) | (id << 29),
+                                     sf_tmem + col, sf_tmem + 4 * G::kSfTiles + col, (ks > ks_begin || k > 0) ? 1u : 0u);
                 }
-                mma_commit_one(empty_bar(s));
+                mma_commit_one(empty_bar(stage));
             }
             __syncwarp();
+            if (++stage == G::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
         // also on the abort path: everything issued completes before TMEM is freed
         if (lane == 0) {
@@ -335,9 +348,8 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
 // --------------------------------------------------- CTA-pair tile kernel --
 //
 // For many tokens: 256 × 256 tiles on a pair of CTAs (cta_group::2), a
-// persistent grid, roles by warp: 0 loads, 1 issues the MMAs (leader CTA), 2-5
-// store, 6 copies each stage's scales into Tensor Memory (leader CTA), so that
-// no copy stands between two MMAs in the issuing thread's stream.
+// persistent grid, roles by warp: 0 loads, 1 issues the scale copies and the
+// MMAs (leader CTA), 2-5 store.
 //
 // Tensor Memory holds two accumulators of 256 columns and a ring of scale
 // slots, which together need more than its 512 columns: the accumulators
@@ -352,7 +364,8 @@ struct PairGeometry {
     static constexpr int kOpBytes = 128 * kStageRowBytes;                   // A or B rows of one CTA and stage
     static constexpr int kStageSf = 3 * kSfBytes;                           // own A rows, both halves of B
     static constexpr int kStageBytes = 2 * kOpBytes + kStageSf;
-    static constexpr int kStages = (kSmemLimit - 2048) / kStageBytes > 6 ? 6 : (kSmemLimit - 2048) / kStageBytes;
+    static constexpr int kFit = (kSmemLimit - 2048 - 4 * 2048) / kStageBytes;
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static_assert(kStages >= 4, "pipeline too shallow");
     static constexpr int kSfCols = 12 * kSfTiles;                           // TMEM columns of a stage's scales
     static constexpr int kSlots = kFmt == kMxfp4 ? 4 : 3;                   // scale slots
@@ -363,15 +376,17 @@ struct PairGeometry {
     static constexpr int kOffA = 0;
     static constexpr int kOffB = kStages * kOpBytes;
     static constexpr int kOffSf = 2 * kStages * kOpBytes;
-    // full[S], empty[S], sf_full[slots], acc_full[2], acc_free, drain[2]
-    static constexpr int kOffBars = kOffSf + kStages * kStageSf;
-    static constexpr int kNumBars = 2 * kStages + kSlots + 5;
+    static constexpr int kStoreBytes = 32 * 64;                             // 32 × 32 outputs that a warp stores at a time
+    static constexpr int kOffStore = kOffSf + kStages * kStageSf;
+    // full[S], empty[S], acc_full[2], acc_free, drain
+    static constexpr int kOffBars = kOffStore + 4 * kStoreBytes;
+    static constexpr int kNumBars = 2 * kStages + 4;
     static constexpr int kOffHolder = kOffBars + kNumBars * 8;              // TMEM address, two flags
     static constexpr int kSmemBytes = kOffHolder + 16 + 1024;
     static_assert(kSmemBytes <= kSmemLimit, "shared memory");
     static constexpr uint32_t kIdesc = idesc_fp4_f32(256, 256, kFmt);
     static constexpr uint32_t kIdescHalf = idesc_fp4_f32(256, 128, kFmt);
-    static constexpr int kThreads = 224;
+    static constexpr int kThreads = 192;
 };
 
 // Work unit u -> tile and half (-1: the whole tile).
@@ -391,56 +406,74 @@ __device__ __forceinline__ void pair_unit(const Fp4Params& p, int u, int& tm, in
     tn = local / rows;
 }
 
-// 32 sums of one row to bf16, stored at columns [col, col + 32).
-__device__ __forceinline__ void store_sums(const Fp4Params& p, const uint32_t (&v)[32], float alpha, int row, int col) {
-    if (row >= p.M || col >= p.N) return;
-    uint16_t* const dst = p.c + static_cast<int64_t>(row) * p.ldc + col;
-    uint32_t w[16];
+// 32 rows × 32 columns of sums (lane: row) to bf16 and to C at (row0, col0),
+// through the warp's buffer in shared memory (64-byte rows, swizzled) and a TMA store.
+// Where TMA cannot write C (rows not 16-byte aligned; N not a multiple of 8 at
+// the last columns, since it bounds a row to 16 bytes only) a warp writes a row's
+// 32 columns at a time.
+__device__ __forceinline__ void store_sums(const Fp4Params& p, const void* tmap_c, uint32_t buf, const uint8_t* buf_ptr,
+                                           const uint32_t (&v)[32], float alpha, int row0, int col0) {
+    const uint32_t lane = lane_id();
+    if (row0 >= p.M || col0 >= p.N) return;          // (the same in every lane)
+    if (lane == 0) bulk_wait_group_read<0>();        // the store before has read the buffer
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        w[i] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(v[2 * i]) * alpha), __float_as_uint(__uint_as_float(v[2 * i + 1]) * alpha));
-    if (p.vec_c && col + 32 <= p.N) {
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) st_global_v4(dst + 8 * q, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        for (int i = 0; i < 4; ++i)
+            w[i] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(v[8 * j + 2 * i]) * alpha),
+                                  __float_as_uint(__uint_as_float(v[8 * j + 2 * i + 1]) * alpha));
+        st_shared_v4(buf + lane * 64u + ((static_cast<uint32_t>(j) ^ ((lane >> 1) & 3u)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    if (p.vec_c && (col0 + 32 <= p.N || p.N % 8 == 0)) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tmap_c, buf, col0, row0);
+            bulk_commit_group();
+        }
     } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (col + e < p.N) dst[e] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
+        __syncwarp();
+        const int rows = min(32, p.M - row0);
+        if (col0 + static_cast<int>(lane) < p.N) {
+            uint16_t* dst = p.c + static_cast<int64_t>(row0) * p.ldc + col0 + lane;
+            for (int r = 0; r < rows; ++r, dst += p.ldc)
+                *dst = *reinterpret_cast<const uint16_t*>(buf_ptr + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+        }
+        __syncwarp();                                // (before the buffer is written again)
     }
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(224, 1)
+__global__ void __launch_bounds__(192, 1)
 gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const __grid_constant__ CUtensorMap tmap_b_half, const __grid_constant__ CUtensorMap tmap_sfa,
-                     const __grid_constant__ CUtensorMap tmap_sfb, const Fp4Params p) {
+                     const __grid_constant__ CUtensorMap tmap_sfb, const __grid_constant__ CUtensorMap tmap_c,
+                     const Fp4Params p) {
     using G = PairGeometry<kFmt>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const smem = smem_raw + (base - raw);
-    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // known to be the same in every lane
     const uint32_t lane = lane_id();
     const uint32_t rank = cluster_cta_rank();
     const int unit = blockIdx.x / 2, num_units = gridDim.x / 2;
 
     auto full_bar = [&](int s) { return base + G::kOffBars + 8u * s; };
     auto empty_bar = [&](int s) { return base + G::kOffBars + 8u * (G::kStages + s); };
-    auto sf_full_bar = [&](int j) { return base + G::kOffBars + 8u * (2 * G::kStages + j); };
-    auto acc_full_bar = [&](int b) { return base + G::kOffBars + 8u * (2 * G::kStages + G::kSlots + b); };
-    const uint32_t acc_free_bar = base + G::kOffBars + 8u * (2 * G::kStages + G::kSlots + 2);
-    auto drain_bar = [&](int i) { return base + G::kOffBars + 8u * (2 * G::kStages + G::kSlots + 3 + i); };
+    auto acc_full_bar = [&](int b) { return base + G::kOffBars + 8u * (2 * G::kStages + b); };
+    const uint32_t acc_free_bar = base + G::kOffBars + 8u * (2 * G::kStages + 2);
+    const uint32_t drain_bar = base + G::kOffBars + 8u * (2 * G::kStages + 3);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        for (int j = 0; j < G::kSlots; ++j) mbar_init(sf_full_bar(j), 1);
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(acc_full_bar(b), 1);
-            mbar_init(drain_bar(b), 1);
-        }
+        for (int b = 0; b < 2; ++b) mbar_init(acc_full_bar(b), 1);
+        mbar_init(drain_bar, 1);
         mbar_init(acc_free_bar, 8);            // four storing warps of each CTA
         fence_mbar_init_cluster();
     }
@@ -449,6 +482,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         prefetch_tensor_map(&tmap_b);
         prefetch_tensor_map(&tmap_sfa);
         prefetch_tensor_map(&tmap_sfb);
+        if (p.vec_c) prefetch_tensor_map(&tmap_c);
     }
     if (warp == 1) {
         tmem_alloc_pair(base + G::kOffHolder, 512);
@@ -475,13 +509,13 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 const void* const b_map = half < 0 ? static_cast<const void*>(&tmap_b) : static_cast<const void*>(&tmap_b_half);
                 // rows of 256 bytes of the scale tiles: kSfBytes per 128 rows and stage
                 constexpr int kSfRows = G::kSfBytes / 256;
-                const int sfa_row = (tm * 2 + static_cast<int>(rank)) * p.k_stages * kSfRows;
-                const int sfb_row = (tn * 2 + (half > 0 ? 1 : 0)) * p.k_stages * kSfRows;
-                // (groups of rows past the matrix read as 0)
-                const uint32_t bytes = half < 0 ? 2u * (2 * G::kOpBytes + 3 * G::kSfBytes)
-                                                : 2u * (G::kOpBytes + G::kOpBytes / 2 + 2 * G::kSfBytes);
+                const int sfa_group = tm * 2 + static_cast<int>(rank);
+                // both groups of 128 rows of B in one load (of a half tile its own and the next; past the
+                // matrix they read as 0)
+                const int sfb_group = tn * 2 + (half > 0 ? 1 : 0);
+                const uint32_t bytes = 2u * (G::kOpBytes + (half < 0 ? G::kOpBytes : G::kOpBytes / 2) + 3 * G::kSfBytes);
                 for (int ks = 0; ks < p.k_stages; ++ks) {
-                    if (!wait_mbar(p.wait, empty_bar(stage), phase ^ 1u, kErrWaitRing)) {
+                    if (!wait_mbar_poll(p.wait, empty_bar(stage), phase ^ 1u, kErrWaitRing)) {
                         ok = false;
                         break;
                     }
@@ -491,9 +525,8 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                     }
                     const uint32_t full = map_to_cta(full_bar(stage), 0);
                     const uint32_t sf = base + G::kOffSf + stage * G::kStageSf;
-                    tma_load_2d_pair(sf, &tmap_sfa, 0, sfa_row + ks * kSfRows, full);
-                    tma_load_2d_pair(sf + G::kSfBytes, &tmap_sfb, 0, sfb_row + ks * kSfRows, full);
-                    if (half < 0) tma_load_2d_pair(sf + 2 * G::kSfBytes, &tmap_sfb, 0, sfb_row + (p.k_stages + ks) * kSfRows, full);
+                    tma_load_3d_pair(sf, &tmap_sfa, 0, ks * kSfRows, sfa_group, full);
+                    tma_load_3d_pair(sf + G::kSfBytes, &tmap_sfb, 0, ks * kSfRows, sfb_group, full);
                     tma_load_2d_pair(base + G::kOffA + stage * G::kOpBytes, &tmap_a, ks * kStageRowBytes, a_row, full);
                     tma_load_2d_pair(base + G::kOffB + stage * G::kOpBytes, b_map, ks * kStageRowBytes, b_row, full);
                     ++fills;
@@ -512,36 +545,51 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         // -------------------------------------------------------- MMAs --
         if (rank == 0) {
             int stage = 0, slot = 0, local = 0;
-            uint32_t phase = 0, slot_phase = 0;
-            for (int u = unit; u < p.total_units && ok; u += num_units, ++local) {
+            int old_stage = 0;                  // the stage whose MMAs used this slot last
+            uint32_t phase = 0, old_phase = 0;
+            int64_t it = 0;
+            // (after a wait that gave up the loops run on without issuing: their exits depend on no wait, so
+            // that the compiler sees every index as the same in all lanes)
+            for (int u = unit; u < p.total_units; u += num_units, ++local) {
                 int tm, tn, half;
                 pair_unit(p, u, tm, tn, half);
                 const uint32_t idesc = half < 0 ? G::kIdesc : G::kIdescHalf;
                 const uint32_t d_tmem = tmem_base + (local & 1 ? G::kCol1 : 0);
                 // the previous tile's epilogue has read the columns this accumulator shares with it
-                if (local > 0 && !__all_sync(0xffffffffu, wait_mbar_cluster(p.wait, acc_free_bar, (local - 1) & 1, kErrWaitAcc))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                for (int ks = 0; ks < p.k_stages; ++ks) {
-                    if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(stage), phase, kErrWaitData) &&
-                                                     wait_mbar(p.wait, sf_full_bar(slot), slot_phase, kErrWaitData))) {
-                        ok = false;
-                        break;
+                if (ok && local > 0) ok = wait_mbar_cluster(p.wait, acc_free_bar, (local - 1) & 1, kErrWaitAcc);
+                for (int ks = 0; ks < p.k_stages; ++ks, ++it) {
+                    if (ok) ok = wait_mbar_poll(p.wait, full_bar(stage), phase, kErrWaitData);
+                    // the slot's last scales have been used: those MMAs completed (the phase of their stage's
+                    // empty barrier, which cannot run on past it before this stage's MMAs are issued)
+                    if (it >= G::kSlots) {
+                        if (ok) ok = wait_mbar_poll(p.wait, empty_bar(old_stage), old_phase, kErrWaitRing);
+                        if (++old_stage == G::kStages) {
+                            old_stage = 0;
+                            old_phase ^= 1u;
+                        }
                     }
+                    ok = __all_sync(0xffffffffu, ok);
                     tc_fence_after_sync();
-                    const uint64_t ad = smem_desc_kmajor_sw128(base + G::kOffA + stage * G::kOpBytes);
-                    const uint64_t bd = smem_desc_kmajor_sw128(base + G::kOffB + stage * G::kOpBytes);
+                    const uint32_t ad = desc_low(base + G::kOffA + stage * G::kOpBytes, 16);
+                    const uint32_t bd = desc_low(base + G::kOffB + stage * G::kOpBytes, 16);
+                    const uint32_t src = desc_low(base + G::kOffSf + stage * G::kStageSf, 16);
                     const uint32_t sf = tmem_base + G::kColSf + slot * G::kSfCols;
-                    if (lane == 0) {
+                    if (ok && elect_one()) {
+                        // a slot holds a stage's scale tiles in order, of each first A's, then B's two groups of
+                        // rows (a half tile has one group; what the other's place holds is copied and not used)
+#pragma unroll
+                        for (int q = 0; q < G::kSfTiles; ++q)
+#pragma unroll
+                            for (int j = 0; j < 3; ++j)
+                                tmem_cp_128x16b_pair(sf + 12 * q + 4 * j,
+                                                     smem_desc(src + ((j * G::kSfBytes + 512 * q) >> 4), desc_high_plain(128)));
 #pragma unroll
                         for (int k = 0; k < kMmasPerStage; ++k) {
                             const uint32_t id = mma_scale_id<kFmt>(k);
-                            // slot: a stage's tiles in order, of each first A's, then B's two groups
                             const uint32_t at = sf + 12 * mma_scale_tile<kFmt>(k);
-                            mma_fp4<2, kFmt>(d_tmem, ad + 2u * k, bd + 2u * k, idesc | (id << 4) | (id << 29), at, at + 4,
-                                             (ks > 0 || k > 0) ? 1u : 0u);
+                            mma_fp4<2, kFmt>(d_tmem, smem_desc(ad + 2 * k, kDescHighKmajorSw128),
+                                             smem_desc(bd + 2 * k, kDescHighKmajorSw128), idesc | (id << 4) | (id << 29), at,
+                                             at + 4, (ks > 0 || k > 0) ? 1u : 0u);
                         }
                         mma_commit_pair_mask(empty_bar(stage), 0x3);
                     }
@@ -550,67 +598,25 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++slot == G::kSlots) {
-                        slot = 0;
-                        slot_phase ^= 1u;
-                    }
+                    if (++slot == G::kSlots) slot = 0;
                 }
-                if (!ok) break;
-                if (lane == 0) mma_commit_pair_mask(acc_full_bar(local & 1), 0x3);
+                if (ok && elect_one()) mma_commit_pair_mask(acc_full_bar(local & 1), 0x3);
                 __syncwarp();
             }
             if (!ok || wait_aborted(p.wait)) {      // everything issued completes before TMEM is freed
                 if (lane == 0) {
-                    mma_commit_pair_mask(drain_bar(0), 0x1);
-                    wait_mbar_drain(drain_bar(0), 0);
+                    mma_commit_pair_mask(drain_bar, 0x1);
+                    wait_mbar_drain(drain_bar, 0);
                 }
                 __syncwarp();
-            }
-        }
-    } else if (warp == 6) {
-        // ------------------------------------------------ scale copies --
-        if (rank == 0 && lane == 0) {
-            int stage = 0, slot = 0;
-            uint32_t phase = 0;
-            int64_t it = 0;
-            for (int u = unit; u < p.total_units && ok; u += num_units) {
-                int tm, tn, half;
-                pair_unit(p, u, tm, tn, half);
-                for (int ks = 0; ks < p.k_stages; ++ks, ++it) {
-                    // the slot is free once the MMAs of the stage kSlots before have completed: the phase
-                    // of that stage's empty barrier (it cannot run on past it, since the MMAs need this copy)
-                    const int64_t old = it - G::kSlots;
-                    if (!wait_mbar(p.wait, full_bar(stage), phase, kErrWaitData) ||
-                        (old >= 0 && !wait_mbar(p.wait, empty_bar(static_cast<int>(old % G::kStages)),
-                                                static_cast<uint32_t>((old / G::kStages) & 1), kErrWaitRing))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t src = base + G::kOffSf + stage * G::kStageSf;
-                    const uint32_t dst = tmem_base + G::kColSf + slot * G::kSfCols;
-                    const int groups = half < 0 ? 3 : 2;
-#pragma unroll
-                    for (int q = 0; q < G::kSfTiles; ++q)
-                        for (int j = 0; j < groups; ++j)
-                            tmem_cp_128x16b_pair(dst + 12 * q + 4 * j, smem_desc_plain(src + j * G::kSfBytes + 512 * q, 16, 128));
-                    mma_commit_pair_mask(sf_full_bar(slot), 0x1);
-                    if (++stage == G::kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    if (++slot == G::kSlots) slot = 0;
-                }
-            }
-            if (!ok || wait_aborted(p.wait)) {
-                mma_commit_pair_mask(drain_bar(1), 0x1);
-                wait_mbar_drain(drain_bar(1), 0);
             }
         }
     } else {
         // ----------------------------------------------------- epilogue --
         const uint32_t q = warp & 3u;                 // TMEM lanes 32 q .. 32 q + 31
         const float alpha = global_alpha(p);
+        const uint32_t buf_addr = base + G::kOffStore + (warp - 2) * G::kStoreBytes;
+        const uint8_t* const buf_ptr = smem + G::kOffStore + (warp - 2) * G::kStoreBytes;
         int local = 0;
         for (int u = unit; u < p.total_units; u += num_units, ++local) {
             int tm, tn, half;
@@ -629,7 +635,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 }
             }
             tc_fence_after_sync();
-            const int row = tm * 256 + static_cast<int>(rank * 128 + q * 32 + lane);
+            const int row0 = tm * 256 + static_cast<int>(rank * 128 + q * 32);
             const int col0 = tn * 256 + (half > 0 ? 128 : 0);
             const int chunks = half < 0 ? 8 : 4;
             const uint32_t t_row = tmem_base + ((q * 32u) << 16) + (buf ? G::kCol1 : 0);
@@ -645,15 +651,16 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
             if (lane == 0) mbar_arrive_cluster_relaxed(map_to_cta(acc_free_bar, 0));
 #pragma unroll
             for (int i = 0; i < G::kFirstChunks; ++i)
-                if (i < chunks) store_sums(p, v[i], alpha, row, col0 + 32 * chunk_of(i));
+                if (i < chunks) store_sums(p, &tmap_c, buf_addr, buf_ptr, v[i], alpha, row0, col0 + 32 * chunk_of(i));
 #pragma unroll 1
             for (int i = G::kFirstChunks; i < chunks; ++i) {
                 tmem_load_32cols(t_row + 32 * chunk_of(i), v[0]);
                 tmem_wait_ld();
-                store_sums(p, v[0], alpha, row, col0 + 32 * chunk_of(i));
+                store_sums(p, &tmap_c, buf_addr, buf_ptr, v[0], alpha, row0, col0 + 32 * chunk_of(i));
             }
             tc_fence_before_sync();
         }
+        if (lane == 0) bulk_wait_group<0>();
     }
     __syncwarp();
     tc_fence_before_sync();

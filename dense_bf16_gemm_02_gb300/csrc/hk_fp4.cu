@@ -125,7 +125,7 @@ const SingleVariant kSingle[2][4] = {
     {single_variant<16, kNvfp4>(), single_variant<32, kNvfp4>(), single_variant<64, kNvfp4>(), single_variant<128, kNvfp4>()},
 };
 
-using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Fp4Params);
+using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, Fp4Params);
 
 struct PairVariant {
     PairFn fn;
@@ -174,15 +174,15 @@ hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, 
     return HK_OK;
 }
 
-// Scale tiles as rows of 256 bytes, in boxes of one stage's tiles of 128 matrix rows.
+// Scale tiles as [groups of 128 matrix rows][rows of 256 bytes], in boxes of one stage's tiles of `groups` groups.
 hk_status encode_scales(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
-                        int32_t format, const char* name) {
-    const int64_t bytes = static_cast<int64_t>(hk_fp4_scales_size(rows, cols, format));
-    cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(bytes / 256)};
-    cuuint64_t strides[1] = {256};
-    cuuint32_t box[2] = {256, static_cast<cuuint32_t>(2 * scale_tiles(format))};
-    cuuint32_t elem_strides[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, elem_strides,
+                        int32_t format, uint32_t groups, const char* name) {
+    const int64_t group_bytes = padded_blocks(cols, format) * 128;
+    cuuint64_t dims[3] = {256, static_cast<cuuint64_t>(group_bytes / 256), static_cast<cuuint64_t>(ceil_div(rows, 128))};
+    cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(group_bytes)};
+    cuuint32_t box[3] = {256, static_cast<cuuint32_t>(2 * scale_tiles(format)), groups};
+    cuuint32_t elem_strides[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, elem_strides,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
@@ -208,8 +208,19 @@ hk_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 enc, Fp4Params p, const 
     if ((s = encode_codes(enc, &ta, A, p.M, K, lda, 128, "A")) != HK_OK) return s;
     if ((s = encode_codes(enc, &tb, B, p.N, K, ldb, 128, "B")) != HK_OK) return s;
     if ((s = encode_codes(enc, &tbh, B, p.N, K, ldb, 64, "B")) != HK_OK) return s;
-    if ((s = encode_scales(enc, &tsa, p.sfa, p.M, K, format, "A's scales")) != HK_OK) return s;
-    if ((s = encode_scales(enc, &tsb, p.sfb, p.N, K, format, "B's scales")) != HK_OK) return s;
+    if ((s = encode_scales(enc, &tsa, p.sfa, p.M, K, format, 1, "A's scales")) != HK_OK) return s;
+    if ((s = encode_scales(enc, &tsb, p.sfb, p.N, K, format, 2, "B's scales")) != HK_OK) return s;
+    CUtensorMap tc = ta;                 // (not used where C's rows are not 16-byte aligned)
+    if (p.vec_c) {
+        cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M)};
+        cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.ldc) * 2};
+        cuuint32_t box[2] = {32, 32};
+        cuuint32_t elem_strides[2] = {1, 1};
+        CUresult r = enc(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, dims, strides, box, elem_strides,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of C failed (CUresult %d)", (int)r);
+    }
     const PairVariant& v = kPair[format == HK_FP4_NVFP4];
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -223,7 +234,7 @@ hk_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 enc, Fp4Params p, const 
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, ta, tb, tbh, tsa, tsb, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, ta, tb, tbh, tsa, tsb, tc, p);
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the 4-bit product", e);
 }
 
