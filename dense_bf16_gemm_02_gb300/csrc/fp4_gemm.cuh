@@ -122,9 +122,9 @@ __device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&v)[1
         : "r"(taddr));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -320,19 +320,41 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     __syncwarp();
     if (splits > 1) {
         cluster_sync();
+        // this CTA's share of the tokens, four features of a token per thread (32 threads a token, so a
+        // warp reads whole 512-byte rows), the loads of all parts in flight together
         if (warp >= 2) {
-            const int f_local = static_cast<int>((warp & 3u) * 32 + lane);
-            const int feature = tn * G::kTileF + f_local;
+            const int each = (kTok + splits - 1) / splits;
+            const int t_end = min(min(kTok, (part + 1) * each), p.M - tm * kTok);
+            const int feature = tn * G::kTileF + static_cast<int>(lane) * 4;
             const float alpha = global_alpha(p);
-            for (int t = part; t < kTok; t += splits) {
-                const int token = tm * kTok + t;
-                if (token >= p.M) break;
-                const uint32_t at = base + static_cast<uint32_t>(t * G::kTileF + f_local) * 4u;
-                float sum = 0.0f;
-                for (int r = 0; r < splits; ++r) sum += ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(r)));
-                if (ok && feature < p.N)
-                    p.c[static_cast<int64_t>(token) * p.ldc + feature] =
-                        __bfloat16_as_ushort(__float2bfloat16_rn(sum * alpha));
+#pragma unroll 2
+            for (int t = part * each + static_cast<int>(warp) - 2; t < t_end; t += 4) {
+                const uint32_t at = base + static_cast<uint32_t>(t * G::kTileF + static_cast<int>(lane) * 4) * 4u;
+                float4 x[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < splits) x[r] = ld_cluster_v4(map_to_cta(at, static_cast<uint32_t>(r)));
+                float4 sum = x[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    if (r < splits) {
+                        sum.x += x[r].x;
+                        sum.y += x[r].y;
+                        sum.z += x[r].z;
+                        sum.w += x[r].w;
+                    }
+                if (!ok) continue;
+                uint16_t* const dst = p.c + static_cast<int64_t>(tm * kTok + t) * p.ldc + feature;
+                const uint32_t w0 = pack_bf16x2_rn(__float_as_uint(sum.x * alpha), __float_as_uint(sum.y * alpha));
+                const uint32_t w1 = pack_bf16x2_rn(__float_as_uint(sum.z * alpha), __float_as_uint(sum.w * alpha));
+                if (p.vec_c && feature + 4 <= p.N) {
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(w0, w1);
+                } else {
+                    const uint32_t w[2] = {w0, w1};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (feature + e < p.N) dst[e] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
+                }
             }
         }
         cluster_sync();    // no CTA leaves while another reads its sums
