@@ -25,14 +25,15 @@ template <> __device__ __forceinline__ __half from_float<__half>(float x) { retu
 template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
 
 // Elements [col, col + 8) of a row of `cols`, 0 past its end. `vec`: the row
-// is 16-byte aligned (16-byte loads).
+// is 16-byte aligned (16-byte loads). (Ordinary loads, not the read-only path:
+// the kernels that use them may have started before the data was written.)
 template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* row, int64_t col, int64_t cols, bool vec) {
     Raw8<T> r;
     if (vec && col + 8 <= cols) {
         const uint4* p = reinterpret_cast<const uint4*>(row + col);
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = __ldg(p + i);
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = p[i];
     } else {
         T e[8];
 #pragma unroll

@@ -75,13 +75,29 @@ hk_status current_device(int* device, int* sm_count) {
     return hk_host::check_device(*device, sm_count);
 }
 
-template <int kWarps>
-void launch_append(const AppendParams& p, int32_t type, unsigned blocks, cudaStream_t st) {
-    switch (type) {
-        case HK_TYPE_BF16: kv8_append_kernel<__nv_bfloat16, kWarps><<<blocks, 256, 0, st>>>(p); break;
-        case HK_TYPE_FP16: kv8_append_kernel<__half, kWarps><<<blocks, 256, 0, st>>>(p); break;
-        default: kv8_append_kernel<float, kWarps><<<blocks, 256, 0, st>>>(p); break;
-    }
+// A launch that may begin while the kernel before it on the stream ends (the kernel waits for that end itself).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*fn)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <typename T, int kWarps>
+cudaError_t launch_append(const AppendParams& p, int steps, unsigned blocks, cudaStream_t st) {
+    auto* fn = steps <= 1   ? &kv8_append_kernel<T, kWarps, 1>
+               : steps <= 2 ? &kv8_append_kernel<T, kWarps, 2>
+               : steps <= 4 ? &kv8_append_kernel<T, kWarps, 4>
+                            : &kv8_append_kernel<T, kWarps, 8>;
+    return launch_early(fn, dim3(blocks), dim3(256), 0, st, p);
 }
 
 // Codes of keys or values as [pages · heads, page_size, D] in boxes of up to 32 tokens of one head.
@@ -206,20 +222,12 @@ void launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
 
 template <int kD, typename T>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, cudaStream_t st) {
-    kv8_decode_kernel<kD, T><<<static_cast<unsigned>(blocks), 32 * kDecodeWarps, DecodeGeometry<kD>::kSmemBytes, st>>>(tk, tv, p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(&kv8_decode_kernel<kD, T>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kDecodeWarps),
+                                 DecodeGeometry<kD>::kSmemBytes, st, tk, tv, p);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
     const int warps_per_row = 4;
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks * kDecodeWarps), static_cast<unsigned>(kRows / (8 / warps_per_row)));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv8_combine_kernel<kD, T>, p, warps_per_row);
+    return launch_early(&kv8_combine_kernel<kD, T>, dim3(static_cast<unsigned>(blocks * kDecodeWarps), kRows / (8 / warps_per_row)),
+                        dim3(256), 0, st, p, warps_per_row);
 }
 
 // Many query rows per KV head: the sequences' keys and values to bf16, then the
@@ -340,23 +348,29 @@ extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, con
     p.counts = counts;
     p.B = static_cast<int32_t>(B);
     p.T = static_cast<int32_t>(T);
-    p.Hkv = cache->heads;
+    p.Hkv = static_cast<uint32_t>(cache->heads);
     p.D = cache->head_dim;
     p.page_size = cache->page_size;
     p.max_pages = static_cast<int32_t>(max_pages);
     p.num_pages = cache->num_pages;
-    p.slots = static_cast<int32_t>((T + p.page_size - 2) / p.page_size + 1);
+    p.slots = static_cast<uint32_t>((T + p.page_size - 2) / p.page_size + 1);
     p.status = status;
     if (B > (int64_t(1) << 40) / p.slots / p.Hkv) return fail(HK_ERR_INVALID_ARG, "problem too large");
     p.items = B * p.slots * p.Hkv * 2;
     // one warp holds the new tokens of a page as long as they fit its registers (8 steps of 256 elements)
-    const bool one_warp = std::min<int64_t>(T, p.page_size) * p.D <= kAppendSteps * 256;
+    const int64_t elements = std::min<int64_t>(T, p.page_size) * p.D;
+    const bool one_warp = elements <= kAppendSteps * 256;
+    const int steps = static_cast<int>(ceil_div(elements, one_warp ? 256 : 8 * 256));
     const int64_t blocks = one_warp ? ceil_div(p.items, 8) : p.items;
-    if (blocks > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
+    if (p.items > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (one_warp) launch_append<1>(p, type, static_cast<unsigned>(blocks), st);
-    else launch_append<8>(p, type, static_cast<unsigned>(blocks), st);
-    cudaError_t e = cudaGetLastError();
+    auto go = [&](auto one, auto eight) { return (one_warp ? one : eight)(p, steps, static_cast<unsigned>(blocks), st); };
+    cudaError_t e;
+    switch (type) {
+        case HK_TYPE_BF16: e = go(&launch_append<__nv_bfloat16, 1>, &launch_append<__nv_bfloat16, 8>); break;
+        case HK_TYPE_FP16: e = go(&launch_append<__half, 1>, &launch_append<__half, 8>); break;
+        default: e = go(&launch_append<float, 1>, &launch_append<float, 8>); break;
+    }
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the cache append", e);
 }
 
@@ -439,14 +453,17 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.num_pages = cache->num_pages;
     p.causal = causal ? 1 : 0;
     p.scale_log2 = scale_log2;
-    p.min_tiles = 2;
+    p.min_tiles = 1;
     char* const w = static_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(w);
     p.part_ml = reinterpret_cast<float*>(w + ws.ml);
     p.info = reinterpret_cast<int4*>(w + ws.info);
     p.wait.status = status;
     p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
-    const int blocks = 2 * std::min(sms, kSms);
+    // one round of blocks, and no more than the table has room for tiles
+    const int64_t room = ceil_div(std::min(B, int64_t(kMaxBatch)) * p.Hkv * p.row_tiles * ceil_div(max_pages * p.page_size, kTileKeys),
+                                  kDecodeWarps);
+    const int blocks = static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), room));
     for (int64_t b0 = 0; b0 < B; b0 += kMaxBatch) {       // (launches of one stream: they may share the workspace)
         p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, kMaxBatch));
         p.q = static_cast<const uint16_t*>(Q) + b0 * p.q_stride_b;

@@ -13,8 +13,9 @@
 // One item is a (sequence, touched page, head) of keys or of values: one warp
 // when few tokens arrive per page, else eight warps. The new tokens of an item
 // stay in registers between the maximum and the rounding, so that they are read
-// once; for one token per sequence the kernel is a launch and two dependent
-// reads (the page's index, then its scale beside the token).
+// once. A block does one item, so latency and the number of blocks on an SM
+// bound the kernel: the registers hold no more steps than a page needs, and the
+// tokens are asked for before the page's index is looked at.
 #pragma once
 
 #include <cstdint>
@@ -34,15 +35,16 @@ struct AppendParams {
     int64_t table_stride;
     const int32_t* starts;         // tokens of each sequence before the append
     const int32_t* counts;         // new tokens of each sequence, or null (T)
-    int64_t items;                 // B * slots * Hkv * 2
-    int32_t B, T, Hkv, D, page_size, max_pages;
+    int64_t items;                 // B * slots * Hkv * 2, below 2^32
+    int32_t B, T;
+    uint32_t Hkv, slots;           // heads; pages a sequence can touch
+    int32_t D, page_size, max_pages;
     int64_t num_pages;
-    int32_t slots;                 // pages a sequence can touch
     int32_t vec[2];                // 16-byte loads
     uint32_t* status;
 };
 
-constexpr int kAppendSteps = 8;    // steps of a group of warps: 8 elements per lane and step
+constexpr int kAppendSteps = 8;    // most steps of a group of warps: 8 elements per lane and step
 
 // The exponent field of the page scale for a largest magnitude (its bits).
 __device__ __forceinline__ uint32_t scale_field(uint32_t amax_bits) {
@@ -62,17 +64,19 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
     return out;
 }
 
-template <typename T, int kWarps>
+template <typename T, int kWarps, int kSteps>
 __global__ void __launch_bounds__(256)
 kv8_append_kernel(const AppendParams p) {
     __shared__ uint32_t warp_top[8];
+    griddep_launch_dependents();
+    griddep_wait();                  // launched early behind the kernel that may have written the tokens
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t warp = threadIdx.x >> 5;
     const uint32_t member = kWarps == 1 ? 0 : warp;          // this warp's place in its item
     const int64_t item = kWarps == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : static_cast<int64_t>(blockIdx.x);
     if (item >= p.items) return;
     const int kv = static_cast<int>(item & 1);
-    int64_t rest = item >> 1;
+    uint32_t rest = static_cast<uint32_t>(item >> 1);
     const int h = static_cast<int>(rest % p.Hkv);
     rest /= p.Hkv;
     const int b = static_cast<int>(rest / p.slots);
@@ -90,6 +94,20 @@ kv8_append_kernel(const AppendParams p) {
     const int64_t lo = max(static_cast<int64_t>(start), slot * p.page_size);              // new tokens of this page
     const int64_t hi = min(static_cast<int64_t>(start) + count, (slot + 1) * p.page_size);
     if (lo >= hi) return;
+    const int lanes_per_token = p.D >> 3;
+    const int per_step = kWarps * (32 / lanes_per_token);
+    const int sub = static_cast<int>(member) * (32 / lanes_per_token) + static_cast<int>(lane) / lanes_per_token;
+    const int d = static_cast<int>(lane) % lanes_per_token * 8;
+    const int n = static_cast<int>(hi - lo);
+    const T* const src = static_cast<const T*>(p.src[kv]) + b * p.stride_b[kv] + (lo - start) * p.stride_t[kv] +
+                         h * p.stride_h[kv];
+    Raw8<T> raw[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int t = i * per_step + sub;
+        if (i * per_step < n)
+            raw[i] = load8<T>(src + t * p.stride_t[kv], d, t < n ? p.D : 0, p.vec[kv] != 0);
+    }
     const int64_t page = p.table[b * p.table_stride + slot];
     if (page < 0 || page >= p.num_pages) {
         if (lane == 0) atomicOr(p.status, kErrPage);
@@ -98,24 +116,9 @@ kv8_append_kernel(const AppendParams p) {
     const int64_t ph = page * p.Hkv + h;
     const int old_tokens = static_cast<int>(lo - slot * p.page_size);
     const float had = old_tokens > 0 ? p.scale[kv][ph] : 0.0f;
-
-    const int lanes_per_token = p.D >> 3;
-    const int per_step = kWarps * (32 / lanes_per_token);
-    const int sub = static_cast<int>(member) * (32 / lanes_per_token) + static_cast<int>(lane) / lanes_per_token;
-    const int d = static_cast<int>(lane) % lanes_per_token * 8;
-    const int n = static_cast<int>(hi - lo);
-    const T* const src = static_cast<const T*>(p.src[kv]) + b * p.stride_b[kv] + (lo - start) * p.stride_t[kv] +
-                         h * p.stride_h[kv];
-    Raw8<T> raw[kAppendSteps];
-#pragma unroll
-    for (int i = 0; i < kAppendSteps; ++i) {
-        const int t = i * per_step + sub;
-        if (i * per_step < n)
-            raw[i] = load8<T>(src + t * p.stride_t[kv], d, t < n ? p.D : 0, p.vec[kv] != 0);
-    }
     uint32_t top = 0;       // largest finite magnitude, as bits
 #pragma unroll
-    for (int i = 0; i < kAppendSteps; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         if (i * per_step < n) {
             float v[8];
             widen8<T>(raw[i], v);
@@ -151,7 +154,7 @@ kv8_append_kernel(const AppendParams p) {
     }
     const float inv = 1.0f / scale;      // exact: a power of two
 #pragma unroll
-    for (int i = 0; i < kAppendSteps; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         const int t = i * per_step + sub;
         if (t < n) {
             float v[8];

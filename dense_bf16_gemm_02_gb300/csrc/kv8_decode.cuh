@@ -201,6 +201,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     const int self = static_cast<int>(blockIdx.x) * kDecodeWarps + static_cast<int>(warp);
 
     griddep_launch_dependents();             // the combining kernel may be scheduled; it waits for this grid's end
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tmap_k);
+        prefetch_tensor_map(&tmap_v);
+    }
 
     const uint32_t ring = base + warp * G::kWarpBytes;
     auto full_bar = [&](int s) { return base + G::kOffBars + 8u * (warp * G::kStages + s); };
@@ -208,6 +212,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         for (int s = 0; s < G::kStages; ++s) mbar_init(full_bar(s), 1);
         fence_mbar_init_cluster();
     }
+    griddep_wait();                          // launched early behind the kernel that may have written the cache or q
     // prefix[b]: tiles of the sequences before b, all KV heads
     int64_t* const prefix = reinterpret_cast<int64_t*>(smem + G::kOffPrefix);
     if (warp == 0) {
@@ -262,6 +267,74 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         const int unit_tiles = tiles_of(key_end);
         const int last = static_cast<int>(min(static_cast<int64_t>(unit_tiles), first + (end - at)));   // tiles [first, last)
 
+        // ---- pages and scales of 32 tiles, one tile per lane (two pages where a page is 16 tokens; -1: not a
+        // page), for the tiles from `base` on and, once a load runs past them, for the 32 after those
+        struct Window {
+            int page0, page1;
+            float ks0, ks1, vs0, vs1;
+        };
+        const bool two = p.page_size < kTileKeys;
+        auto look_up = [&](Window& w, int tile0) {
+            auto page_of = [&](int key) {
+                if (key >= key_end) return -1;
+                const int32_t pg = p.table[b * p.table_stride + (key >> p.page_shift)];
+                if (pg < 0 || pg >= p.num_pages) {
+                    atomicOr(p.wait.status, kErrPage);
+                    return -1;
+                }
+                return static_cast<int>(pg);
+            };
+            const int key = (tile0 + static_cast<int>(lane)) * kTileKeys;
+            w.page0 = page_of(key);
+            w.page1 = two ? page_of(key + 16) : w.page0;
+        };
+        // (no page: scale 0, so that nothing of page 0, read in its place, comes through)
+        auto look_up_scales = [&](Window& w) {
+            auto scale_of = [&](const float* scale, int pg) {
+                return pg >= 0 ? scale[static_cast<int64_t>(pg) * p.Hkv + h] : 0.0f;
+            };
+            w.ks0 = scale_of(p.k_scale, w.page0);
+            w.vs0 = scale_of(p.v_scale, w.page0);
+            w.ks1 = two ? scale_of(p.k_scale, w.page1) : w.ks0;
+            w.vs1 = two ? scale_of(p.v_scale, w.page1) : w.vs0;
+        };
+        const int seen = key_end > 0 ? last : first;      // a unit that sees nothing has no tile to read
+        int base_tile = first, next = first;              // the current window's first tile, the next tile to load
+        Window cur = {0, 0, 0.0f, 0.0f, 0.0f, 0.0f}, nxt = cur;
+        auto feed = [&]() {
+            const int at32 = next - base_tile;
+            if (at32 == 32) {
+                look_up(nxt, next);
+                look_up_scales(nxt);
+            }
+            const int pg0 = __shfl_sync(0xffffffffu, at32 < 32 ? cur.page0 : nxt.page0, at32 & 31);
+            const int pg1 = two ? __shfl_sync(0xffffffffu, at32 < 32 ? cur.page1 : nxt.page1, at32 & 31) : pg0;
+            const int s = fills % G::kStages;
+            if (lane == 0) {
+                const uint32_t dst = ring + s * G::kStageBytes;
+                mbar_arrive_expect_tx(full_bar(s), G::kStageBytes);
+                const int row = (next * kTileKeys) & (p.page_size - 1);
+                const int z0 = max(pg0, 0) * p.Hkv + h, z1 = max(pg1, 0) * p.Hkv + h;
+                if (!two) {
+                    tma_load_3d(dst, &tmap_k, 0, row, z0, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, row, z0, full_bar(s));
+                } else {
+                    tma_load_3d(dst, &tmap_k, 0, 0, z0, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes / 2, &tmap_k, 0, 0, z1, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, 0, z0, full_bar(s));
+                    tma_load_3d(dst + G::kHalfBytes * 3 / 2, &tmap_v, 0, 0, z1, full_bar(s));
+                }
+            }
+            ++fills;
+            ++next;
+        };
+        // the first tiles' loads go out before anything else is waited for
+        if (first < seen) {
+            look_up(cur, first);
+            for (int i = 0; i < G::kStages && next < seen; ++i) feed();
+            look_up_scales(cur);
+        }
+
         // ---- query rows g and g + 8 of the unit: f16 fragments and the factor of their scores
         uint32_t qf[kWords][4];
         float factor[2];
@@ -314,82 +387,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-        // Pages of the next 32 tiles, one tile per lane (two pages where a page is 16 tokens); -1: not a page
-        int page0 = 0, page1 = 0;
-        float ks0 = 0, ks1 = 0, vs0 = 0, vs1 = 0;
-        auto look_up = [&](int tile0) {
-            auto page_of = [&](int key) {
-                if (key >= key_end) return -1;
-                const int32_t pg = p.table[b * p.table_stride + (key >> p.page_shift)];
-                if (pg < 0 || pg >= p.num_pages) {
-                    atomicOr(p.wait.status, kErrPage);
-                    return -1;
-                }
-                return static_cast<int>(pg);
-            };
-            const int key = (tile0 + static_cast<int>(lane)) * kTileKeys;
-            page0 = page_of(key);
-            page1 = p.page_size < kTileKeys ? page_of(key + 16) : page0;
-            // (no page: scale 0, so that nothing of page 0, read in its place, comes through)
-            auto scale_of = [&](const float* scale, int pg) {
-                return pg >= 0 ? scale[static_cast<int64_t>(pg) * p.Hkv + h] : 0.0f;
-            };
-            ks0 = scale_of(p.k_scale, page0);
-            vs0 = scale_of(p.v_scale, page0);
-            ks1 = p.page_size < kTileKeys ? scale_of(p.k_scale, page1) : ks0;
-            vs1 = p.page_size < kTileKeys ? scale_of(p.v_scale, page1) : vs0;
-        };
-        // (a page that is not one is read as page 0 and masked)
-        auto load_tile = [&](int tile, int pg0, int pg1) {
-            const int s = fills % G::kStages;
-            if (lane == 0) {
-                const uint32_t dst = ring + s * G::kStageBytes;
-                mbar_arrive_expect_tx(full_bar(s), G::kStageBytes);
-                const int row = (tile * kTileKeys) & (p.page_size - 1);
-                const int z0 = max(pg0, 0) * p.Hkv + h, z1 = max(pg1, 0) * p.Hkv + h;
-                if (p.page_size >= kTileKeys) {
-                    tma_load_3d(dst, &tmap_k, 0, row, z0, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, row, z0, full_bar(s));
-                } else {
-                    tma_load_3d(dst, &tmap_k, 0, 0, z0, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes / 2, &tmap_k, 0, 0, z1, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, 0, z0, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes * 3 / 2, &tmap_v, 0, 0, z1, full_bar(s));
-                }
-            }
-            ++fills;
-        };
-
-        int looked = first;                  // tiles [looked, looked + 32) are in the lanes
-        int next = first;                    // next tile to load
-        if (key_end > 0) look_up(first);
-        const int seen = key_end > 0 ? last : first;      // a unit that sees nothing has no tile to read
-        // the scales of the tiles in the ring, by place
-        float rks0[G::kStages], rks1[G::kStages], rvs0[G::kStages], rvs1[G::kStages];
-        int rbad[G::kStages];
-        auto feed = [&](int place) {
-            if (next - looked == 32) {
-                looked = next;
-                look_up(next);
-            }
-            const int src = next - looked;
-            const int pg0 = __shfl_sync(0xffffffffu, page0, src), pg1 = __shfl_sync(0xffffffffu, page1, src);
-            const float a = __shfl_sync(0xffffffffu, ks0, src), bq = __shfl_sync(0xffffffffu, ks1, src);
-            const float cq = __shfl_sync(0xffffffffu, vs0, src), dq = __shfl_sync(0xffffffffu, vs1, src);
-#pragma unroll
-            for (int s = 0; s < G::kStages; ++s)
-                if (s == place) {
-                    rks0[s] = a;
-                    rks1[s] = bq;
-                    rvs0[s] = cq;
-                    rvs1[s] = dq;
-                    rbad[s] = (pg0 < 0 ? 1 : 0) | (pg1 < 0 ? 2 : 0);
-                }
-            load_tile(next, pg0, pg1);
-            ++next;
-        };
-        for (int i = 0; i < G::kStages && next < seen; ++i) feed(fills % G::kStages);
-
         for (int tile = first; tile < seen; ++tile) {
             const int s = uses % G::kStages;
             if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(s), (uses / G::kStages) & 1, kErrWaitData))) {
@@ -397,17 +394,14 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 break;
             }
             ++uses;
-            float tks0 = 0, tks1 = 0, tvs0 = 0, tvs1 = 0;
-            int bad = 0;
-#pragma unroll
-            for (int q = 0; q < G::kStages; ++q)
-                if (q == s) {
-                    tks0 = rks0[q];
-                    tks1 = rks1[q];
-                    tvs0 = rvs0[q];
-                    tvs1 = rvs1[q];
-                    bad = rbad[q];
-                }
+            if (tile - base_tile == 32) {
+                cur = nxt;
+                base_tile = tile;
+            }
+            const float tks0 = __shfl_sync(0xffffffffu, cur.ks0, tile - base_tile);
+            const float tvs0 = __shfl_sync(0xffffffffu, cur.vs0, tile - base_tile);
+            const float tks1 = two ? __shfl_sync(0xffffffffu, cur.ks1, tile - base_tile) : tks0;
+            const float tvs1 = two ? __shfl_sync(0xffffffffu, cur.vs1, tile - base_tile) : tvs0;
             const uint32_t kb = ring + s * G::kStageBytes, vb = kb + G::kHalfBytes;
             const int key0 = tile * kTileKeys;
             if (key0 + kTileKeys > key_end) {
@@ -440,7 +434,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             }
             // ---- softmax of rows g (elements 0, 1) and g + 8 (2, 3); columns 2 c, 2 c + 1 of each tile
             float mx[2] = {-INFINITY, -INFINITY};
-            const bool masked = key0 + kTileKeys > all_see || bad != 0;
+            const bool masked = key0 + kTileKeys > all_see;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float ks = j < 2 ? tks0 : tks1;
@@ -449,7 +443,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     float x = sc[j][e] * (factor[e >> 1] * ks);
                     if (masked) {
                         const int key = key0 + 8 * j + static_cast<int>(2 * c) + (e & 1);
-                        if (key >= limit[e >> 1] || (bad & (j < 2 ? 1 : 2))) x = -INFINITY;
+                        if (key >= limit[e >> 1]) x = -INFINITY;
                     }
                     sc[j][e] = x;
                     mx[e >> 1] = fmaxf(mx[e >> 1], x);
@@ -527,7 +521,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             }
             if (key0 + kTileKeys > key_end) fence_proxy_async_smem();   // the cleared rows, before a load may follow
             __syncwarp();                    // every lane has read the stage
-            if (next < seen) feed(s);
+            if (next < seen) feed();
         }
         if (!ok) break;
 
