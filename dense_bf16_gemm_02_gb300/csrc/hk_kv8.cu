@@ -119,7 +119,9 @@ bool g_setup[kMaxDevices] = {};
 
 template <int kD, typename T>
 cudaError_t setup_decode() {
-    return cudaFuncSetAttribute(kv8_decode_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeGeometry<kD>::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeGeometry<kD>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kv8_decode_block_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, BlockGeometry<kD>::kSmemBytes);
 }
 
 template <int kD>
@@ -161,6 +163,9 @@ DecodeWorkspace decode_workspace(int64_t D) {
 // kernel takes the work: below it the keys and values are read once or a few
 // times as codes, above it they are brought to bf16 first.
 constexpr int64_t kPrefillRows = 64;
+
+// Tiles per warp up to which a unit is one block's (beyond, its tiles are spread over the whole GPU).
+constexpr int kBlockTiles = 16;
 
 // Sequences that are brought to bf16 at a time: as many as fit 512 MB, one at least.
 constexpr int64_t kWidenBytes = int64_t(512) << 20;
@@ -221,7 +226,10 @@ void launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
 }
 
 template <int kD, typename T>
-cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, cudaStream_t st) {
+cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, bool by_unit, cudaStream_t st) {
+    if (by_unit)
+        return launch_early(&kv8_decode_block_kernel<kD, T>, dim3(static_cast<unsigned>(p.B * p.Hkv * p.row_tiles)),
+                            dim3(32 * kBlockWarps), BlockGeometry<kD>::kSmemBytes, st, tk, tv, p);
     cudaError_t e = launch_early(&kv8_decode_kernel<kD, T>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kDecodeWarps),
                                  DecodeGeometry<kD>::kSmemBytes, st, tk, tv, p);
     if (e != cudaSuccess) return e;
@@ -461,9 +469,11 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.wait.status = status;
     p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
     // one round of blocks, and no more than the table has room for tiles
-    const int64_t room = ceil_div(std::min(B, int64_t(kMaxBatch)) * p.Hkv * p.row_tiles * ceil_div(max_pages * p.page_size, kTileKeys),
-                                  kDecodeWarps);
-    const int blocks = static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), room));
+    const int64_t units = std::min(B, int64_t(kMaxBatch)) * p.Hkv * p.row_tiles;
+    const int64_t unit_room = ceil_div(max_pages * p.page_size, kTileKeys);
+    const int blocks = static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), ceil_div(units * unit_room, kDecodeWarps)));
+    // units that one round of blocks holds, and short ones: a block each
+    const bool by_unit = units <= sms && unit_room <= kBlockWarps * kBlockTiles;
     for (int64_t b0 = 0; b0 < B; b0 += kMaxBatch) {       // (launches of one stream: they may share the workspace)
         p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, kMaxBatch));
         p.q = static_cast<const uint16_t*>(Q) + b0 * p.q_stride_b;
@@ -476,9 +486,11 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
         cudaError_t e;
         const bool half = type == HK_TYPE_FP16;
         if (cache->head_dim == 64)
-            e = half ? launch_decode<64, __half>(tk, tv, p, blocks, st) : launch_decode<64, __nv_bfloat16>(tk, tv, p, blocks, st);
+            e = half ? launch_decode<64, __half>(tk, tv, p, blocks, by_unit, st)
+                     : launch_decode<64, __nv_bfloat16>(tk, tv, p, blocks, by_unit, st);
         else
-            e = half ? launch_decode<128, __half>(tk, tv, p, blocks, st) : launch_decode<128, __nv_bfloat16>(tk, tv, p, blocks, st);
+            e = half ? launch_decode<128, __half>(tk, tv, p, blocks, by_unit, st)
+                     : launch_decode<128, __nv_bfloat16>(tk, tv, p, blocks, by_unit, st);
         if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache attention", e);
     }
     return HK_OK;

@@ -183,12 +183,292 @@ __device__ __forceinline__ void store_row(T* dst, const float (&v)[kCols], bool 
     }
 }
 
+// One warp over tiles [first, last) of a unit (16 query rows rt of sequence b,
+// KV head h): the unnormalised output, maxima (log2 units) and this thread's
+// share of the sums. `ring`, `bars`: the warp's own stages and their barriers.
+// False when a wait gave up (the copies in flight are then still to be waited for).
+template <int kD, typename T, int kStages>
+__device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k, const void* tmap_v, uint32_t ring, uint32_t bars,
+                                       int& fills, int& uses, int b, int h, int rt, const Sequence& seq, int key_end, int first,
+                                       int last, float (&o)[kD / 8][4], float (&m)[2], float (&l)[2]) {
+    constexpr int kWords = kD / 16;          // 4-code words of a row that a thread holds (one K step each)
+    constexpr int kNTiles = kD / 8;          // 8-column tiles of the output
+    constexpr int kOwn = kD / 4;             // output columns of a thread
+    constexpr int kHalfBytes = kTileKeys * kD, kStageBytes = 2 * kHalfBytes;
+    const uint32_t lane = lane_id();
+    const uint32_t g = lane >> 2, c = lane & 3u;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    bool ok = true;
+
+    // ---- pages and scales of 32 tiles, one tile per lane (two pages where a page is 16 tokens; -1: not a
+    // page), for the tiles from `base` on and, once a load runs past them, for the 32 after those
+    struct Window {
+        int page0, page1;
+        float ks0, ks1, vs0, vs1;
+    };
+    const bool two = p.page_size < kTileKeys;
+    auto look_up = [&](Window& w, int tile0) {
+        auto page_of = [&](int key) {
+            if (key >= key_end) return -1;
+            const int32_t pg = p.table[b * p.table_stride + (key >> p.page_shift)];
+            if (pg < 0 || pg >= p.num_pages) {
+                atomicOr(p.wait.status, kErrPage);
+                return -1;
+            }
+            return static_cast<int>(pg);
+        };
+        const int key = (tile0 + static_cast<int>(lane)) * kTileKeys;
+        w.page0 = page_of(key);
+        w.page1 = two ? page_of(key + 16) : w.page0;
+    };
+    // (no page: scale 0, so that nothing of page 0, read in its place, comes through)
+    auto look_up_scales = [&](Window& w) {
+        auto scale_of = [&](const float* scale, int pg) {
+            return pg >= 0 ? scale[static_cast<int64_t>(pg) * p.Hkv + h] : 0.0f;
+        };
+        w.ks0 = scale_of(p.k_scale, w.page0);
+        w.vs0 = scale_of(p.v_scale, w.page0);
+        w.ks1 = two ? scale_of(p.k_scale, w.page1) : w.ks0;
+        w.vs1 = two ? scale_of(p.v_scale, w.page1) : w.vs0;
+    };
+    const int seen = key_end > 0 ? last : first;      // a unit that sees nothing has no tile to read
+    int base_tile = first, next = first;              // the current window's first tile, the next tile to load
+    Window cur = {0, 0, 0.0f, 0.0f, 0.0f, 0.0f}, nxt = cur;
+    auto feed = [&]() {
+        const int at32 = next - base_tile;
+        if (at32 == 32) {
+            look_up(nxt, next);
+            look_up_scales(nxt);
+        }
+        const int pg0 = __shfl_sync(0xffffffffu, at32 < 32 ? cur.page0 : nxt.page0, at32 & 31);
+        const int pg1 = two ? __shfl_sync(0xffffffffu, at32 < 32 ? cur.page1 : nxt.page1, at32 & 31) : pg0;
+        const int s = fills % kStages;
+        if (lane == 0) {
+            const uint32_t dst = ring + s * kStageBytes;
+            mbar_arrive_expect_tx(full_bar(s), kStageBytes);
+            const int row = (next * kTileKeys) & (p.page_size - 1);
+            const int z0 = max(pg0, 0) * p.Hkv + h, z1 = max(pg1, 0) * p.Hkv + h;
+            if (!two) {
+                tma_load_3d(dst, tmap_k, 0, row, z0, full_bar(s));
+                tma_load_3d(dst + kHalfBytes, tmap_v, 0, row, z0, full_bar(s));
+            } else {
+                tma_load_3d(dst, tmap_k, 0, 0, z0, full_bar(s));
+                tma_load_3d(dst + kHalfBytes / 2, tmap_k, 0, 0, z1, full_bar(s));
+                tma_load_3d(dst + kHalfBytes, tmap_v, 0, 0, z0, full_bar(s));
+                tma_load_3d(dst + kHalfBytes * 3 / 2, tmap_v, 0, 0, z1, full_bar(s));
+            }
+        }
+        ++fills;
+        ++next;
+    };
+    // the first tiles' loads go out before anything else is waited for
+    if (first < seen) {
+        look_up(cur, first);
+        for (int i = 0; i < kStages && next < seen; ++i) feed();
+        look_up_scales(cur);
+    }
+
+    // ---- query rows g and g + 8 of the unit: f16 fragments and the factor of their scores
+    uint32_t qf[kWords][4];
+    float factor[2];
+    int limit[2];                        // tokens the row sees
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = rt * kRows + static_cast<int>(g) + 8 * i;
+        const int t = row / p.group;
+        const bool live = t < seq.count;
+        // (rows past T are never stored and need no mask)
+        limit[i] = t >= p.T ? 0x7FFFFFFF : !live ? 0 : p.causal ? max(0, seq.len - seq.count + t + 1) : seq.len;
+        const T* const src = static_cast<const T*>(p.q) + b * p.q_stride_b + t * p.q_stride_t +
+                             static_cast<int64_t>(h * p.group + row % p.group) * p.q_stride_h;
+        Raw8<T> rawq[kD / 32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k) {
+            rawq[k] = load8<T>(src, static_cast<int64_t>(c) * kOwn + 8 * k, live ? kD : 0, p.vec_q != 0);
+            float v[8];
+            widen8<T>(rawq[k], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(10 - floor(log2 top)), kept a normal number; 1 for rows of zeros and rows with an infinity or NaN
+        int field = 127 + 10 - (static_cast<int>(top >> 23) - 127);
+        if (top == 0 || top >= 0x7F800000u) field = 127;
+        field = min(max(field, 1), 253);
+        const float mul = __uint_as_float(static_cast<uint32_t>(field) << 23);
+        factor[i] = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * p.scale_log2;
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k) {
+            float v[8];
+            widen8<T>(rawq[k], v);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                qf[2 * k + w][i] = pack_f16x2(v[4 * w] * mul, v[4 * w + 1] * mul);
+                qf[2 * k + w][2 + i] = pack_f16x2(v[4 * w + 2] * mul, v[4 * w + 3] * mul);
+            }
+        }
+    }
+    int all_see = min(limit[0], limit[1]);      // tokens that every row sees: no mask needed below
+    all_see = __reduce_min_sync(0xffffffffu, all_see);
+
+#pragma unroll
+    for (int j = 0; j < kNTiles; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
+
+    for (int tile = first; tile < seen; ++tile) {
+        const int s = uses % kStages;
+        if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(s), (uses / kStages) & 1, kErrWaitData))) {
+            ok = false;
+            break;
+        }
+        ++uses;
+        if (tile - base_tile == 32) {
+            cur = nxt;
+            base_tile = tile;
+        }
+        const float tks0 = __shfl_sync(0xffffffffu, cur.ks0, tile - base_tile);
+        const float tvs0 = __shfl_sync(0xffffffffu, cur.vs0, tile - base_tile);
+        const float tks1 = two ? __shfl_sync(0xffffffffu, cur.ks1, tile - base_tile) : tks0;
+        const float tvs1 = two ? __shfl_sync(0xffffffffu, cur.vs1, tile - base_tile) : tvs0;
+        const uint32_t kb = ring + s * kStageBytes, vb = kb + kHalfBytes;
+        const int key0 = tile * kTileKeys;
+        if (key0 + kTileKeys > key_end) {
+            // rows past the end hold whatever the page holds there, perhaps NaN codes that
+            // a weight of 0 would not silence: V's are cleared
+            const int from = key_end - key0;
+            for (int i = static_cast<int>(lane); i < (kTileKeys - from) * (kD / 16); i += 32)
+                st_shared_v4(vb + static_cast<uint32_t>(from * kD + 16 * i), 0, 0, 0, 0);   // (whole rows: any order inside)
+            __syncwarp();
+        }
+
+        // ---- scores of 32 tokens: key tiles of 8, column g of tile j is token 8 j + g
+        float sc[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
+            uint32_t w[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 x = ld_shared_v4(kb + chunk_offset<kD>(8u * j + g, (kWords / 4) * c + i));
+                w[4 * i] = x.x;
+                w[4 * i + 1] = x.y;
+                w[4 * i + 2] = x.z;
+                w[4 * i + 3] = x.w;
+            }
+#pragma unroll
+            for (int k = 0; k < kWords; ++k)
+                mma_f16(sc[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], e4m3x2_to_f16x2(w[k] & 0xFFFFu),
+                        e4m3x2_to_f16x2(w[k] >> 16));
+        }
+        // ---- softmax of rows g (elements 0, 1) and g + 8 (2, 3); columns 2 c, 2 c + 1 of each tile
+        float mx[2] = {-INFINITY, -INFINITY};
+        const bool masked = key0 + kTileKeys > all_see;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float ks = j < 2 ? tks0 : tks1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = sc[j][e] * (factor[e >> 1] * ks);
+                if (masked) {
+                    const int key = key0 + 8 * j + static_cast<int>(2 * c) + (e & 1);
+                    if (key >= limit[e >> 1]) x = -INFINITY;
+                }
+                sc[j][e] = x;
+                mx[e >> 1] = fmaxf(mx[e >> 1], x);
+            }
+        }
+        float alpha[2];
+        bool moved = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            const float now = fmaxf(m[i], mx[i]);
+            alpha[i] = now > m[i] ? ex2_approx(m[i] - now) : 1.0f;
+            moved = moved || now > m[i];
+            m[i] = now;
+            l[i] *= alpha[i];
+        }
+        const float sub0 = m[0] == -INFINITY ? 0.0f : m[0], sub1 = m[1] == -INFINITY ? 0.0f : m[1];
+        uint32_t pf[4][2];               // P of tile j, rows g and g + 8, as f16 pairs
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p0 = ex2_approx(sc[j][0] - sub0), p1 = ex2_approx(sc[j][1] - sub0);
+            const float p2 = ex2_approx(sc[j][2] - sub1), p3 = ex2_approx(sc[j][3] - sub1);
+            l[0] += p0 + p1;
+            l[1] += p2 + p3;
+            pf[j][0] = pack_f16x2(p0, p1);
+            pf[j][1] = pack_f16x2(p2, p3);
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int j = 0; j < kNTiles; ++j) {
+                o[j][0] *= alpha[0];
+                o[j][1] *= alpha[0];
+                o[j][2] *= alpha[1];
+                o[j][3] *= alpha[1];
+            }
+        }
+        // ---- O += (P·V) · scale: tokens in two steps of 16; column g of output tile j is
+        // dimension g · (D / 8) + j, so a thread reads D / 8 consecutive codes of four rows
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const float vs = st == 0 ? tvs0 : tvs1;
+            uint32_t r[4][kD / 32];      // rows 16 st + 2 c, + 1, + 8, + 9
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t row = 16u * st + 2u * c + (i & 1) + (i >> 1) * 8u;
+                if constexpr (kD == 128) {
+                    const uint4 x = ld_shared_v4(vb + chunk_offset<kD>(row, g));
+                    r[i][0] = x.x;
+                    r[i][1] = x.y;
+                    r[i][2] = x.z;
+                    r[i][3] = x.w;
+                } else {
+                    const uint2 x = ld_shared_v2(vb + chunk_offset<kD>(row, g >> 1) + (g & 1u) * 8u);
+                    r[i][0] = x.x;
+                    r[i][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < kD / 32; ++w) {
+                const uint32_t a0 = __byte_perm(r[0][w], r[1][w], 0x5140), a1 = __byte_perm(r[0][w], r[1][w], 0x7362);
+                const uint32_t b0 = __byte_perm(r[2][w], r[3][w], 0x5140), b1 = __byte_perm(r[2][w], r[3][w], 0x7362);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = e < 2 ? a0 : a1, hi = e < 2 ? b0 : b1;
+                    const uint32_t v0 = e & 1 ? lo >> 16 : lo & 0xFFFFu, v1 = e & 1 ? hi >> 16 : hi & 0xFFFFu;
+                    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma_f16(t, pf[2 * st][0], pf[2 * st][1], pf[2 * st + 1][0], pf[2 * st + 1][1], e4m3x2_to_f16x2(v0),
+                            e4m3x2_to_f16x2(v1));
+                    const int j = 4 * w + e;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[j][q] = fmaf(t[q], vs, o[j][q]);
+                }
+            }
+        }
+        if (key0 + kTileKeys > key_end) fence_proxy_async_smem();   // the cleared rows, before a load may follow
+        __syncwarp();                    // every lane has read the stage
+        if (next < seen) feed();
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {            // the rows' sums over their four threads
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    return ok;
+}
+
 template <int kD, typename T>
 __global__ void __launch_bounds__(32 * kDecodeWarps, 2)
 kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const DecodeParams p) {
     using G = DecodeGeometry<kD>;
-    constexpr int kWords = kD / 16;          // 4-code words of a row that a thread holds (one K step each)
     constexpr int kNTiles = kD / 8;          // 8-column tiles of the output
     constexpr int kOwn = kD / 4;             // output columns of a thread
     extern __shared__ uint8_t smem_raw[];
@@ -207,9 +487,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     }
 
     const uint32_t ring = base + warp * G::kWarpBytes;
-    auto full_bar = [&](int s) { return base + G::kOffBars + 8u * (warp * G::kStages + s); };
+    const uint32_t bars = base + G::kOffBars + 8u * warp * G::kStages;
     if (lane == 0) {
-        for (int s = 0; s < G::kStages; ++s) mbar_init(full_bar(s), 1);
+        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, 1);
         fence_mbar_init_cluster();
     }
     griddep_wait();                          // launched early behind the kernel that may have written the cache or q
@@ -267,270 +547,11 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         const int unit_tiles = tiles_of(key_end);
         const int last = static_cast<int>(min(static_cast<int64_t>(unit_tiles), first + (end - at)));   // tiles [first, last)
 
-        // ---- pages and scales of 32 tiles, one tile per lane (two pages where a page is 16 tokens; -1: not a
-        // page), for the tiles from `base` on and, once a load runs past them, for the 32 after those
-        struct Window {
-            int page0, page1;
-            float ks0, ks1, vs0, vs1;
-        };
-        const bool two = p.page_size < kTileKeys;
-        auto look_up = [&](Window& w, int tile0) {
-            auto page_of = [&](int key) {
-                if (key >= key_end) return -1;
-                const int32_t pg = p.table[b * p.table_stride + (key >> p.page_shift)];
-                if (pg < 0 || pg >= p.num_pages) {
-                    atomicOr(p.wait.status, kErrPage);
-                    return -1;
-                }
-                return static_cast<int>(pg);
-            };
-            const int key = (tile0 + static_cast<int>(lane)) * kTileKeys;
-            w.page0 = page_of(key);
-            w.page1 = two ? page_of(key + 16) : w.page0;
-        };
-        // (no page: scale 0, so that nothing of page 0, read in its place, comes through)
-        auto look_up_scales = [&](Window& w) {
-            auto scale_of = [&](const float* scale, int pg) {
-                return pg >= 0 ? scale[static_cast<int64_t>(pg) * p.Hkv + h] : 0.0f;
-            };
-            w.ks0 = scale_of(p.k_scale, w.page0);
-            w.vs0 = scale_of(p.v_scale, w.page0);
-            w.ks1 = two ? scale_of(p.k_scale, w.page1) : w.ks0;
-            w.vs1 = two ? scale_of(p.v_scale, w.page1) : w.vs0;
-        };
-        const int seen = key_end > 0 ? last : first;      // a unit that sees nothing has no tile to read
-        int base_tile = first, next = first;              // the current window's first tile, the next tile to load
-        Window cur = {0, 0, 0.0f, 0.0f, 0.0f, 0.0f}, nxt = cur;
-        auto feed = [&]() {
-            const int at32 = next - base_tile;
-            if (at32 == 32) {
-                look_up(nxt, next);
-                look_up_scales(nxt);
-            }
-            const int pg0 = __shfl_sync(0xffffffffu, at32 < 32 ? cur.page0 : nxt.page0, at32 & 31);
-            const int pg1 = two ? __shfl_sync(0xffffffffu, at32 < 32 ? cur.page1 : nxt.page1, at32 & 31) : pg0;
-            const int s = fills % G::kStages;
-            if (lane == 0) {
-                const uint32_t dst = ring + s * G::kStageBytes;
-                mbar_arrive_expect_tx(full_bar(s), G::kStageBytes);
-                const int row = (next * kTileKeys) & (p.page_size - 1);
-                const int z0 = max(pg0, 0) * p.Hkv + h, z1 = max(pg1, 0) * p.Hkv + h;
-                if (!two) {
-                    tma_load_3d(dst, &tmap_k, 0, row, z0, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, row, z0, full_bar(s));
-                } else {
-                    tma_load_3d(dst, &tmap_k, 0, 0, z0, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes / 2, &tmap_k, 0, 0, z1, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes, &tmap_v, 0, 0, z0, full_bar(s));
-                    tma_load_3d(dst + G::kHalfBytes * 3 / 2, &tmap_v, 0, 0, z1, full_bar(s));
-                }
-            }
-            ++fills;
-            ++next;
-        };
-        // the first tiles' loads go out before anything else is waited for
-        if (first < seen) {
-            look_up(cur, first);
-            for (int i = 0; i < G::kStages && next < seen; ++i) feed();
-            look_up_scales(cur);
-        }
-
-        // ---- query rows g and g + 8 of the unit: f16 fragments and the factor of their scores
-        uint32_t qf[kWords][4];
-        float factor[2];
-        int limit[2];                        // tokens the row sees
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = rt * kRows + static_cast<int>(g) + 8 * i;
-            const int t = row / p.group;
-            const bool live = t < seq.count;
-            // (rows past T are never stored and need no mask)
-            limit[i] = t >= p.T ? 0x7FFFFFFF : !live ? 0 : p.causal ? max(0, seq.len - seq.count + t + 1) : seq.len;
-            const T* const src = static_cast<const T*>(p.q) + b * p.q_stride_b + t * p.q_stride_t +
-                                 static_cast<int64_t>(h * p.group + row % p.group) * p.q_stride_h;
-            Raw8<T> rawq[kD / 32];
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < kD / 32; ++k) {
-                rawq[k] = load8<T>(src, static_cast<int64_t>(c) * kOwn + 8 * k, live ? kD : 0, p.vec_q != 0);
-                float v[8];
-                widen8<T>(rawq[k], v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^(10 - floor(log2 top)), kept a normal number; 1 for rows of zeros and rows with an infinity or NaN
-            int field = 127 + 10 - (static_cast<int>(top >> 23) - 127);
-            if (top == 0 || top >= 0x7F800000u) field = 127;
-            field = min(max(field, 1), 253);
-            const float mul = __uint_as_float(static_cast<uint32_t>(field) << 23);
-            factor[i] = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * p.scale_log2;
-#pragma unroll
-            for (int k = 0; k < kD / 32; ++k) {
-                float v[8];
-                widen8<T>(rawq[k], v);
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    qf[2 * k + w][i] = pack_f16x2(v[4 * w] * mul, v[4 * w + 1] * mul);
-                    qf[2 * k + w][2 + i] = pack_f16x2(v[4 * w + 2] * mul, v[4 * w + 3] * mul);
-                }
-            }
-        }
-        int all_see = min(limit[0], limit[1]);      // tokens that every row sees: no mask needed below
-        all_see = __reduce_min_sync(0xffffffffu, all_see);
-
-        float o[kNTiles][4];
-#pragma unroll
-        for (int j = 0; j < kNTiles; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
-        for (int tile = first; tile < seen; ++tile) {
-            const int s = uses % G::kStages;
-            if (!__all_sync(0xffffffffu, wait_mbar(p.wait, full_bar(s), (uses / G::kStages) & 1, kErrWaitData))) {
-                ok = false;
-                break;
-            }
-            ++uses;
-            if (tile - base_tile == 32) {
-                cur = nxt;
-                base_tile = tile;
-            }
-            const float tks0 = __shfl_sync(0xffffffffu, cur.ks0, tile - base_tile);
-            const float tvs0 = __shfl_sync(0xffffffffu, cur.vs0, tile - base_tile);
-            const float tks1 = two ? __shfl_sync(0xffffffffu, cur.ks1, tile - base_tile) : tks0;
-            const float tvs1 = two ? __shfl_sync(0xffffffffu, cur.vs1, tile - base_tile) : tvs0;
-            const uint32_t kb = ring + s * G::kStageBytes, vb = kb + G::kHalfBytes;
-            const int key0 = tile * kTileKeys;
-            if (key0 + kTileKeys > key_end) {
-                // rows past the end hold whatever the page holds there, perhaps NaN codes that
-                // a weight of 0 would not silence: V's are cleared
-                const int from = key_end - key0;
-                for (int i = static_cast<int>(lane); i < (kTileKeys - from) * (kD / 16); i += 32)
-                    st_shared_v4(vb + static_cast<uint32_t>(from * kD + 16 * i), 0, 0, 0, 0);   // (whole rows: any order inside)
-                __syncwarp();
-            }
-
-            // ---- scores of 32 tokens: key tiles of 8, column g of tile j is token 8 j + g
-            float sc[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
-                uint32_t w[kWords];
-#pragma unroll
-                for (int i = 0; i < kWords / 4; ++i) {
-                    const uint4 x = ld_shared_v4(kb + chunk_offset<kD>(8u * j + g, (kWords / 4) * c + i));
-                    w[4 * i] = x.x;
-                    w[4 * i + 1] = x.y;
-                    w[4 * i + 2] = x.z;
-                    w[4 * i + 3] = x.w;
-                }
-#pragma unroll
-                for (int k = 0; k < kWords; ++k)
-                    mma_f16(sc[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], e4m3x2_to_f16x2(w[k] & 0xFFFFu),
-                            e4m3x2_to_f16x2(w[k] >> 16));
-            }
-            // ---- softmax of rows g (elements 0, 1) and g + 8 (2, 3); columns 2 c, 2 c + 1 of each tile
-            float mx[2] = {-INFINITY, -INFINITY};
-            const bool masked = key0 + kTileKeys > all_see;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float ks = j < 2 ? tks0 : tks1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = sc[j][e] * (factor[e >> 1] * ks);
-                    if (masked) {
-                        const int key = key0 + 8 * j + static_cast<int>(2 * c) + (e & 1);
-                        if (key >= limit[e >> 1]) x = -INFINITY;
-                    }
-                    sc[j][e] = x;
-                    mx[e >> 1] = fmaxf(mx[e >> 1], x);
-                }
-            }
-            float alpha[2];
-            bool moved = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-                const float now = fmaxf(m[i], mx[i]);
-                alpha[i] = now > m[i] ? ex2_approx(m[i] - now) : 1.0f;
-                moved = moved || now > m[i];
-                m[i] = now;
-                l[i] *= alpha[i];
-            }
-            const float sub0 = m[0] == -INFINITY ? 0.0f : m[0], sub1 = m[1] == -INFINITY ? 0.0f : m[1];
-            uint32_t pf[4][2];               // P of tile j, rows g and g + 8, as f16 pairs
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float p0 = ex2_approx(sc[j][0] - sub0), p1 = ex2_approx(sc[j][1] - sub0);
-                const float p2 = ex2_approx(sc[j][2] - sub1), p3 = ex2_approx(sc[j][3] - sub1);
-                l[0] += p0 + p1;
-                l[1] += p2 + p3;
-                pf[j][0] = pack_f16x2(p0, p1);
-                pf[j][1] = pack_f16x2(p2, p3);
-            }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int j = 0; j < kNTiles; ++j) {
-                    o[j][0] *= alpha[0];
-                    o[j][1] *= alpha[0];
-                    o[j][2] *= alpha[1];
-                    o[j][3] *= alpha[1];
-                }
-            }
-            // ---- O += (P·V) · scale: tokens in two steps of 16; column g of output tile j is
-            // dimension g · (D / 8) + j, so a thread reads D / 8 consecutive codes of four rows
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const float vs = st == 0 ? tvs0 : tvs1;
-                uint32_t r[4][kD / 32];      // rows 16 st + 2 c, + 1, + 8, + 9
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t row = 16u * st + 2u * c + (i & 1) + (i >> 1) * 8u;
-                    if constexpr (kD == 128) {
-                        const uint4 x = ld_shared_v4(vb + chunk_offset<kD>(row, g));
-                        r[i][0] = x.x;
-                        r[i][1] = x.y;
-                        r[i][2] = x.z;
-                        r[i][3] = x.w;
-                    } else {
-                        const uint2 x = ld_shared_v2(vb + chunk_offset<kD>(row, g >> 1) + (g & 1u) * 8u);
-                        r[i][0] = x.x;
-                        r[i][1] = x.y;
-                    }
-                }
-#pragma unroll
-                for (int w = 0; w < kD / 32; ++w) {
-                    const uint32_t a0 = __byte_perm(r[0][w], r[1][w], 0x5140), a1 = __byte_perm(r[0][w], r[1][w], 0x7362);
-                    const uint32_t b0 = __byte_perm(r[2][w], r[3][w], 0x5140), b1 = __byte_perm(r[2][w], r[3][w], 0x7362);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t lo = e < 2 ? a0 : a1, hi = e < 2 ? b0 : b1;
-                        const uint32_t v0 = e & 1 ? lo >> 16 : lo & 0xFFFFu, v1 = e & 1 ? hi >> 16 : hi & 0xFFFFu;
-                        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma_f16(t, pf[2 * st][0], pf[2 * st][1], pf[2 * st + 1][0], pf[2 * st + 1][1], e4m3x2_to_f16x2(v0),
-                                e4m3x2_to_f16x2(v1));
-                        const int j = 4 * w + e;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) o[j][q] = fmaf(t[q], vs, o[j][q]);
-                    }
-                }
-            }
-            if (key0 + kTileKeys > key_end) fence_proxy_async_smem();   // the cleared rows, before a load may follow
-            __syncwarp();                    // every lane has read the stage
-            if (next < seen) feed();
-        }
+        float o[kNTiles][4], m[2], l[2];
+        ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, b, h, rt, seq, key_end, first, last, o, m, l);
         if (!ok) break;
 
-        // ---- the rows' sums over their four threads; finish the unit or leave its partial sums
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
+        // ---- finish the unit or leave its partial sums
         const bool whole = first == 0 && last == unit_tiles;
         const int slot = 2 * self + (at == begin ? 0 : 1);
         if (!whole && first == 0) {          // this run holds the unit's first tile: it leads the sum
@@ -575,7 +596,129 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     if (lane == 0) p.info[self] = info;
     // abort: the copies in flight land before the block ends
     if (!ok)
-        for (; uses < fills; ++uses) wait_mbar_drain(full_bar(uses % G::kStages), (uses / G::kStages) & 1);
+        for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
+}
+
+// One block per unit: its eight warps share the unit's tiles out among them and
+// join their sums through shared memory. For short sequences, and no more units
+// than SMs: one launch, and no pass over lengths before the first load.
+constexpr int kBlockWarps = 8;
+
+template <int kD>
+struct BlockGeometry {
+    using G = DecodeGeometry<kD>;
+    static constexpr int kOffBars = kBlockWarps * G::kWarpBytes;
+    static constexpr int kSmemBytes = kOffBars + kBlockWarps * G::kStages * 8 + 1024;
+    // a warp's sums in its ring's place: the columns of a thread 16 bytes apart from the next thread's, so
+    // that eight threads' 16-byte stores meet no bank twice
+    static constexpr int kOwn = kD / 4;
+    static constexpr int kPitch = kOwn + 4;                           // floats
+    static_assert(kRows * 4 * kPitch * 4 <= G::kWarpBytes && kSmemBytes <= 232448, "shared memory");
+};
+
+template <int kD, typename T>
+__global__ void __launch_bounds__(32 * kBlockWarps, 1)
+kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                        const DecodeParams p) {
+    using G = DecodeGeometry<kD>;
+    using B = BlockGeometry<kD>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ float warp_ml[kBlockWarps][kRows][2];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw);
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    const uint32_t g = lane >> 2, c = lane & 3u;
+    const uint32_t ring = base + warp * G::kWarpBytes, bars = base + B::kOffBars + 8u * warp * G::kStages;
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tmap_k);
+        prefetch_tensor_map(&tmap_v);
+    }
+    if (lane == 0) {
+        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, 1);
+        fence_mbar_init_cluster();
+    }
+    __syncwarp();
+    griddep_wait();                          // launched early behind the kernel that may have written the cache or q
+    int unit = static_cast<int>(blockIdx.x);
+    const int rt = unit % p.row_tiles;
+    unit /= p.row_tiles;
+    const int h = unit % p.Hkv, b = unit / p.Hkv;
+    const Sequence seq = sequence(p, b);
+    const int key_end = row_tile_end(p, seq, rt);
+    const int tiles = (key_end + kTileKeys - 1) / kTileKeys;
+    const int each = (tiles + kBlockWarps - 1) / kBlockWarps;
+    const int first = min(tiles, static_cast<int>(warp) * each), last = min(tiles, first + each);
+    bool ok = true;
+    {
+        float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        if (first < last) {
+            int fills = 0, uses = 0;
+            ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, b, h, rt, seq, key_end, first, last, o, m, l);
+            if (ok) {
+                float* const part = reinterpret_cast<float*>(smem + warp * G::kWarpBytes);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float4* const dst = reinterpret_cast<float4*>(part + ((g + 8 * i) * 4 + c) * B::kPitch);
+#pragma unroll
+                    for (int k = 0; k < kD / 32; ++k) {
+                        dst[k] = make_float4(o[4 * k][2 * i], o[4 * k + 1][2 * i], o[4 * k + 2][2 * i], o[4 * k + 3][2 * i]);
+                        dst[kD / 32 + k] =
+                            make_float4(o[4 * k][2 * i + 1], o[4 * k + 1][2 * i + 1], o[4 * k + 2][2 * i + 1], o[4 * k + 3][2 * i + 1]);
+                    }
+                }
+            } else {                         // the copies in flight land before the block ends
+                for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
+            }
+        }
+        if (c == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                warp_ml[warp][g + 8 * i][0] = ok ? m[i] : -INFINITY;
+                warp_ml[warp][g + 8 * i][1] = ok ? l[i] : 0.0f;
+            }
+        }
+    }
+    if (__syncthreads_or(!ok)) return;       // (nothing is stored after a wait that gave up)
+    // 16 threads per row, kD / 16 columns each
+    constexpr int kCols = kD / 16;
+    const int r = static_cast<int>(threadIdx.x >> 4), col = static_cast<int>(threadIdx.x & 15u) * kCols;
+    const int row = rt * kRows + r;
+    const int t = row / p.group, head = h * p.group + row % p.group;
+    if (t >= p.T) return;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kBlockWarps; ++w) m = fmaxf(m, warp_ml[w][r][0]);
+    float l = 0.0f, acc[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBlockWarps; ++w) {
+        if (w * each >= tiles) break;        // (that warp had no tile, nor has any after it)
+        const float mw = warp_ml[w][r][0];
+        const float weight = mw == -INFINITY ? 0.0f : ex2_approx(mw - m);
+        l += warp_ml[w][r][1] * weight;
+        const float* const part = reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + (r * 4 + col / B::kOwn) * B::kPitch + col % B::kOwn;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] += part[k] * weight;
+    }
+    const bool any = l > 0.0f || l != l;
+    const float mul = any ? 1.0f / l : 0.0f;
+    T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + col;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] *= mul;
+    if (p.vec_o) {
+#pragma unroll
+        for (int k = 0; k < kCols / 4; ++k)
+            reinterpret_cast<uint2*>(dst)[k] =
+                make_uint2(pack_out<T>(acc[4 * k], acc[4 * k + 1]), pack_out<T>(acc[4 * k + 2], acc[4 * k + 3]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) dst[k] = from_float<T>(acc[k]);
+    }
+    if (p.lse != nullptr && col == 0)
+        p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Adds up the partial sums of the units that several warps' runs share. Block
