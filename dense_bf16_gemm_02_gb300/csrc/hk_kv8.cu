@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -144,18 +145,23 @@ hk_status setup(int device) {
     return HK_OK;
 }
 
-// Workspace of the split kernel: partial sums and their maxima and sums for two
-// units per warp, and a record per warp.
+// Sequences of one launch of the few-row kernels: units stay below 2^20 (or are one sequence's).
+int64_t decode_batch(int64_t B, int64_t heads, int64_t row_tiles) {
+    return std::min(B, std::min<int64_t>(kMaxBatch, std::max<int64_t>(1, (int64_t(1) << 20) / (heads * row_tiles))));
+}
+
+// Workspace of the kernel that spreads tiles over the GPU: partial sums and their
+// maxima and sums for two units per warp, and a record per unit.
 struct DecodeWorkspace {
     size_t ml, info, total;
 };
-
-DecodeWorkspace decode_workspace(int64_t D) {
+DecodeWorkspace decode_workspace(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq) {
     const size_t warps = static_cast<size_t>(2 * kSms) * kDecodeWarps;
+    const int64_t row_tiles = ceil_div(T * (Hq / c->heads), kRows);
     DecodeWorkspace w;
-    w.ml = 2 * warps * kRows * static_cast<size_t>(D) * 4;
+    w.ml = 2 * warps * kRows * static_cast<size_t>(c->head_dim) * 4;
     w.info = w.ml + 2 * warps * kRows * 2 * 4;
-    w.total = w.info + warps * sizeof(int4);
+    w.total = w.info + static_cast<size_t>(decode_batch(B, c->heads, row_tiles) * c->heads * row_tiles) * sizeof(int4);
     return w;
 }
 
@@ -225,17 +231,35 @@ void launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
         <<<static_cast<unsigned>(std::min(p.n_items, sms)), G::kThreads, G::kSmemBytes, st>>>(tq, tk, tv, p);
 }
 
+// `cluster`: blocks per unit, or 0 for the kernel that spreads all tiles over the GPU.
 template <int kD, typename T>
-cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, bool by_unit, cudaStream_t st) {
-    if (by_unit)
-        return launch_early(&kv8_decode_block_kernel<kD, T>, dim3(static_cast<unsigned>(p.B * p.Hkv * p.row_tiles)),
-                            dim3(32 * kBlockWarps), BlockGeometry<kD>::kSmemBytes, st, tk, tv, p);
+cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, int cluster, cudaStream_t st) {
+    if (cluster > 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.row_tiles * cluster));
+        cfg.blockDim = dim3(32 * kBlockWarps);
+        cfg.dynamicSmemBytes = BlockGeometry<kD>::kSmemBytes;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, &kv8_decode_block_kernel<kD, T>, tk, tv, p, cluster);
+    }
     cudaError_t e = launch_early(&kv8_decode_kernel<kD, T>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kDecodeWarps),
                                  DecodeGeometry<kD>::kSmemBytes, st, tk, tv, p);
     if (e != cudaSuccess) return e;
-    const int warps_per_row = 4;
-    return launch_early(&kv8_combine_kernel<kD, T>, dim3(static_cast<unsigned>(blocks * kDecodeWarps), kRows / (8 / warps_per_row)),
-                        dim3(256), 0, st, p, warps_per_row);
+    const int64_t units = int64_t(p.B) * p.Hkv * p.row_tiles;
+    const int rows = std::min(kRows, p.T * p.group);
+    const unsigned x = static_cast<unsigned>(units);
+    if (units * rows <= 8 * kSms)
+        return launch_early(&kv8_combine_kernel<kD, T, 8>, dim3(x, static_cast<unsigned>(rows)), dim3(256), 0, st, p);
+    return launch_early(&kv8_combine_kernel<kD, T, 1>, dim3(x, static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, p);
 }
 
 // Many query rows per KV head: the sequences' keys and values to bf16, then the
@@ -384,10 +408,10 @@ extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, con
 
 extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                   int64_t max_pages) {
-    if (!cache || cache->heads < 1 || cache->page_size < 1 || cache->head_dim < 1 || B <= 0 || T <= 0 || Hq <= 0 ||
-        max_pages <= 0 || max_pages > kLimit / cache->page_size)
+    if (!cache || cache->heads < 1 || cache->page_size < 1 || cache->head_dim < 1 || B <= 0 || T <= 0 || Hq < cache->heads ||
+        T > kLimit / 16 / (Hq / cache->heads) || max_pages <= 0 || max_pages > kLimit / cache->page_size)
         return 0;
-    const size_t split = decode_workspace(cache->head_dim).total;
+    const size_t split = decode_workspace(cache, B, T, Hq).total;
     if (T <= kPrefillRows * cache->heads / Hq) return split;
     return std::max(split, prefill_workspace(cache, B, max_pages).total);
 }
@@ -412,7 +436,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     const int64_t group = Hq / cache->heads;
     if (T > kLimit / 16 / group || ceil_div(T * group, kRows) * (ceil_div(max_pages * cache->page_size, kTileKeys) + 1) > kLimit)
         return fail(HK_ERR_INVALID_ARG, "problem too large");
-    const DecodeWorkspace ws = decode_workspace(cache->head_dim);
+    const DecodeWorkspace ws = decode_workspace(cache, B, T, Hq);
     const size_t need = hk_attention_kv8_workspace_size(cache, B, T, Hq, max_pages);
     if (!workspace || workspace_bytes < need)
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
@@ -469,13 +493,23 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.wait.status = status;
     p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
     // one round of blocks, and no more than the table has room for tiles
-    const int64_t units = std::min(B, int64_t(kMaxBatch)) * p.Hkv * p.row_tiles;
+    const int64_t batch = decode_batch(B, p.Hkv, p.row_tiles);
+    const int64_t units = batch * p.Hkv * p.row_tiles;
+    if (units > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
     const int64_t unit_room = ceil_div(max_pages * p.page_size, kTileKeys);
     const int blocks = static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), ceil_div(units * unit_room, kDecodeWarps)));
-    // units that one round of blocks holds, and short ones: a block each
-    const bool by_unit = units <= sms && unit_room <= kBlockWarps * kBlockTiles;
-    for (int64_t b0 = 0; b0 < B; b0 += kMaxBatch) {       // (launches of one stream: they may share the workspace)
-        p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, kMaxBatch));
+    // units that one round of blocks holds: a cluster of as many blocks as there is room for, while a warp's
+    // share of the table's tiles stays small
+    int cluster = 0;
+    if (units <= sms) {
+        cluster = 1;
+        while (cluster < 8 && 2 * cluster * units <= sms && 2 * cluster * kBlockWarps <= 2 * unit_room) cluster *= 2;
+        if (unit_room > cluster * kBlockWarps * kBlockTiles) cluster = 0;
+    }
+    if (const char* f = std::getenv("HK_TMP_CLUSTER")) cluster = std::atoi(f);
+    if (const char* f = std::getenv("HK_TMP_MIN")) p.min_tiles = std::atoi(f);
+    for (int64_t b0 = 0; b0 < B; b0 += batch) {       // (launches of one stream: they may share the workspace)
+        p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, batch));
         p.q = static_cast<const uint16_t*>(Q) + b0 * p.q_stride_b;
         p.o = static_cast<uint16_t*>(O) + b0 * p.o_stride_b;
         p.lse = lse ? lse + b0 * T * Hq : nullptr;
@@ -486,11 +520,11 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
         cudaError_t e;
         const bool half = type == HK_TYPE_FP16;
         if (cache->head_dim == 64)
-            e = half ? launch_decode<64, __half>(tk, tv, p, blocks, by_unit, st)
-                     : launch_decode<64, __nv_bfloat16>(tk, tv, p, blocks, by_unit, st);
+            e = half ? launch_decode<64, __half>(tk, tv, p, blocks, cluster, st)
+                     : launch_decode<64, __nv_bfloat16>(tk, tv, p, blocks, cluster, st);
         else
-            e = half ? launch_decode<128, __half>(tk, tv, p, blocks, by_unit, st)
-                     : launch_decode<128, __nv_bfloat16>(tk, tv, p, blocks, by_unit, st);
+            e = half ? launch_decode<128, __half>(tk, tv, p, blocks, cluster, st)
+                     : launch_decode<128, __nv_bfloat16>(tk, tv, p, blocks, cluster, st);
         if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache attention", e);
     }
     return HK_OK;

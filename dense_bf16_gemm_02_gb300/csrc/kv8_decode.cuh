@@ -82,7 +82,7 @@ struct DecodeParams {
     int32_t min_tiles;                              // least tiles of a run
     float* part_o;                                  // [2 · warps][16][D]
     float* part_ml;                                 // [2 · warps][16][2]
-    int4* info;                                     // [warps]: the unit whose partial sums begin with this warp's run
+    int4* info;                                     // [units]: parts whose sums make up the unit (0: it is finished), first slot, first warp
     WaitCtx wait;
 };
 
@@ -347,23 +347,24 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
         }
 
         // ---- scores of 32 tokens: key tiles of 8, column g of tile j is token 8 j + g
+        // (the four tiles' sums are independent: they go round K step by K step)
         float sc[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
-            uint32_t w[kWords];
+        for (int j = 0; j < 4; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 x = ld_shared_v4(kb + chunk_offset<kD>(8u * j + g, (kWords / 4) * c + i));
-                w[4 * i] = x.x;
-                w[4 * i + 1] = x.y;
-                w[4 * i + 2] = x.z;
-                w[4 * i + 3] = x.w;
+        for (int i = 0; i < kWords / 4; ++i) {
+            uint4 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = ld_shared_v4(kb + chunk_offset<kD>(8u * j + g, (kWords / 4) * c + i));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = 4 * i + e;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = e == 0 ? x[j].x : e == 1 ? x[j].y : e == 2 ? x[j].z : x[j].w;
+                    mma_f16(sc[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], e4m3x2_to_f16x2(w & 0xFFFFu), e4m3x2_to_f16x2(w >> 16));
+                }
             }
-#pragma unroll
-            for (int k = 0; k < kWords; ++k)
-                mma_f16(sc[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], e4m3x2_to_f16x2(w[k] & 0xFFFFu),
-                        e4m3x2_to_f16x2(w[k] >> 16));
         }
         // ---- softmax of rows g (elements 0, 1) and g + 8 (2, 3); columns 2 c, 2 c + 1 of each tile
         float mx[2] = {-INFINITY, -INFINITY};
@@ -517,7 +518,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     const int64_t total = prefix[p.B];
     const int64_t per = max(static_cast<int64_t>(p.min_tiles), (total + warps - 1) / warps);
     const int64_t begin = min(total, self * per), end = min(total, begin + per);
-    int4 info = make_int4(0, 0, 0, 0);
     bool ok = true;
     int fills = 0, uses = 0;                 // ring stages filled and consumed so far
 
@@ -554,10 +554,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         // ---- finish the unit or leave its partial sums
         const bool whole = first == 0 && last == unit_tiles;
         const int slot = 2 * self + (at == begin ? 0 : 1);
-        if (!whole && first == 0) {          // this run holds the unit's first tile: it leads the sum
-            const int64_t unit_begin = at, unit_end = at + unit_tiles;
-            const int parts = static_cast<int>((unit_end - 1) / per - unit_begin / per + 1);
-            info = make_int4(parts, slot, b, h * p.row_tiles + rt);
+        if (first == 0 && lane == 0) {       // this run holds the unit's first tile: it tells how the unit is made up
+            const int parts = whole ? 0 : static_cast<int>((at + unit_tiles - 1) / per - at / per + 1);
+            p.info[(static_cast<int64_t>(b) * p.Hkv + h) * p.row_tiles + rt] = make_int4(parts, slot, self, 0);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -593,15 +592,16 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         }
         at += last - first;
     }
-    if (lane == 0) p.info[self] = info;
     // abort: the copies in flight land before the block ends
     if (!ok)
         for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
 }
 
-// One block per unit: its eight warps share the unit's tiles out among them and
-// join their sums through shared memory. For short sequences, and no more units
-// than SMs: one launch, and no pass over lengths before the first load.
+// One cluster of blocks per unit: its warps share the unit's tiles out among
+// them, a block joins its eight warps' sums in shared memory and the blocks
+// then join theirs through distributed shared memory, each for its share of the
+// rows. For sequences that are short, or few: one launch, no pass over lengths
+// before the first load, no sums through memory.
 constexpr int kBlockWarps = 8;
 
 template <int kD>
@@ -613,17 +613,33 @@ struct BlockGeometry {
     // that eight threads' 16-byte stores meet no bank twice
     static constexpr int kOwn = kD / 4;
     static constexpr int kPitch = kOwn + 4;                           // floats
-    static_assert(kRows * 4 * kPitch * 4 <= G::kWarpBytes && kSmemBytes <= 232448, "shared memory");
+    static constexpr int kSumBytes = kRows * 4 * kPitch * 4;
+    // the block's joined sums: [row][D] after the first warp's
+    static constexpr int kOffJoined = (kSumBytes + 15) / 16 * 16;
+    static_assert(kOffJoined + kRows * kD * 4 <= G::kWarpBytes && kSmemBytes <= 232448, "shared memory");
 };
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 
 template <int kD, typename T>
 __global__ void __launch_bounds__(32 * kBlockWarps, 1)
 kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                        const DecodeParams p) {
+                        const DecodeParams p, const int blocks) {
     using G = DecodeGeometry<kD>;
     using B = BlockGeometry<kD>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ float warp_ml[kBlockWarps][kRows][2];
+    __shared__ float block_ml[kRows][2];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* const smem = smem_raw + (base - raw);
@@ -641,15 +657,18 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
     }
     __syncwarp();
     griddep_wait();                          // launched early behind the kernel that may have written the cache or q
-    int unit = static_cast<int>(blockIdx.x);
+    const int rank = static_cast<int>(blockIdx.x) % blocks;        // the block's place in its cluster
+    int unit = static_cast<int>(blockIdx.x) / blocks;
     const int rt = unit % p.row_tiles;
     unit /= p.row_tiles;
     const int h = unit % p.Hkv, b = unit / p.Hkv;
     const Sequence seq = sequence(p, b);
     const int key_end = row_tile_end(p, seq, rt);
     const int tiles = (key_end + kTileKeys - 1) / kTileKeys;
-    const int each = (tiles + kBlockWarps - 1) / kBlockWarps;
-    const int first = min(tiles, static_cast<int>(warp) * each), last = min(tiles, first + each);
+    // tiles to warps, the blocks' first warps before the second ones, so that few tiles meet many SMs
+    const int shares = blocks * kBlockWarps, share = static_cast<int>(warp) * blocks + rank;
+    const int first = static_cast<int>(static_cast<int64_t>(share) * tiles / shares);
+    const int last = static_cast<int>(static_cast<int64_t>(share + 1) * tiles / shares);
     bool ok = true;
     {
         float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -672,7 +691,7 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
                 for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
             }
         }
-        if (c == 0) {
+        if (c == 0) {                        // (a warp without tiles has a maximum of -inf)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 warp_ml[warp][g + 8 * i][0] = ok ? m[i] : -INFINITY;
@@ -680,13 +699,12 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
             }
         }
     }
-    if (__syncthreads_or(!ok)) return;       // (nothing is stored after a wait that gave up)
+    ok = !__syncthreads_or(!ok);
     // 16 threads per row, kD / 16 columns each
     constexpr int kCols = kD / 16;
     const int r = static_cast<int>(threadIdx.x >> 4), col = static_cast<int>(threadIdx.x & 15u) * kCols;
     const int row = rt * kRows + r;
     const int t = row / p.group, head = h * p.group + row % p.group;
-    if (t >= p.T) return;
     float m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kBlockWarps; ++w) m = fmaxf(m, warp_ml[w][r][0]);
@@ -695,14 +713,67 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
     for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBlockWarps; ++w) {
-        if (w * each >= tiles) break;        // (that warp had no tile, nor has any after it)
-        const float mw = warp_ml[w][r][0];
-        const float weight = mw == -INFINITY ? 0.0f : ex2_approx(mw - m);
-        l += warp_ml[w][r][1] * weight;
-        const float* const part = reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + (r * 4 + col / B::kOwn) * B::kPitch + col % B::kOwn;
+        const float mw = warp_ml[w][r][0], lw = warp_ml[w][r][1];
+        if (mw > -INFINITY || lw != 0.0f) {  // (a row that a warp's tokens are all hidden from has left zeros)
+            const float weight = ex2_approx(mw - m);
+            l += lw * weight;
+            const float* const part =
+                reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + (r * 4 + col / B::kOwn) * B::kPitch + col % B::kOwn;
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] += part[k] * weight;
+            for (int k = 0; k < kCols; ++k) acc[k] += part[k] * weight;
+        }
     }
+    bool mine = true;                        // does this block store this row
+    if (blocks > 1) {
+        float* const joined = reinterpret_cast<float*>(smem + B::kOffJoined);
+#pragma unroll
+        for (int k = 0; k < kCols / 4; ++k)
+            reinterpret_cast<float4*>(joined + r * kD + col)[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+        if (col == 0) {
+            block_ml[r][0] = ok ? m : -INFINITY;
+            block_ml[r][1] = ok ? l : 0.0f;
+        }
+        cluster_sync();
+        mine = r % blocks == rank;
+        if (mine) {
+            const uint32_t ml_at = smem_addr(&block_ml[r][0]);
+            const uint32_t at = base + B::kOffJoined + static_cast<uint32_t>(r * kD + col) * 4u;
+            float ms[8], ls[8];
+            float4 x[8][kCols / 4];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q < blocks) {
+                    ms[q] = ld_cluster_f32(map_to_cta(ml_at, q));
+                    ls[q] = ld_cluster_f32(map_to_cta(ml_at + 4, q));
+#pragma unroll
+                    for (int k = 0; k < kCols / 4; ++k) x[q][k] = ld_cluster_v4(map_to_cta(at + 16 * k, q));
+                }
+            }
+            m = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < blocks) m = fmaxf(m, ms[q]);
+            l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q < blocks && (ms[q] > -INFINITY || ls[q] != 0.0f)) {
+                    const float weight = ex2_approx(ms[q] - m);
+                    l += ls[q] * weight;
+#pragma unroll
+                    for (int k = 0; k < kCols / 4; ++k) {
+                        acc[4 * k] += x[q][k].x * weight;
+                        acc[4 * k + 1] += x[q][k].y * weight;
+                        acc[4 * k + 2] += x[q][k].z * weight;
+                        acc[4 * k + 3] += x[q][k].w * weight;
+                    }
+                }
+            }
+        }
+        cluster_sync();                      // no block leaves while another reads its sums
+    }
+    if (!ok || !mine || t >= p.T) return;    // (nothing is stored by a block whose wait gave up)
     const bool any = l > 0.0f || l != l;
     const float mul = any ? 1.0f / l : 0.0f;
     T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + col;
@@ -721,85 +792,97 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
         p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Adds up the partial sums of the units that several warps' runs share. Block
-// (x: the warp whose run such a unit begins in, y: which rows); the parts of a
-// row are shared out over `kSplit` of its warps and joined through shared
-// memory in order.
-template <int kD, typename T>
+// Adds up the partial sums of the units that several warps' runs share: grid
+// (unit, rows), kSplit warps to a row, of which each takes every kSplit-th part:
+// the row's maximum over the parts first, then the weighted sums, joined through
+// shared memory in order. Eight warps to a row where there are few units (of
+// many parts each), one where there are many (of few).
+template <int kD, typename T, int kSplit>
 __global__ void __launch_bounds__(256)
-kv8_combine_kernel(const DecodeParams p, const int warps_per_row) {
+kv8_combine_kernel(const DecodeParams p) {
     constexpr int kVec = kD / 32;            // floats of a lane
-    __shared__ float joined[8][kD + 2];
+    constexpr int kBatch = kSplit > 1 ? 8 : 4;   // parts whose loads are in flight at a time
+    __shared__ float joined[8][kD + 1];
+    griddep_launch_dependents();
     griddep_wait();
     const int4 info = __ldcg(p.info + blockIdx.x);   // (past L1: this grid may have started before the writes)
     const int parts = info.x;
     if (parts == 0) return;
     const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
-    const int rows_per_block = 8 / warps_per_row;
-    const int b = info.z, h = info.w / p.row_tiles, rt = info.w % p.row_tiles;
-    for (int r0 = static_cast<int>(blockIdx.y) * rows_per_block; r0 < kRows; r0 += static_cast<int>(gridDim.y) * rows_per_block) {
-        const int r = r0 + warp / warps_per_row;
-        const int share = warp % warps_per_row;
-        const int row = rt * kRows + r;
-        const int t = row / p.group, head = h * p.group + row % p.group;
-        const bool live = t < p.T;
-        float m = -INFINITY, l = 0.0f, acc[kVec];
+    int unit = static_cast<int>(blockIdx.x);
+    const int rt = unit % p.row_tiles;
+    unit /= p.row_tiles;
+    const int h = unit % p.Hkv, b = unit / p.Hkv;
+    const int r = static_cast<int>(blockIdx.y) * (8 / kSplit) + warp / kSplit, row = rt * kRows + r;
+    const int share = warp % kSplit;
+    const int t = row / p.group, head = h * p.group + row % p.group;
+    const bool live = t < p.T;
+    // part i of the unit: the leader's slot, then the first slot of each warp that follows
+    auto row_of = [&](int i) {
+        const int64_t slot = i == 0 ? info.y : 2 * (static_cast<int64_t>(info.z) + i);
+        return slot * kRows + r;
+    };
+    float m = -INFINITY, l = 0.0f, acc[kVec];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) acc[k] = 0.0f;
-        if (live) {
-            // part i of the unit: the leader's slot, then the first slot of each warp that follows
-            auto row_of = [&](int i) {
-                const int64_t slot = i == 0 ? info.y : 2 * (static_cast<int64_t>(blockIdx.x) + i);
-                return slot * kRows + r;
-            };
-#pragma unroll 4
-            for (int i = share; i < parts; i += warps_per_row) {
-                const int64_t a = row_of(i);
-                const float pm = __ldcg(p.part_ml + 2 * a), pl = __ldcg(p.part_ml + 2 * a + 1);
-                float x[kVec];
-                if constexpr (kVec == 4) {
-                    const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * kD) + lane);
-                    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-                } else {
-                    const float2 f = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * kD) + lane);
-                    x[0] = f.x; x[1] = f.y;
+    for (int k = 0; k < kVec; ++k) acc[k] = 0.0f;
+    if (live) {
+        // (every warp of a row looks at all its maxima)
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.part_ml + 2 * row_of(i)));
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int i0 = share; i0 < parts; i0 += kSplit * kBatch) {
+            float pm[kBatch], pl[kBatch], x[kBatch][kVec];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int i = i0 + kSplit * q;
+                pm[q] = -INFINITY;
+                pl[q] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) x[q][k] = 0.0f;
+                if (i < parts) {
+                    const int64_t a = row_of(i);
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
+                    pm[q] = ml.x;
+                    pl[q] = ml.y;
+                    if constexpr (kVec == 4) {
+                        const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * kD) + lane);
+                        x[q][0] = f.x; x[q][1] = f.y; x[q][2] = f.z; x[q][3] = f.w;
+                    } else {
+                        const float2 f = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * kD) + lane);
+                        x[q][0] = f.x; x[q][1] = f.y;
+                    }
                 }
-                const float now = fmaxf(m, pm);
-                const float ws = now == -INFINITY ? 0.0f : ex2_approx(m - now), wp = now == -INFINITY ? 0.0f : ex2_approx(pm - now);
-                m = now;
-                l = l * ws + pl * wp;
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) acc[k] = acc[k] * ws + x[k] * wp;
             }
-        }
-        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) joined[warp][lane * kVec + k] = acc[k];
-        if (lane == 0) {
-            joined[warp][kD] = m;
-            joined[warp][kD + 1] = l;
-        }
-        __syncthreads();
-        if (share == 0 && live) {
-            for (int w = 1; w < warps_per_row; ++w) {
-                const float pm = joined[warp + w][kD], pl = joined[warp + w][kD + 1];
-                const float now = fmaxf(m, pm);
-                const float ws = now == -INFINITY ? 0.0f : ex2_approx(m - now), wp = now == -INFINITY ? 0.0f : ex2_approx(pm - now);
-                m = now;
-                l = l * ws + pl * wp;
+            for (int q = 0; q < kBatch; ++q) {
+                const float weight = pm[q] == -INFINITY ? 0.0f : ex2_approx(pm[q] - m);
+                l += pl[q] * (pm[q] == -INFINITY ? 1.0f : weight);      // (a NaN sum stays one)
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) acc[k] = acc[k] * ws + joined[warp + w][lane * kVec + k] * wp;
+                for (int k = 0; k < kVec; ++k) acc[k] += x[q][k] * weight;
             }
-            const bool any = l > 0.0f || l != l;
-            const float mul = any ? 1.0f / l : 0.0f;
-            T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + lane * kVec;
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) dst[k] = from_float<T>(acc[k] * mul);
-            if (p.lse != nullptr && lane == 0)
-                p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] =
-                    any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
     }
+    if constexpr (kSplit > 1) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) joined[warp][lane * kVec + k] = acc[k];
+        if (lane == 0) joined[warp][kD] = l;
+        __syncthreads();
+        if (share != 0) return;
+#pragma unroll
+        for (int w = 1; w < kSplit; ++w) {
+            l += joined[warp + w][kD];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) acc[k] += joined[warp + w][lane * kVec + k];
+        }
+    }
+    if (!live) return;
+    const bool any = l > 0.0f || l != l;
+    const float mul = any ? 1.0f / l : 0.0f;
+    T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + lane * kVec;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) dst[k] = from_float<T>(acc[k] * mul);
+    if (p.lse != nullptr && lane == 0)
+        p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace kv8
