@@ -7,7 +7,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -117,12 +116,22 @@ hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, 
 
 std::mutex g_setup_mutex;
 bool g_setup[kMaxDevices] = {};
+int g_cluster_blocks[kMaxDevices][4] = {};     // blocks of clusters of 1, 2, 4 and 8 that run at a time
+
+template <int kD, typename T, int kWarps>
+cudaError_t setup_block() {
+    return cudaFuncSetAttribute(kv8_decode_block_kernel<kD, T, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                BlockGeometry<kD, kWarps>::kSmemBytes);
+}
 
 template <int kD, typename T>
 cudaError_t setup_decode() {
     cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeGeometry<kD>::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(kv8_decode_block_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, BlockGeometry<kD>::kSmemBytes);
+    if (e == cudaSuccess) e = setup_block<kD, T, 1>();
+    if (e == cudaSuccess) e = setup_block<kD, T, 2>();
+    if (e == cudaSuccess) e = setup_block<kD, T, 4>();
+    if (e == cudaSuccess) e = setup_block<kD, T, 8>();
+    return e;
 }
 
 template <int kD>
@@ -140,6 +149,23 @@ hk_status setup(int device) {
     if (e == cudaSuccess) e = setup_decode<128, __half>();
     if (e == cudaSuccess) e = setup_prefill<64>();
     if (e == cudaSuccess) e = setup_prefill<128>();
+    // (a cluster needs its SMs in one part of the GPU: fewer blocks run at a time than there are SMs)
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3(8 * kSms);
+        cfg.blockDim = dim3(32 * kBlockWarps);
+        cfg.dynamicSmemBytes = BlockGeometry<128, kBlockWarps>::kSmemBytes;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, kv8_decode_block_kernel<128, __nv_bfloat16, kBlockWarps>, &cfg);
+        g_cluster_blocks[device][i] = clusters << i;
+    }
     if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring the cache attention kernels", e);
     g_setup[device] = true;
     return HK_OK;
@@ -165,13 +191,29 @@ DecodeWorkspace decode_workspace(const hk_kv8_cache* c, int64_t B, int64_t T, in
     return w;
 }
 
-// Rows of a KV head (query tokens times heads) from which the tensor-core
-// kernel takes the work: below it the keys and values are read once or a few
-// times as codes, above it they are brought to bf16 first.
-constexpr int64_t kPrefillRows = 64;
+// Query heads of a KV head that share a 128-row tile of the tensor-core kernel, as a power of two: all, where
+// they divide it evenly.
+int pack_shift_of(int64_t group) {
+    int shift = 0;
+    while (shift < 7 && group % (int64_t(2) << shift) == 0) ++shift;
+    return shift;
+}
+
+// Do the rows go to the tensor-core kernel? Both forms' time grows with the cached tokens; per token, in
+// millionths of a microsecond, measured (D 64 and 128, 2000 to 16000 tokens): 35 for each unit of 16 rows and KV
+// head, whatever their number, against 13000 for each round of 256-row items over the SMs and 120 for bringing
+// one KV head's token to bf16. So 4 sequences x 8 heads x 8 queries run at 96 us by units and 236 us by items
+// (16000 tokens), 32 queries at 300 and 269 us.
+bool many_rows(int64_t B, int64_t T, int64_t Hq, int64_t heads) {
+    const int64_t group = Hq / heads;
+    const double units = static_cast<double>(B) * heads * ceil_div(T * group, kRows);
+    const int pack = pack_shift_of(group);
+    const double items = static_cast<double>(B) * (Hq >> pack) * ceil_div(T, (hk::attn::kTiles * hk::attn::kTileQ) >> pack);
+    return 35.0 * units > 13000.0 * std::ceil(items / kSms) + 120.0 * static_cast<double>(B) * heads;
+}
 
 // Tiles per warp up to which a unit is one block's (beyond, its tiles are spread over the whole GPU).
-constexpr int kBlockTiles = 16;
+constexpr int kBlockTiles = 32;
 
 // Sequences that are brought to bf16 at a time: as many as fit 512 MB, one at least.
 constexpr int64_t kWidenBytes = int64_t(512) << 20;
@@ -231,26 +273,41 @@ void launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensor
         <<<static_cast<unsigned>(std::min(p.n_items, sms)), G::kThreads, G::kSmemBytes, st>>>(tq, tk, tv, p);
 }
 
-// `cluster`: blocks per unit, or 0 for the kernel that spreads all tiles over the GPU.
+template <int kD, typename T, int kWarps>
+cudaError_t launch_block(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int cluster, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.row_tiles * cluster));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = BlockGeometry<kD, kWarps>::kSmemBytes;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, &kv8_decode_block_kernel<kD, T, kWarps>, tk, tv, p, cluster);
+}
+
+// How the few-row kernels share a call out: warps per unit in a block of its
+// own (times the blocks of a cluster), or 0: all tiles over all warps of the GPU.
+struct DecodePlan {
+    int warps, cluster, blocks;
+};
+
 template <int kD, typename T>
-cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int blocks, int cluster, cudaStream_t st) {
-    if (cluster > 0) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[2];
-        cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.Hkv * p.row_tiles * cluster));
-        cfg.blockDim = dim3(32 * kBlockWarps);
-        cfg.dynamicSmemBytes = BlockGeometry<kD>::kSmemBytes;
-        cfg.stream = st;
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, &kv8_decode_block_kernel<kD, T>, tk, tv, p, cluster);
+cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, const DecodePlan& plan, cudaStream_t st) {
+    switch (plan.warps) {
+        case 1: return launch_block<kD, T, 1>(tk, tv, p, 1, st);
+        case 2: return launch_block<kD, T, 2>(tk, tv, p, 1, st);
+        case 4: return launch_block<kD, T, 4>(tk, tv, p, 1, st);
+        case 8: return launch_block<kD, T, 8>(tk, tv, p, plan.cluster, st);
+        default: break;
     }
+    const int blocks = plan.blocks;
     cudaError_t e = launch_early(&kv8_decode_kernel<kD, T>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kDecodeWarps),
                                  DecodeGeometry<kD>::kSmemBytes, st, tk, tv, p);
     if (e != cudaSuccess) return e;
@@ -271,8 +328,7 @@ hk_status prefill(const void* Q, const int64_t q_strides[3], const hk_kv8_cache*
     const PrefillWorkspace ws = prefill_workspace(c, B, max_pages);
     char* const wide[2] = {static_cast<char*>(workspace), static_cast<char*>(workspace) + ws.half};
     const int64_t group = Hq / c->heads;
-    int pack_shift = 0;                            // all heads of a KV head share a tile, where they divide it evenly
-    while (pack_shift < 7 && group % (int64_t(2) << pack_shift) == 0) ++pack_shift;
+    const int pack_shift = pack_shift_of(group);
     hk_status s;
     for (int64_t b0 = 0; b0 < B; b0 += ws.seqs) {
         const int64_t n = std::min(ws.seqs, B - b0);
@@ -412,7 +468,7 @@ extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int
         T > kLimit / 16 / (Hq / cache->heads) || max_pages <= 0 || max_pages > kLimit / cache->page_size)
         return 0;
     const size_t split = decode_workspace(cache, B, T, Hq).total;
-    if (T <= kPrefillRows * cache->heads / Hq) return split;
+    if (!many_rows(B, T, Hq, cache->heads)) return split;
     return std::max(split, prefill_workspace(cache, B, max_pages).total);
 }
 
@@ -455,7 +511,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // (the tensor-core kernel takes bf16 rows that TMA can read: aligned, and not one row for several places)
     const bool spread = (B == 1 || q_strides[0] > 0) && (T == 1 || q_strides[1] > 0) && (Hq == 1 || q_strides[2] > 0);
-    if (T > kPrefillRows * cache->heads / Hq && type == HK_TYPE_BF16 && vec_q && vec_o && spread)
+    if (many_rows(B, T, Hq, cache->heads) && type == HK_TYPE_BF16 && vec_q && vec_o && spread)
         return prefill(Q, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse, B, T, Hq,
                        causal, scale_log2, workspace, status, timeout_ns, enc, sms, st);
     CUtensorMap tk, tv;
@@ -497,17 +553,15 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     const int64_t units = batch * p.Hkv * p.row_tiles;
     if (units > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
     const int64_t unit_room = ceil_div(max_pages * p.page_size, kTileKeys);
-    const int blocks = static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), ceil_div(units * unit_room, kDecodeWarps)));
-    // units that one round of blocks holds: a cluster of as many blocks as there is room for, while a warp's
-    // share of the table's tiles stays small
-    int cluster = 0;
-    if (units <= sms) {
-        cluster = 1;
-        while (cluster < 8 && 2 * cluster * units <= sms && 2 * cluster * kBlockWarps <= 2 * unit_room) cluster *= 2;
-        if (unit_room > cluster * kBlockWarps * kBlockTiles) cluster = 0;
-    }
-    if (const char* f = std::getenv("HK_TMP_CLUSTER")) cluster = std::atoi(f);
-    if (const char* f = std::getenv("HK_TMP_MIN")) p.min_tiles = std::atoi(f);
+    DecodePlan plan = {0, 1, static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), ceil_div(units * unit_room, kDecodeWarps)))};
+    // a block per unit, as wide as lets one round of blocks hold all units (a cluster of blocks where that
+    // leaves SMs idle), while a warp's share of the room for tiles stays small
+    int warps = kBlockWarps;
+    while (warps > 1 && units > int64_t(sms) * (kBlockWarps / warps)) warps /= 2;
+    if (warps == kBlockWarps)
+        for (int i = 1; i < 4 && (units << i) <= g_cluster_blocks[device][i] && (kBlockWarps << (i - 1)) <= unit_room; ++i)
+            plan.cluster = 1 << i;
+    if (unit_room <= int64_t(plan.cluster) * warps * kBlockTiles) plan.warps = warps;
     for (int64_t b0 = 0; b0 < B; b0 += batch) {       // (launches of one stream: they may share the workspace)
         p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, batch));
         p.q = static_cast<const uint16_t*>(Q) + b0 * p.q_stride_b;
@@ -520,11 +574,11 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
         cudaError_t e;
         const bool half = type == HK_TYPE_FP16;
         if (cache->head_dim == 64)
-            e = half ? launch_decode<64, __half>(tk, tv, p, blocks, cluster, st)
-                     : launch_decode<64, __nv_bfloat16>(tk, tv, p, blocks, cluster, st);
+            e = half ? launch_decode<64, __half>(tk, tv, p, plan, st)
+                     : launch_decode<64, __nv_bfloat16>(tk, tv, p, plan, st);
         else
-            e = half ? launch_decode<128, __half>(tk, tv, p, blocks, cluster, st)
-                     : launch_decode<128, __nv_bfloat16>(tk, tv, p, blocks, cluster, st);
+            e = half ? launch_decode<128, __half>(tk, tv, p, plan, st)
+                     : launch_decode<128, __nv_bfloat16>(tk, tv, p, plan, st);
         if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache attention", e);
     }
     return HK_OK;

@@ -597,18 +597,19 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
 }
 
-// One cluster of blocks per unit: its warps share the unit's tiles out among
-// them, a block joins its eight warps' sums in shared memory and the blocks
-// then join theirs through distributed shared memory, each for its share of the
-// rows. For sequences that are short, or few: one launch, no pass over lengths
-// before the first load, no sums through memory.
-constexpr int kBlockWarps = 8;
+// One block, or cluster of blocks, per unit: its kWarps warps (1 to 8, so that an
+// SM always holds 8) share the unit's tiles out among them, a block joins its
+// warps' sums in shared memory and the blocks of a cluster then join theirs
+// through distributed shared memory, each for its share of the rows. For
+// sequences that are short, or few: one launch, no pass over lengths before the
+// first load, no sums through memory.
+constexpr int kBlockWarps = 8;         // warps of an SM; of a block in a cluster
 
-template <int kD>
+template <int kD, int kWarps>
 struct BlockGeometry {
     using G = DecodeGeometry<kD>;
-    static constexpr int kOffBars = kBlockWarps * G::kWarpBytes;
-    static constexpr int kSmemBytes = kOffBars + kBlockWarps * G::kStages * 8 + 1024;
+    static constexpr int kOffBars = kWarps * G::kWarpBytes;
+    static constexpr int kSmemBytes = kOffBars + kWarps * G::kStages * 8 + 1024;
     // a warp's sums in its ring's place: the columns of a thread 16 bytes apart from the next thread's, so
     // that eight threads' 16-byte stores meet no bank twice
     static constexpr int kOwn = kD / 4;
@@ -616,7 +617,8 @@ struct BlockGeometry {
     static constexpr int kSumBytes = kRows * 4 * kPitch * 4;
     // the block's joined sums: [row][D] after the first warp's
     static constexpr int kOffJoined = (kSumBytes + 15) / 16 * 16;
-    static_assert(kOffJoined + kRows * kD * 4 <= G::kWarpBytes && kSmemBytes <= 232448, "shared memory");
+    static_assert(kOffJoined + kRows * kD * 4 <= G::kWarpBytes &&
+                      (kSmemBytes + 3 * 1024) * (kBlockWarps / kWarps) <= 228 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -631,14 +633,14 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
     return v;
 }
 
-template <int kD, typename T>
-__global__ void __launch_bounds__(32 * kBlockWarps, 1)
+template <int kD, typename T, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kBlockWarps / kWarps)
 kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         const DecodeParams p, const int blocks) {
     using G = DecodeGeometry<kD>;
-    using B = BlockGeometry<kD>;
+    using B = BlockGeometry<kD, kWarps>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ float warp_ml[kBlockWarps][kRows][2];
+    __shared__ float warp_ml[kWarps][kRows][2];
     __shared__ float block_ml[kRows][2];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -666,7 +668,7 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
     const int key_end = row_tile_end(p, seq, rt);
     const int tiles = (key_end + kTileKeys - 1) / kTileKeys;
     // tiles to warps, the blocks' first warps before the second ones, so that few tiles meet many SMs
-    const int shares = blocks * kBlockWarps, share = static_cast<int>(warp) * blocks + rank;
+    const int shares = blocks * kWarps, share = static_cast<int>(warp) * blocks + rank;
     const int first = static_cast<int>(static_cast<int64_t>(share) * tiles / shares);
     const int last = static_cast<int>(static_cast<int64_t>(share + 1) * tiles / shares);
     bool ok = true;
@@ -702,94 +704,99 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
     ok = !__syncthreads_or(!ok);
     // 16 threads per row, kD / 16 columns each
     constexpr int kCols = kD / 16;
-    const int r = static_cast<int>(threadIdx.x >> 4), col = static_cast<int>(threadIdx.x & 15u) * kCols;
-    const int row = rt * kRows + r;
-    const int t = row / p.group, head = h * p.group + row % p.group;
-    float m = -INFINITY;
+    const int col = static_cast<int>(threadIdx.x & 15u) * kCols;
+    // (two rows to a warp: one pass with eight warps, as in a cluster)
+#pragma unroll 1
+    for (int r = static_cast<int>(threadIdx.x >> 4); r < kRows; r += 2 * kWarps) {
+        const int row = rt * kRows + r;
+        const int t = row / p.group, head = h * p.group + row % p.group;
+        if (kWarps < kBlockWarps && t >= p.T) continue;
+        float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kBlockWarps; ++w) m = fmaxf(m, warp_ml[w][r][0]);
-    float l = 0.0f, acc[kCols];
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][r][0]);
+        float l = 0.0f, acc[kCols];
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+        for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kBlockWarps; ++w) {
-        const float mw = warp_ml[w][r][0], lw = warp_ml[w][r][1];
-        if (mw > -INFINITY || lw != 0.0f) {  // (a row that a warp's tokens are all hidden from has left zeros)
-            const float weight = ex2_approx(mw - m);
-            l += lw * weight;
-            const float* const part =
-                reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + (r * 4 + col / B::kOwn) * B::kPitch + col % B::kOwn;
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = warp_ml[w][r][0], lw = warp_ml[w][r][1];
+            if (mw > -INFINITY || lw != 0.0f) {  // (a row that a warp's tokens are all hidden from has left zeros)
+                const float weight = ex2_approx(mw - m);
+                l += lw * weight;
+                const float* const part =
+                    reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + (r * 4 + col / B::kOwn) * B::kPitch + col % B::kOwn;
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) acc[k] += part[k] * weight;
-        }
-    }
-    bool mine = true;                        // does this block store this row
-    if (blocks > 1) {
-        float* const joined = reinterpret_cast<float*>(smem + B::kOffJoined);
-#pragma unroll
-        for (int k = 0; k < kCols / 4; ++k)
-            reinterpret_cast<float4*>(joined + r * kD + col)[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
-        if (col == 0) {
-            block_ml[r][0] = ok ? m : -INFINITY;
-            block_ml[r][1] = ok ? l : 0.0f;
-        }
-        cluster_sync();
-        mine = r % blocks == rank;
-        if (mine) {
-            const uint32_t ml_at = smem_addr(&block_ml[r][0]);
-            const uint32_t at = base + B::kOffJoined + static_cast<uint32_t>(r * kD + col) * 4u;
-            float ms[8], ls[8];
-            float4 x[8][kCols / 4];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (q < blocks) {
-                    ms[q] = ld_cluster_f32(map_to_cta(ml_at, q));
-                    ls[q] = ld_cluster_f32(map_to_cta(ml_at + 4, q));
-#pragma unroll
-                    for (int k = 0; k < kCols / 4; ++k) x[q][k] = ld_cluster_v4(map_to_cta(at + 16 * k, q));
-                }
+                for (int k = 0; k < kCols; ++k) acc[k] += part[k] * weight;
             }
-            m = -INFINITY;
+        }
+        bool mine = true;                        // does this block store this row
+        if (kWarps == kBlockWarps && blocks > 1) {
+            float* const joined = reinterpret_cast<float*>(smem + B::kOffJoined);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < blocks) m = fmaxf(m, ms[q]);
-            l = 0.0f;
+            for (int k = 0; k < kCols / 4; ++k)
+                reinterpret_cast<float4*>(joined + r * kD + col)[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+            if (col == 0) {
+                block_ml[r][0] = ok ? m : -INFINITY;
+                block_ml[r][1] = ok ? l : 0.0f;
+            }
+            cluster_sync();
+            mine = r % blocks == rank;
+            if (mine) {
+                const uint32_t ml_at = smem_addr(&block_ml[r][0]);
+                const uint32_t at = base + B::kOffJoined + static_cast<uint32_t>(r * kD + col) * 4u;
+                float ms[8], ls[8];
+                float4 x[8][kCols / 4];
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+                for (int q = 0; q < 8; ++q) {
+                    if (q < blocks) {
+                        ms[q] = ld_cluster_f32(map_to_cta(ml_at, q));
+                        ls[q] = ld_cluster_f32(map_to_cta(ml_at + 4, q));
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (q < blocks && (ms[q] > -INFINITY || ls[q] != 0.0f)) {
-                    const float weight = ex2_approx(ms[q] - m);
-                    l += ls[q] * weight;
+                        for (int k = 0; k < kCols / 4; ++k) x[q][k] = ld_cluster_v4(map_to_cta(at + 16 * k, q));
+                    }
+                }
+                m = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < kCols / 4; ++k) {
-                        acc[4 * k] += x[q][k].x * weight;
-                        acc[4 * k + 1] += x[q][k].y * weight;
-                        acc[4 * k + 2] += x[q][k].z * weight;
-                        acc[4 * k + 3] += x[q][k].w * weight;
+                for (int q = 0; q < 8; ++q)
+                    if (q < blocks) m = fmaxf(m, ms[q]);
+                l = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (q < blocks && (ms[q] > -INFINITY || ls[q] != 0.0f)) {
+                        const float weight = ex2_approx(ms[q] - m);
+                        l += ls[q] * weight;
+#pragma unroll
+                        for (int k = 0; k < kCols / 4; ++k) {
+                            acc[4 * k] += x[q][k].x * weight;
+                            acc[4 * k + 1] += x[q][k].y * weight;
+                            acc[4 * k + 2] += x[q][k].z * weight;
+                            acc[4 * k + 3] += x[q][k].w * weight;
+                        }
                     }
                 }
             }
+            cluster_sync();                      // no block leaves while another reads its sums
         }
-        cluster_sync();                      // no block leaves while another reads its sums
+        if (!ok || !mine || t >= p.T) continue;  // (nothing is stored by a block whose wait gave up)
+        const bool any = l > 0.0f || l != l;
+        const float mul = any ? 1.0f / l : 0.0f;
+        T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + col;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] *= mul;
+        if (p.vec_o) {
+#pragma unroll
+            for (int k = 0; k < kCols / 4; ++k)
+                reinterpret_cast<uint2*>(dst)[k] =
+                    make_uint2(pack_out<T>(acc[4 * k], acc[4 * k + 1]), pack_out<T>(acc[4 * k + 2], acc[4 * k + 3]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) dst[k] = from_float<T>(acc[k]);
+        }
+        if (p.lse != nullptr && col == 0)
+            p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
-    if (!ok || !mine || t >= p.T) return;    // (nothing is stored by a block whose wait gave up)
-    const bool any = l > 0.0f || l != l;
-    const float mul = any ? 1.0f / l : 0.0f;
-    T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + col;
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] *= mul;
-    if (p.vec_o) {
-#pragma unroll
-        for (int k = 0; k < kCols / 4; ++k)
-            reinterpret_cast<uint2*>(dst)[k] =
-                make_uint2(pack_out<T>(acc[4 * k], acc[4 * k + 1]), pack_out<T>(acc[4 * k + 2], acc[4 * k + 3]));
-    } else {
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) dst[k] = from_float<T>(acc[k]);
-    }
-    if (p.lse != nullptr && col == 0)
-        p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Adds up the partial sums of the units that several warps' runs share: grid
@@ -827,34 +834,34 @@ kv8_combine_kernel(const DecodeParams p) {
     for (int k = 0; k < kVec; ++k) acc[k] = 0.0f;
     if (live) {
         // (every warp of a row looks at all its maxima)
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(p.part_ml + 2 * row_of(i)));
+        for (int i0 = 0; i0 < parts; i0 += 256) {
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = __ldcg(p.part_ml + 2 * row_of(min(i0 + 32 * q + lane, parts - 1)));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = fmaxf(m, x[q]);
+        }
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         for (int i0 = share; i0 < parts; i0 += kSplit * kBatch) {
             float pm[kBatch], pl[kBatch], x[kBatch][kVec];
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int i = i0 + kSplit * q;
-                pm[q] = -INFINITY;
-                pl[q] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) x[q][k] = 0.0f;
-                if (i < parts) {
-                    const int64_t a = row_of(i);
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
-                    pm[q] = ml.x;
-                    pl[q] = ml.y;
-                    if constexpr (kVec == 4) {
-                        const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * kD) + lane);
-                        x[q][0] = f.x; x[q][1] = f.y; x[q][2] = f.z; x[q][3] = f.w;
-                    } else {
-                        const float2 f = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * kD) + lane);
-                        x[q][0] = f.x; x[q][1] = f.y;
-                    }
+            for (int q = 0; q < kBatch; ++q) {       // (past the last part: loaded again and not counted)
+                const int64_t a = row_of(min(i0 + kSplit * q, parts - 1));
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
+                pm[q] = ml.x;
+                pl[q] = ml.y;
+                if constexpr (kVec == 4) {
+                    const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * kD) + lane);
+                    x[q][0] = f.x; x[q][1] = f.y; x[q][2] = f.z; x[q][3] = f.w;
+                } else {
+                    const float2 f = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * kD) + lane);
+                    x[q][0] = f.x; x[q][1] = f.y;
                 }
             }
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
+                if (i0 + kSplit * q >= parts) break;
                 const float weight = pm[q] == -INFINITY ? 0.0f : ex2_approx(pm[q] - m);
                 l += pl[q] * (pm[q] == -INFINITY ? 1.0f : weight);      // (a NaN sum stays one)
 #pragma unroll
