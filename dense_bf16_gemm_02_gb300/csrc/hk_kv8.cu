@@ -199,6 +199,16 @@ int pack_shift_of(int64_t group) {
     return shift;
 }
 
+// Tiles per warp up to which a unit is one block's (beyond, its tiles are spread over the whole GPU).
+constexpr int kBlockTiles = 32;
+
+// Warps of a block that has a unit to itself: as many as let one round of blocks hold all units.
+int block_warps(int64_t units) {
+    int warps = kBlockWarps;
+    while (warps > 1 && units > int64_t(kSms) * (kBlockWarps / warps)) warps /= 2;
+    return warps;
+}
+
 // Do the rows go to the tensor-core kernel? Both forms' time grows with the cached tokens; per token, in
 // millionths of a microsecond, measured (D 64 and 128, 2000 to 16000 tokens): 35 for each unit of 16 rows and KV
 // head, whatever their number, against 13000 for each round of 256-row items over the SMs and 120 for bringing
@@ -211,9 +221,6 @@ bool many_rows(int64_t B, int64_t T, int64_t Hq, int64_t heads) {
     const double items = static_cast<double>(B) * (Hq >> pack) * ceil_div(T, (hk::attn::kTiles * hk::attn::kTileQ) >> pack);
     return 35.0 * units > 13000.0 * std::ceil(items / kSms) + 120.0 * static_cast<double>(B) * heads;
 }
-
-// Tiles per warp up to which a unit is one block's (beyond, its tiles are spread over the whole GPU).
-constexpr int kBlockTiles = 32;
 
 // Sequences that are brought to bf16 at a time: as many as fit 512 MB, one at least.
 constexpr int64_t kWidenBytes = int64_t(512) << 20;
@@ -467,7 +474,11 @@ extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int
     if (!cache || cache->heads < 1 || cache->page_size < 1 || cache->head_dim < 1 || B <= 0 || T <= 0 || Hq < cache->heads ||
         T > kLimit / 16 / (Hq / cache->heads) || max_pages <= 0 || max_pages > kLimit / cache->page_size)
         return 0;
-    const size_t split = decode_workspace(cache, B, T, Hq).total;
+    size_t split = decode_workspace(cache, B, T, Hq).total;
+    // (blocks that have a unit to themselves need none)
+    const int64_t row_tiles = ceil_div(T * (Hq / cache->heads), kRows);
+    const int64_t units = decode_batch(B, cache->heads, row_tiles) * cache->heads * row_tiles;
+    if (ceil_div(max_pages * cache->page_size, kTileKeys) <= block_warps(units) * kBlockTiles) split = 0;
     if (!many_rows(B, T, Hq, cache->heads)) return split;
     return std::max(split, prefill_workspace(cache, B, max_pages).total);
 }
@@ -494,7 +505,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
         return fail(HK_ERR_INVALID_ARG, "problem too large");
     const DecodeWorkspace ws = decode_workspace(cache, B, T, Hq);
     const size_t need = hk_attention_kv8_workspace_size(cache, B, T, Hq, max_pages);
-    if (!workspace || workspace_bytes < need)
+    if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
     if (!aligned(workspace, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
     int device = 0, sms = 0;
@@ -554,14 +565,12 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if (units > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
     const int64_t unit_room = ceil_div(max_pages * p.page_size, kTileKeys);
     DecodePlan plan = {0, 1, static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), ceil_div(units * unit_room, kDecodeWarps)))};
-    // a block per unit, as wide as lets one round of blocks hold all units (a cluster of blocks where that
-    // leaves SMs idle), while a warp's share of the room for tiles stays small
-    int warps = kBlockWarps;
-    while (warps > 1 && units > int64_t(sms) * (kBlockWarps / warps)) warps /= 2;
-    if (warps == kBlockWarps)
+    const int warps = block_warps(units);
+    if (warps == kBlockWarps)       // a cluster of blocks where one block to a unit leaves SMs idle
         for (int i = 1; i < 4 && (units << i) <= g_cluster_blocks[device][i] && (kBlockWarps << (i - 1)) <= unit_room; ++i)
             plan.cluster = 1 << i;
     if (unit_room <= int64_t(plan.cluster) * warps * kBlockTiles) plan.warps = warps;
+
     for (int64_t b0 = 0; b0 < B; b0 += batch) {       // (launches of one stream: they may share the workspace)
         p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, batch));
         p.q = static_cast<const uint16_t*>(Q) + b0 * p.q_stride_b;

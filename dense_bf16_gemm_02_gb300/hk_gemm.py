@@ -173,7 +173,7 @@ def load() -> ctypes.CDLL:
         lib.hk_gemm_fp4.restype = I32
         lib.hk_gemm_fp4_ex.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, P, I32, I32, U32, U64, P]
         lib.hk_gemm_fp4_ex.restype = I32
-        CP, F = ctypes.POINTER(hk_kv8_cache), ctypes.c_float
+        CP, F = P, ctypes.c_float         # (a cache: byref(hk_kv8_cache) or its bytes)
         lib.hk_kv8_append.argtypes = [CP, P, P, I32, I64, I64, P, P, P, I64, I64, P, P, P]
         lib.hk_kv8_append.restype = I32
         lib.hk_attention_kv8.argtypes = [P, I32, P, CP, P, I64, I64, P, P, P, P, P, I64, I64, I64, I32, F, P, SZ, P]

@@ -16,7 +16,6 @@ quantisation).
 """
 from __future__ import annotations
 
-import ctypes
 import struct
 
 import torch
@@ -28,6 +27,7 @@ _FORMATS = {"mxfp4": _hk.HK_FP4_MXFP4, "nvfp4": _hk.HK_FP4_NVFP4}
 _BLOCK = {"mxfp4": 32, "nvfp4": 16}
 _TYPES = {torch.bfloat16: _hk.HK_TYPE_BF16, torch.float16: _hk.HK_TYPE_FP16, torch.float32: _hk.HK_TYPE_FP32}
 _strides = struct.Struct("3q").pack       # three element strides, as the C entry points take them
+_cache_struct = struct.Struct("PPPPq4i").pack      # hk_kv8_cache
 _u8, _bf16, _f32, _i32 = torch.uint8, torch.bfloat16, torch.float32, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -79,7 +79,8 @@ class Fp4Matrix:
     block scales in 128×4 tiles; ``global_scale``: a float32 CUDA tensor of one
     element (NVFP4 only) or None."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "format", "global_scale", "_ld")
+    __slots__ = ("_codes", "_scales", "_buffer", "_codes_ptr", "_scales_ptr", "_ld", "rows", "cols", "format",
+                 "global_scale")
 
     def __init__(self, codes, scales, rows, cols, format="mxfp4", global_scale=None):
         if format not in _FORMATS:
@@ -92,8 +93,31 @@ class Fp4Matrix:
         if not scales.is_contiguous() or scales.numel() < self.scales_size(rows, cols, format):
             raise ValueError("scales must be contiguous and hold hk_fp4_scales_size bytes")
         self._ld = _row_stride(codes, "codes")
-        self.codes, self.scales, self.rows, self.cols, self.format = codes, scales, rows, cols, format
+        self._buffer = None
+        self._codes, self._scales, self.rows, self.cols, self.format = codes, scales, rows, cols, format
+        self._codes_ptr, self._scales_ptr = codes.data_ptr(), scales.data_ptr()
         self.global_scale = None if global_scale is None else _checked_global_scale(global_scale, format)
+
+    # (quantize_fp4 allocates once for both arrays; what nobody looks at needs no views)
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buffer[self._scales_bytes:].view(self.rows, self._ld)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buffer[: self._scales_bytes]
+        return self._scales
+
+    @property
+    def _any(self):
+        return self._codes if self._buffer is None else self._buffer
+
+    @property
+    def _scales_bytes(self):
+        return self.scales_size(self.rows, self.cols, self.format)
 
     @staticmethod
     def scales_size(rows, cols, format):
@@ -108,7 +132,7 @@ class Fp4Matrix:
         """The block scales' bytes as [rows, ceil(cols / block)] (UE8M0 or E4M3)."""
         blk = _BLOCK[self.format]
         nb = -(-self.cols // 256) * (256 // blk)
-        s = self.scales.view(-1)[: self.scales_size(self.rows, self.cols, self.format)]
+        s = self.scales.view(-1)[: self._scales_bytes]
         s = s.view(-1, nb // 4, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(-1, nb)
         return s[: self.rows, : -(-self.cols // blk)]
 
@@ -131,15 +155,17 @@ def quantize_fp4(x, format="mxfp4", global_scale=None, out=None, stream=None) ->
     ldx = _row_stride(x, "x")
     if out is None:
         out = Fp4Matrix.__new__(Fp4Matrix)
-        out._ld = (cols + 31) // 32 * 16
-        out.codes = _empty((rows, out._ld), _u8, x, stream)
-        out.scales = _empty(Fp4Matrix.scales_size(rows, cols, format), _u8, x, stream)
+        out._ld = ld = (cols + 31) // 32 * 16
+        size = Fp4Matrix.scales_size(rows, cols, format)      # (a multiple of 1024: the codes behind it are aligned)
+        out._buffer = buffer = _empty(size + rows * ld, _u8, x, stream)
+        out._codes = out._scales = None
+        out._scales_ptr = ptr = buffer.data_ptr()
+        out._codes_ptr = ptr + size
         out.rows, out.cols, out.format = rows, cols, format
     elif out.rows != rows or out.cols != cols or out.format != format:
         raise ValueError("out must have x's shape and the asked format")
     out.global_scale = global_scale
-    st = _hk.load().hk_fp4_quantize(x.data_ptr(), code, rows, cols, ldx, out.codes.data_ptr(), out._ld,
-                                    out.scales.data_ptr(), fmt,
+    st = _hk.load().hk_fp4_quantize(x.data_ptr(), code, rows, cols, ldx, out._codes_ptr, out._ld, out._scales_ptr, fmt,
                                     None if global_scale is None else global_scale.data_ptr(), _stream(stream, x))
     if st != HK_OK:
         raise HKError(st, "hk_fp4_quantize")
@@ -149,11 +175,11 @@ def quantize_fp4(x, format="mxfp4", global_scale=None, out=None, stream=None) ->
 def dequantize_fp4(q: Fp4Matrix, dtype=None, out=None, stream=None):
     """The values of a quantised matrix (default bf16)."""
     if out is None:
-        out = _empty((q.rows, q.cols), dtype or _bf16, q.codes, stream)
+        out = _empty((q.rows, q.cols), dtype or _bf16, q._any, stream)
     elif tuple(out.shape) != q.shape or (dtype is not None and out.dtype != dtype) or not out.is_cuda:
         raise ValueError("out must be a CUDA tensor of the matrix's shape and the asked type")
     g = q.global_scale
-    st = _hk.load().hk_fp4_dequantize(q.codes.data_ptr(), q._ld, q.scales.data_ptr(), _FORMATS[q.format],
+    st = _hk.load().hk_fp4_dequantize(q._codes_ptr, q._ld, q._scales_ptr, _FORMATS[q.format],
                                       None if g is None else g.data_ptr(), q.rows, q.cols, out.data_ptr(),
                                       _type_code(out, "out"), _row_stride(out, "out"), _stream(stream, out))
     if st != HK_OK:
@@ -169,15 +195,14 @@ def gemm_fp4(a: Fp4Matrix, b: Fp4Matrix, out=None, stream=None):
         raise ValueError(f"a [{a.rows}, {a.cols}] {a.format} and b [{b.rows}, {b.cols}] {b.format} do not match")
     M, N = a.rows, b.rows
     if out is None:
-        out = _empty((M, N), _bf16, a.codes, stream)
+        out = _empty((M, N), _bf16, a._any, stream)
         ldc = N
     else:
         if tuple(out.shape) != (M, N) or out.dtype != _bf16 or not out.is_cuda:
             raise ValueError("out must be a bfloat16 CUDA tensor [a.rows, b.rows]")
         ldc = _row_stride(out, "out")
     ga, gb = a.global_scale, b.global_scale
-    st = _hk.load().hk_gemm_fp4(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
-                                out.data_ptr(), M, N, a.cols, a._ld, b._ld, ldc, _FORMATS[a.format],
+    st = _hk.load().hk_gemm_fp4(a._codes_ptr, a._scales_ptr, b._codes_ptr, b._scales_ptr, out.data_ptr(), M, N, a.cols, a._ld, b._ld, ldc, _FORMATS[a.format],
                                 None if ga is None else ga.data_ptr(), None if gb is None else gb.data_ptr(),
                                 _stream(stream, out))
     if st != HK_OK:
@@ -195,18 +220,17 @@ class Kv8Cache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "page_size", "head_dim", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale):
-        for t, name, dtype, dims in ((k, "k", _u8, 4), (v, "v", _u8, 4), (k_scale, "k_scale", _f32, 2),
-                                     (v_scale, "v_scale", _f32, 2)):
-            if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.dim() != dims:
-                raise TypeError(f"{name} must be a {dims}-D {dtype} CUDA tensor")
+        for t, dtype in ((k, _u8), (v, _u8), (k_scale, _f32), (v_scale, _f32)):
+            if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+                raise TypeError("k and v must be uint8, k_scale and v_scale float32 CUDA tensors")
             if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-        shape = k.shape
-        if v.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
-            raise ValueError("v must have k's shape, the scales [pages, heads]")
+                raise ValueError("a cache's tensors must be contiguous")
+        shape = tuple(k.shape)
+        if len(shape) != 4 or tuple(v.shape) != shape or tuple(k_scale.shape) != shape[:2] or tuple(v_scale.shape) != shape[:2]:
+            raise ValueError("k and v must be [pages, heads, page_size, head_dim], the scales [pages, heads]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.head_dim = shape
-        self._ref = ctypes.byref(_hk.hk_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape))
+        self._ref = _cache_struct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape, 0)
 
     @classmethod
     def empty(cls, pages, heads, head_dim, page_size=64, device="cuda"):
@@ -297,11 +321,11 @@ def attention_kv8(q, cache: Kv8Cache, block_table, lengths, counts=None, causal=
     lse = _empty((B, T, Hq), _f32, q, stream) if return_lse else None
     lib = _hk.load()
     size = lib.hk_attention_kv8_workspace_size(cache._ref, B, T, Hq, pages)
-    workspace = _empty(size, _u8, q, stream)
+    workspace = _empty(size, _u8, q, stream) if size else None
     st = lib.hk_attention_kv8(q.data_ptr(), code, qs, cache._ref, block_table.data_ptr(), ld, pages, lengths.data_ptr(),
                               None if counts is None else counts.data_ptr(), out.data_ptr(), os,
                               None if lse is None else lse.data_ptr(), B, T, Hq, 1 if causal else 0, scale,
-                              workspace.data_ptr(), size, _stream(stream, q))
+                              None if workspace is None else workspace.data_ptr(), size, _stream(stream, q))
     if st != HK_OK:
         raise HKError(st, "hk_attention_kv8")
     return (out, lse) if return_lse else out

@@ -507,7 +507,9 @@ hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strid
                               void* workspace, size_t workspace_bytes, uint32_t flags, uint64_t timeout_ns,
                               void* stream);
 
-/* Bytes of workspace hk_attention_kv8 needs (0 for an empty problem). */
+/* Bytes of workspace hk_attention_kv8 needs: 0 for an empty problem and for few
+ * query rows over short block tables; else 20 MB, or (many query rows) the bf16
+ * keys and values of as many sequences as fit 512 MB, of one at least. */
 size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq, int64_t max_pages);
 
 /* Static description of a status code. */

@@ -62,14 +62,20 @@ def test_attention_refusals(lib):
     for bad in BAD_CACHES:
         assert at(_cache(**bad)) == INV, bad
     assert at(type=2) == INV and at(Hq=7) == INV and at(B=-1) == INV and at(T=-1) == INV and at(Hq=-2) == INV
-    assert at(scale=float("nan")) == INV and at(scale=float("inf")) == INV and at(flags=1) == INV
+    assert at(scale=float("nan")) == INV and at(scale=float("inf")) == INV and at(scale=-1.0) == INV and at(flags=1) == INV
     assert at(Q=None) == INV and at(O=None) == INV and at(qs=None) == INV and at(os=None) == INV
     assert at(table=None) == INV and at(lengths=None) == INV and at(pages=0) == INV and at(stride=2) == INV
     assert at(T=1 << 30) == INV
     assert at(Q=P + 1) == MIS and at(O=P + 1) == MIS and at(lse=P + 2) == MIS and at(counts=P + 1) == MIS
     c = _cache()
-    need = h.hk_attention_kv8_workspace_size(c, 2, 1, 8, 4)
-    assert need > 0 and at(wsb=need - 1) == WS and at(ws=None) == WS and at(ws=P + 128) == WS
+    long = dict(pages=4000, stride=4000)
+    need = h.hk_attention_kv8_workspace_size(c, 2, 1, 8, 4000)
+    assert need > 0 and at(wsb=need - 1, **long) == WS and at(ws=None, **long) == WS and at(ws=P + 128, **long) == WS
+    assert h.hk_attention_kv8_workspace_size(c, 2, 1, 8, 4) == 0         # short: nothing is left in memory
+    wide = h.hk_attention_kv8_workspace_size(c, 2, 4000, 8, 1000)        # bf16 keys and values of two sequences
+    assert wide == 2 * 2 * 1000 * 64 * 2 * 64 * 2
+    assert h.hk_attention_kv8_workspace_size(c, 64, 4000, 8, 4000) <= 512 << 20
+    assert h.hk_attention_kv8_workspace_size(c, 64, 4000, 8, 100000) == 2 * 100000 * 64 * 2 * 64 * 2
     assert h.hk_attention_kv8_workspace_size(c, 0, 1, 8, 4) == 0
     assert lib.hk_attention_kv8(P, 0, S3, ctypes.byref(c), P, 4, 4, P, None, P, S3, None, 2, 1, 7, 1, 0.0, P, need, None) == INV
 
