@@ -21,11 +21,16 @@
 // scale_offset), with blocks padded (scale 0) to whole 256-column chunks and
 // rows to whole tiles.
 //
-// Both kernels are bound by memory: per value 2 (or 4) bytes are read and
-// 0.53 or 0.56 written. A warp takes 1024 columns of a row, four chunks of 256
-// whose loads (16 bytes per lane and chunk, contiguous over the warp) are all
+// What bounds both kernels is memory (per value 2 or 4 bytes are read and 0.53 or
+// 0.56 written, or the other way round) as long as their instructions stay under
+// some 60 per eight values: at 141 (a first form) issuing them took 79 us for
+// 16384 x 8192 bf16 values. A warp takes 1024 columns of a row, four chunks of 256
+// whose loads (eight values per lane and chunk, 16 bytes of a 16-bit type) are all
 // issued before the first is used; a block's maximum is a two- or one-step
-// butterfly over the 4 or 2 lanes that hold it.
+// butterfly over the 4 or 2 lanes that hold it; the scale bytes of the four chunks
+// are gathered into words together. Rows that are not 16-byte aligned, and a row's
+// last columns, go through shared memory, so that memory is still read and written
+// in consecutive elements.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -102,42 +107,105 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return kFmt == kNvfp4 ? e4m3_value(byte) : ue8m0_value(byte);
 }
 
+// The largest magnitude of three values; NaN if one of them is.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A chunk's elements lane, lane + 32, ... (0 past the row's end) as they are
+// read and written when a row cannot be taken 16 bytes at a time.
+template <typename T>
+struct Spread8 {
+    T e[8];
+};
+
+template <typename T>
+__device__ __forceinline__ Spread8<T> load_spread(const T* row, int64_t col, int64_t cols, uint32_t lane) {
+    Spread8<T> r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t c = col + lane + 32 * j;
+        r.e[j] = c < cols ? row[c] : from_float<T>(0.0f);
+    }
+    return r;
+}
+
 // ------------------------------------------------------------- quantise --
 
-// One chunk of a row: this lane's 8 values to codes, the block's scale, and
-// the scale words of the chunk (4 blocks each), which the first lane of each
-// word's lanes stores.
+// NVFP4: what the scale bytes of a matrix with global scale g mean to the
+// quantisation, 1 / (e4m3 · g), once per block of threads (two divisions per
+// block of values would cost more than everything else).
+__device__ __forceinline__ void fill_reciprocals(float (&table)[128], float g) {
+    for (int i = static_cast<int>(threadIdx.y * 32 + threadIdx.x); i < 128; i += 32 * kQuantWarps) {
+        const float d = __fmul_rn(e4m3_value(static_cast<uint32_t>(i)), g);
+        table[i] = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+    }
+    __syncthreads();
+}
+
+// Eight values of a block to codes; the block's scale byte. `six_g`, `per_six_g`:
+// 6·g and its reciprocal, both rounded to nearest.
 template <int kFmt>
-__device__ __forceinline__ void quantize_chunk(const float (&v)[8], float g, uint32_t lane, uint32_t& codes,
-                                               uint32_t& scale_word) {
-    uint32_t top = 0;   // the largest magnitude, as bits: NaN above infinity above numbers
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    if constexpr (kFmt == kMxfp4) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    uint32_t byte;
+__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], float six_g, float per_six_g, const float* reciprocals,
+                                              uint32_t& byte) {
+    float m = amax3(v[0], v[1], v[2]);
+    m = amax3(m, v[3], v[4]);
+    m = amax3(m, v[5], v[6]);
+    m = amax3(m, v[7], 0.0f);
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if constexpr (kFmt == kMxfp4) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t top = __float_as_uint(m);
     float mul;
     if constexpr (kFmt == kMxfp4) {
-        const uint32_t exp_field = top >> 23;
-        byte = exp_field > 2 ? exp_field - 2 : 0;
+        byte = max(top >> 23, 2u) - 2u;
         mul = __uint_as_float((254u - byte) << 23);        // 2^-(byte - 127), exact
     } else {
-        byte = e4m3_of(__fdiv_rn(__uint_as_float(top), __fmul_rn(6.0f, g)));
-        const float d = __fmul_rn(e4m3_value(byte), g);
-        mul = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+        // m / (6·g) to nearest by one correction of m · (1 / (6·g)) with its exact remainder (P. Markstein,
+        // IBM J. Res. Dev. 34, 1990); where that leaves fp32's range the quotient is 0 or above 448 either way
+        const float q0 = __fmul_rn(m, per_six_g);
+        const float q = __fmaf_rn(__fmaf_rn(-q0, six_g, m), per_six_g, q0);
+        byte = e4m3_of(isfinite(q) ? q : q0);
+        mul = reciprocals[byte & 0x7Fu];
     }
+    const uint64_t mul2 = f32x2(mul, mul);
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = v[i] * mul;
-    codes = pack_e2m1x8(y);
-    if (top >= 0x7F800000u) {
-        byte = kFmt == kMxfp4 ? 255u : 0x7Fu;
-        codes = 0;
+    for (int i = 0; i < 4; ++i) f32x2_split(fmul2(f32x2(v[2 * i], v[2 * i + 1]), mul2), y[2 * i], y[2 * i + 1]);
+    const uint32_t codes = pack_e2m1x8(y);
+    const bool finite = top < 0x7F800000u;
+    byte = finite ? byte : kFmt == kMxfp4 ? 255u : 0x7Fu;
+    return finite ? codes : 0u;
+}
+
+// The scale bytes of four consecutive chunks, byte[i] of chunk i in all lanes of
+// its block, to words of four blocks in the scale tiles: `at` is the address of
+// the first chunk's first word (tiles are 512 bytes apart). Lanes of one block
+// each take another chunk's byte, so that one exchange serves several chunks.
+template <int kFmt>
+__device__ __forceinline__ void store_scales(const uint32_t (&byte)[kSpanChunks], uint8_t* at, int chunks, uint32_t lane) {
+    constexpr uint32_t kLanes = block_cols(kFmt) / 8;      // lanes of a block: 4 or 2
+    constexpr int kWords = kChunkCols / block_cols(kFmt) / 4;   // words of a chunk: 2 or 4
+    const uint32_t sub = lane % kLanes;
+#pragma unroll
+    for (int i0 = 0; i0 < kSpanChunks; i0 += static_cast<int>(kLanes)) {
+        uint32_t b = byte[i0];
+#pragma unroll
+        for (uint32_t k = 1; k < kLanes; ++k) b = sub == k ? byte[i0 + k] : b;
+        uint32_t word = b << (8 * ((lane / kLanes) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, kLanes);
+        word |= __shfl_xor_sync(0xffffffffu, word, 2 * kLanes);
+        const int chunk = i0 + static_cast<int>(sub);
+        if (((lane / kLanes) & 3) == 0 && chunk < chunks)
+            *reinterpret_cast<uint32_t*>(at + (chunk * kWords + static_cast<int>(lane / (4 * kLanes))) * 512) = word;
     }
-    constexpr int kLanes = block_cols(kFmt) / 8;           // lanes of a block
-    scale_word = byte << (8 * ((lane / kLanes) & 3));
-    scale_word |= __shfl_xor_sync(0xffffffffu, scale_word, kLanes);
-    scale_word |= __shfl_xor_sync(0xffffffffu, scale_word, 2 * kLanes);
 }
 
 // Block (32, kQuantWarps): `warps_per_row` (a power of two) warps of the block
@@ -145,102 +213,166 @@ __device__ __forceinline__ void quantize_chunk(const float (&v)[8], float g, uin
 // scale tile included: their scales are 0).
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-quantize_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* __restrict__ codes,
-                int64_t ld_codes, uint8_t* __restrict__ scales, const float* __restrict__ global_scale,
-                int warps_per_row, int vec) {
+quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                const float* global_scale, int warps_per_row, int vec) {
+    __shared__ float staged[kQuantWarps][kChunkCols];
+    __shared__ float reciprocals[kFmt == kNvfp4 ? 128 : 1];
+    griddep_launch_dependents();
+    griddep_wait();                  // launched early behind the kernel that may have written x
     const uint32_t lane = threadIdx.x;
     const int rows_per_block = kQuantWarps / warps_per_row;
     const int w = static_cast<int>(threadIdx.y) & (warps_per_row - 1);
     const int sub = static_cast<int>(threadIdx.y) / warps_per_row;
-    const float g = kFmt == kNvfp4 && global_scale != nullptr ? *global_scale : 1.0f;
-    const int64_t nb = padded_blocks(cols, kFmt);
+    float six_g = 6.0f, per_six_g = 0.0f;
+    if constexpr (kFmt == kNvfp4) {
+        const float g = global_scale != nullptr ? *global_scale : 1.0f;
+        six_g = __fmul_rn(6.0f, g);
+        per_six_g = fminf(__fdiv_rn(1.0f, six_g), 3.4028235e38f);   // (finite: 0 times it is 0)
+        fill_reciprocals(reciprocals, g);
+    }
     const int64_t chunks = (cols + kChunkCols - 1) / kChunkCols;
+    const int64_t whole = vec ? cols / kChunkCols : 0;     // chunks that are read 16 bytes at a time
     const int64_t code_cols = (cols + 31) / 32 * 32;
+    constexpr int kScaleStep = kChunkCols / block_cols(kFmt) / 4 * 512;    // bytes of a chunk's scale tiles
     const int64_t rows_pad = (rows + 127) / 128 * 128;
-    constexpr int kLanesPerWord = 4 * block_cols(kFmt) / 8;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub; row < rows_pad;
          row += static_cast<int64_t>(gridDim.x) * rows_per_block) {
         const T* const src = x + row * ldx;
+        uint8_t* const dst = codes + row * ld_codes + lane * 4;
+        uint8_t* const scale_row = scales + (row >> 7) * chunks * kScaleStep + (row & 31) * 16 + ((row >> 5) & 3) * 4;
         for (int64_t c0 = (static_cast<int64_t>(blockIdx.y) * warps_per_row + w) * kSpanChunks; c0 < chunks;
              c0 += static_cast<int64_t>(gridDim.y) * warps_per_row * kSpanChunks) {
-            Raw8<T> raw[kSpanChunks];
-            if (row < rows) {
+            uint32_t byte[kSpanChunks];
+            const int n = static_cast<int>(min(chunks - c0, static_cast<int64_t>(kSpanChunks)));
+            if (row >= rows) {
 #pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i)
-                    raw[i] = load8<T>(src, (c0 + i) * kChunkCols + lane * 8, cols, vec != 0);
+                for (int i = 0; i < kSpanChunks; ++i) byte[i] = 0;
+            } else if (c0 + kSpanChunks <= whole) {
+                Raw8<T> raw[kSpanChunks];
+                const T* const at = src + c0 * kChunkCols + lane * 8;
+#pragma unroll
+                for (int i = 0; i < kSpanChunks; ++i) raw[i] = load8<T>(at + i * kChunkCols, 0, 8, true);
+                uint8_t* const out = dst + c0 * (kChunkCols / 2);
+#pragma unroll
+                for (int i = 0; i < kSpanChunks; ++i) {
+                    float v[8];
+                    widen8<T>(raw[i], v);
+                    *reinterpret_cast<uint32_t*>(out + i * (kChunkCols / 2)) = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
+                }
             } else {
-                memset(raw, 0, sizeof raw);
-            }
+                Spread8<T> raw[kSpanChunks];
 #pragma unroll
-            for (int i = 0; i < kSpanChunks; ++i) {
-                const int64_t chunk = c0 + i;
-                if (chunk >= chunks) break;
-                float v[8];
-                widen8<T>(raw[i], v);
-                uint32_t packed, word;
-                quantize_chunk<kFmt>(v, g, lane, packed, word);
-                const int64_t col = chunk * kChunkCols + lane * 8;
-                if (row < rows && col < code_cols)
-                    *reinterpret_cast<uint32_t*>(codes + row * ld_codes + col / 2) = packed;
-                if (lane % kLanesPerWord == 0)
-                    *reinterpret_cast<uint32_t*>(scales + scale_offset(row, col / block_cols(kFmt), nb)) = word;
+                for (int i = 0; i < kSpanChunks; ++i) raw[i] = load_spread<T>(src, (c0 + i) * kChunkCols, cols, lane);
+                float* const buf = staged[threadIdx.y];
+#pragma unroll
+                for (int i = 0; i < kSpanChunks; ++i) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) buf[lane + 32 * j] = to_float(raw[i].e[j]);
+                    __syncwarp();
+                    float v[8];
+                    memcpy(v, buf + lane * 8, sizeof v);
+                    const uint32_t packed = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
+                    if ((c0 + i) * kChunkCols + lane * 8 < code_cols)
+                        *reinterpret_cast<uint32_t*>(dst + (c0 + i) * (kChunkCols / 2)) = packed;
+                }
             }
+            store_scales<kFmt>(byte, scale_row + c0 * kScaleStep, n, lane);
         }
     }
 }
 
 // ----------------------------------------------------------- dequantise --
 
+// Eight codes times their scale, rounded once to T.
+template <typename T>
+__device__ __forceinline__ void dequantize8(uint32_t codes, float scale, T (&e)[8]) {
+    float v[8];
+    unpack_e2m1x8(codes, v);
+    const uint64_t s2 = f32x2(scale, scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f32x2_split(fmul2(f32x2(v[2 * i], v[2 * i + 1]), s2), a, b);
+        if constexpr (sizeof(T) == 4) {
+            e[2 * i] = a;
+            e[2 * i + 1] = b;
+        } else {
+            const uint32_t pair = pack_pair<T>(a, b);
+            memcpy(&e[2 * i], &pair, 4);
+        }
+    }
+}
+
 // y = code · (scale · g), rounded once to T.
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-dequantize_kernel(const uint8_t* __restrict__ codes, int64_t ld_codes, const uint8_t* __restrict__ scales,
-                  const float* __restrict__ global_scale, int64_t rows, int64_t cols, T* __restrict__ y, int64_t ldy,
-                  int warps_per_row, int vec) {
+dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, const float* global_scale, int64_t rows,
+                  int64_t cols, T* y, int64_t ldy, int warps_per_row, int vec) {
+    __shared__ T staged[kQuantWarps][kChunkCols];
+    griddep_launch_dependents();
+    griddep_wait();                  // launched early behind the kernel that may have written the codes
     const uint32_t lane = threadIdx.x;
     const int rows_per_block = kQuantWarps / warps_per_row;
     const int w = static_cast<int>(threadIdx.y) & (warps_per_row - 1);
     const int sub = static_cast<int>(threadIdx.y) / warps_per_row;
     const float g = kFmt == kNvfp4 && global_scale != nullptr ? *global_scale : 1.0f;
-    const int64_t nb = padded_blocks(cols, kFmt);
     const int64_t chunks = (cols + kChunkCols - 1) / kChunkCols;
+    const int64_t whole = vec ? cols / kChunkCols : 0;
+    const int64_t code_cols = (cols + 31) / 32 * 32;
+    constexpr int kLanes = block_cols(kFmt) / 8;
+    constexpr int kScaleStep = kChunkCols / block_cols(kFmt) / 4 * 512;
+    const int block = static_cast<int>(lane) / kLanes;     // of this lane's values in a chunk
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub; row < rows;
          row += static_cast<int64_t>(gridDim.x) * rows_per_block) {
-        const uint8_t* const src = codes + row * ld_codes;
+        const uint8_t* const src = codes + row * ld_codes + lane * 4;
+        const uint8_t* const scale_row = scales + (row >> 7) * chunks * kScaleStep + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
+                                         (block >> 2) * 512 + (block & 3);
         T* const dst = y + row * ldy;
         for (int64_t c0 = (static_cast<int64_t>(blockIdx.y) * warps_per_row + w) * kSpanChunks; c0 < chunks;
              c0 += static_cast<int64_t>(gridDim.y) * warps_per_row * kSpanChunks) {
             uint32_t packed[kSpanChunks], byte[kSpanChunks];
+            const uint8_t* const at = src + c0 * (kChunkCols / 2);
+            const uint8_t* const scale_at = scale_row + c0 * kScaleStep;
+            if (c0 + kSpanChunks <= whole) {
 #pragma unroll
-            for (int i = 0; i < kSpanChunks; ++i) {
-                const int64_t col = (c0 + i) * kChunkCols + lane * 8;
-                packed[i] = byte[i] = 0;
-                if (col < cols) {
-                    packed[i] = __ldg(reinterpret_cast<const uint32_t*>(src + col / 2));
-                    byte[i] = __ldg(scales + scale_offset(row, col / block_cols(kFmt), nb));
+                for (int i = 0; i < kSpanChunks; ++i) {
+                    packed[i] = *reinterpret_cast<const uint32_t*>(at + i * (kChunkCols / 2));
+                    byte[i] = scale_at[i * kScaleStep];
                 }
-            }
+                T* const out = dst + c0 * kChunkCols + lane * 8;
 #pragma unroll
-            for (int i = 0; i < kSpanChunks; ++i) {
-                const int64_t col = (c0 + i) * kChunkCols + lane * 8;
-                if (col >= cols) break;
-                float v[8];
-                unpack_e2m1x8(packed[i], v);
-                float s = scale_value<kFmt>(byte[i]);
-                if constexpr (kFmt == kNvfp4) s *= g;
-                T e[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) e[k] = from_float<T>(v[k] * s);
-                if (vec && col + 8 <= cols) {
-                    uint4* p = reinterpret_cast<uint4*>(dst + col);
+                for (int i = 0; i < kSpanChunks; ++i) {
+                    T e[8];
+                    dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
                     uint4 o[sizeof(T) / 2];
                     memcpy(o, e, sizeof o);
 #pragma unroll
-                    for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) p[k] = o[k];
-                } else {
+                    for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) reinterpret_cast<uint4*>(out + i * kChunkCols)[k] = o[k];
+                }
+            } else {
+                const int n = static_cast<int>(min(chunks - c0, static_cast<int64_t>(kSpanChunks)));
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (col + k < cols) dst[col + k] = e[k];
+                for (int i = 0; i < kSpanChunks; ++i) {
+                    packed[i] = byte[i] = 0;
+                    if (i < n && (c0 + i) * kChunkCols + lane * 8 < code_cols) {
+                        packed[i] = *reinterpret_cast<const uint32_t*>(at + i * (kChunkCols / 2));
+                        byte[i] = scale_at[i * kScaleStep];
+                    }
+                }
+                T* const buf = staged[threadIdx.y];
+#pragma unroll
+                for (int i = 0; i < kSpanChunks; ++i) {
+                    if (i >= n) break;
+                    T e[8];
+                    dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
+                    __syncwarp();
+                    memcpy(buf + lane * 8, e, sizeof e);
+                    __syncwarp();
+                    const int64_t col = (c0 + i) * kChunkCols + lane;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (col + 32 * j < cols) dst[col + 32 * j] = buf[lane + 32 * j];
                 }
             }
         }

@@ -36,6 +36,7 @@ hk_status cuda_fail(hk_status s, const char* what, cudaError_t e) {
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;   // 1 s per bounded wait
 constexpr int kMaxDevices = 64;
 constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
+constexpr int64_t kQuantBlocks = 152 * 16;               // blocks of a (de)quantisation, several rounds of what fits
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -78,30 +79,48 @@ int warps_per_row(int64_t cols) {
     return w;
 }
 
-template <typename T, int kFmt>
-void launch_quantize(const void* x, int64_t rows, int64_t cols, int64_t ldx, void* codes, int64_t ld, void* scales,
-                     const float* g, cudaStream_t st) {
-    const int wpr = warps_per_row(cols);
-    const int64_t blocks = ceil_div(ceil_div(rows, 128) * 128, kQuantWarps / wpr);
-    const int64_t spans = ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr);
-    const int vec = aligned(x, 16) && (ldx * sizeof(T)) % 16 == 0;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20)),
-                    static_cast<unsigned>(std::min<int64_t>(spans, 4096)));
-    quantize_kernel<T, kFmt><<<grid, dim3(32, kQuantWarps), 0, st>>>(
-        static_cast<const T*>(x), rows, cols, ldx, static_cast<uint8_t*>(codes), ld, static_cast<uint8_t*>(scales), g, wpr, vec);
+// Blocks along the rows: enough to fill the SMs several times over, each walking its rows (what a block of
+// threads sets up is then paid for once).
+unsigned row_blocks(int64_t rows, int wpr, int64_t span_blocks) {
+    return static_cast<unsigned>(std::min<int64_t>(ceil_div(rows, kQuantWarps / wpr), std::max<int64_t>(1, kQuantBlocks / span_blocks)));
+}
+
+// A launch that may begin while the kernel before it on the stream ends (the kernel waits for that end itself).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*fn)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
 template <typename T, int kFmt>
-void launch_dequantize(const void* codes, int64_t ld, const void* scales, const float* g, int64_t rows, int64_t cols,
-                       void* y, int64_t ldy, cudaStream_t st) {
+cudaError_t launch_quantize(const void* x, int64_t rows, int64_t cols, int64_t ldx, void* codes, int64_t ld, void* scales,
+                            const float* g, cudaStream_t st) {
     const int wpr = warps_per_row(cols);
-    const int64_t blocks = ceil_div(rows, kQuantWarps / wpr);
-    const int64_t spans = ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr);
+    const int64_t spans = std::min<int64_t>(ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr), 4096);
+    const int vec = aligned(x, 16) && (ldx * sizeof(T)) % 16 == 0;
+    return launch_early(&quantize_kernel<T, kFmt>, dim3(row_blocks(ceil_div(rows, 128) * 128, wpr, spans), static_cast<unsigned>(spans)),
+                        dim3(32, kQuantWarps), 0, st, static_cast<const T*>(x), rows, cols, ldx, static_cast<uint8_t*>(codes), ld,
+                        static_cast<uint8_t*>(scales), g, wpr, vec);
+}
+
+template <typename T, int kFmt>
+cudaError_t launch_dequantize(const void* codes, int64_t ld, const void* scales, const float* g, int64_t rows, int64_t cols,
+                              void* y, int64_t ldy, cudaStream_t st) {
+    const int wpr = warps_per_row(cols);
+    const int64_t spans = std::min<int64_t>(ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr), 4096);
     const int vec = aligned(y, 16) && (ldy * sizeof(T)) % 16 == 0;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, 1 << 20)),
-                    static_cast<unsigned>(std::min<int64_t>(spans, 4096)));
-    dequantize_kernel<T, kFmt><<<grid, dim3(32, kQuantWarps), 0, st>>>(
-        static_cast<const uint8_t*>(codes), ld, static_cast<const uint8_t*>(scales), g, rows, cols, static_cast<T*>(y), ldy, wpr, vec);
+    return launch_early(&dequantize_kernel<T, kFmt>, dim3(row_blocks(rows, wpr, spans), static_cast<unsigned>(spans)),
+                        dim3(32, kQuantWarps), 0, st, static_cast<const uint8_t*>(codes), ld, static_cast<const uint8_t*>(scales), g,
+                        rows, cols, static_cast<T*>(y), ldy, wpr, vec);
 }
 
 // ------------------------------------------------------------- the product --
@@ -271,13 +290,13 @@ extern "C" hk_status hk_fp4_quantize(const void* X, int32_t x_type, int64_t rows
     if ((s = current_device(&device, &sms)) != HK_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool nv = format == HK_FP4_NVFP4;
-    auto go = [&](auto mx_fn, auto nv_fn) { (nv ? nv_fn : mx_fn)(X, rows, cols, ldx, codes, ld_codes, scales, global_scale, st); };
+    auto go = [&](auto mx_fn, auto nv_fn) { return (nv ? nv_fn : mx_fn)(X, rows, cols, ldx, codes, ld_codes, scales, global_scale, st); };
+    cudaError_t e;
     switch (x_type) {
-        case HK_TYPE_BF16: go(&launch_quantize<__nv_bfloat16, kMxfp4>, &launch_quantize<__nv_bfloat16, kNvfp4>); break;
-        case HK_TYPE_FP16: go(&launch_quantize<__half, kMxfp4>, &launch_quantize<__half, kNvfp4>); break;
-        default: go(&launch_quantize<float, kMxfp4>, &launch_quantize<float, kNvfp4>); break;
+        case HK_TYPE_BF16: e = go(&launch_quantize<__nv_bfloat16, kMxfp4>, &launch_quantize<__nv_bfloat16, kNvfp4>); break;
+        case HK_TYPE_FP16: e = go(&launch_quantize<__half, kMxfp4>, &launch_quantize<__half, kNvfp4>); break;
+        default: e = go(&launch_quantize<float, kMxfp4>, &launch_quantize<float, kNvfp4>); break;
     }
-    cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the quantisation", e);
 }
 
@@ -297,13 +316,13 @@ extern "C" hk_status hk_fp4_dequantize(const void* codes, int64_t ld_codes, cons
     if ((s = current_device(&device, &sms)) != HK_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool nv = format == HK_FP4_NVFP4;
-    auto go = [&](auto mx_fn, auto nv_fn) { (nv ? nv_fn : mx_fn)(codes, ld_codes, scales, global_scale, rows, cols, Y, ldy, st); };
+    auto go = [&](auto mx_fn, auto nv_fn) { return (nv ? nv_fn : mx_fn)(codes, ld_codes, scales, global_scale, rows, cols, Y, ldy, st); };
+    cudaError_t e;
     switch (y_type) {
-        case HK_TYPE_BF16: go(&launch_dequantize<__nv_bfloat16, kMxfp4>, &launch_dequantize<__nv_bfloat16, kNvfp4>); break;
-        case HK_TYPE_FP16: go(&launch_dequantize<__half, kMxfp4>, &launch_dequantize<__half, kNvfp4>); break;
-        default: go(&launch_dequantize<float, kMxfp4>, &launch_dequantize<float, kNvfp4>); break;
+        case HK_TYPE_BF16: e = go(&launch_dequantize<__nv_bfloat16, kMxfp4>, &launch_dequantize<__nv_bfloat16, kNvfp4>); break;
+        case HK_TYPE_FP16: e = go(&launch_dequantize<__half, kMxfp4>, &launch_dequantize<__half, kNvfp4>); break;
+        default: e = go(&launch_dequantize<float, kMxfp4>, &launch_dequantize<float, kNvfp4>); break;
     }
-    cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the dequantisation", e);
 }
 

@@ -159,15 +159,6 @@ __device__ __forceinline__ uint32_t chunk_offset(uint32_t r, uint32_t c) {
     return kD == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack_out(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack_out<__nv_bfloat16>(float a, float b) {
-    return pack_bf16x2_rn(__float_as_uint(a), __float_as_uint(b));
-}
-template <>
-__device__ __forceinline__ uint32_t pack_out<__half>(float a, float b) { return pack_f16x2(a, b); }
-
 // kCols consecutive values of an output row, 16-byte stores where `vec`.
 template <typename T, int kCols>
 __device__ __forceinline__ void store_row(T* dst, const float (&v)[kCols], bool vec) {
@@ -175,8 +166,8 @@ __device__ __forceinline__ void store_row(T* dst, const float (&v)[kCols], bool 
 #pragma unroll
         for (int i = 0; i < kCols / 8; ++i)
             reinterpret_cast<uint4*>(dst)[i] =
-                make_uint4(pack_out<T>(v[8 * i], v[8 * i + 1]), pack_out<T>(v[8 * i + 2], v[8 * i + 3]),
-                           pack_out<T>(v[8 * i + 4], v[8 * i + 5]), pack_out<T>(v[8 * i + 6], v[8 * i + 7]));
+                make_uint4(pack_pair<T>(v[8 * i], v[8 * i + 1]), pack_pair<T>(v[8 * i + 2], v[8 * i + 3]),
+                           pack_pair<T>(v[8 * i + 4], v[8 * i + 5]), pack_pair<T>(v[8 * i + 6], v[8 * i + 7]));
     } else {
 #pragma unroll
         for (int i = 0; i < kCols; ++i) dst[i] = from_float<T>(v[i]);
@@ -789,7 +780,7 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
 #pragma unroll
             for (int k = 0; k < kCols / 4; ++k)
                 reinterpret_cast<uint2*>(dst)[k] =
-                    make_uint2(pack_out<T>(acc[4 * k], acc[4 * k + 1]), pack_out<T>(acc[4 * k + 2], acc[4 * k + 3]));
+                    make_uint2(pack_pair<T>(acc[4 * k], acc[4 * k + 1]), pack_pair<T>(acc[4 * k + 2], acc[4 * k + 3]));
         } else {
 #pragma unroll
             for (int k = 0; k < kCols; ++k) dst[k] = from_float<T>(acc[k]);
