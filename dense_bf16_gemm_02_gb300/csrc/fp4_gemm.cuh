@@ -191,7 +191,10 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     auto empty_bar = [&](int s) { return base + G::kOffBars + 8u * (G::kStages + s); };
     const uint32_t acc_bar = base + G::kOffBars + 8u * (2 * G::kStages);
 
+    griddep_launch_dependents();
     if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tmap_a);
+        prefetch_tensor_map(&tmap_b);
         for (int s = 0; s < G::kStages; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
@@ -211,6 +214,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
 
     if (warp == 0) {
         if (lane == 0) {
+            griddep_wait();              // launched early behind the kernel that may have written the operands
             const uint8_t* const sft = p.sfa + (static_cast<int64_t>(tm) * kTok / 128) * p.k_stages * G::kSfBytes;
             const uint8_t* const sfw = p.sfb + static_cast<int64_t>(tn) * p.k_stages * G::kSfBytes;
             int fills = 0, dropped = -1;
@@ -277,6 +281,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue --
+        griddep_wait();                  // before C is written or the global scales are read
         ok = __all_sync(0xffffffffu, wait_mbar(p.wait, acc_bar, 0, kErrWaitAcc) && !wait_aborted(p.wait));
         tc_fence_after_sync();
         const uint32_t q = warp & 3u;
@@ -499,6 +504,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         mbar_init(acc_free_bar, 8);            // four storing warps of each CTA
         fence_mbar_init_cluster();
     }
+    griddep_launch_dependents();
     if (warp == 0 && lane == 0) {
         prefetch_tensor_map(&tmap_a);
         prefetch_tensor_map(&tmap_b);
@@ -519,6 +525,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
     if (warp == 0) {
         // ------------------------------------------------------- loads --
         if (lane == 0) {
+            griddep_wait();              // launched early behind the kernel that may have written the operands
             int stage = 0;
             uint32_t phase = 0;
             int64_t fills = 0, dropped = -1;
@@ -635,6 +642,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         }
     } else {
         // ----------------------------------------------------- epilogue --
+        griddep_wait();                               // before C is written or the global scales are read
         const uint32_t q = warp & 3u;                 // TMEM lanes 32 q .. 32 q + 31
         const float alpha = global_alpha(p);
         const uint32_t buf_addr = base + G::kOffStore + (warp - 2) * G::kStoreBytes;

@@ -208,21 +208,28 @@ __device__ __forceinline__ void store_scales(const uint32_t (&byte)[kSpanChunks]
     }
 }
 
-// Block (32, kQuantWarps): `warps_per_row` (a power of two) warps of the block
-// share a row; row groups of the block walk the rows (padding rows of the last
-// scale tile included: their scales are 0).
+// What a warp works on: item i of rows × spans, a span being the 1024 columns
+// that it loads at once. (A 64-bit division would cost a quarter of the item.)
+struct Item {
+    int64_t row, chunk;        // the span's first chunk
+};
+
+__device__ __forceinline__ Item item_of(uint64_t i, uint64_t items, uint32_t spans) {
+    const uint64_t row = items <= 0xFFFFFFFFull ? static_cast<uint32_t>(i) / spans : i / spans;
+    return Item{static_cast<int64_t>(row), static_cast<int64_t>(i - row * spans) * kSpanChunks};
+}
+
+// Block (32, kQuantWarps), every warp on items of its own: spans of the rows,
+// padding rows of the last scale tile included (their scales are 0).
 template <typename T, int kFmt>
-__global__ void __launch_bounds__(32 * kQuantWarps)
+__global__ void __launch_bounds__(32 * kQuantWarps, 4)
 quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
-                const float* global_scale, int warps_per_row, int vec) {
+                const float* global_scale, uint32_t spans, int vec) {
     __shared__ float staged[kQuantWarps][kChunkCols];
     __shared__ float reciprocals[kFmt == kNvfp4 ? 128 : 1];
     griddep_launch_dependents();
     griddep_wait();                  // launched early behind the kernel that may have written x
     const uint32_t lane = threadIdx.x;
-    const int rows_per_block = kQuantWarps / warps_per_row;
-    const int w = static_cast<int>(threadIdx.y) & (warps_per_row - 1);
-    const int sub = static_cast<int>(threadIdx.y) / warps_per_row;
     float six_g = 6.0f, per_six_g = 0.0f;
     if constexpr (kFmt == kNvfp4) {
         const float g = global_scale != nullptr ? *global_scale : 1.0f;
@@ -234,51 +241,50 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
     const int64_t whole = vec ? cols / kChunkCols : 0;     // chunks that are read 16 bytes at a time
     const int64_t code_cols = (cols + 31) / 32 * 32;
     constexpr int kScaleStep = kChunkCols / block_cols(kFmt) / 4 * 512;    // bytes of a chunk's scale tiles
-    const int64_t rows_pad = (rows + 127) / 128 * 128;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub; row < rows_pad;
-         row += static_cast<int64_t>(gridDim.x) * rows_per_block) {
+    const uint64_t items = static_cast<uint64_t>((rows + 127) / 128 * 128) * spans;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kQuantWarps + threadIdx.y; i < items;
+         i += static_cast<uint64_t>(gridDim.x) * kQuantWarps) {
+        const Item item = item_of(i, items, spans);
+        const int64_t row = item.row, c0 = item.chunk;
         const T* const src = x + row * ldx;
         uint8_t* const dst = codes + row * ld_codes + lane * 4;
         uint8_t* const scale_row = scales + (row >> 7) * chunks * kScaleStep + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-        for (int64_t c0 = (static_cast<int64_t>(blockIdx.y) * warps_per_row + w) * kSpanChunks; c0 < chunks;
-             c0 += static_cast<int64_t>(gridDim.y) * warps_per_row * kSpanChunks) {
-            uint32_t byte[kSpanChunks];
-            const int n = static_cast<int>(min(chunks - c0, static_cast<int64_t>(kSpanChunks)));
-            if (row >= rows) {
+        uint32_t byte[kSpanChunks];
+        const int n = static_cast<int>(min(chunks - c0, static_cast<int64_t>(kSpanChunks)));
+        if (row >= rows) {
 #pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) byte[i] = 0;
-            } else if (c0 + kSpanChunks <= whole) {
-                Raw8<T> raw[kSpanChunks];
-                const T* const at = src + c0 * kChunkCols + lane * 8;
+            for (int i = 0; i < kSpanChunks; ++i) byte[i] = 0;
+        } else if (c0 + kSpanChunks <= whole) {
+            Raw8<T> raw[kSpanChunks];
+            const T* const at = src + c0 * kChunkCols + lane * 8;
 #pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) raw[i] = load8<T>(at + i * kChunkCols, 0, 8, true);
-                uint8_t* const out = dst + c0 * (kChunkCols / 2);
+            for (int i = 0; i < kSpanChunks; ++i) raw[i] = load8<T>(at + i * kChunkCols, 0, 8, true);
+            uint8_t* const out = dst + c0 * (kChunkCols / 2);
 #pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) {
-                    float v[8];
-                    widen8<T>(raw[i], v);
-                    *reinterpret_cast<uint32_t*>(out + i * (kChunkCols / 2)) = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
-                }
-            } else {
-                Spread8<T> raw[kSpanChunks];
-#pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) raw[i] = load_spread<T>(src, (c0 + i) * kChunkCols, cols, lane);
-                float* const buf = staged[threadIdx.y];
-#pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) {
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) buf[lane + 32 * j] = to_float(raw[i].e[j]);
-                    __syncwarp();
-                    float v[8];
-                    memcpy(v, buf + lane * 8, sizeof v);
-                    const uint32_t packed = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
-                    if ((c0 + i) * kChunkCols + lane * 8 < code_cols)
-                        *reinterpret_cast<uint32_t*>(dst + (c0 + i) * (kChunkCols / 2)) = packed;
-                }
+            for (int i = 0; i < kSpanChunks; ++i) {
+                float v[8];
+                widen8<T>(raw[i], v);
+                *reinterpret_cast<uint32_t*>(out + i * (kChunkCols / 2)) = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
             }
-            store_scales<kFmt>(byte, scale_row + c0 * kScaleStep, n, lane);
+        } else {
+            Spread8<T> raw[kSpanChunks];
+#pragma unroll
+            for (int i = 0; i < kSpanChunks; ++i) raw[i] = load_spread<T>(src, (c0 + i) * kChunkCols, cols, lane);
+            float* const buf = staged[threadIdx.y];
+#pragma unroll
+            for (int i = 0; i < kSpanChunks; ++i) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) buf[lane + 32 * j] = to_float(raw[i].e[j]);
+                __syncwarp();
+                float v[8];
+                memcpy(v, buf + lane * 8, sizeof v);
+                const uint32_t packed = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
+                if ((c0 + i) * kChunkCols + lane * 8 < code_cols)
+                    *reinterpret_cast<uint32_t*>(dst + (c0 + i) * (kChunkCols / 2)) = packed;
+            }
         }
+        store_scales<kFmt>(byte, scale_row + c0 * kScaleStep, n, lane);
     }
 }
 
@@ -306,16 +312,13 @@ __device__ __forceinline__ void dequantize8(uint32_t codes, float scale, T (&e)[
 
 // y = code · (scale · g), rounded once to T.
 template <typename T, int kFmt>
-__global__ void __launch_bounds__(32 * kQuantWarps)
+__global__ void __launch_bounds__(32 * kQuantWarps, 6)
 dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, const float* global_scale, int64_t rows,
-                  int64_t cols, T* y, int64_t ldy, int warps_per_row, int vec) {
+                  int64_t cols, T* y, int64_t ldy, uint32_t spans, int vec) {
     __shared__ T staged[kQuantWarps][kChunkCols];
     griddep_launch_dependents();
     griddep_wait();                  // launched early behind the kernel that may have written the codes
     const uint32_t lane = threadIdx.x;
-    const int rows_per_block = kQuantWarps / warps_per_row;
-    const int w = static_cast<int>(threadIdx.y) & (warps_per_row - 1);
-    const int sub = static_cast<int>(threadIdx.y) / warps_per_row;
     const float g = kFmt == kNvfp4 && global_scale != nullptr ? *global_scale : 1.0f;
     const int64_t chunks = (cols + kChunkCols - 1) / kChunkCols;
     const int64_t whole = vec ? cols / kChunkCols : 0;
@@ -323,57 +326,57 @@ dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
     constexpr int kLanes = block_cols(kFmt) / 8;
     constexpr int kScaleStep = kChunkCols / block_cols(kFmt) / 4 * 512;
     const int block = static_cast<int>(lane) / kLanes;     // of this lane's values in a chunk
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub; row < rows;
-         row += static_cast<int64_t>(gridDim.x) * rows_per_block) {
+    const uint64_t items = static_cast<uint64_t>(rows) * spans;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kQuantWarps + threadIdx.y; i < items;
+         i += static_cast<uint64_t>(gridDim.x) * kQuantWarps) {
+        const Item item = item_of(i, items, spans);
+        const int64_t row = item.row, c0 = item.chunk;
         const uint8_t* const src = codes + row * ld_codes + lane * 4;
         const uint8_t* const scale_row = scales + (row >> 7) * chunks * kScaleStep + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
                                          (block >> 2) * 512 + (block & 3);
         T* const dst = y + row * ldy;
-        for (int64_t c0 = (static_cast<int64_t>(blockIdx.y) * warps_per_row + w) * kSpanChunks; c0 < chunks;
-             c0 += static_cast<int64_t>(gridDim.y) * warps_per_row * kSpanChunks) {
-            uint32_t packed[kSpanChunks], byte[kSpanChunks];
-            const uint8_t* const at = src + c0 * (kChunkCols / 2);
-            const uint8_t* const scale_at = scale_row + c0 * kScaleStep;
-            if (c0 + kSpanChunks <= whole) {
+        uint32_t packed[kSpanChunks], byte[kSpanChunks];
+        const uint8_t* const at = src + c0 * (kChunkCols / 2);
+        const uint8_t* const scale_at = scale_row + c0 * kScaleStep;
+        if (c0 + kSpanChunks <= whole) {
 #pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) {
+            for (int i = 0; i < kSpanChunks; ++i) {
+                packed[i] = *reinterpret_cast<const uint32_t*>(at + i * (kChunkCols / 2));
+                byte[i] = scale_at[i * kScaleStep];
+            }
+            T* const out = dst + c0 * kChunkCols + lane * 8;
+#pragma unroll
+            for (int i = 0; i < kSpanChunks; ++i) {
+                T e[8];
+                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
+                uint4 o[sizeof(T) / 2];
+                memcpy(o, e, sizeof o);
+#pragma unroll
+                for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) reinterpret_cast<uint4*>(out + i * kChunkCols)[k] = o[k];
+            }
+        } else {
+            const int n = static_cast<int>(min(chunks - c0, static_cast<int64_t>(kSpanChunks)));
+#pragma unroll
+            for (int i = 0; i < kSpanChunks; ++i) {
+                packed[i] = byte[i] = 0;
+                if (i < n && (c0 + i) * kChunkCols + lane * 8 < code_cols) {
                     packed[i] = *reinterpret_cast<const uint32_t*>(at + i * (kChunkCols / 2));
                     byte[i] = scale_at[i * kScaleStep];
                 }
-                T* const out = dst + c0 * kChunkCols + lane * 8;
+            }
+            T* const buf = staged[threadIdx.y];
 #pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) {
-                    T e[8];
-                    dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
-                    uint4 o[sizeof(T) / 2];
-                    memcpy(o, e, sizeof o);
+            for (int i = 0; i < kSpanChunks; ++i) {
+                if (i >= n) break;
+                T e[8];
+                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
+                __syncwarp();
+                memcpy(buf + lane * 8, e, sizeof e);
+                __syncwarp();
+                const int64_t col = (c0 + i) * kChunkCols + lane;
 #pragma unroll
-                    for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) reinterpret_cast<uint4*>(out + i * kChunkCols)[k] = o[k];
-                }
-            } else {
-                const int n = static_cast<int>(min(chunks - c0, static_cast<int64_t>(kSpanChunks)));
-#pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) {
-                    packed[i] = byte[i] = 0;
-                    if (i < n && (c0 + i) * kChunkCols + lane * 8 < code_cols) {
-                        packed[i] = *reinterpret_cast<const uint32_t*>(at + i * (kChunkCols / 2));
-                        byte[i] = scale_at[i * kScaleStep];
-                    }
-                }
-                T* const buf = staged[threadIdx.y];
-#pragma unroll
-                for (int i = 0; i < kSpanChunks; ++i) {
-                    if (i >= n) break;
-                    T e[8];
-                    dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
-                    __syncwarp();
-                    memcpy(buf + lane * 8, e, sizeof e);
-                    __syncwarp();
-                    const int64_t col = (c0 + i) * kChunkCols + lane;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + 32 * j < cols) dst[col + 32 * j] = buf[lane + 32 * j];
-                }
+                for (int j = 0; j < 8; ++j)
+                    if (col + 32 * j < cols) dst[col + 32 * j] = buf[lane + 32 * j];
             }
         }
     }

@@ -70,19 +70,12 @@ hk_status current_device(int* device, int* sm_count) {
 
 // ------------------------------------------------ quantise and dequantise --
 
-// Warps of a block that share a row: a warp takes 1024 columns at a time, and
-// a narrow row leaves the block's other warps to other rows.
-int warps_per_row(int64_t cols) {
-    const int64_t spans = ceil_div(cols, kChunkCols * kSpanChunks);
-    int w = 1;
-    while (w < kQuantWarps && w < spans) w *= 2;
-    return w;
-}
+uint32_t spans_of(int64_t cols) { return static_cast<uint32_t>(ceil_div(cols, kChunkCols * kSpanChunks)); }
 
-// Blocks along the rows: enough to fill the SMs several times over, each walking its rows (what a block of
-// threads sets up is then paid for once).
-unsigned row_blocks(int64_t rows, int wpr, int64_t span_blocks) {
-    return static_cast<unsigned>(std::min<int64_t>(ceil_div(rows, kQuantWarps / wpr), std::max<int64_t>(1, kQuantBlocks / span_blocks)));
+// Blocks of a (de)quantisation: a warp to a span of a row, up to several rounds of what fits the SMs (what a
+// block of threads sets up is then paid for once).
+unsigned quant_blocks(int64_t rows, int64_t cols) {
+    return static_cast<unsigned>(std::min<int64_t>(ceil_div(rows * spans_of(cols), kQuantWarps), kQuantBlocks));
 }
 
 // A launch that may begin while the kernel before it on the stream ends (the kernel waits for that end itself).
@@ -104,23 +97,19 @@ cudaError_t launch_early(void (*fn)(Params...), dim3 grid, dim3 block, size_t sm
 template <typename T, int kFmt>
 cudaError_t launch_quantize(const void* x, int64_t rows, int64_t cols, int64_t ldx, void* codes, int64_t ld, void* scales,
                             const float* g, cudaStream_t st) {
-    const int wpr = warps_per_row(cols);
-    const int64_t spans = std::min<int64_t>(ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr), 4096);
     const int vec = aligned(x, 16) && (ldx * sizeof(T)) % 16 == 0;
-    return launch_early(&quantize_kernel<T, kFmt>, dim3(row_blocks(ceil_div(rows, 128) * 128, wpr, spans), static_cast<unsigned>(spans)),
-                        dim3(32, kQuantWarps), 0, st, static_cast<const T*>(x), rows, cols, ldx, static_cast<uint8_t*>(codes), ld,
-                        static_cast<uint8_t*>(scales), g, wpr, vec);
+    return launch_early(&quantize_kernel<T, kFmt>, dim3(quant_blocks(ceil_div(rows, 128) * 128, cols)), dim3(32, kQuantWarps), 0, st,
+                        static_cast<const T*>(x), rows, cols, ldx, static_cast<uint8_t*>(codes), ld, static_cast<uint8_t*>(scales), g,
+                        spans_of(cols), vec);
 }
 
 template <typename T, int kFmt>
 cudaError_t launch_dequantize(const void* codes, int64_t ld, const void* scales, const float* g, int64_t rows, int64_t cols,
                               void* y, int64_t ldy, cudaStream_t st) {
-    const int wpr = warps_per_row(cols);
-    const int64_t spans = std::min<int64_t>(ceil_div(cols, int64_t(kChunkCols) * kSpanChunks * wpr), 4096);
     const int vec = aligned(y, 16) && (ldy * sizeof(T)) % 16 == 0;
-    return launch_early(&dequantize_kernel<T, kFmt>, dim3(row_blocks(rows, wpr, spans), static_cast<unsigned>(spans)),
-                        dim3(32, kQuantWarps), 0, st, static_cast<const uint8_t*>(codes), ld, static_cast<const uint8_t*>(scales), g,
-                        rows, cols, static_cast<T*>(y), ldy, wpr, vec);
+    return launch_early(&dequantize_kernel<T, kFmt>, dim3(quant_blocks(rows, cols)), dim3(32, kQuantWarps), 0, st,
+                        static_cast<const uint8_t*>(codes), ld, static_cast<const uint8_t*>(scales), g, rows, cols,
+                        static_cast<T*>(y), ldy, spans_of(cols), vec);
 }
 
 // ------------------------------------------------------------- the product --
@@ -242,7 +231,7 @@ hk_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 enc, Fp4Params p, const 
     }
     const PairVariant& v = kPair[format == HK_FP4_NVFP4];
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, p.total_units)));
     cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
@@ -251,8 +240,10 @@ hk_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 enc, Fp4Params p, const 
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, v.fn, ta, tb, tbh, tsa, tsb, tc, p);
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the 4-bit product", e);
 }
@@ -393,7 +384,7 @@ extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* 
     if ((s = encode_codes(enc, &ta, A, M, K, lda, static_cast<uint32_t>(v->tok), "A")) != HK_OK) return s;
     if ((s = encode_codes(enc, &tb, B, N, K, ldb, 128, "B")) != HK_OK) return s;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
     cfg.blockDim = dim3(static_cast<unsigned>(v->threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(v->smem);
@@ -402,8 +393,10 @@ extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* 
     attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, v->fn, ta, tb, p, splits);
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the 4-bit product", e);
 }
