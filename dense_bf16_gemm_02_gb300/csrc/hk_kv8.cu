@@ -451,7 +451,7 @@ extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, con
     p.slots = static_cast<uint32_t>((T + p.page_size - 2) / p.page_size + 1);
     p.status = status;
     if (B > (int64_t(1) << 40) / p.slots / p.Hkv) return fail(HK_ERR_INVALID_ARG, "problem too large");
-    p.items = B * p.slots * p.Hkv * 2;
+    p.items = B * p.slots * p.Hkv;
     // one warp holds the new tokens of a page as long as they fit its registers (8 steps of 256 elements)
     const int64_t elements = std::min<int64_t>(T, p.page_size) * p.D;
     const bool one_warp = elements <= kAppendSteps * 256;

@@ -10,12 +10,13 @@
 // are rounded once more to the new scale (exact unless they fall below E4M3's
 // smallest normal number).
 //
-// One item is a (sequence, touched page, head) of keys or of values: one warp
-// when few tokens arrive per page, else eight warps. The new tokens of an item
+// One item is a (sequence, touched page, head), keys and values: one warp when
+// few tokens arrive per page, else eight warps. The new tokens of an item
 // stay in registers between the maximum and the rounding, so that they are read
 // once. A block does one item, so latency and the number of blocks on an SM
-// bound the kernel: the registers hold no more steps than a page needs, and the
-// tokens are asked for before the page's index is looked at.
+// bound the kernel: the registers hold no more steps than a page needs, keys and
+// values are in flight together, and both are asked for before the page's index
+// is looked at.
 #pragma once
 
 #include <cstdint>
@@ -35,7 +36,7 @@ struct AppendParams {
     int64_t table_stride;
     const int32_t* starts;         // tokens of each sequence before the append
     const int32_t* counts;         // new tokens of each sequence, or null (T)
-    int64_t items;                 // B * slots * Hkv * 2, below 2^32
+    int64_t items;                 // B * slots * Hkv, below 2^32
     int32_t B, T;
     uint32_t Hkv, slots;           // heads; pages a sequence can touch
     int32_t D, page_size, max_pages;
@@ -64,10 +65,58 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float ratio) {
     return out;
 }
 
+// The largest of the magnitude bits of eight elements, as they are held (16-bit
+// types two to a word), and what a word of them means as fp32 bits. Kept apart
+// from the conversion to fp32, so that no more than the elements themselves
+// lives in registers between the loads and the stores.
+template <typename T>
+struct Magnitude;
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+template <>
+struct Magnitude<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t of(const Raw8<__nv_bfloat16>& r, uint32_t m) {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
+        return m;
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return max(m & 0xFFFFu, m >> 16) << 16; }
+};
+
+template <>
+struct Magnitude<__half> {
+    static __device__ __forceinline__ uint32_t of(const Raw8<__half>& r, uint32_t m) {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
+        return m;
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) {
+        return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(max(m & 0xFFFFu, m >> 16)))));
+    }
+};
+
+template <>
+struct Magnitude<float> {
+    static __device__ __forceinline__ uint32_t of(const Raw8<float>& r, uint32_t m) {
+        const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+        return m;
+    }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
+};
+
 template <typename T, int kWarps, int kSteps>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2 * kSteps * sizeof(Raw8<T>) <= 128 ? 4 : 2)
 kv8_append_kernel(const AppendParams p) {
-    __shared__ uint32_t warp_top[8];
+    __shared__ uint32_t warp_top[2][8];
     griddep_launch_dependents();
     griddep_wait();                  // launched early behind the kernel that may have written the tokens
     const uint32_t lane = threadIdx.x & 31u;
@@ -75,8 +124,7 @@ kv8_append_kernel(const AppendParams p) {
     const uint32_t member = kWarps == 1 ? 0 : warp;          // this warp's place in its item
     const int64_t item = kWarps == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : static_cast<int64_t>(blockIdx.x);
     if (item >= p.items) return;
-    const int kv = static_cast<int>(item & 1);
-    uint32_t rest = static_cast<uint32_t>(item >> 1);
+    uint32_t rest = static_cast<uint32_t>(item);
     const int h = static_cast<int>(rest % p.Hkv);
     rest /= p.Hkv;
     const int b = static_cast<int>(rest / p.slots);
@@ -94,19 +142,33 @@ kv8_append_kernel(const AppendParams p) {
     const int64_t lo = max(static_cast<int64_t>(start), slot * p.page_size);              // new tokens of this page
     const int64_t hi = min(static_cast<int64_t>(start) + count, (slot + 1) * p.page_size);
     if (lo >= hi) return;
+    const int old_tokens = static_cast<int>(lo - slot * p.page_size);
+    const int n = static_cast<int>(hi - lo);
+
     const int lanes_per_token = p.D >> 3;
     const int per_step = kWarps * (32 / lanes_per_token);
     const int sub = static_cast<int>(member) * (32 / lanes_per_token) + static_cast<int>(lane) / lanes_per_token;
     const int d = static_cast<int>(lane) % lanes_per_token * 8;
-    const int n = static_cast<int>(hi - lo);
-    const T* const src = static_cast<const T*>(p.src[kv]) + b * p.stride_b[kv] + (lo - start) * p.stride_t[kv] +
-                         h * p.stride_h[kv];
-    Raw8<T> raw[kSteps];
+    Raw8<T> raw[2][kSteps];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int t = i * per_step + sub;
-        if (i * per_step < n)
-            raw[i] = load8<T>(src + t * p.stride_t[kv], d, t < n ? p.D : 0, p.vec[kv] != 0);
+    for (int kv = 0; kv < 2; ++kv) {
+        const T* const src = static_cast<const T*>(p.src[kv]) + b * p.stride_b[kv] + (lo - start) * p.stride_t[kv] +
+                             h * p.stride_h[kv];
+        // (one choice for all steps: with a choice at each load the next one waited for it)
+        if (p.vec[kv]) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int t = i * per_step + sub;
+                raw[kv][i] = Raw8<T>{};
+                if (t < n) raw[kv][i] = load8<T>(src + t * p.stride_t[kv] + d, 0, 8, true);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int t = i * per_step + sub;
+                raw[kv][i] = load8<T>(src + t * p.stride_t[kv], d, t < n ? p.D : 0, false);
+            }
+        }
     }
     const int64_t page = p.table[b * p.table_stride + slot];
     if (page < 0 || page >= p.num_pages) {
@@ -114,63 +176,79 @@ kv8_append_kernel(const AppendParams p) {
         return;
     }
     const int64_t ph = page * p.Hkv + h;
-    const int old_tokens = static_cast<int>(lo - slot * p.page_size);
-    const float had = old_tokens > 0 ? p.scale[kv][ph] : 0.0f;
-    uint32_t top = 0;       // largest finite magnitude, as bits
+    float had[2] = {0.0f, 0.0f};
+    if (old_tokens > 0) {
+        had[0] = p.scale[0][ph];
+        had[1] = p.scale[1][ph];
+    }
+    uint32_t top[2];                // largest finite magnitude, as bits
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        if (i * per_step < n) {
-            float v[8];
-            widen8<T>(raw[i], v);
+    for (int kv = 0; kv < 2; ++kv) {
+        uint32_t m = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t m = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-                top = max(top, m < 0x7F800000u ? m : 0u);
+        for (int i = 0; i < kSteps; ++i) m = Magnitude<T>::of(raw[kv][i], m);
+        top[kv] = __reduce_max_sync(0xffffffffu, Magnitude<T>::bits(m));
+        if (top[kv] >= 0x7F800000u) {           // an infinity or NaN among this warp's values: without them
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                float v[8];
+                widen8<T>(raw[kv][i], v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = max(m, isfinite(v[k]) ? __float_as_uint(v[k]) & 0x7FFFFFFFu : 0u);
             }
+            top[kv] = __reduce_max_sync(0xffffffffu, m);
         }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
     if constexpr (kWarps > 1) {
-        if (lane == 0) warp_top[warp] = top;
+        if (lane == 0) {
+            warp_top[0][warp] = top[0];
+            warp_top[1][warp] = top[1];
+        }
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = max(top, warp_top[w]);
-    }
-    const float need = __uint_as_float(scale_field(top) << 23);
-    const float scale = old_tokens > 0 ? fmaxf(need, had) : need;
-
-    uint8_t* const dst = p.codes[kv] + ph * p.page_size * p.D;
-    if (old_tokens > 0 && scale > had) {
-        const float ratio = had / scale;
-        uint4* const old = reinterpret_cast<uint4*>(dst);
-        for (int i = static_cast<int>(member * 32 + lane); i < old_tokens * p.D / 16; i += 32 * kWarps) {
-            uint4 w = old[i];
-            w.x = rescale_codes(w.x, ratio);
-            w.y = rescale_codes(w.y, ratio);
-            w.z = rescale_codes(w.z, ratio);
-            w.w = rescale_codes(w.w, ratio);
-            old[i] = w;
+        for (int w = 0; w < kWarps; ++w) {
+            top[0] = max(top[0], warp_top[0][w]);
+            top[1] = max(top[1], warp_top[1][w]);
         }
     }
-    const float inv = 1.0f / scale;      // exact: a power of two
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int t = i * per_step + sub;
-        if (t < n) {
-            float v[8];
-            widen8<T>(raw[i], v);
-            uint32_t w[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint16_t c0, c1;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c0) : "f"(v[4 * k + 1] * inv), "f"(v[4 * k] * inv));
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c1) : "f"(v[4 * k + 3] * inv), "f"(v[4 * k + 2] * inv));
-                w[k] = static_cast<uint32_t>(c0) | static_cast<uint32_t>(c1) << 16;
+    for (int kv = 0; kv < 2; ++kv) {
+        const float need = __uint_as_float(scale_field(top[kv]) << 23);
+        const float scale = old_tokens > 0 ? fmaxf(need, had[kv]) : need;
+        uint8_t* const dst = p.codes[kv] + ph * p.page_size * p.D;
+        if (old_tokens > 0 && scale > had[kv]) {
+            const float ratio = had[kv] / scale;
+            uint4* const old = reinterpret_cast<uint4*>(dst);
+            for (int i = static_cast<int>(member * 32 + lane); i < old_tokens * p.D / 16; i += 32 * kWarps) {
+                uint4 w = old[i];
+                w.x = rescale_codes(w.x, ratio);
+                w.y = rescale_codes(w.y, ratio);
+                w.z = rescale_codes(w.z, ratio);
+                w.w = rescale_codes(w.w, ratio);
+                old[i] = w;
             }
-            *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(old_tokens + t) * p.D + d) = make_uint2(w[0], w[1]);
         }
+        const float inv = 1.0f / scale;      // exact: a power of two
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int t = i * per_step + sub;
+            if (t < n) {
+                float v[8];
+                widen8<T>(raw[kv][i], v);
+                uint32_t w[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint16_t c0, c1;
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c0) : "f"(v[4 * k + 1] * inv), "f"(v[4 * k] * inv));
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c1) : "f"(v[4 * k + 3] * inv), "f"(v[4 * k + 2] * inv));
+                    w[k] = static_cast<uint32_t>(c0) | static_cast<uint32_t>(c1) << 16;
+                }
+                *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(old_tokens + t) * p.D + d) = make_uint2(w[0], w[1]);
+            }
+        }
+        if (member == 0 && lane == 0) p.scale[kv][ph] = scale;
     }
-    if (member == 0 && lane == 0) p.scale[kv][ph] = scale;
 }
 
 }  // namespace kv8
