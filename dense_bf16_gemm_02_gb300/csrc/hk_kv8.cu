@@ -43,13 +43,23 @@ constexpr int kSms = 152;                               // the device's SMs: the
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+constexpr int kMaxHeads = 65535;
+
+// (the sizes below stay within 64 bits for what passes; the tokens of a sequence, rounded up to a tile, within 31)
+bool cache_shape_ok(const hk_kv8_cache* c) {
+    return (c->head_dim == 64 || c->head_dim == 128) &&
+           (c->page_size == 16 || c->page_size == 32 || c->page_size == 64 || c->page_size == 128) && c->heads >= 1 &&
+           c->heads <= kMaxHeads && c->num_pages >= 1 && c->num_pages <= kLimit / c->heads;
+}
+bool table_width_ok(int64_t max_pages, int32_t page_size) { return max_pages >= 1 && max_pages <= (kLimit - 127) / page_size; }
+
 hk_status check_cache(const hk_kv8_cache* c) {
     if (!c) return fail(HK_ERR_INVALID_ARG, "null cache");
     if (c->head_dim != 64 && c->head_dim != 128)
         return fail(HK_ERR_INVALID_ARG, "head dimension %d (supported: 64, 128)", (int)c->head_dim);
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return fail(HK_ERR_INVALID_ARG, "page size %d (supported: 16, 32, 64, 128)", (int)c->page_size);
-    if (c->heads < 1 || c->num_pages < 1 || c->num_pages > kLimit / c->heads)
+    if (!cache_shape_ok(c))
         return fail(HK_ERR_INVALID_ARG, "%lld pages of %d heads", (long long)c->num_pages, (int)c->heads);
     if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return fail(HK_ERR_INVALID_ARG, "null cache pointer");
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
@@ -59,7 +69,7 @@ hk_status check_cache(const hk_kv8_cache* c) {
 
 hk_status check_table(const int32_t* table, int64_t stride, int64_t max_pages, int64_t B, const int32_t* lengths,
                       const int32_t* counts, int32_t page_size) {
-    if (max_pages < 1 || max_pages * page_size > kLimit)
+    if (!table_width_ok(max_pages, page_size))
         return fail(HK_ERR_INVALID_ARG, "a block table of %lld pages per sequence", (long long)max_pages);
     if (stride < max_pages && B > 1) return fail(HK_ERR_INVALID_ARG, "block table rows overlap");
     if (!table || !lengths) return fail(HK_ERR_INVALID_ARG, "null block table or lengths");
@@ -362,7 +372,7 @@ hk_status prefill(const void* Q, const int64_t q_strides[3], const hk_kv8_cache*
         const int64_t tokens_per_pair = (hk::attn::kTiles * hk::attn::kTileQ) >> pack_shift;
         const int64_t q_pairs = ceil_div(T, tokens_per_pair);
         const int64_t items = n * (Hq >> pack_shift) * q_pairs;
-        if (items > kLimit || n * c->heads > kLimit || c->heads > 65535) return fail(HK_ERR_INVALID_ARG, "problem too large");
+        if (items > kLimit || n * c->heads > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
         PrefillParams p = {};
         p.B = static_cast<int32_t>(n);
         p.Hq = static_cast<int32_t>(Hq);
@@ -471,8 +481,8 @@ extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, con
 
 extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                   int64_t max_pages) {
-    if (!cache || cache->heads < 1 || cache->page_size < 1 || cache->head_dim < 1 || B <= 0 || T <= 0 || Hq < cache->heads ||
-        T > kLimit / 16 / (Hq / cache->heads) || max_pages <= 0 || max_pages > kLimit / cache->page_size)
+    if (!cache || !cache_shape_ok(cache) || !table_width_ok(max_pages, cache->page_size) || B <= 0 || B > kLimit || T <= 0 ||
+        Hq < cache->heads || Hq > kLimit || T > kLimit / 16 / (Hq / cache->heads))
         return 0;
     size_t split = decode_workspace(cache, B, T, Hq).total;
     // (blocks that have a unit to themselves need none)
@@ -552,7 +562,6 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.num_pages = cache->num_pages;
     p.causal = causal ? 1 : 0;
     p.scale_log2 = scale_log2;
-    p.min_tiles = 1;
     char* const w = static_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(w);
     p.part_ml = reinterpret_cast<float*>(w + ws.ml);
@@ -570,6 +579,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
         for (int i = 1; i < 4 && (units << i) <= g_cluster_blocks[device][i] && (kBlockWarps << (i - 1)) <= unit_room; ++i)
             plan.cluster = 1 << i;
     if (unit_room <= int64_t(plan.cluster) * warps * kBlockTiles) plan.warps = warps;
+    p.warps = plan.blocks * kDecodeWarps;
 
     for (int64_t b0 = 0; b0 < B; b0 += batch) {       // (launches of one stream: they may share the workspace)
         p.B = static_cast<int32_t>(std::min<int64_t>(B - b0, batch));

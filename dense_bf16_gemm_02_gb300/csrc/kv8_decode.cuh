@@ -79,7 +79,7 @@ struct DecodeParams {
     int64_t num_pages;
     int32_t causal, vec_q, vec_o;
     float scale_log2;                               // softmax scale · log2(e)
-    int32_t min_tiles;                              // least tiles of a run
+    int32_t warps;                                  // of kv8_decode_kernel's grid
     float* part_o;                                  // [2 · warps][16][D]
     float* part_ml;                                 // [2 · warps][16][2]
     int4* info;                                     // [units]: parts whose sums make up the unit (0: it is finished), first slot, first warp
@@ -469,7 +469,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     uint8_t* const smem = smem_raw + (base - raw);
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
     const uint32_t g = lane >> 2, c = lane & 3u;
-    const int warps = static_cast<int>(gridDim.x) * kDecodeWarps;
     const int self = static_cast<int>(blockIdx.x) * kDecodeWarps + static_cast<int>(warp);
 
     griddep_launch_dependents();             // the combining kernel may be scheduled; it waits for this grid's end
@@ -507,34 +506,31 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     __syncthreads();
 
     const int64_t total = prefix[p.B];
-    const int64_t per = max(static_cast<int64_t>(p.min_tiles), (total + warps - 1) / warps);
+    const int64_t per = (total + p.warps - 1) / p.warps;
     const int64_t begin = min(total, self * per), end = min(total, begin + per);
     bool ok = true;
     int fills = 0, uses = 0;                 // ring stages filled and consumed so far
 
-    // the sequence of the run's first tile
-    int b = 0;
-    {
+    // the unit of the run's first tile, and the tile's place in it
+    int b = 0, h = 0, rt = 0, first = 0;
+    Sequence seq = {0, 0};
+    if (begin < end) {
         int lo = 0, hi = p.B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (prefix[mid] <= begin) lo = mid; else hi = mid - 1;
         }
         b = lo;
+        seq = sequence(p, b);
+        const int head_tiles = sequence_tiles(p, seq);
+        const int64_t local = begin - prefix[b];
+        h = static_cast<int>(local / head_tiles);
+        first = static_cast<int>(local - static_cast<int64_t>(h) * head_tiles);
+        for (int n; first >= (n = tiles_of(row_tile_end(p, seq, rt))); ++rt) first -= n;
     }
     int64_t at = begin;
-    while (at < end && ok) {
-        while (at >= prefix[b + 1]) ++b;
-        const Sequence seq = sequence(p, b);
-        const int head_tiles = sequence_tiles(p, seq);
-        const int64_t local = at - prefix[b];
-        const int h = static_cast<int>(local / head_tiles);
-        int first = static_cast<int>(local - static_cast<int64_t>(h) * head_tiles);
-        int rt = 0, key_end = row_tile_end(p, seq, 0);
-        while (first >= tiles_of(key_end)) {
-            first -= tiles_of(key_end);
-            key_end = row_tile_end(p, seq, ++rt);
-        }
+    while (at < end) {
+        const int key_end = row_tile_end(p, seq, rt);
         const int unit_tiles = tiles_of(key_end);
         const int last = static_cast<int>(min(static_cast<int64_t>(unit_tiles), first + (end - at)));   // tiles [first, last)
 
@@ -581,7 +577,16 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 }
             }
         }
+        // the next unit: row tiles innermost, then heads, then sequences (every sequence has tiles)
         at += last - first;
+        first = 0;
+        if (++rt == p.row_tiles) {
+            rt = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                if (++b < p.B) seq = sequence(p, b);
+            }
+        }
     }
     // abort: the copies in flight land before the block ends
     if (!ok)
@@ -806,6 +811,8 @@ kv8_combine_kernel(const DecodeParams p) {
     const int4 info = __ldcg(p.info + blockIdx.x);   // (past L1: this grid may have started before the writes)
     const int parts = info.x;
     if (parts == 0) return;
+    // (a launch whose waits gave up leaves records unwritten: what they hold is no place to read from)
+    if (parts < 0 || info.y < 0 || info.y >= 2 * p.warps || info.z < 0 || parts > p.warps - info.z) return;
     const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
     int unit = static_cast<int>(blockIdx.x);
     const int rt = unit % p.row_tiles;

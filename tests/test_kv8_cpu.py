@@ -112,3 +112,25 @@ def test_reference_attention_by_hand():
     o, lse, _ = ref.attention(q, codes, scale, v, scale, [[0]], [2], [3], True, 1.0)
     assert np.all(o[0, 0] == 0) and np.isneginf(lse[0, 0, 0])            # stands before the first token
     assert np.all(o[0, 1] == 1.0) and np.allclose(o[0, 2], 1.5) and np.isclose(lse[0, 2, 0], np.log(2))
+
+
+def test_sizes_that_pass_64_bits_are_refused(lib):
+    """Shapes whose products (rows x heads x head_dim) pass what 64 bits hold: refused, and no bytes asked for."""
+    from dense_bf16_gemm_02_gb300 import hk_gemm as h
+    INV = h.HK_ERR_INVALID_ARG
+
+    def at(cache, T, Hq, pages):
+        return lib.hk_attention_kv8(P, 0, S3, ctypes.byref(cache), P, pages, pages, P, None, P, S3, None, 1, T, Hq, 1, 0.0,
+                                    P, 1 << 40, None)
+    many_heads = _cache(num_pages=1, heads=1 << 27, page_size=16, head_dim=128)
+    assert h.hk_attention_kv8_workspace_size(many_heads, 1, 128, 1 << 27, 1 << 26) == 0
+    assert at(many_heads, 128, 1 << 27, 1 << 26) == INV
+    one_page = _cache(num_pages=1, heads=65535, page_size=128, head_dim=128)
+    assert h.hk_attention_kv8_workspace_size(one_page, 1, 4096, 65535, (1 << 24) - 1) > 1 << 40    # (huge, but a size)
+    assert h.hk_attention_kv8_workspace_size(one_page, 1, 4096, 65535, 1 << 24) == 0               # 2^31 tokens
+    assert at(one_page, 4096, 65535, 1 << 24) == INV
+    for bad in BAD_CACHES:
+        if all(v is not None for v in bad.values()):
+            assert h.hk_attention_kv8_workspace_size(_cache(**bad), 2, 4000, 8, 4000) == 0, bad
+    assert h.hk_attention_kv8_workspace_size(_cache(), 2, 1 << 40, 8, 4000) == 0
+    assert h.hk_attention_kv8_workspace_size(_cache(), 1 << 40, 1, 8, 4000) == 0

@@ -371,3 +371,31 @@ def test_repeats_exactly_on_streams_and_in_graphs(hk, T):
     again = hk.attention_kv8(q, cache, table[1], _i32([100, 700, 20]))
     assert torch.equal(captured.view(torch.int16), again.view(torch.int16))
     assert _status(hk) == hk.HK_OK
+
+
+@pytest.mark.parametrize("T,dtype", [(1, "bfloat16"), (9, "float16"), (70, "float16")])
+def test_workspace_contents_do_not_matter(hk, T, dtype):
+    """Long tables, whose units several warps share: every record and sum that is read was written by the call."""
+    import ctypes
+
+    import torch
+    rng = np.random.default_rng(23)
+    lengths, counts = [66000, 40, 0, 3000], [T, 1, T, max(T - 3, 0)]
+    H, D, group = 2, 64, 3
+    cache, table = _filled(hk, rng, lengths, H, D, 64)
+    q = _tokens(rng, 4, T, H * group, D, getattr(torch, dtype), 1)
+    want = _assert_attention(hk, q, cache, table, lengths, counts, True)
+    lib = hk.load()
+    size = lib.hk_attention_kv8_workspace_size(cache._ref, 4, T, H * group, table[1].size(1))
+    assert size > 0
+    n, c = _i32(lengths), _i32(counts)
+    strides = (ctypes.c_int64 * 3)(*q.stride()[:3])
+    for fill in (0, 0x7F, 0xFF):
+        workspace = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        assert lib.hk_attention_kv8(q.data_ptr(), hk.HK_TYPE_BF16 if dtype == "bfloat16" else hk.HK_TYPE_FP16, strides,
+                                    cache._ref, table[1].data_ptr(), table[1].stride(0), table[1].size(1), n.data_ptr(),
+                                    c.data_ptr(), out.data_ptr(), strides, None, 4, T, H * group, 1, 0.0,
+                                    workspace.data_ptr(), size, torch.cuda.current_stream().cuda_stream) == hk.HK_OK
+        assert _status(hk) == hk.HK_OK
+        assert torch.equal(out, want)
