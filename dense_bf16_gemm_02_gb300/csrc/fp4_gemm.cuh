@@ -213,33 +213,34 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     bool ok = true;
 
     if (warp == 0) {
-        if (lane == 0) {
-            griddep_wait();              // launched early behind the kernel that may have written the operands
-            const uint8_t* const sft = p.sfa + (static_cast<int64_t>(tm) * kTok / 128) * p.k_stages * G::kSfBytes;
-            const uint8_t* const sfw = p.sfb + static_cast<int64_t>(tn) * p.k_stages * G::kSfBytes;
-            int fills = 0, dropped = -1;
-            for (int ks = ks_begin; ks < ks_end; ++ks, ++fills) {
-                const int s = fills % G::kStages;
-                if (!wait_mbar_poll(p.wait, empty_bar(s), ((fills / G::kStages) & 1) ^ 1u, kErrWaitRing)) {
-                    ok = false;
-                    break;
-                }
-                if ((p.flags & kFlagDropArrive) && fills == 0) {   // test only: this stage is never filled
-                    dropped = 0;
-                    continue;
-                }
-                mbar_arrive_expect_tx(full_bar(s), G::kStageBytes);
-                tma_load_2d(base + G::kOffW + s * G::kWBytes, &tmap_b, ks * kStageRowBytes, tn * G::kTileF, full_bar(s));
-                tma_load_2d(base + G::kOffT + s * G::kTBytes, &tmap_a, ks * kStageRowBytes, tm * kTok, full_bar(s));
-                const uint32_t sf = base + G::kOffSf + s * 2 * G::kSfBytes;
-                bulk_load(sf, sfw + static_cast<int64_t>(ks) * G::kSfBytes, G::kSfBytes, full_bar(s));
-                bulk_load(sf + G::kSfBytes, sft + static_cast<int64_t>(ks) * G::kSfBytes, G::kSfBytes, full_bar(s));
+        griddep_wait();                  // launched early behind the kernel that may have written the operands
+        const uint8_t* const sft = p.sfa + (static_cast<int64_t>(tm) * kTok / 128) * p.k_stages * G::kSfBytes;
+        const uint8_t* const sfw = p.sfb + static_cast<int64_t>(tn) * p.k_stages * G::kSfBytes;
+        const bool drop = p.flags & kFlagDropArrive;       // test only: the first stage is never filled
+        int fills = 0, stage = 0;
+        uint32_t phase = 1;
+        for (int ks = ks_begin; ks < ks_end; ++ks) {
+            if (ok) ok = wait_mbar_poll(p.wait, empty_bar(stage), phase, kErrWaitRing);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && !(drop && ks == ks_begin) && elect_one()) {
+                const uint32_t sf = base + G::kOffSf + stage * 2 * G::kSfBytes;
+                mbar_arrive_expect_tx(full_bar(stage), G::kStageBytes);
+                tma_load_2d(base + G::kOffW + stage * G::kWBytes, &tmap_b, ks * kStageRowBytes, tn * G::kTileF, full_bar(stage));
+                tma_load_2d(base + G::kOffT + stage * G::kTBytes, &tmap_a, ks * kStageRowBytes, tm * kTok, full_bar(stage));
+                bulk_load(sf, sfw + static_cast<int64_t>(ks) * G::kSfBytes, G::kSfBytes, full_bar(stage));
+                bulk_load(sf + G::kSfBytes, sft + static_cast<int64_t>(ks) * G::kSfBytes, G::kSfBytes, full_bar(stage));
             }
-            // abort: the copies in flight land before the CTA ends
-            if (!ok || wait_aborted(p.wait))
-                for (int f = fills > G::kStages ? fills - G::kStages : 0; f < fills; ++f)
-                    if (f != dropped) wait_mbar_drain(full_bar(f % G::kStages), (f / G::kStages) & 1);
+            __syncwarp();
+            if (ok) ++fills;
+            if (++stage == G::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
+        // abort: the copies in flight land before the CTA ends
+        if (lane == 0 && (!ok || wait_aborted(p.wait)))
+            for (int f = fills > G::kStages ? fills - G::kStages : 0; f < fills; ++f)
+                if (!drop || f > 0) wait_mbar_drain(full_bar(f % G::kStages), (f / G::kStages) & 1);
     } else if (warp == 1) {
         int stage = 0;
         uint32_t phase = 0;
