@@ -132,15 +132,97 @@ __device__ __forceinline__ float global_alpha(const Fp4Params& p) {
     return (p.ga != nullptr ? *p.ga : 1.0f) * (p.gb != nullptr ? *p.gb : 1.0f);
 }
 
+template <int kCols>
+__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, uint32_t (&v)[kCols]) {
+    static_assert(kCols == 16 || kCols == 32, "16 or 32 columns");
+    if constexpr (kCols == 16) tmem_load_16cols(taddr, v);
+    else tmem_load_32cols(taddr, v);
+}
+
+// Sums of one feature and kStep tokens to their rows of C, as far as there are tokens.
+template <int kStep>
+__device__ __forceinline__ void store_tokens(uint16_t* dst, int64_t ldc, const uint32_t (&v)[kStep], float alpha, int tokens) {
+    uint32_t w[kStep / 2];
+#pragma unroll
+    for (int i = 0; i < kStep / 2; ++i)
+        w[i] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(v[2 * i]) * alpha),
+                              __float_as_uint(__uint_as_float(v[2 * i + 1]) * alpha));
+    if (tokens >= kStep) {
+#pragma unroll
+        for (int e = 0; e < kStep; ++e) dst[e * ldc] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kStep; ++e)
+            if (e < tokens) dst[e * ldc] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]);
+    }
+}
+
+// Tokens [t0, t1) of a tile whose K range kParts CTAs of a cluster shared: the
+// sums of the parts, added in order. Four features of a token per thread (32
+// threads a token, so a warp reads whole 512-byte rows); sixteen loads of each
+// thread are in flight, since another CTA's shared memory is
+// far away; none past t1, since its rate is low.
+template <int kTok, int kParts>
+__device__ __forceinline__ void join_tokens(const Fp4Params& p, uint32_t base, int tm, int tn, int t0, int t1, int warp, bool ok) {
+    constexpr int kTokens = 16 / kParts;
+    const int lane = static_cast<int>(lane_id());
+    const int feature = tn * 128 + lane * 4;
+    const float alpha = global_alpha(p);
+    uint32_t from[kParts];
+#pragma unroll
+    for (int r = 0; r < kParts; ++r) from[r] = map_to_cta(base + static_cast<uint32_t>(lane) * 16u, static_cast<uint32_t>(r));
+#pragma unroll 1
+    for (int t = t0 + warp; t < t1; t += 4 * kTokens) {
+        float4 x[kTokens][kParts];
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            if (t + 4 * i < t1) {
+#pragma unroll
+                for (int r = 0; r < kParts; ++r) x[i][r] = ld_cluster_v4(from[r] + static_cast<uint32_t>(t + 4 * i) * 512u);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            float4 sum = x[i][0];
+#pragma unroll
+            for (int r = 1; r < kParts; ++r) {
+                sum.x += x[i][r].x;
+                sum.y += x[i][r].y;
+                sum.z += x[i][r].z;
+                sum.w += x[i][r].w;
+            }
+            if (!ok || t + 4 * i >= t1) continue;
+            uint16_t* const dst = p.c + static_cast<int64_t>(tm * kTok + t + 4 * i) * p.ldc + feature;
+            const uint32_t w0 = pack_bf16x2_rn(__float_as_uint(sum.x * alpha), __float_as_uint(sum.y * alpha));
+            const uint32_t w1 = pack_bf16x2_rn(__float_as_uint(sum.z * alpha), __float_as_uint(sum.w * alpha));
+            if (p.vec_c && feature + 4 <= p.N) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(w0, w1);
+            } else {
+                const uint32_t w[2] = {w0, w1};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (feature + e < p.N) dst[e] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------- one-CTA tile kernel --
 //
-// For few tokens (rows of A): a tile is 128 features × kTok tokens and the
-// MMA's M side takes the features (rows of B), so that its N side need only be
-// as wide as the tokens are many. The tile's K range may be cut over the CTAs
-// of a cluster (one CTA per part); each leaves its fp32 sums in its shared
-// memory, and the CTAs then each add up and store a share of the tile's
+// For few tokens (rows of A) and for few tiles: a tile is 128 features × kTok
+// tokens and the MMA's M side takes the features (rows of B), so that its N side
+// need only be as wide as the tokens are many. The tile's K range may be cut over
+// the CTAs of a cluster (one CTA per part); each leaves its fp32 sums in its
+// shared memory, and the CTAs then each add up and store a share of the tile's
 // tokens, in the order of the parts (the result does not depend on timing).
 // Two CTAs fit on an SM, so a tile's start and end overlap another's stream.
+//
+// One token is bound by reading B: 28672 × 8192 MXFP4 in 20.8 us, 6.0 TB/s of the
+// 6.8 that a copy reaches. Toward 128 tokens the tile's end counts: A's traffic
+// from L2 comes to B's, and the sums go through one CTA's registers and, where K
+// is cut, through other SMs' shared memory, whose rate is low (128 tokens in 4
+// parts: 3 of 13 us at 8192 × 8192). 128 × 28672 × 8192 takes 24.3 us (26.2 when the
+// epilogue took 16 columns at a time and tested each token).
 template <int kTok, int kFmt>
 struct SingleGeometry {
     static_assert(kTok == 16 || kTok == 32 || kTok == 64 || kTok == 128, "tokens per tile");
@@ -244,6 +326,8 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     } else if (warp == 1) {
         int stage = 0;
         uint32_t phase = 0;
+        // (a column of a scale tile holds 32 rows: the second 64 tokens of 128 begin two columns on)
+        const uint32_t t_shift = kTok == 64 ? 2u * (static_cast<uint32_t>(tm) & 1u) : 0u;
         // (after a wait that gave up the loop runs on without issuing: its exit depends on no wait, so that the
         // compiler sees every index as the same in all lanes)
         for (int ks = ks_begin; ks < ks_end; ++ks) {
@@ -264,7 +348,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     const uint32_t col = 4 * mma_scale_tile<kFmt>(k);
                     mma_fp4<1, kFmt>(tmem_base, smem_desc(wd + 2 * k, kDescHighKmajorSw128),
                                      smem_desc(td + 2 * k, kDescHighKmajorSw128), G::kIdesc | (id << 4) | (id << 29),
-                                     sf_tmem + col, sf_tmem + 4 * G::kSfTiles + col, (ks > ks_begin || k > 0) ? 1u : 0u);
+                                     sf_tmem + col, sf_tmem + 4 * G::kSfTiles + col + t_shift, (ks > ks_begin || k > 0) ? 1u : 0u);
                 }
                 mma_commit_one(empty_bar(stage));
             }
@@ -290,34 +374,32 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
         const int feature = tn * G::kTileF + f_local;
         const uint32_t t_row = tmem_base + ((q * 32u) << 16);
         const float alpha = global_alpha(p);
+        // (columns of 32 tokens at a time, and no test or address of its own for each token where all of them are
+        // inside C: one warp of a scheduler pays the latency of every instruction that depends on another)
+        constexpr int kStep = kTok < 32 ? kTok : 32;
         if (splits == 1) {
 #pragma unroll 1
-            for (int c = 0; c < kTok; c += 16) {
-                const int token0 = tm * kTok + c;
-                if (token0 >= p.M) break;
-                uint32_t v[16];
-                tmem_load_16cols(t_row + c, v);
+            for (int c = 0; c < kTok; c += kStep) {
+                const int left = p.M - (tm * kTok + c);
+                if (left <= 0) break;
+                uint32_t v[kStep];
+                tmem_load_cols<kStep>(t_row + c, v);
                 tmem_wait_ld();
-                if (ok && feature < p.N) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (token0 + e < p.M)
-                            p.c[static_cast<int64_t>(token0 + e) * p.ldc + feature] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[e]) * alpha));
-                }
+                if (ok && feature < p.N)
+                    store_tokens<kStep>(p.c + static_cast<int64_t>(tm * kTok + c) * p.ldc + feature, p.ldc, v, alpha, left);
             }
         } else {
             // this part's sums: [token][feature] fp32 in the ring's place (every MMA has
             // read its operands, and no copy is in flight)
             float* const sums = reinterpret_cast<float*>(smem);
 #pragma unroll 1
-            for (int c = 0; c < kTok; c += 16) {
-                uint32_t v[16];
-                tmem_load_16cols(t_row + c, v);
+            for (int c = 0; c < kTok; c += kStep) {
+                uint32_t v[kStep];
+                tmem_load_cols<kStep>(t_row + c, v);
                 tmem_wait_ld();
                 if (ok) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) sums[(c + e) * G::kTileF + f_local] = __uint_as_float(v[e]);
+                    for (int e = 0; e < kStep; ++e) sums[(c + e) * G::kTileF + f_local] = __uint_as_float(v[e]);
                 }
             }
         }
@@ -326,42 +408,13 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     __syncwarp();
     if (splits > 1) {
         cluster_sync();
-        // this CTA's share of the tokens, four features of a token per thread (32 threads a token, so a
-        // warp reads whole 512-byte rows), the loads of all parts in flight together
+        // this CTA's share of the tokens
         if (warp >= 2) {
             const int each = (kTok + splits - 1) / splits;
-            const int t_end = min(min(kTok, (part + 1) * each), p.M - tm * kTok);
-            const int feature = tn * G::kTileF + static_cast<int>(lane) * 4;
-            const float alpha = global_alpha(p);
-#pragma unroll 2
-            for (int t = part * each + static_cast<int>(warp) - 2; t < t_end; t += 4) {
-                const uint32_t at = base + static_cast<uint32_t>(t * G::kTileF + static_cast<int>(lane) * 4) * 4u;
-                float4 x[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < splits) x[r] = ld_cluster_v4(map_to_cta(at, static_cast<uint32_t>(r)));
-                float4 sum = x[0];
-#pragma unroll
-                for (int r = 1; r < 8; ++r)
-                    if (r < splits) {
-                        sum.x += x[r].x;
-                        sum.y += x[r].y;
-                        sum.z += x[r].z;
-                        sum.w += x[r].w;
-                    }
-                if (!ok) continue;
-                uint16_t* const dst = p.c + static_cast<int64_t>(tm * kTok + t) * p.ldc + feature;
-                const uint32_t w0 = pack_bf16x2_rn(__float_as_uint(sum.x * alpha), __float_as_uint(sum.y * alpha));
-                const uint32_t w1 = pack_bf16x2_rn(__float_as_uint(sum.z * alpha), __float_as_uint(sum.w * alpha));
-                if (p.vec_c && feature + 4 <= p.N) {
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(w0, w1);
-                } else {
-                    const uint32_t w[2] = {w0, w1};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (feature + e < p.N) dst[e] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
-                }
-            }
+            const int t0 = part * each, t1 = min(min(kTok, t0 + each), p.M - tm * kTok);
+            if (splits == 2) join_tokens<kTok, 2>(p, base, tm, tn, t0, t1, static_cast<int>(warp) - 2, ok);
+            else if (splits == 4) join_tokens<kTok, 4>(p, base, tm, tn, t0, t1, static_cast<int>(warp) - 2, ok);
+            else join_tokens<kTok, 8>(p, base, tm, tn, t0, t1, static_cast<int>(warp) - 2, ok);
         }
         cluster_sync();    // no CTA leaves while another reads its sums
     } else {

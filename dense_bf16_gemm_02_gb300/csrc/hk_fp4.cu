@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -248,12 +249,56 @@ hk_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 enc, Fp4Params p, const 
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the 4-bit product", e);
 }
 
-// K parts of a tile: the most that keep the launch within one round of
-// resident CTAs (two per SM) and each part at least four stages long.
-int choose_splits(int64_t tiles, int64_t k_stages, int sm_count) {
-    int s = 1;
-    while (s < 8 && tiles * s * 2 <= 2 * int64_t(sm_count) && k_stages >= 4 * s * 2) s *= 2;
-    return s;
+// The one-CTA kernel's tile width and K parts. Estimated time in microseconds, fitted to 600 timings (M 1 to 128, 11
+// shapes from 1000 x 3000 to 28672 x 8192, both formats): what memory (6.6 TB/s), the traffic from L2 (27 TB/s;
+// rows that do not start on 128 bytes cost two lines for one) and the chain of stages (0.23 each) take, joined as a
+// root of squares, and per round of CTAs the tile's epilogue (0.033 per token) and the join of K parts (1.0, of
+// eight 1.4). The choice is 0.3 % off the best of what is allowed on average, 8 % at worst; the narrowest tile that
+// holds all tokens with K cut until the GPU is full was 7 % and 47 % off (128 x 2048 x 8192: 64 tokens in 8 parts
+// 7.7 us, 128 tokens in 8 parts 9.7; 100 x 6144 x 2048: 64 tokens unsplit 6.1, 128 tokens in 2 parts 8.0).
+struct SinglePlan {
+    const SingleVariant* v;
+    int splits;
+    double us;
+};
+
+SinglePlan plan_single(int64_t M, int64_t N, int64_t K, bool aligned_rows, int32_t format, int forced_splits, int sm_count) {
+    SinglePlan best = {nullptr, 1, 0.0};
+    const double k_stages = static_cast<double>(ceil_div(K, kStageCols));
+    const double dram = static_cast<double>(M + N) * static_cast<double>(K) * (0.5 + 1.0 / block_cols(format)) * 1e-6;
+    for (const SingleVariant& v : kSingle[format == HK_FP4_NVFP4]) {
+        // 16 and 32 tokens only as the one tile (the scales of 128 rows come in columns of 32, and a tile may
+        // begin at every second one); nothing wider than holds every token
+        if (v.tok < 64 && M > v.tok) continue;
+        if (v.tok > 16 && v.tok / 2 >= M) break;
+        const double tiles = static_cast<double>(ceil_div(M, v.tok)) * static_cast<double>(ceil_div(N, 128));
+        const double stage = (aligned_rows ? 1.0 : 2.0) * (128 + v.tok) * kStageRowBytes + 2.0 * 512 * scale_tiles(format);
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            if (forced_splits ? splits != forced_splits : splits > 1 && (splits > k_stages || tiles * splits > 4 * sm_count)) continue;
+            const double rounds = std::ceil(tiles * splits / (2 * sm_count));
+            const double join = splits == 1 ? 0.0 : splits == 8 ? 1.4 : 1.0;
+            const double memory = dram / 6.6, l2 = tiles * k_stages * stage * 1e-6 / 27.0;
+            const double chain = 0.23 * std::ceil(k_stages / splits) * rounds;
+            const double us = rounds * (0.033 * v.tok + join) + std::sqrt(memory * memory + l2 * l2 + chain * chain);
+            if (best.v == nullptr || us < best.us) best = {&v, splits, us};
+        }
+    }
+    best.us += 1.5;
+    return best;
+}
+
+// The CTA-pair kernel's time, fitted likewise (M 130 to 2048, 8 shapes): memory and the chain of its 256 x 256 tiles'
+// stages. Taking the kernel with the lower estimate is 0.2 % off the better of the two on average, 5 % at worst.
+// (512 x 1024 x 4096: one CTA 7.0 us, pair 9.1; 512 x 8192 x 8192: 16.9 and 16.1; 1024 x 1024 x 28672: 19.4 and 38.8;
+// 256 x 28672 x 8192: 35.8 and 30.9; 2048 x 4096 x 4096: 19.5 and 16.4.)
+double pair_us(int64_t M, int64_t N, int64_t K, int32_t format, int sm_count) {
+    const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 256), units = sm_count / 2, rounds = ceil_div(tiles, units);
+    const bool halves = 2 * (tiles - (rounds - 1) * units) <= units;          // the last round's tiles run as halves
+    const double bytes = static_cast<double>(M + N) * static_cast<double>(K) * (0.5 + 1.0 / block_cols(format)) +
+                         2.0 * static_cast<double>(M) * static_cast<double>(N);
+    const double memory = bytes * 1e-6 / 5.8;
+    const double chain = 0.46 * static_cast<double>(ceil_div(K, kStageCols)) * (static_cast<double>(rounds) - (halves ? 0.5 : 0.0));
+    return 5.3 + std::sqrt(memory * memory + chain * chain);
 }
 
 }  // namespace
@@ -369,16 +414,14 @@ extern "C" hk_status hk_gemm_fp4_ex(const void* A, const void* SFA, const void* 
     p.wait.launch_id = hk_host::next_launch_id();
     p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
 
-    if (kernel == HK_KERNEL_PAIR_256x256 || (kernel == HK_KERNEL_AUTO && M > 128))
+    const SinglePlan plan = plan_single(M, N, K, lda % 128 == 0 && ldb % 128 == 0, format, split_k, sms);
+    if (kernel == HK_KERNEL_PAIR_256x256 || (kernel == HK_KERNEL_AUTO && M > 128 && pair_us(M, N, K, format, sms) < plan.us))
         return launch_pair(enc, p, A, B, K, lda, ldb, format, sms, st);
-    // the narrowest tile that holds every token: the MMA's time and a stage's shared memory grow with it
-    const SingleVariant* v = &kSingle[format == HK_FP4_NVFP4][3];
-    for (int i = 2; i >= 0; --i)
-        if (M <= kSingle[format == HK_FP4_NVFP4][i].tok) v = &kSingle[format == HK_FP4_NVFP4][i];
+    const SingleVariant* const v = plan.v;
     p.tiles_m = static_cast<int32_t>(ceil_div(M, v->tok));
     p.tiles_n = static_cast<int32_t>(ceil_div(N, 128));
     const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
-    int splits = split_k ? split_k : choose_splits(tiles, p.k_stages, sms);
+    int splits = plan.splits;
     while (splits > p.k_stages) splits /= 2;     // every part owns at least one stage
     CUtensorMap ta, tb;
     if ((s = encode_codes(enc, &ta, A, M, K, lda, static_cast<uint32_t>(v->tok), "A")) != HK_OK) return s;

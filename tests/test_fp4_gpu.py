@@ -330,3 +330,16 @@ def test_product_wait_that_runs_out_is_reported(hk, M):
     assert hk.hk_gemm_last_device_status(0) == hk.HK_ERR_TIMEOUT
     _assert_product(hk.gemm_fp4(a, b), av, bv, 4096)     # the context is usable, the next call right
     _status_ok(hk)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K,split", [(100, 8200, 1500, 1), (128, 1030, 2048, 4), (90, 2000, 4096, 2), (128, 300, 4096, 8),
+                                         (200, 130, 600, 1), (333, 520, 1024, 2), (1000, 257, 300, 1)])
+def test_product_tiles_of_fewer_tokens_than_there_are(hk, fmt, M, N, K, split):
+    """Several tiles along M whose scales lie in one tile of 128 rows."""
+    from dense_bf16_gemm_02_gb300 import hk_gemm as h
+    a, av = _random_matrix(hk, M, K, fmt, 11)
+    b, bv = _random_matrix(hk, N, K, fmt, 12)
+    _assert_product(_forced(hk, a, b, h.HK_KERNEL_SINGLE_128x128, split), av, bv, K)
+    _assert_product(_forced(hk, a, b, h.HK_KERNEL_SINGLE_128x128, 0), av, bv, K)
+    _status_ok(hk)
