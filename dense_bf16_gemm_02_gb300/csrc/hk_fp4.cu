@@ -254,8 +254,8 @@ hk_status launch_pair(PFN_cuTensorMapEncodeTiled_v12000 enc, Fp4Params p, const 
 // rows that do not start on 128 bytes cost two lines for one) and the chain of stages (0.23 each) take, joined as a
 // root of squares, and per round of CTAs the tile's epilogue (0.033 per token) and the join of K parts (1.0, of
 // eight 1.4). The choice is 0.3 % off the best of what is allowed on average, 8 % at worst; the narrowest tile that
-// holds all tokens with K cut until the GPU is full was 7 % and 47 % off (128 x 2048 x 8192: 64 tokens in 8 parts
-// 7.7 us, 128 tokens in 8 parts 9.7; 100 x 6144 x 2048: 64 tokens unsplit 6.1, 128 tokens in 2 parts 8.0).
+// holds all tokens with K cut until the GPU is full was 7 % and 47 % off (128 x 2048 x 8192: 64 tokens in 4 parts
+// 7.8 us, 128 tokens in 8 parts 9.7; 100 x 6144 x 2048: 64 tokens unsplit 5.5, 128 tokens in 2 parts 7.9).
 struct SinglePlan {
     const SingleVariant* v;
     int splits;

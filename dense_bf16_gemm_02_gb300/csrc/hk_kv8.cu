@@ -101,14 +101,22 @@ cudaError_t launch_early(void (*fn)(Params...), dim3 grid, dim3 block, size_t sm
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-template <typename T, int kWarps>
+template <typename T, int kD, int kWarps>
 cudaError_t launch_append(const AppendParams& p, int steps, unsigned blocks, cudaStream_t st) {
-    auto* fn = steps <= 1   ? &kv8_append_kernel<T, kWarps, 1>
-               : steps <= 2 ? &kv8_append_kernel<T, kWarps, 2>
-               : steps <= 4 ? &kv8_append_kernel<T, kWarps, 4>
-                            : &kv8_append_kernel<T, kWarps, 8>;
+    auto* fn = steps <= 1   ? &kv8_append_kernel<T, kD, kWarps, 1>
+               : steps <= 2 ? &kv8_append_kernel<T, kD, kWarps, 2>
+               : steps <= 4 ? &kv8_append_kernel<T, kD, kWarps, 4>
+                            : &kv8_append_kernel<T, kD, kWarps, 8>;
     return launch_early(fn, dim3(blocks), dim3(256), 0, st, p);
 }
+
+template <typename T>
+cudaError_t launch_append(const AppendParams& p, int D, bool one_warp, int steps, unsigned blocks, cudaStream_t st) {
+    if (D == 64) return one_warp ? launch_append<T, 64, 1>(p, steps, blocks, st) : launch_append<T, 64, 8>(p, steps, blocks, st);
+    return one_warp ? launch_append<T, 128, 1>(p, steps, blocks, st) : launch_append<T, 128, 8>(p, steps, blocks, st);
+}
+
+int page_shift(int32_t page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
 
 // Codes of keys or values as [pages · heads, page_size, D] in boxes of up to 32 tokens of one head.
 hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, const hk_kv8_cache* c) {
@@ -454,27 +462,25 @@ extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, con
     p.B = static_cast<int32_t>(B);
     p.T = static_cast<int32_t>(T);
     p.Hkv = static_cast<uint32_t>(cache->heads);
-    p.D = cache->head_dim;
-    p.page_size = cache->page_size;
+    p.page_shift = page_shift(cache->page_size);
     p.max_pages = static_cast<int32_t>(max_pages);
     p.num_pages = cache->num_pages;
-    p.slots = static_cast<uint32_t>((T + p.page_size - 2) / p.page_size + 1);
+    p.slots = static_cast<uint32_t>((T + cache->page_size - 2) / cache->page_size + 1);
     p.status = status;
     if (B > (int64_t(1) << 40) / p.slots / p.Hkv) return fail(HK_ERR_INVALID_ARG, "problem too large");
     p.items = B * p.slots * p.Hkv;
     // one warp holds the new tokens of a page as long as they fit its registers (8 steps of 256 elements)
-    const int64_t elements = std::min<int64_t>(T, p.page_size) * p.D;
+    const int64_t elements = std::min<int64_t>(T, cache->page_size) * cache->head_dim;
     const bool one_warp = elements <= kAppendSteps * 256;
     const int steps = static_cast<int>(ceil_div(elements, one_warp ? 256 : 8 * 256));
     const int64_t blocks = one_warp ? ceil_div(p.items, 8) : p.items;
     if (p.items > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto go = [&](auto one, auto eight) { return (one_warp ? one : eight)(p, steps, static_cast<unsigned>(blocks), st); };
     cudaError_t e;
     switch (type) {
-        case HK_TYPE_BF16: e = go(&launch_append<__nv_bfloat16, 1>, &launch_append<__nv_bfloat16, 8>); break;
-        case HK_TYPE_FP16: e = go(&launch_append<__half, 1>, &launch_append<__half, 8>); break;
-        default: e = go(&launch_append<float, 1>, &launch_append<float, 8>); break;
+        case HK_TYPE_BF16: e = launch_append<__nv_bfloat16>(p, cache->head_dim, one_warp, steps, static_cast<unsigned>(blocks), st); break;
+        case HK_TYPE_FP16: e = launch_append<__half>(p, cache->head_dim, one_warp, steps, static_cast<unsigned>(blocks), st); break;
+        default: e = launch_append<float>(p, cache->head_dim, one_warp, steps, static_cast<unsigned>(blocks), st); break;
     }
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the cache append", e);
 }
@@ -557,7 +563,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.group = static_cast<int32_t>(group);
     p.row_tiles = static_cast<int32_t>(ceil_div(T * group, kRows));
     p.page_size = cache->page_size;
-    p.page_shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : cache->page_size == 64 ? 6 : 7;
+    p.page_shift = page_shift(cache->page_size);
     p.max_pages = static_cast<int32_t>(max_pages);
     p.num_pages = cache->num_pages;
     p.causal = causal ? 1 : 0;

@@ -39,7 +39,7 @@ struct AppendParams {
     int64_t items;                 // B * slots * Hkv, below 2^32
     int32_t B, T;
     uint32_t Hkv, slots;           // heads; pages a sequence can touch
-    int32_t D, page_size, max_pages;
+    int32_t page_shift, max_pages; // log2 of the page's tokens
     int64_t num_pages;
     int32_t vec[2];                // 16-byte loads
     uint32_t* status;
@@ -113,9 +113,11 @@ struct Magnitude<float> {
     static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
 };
 
-template <typename T, int kWarps, int kSteps>
+template <typename T, int kD, int kWarps, int kSteps>
 __global__ void __launch_bounds__(256, 2 * kSteps * sizeof(Raw8<T>) <= 128 ? 4 : 2)
 kv8_append_kernel(const AppendParams p) {
+    constexpr int kLanes = kD / 8;                   // of a token: 8 elements each
+    constexpr int kStepTokens = kWarps * 32 / kLanes;
     __shared__ uint32_t warp_top[2][8];
     griddep_launch_dependents();
     griddep_wait();                  // launched early behind the kernel that may have written the tokens
@@ -125,49 +127,45 @@ kv8_append_kernel(const AppendParams p) {
     const int64_t item = kWarps == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : static_cast<int64_t>(blockIdx.x);
     if (item >= p.items) return;
     uint32_t rest = static_cast<uint32_t>(item);
-    const int h = static_cast<int>(rest % p.Hkv);
+    const uint32_t h = rest % p.Hkv;
     rest /= p.Hkv;
     const int b = static_cast<int>(rest / p.slots);
-    const int nth = static_cast<int>(rest % p.slots);
+    const uint32_t nth = rest % p.slots;
 
     const int32_t start = p.starts[b];
     const int32_t count = p.counts != nullptr ? p.counts[b] : p.T;
-    const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+    const int64_t room = static_cast<int64_t>(p.max_pages) << p.page_shift;
     const bool bad = start < 0 || count < 0 || count > p.T || start + static_cast<int64_t>(count) > room;
     if (bad) {
         if (lane == 0 && nth == 0) atomicOr(p.status, kErrPage);
         return;
     }
-    const int64_t slot = start / p.page_size + nth;
-    const int64_t lo = max(static_cast<int64_t>(start), slot * p.page_size);              // new tokens of this page
-    const int64_t hi = min(static_cast<int64_t>(start) + count, (slot + 1) * p.page_size);
+    // (below 2^32: the room is below 2^31, and so are the pages that T tokens can touch)
+    const uint32_t slot = (static_cast<uint32_t>(start) >> p.page_shift) + nth;
+    const uint32_t first = slot << p.page_shift;
+    const uint32_t lo = max(static_cast<uint32_t>(start), first);                         // new tokens of this page
+    const uint32_t hi = min(static_cast<uint32_t>(start) + static_cast<uint32_t>(count), first + (1u << p.page_shift));
     if (lo >= hi) return;
-    const int old_tokens = static_cast<int>(lo - slot * p.page_size);
+    const int old_tokens = static_cast<int>(lo - first);
     const int n = static_cast<int>(hi - lo);
 
-    const int lanes_per_token = p.D >> 3;
-    const int per_step = kWarps * (32 / lanes_per_token);
-    const int sub = static_cast<int>(member) * (32 / lanes_per_token) + static_cast<int>(lane) / lanes_per_token;
-    const int d = static_cast<int>(lane) % lanes_per_token * 8;
+    const int sub = static_cast<int>((member * 32 + lane) / kLanes);      // this lane's token of each step
+    const int d = static_cast<int>(lane) % kLanes * 8;
     Raw8<T> raw[2][kSteps];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        const T* const src = static_cast<const T*>(p.src[kv]) + b * p.stride_b[kv] + (lo - start) * p.stride_t[kv] +
-                             h * p.stride_h[kv];
-        // (one choice for all steps: with a choice at each load the next one waited for it)
+        const T* const src = static_cast<const T*>(p.src[kv]) + b * p.stride_b[kv] +
+                             static_cast<int64_t>(lo - static_cast<uint32_t>(start)) * p.stride_t[kv] + h * p.stride_h[kv] + d;
+        // (one choice for all steps: with a choice at each load the next one waited for it; past the last token
+        // it is taken again, which moves no maximum and needs no test)
         if (p.vec[kv]) {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int t = i * per_step + sub;
-                raw[kv][i] = Raw8<T>{};
-                if (t < n) raw[kv][i] = load8<T>(src + t * p.stride_t[kv] + d, 0, 8, true);
-            }
+            for (int i = 0; i < kSteps; ++i)
+                raw[kv][i] = load8<T>(src + min(i * kStepTokens + sub, n - 1) * p.stride_t[kv], 0, 8, true);
         } else {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int t = i * per_step + sub;
-                raw[kv][i] = load8<T>(src + t * p.stride_t[kv], d, t < n ? p.D : 0, false);
-            }
+            for (int i = 0; i < kSteps; ++i)
+                raw[kv][i] = load8<T>(src + min(i * kStepTokens + sub, n - 1) * p.stride_t[kv], 0, 8, false);
         }
     }
     const int64_t page = p.table[b * p.table_stride + slot];
@@ -201,26 +199,20 @@ kv8_append_kernel(const AppendParams p) {
         }
     }
     if constexpr (kWarps > 1) {
-        if (lane == 0) {
-            warp_top[0][warp] = top[0];
-            warp_top[1][warp] = top[1];
-        }
+        if (lane < 2) warp_top[lane][warp] = lane == 0 ? top[0] : top[1];
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            top[0] = max(top[0], warp_top[0][w]);
-            top[1] = max(top[1], warp_top[1][w]);
-        }
+        for (int kv = 0; kv < 2; ++kv) top[kv] = __reduce_max_sync(0xffffffffu, warp_top[kv][lane & 7u]);
     }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
         const float need = __uint_as_float(scale_field(top[kv]) << 23);
         const float scale = old_tokens > 0 ? fmaxf(need, had[kv]) : need;
-        uint8_t* const dst = p.codes[kv] + ph * p.page_size * p.D;
+        uint8_t* const dst = p.codes[kv] + (ph << p.page_shift) * kD;
         if (old_tokens > 0 && scale > had[kv]) {
             const float ratio = had[kv] / scale;
             uint4* const old = reinterpret_cast<uint4*>(dst);
-            for (int i = static_cast<int>(member * 32 + lane); i < old_tokens * p.D / 16; i += 32 * kWarps) {
+            for (int i = static_cast<int>(member * 32 + lane); i < old_tokens * (kD / 16); i += 32 * kWarps) {
                 uint4 w = old[i];
                 w.x = rescale_codes(w.x, ratio);
                 w.y = rescale_codes(w.y, ratio);
@@ -230,21 +222,27 @@ kv8_append_kernel(const AppendParams p) {
             }
         }
         const float inv = 1.0f / scale;      // exact: a power of two
+        const uint64_t inv2 = f32x2(inv, inv);
+        uint8_t* const at = dst + (old_tokens + sub) * kD + d;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int t = i * per_step + sub;
-            if (t < n) {
+            if (i * kStepTokens + sub < n) {
                 float v[8];
                 widen8<T>(raw[kv][i], v);
                 uint32_t w[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint16_t c0, c1;
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c0) : "f"(v[4 * k + 1] * inv), "f"(v[4 * k] * inv));
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c1) : "f"(v[4 * k + 3] * inv), "f"(v[4 * k + 2] * inv));
-                    w[k] = static_cast<uint32_t>(c0) | static_cast<uint32_t>(c1) << 16;
+                    float y[4];
+                    f32x2_split(fmul2(f32x2(v[4 * k], v[4 * k + 1]), inv2), y[0], y[1]);
+                    f32x2_split(fmul2(f32x2(v[4 * k + 2], v[4 * k + 3]), inv2), y[2], y[3]);
+                    asm("{\n\t.reg .b16 lo, hi;\n\t"
+                        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+                        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+                        "mov.b32 %0, {lo, hi};\n\t}"
+                        : "=r"(w[k])
+                        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
                 }
-                *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(old_tokens + t) * p.D + d) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(at + i * (kStepTokens * kD)) = make_uint2(w[0], w[1]);
             }
         }
         if (member == 0 && lane == 0) p.scale[kv][ph] = scale;
