@@ -35,6 +35,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "bounded_wait.cuh"
 #include "elements.cuh"
@@ -841,10 +842,13 @@ kv8_combine_kernel(const DecodeParams p) {
         }
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int i0 = share; i0 < parts; i0 += kSplit * kBatch) {
-            float pm[kBatch], pl[kBatch], x[kBatch][kVec];
+        // up to kN parts, their loads in flight together: no test or branch between them, which would take them
+        // one at a time (past the last part it is loaded again and not counted)
+        auto batch = [&](int i0, auto size) {
+            constexpr int kN = decltype(size)::value;
+            float pm[kN], pl[kN], x[kN][kVec];
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {       // (past the last part: loaded again and not counted)
+            for (int q = 0; q < kN; ++q) {
                 const int64_t a = row_of(min(i0 + kSplit * q, parts - 1));
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
                 pm[q] = ml.x;
@@ -858,14 +862,17 @@ kv8_combine_kernel(const DecodeParams p) {
                 }
             }
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                if (i0 + kSplit * q >= parts) break;
-                const float weight = pm[q] == -INFINITY ? 0.0f : ex2_approx(pm[q] - m);
-                l += pl[q] * (pm[q] == -INFINITY ? 1.0f : weight);      // (a NaN sum stays one)
+            for (int q = 0; q < kN; ++q) {
+                const bool counts = i0 + kSplit * q < parts;
+                const float weight = !counts || pm[q] == -INFINITY ? 0.0f : ex2_approx(pm[q] - m);
+                l += !counts ? 0.0f : pm[q] == -INFINITY ? pl[q] : pl[q] * weight;       // (a NaN sum stays one)
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) acc[k] += x[q][k] * weight;
             }
-        }
+        };
+        int i0 = share;
+        for (; i0 + kSplit * 2 < parts; i0 += kSplit * kBatch) batch(i0, std::integral_constant<int, kBatch>{});
+        if (i0 < parts) batch(i0, std::integral_constant<int, 2>{});
     }
     if constexpr (kSplit > 1) {
 #pragma unroll
