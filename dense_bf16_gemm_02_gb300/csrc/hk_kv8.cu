@@ -134,12 +134,15 @@ hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, 
 
 std::mutex g_setup_mutex;
 bool g_setup[kMaxDevices] = {};
-int g_cluster_blocks[kMaxDevices][4] = {};     // blocks of clusters of 1, 2, 4 and 8 that run at a time
+int g_clusters[kMaxDevices][kMaxCluster + 1] = {};     // clusters of each size that run at a time
 
 template <int kD, typename T, int kWarps>
 cudaError_t setup_block() {
-    return cudaFuncSetAttribute(kv8_decode_block_kernel<kD, T, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                BlockGeometry<kD, kWarps>::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kv8_decode_block_kernel<kD, T, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         BlockGeometry<kD, kWarps>::kSmemBytes);
+    if (e == cudaSuccess && kWarps == kBlockWarps)       // (clusters of 16 are more than every device has to run)
+        e = cudaFuncSetAttribute(kv8_decode_block_kernel<kD, T, kWarps>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
 }
 
 template <int kD, typename T>
@@ -168,21 +171,21 @@ hk_status setup(int device) {
     if (e == cudaSuccess) e = setup_prefill<64>();
     if (e == cudaSuccess) e = setup_prefill<128>();
     // (a cluster needs its SMs in one part of the GPU: fewer blocks run at a time than there are SMs)
-    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+    for (int size = 1; size <= kMaxCluster && e == cudaSuccess; ++size) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
-        cfg.gridDim = dim3(8 * kSms);
+        cfg.gridDim = dim3(static_cast<unsigned>(size * kSms));
         cfg.blockDim = dim3(32 * kBlockWarps);
         cfg.dynamicSmemBytes = BlockGeometry<128, kBlockWarps>::kSmemBytes;
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(size);
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
         e = cudaOccupancyMaxActiveClusters(&clusters, kv8_decode_block_kernel<128, __nv_bfloat16, kBlockWarps>, &cfg);
-        g_cluster_blocks[device][i] = clusters << i;
+        g_clusters[device][size] = clusters;
     }
     if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring the cache attention kernels", e);
     g_setup[device] = true;
@@ -217,7 +220,12 @@ int pack_shift_of(int64_t group) {
     return shift;
 }
 
-// Tiles per warp up to which a unit is one block's (beyond, its tiles are spread over the whole GPU).
+// Tiles per warp up to which a unit is one block's or cluster's; beyond, all tiles are spread over the whole GPU and
+// a second kernel adds up. By the table's width, which the host knows. Both sides, D 128, 8 KV heads, in microseconds
+// by block or cluster and spread: 1 x 500 tokens 7.8 and 10.8, 1 x 32768 24.5 and 32.6, 8 x 4000 20.9 and 25.8,
+// 64 x 1000 29 and 40, 64 x 2000 49 and 61; of every length up to 2000 46.5 and 46.4: lengths that differ cost blocks
+// more, and longer tables leave more room for that, while what spreading costs (lengths are summed up before the
+// first load, sums go through memory: some 10) stays the same.
 constexpr int kBlockTiles = 32;
 
 // Warps of a block that has a unit to itself: as many as let one round of blocks hold all units.
@@ -581,9 +589,11 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     const int64_t unit_room = ceil_div(max_pages * p.page_size, kTileKeys);
     DecodePlan plan = {0, 1, static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), ceil_div(units * unit_room, kDecodeWarps)))};
     const int warps = block_warps(units);
-    if (warps == kBlockWarps)       // a cluster of blocks where one block to a unit leaves SMs idle
-        for (int i = 1; i < 4 && (units << i) <= g_cluster_blocks[device][i] && (kBlockWarps << (i - 1)) <= unit_room; ++i)
-            plan.cluster = 1 << i;
+    // a cluster of blocks where one block to a unit leaves SMs idle, as long as its warps have half a tile each (8
+    // units: 12 blocks, 32768 tokens 24.5 us; 8 blocks 30)
+    if (warps == kBlockWarps)
+        for (int size = 2; size <= kMaxCluster && units <= g_clusters[device][size] && kBlockWarps / 2 * size <= unit_room; ++size)
+            plan.cluster = size;
     if (unit_room <= int64_t(plan.cluster) * warps * kBlockTiles) plan.warps = warps;
     p.warps = plan.blocks * kDecodeWarps;
 

@@ -399,3 +399,15 @@ def test_workspace_contents_do_not_matter(hk, T, dtype):
                                     workspace.data_ptr(), size, torch.cuda.current_stream().cuda_stream) == hk.HK_OK
         assert _status(hk) == hk.HK_OK
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,group,lengths", [(1, 1, 8, [9000]), (1, 8, 4, [4100]), (2, 4, 16, [2500, 33]), (1, 4, 1, [2100]),
+                                               (5, 3, 2, [3000, 0, 1, 2000, 64])])
+def test_few_units_over_many_blocks(hk, D, B, H, group, lengths):
+    """Units that clusters of 2 to 16 blocks share, parts without tokens among them."""
+    import torch
+    rng = np.random.default_rng(31)
+    cache, table = _filled(hk, rng, lengths, H, D, 64)
+    q = _tokens(rng, B, 1, H * group, D, torch.bfloat16, 1)
+    _assert_attention(hk, q, cache, table, lengths, None, True)
