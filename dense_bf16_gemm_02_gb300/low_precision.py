@@ -10,9 +10,10 @@ torch's current device.
 
 A decoding step makes many calls of a few microseconds of GPU time each, so
 the way through Python is kept short: one check per condition, no context
-managers and no stream object unless a stream is given (measured on the GPU
-host: 17 -> 9 us for a one-token product, 23 -> 11 us for a one-token
-quantisation).
+managers and no stream object unless a stream is given. Measured in a loop on the
+GPU's host: a one-token quantisation 10 us (3 of them its Python, 3 the launch, the
+rest what the two and the allocator cost each other in caches), a one-token product
+9, an append 7, attention 14; a captured step pays none of it.
 """
 from __future__ import annotations
 

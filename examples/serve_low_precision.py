@@ -87,7 +87,8 @@ def run(hidden=4096, heads=32, kv_heads=8, head_dim=128, batch=8, prompt=512, st
         graph.replay()
         outputs.append(y.clone())
     torch.cuda.synchronize()
-    say(f"{batch} sequences, prompts of {counts.min().item()} to {counts.max().item()} tokens: {(time.perf_counter() - began) / steps * 1e6:.0f} us a step")
+    took = (time.perf_counter() - began) / steps
+    say(f"{batch} sequences, prompts of {counts.min().item()} to {counts.max().item()} tokens: {took * 1e6:.0f} us a step")
     if hk.hk_gemm_last_device_status(torch.cuda.current_device()) != hk.HK_OK:
         raise RuntimeError(hk.hk_gemm_last_error_string())
 
