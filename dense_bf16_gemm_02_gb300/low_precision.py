@@ -163,6 +163,8 @@ def quantize_fp4(x, format="mxfp4", global_scale=None, out=None, stream=None) ->
         out._scales_ptr = ptr = buffer.data_ptr()
         out._codes_ptr = ptr + size
         out.rows, out.cols, out.format = rows, cols, format
+    elif not isinstance(out, Fp4Matrix):
+        raise TypeError("out must be an Fp4Matrix")
     elif out.rows != rows or out.cols != cols or out.format != format:
         raise ValueError("out must have x's shape and the asked format")
     out.global_scale = global_scale
@@ -175,6 +177,8 @@ def quantize_fp4(x, format="mxfp4", global_scale=None, out=None, stream=None) ->
 
 def dequantize_fp4(q: Fp4Matrix, dtype=None, out=None, stream=None):
     """The values of a quantised matrix (default bf16)."""
+    if not isinstance(q, Fp4Matrix):
+        raise TypeError("q must be an Fp4Matrix (see quantize_fp4)")
     if out is None:
         out = _empty((q.rows, q.cols), dtype or _bf16, q._any, stream)
     elif tuple(out.shape) != q.shape or (dtype is not None and out.dtype != dtype) or not out.is_cuda:
@@ -241,13 +245,15 @@ class Kv8Cache:
                    torch.empty(shape[:2], dtype=_f32, device=device), torch.empty(shape[:2], dtype=_f32, device=device))
 
 
-def _tokens_shape(t, name, cache, heads):
+def _tokens_shape(t, name, cache, all_heads):
     """(B, T, heads) and packed strides of [B, T, heads, head_dim]."""
+    if not isinstance(cache, Kv8Cache):
+        raise TypeError("cache must be a Kv8Cache")
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
         raise TypeError(f"{name} must be a CUDA tensor [B, T, heads, head_dim]")
     B, T, H, D = t.shape
     sb, st, sh, sd = t.stride()
-    if D != cache.head_dim or (heads and H != heads):
+    if D != cache.head_dim or (all_heads and H != cache.heads):
         raise ValueError(f"{name} {tuple(t.shape)} does not fit the cache ({cache.heads} heads of {cache.head_dim})")
     if sd != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
@@ -275,8 +281,8 @@ def kv8_append(cache: Kv8Cache, k, v, block_table, starts, counts=None, stream=N
     that hold ``starts`` tokens; ``counts``: of each sequence's T tokens the first
     so many (None: all). ``block_table`` [B, max_pages], ``starts``, ``counts``
     [B]: int32. See hk_kv8_append for the scales."""
-    B, T, _, ks = _tokens_shape(k, "k", cache, cache.heads)
-    vb, vt, _, vs = _tokens_shape(v, "v", cache, cache.heads)
+    B, T, _, ks = _tokens_shape(k, "k", cache, True)
+    vb, vt, _, vs = _tokens_shape(v, "v", cache, True)
     if vb != B or vt != T or v.dtype != k.dtype:
         raise ValueError("v must have k's shape and type")
     ld, pages = _table(block_table, B)
@@ -300,7 +306,7 @@ def attention_kv8(q, cache: Kv8Cache, block_table, lengths, counts=None, causal=
     int32: valid queries of each sequence, None: T). Queries that see no token,
     or lie past ``counts``, give zeros. Returns o [B, T, Hq, head_dim] (and the
     fp32 log-sum-exp [B, T, Hq] with ``return_lse``). ``scale``: 1/sqrt(head_dim)."""
-    B, T, Hq, qs = _tokens_shape(q, "q", cache, 0)
+    B, T, Hq, qs = _tokens_shape(q, "q", cache, False)
     code = _type_code(q, "q")
     if code == _hk.HK_TYPE_FP32:
         raise TypeError("q must be bfloat16 or float16")
@@ -316,9 +322,9 @@ def attention_kv8(q, cache: Kv8Cache, block_table, lengths, counts=None, causal=
         out = _empty((B, T, Hq, cache.head_dim), q.dtype, q, stream)
         os = _strides(T * Hq * cache.head_dim, Hq * cache.head_dim, cache.head_dim)
     else:
-        if out.dtype != q.dtype or out.shape != q.shape:
+        if not isinstance(out, torch.Tensor) or out.dtype != q.dtype or out.shape != q.shape:
             raise ValueError("out must have q's shape and type")
-        os = _tokens_shape(out, "out", cache, 0)[3]
+        os = _tokens_shape(out, "out", cache, False)[3]
     lse = _empty((B, T, Hq), _f32, q, stream) if return_lse else None
     lib = _hk.load()
     size = lib.hk_attention_kv8_workspace_size(cache._ref, B, T, Hq, pages)

@@ -97,3 +97,13 @@ def test_python_refusals():
         hk.Fp4Matrix(torch.zeros(1, 16, dtype=torch.uint8), torch.zeros(2048, dtype=torch.uint8), 1, 1)
     with pytest.raises(TypeError):
         hk.gemm_fp4(None, None)
+
+
+def test_what_is_no_quantised_matrix_is_refused():
+    import torch
+
+    from dense_bf16_gemm_02_gb300 import dequantize_fp4, gemm_fp4
+    x = torch.zeros(4, 32)
+    for f in (lambda: dequantize_fp4(x), lambda: dequantize_fp4(None), lambda: gemm_fp4(x, x)):
+        with pytest.raises(TypeError):
+            f()

@@ -343,3 +343,11 @@ def test_product_tiles_of_fewer_tokens_than_there_are(hk, fmt, M, N, K, split):
     _assert_product(_forced(hk, a, b, h.HK_KERNEL_SINGLE_128x128, split), av, bv, K)
     _assert_product(_forced(hk, a, b, h.HK_KERNEL_SINGLE_128x128, 0), av, bv, K)
     _status_ok(hk)
+
+
+def test_out_that_is_no_quantised_matrix_is_refused(hk):
+    import torch
+    x = torch.zeros(4, 32, device="cuda")
+    for out in (x, (4, 32)):
+        with pytest.raises(TypeError):
+            hk.quantize_fp4(x, out=out)

@@ -134,3 +134,15 @@ def test_sizes_that_pass_64_bits_are_refused(lib):
             assert h.hk_attention_kv8_workspace_size(_cache(**bad), 2, 4000, 8, 4000) == 0, bad
     assert h.hk_attention_kv8_workspace_size(_cache(), 2, 1 << 40, 8, 4000) == 0
     assert h.hk_attention_kv8_workspace_size(_cache(), 1 << 40, 1, 8, 4000) == 0
+
+
+def test_what_is_no_cache_is_refused():
+    import torch
+
+    from dense_bf16_gemm_02_gb300 import attention_kv8, kv8_append
+    t, table, n = torch.zeros(1, 1, 1, 64), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for cache in (None, (t, t, t, t)):
+        with pytest.raises(TypeError):
+            kv8_append(cache, t, t, table, n)
+        with pytest.raises(TypeError):
+            attention_kv8(t, cache, table, n)
