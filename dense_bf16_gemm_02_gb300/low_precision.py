@@ -17,6 +17,7 @@ rest what the two and the allocator cost each other in caches), a one-token prod
 """
 from __future__ import annotations
 
+import operator
 import struct
 
 import torch
@@ -65,6 +66,12 @@ def _row_stride(t, name):
     return row
 
 
+def _read_only(slot, doc=None):
+    """A property without a setter over a slot: the pointers of an object go to the kernels as it was made with
+    them, so that another tensor or size needs another object."""
+    return property(operator.attrgetter(slot), doc=doc)
+
+
 def _checked_global_scale(g, format):
     if format != "nvfp4":
         raise ValueError("only nvfp4 has a global scale")
@@ -78,10 +85,12 @@ class Fp4Matrix:
 
     ``codes``: uint8 [rows, ld], two codes per byte; ``scales``: uint8, the
     block scales in 128×4 tiles; ``global_scale``: a float32 CUDA tensor of one
-    element (NVFP4 only) or None."""
+    element (NVFP4 only) or None. None of them can be set to another tensor or size."""
 
-    __slots__ = ("_codes", "_scales", "_buffer", "_codes_ptr", "_scales_ptr", "_ld", "rows", "cols", "format",
-                 "global_scale")
+    __slots__ = ("_codes", "_scales", "_buffer", "_codes_ptr", "_scales_ptr", "_ld", "_rows", "_cols", "_format",
+                 "_global_scale")
+    rows, cols, format = _read_only("_rows"), _read_only("_cols"), _read_only("_format")
+    global_scale = _read_only("_global_scale")
 
     def __init__(self, codes, scales, rows, cols, format="mxfp4", global_scale=None):
         if format not in _FORMATS:
@@ -95,9 +104,9 @@ class Fp4Matrix:
             raise ValueError("scales must be contiguous and hold hk_fp4_scales_size bytes")
         self._ld = _row_stride(codes, "codes")
         self._buffer = None
-        self._codes, self._scales, self.rows, self.cols, self.format = codes, scales, rows, cols, format
+        self._codes, self._scales, self._rows, self._cols, self._format = codes, scales, rows, cols, format
         self._codes_ptr, self._scales_ptr = codes.data_ptr(), scales.data_ptr()
-        self.global_scale = None if global_scale is None else _checked_global_scale(global_scale, format)
+        self._global_scale = None if global_scale is None else _checked_global_scale(global_scale, format)
 
     # (quantize_fp4 allocates once for both arrays; what nobody looks at needs no views)
     @property
@@ -127,7 +136,7 @@ class Fp4Matrix:
 
     @property
     def shape(self):
-        return (self.rows, self.cols)
+        return (self._rows, self._cols)
 
     def scale_matrix(self):
         """The block scales' bytes as [rows, ceil(cols / block)] (UE8M0 or E4M3)."""
@@ -162,16 +171,16 @@ def quantize_fp4(x, format="mxfp4", global_scale=None, out=None, stream=None) ->
         out._codes = out._scales = None
         out._scales_ptr = ptr = buffer.data_ptr()
         out._codes_ptr = ptr + size
-        out.rows, out.cols, out.format = rows, cols, format
+        out._rows, out._cols, out._format = rows, cols, format
     elif not isinstance(out, Fp4Matrix):
         raise TypeError("out must be an Fp4Matrix")
-    elif out.rows != rows or out.cols != cols or out.format != format:
+    elif out._rows != rows or out._cols != cols or out._format != format:
         raise ValueError("out must have x's shape and the asked format")
-    out.global_scale = global_scale
     st = _hk.load().hk_fp4_quantize(x.data_ptr(), code, rows, cols, ldx, out._codes_ptr, out._ld, out._scales_ptr, fmt,
                                     None if global_scale is None else global_scale.data_ptr(), _stream(stream, x))
     if st != HK_OK:
         raise HKError(st, "hk_fp4_quantize")
+    out._global_scale = global_scale
     return out
 
 
@@ -180,12 +189,12 @@ def dequantize_fp4(q: Fp4Matrix, dtype=None, out=None, stream=None):
     if not isinstance(q, Fp4Matrix):
         raise TypeError("q must be an Fp4Matrix (see quantize_fp4)")
     if out is None:
-        out = _empty((q.rows, q.cols), dtype or _bf16, q._any, stream)
+        out = _empty((q._rows, q._cols), dtype or _bf16, q._any, stream)
     elif tuple(out.shape) != q.shape or (dtype is not None and out.dtype != dtype) or not out.is_cuda:
         raise ValueError("out must be a CUDA tensor of the matrix's shape and the asked type")
-    g = q.global_scale
-    st = _hk.load().hk_fp4_dequantize(q._codes_ptr, q._ld, q._scales_ptr, _FORMATS[q.format],
-                                      None if g is None else g.data_ptr(), q.rows, q.cols, out.data_ptr(),
+    g = q._global_scale
+    st = _hk.load().hk_fp4_dequantize(q._codes_ptr, q._ld, q._scales_ptr, _FORMATS[q._format],
+                                      None if g is None else g.data_ptr(), q._rows, q._cols, out.data_ptr(),
                                       _type_code(out, "out"), _row_stride(out, "out"), _stream(stream, out))
     if st != HK_OK:
         raise HKError(st, "hk_fp4_dequantize")
@@ -196,9 +205,9 @@ def gemm_fp4(a: Fp4Matrix, b: Fp4Matrix, out=None, stream=None):
     """C = A·Bᵀ in bf16 for quantised A (M×K) and B (N×K) of one format."""
     if not isinstance(a, Fp4Matrix) or not isinstance(b, Fp4Matrix):
         raise TypeError("a and b must be Fp4Matrix (see quantize_fp4)")
-    if a.cols != b.cols or a.format != b.format:
-        raise ValueError(f"a [{a.rows}, {a.cols}] {a.format} and b [{b.rows}, {b.cols}] {b.format} do not match")
-    M, N = a.rows, b.rows
+    if a._cols != b._cols or a._format != b._format:
+        raise ValueError(f"a [{a._rows}, {a._cols}] {a._format} and b [{b._rows}, {b._cols}] {b._format} do not match")
+    M, N = a._rows, b._rows
     if out is None:
         out = _empty((M, N), _bf16, a._any, stream)
         ldc = N
@@ -206,8 +215,8 @@ def gemm_fp4(a: Fp4Matrix, b: Fp4Matrix, out=None, stream=None):
         if tuple(out.shape) != (M, N) or out.dtype != _bf16 or not out.is_cuda:
             raise ValueError("out must be a bfloat16 CUDA tensor [a.rows, b.rows]")
         ldc = _row_stride(out, "out")
-    ga, gb = a.global_scale, b.global_scale
-    st = _hk.load().hk_gemm_fp4(a._codes_ptr, a._scales_ptr, b._codes_ptr, b._scales_ptr, out.data_ptr(), M, N, a.cols, a._ld, b._ld, ldc, _FORMATS[a.format],
+    ga, gb = a._global_scale, b._global_scale
+    st = _hk.load().hk_gemm_fp4(a._codes_ptr, a._scales_ptr, b._codes_ptr, b._scales_ptr, out.data_ptr(), M, N, a._cols, a._ld, b._ld, ldc, _FORMATS[a._format],
                                 None if ga is None else ga.data_ptr(), None if gb is None else gb.data_ptr(),
                                 _stream(stream, out))
     if st != HK_OK:
@@ -220,9 +229,12 @@ class Kv8Cache:
 
     ``k``, ``v``: uint8 [pages, heads, page_size, head_dim]; ``k_scale``,
     ``v_scale``: float32 [pages, heads]; all contiguous CUDA tensors.
-    ``Kv8Cache.empty`` makes them."""
+    ``Kv8Cache.empty`` makes them. None of them can be set to another tensor: a
+    larger pool is a new Kv8Cache over tensors that the old ones were copied to."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "page_size", "head_dim", "_ref")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_pages", "_heads", "_page_size", "_head_dim", "_ref")
+    k, v, k_scale, v_scale = (_read_only(n) for n in __slots__[:4])
+    pages, heads, page_size, head_dim = (_read_only(n) for n in __slots__[4:8])
 
     def __init__(self, k, v, k_scale, v_scale):
         for t, dtype in ((k, _u8), (v, _u8), (k_scale, _f32), (v_scale, _f32)):
@@ -233,8 +245,8 @@ class Kv8Cache:
         shape = tuple(k.shape)
         if len(shape) != 4 or tuple(v.shape) != shape or tuple(k_scale.shape) != shape[:2] or tuple(v_scale.shape) != shape[:2]:
             raise ValueError("k and v must be [pages, heads, page_size, head_dim], the scales [pages, heads]")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.heads, self.page_size, self.head_dim = shape
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        self._pages, self._heads, self._page_size, self._head_dim = shape
         self._ref = _cache_struct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape, 0)
 
     @classmethod
@@ -253,8 +265,8 @@ def _tokens_shape(t, name, cache, all_heads):
         raise TypeError(f"{name} must be a CUDA tensor [B, T, heads, head_dim]")
     B, T, H, D = t.shape
     sb, st, sh, sd = t.stride()
-    if D != cache.head_dim or (all_heads and H != cache.heads):
-        raise ValueError(f"{name} {tuple(t.shape)} does not fit the cache ({cache.heads} heads of {cache.head_dim})")
+    if D != cache._head_dim or (all_heads and H != cache._heads):
+        raise ValueError(f"{name} {tuple(t.shape)} does not fit the cache ({cache._heads} heads of {cache._head_dim})")
     if sd != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
     return B, T, H, _strides(sb, st, sh)
@@ -319,8 +331,8 @@ def attention_kv8(q, cache: Kv8Cache, block_table, lengths, counts=None, causal=
     if counts is not None:
         _check_vector(counts, "counts", B)
     if out is None:
-        out = _empty((B, T, Hq, cache.head_dim), q.dtype, q, stream)
-        os = _strides(T * Hq * cache.head_dim, Hq * cache.head_dim, cache.head_dim)
+        out = _empty((B, T, Hq, cache._head_dim), q.dtype, q, stream)
+        os = _strides(T * Hq * cache._head_dim, Hq * cache._head_dim, cache._head_dim)
     else:
         if not isinstance(out, torch.Tensor) or out.dtype != q.dtype or out.shape != q.shape:
             raise ValueError("out must have q's shape and type")
