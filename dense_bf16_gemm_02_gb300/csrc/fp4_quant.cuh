@@ -139,6 +139,12 @@ __device__ __forceinline__ Spread8<T> load_spread(const T* row, int64_t col, int
     return r;
 }
 
+// A global scale below 2^-60 is taken times 2^64 (kLift), and so is what meets it, so that s·g and its reciprocal
+// stay within fp32's normal numbers (for s·g < 2^-128 the reciprocal alone would be infinite). Powers of two:
+// every code and scale is the one that fp32 without a least exponent would give.
+constexpr float kSmallScale = 0x1p-60f;
+constexpr float kLift = 0x1p64f;
+
 // ------------------------------------------------------------- quantise --
 
 // NVFP4: what the scale bytes of a matrix with global scale g mean to the
@@ -153,9 +159,9 @@ __device__ __forceinline__ void fill_reciprocals(float (&table)[128], float g) {
 }
 
 // Eight values of a block to codes; the block's scale byte. `six_g`, `per_six_g`:
-// 6·g and its reciprocal, both rounded to nearest.
+// 6·g and its reciprocal, both rounded to nearest; `lift`: kLift where g was lifted, else 1.
 template <int kFmt>
-__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], float six_g, float per_six_g, const float* reciprocals,
+__device__ __forceinline__ uint32_t quantize8(float (&v)[8], float six_g, float per_six_g, float lift, const float* reciprocals,
                                               uint32_t& byte) {
     float m = amax3(v[0], v[1], v[2]);
     m = amax3(m, v[3], v[4]);
@@ -171,6 +177,11 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], float six_g, 
     } else {
         // m / (6·g) to nearest by one correction of m · (1 / (6·g)) with its exact remainder (P. Markstein,
         // IBM J. Res. Dev. 34, 1990); where that leaves fp32's range the quotient is 0 or above 448 either way
+        if (lift != 1.0f) {              // (the same in every thread)
+            m = __fmul_rn(m, lift);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], lift);
+        }
         const float q0 = __fmul_rn(m, per_six_g);
         const float q = __fmaf_rn(__fmaf_rn(-q0, six_g, m), per_six_g, q0);
         byte = e4m3_of(isfinite(q) ? q : q0);
@@ -231,9 +242,13 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
     griddep_launch_dependents();
     griddep_wait();                  // launched early behind the kernel that may have written x
     const uint32_t lane = threadIdx.x;
-    float six_g = 6.0f, per_six_g = 0.0f;
+    float six_g = 6.0f, per_six_g = 0.0f, lift = 1.0f;
     if constexpr (kFmt == kNvfp4) {
-        const float g = global_scale != nullptr ? *global_scale : 1.0f;
+        float g = global_scale != nullptr ? *global_scale : 1.0f;
+        if (g < kSmallScale) {
+            lift = kLift;
+            g = __fmul_rn(g, kLift);
+        }
         six_g = __fmul_rn(6.0f, g);
         per_six_g = fminf(__fdiv_rn(1.0f, six_g), 3.4028235e38f);   // (finite: 0 times it is 0)
         fill_reciprocals(reciprocals, g);
@@ -265,7 +280,7 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
             for (int i = 0; i < kSpanChunks; ++i) {
                 float v[8];
                 widen8<T>(raw[i], v);
-                *reinterpret_cast<uint32_t*>(out + i * (kChunkCols / 2)) = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
+                *reinterpret_cast<uint32_t*>(out + i * (kChunkCols / 2)) = quantize8<kFmt>(v, six_g, per_six_g, lift, reciprocals, byte[i]);
             }
         } else {
             Spread8<T> raw[kSpanChunks];
@@ -280,7 +295,7 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
                 __syncwarp();
                 float v[8];
                 memcpy(v, buf + lane * 8, sizeof v);
-                const uint32_t packed = quantize8<kFmt>(v, six_g, per_six_g, reciprocals, byte[i]);
+                const uint32_t packed = quantize8<kFmt>(v, six_g, per_six_g, lift, reciprocals, byte[i]);
                 if ((c0 + i) * kChunkCols + lane * 8 < code_cols)
                     *reinterpret_cast<uint32_t*>(dst + (c0 + i) * (kChunkCols / 2)) = packed;
             }
@@ -291,11 +306,16 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
 
 // ----------------------------------------------------------- dequantise --
 
-// Eight codes times their scale, rounded once to T.
+// Eight codes times their scale (lifted, with `lower` 2^-64, or not, with 1), rounded once to T.
 template <typename T>
-__device__ __forceinline__ void dequantize8(uint32_t codes, float scale, T (&e)[8]) {
+__device__ __forceinline__ void dequantize8(uint32_t codes, float scale, float lower, T (&e)[8]) {
     float v[8];
     unpack_e2m1x8(codes, v);
+    if (lower != 1.0f) {                 // (the same in every thread; v·scale does not fit fp32's normal numbers)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], scale), lower);
+        scale = 1.0f;
+    }
     const uint64_t s2 = f32x2(scale, scale);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -320,7 +340,11 @@ dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
     griddep_launch_dependents();
     griddep_wait();                  // launched early behind the kernel that may have written the codes
     const uint32_t lane = threadIdx.x;
-    const float g = kFmt == kNvfp4 && global_scale != nullptr ? *global_scale : 1.0f;
+    float g = kFmt == kNvfp4 && global_scale != nullptr ? *global_scale : 1.0f, lower = 1.0f;
+    if (kFmt == kNvfp4 && g < kSmallScale) {
+        g = __fmul_rn(g, kLift);
+        lower = 1.0f / kLift;
+    }
     const int64_t chunks = (cols + kChunkCols - 1) / kChunkCols;
     const int64_t whole = vec ? cols / kChunkCols : 0;
     const int64_t code_cols = (cols + 31) / 32 * 32;
@@ -349,7 +373,7 @@ dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
 #pragma unroll
             for (int i = 0; i < kSpanChunks; ++i) {
                 T e[8];
-                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
+                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), kFmt == kNvfp4 ? lower : 1.0f, e);
                 uint4 o[sizeof(T) / 2];
                 memcpy(o, e, sizeof o);
 #pragma unroll
@@ -370,7 +394,7 @@ dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
             for (int i = 0; i < kSpanChunks; ++i) {
                 if (i >= n) break;
                 T e[8];
-                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
+                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), kFmt == kNvfp4 ? lower : 1.0f, e);
                 __syncwarp();
                 memcpy(buf + lane * 8, e, sizeof e);
                 __syncwarp();
