@@ -24,9 +24,12 @@
 // unit. Codes become f16 exactly, two per conversion. A query row is scaled by
 // a power of two so that its largest magnitude lies in [2^10, 2^11): exact for
 // every element down to 2^-24 of that, and the others err by at most 2^-35 of
-// it. P is rounded to f16 (11 bits), its sum is kept unrounded in fp32. The
-// page's scale multiplies the scores of its tokens and, for V, the sums of each
-// tile's products before they join the running output, all in fp32.
+// it. P is taken times 2^15 and rounded to f16: 11 bits down to 2^-29 of the
+// row's largest weight, an absolute 2^-40 of it below (at P <= 1 f16's subnormal
+// numbers began at 2^-14, and a tail of many small weights lost its mass while the
+// sum counted it). The sum is kept unrounded in fp32. The page's scale multiplies
+// the scores of its tokens and, for V and with the 2^-15, the sums of each tile's
+// products before they join the running output, all in fp32.
 //
 // Column orders. A thread's fragment registers need pairs along K: the columns
 // of an operand may be in any order as long as both operands agree, so a
@@ -50,6 +53,8 @@ constexpr int kRows = 16;              // query rows of a unit
 constexpr int kTileKeys = 32;
 constexpr int kDecodeWarps = 4;        // warps of a block, each on its own
 constexpr int kMaxBatch = 1024;        // sequences of one launch
+constexpr float kWeightShift = 15.0f;  // P is held times 2^15
+constexpr float kWeightUnit = 0x1p-15f;
 
 template <int kD>
 struct DecodeGeometry {
@@ -221,9 +226,9 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
             return pg >= 0 ? scale[static_cast<int64_t>(pg) * p.Hkv + h] : 0.0f;
         };
         w.ks0 = scale_of(p.k_scale, w.page0);
-        w.vs0 = scale_of(p.v_scale, w.page0);
+        w.vs0 = scale_of(p.v_scale, w.page0) * kWeightUnit;
         w.ks1 = two ? scale_of(p.k_scale, w.page1) : w.ks0;
-        w.vs1 = two ? scale_of(p.v_scale, w.page1) : w.vs0;
+        w.vs1 = two ? scale_of(p.v_scale, w.page1) * kWeightUnit : w.vs0;
     };
     const int seen = key_end > 0 ? last : first;      // a unit that sees nothing has no tile to read
     int base_tile = first, next = first;              // the current window's first tile, the next tile to load
@@ -389,8 +394,8 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
             m[i] = now;
             l[i] *= alpha[i];
         }
-        const float sub0 = m[0] == -INFINITY ? 0.0f : m[0], sub1 = m[1] == -INFINITY ? 0.0f : m[1];
-        uint32_t pf[4][2];               // P of tile j, rows g and g + 8, as f16 pairs
+        const float sub0 = m[0] == -INFINITY ? 0.0f : m[0] - kWeightShift, sub1 = m[1] == -INFINITY ? 0.0f : m[1] - kWeightShift;
+        uint32_t pf[4][2];               // P · 2^15 of tile j, rows g and g + 8, as f16 pairs
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float p0 = ex2_approx(sc[j][0] - sub0), p1 = ex2_approx(sc[j][1] - sub0);
@@ -455,6 +460,7 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
     for (int i = 0; i < 2; ++i) {            // the rows' sums over their four threads
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        l[i] *= kWeightUnit;
     }
     return ok;
 }
