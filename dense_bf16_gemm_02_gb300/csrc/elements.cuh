@@ -77,4 +77,7 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
     return __low2float(*reinterpret_cast<const __half2*>(&h));
 }
 
+// 0xFF in the place of each of four E4M3 codes that is a NaN, 0 elsewhere.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
+
 }  // namespace hk

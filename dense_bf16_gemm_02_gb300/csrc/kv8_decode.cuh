@@ -342,7 +342,59 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
             const int from = key_end - key0;
             for (int i = static_cast<int>(lane); i < (kTileKeys - from) * (kD / 16); i += 32)
                 st_shared_v4(vb + static_cast<uint32_t>(from * kD + 16 * i), 0, 0, 0, 0);   // (whole rows: any order inside)
+            fence_proxy_async_smem();        // before a load into the stage may follow
             __syncwarp();
+        }
+        const bool masked = key0 + kTileKeys > all_see;
+        if (masked) {
+            // a token that some rows see and others do not: if its V holds NaN codes, a weight of 0 does not keep them
+            // out of the others' sums. They go to the rows that see it here, and are cleared. (Rows that see
+            // nothing need no care: what is stored for them does not come from the sums.)
+            const int some = min(limit[0] > 0 ? limit[0] : 0x7FFFFFFF, limit[1] > 0 ? limit[1] : 0x7FFFFFFF);
+            if (__reduce_min_sync(0xffffffffu, some) < min(key0 + kTileKeys, key_end)) {
+                const uint32_t row = vb + lane * kD;         // (a lane looks at a token: whole rows, any order inside)
+                bool nan = false;
+#pragma unroll 1
+                for (int i = 0; i < kD / 16; ++i) {
+                    const uint4 x = ld_shared_v4(row + 16 * i);
+                    nan = nan || ((nan_codes(x.x) | nan_codes(x.y)) | (nan_codes(x.z) | nan_codes(x.w))) != 0;
+                }
+                uint32_t tokens = __ballot_sync(0xffffffffu, nan);
+#pragma unroll 1
+                for (; tokens != 0; tokens &= tokens - 1) {
+                    const int at = __ffs(static_cast<int>(tokens)) - 1;
+                    const float add[2] = {key0 + at < limit[0] ? NAN : 0.0f, key0 + at < limit[1] ? NAN : 0.0f};
+                    // this thread's output columns: kD / 8 consecutive ones of either half
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[kD / 32];
+                        if constexpr (kD == 128) {
+                            const uint4 x = ld_shared_v4(vb + chunk_offset<kD>(at, 2 * c + e));
+                            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                        } else {
+                            const uint2 x = ld_shared_v2(vb + chunk_offset<kD>(at, c) + 8 * e);
+                            w[0] = x.x; w[1] = x.y;
+                        }
+#pragma unroll
+                        for (int j = 0; j < kNTiles; ++j) {
+                            if (nan_codes(w[j >> 2]) >> (8 * (j & 3)) & 1u) {
+                                o[j][e] += add[0];
+                                o[j][2 + e] += add[1];
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (nan) {
+#pragma unroll 1
+                    for (int i = 0; i < kD / 16; ++i) {
+                        const uint4 x = ld_shared_v4(row + 16 * i);
+                        st_shared_v4(row + 16 * i, x.x & ~nan_codes(x.x), x.y & ~nan_codes(x.y), x.z & ~nan_codes(x.z), x.w & ~nan_codes(x.w));
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+            }
         }
 
         // ---- scores of 32 tokens: key tiles of 8, column g of tile j is token 8 j + g
@@ -367,7 +419,6 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
         }
         // ---- softmax of rows g (elements 0, 1) and g + 8 (2, 3); columns 2 c, 2 c + 1 of each tile
         float mx[2] = {-INFINITY, -INFINITY};
-        const bool masked = key0 + kTileKeys > all_see;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float ks = j < 2 ? tks0 : tks1;
@@ -452,7 +503,6 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
                 }
             }
         }
-        if (key0 + kTileKeys > key_end) fence_proxy_async_smem();   // the cleared rows, before a load may follow
         __syncwarp();                    // every lane has read the stage
         if (next < seen) feed();
     }
@@ -561,11 +611,12 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             const int head = h * p.group + row % p.group;
             float v[kOwn];
             // columns 2 c and 2 c + 1 of output tile j: dimensions 2 c (D / 8) + j and (2 c + 1)(D / 8) + j
-            const float mul = !whole ? 1.0f : l[i] > 0.0f || l[i] != l[i] ? 1.0f / l[i] : 0.0f;
+            const bool any = l[i] > 0.0f || l[i] != l[i];        // (a row that sees nothing may hold NaN sums)
+            const float mul = !whole ? 1.0f : 1.0f / l[i];
 #pragma unroll
             for (int j = 0; j < kNTiles; ++j) {
-                v[j] = o[j][2 * i] * mul;
-                v[kNTiles + j] = o[j][2 * i + 1] * mul;
+                v[j] = any ? o[j][2 * i] * mul : 0.0f;
+                v[kNTiles + j] = any ? o[j][2 * i + 1] * mul : 0.0f;
             }
             if (whole) {
                 if (t < p.T) {
@@ -573,7 +624,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     store_row<T, kOwn>(dst, v, p.vec_o != 0);
                     if (p.lse != nullptr && c == 0)
                         p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] =
-                            l[i] > 0.0f || l[i] != l[i] ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+                            any ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
                 }
             } else if (t < p.T) {
                 const int64_t at_row = static_cast<int64_t>(slot) * kRows + g + 8 * i;
