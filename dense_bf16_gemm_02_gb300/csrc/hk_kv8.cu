@@ -422,6 +422,7 @@ hk_status prefill(const void* Q, const int64_t q_strides[3], const hk_kv8_cache*
         if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache's conversion", e);
         if (c->head_dim == 64) launch_prefill<64>(tq, tk, tv, p, sms, st);
         else launch_prefill<128>(tq, tk, tv, p, sms, st);
+        kv8_nan_values_kernel<<<dim3(static_cast<unsigned>(c->heads), static_cast<unsigned>(n)), 256, 0, st>>>(w, p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the cache attention", e);
     }

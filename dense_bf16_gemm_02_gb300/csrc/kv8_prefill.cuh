@@ -15,6 +15,10 @@
 // Rows of a tile are `pack` query heads of one KV head for each of 128 / pack
 // tokens, so that the heads of a group share each K/V block that is loaded and a
 // tile spans few tokens (its causal edge wastes less).
+//
+// A value that is NaN would reach every row of a block of 128 tokens through weights of 0,
+// so the pass writes 0 in its place and notes that there was one; a last kernel, which
+// otherwise ends at once, then puts NaN into the rows that see such a token.
 #pragma once
 
 #include <cstdint>
@@ -98,6 +102,10 @@ struct CachedItems {
     }
 };
 
+// The status word that says that a widened value was NaN, in this or an earlier call (it is never taken back: calls
+// on other streams may still be between the two kernels).
+constexpr int kNanSeen = 2;
+
 struct WidenParams {
     const uint8_t* codes[2];       // keys, values
     const float* scale[2];
@@ -145,7 +153,15 @@ kv8_widen_kernel(const WidenParams p) {
         if (page >= 0 && first + (at >> chunk_shift) < len) {
             const float s = (kv ? p.scale[1] : p.scale[0])[src];
             const uint4 x = __ldg(reinterpret_cast<const uint4*>((kv ? p.codes[1] : p.codes[0]) + src * p.page_size * p.D) + at);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            if (kv == 1) {
+                const uint32_t nan[4] = {nan_codes(w[0]), nan_codes(w[1]), nan_codes(w[2]), nan_codes(w[3])};
+                if (((nan[0] | nan[1]) | (nan[2] | nan[3])) != 0) {
+                    *reinterpret_cast<volatile uint32_t*>(p.status + kNanSeen) = 1u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] &= ~nan[k];
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 uint32_t f;
@@ -157,6 +173,39 @@ kv8_widen_kernel(const WidenParams p) {
         uint4* const out = reinterpret_cast<uint4*>((kv ? p.out[1] : p.out[0]) + dst * p.D) + 2 * at;
         out[0] = make_uint4(o[0], o[1], o[2], o[3]);
         out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// After the attention kernel: NaN into every output that a NaN value belongs to; block (head, sequence). The first
+// token that holds a NaN, for each dimension, says which rows see one.
+static __global__ void __launch_bounds__(256)
+kv8_nan_values_kernel(const WidenParams w, const PrefillParams p) {
+    if (*reinterpret_cast<volatile uint32_t*>(w.status + kNanSeen) == 0u) return;
+    __shared__ int first[128];
+    const int h = static_cast<int>(blockIdx.x), b = static_cast<int>(blockIdx.y);
+    const CachedItems::Seq s = CachedItems::seq(p, b);
+    if (threadIdx.x < 128) first[threadIdx.x] = 0x7FFFFFFF;
+    __syncthreads();
+    const int64_t chunks = static_cast<int64_t>(s.len) * (w.D / 16);      // 16 codes each
+    bool any = false;
+    for (int64_t i = threadIdx.x; i < chunks; i += 256) {
+        const int j = static_cast<int>(i / (w.D / 16)), d = static_cast<int>(i % (w.D / 16)) * 16;
+        const int64_t page = w.table[b * w.table_stride + j / w.page_size];
+        if (page < 0 || page >= w.num_pages) continue;
+        const uint4 x = *reinterpret_cast<const uint4*>(w.codes[1] + ((page * w.Hkv + h) * w.page_size + j % w.page_size) * w.D + d);
+        const uint32_t nan[4] = {nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w)};
+        if (((nan[0] | nan[1]) | (nan[2] | nan[3])) == 0) continue;
+        any = true;
+        for (int k = 0; k < 16; ++k)
+            if (nan[k >> 2] >> (8 * (k & 3)) & 1u) atomicMin(&first[d + k], j);
+    }
+    if (!__syncthreads_or(any)) return;
+    const int64_t outputs = static_cast<int64_t>(s.count) * p.group * w.D;
+    for (int64_t i = threadIdx.x; i < outputs; i += 256) {
+        const int d = static_cast<int>(i % w.D), row = static_cast<int>(i / w.D);
+        const int t = row / p.group, head = h * p.group + row % p.group;
+        const int end = p.causal ? max(0, s.len - s.count + t + 1) : s.len;
+        if (first[d] < end) p.O[b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + d] = 0x7FFFu;
     }
 }
 

@@ -58,3 +58,21 @@ def test_few_queries_that_do_not_see_a_token_are_not_touched_by_it(hk, D, wide, 
 def test_few_queries_past_the_count_and_before_the_first_token_stay_zero(hk, D, wide, causal):  # noqa: F811
     lengths, counts = [200, 3, 100], [2, 6, 1]
     _check(hk, 3, 2, 4, 6, D, 32, lengths, counts, causal, [(0, 198, 0, 5), (1, 1, 1, 9), (2, 50, 0, 63)], wide)
+
+
+# (sizes at which a call runs on the attention-forward kernel: many rows of many heads)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group,T,n", [(8, 100, 300), (3, 300, 400), (1, 700, 700)])
+def test_many_queries_that_do_not_see_a_token_are_not_touched_by_it(hk, D, group, T, n):  # noqa: F811
+    spots = [(0, n - 1, 0, 3), (0, n - 40, 1, D - 2), (0, n - 40, 1, D - 1), (1, n - T // 2, 7, 0), (1, 5, 2, 17)]
+    _check(hk, 2, 8, group, T, D, 64, [n, n], None, True, spots, weight=2.0 ** -8)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_queries_past_the_count_and_before_the_first_token_stay_zero(hk, causal):  # noqa: F811
+    _check(hk, 3, 8, 4, 150, 128, 32, [200, 60, 3], [70, 150, 1], causal, [(0, 198, 0, 5), (1, 1, 1, 9), (1, 59, 3, 8), (2, 2, 7, 63)],
+           weight=2.0 ** -8)
+
+
+def test_many_queries_without_nan_after_a_call_with_it(hk):  # noqa: F811
+    _check(hk, 2, 8, 8, 100, 64, 16, [300, 90], None, True, [], weight=2.0 ** -8)
