@@ -494,18 +494,48 @@ extern "C" hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, con
     return e == cudaSuccess ? HK_OK : cuda_fail(HK_ERR_LAUNCH, "launching the cache append", e);
 }
 
+namespace {
+
+bool attention_shape_ok(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages) {
+    return c && cache_shape_ok(c) && table_width_ok(max_pages, c->page_size) && B > 0 && B <= kLimit && T > 0 && Hq >= c->heads &&
+           Hq <= kLimit && T <= kLimit / 16 / (Hq / c->heads);
+}
+
+// Bytes for the few-row kernels: none where every unit is a block's or a cluster's.
+size_t few_rows_bytes(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages) {
+    const int64_t row_tiles = ceil_div(T * (Hq / c->heads), kRows);
+    const int64_t units = decode_batch(B, c->heads, row_tiles) * c->heads * row_tiles;
+    if (ceil_div(max_pages * c->page_size, kTileKeys) <= block_warps(units) * kBlockTiles) return 0;
+    return decode_workspace(c, B, T, Hq).total;
+}
+
+bool rows_aligned(const void* ptr, const int64_t strides[3]) {
+    return aligned(ptr, 16) && strides[0] % 8 == 0 && strides[1] % 8 == 0 && strides[2] % 8 == 0;
+}
+
+// Can the tensor-core kernel run the call? It takes bf16 rows that TMA can read (aligned, and not one row for
+// several places) and writes 16 bytes at a time.
+bool many_rows_can(const void* Q, int32_t type, const int64_t q_strides[3], const void* O, const int64_t o_strides[3], int64_t B,
+                   int64_t T, int64_t Hq) {
+    return type == HK_TYPE_BF16 && rows_aligned(Q, q_strides) && rows_aligned(O, o_strides) && (B == 1 || q_strides[0] > 0) &&
+           (T == 1 || q_strides[1] > 0) && (Hq == 1 || q_strides[2] > 0);
+}
+
+}  // namespace
+
 extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                   int64_t max_pages) {
-    if (!cache || !cache_shape_ok(cache) || !table_width_ok(max_pages, cache->page_size) || B <= 0 || B > kLimit || T <= 0 ||
-        Hq < cache->heads || Hq > kLimit || T > kLimit / 16 / (Hq / cache->heads))
-        return 0;
-    size_t split = decode_workspace(cache, B, T, Hq).total;
-    // (blocks that have a unit to themselves need none)
-    const int64_t row_tiles = ceil_div(T * (Hq / cache->heads), kRows);
-    const int64_t units = decode_batch(B, cache->heads, row_tiles) * cache->heads * row_tiles;
-    if (ceil_div(max_pages * cache->page_size, kTileKeys) <= block_warps(units) * kBlockTiles) split = 0;
-    if (!many_rows(B, T, Hq, cache->heads)) return split;
-    return std::max(split, prefill_workspace(cache, B, max_pages).total);
+    if (!attention_shape_ok(cache, B, T, Hq, max_pages)) return 0;
+    const size_t few = few_rows_bytes(cache, B, T, Hq, max_pages);
+    return many_rows(B, T, Hq, cache->heads) ? std::max(few, prefill_workspace(cache, B, max_pages).total) : few;
+}
+
+extern "C" size_t hk_attention_kv8_workspace_size_ex(const void* Q, int32_t type, const int64_t q_strides[3],
+                                                     const hk_kv8_cache* cache, int64_t max_pages, const void* O,
+                                                     const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq) {
+    if (!attention_shape_ok(cache, B, T, Hq, max_pages) || !q_strides || !o_strides) return 0;
+    const bool many = many_rows(B, T, Hq, cache->heads) && many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq);
+    return many ? prefill_workspace(cache, B, max_pages).total : few_rows_bytes(cache, B, T, Hq, max_pages);
 }
 
 extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
@@ -529,7 +559,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if (T > kLimit / 16 / group || ceil_div(T * group, kRows) * (ceil_div(max_pages * cache->page_size, kTileKeys) + 1) > kLimit)
         return fail(HK_ERR_INVALID_ARG, "problem too large");
     const DecodeWorkspace ws = decode_workspace(cache, B, T, Hq);
-    const size_t need = hk_attention_kv8_workspace_size(cache, B, T, Hq, max_pages);
+    const size_t need = hk_attention_kv8_workspace_size_ex(Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
     if (!aligned(workspace, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
@@ -540,14 +570,10 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if ((s = hk_host::status_word(device, &status)) != HK_OK) return s;
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     if ((s = hk_host::tensor_map_encoder(&enc)) != HK_OK) return s;
-    const bool vec_q = aligned(Q, 16) && q_strides[0] % 8 == 0 && q_strides[1] % 8 == 0 && q_strides[2] % 8 == 0;
-    const bool vec_o = aligned(O, 16) && o_strides[0] % 8 == 0 && o_strides[1] % 8 == 0 && o_strides[2] % 8 == 0;
     const float scale_log2 = static_cast<float>(
         1.4426950408889634 * (scale != 0.0f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->head_dim))));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // (the tensor-core kernel takes bf16 rows that TMA can read: aligned, and not one row for several places)
-    const bool spread = (B == 1 || q_strides[0] > 0) && (T == 1 || q_strides[1] > 0) && (Hq == 1 || q_strides[2] > 0);
-    if (many_rows(B, T, Hq, cache->heads) && type == HK_TYPE_BF16 && vec_q && vec_o && spread)
+    if (many_rows(B, T, Hq, cache->heads) && many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq))
         return prefill(Q, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse, B, T, Hq,
                        causal, scale_log2, workspace, status, timeout_ns, enc, sms, st);
     CUtensorMap tk, tv;
@@ -561,8 +587,8 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.o_stride_b = o_strides[0];
     p.o_stride_t = o_strides[1];
     p.o_stride_h = o_strides[2];
-    p.vec_q = vec_q;
-    p.vec_o = vec_o;
+    p.vec_q = rows_aligned(Q, q_strides);
+    p.vec_o = rows_aligned(O, o_strides);
     p.k_scale = cache->k_scale;
     p.v_scale = cache->v_scale;
     p.table_stride = table_stride;

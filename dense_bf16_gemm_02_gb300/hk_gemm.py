@@ -62,6 +62,7 @@ EXPORTED = (
     "hk_attention_fwd", "hk_attention_fwd_ex", "hk_gemm_mxfp8", "hk_gemm_mxfp8_ex", "hk_gemm_mxfp8_workspace_size",
     "hk_fp4_scales_size", "hk_fp4_quantize", "hk_fp4_dequantize", "hk_gemm_fp4", "hk_gemm_fp4_ex",
     "hk_kv8_append", "hk_attention_kv8", "hk_attention_kv8_ex", "hk_attention_kv8_workspace_size",
+    "hk_attention_kv8_workspace_size_ex",
 )
 
 
@@ -183,6 +184,8 @@ def load() -> ctypes.CDLL:
         lib.hk_attention_kv8_ex.restype = I32
         lib.hk_attention_kv8_workspace_size.argtypes = [CP, I64, I64, I64, I64]
         lib.hk_attention_kv8_workspace_size.restype = SZ
+        lib.hk_attention_kv8_workspace_size_ex.argtypes = [P, I32, P, CP, I64, P, P, I64, I64, I64]
+        lib.hk_attention_kv8_workspace_size_ex.restype = SZ
         _lib = lib
         return lib
 

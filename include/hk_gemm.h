@@ -492,7 +492,7 @@ hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, const void* V,
  * is bf16 with rows that are 16-byte aligned; fp16 and other rows run on the
  * few-row kernel whatever their number (2048 tokens x 32 heads against 16384: 840 us
  * and 4180 us).
- * `workspace`: device memory of hk_attention_kv8_workspace_size bytes, 256-byte
+ * `workspace`: device memory of hk_attention_kv8_workspace_size(_ex) bytes, 256-byte
  * aligned, scratch of this call (calls that overlap on the GPU must not share
  * it). Asynchronous on `stream`; a bounded wait that runs out is reported by
  * hk_gemm_last_device_status. */
@@ -512,10 +512,18 @@ hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strid
                               void* workspace, size_t workspace_bytes, uint32_t flags, uint64_t timeout_ns,
                               void* stream);
 
-/* Bytes of workspace hk_attention_kv8 needs: 0 for an empty problem and for few
- * query rows over short block tables; else 20 MB, or (many query rows) the bf16
- * keys and values of as many sequences as fit 512 MB, of one at least. */
+/* Bytes of workspace that are enough for hk_attention_kv8 whatever the type and the
+ * strides are: 0 for an empty problem and for few query rows over short block
+ * tables; else 10 to 37 MB, or (many query rows) the bf16 keys and values of as many
+ * sequences as fit 512 MB, of one at least. */
 size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq, int64_t max_pages);
+
+/* Bytes that the call with these arguments needs, and asks for: those of the kernels
+ * that it runs on (fp16 queries and rows that TMA cannot read need no bf16 keys and
+ * values). Q and O are looked at for their alignment only. */
+size_t hk_attention_kv8_workspace_size_ex(const void* Q, int32_t type, const int64_t q_strides[3],
+                                          const hk_kv8_cache* cache, int64_t max_pages, const void* O,
+                                          const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq);
 
 /* Static description of a status code. */
 const char* hk_status_string(hk_status status);

@@ -1,0 +1,38 @@
+"""The workspace of the cache attention is what the kernels that run the call need."""
+import ctypes
+
+import pytest
+
+from test_kv8_cpu import P, S3, _cache, lib  # noqa: F401  (a fixture)
+
+
+def _call(lib, c, size, type=0, Q=P, qs=S3, O=P, os=S3, B=2, T=4000, Hq=8, pages=4000):  # noqa: F811
+    return lib.hk_attention_kv8_ex(Q, type, qs, ctypes.byref(c), P, pages, pages, P, None, O, os, None, B, T, Hq, 1, 0.0, P,
+                                   size, 0, 0, None)
+
+
+def _size(lib, c, type=0, Q=P, qs=S3, O=P, os=S3, B=2, T=4000, Hq=8, pages=4000):  # noqa: F811
+    return lib.hk_attention_kv8_workspace_size_ex(Q, type, qs, ctypes.byref(c), pages, O, os, B, T, Hq)
+
+
+def test_calls_on_the_few_row_kernels_ask_for_no_widened_keys(lib):  # noqa: F811
+    from dense_bf16_gemm_02_gb300 import hk_gemm as h
+    c = _cache()
+    most = h.hk_attention_kv8_workspace_size(c, 2, 4000, 8, 4000)
+    assert most > 100 << 20
+    odd, one = (ctypes.c_int64 * 3)(257, 129, 65), (ctypes.c_int64 * 3)(256, 128, 0)
+    few = 1 << 25
+    for kw in (dict(type=1), dict(qs=odd), dict(os=odd), dict(qs=one), dict(Q=P + 2), dict(O=P + 8)):
+        assert 0 < _size(lib, c, **kw) <= few, kw
+        assert _call(lib, c, few, **kw) != h.HK_ERR_WORKSPACE, kw
+        assert _call(lib, c, _size(lib, c, **kw) - 1, **kw) == h.HK_ERR_WORKSPACE, kw
+    assert _size(lib, c) == most and _call(lib, c, most - 1) == h.HK_ERR_WORKSPACE
+    assert _size(lib, c, type=1, pages=4, T=1) == 0 and _size(lib, c, type=1, T=0) == 0 and _size(lib, c, qs=None) == 0
+
+
+@pytest.mark.parametrize("B,T,Hq,pages", [(1, 1, 2, 4), (2, 4000, 8, 1000), (64, 1, 64, 512), (3, 100, 14, 10000), (1100, 9, 6, 30)])
+def test_the_size_without_a_type_is_enough_for_every_one(lib, B, T, Hq, pages):  # noqa: F811
+    from dense_bf16_gemm_02_gb300 import hk_gemm as h
+    c = _cache(num_pages=1 << 20)
+    most = h.hk_attention_kv8_workspace_size(c, B, T, Hq, pages)
+    assert all(_size(lib, c, type=t, B=B, T=T, Hq=Hq, pages=pages) <= most for t in (0, 1))
