@@ -521,6 +521,15 @@ bool many_rows_can(const void* Q, int32_t type, const int64_t q_strides[3], cons
            (T == 1 || q_strides[1] > 0) && (Hq == 1 || q_strides[2] > 0);
 }
 
+constexpr uint32_t kFormFlags = HK_KV8_FEW_ROWS | HK_KV8_MANY_ROWS;
+
+// Does the call run on the tensor-core kernel?
+bool takes_many_rows(uint32_t flags, const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* c, const void* O,
+                     const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq) {
+    if (flags & kFormFlags) return flags & HK_KV8_MANY_ROWS;
+    return many_rows(B, T, Hq, c->heads) && many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq);
+}
+
 }  // namespace
 
 extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
@@ -532,10 +541,12 @@ extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int
 
 extern "C" size_t hk_attention_kv8_workspace_size_ex(const void* Q, int32_t type, const int64_t q_strides[3],
                                                      const hk_kv8_cache* cache, int64_t max_pages, const void* O,
-                                                     const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq) {
+                                                     const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq,
+                                                     uint32_t flags) {
     if (!attention_shape_ok(cache, B, T, Hq, max_pages) || !q_strides || !o_strides) return 0;
-    const bool many = many_rows(B, T, Hq, cache->heads) && many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq);
-    return many ? prefill_workspace(cache, B, max_pages).total : few_rows_bytes(cache, B, T, Hq, max_pages);
+    return takes_many_rows(flags, Q, type, q_strides, cache, O, o_strides, B, T, Hq)
+               ? prefill_workspace(cache, B, max_pages).total
+               : few_rows_bytes(cache, B, T, Hq, max_pages);
 }
 
 extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
@@ -546,7 +557,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
                                          uint32_t flags, uint64_t timeout_ns, void* stream) {
     hk_status s = check_cache(cache);
     if (s != HK_OK) return s;
-    if (flags) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if ((flags & ~kFormFlags) || (flags & kFormFlags) == kFormFlags) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
     if (type != HK_TYPE_BF16 && type != HK_TYPE_FP16) return fail(HK_ERR_INVALID_ARG, "element type %d (bf16 or fp16)", (int)type);
     if (B < 0 || T < 0 || Hq < 0 || B > kLimit || T > kLimit || Hq > kLimit) return fail(HK_ERR_INVALID_ARG, "invalid size");
     if (Hq % cache->heads) return fail(HK_ERR_INVALID_ARG, "Hq=%lld is not a multiple of the cache's %d heads", (long long)Hq, (int)cache->heads);
@@ -558,8 +569,11 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     const int64_t group = Hq / cache->heads;
     if (T > kLimit / 16 / group || ceil_div(T * group, kRows) * (ceil_div(max_pages * cache->page_size, kTileKeys) + 1) > kLimit)
         return fail(HK_ERR_INVALID_ARG, "problem too large");
+    if ((flags & HK_KV8_MANY_ROWS) && !many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq))
+        return fail(HK_ERR_INVALID_ARG, "the many-row kernel takes bf16 queries and an output with 16-byte aligned rows");
     const DecodeWorkspace ws = decode_workspace(cache, B, T, Hq);
-    const size_t need = hk_attention_kv8_workspace_size_ex(Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq);
+    const bool many = takes_many_rows(flags, Q, type, q_strides, cache, O, o_strides, B, T, Hq);
+    const size_t need = hk_attention_kv8_workspace_size_ex(Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq, flags);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
     if (!aligned(workspace, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
@@ -573,7 +587,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     const float scale_log2 = static_cast<float>(
         1.4426950408889634 * (scale != 0.0f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->head_dim))));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (many_rows(B, T, Hq, cache->heads) && many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq))
+    if (many)
         return prefill(Q, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse, B, T, Hq,
                        causal, scale_log2, workspace, status, timeout_ns, enc, sms, st);
     CUtensorMap tk, tv;

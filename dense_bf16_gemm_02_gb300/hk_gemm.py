@@ -49,6 +49,9 @@ HK_TYPE_BF16 = 0
 HK_TYPE_FP16 = 1
 HK_TYPE_FP32 = 2
 
+HK_KV8_FEW_ROWS = 0x10
+HK_KV8_MANY_ROWS = 0x20
+
 HK_FLAG_NONE = 0x0
 HK_FLAG_FAULT_DROP_ARRIVE = 0x1
 HK_FLAG_NO_TAIL_SPLIT = 0x2
@@ -184,7 +187,7 @@ def load() -> ctypes.CDLL:
         lib.hk_attention_kv8_ex.restype = I32
         lib.hk_attention_kv8_workspace_size.argtypes = [CP, I64, I64, I64, I64]
         lib.hk_attention_kv8_workspace_size.restype = SZ
-        lib.hk_attention_kv8_workspace_size_ex.argtypes = [P, I32, P, CP, I64, P, P, I64, I64, I64]
+        lib.hk_attention_kv8_workspace_size_ex.argtypes = [P, I32, P, CP, I64, P, P, I64, I64, I64, U32]
         lib.hk_attention_kv8_workspace_size_ex.restype = SZ
         _lib = lib
         return lib

@@ -341,7 +341,7 @@ def attention_kv8(q, cache: Kv8Cache, block_table, lengths, counts=None, causal=
     lib = _hk.load()
     size = lib.hk_attention_kv8_workspace_size(cache._ref, B, T, Hq, pages)
     if size:               # (enough for any type and strides; this call may need less)
-        size = lib.hk_attention_kv8_workspace_size_ex(q.data_ptr(), code, qs, cache._ref, pages, out.data_ptr(), os, B, T, Hq)
+        size = lib.hk_attention_kv8_workspace_size_ex(q.data_ptr(), code, qs, cache._ref, pages, out.data_ptr(), os, B, T, Hq, 0)
     workspace = _empty(size, _u8, q, stream) if size else None
     st = lib.hk_attention_kv8(q.data_ptr(), code, qs, cache._ref, block_table.data_ptr(), ld, pages, lengths.data_ptr(),
                               None if counts is None else counts.data_ptr(), out.data_ptr(), os,

@@ -503,7 +503,11 @@ hk_status hk_attention_kv8(const void* Q, int32_t type, const int64_t q_strides[
                            int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale,
                            void* workspace, size_t workspace_bytes, void* stream);
 
-/* The same with test controls: no flag is defined, `timeout_ns` bounds each wait (0: 1 s). */
+/* The same with test controls. `flags`: which kernels run, HK_KV8_FEW_ROWS (whatever
+ * the rows are) or HK_KV8_MANY_ROWS (refused for rows that they cannot take), 0: chosen by
+ * shape. `timeout_ns` bounds each wait (0: 1 s). */
+#define HK_KV8_FEW_ROWS 0x10u
+#define HK_KV8_MANY_ROWS 0x20u
 hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
                               const int32_t* block_table, int64_t table_stride, int64_t max_pages,
                               const int32_t* lengths, const int32_t* counts,
@@ -523,7 +527,8 @@ size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int64_t B, int
  * values). Q and O are looked at for their alignment only. */
 size_t hk_attention_kv8_workspace_size_ex(const void* Q, int32_t type, const int64_t q_strides[3],
                                           const hk_kv8_cache* cache, int64_t max_pages, const void* O,
-                                          const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq);
+                                          const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq,
+                                          uint32_t flags);
 
 /* Static description of a status code. */
 const char* hk_status_string(hk_status status);

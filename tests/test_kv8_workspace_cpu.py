@@ -6,13 +6,13 @@ import pytest
 from test_kv8_cpu import P, S3, _cache, lib  # noqa: F401  (a fixture)
 
 
-def _call(lib, c, size, type=0, Q=P, qs=S3, O=P, os=S3, B=2, T=4000, Hq=8, pages=4000):  # noqa: F811
+def _call(lib, c, size, flags=0, type=0, Q=P, qs=S3, O=P, os=S3, B=2, T=4000, Hq=8, pages=4000):  # noqa: F811
     return lib.hk_attention_kv8_ex(Q, type, qs, ctypes.byref(c), P, pages, pages, P, None, O, os, None, B, T, Hq, 1, 0.0, P,
-                                   size, 0, 0, None)
+                                   size, flags, 0, None)
 
 
-def _size(lib, c, type=0, Q=P, qs=S3, O=P, os=S3, B=2, T=4000, Hq=8, pages=4000):  # noqa: F811
-    return lib.hk_attention_kv8_workspace_size_ex(Q, type, qs, ctypes.byref(c), pages, O, os, B, T, Hq)
+def _size(lib, c, flags=0, type=0, Q=P, qs=S3, O=P, os=S3, B=2, T=4000, Hq=8, pages=4000):  # noqa: F811
+    return lib.hk_attention_kv8_workspace_size_ex(Q, type, qs, ctypes.byref(c), pages, O, os, B, T, Hq, flags)
 
 
 def test_calls_on_the_few_row_kernels_ask_for_no_widened_keys(lib):  # noqa: F811
@@ -36,3 +36,19 @@ def test_the_size_without_a_type_is_enough_for_every_one(lib, B, T, Hq, pages): 
     c = _cache(num_pages=1 << 20)
     most = h.hk_attention_kv8_workspace_size(c, B, T, Hq, pages)
     assert all(_size(lib, c, type=t, B=B, T=T, Hq=Hq, pages=pages) <= most for t in (0, 1))
+
+
+def test_either_form_can_be_asked_for(lib):  # noqa: F811
+    from dense_bf16_gemm_02_gb300 import hk_gemm as h
+    c = _cache()
+    few, many = h.HK_KV8_FEW_ROWS, h.HK_KV8_MANY_ROWS
+    wide = 2 * 2 * 4000 * 64 * 2 * 64 * 2
+    for T in (1, 4000):
+        assert _size(lib, c, many, T=T) == wide and 0 < _size(lib, c, few, T=T) <= 1 << 25
+        assert _call(lib, c, wide - 1, many, T=T) == h.HK_ERR_WORKSPACE
+        assert _call(lib, c, 1 << 25, few, T=T) != h.HK_ERR_WORKSPACE
+    assert _call(lib, c, wide, many, type=1) == h.HK_ERR_INVALID_ARG
+    assert _call(lib, c, wide, many, O=P + 2) == h.HK_ERR_INVALID_ARG
+    assert _call(lib, c, wide, few | many) == h.HK_ERR_INVALID_ARG
+    for other in (0x1, 0x2, 0x8, 0x100, 0x80000000):
+        assert _call(lib, c, wide, other) == h.HK_ERR_INVALID_ARG
