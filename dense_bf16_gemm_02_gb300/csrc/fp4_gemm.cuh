@@ -358,11 +358,11 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                 phase ^= 1u;
             }
         }
-        // also on the abort path: everything issued completes before TMEM is freed
-        if (lane == 0) {
-            mma_commit_one(acc_bar);
-            if (!ok) wait_mbar_drain(acc_bar, 0);
-        }
+        // also on the abort path: everything issued completes before TMEM is freed. (A commit tracks what its own thread
+        // issued, so it is the elected one's too: elect.sync picks the same lane every time, but not a known one.)
+        if (elect_one()) mma_commit_one(acc_bar);
+        __syncwarp();
+        if (lane == 0 && !ok) wait_mbar_drain(acc_bar, 0);
         __syncwarp();
     } else {
         // ------------------------------------------------------ epilogue --
@@ -694,10 +694,9 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
                 __syncwarp();
             }
             if (!ok || wait_aborted(p.wait)) {      // everything issued completes before TMEM is freed
-                if (lane == 0) {
-                    mma_commit_pair_mask(drain_bar, 0x1);
-                    wait_mbar_drain(drain_bar, 0);
-                }
+                if (elect_one()) mma_commit_pair_mask(drain_bar, 0x1);
+                __syncwarp();
+                if (lane == 0) wait_mbar_drain(drain_bar, 0);
                 __syncwarp();
             }
         }
