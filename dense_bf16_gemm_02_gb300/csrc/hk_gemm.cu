@@ -265,7 +265,9 @@ hk_status read_status(StatusWord* w, int device) {
     uint32_t h[2] = {0, 0};
     cudaError_t e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemcpy(h, w->dev, sizeof h, cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && h[0] != 0) e = cudaMemset(w->dev, 0, sizeof(uint32_t));
+    // (the aborted launch's id too: a captured launch keeps its id, and later replays of one that was aborted once
+    // would take themselves for aborted, without an error to show for it)
+    if (e == cudaSuccess && h[0] != 0) e = cudaMemset(w->dev, 0, 2 * sizeof(uint32_t));
     if (prev >= 0 && prev != device) cudaSetDevice(prev);
     if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "reading the device status word", e);
     if (h[0] & ~hk::kErrPage)
