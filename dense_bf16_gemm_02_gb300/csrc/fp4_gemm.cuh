@@ -324,6 +324,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             for (int f = fills > G::kStages ? fills - G::kStages : 0; f < fills; ++f)
                 if (!drop || f > 0) wait_mbar_drain(full_bar(f % G::kStages), (f / G::kStages) & 1);
     } else if (warp == 1) {
+        griddep_wait();                  // (its waits are for loads that begin then: the time limit is theirs alone)
         int stage = 0;
         uint32_t phase = 0;
         // (a column of a scale tile holds 32 rows: the second 64 tokens of 128 begin two columns on)
@@ -633,6 +634,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         }
     } else if (warp == 1) {
         // -------------------------------------------------------- MMAs --
+        griddep_wait();                  // (the time limit of its waits begins with the loads)
         if (rank == 0) {
             int stage = 0, slot = 0, local = 0;
             int old_stage = 0;                  // the stage whose MMAs used this slot last
