@@ -613,6 +613,7 @@ gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
         // The whole warp runs the loop (warp-uniform control flow and
         // descriptor arithmetic) and lane 0 issues the MMAs and commits:
         // measured 3 % faster than a loop run by lane 0 alone.
+        griddep_wait();                   // the time limit of its waits does not count the kernel before
         if (rank == 0) {
             int stage = 0;
             uint32_t phase = 0;
