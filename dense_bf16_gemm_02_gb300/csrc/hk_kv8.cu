@@ -235,19 +235,6 @@ int block_warps(int64_t units) {
     return warps;
 }
 
-// Do the rows go to the tensor-core kernel? Both forms' time grows with the cached tokens; per token, in
-// millionths of a microsecond, measured (D 64 and 128, 2000 to 16000 tokens): 35 for each unit of 16 rows and KV
-// head, whatever their number, against 13000 for each round of 256-row items over the SMs and 120 for bringing
-// one KV head's token to bf16. So 4 sequences x 8 heads x 8 queries run at 96 us by units and 236 us by items
-// (16000 tokens), 32 queries at 300 and 269 us.
-bool many_rows(int64_t B, int64_t T, int64_t Hq, int64_t heads) {
-    const int64_t group = Hq / heads;
-    const double units = static_cast<double>(B) * heads * ceil_div(T * group, kRows);
-    const int pack = pack_shift_of(group);
-    const double items = static_cast<double>(B) * (Hq >> pack) * ceil_div(T, (hk::attn::kTiles * hk::attn::kTileQ) >> pack);
-    return 35.0 * units > 13000.0 * std::ceil(items / kSms) + 120.0 * static_cast<double>(B) * heads;
-}
-
 // Sequences that are brought to bf16 at a time: as many as fit 512 MB, one at least.
 constexpr int64_t kWidenBytes = int64_t(512) << 20;
 
@@ -265,6 +252,24 @@ PrefillWorkspace prefill_workspace(const hk_kv8_cache* c, int64_t B, int64_t max
     w.half = static_cast<size_t>(w.seqs * one / 2);
     w.total = 2 * w.half;
     return w;
+}
+
+// Do the rows go to the tensor-core kernel? Both forms' time grows with the cached tokens; per token, in
+// millionths of a microsecond, measured (D 64 and 128, 2000 to 16000 tokens): 35 for each unit of 16 rows and KV
+// head, whatever their number, against 13000 for each round of 256-row items over the SMs and 120 for bringing
+// one KV head's token to bf16. So 4 sequences x 8 heads x 8 queries run at 96 us by units and 236 us by items
+// (16000 tokens), 32 queries at 300 and 269 us. Sequences that are not widened together (a wide table) do not
+// share a round: 64 sequences of up to 2048 tokens, 32 queries of 32 heads, take 230 us by units and 2112 us by
+// items with a table of 131072 tokens, 180 us by items with one of 2048.
+bool many_rows(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages) {
+    const int64_t group = Hq / c->heads;
+    const double units = static_cast<double>(B) * c->heads * ceil_div(T * group, kRows);
+    const int pack = pack_shift_of(group);
+    const double seq_items = static_cast<double>(Hq >> pack) * ceil_div(T, (hk::attn::kTiles * hk::attn::kTileQ) >> pack);
+    const int64_t seqs = prefill_workspace(c, B, max_pages).seqs;
+    const double rounds = static_cast<double>(B / seqs) * std::ceil(static_cast<double>(seqs) * seq_items / kSms) +
+                          std::ceil(static_cast<double>(B % seqs) * seq_items / kSms);
+    return 35.0 * units > 13000.0 * rounds + 120.0 * static_cast<double>(B) * c->heads;
 }
 
 // Queries as [B, T, heads, D] in boxes of 64 columns × `pack` heads × 128 / pack tokens.
@@ -524,10 +529,10 @@ bool many_rows_can(const void* Q, int32_t type, const int64_t q_strides[3], cons
 constexpr uint32_t kFormFlags = HK_KV8_FEW_ROWS | HK_KV8_MANY_ROWS;
 
 // Does the call run on the tensor-core kernel?
-bool takes_many_rows(uint32_t flags, const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* c, const void* O,
-                     const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq) {
+bool takes_many_rows(uint32_t flags, const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* c, int64_t max_pages,
+                     const void* O, const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq) {
     if (flags & kFormFlags) return flags & HK_KV8_MANY_ROWS;
-    return many_rows(B, T, Hq, c->heads) && many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq);
+    return many_rows(c, B, T, Hq, max_pages) && many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq);
 }
 
 }  // namespace
@@ -536,7 +541,7 @@ extern "C" size_t hk_attention_kv8_workspace_size(const hk_kv8_cache* cache, int
                                                   int64_t max_pages) {
     if (!attention_shape_ok(cache, B, T, Hq, max_pages)) return 0;
     const size_t few = few_rows_bytes(cache, B, T, Hq, max_pages);
-    return many_rows(B, T, Hq, cache->heads) ? std::max(few, prefill_workspace(cache, B, max_pages).total) : few;
+    return many_rows(cache, B, T, Hq, max_pages) ? std::max(few, prefill_workspace(cache, B, max_pages).total) : few;
 }
 
 extern "C" size_t hk_attention_kv8_workspace_size_ex(const void* Q, int32_t type, const int64_t q_strides[3],
@@ -544,7 +549,7 @@ extern "C" size_t hk_attention_kv8_workspace_size_ex(const void* Q, int32_t type
                                                      const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq,
                                                      uint32_t flags) {
     if (!attention_shape_ok(cache, B, T, Hq, max_pages) || !q_strides || !o_strides) return 0;
-    return takes_many_rows(flags, Q, type, q_strides, cache, O, o_strides, B, T, Hq)
+    return takes_many_rows(flags, Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq)
                ? prefill_workspace(cache, B, max_pages).total
                : few_rows_bytes(cache, B, T, Hq, max_pages);
 }
@@ -572,7 +577,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if ((flags & HK_KV8_MANY_ROWS) && !many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq))
         return fail(HK_ERR_INVALID_ARG, "the many-row kernel takes bf16 queries and an output with 16-byte aligned rows");
     const DecodeWorkspace ws = decode_workspace(cache, B, T, Hq);
-    const bool many = takes_many_rows(flags, Q, type, q_strides, cache, O, o_strides, B, T, Hq);
+    const bool many = takes_many_rows(flags, Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq);
     const size_t need = hk_attention_kv8_workspace_size_ex(Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq, flags);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, workspace ? workspace_bytes : size_t(0));

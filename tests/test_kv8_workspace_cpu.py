@@ -52,3 +52,15 @@ def test_either_form_can_be_asked_for(lib):  # noqa: F811
     assert _call(lib, c, wide, few | many) == h.HK_ERR_INVALID_ARG
     for other in (0x1, 0x2, 0x8, 0x100, 0x80000000):
         assert _call(lib, c, wide, other) == h.HK_ERR_INVALID_ARG
+
+
+def test_a_wide_table_does_not_cost_a_round_for_each_sequence(lib):  # noqa: F811
+    """64 sequences, 32 queries of 32 heads each: together they fill the GPU with 256-row items; where the table's
+    width lets only a few be widened at a time, items of one sequence alone would leave most SMs idle."""
+    c = _cache(num_pages=1 << 20, heads=8, head_dim=128)
+    kw = dict(B=64, T=32, Hq=32)
+    one = 2 * 8 * 128 * 2                                      # bytes of a widened token
+    assert _size(lib, c, pages=32, **kw) == 64 * 2048 * one    # 2048 tokens: all at once, on the many-row form
+    assert _size(lib, c, pages=512, **kw) < 64 << 20           # 32768: the few-row form
+    assert _size(lib, c, pages=2048, **kw) < 64 << 20          # 131072
+    assert _size(lib, c, pages=2048, B=64, T=2048, Hq=32) == 131072 * one      # whole prompts: still many rows
