@@ -53,6 +53,13 @@ def test_few_queries_that_do_not_see_a_token_are_not_touched_by_it(hk, D, wide, 
 
 
 @pytest.mark.parametrize("D", [64, 128])
+def test_one_warp_that_has_tiles_before_the_one_with_nan(hk, D):  # noqa: F811
+    """720 units, a warp each: rows that see the first three tiles and nothing, or not all, of the last."""
+    n = 97
+    _check(hk, 90, 8, 1, 16, D, 32, [n] * 90, None, True, [(0, n - 1, 0, 3), (1, n - 2, 1, 5), (2, n - 9, 2, 7), (3, 40, 3, 0)])
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("wide", [0, 3000])
 @pytest.mark.parametrize("causal", [True, False])
 def test_few_queries_past_the_count_and_before_the_first_token_stay_zero(hk, D, wide, causal):  # noqa: F811
