@@ -15,7 +15,8 @@ from .hk_gemm import (HK_ACT_GELU, HK_ACT_NONE, HK_ACT_RELU, HK_ACT_SILU, HK_ERR
                       hk_attention_fwd, hk_attention_fwd_ex, hk_gemm_bf16, hk_gemm_bf16_epilogue, hk_gemm_bf16_fused,
                       hk_gemm_bf16_noalloc, hk_gemm_fp8_e4m3, hk_gemm_last_device_status, hk_gemm_last_error_string,
                       hk_gemm_mxfp8, hk_gemm_mxfp8_ex, hk_gemm_mxfp8_workspace_size, hk_status_string, load,
-                      HK_FP4_MXFP4, HK_FP4_NVFP4, HK_KV8_FEW_ROWS, HK_KV8_MANY_ROWS, HK_TYPE_BF16, HK_TYPE_FP16, HK_TYPE_FP32, hk_fp4_dequantize,
+                      HK_FP4_MXFP4, HK_FP4_NVFP4, HK_KV8_FAULT_DROP_ARRIVE, HK_KV8_FEW_ROWS, HK_KV8_MANY_ROWS,
+                      HK_TYPE_BF16, HK_TYPE_FP16, HK_TYPE_FP32, hk_fp4_dequantize,
                       hk_attention_kv8, hk_attention_kv8_workspace_size, hk_fp4_quantize, hk_fp4_scales_size,
                       hk_gemm_fp4, hk_gemm_fp4_ex, hk_kv8_append, hk_kv8_cache)
 
@@ -41,4 +42,5 @@ __all__ = ["attention", "gemm", "Plan", "HKError", "load",
            "Fp4Matrix", "quantize_fp4", "dequantize_fp4", "gemm_fp4", "Kv8Cache", "kv8_append", "attention_kv8",
            "hk_kv8_cache", "hk_kv8_append", "hk_attention_kv8", "hk_attention_kv8_workspace_size",
            "hk_fp4_quantize", "hk_fp4_dequantize", "hk_fp4_scales_size", "hk_gemm_fp4", "hk_gemm_fp4_ex",
-           "HK_FP4_MXFP4", "HK_FP4_NVFP4", "HK_KV8_FEW_ROWS", "HK_KV8_MANY_ROWS", "HK_TYPE_BF16", "HK_TYPE_FP16", "HK_TYPE_FP32"]
+           "HK_FP4_MXFP4", "HK_FP4_NVFP4", "HK_KV8_FAULT_DROP_ARRIVE", "HK_KV8_FEW_ROWS", "HK_KV8_MANY_ROWS",
+           "HK_TYPE_BF16", "HK_TYPE_FP16", "HK_TYPE_FP32"]

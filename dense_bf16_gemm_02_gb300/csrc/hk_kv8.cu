@@ -362,7 +362,7 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const De
 hk_status prefill(const void* Q, const int64_t q_strides[3], const hk_kv8_cache* c, const int32_t* table, int64_t table_stride,
                   int64_t max_pages, const int32_t* lengths, const int32_t* counts, void* O, const int64_t o_strides[3],
                   float* lse, int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale_log2, void* workspace,
-                  uint32_t* status, uint64_t timeout_ns, PFN_cuTensorMapEncodeTiled_v12000 enc, int sms, cudaStream_t st) {
+                  uint32_t* status, uint32_t flags, uint64_t timeout_ns, PFN_cuTensorMapEncodeTiled_v12000 enc, int sms, cudaStream_t st) {
     const PrefillWorkspace ws = prefill_workspace(c, B, max_pages);
     char* const wide[2] = {static_cast<char*>(workspace), static_cast<char*>(workspace) + ws.half};
     const int64_t group = Hq / c->heads;
@@ -406,6 +406,7 @@ hk_status prefill(const void* Q, const int64_t q_strides[3], const hk_kv8_cache*
         p.lse = lse ? lse + b0 * T * Hq : nullptr;
         p.status = status;
         p.launch_id = hk_host::next_launch_id();
+        p.flags = flags & HK_KV8_FAULT_DROP_ARRIVE ? hk::attn::kFlagDropArrive : 0u;
         p.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
         p.lengths = w.lengths;
         p.counts = w.counts;
@@ -562,7 +563,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
                                          uint32_t flags, uint64_t timeout_ns, void* stream) {
     hk_status s = check_cache(cache);
     if (s != HK_OK) return s;
-    if ((flags & ~kFormFlags) || (flags & kFormFlags) == kFormFlags) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if ((flags & ~(kFormFlags | HK_KV8_FAULT_DROP_ARRIVE)) || (flags & kFormFlags) == kFormFlags) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
     if (type != HK_TYPE_BF16 && type != HK_TYPE_FP16) return fail(HK_ERR_INVALID_ARG, "element type %d (bf16 or fp16)", (int)type);
     if (B < 0 || T < 0 || Hq < 0 || B > kLimit || T > kLimit || Hq > kLimit) return fail(HK_ERR_INVALID_ARG, "invalid size");
     if (Hq % cache->heads) return fail(HK_ERR_INVALID_ARG, "Hq=%lld is not a multiple of the cache's %d heads", (long long)Hq, (int)cache->heads);
@@ -594,7 +595,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (many)
         return prefill(Q, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse, B, T, Hq,
-                       causal, scale_log2, workspace, status, timeout_ns, enc, sms, st);
+                       causal, scale_log2, workspace, status, flags, timeout_ns, enc, sms, st);
     CUtensorMap tk, tv;
     if ((s = encode_codes(enc, &tk, cache->k_codes, cache)) != HK_OK) return s;
     if ((s = encode_codes(enc, &tv, cache->v_codes, cache)) != HK_OK) return s;
@@ -622,6 +623,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     p.num_pages = cache->num_pages;
     p.causal = causal ? 1 : 0;
     p.scale_log2 = scale_log2;
+    p.flags = flags & HK_KV8_FAULT_DROP_ARRIVE ? kFlagDropArrive : 0u;
     char* const w = static_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(w);
     p.part_ml = reinterpret_cast<float*>(w + ws.ml);

@@ -53,6 +53,7 @@ constexpr int kRows = 16;              // query rows of a unit
 constexpr int kTileKeys = 32;
 constexpr int kDecodeWarps = 4;        // warps of a block, each on its own
 constexpr int kMaxBatch = 1024;        // sequences of one launch
+constexpr uint32_t kFlagDropArrive = 0x1u; // test only: the first stage of no warp ever counts as filled
 constexpr float kWeightShift = 15.0f;  // P is held times 2^15
 constexpr float kWeightUnit = 0x1p-15f;
 
@@ -88,6 +89,7 @@ struct DecodeParams {
     int32_t causal, vec_q, vec_o;
     float scale_log2;                               // softmax scale · log2(e)
     int32_t warps;                                  // of kv8_decode_kernel's grid
+    uint32_t flags;
     float* part_o;                                  // [2 · warps][16][D]
     float* part_ml;                                 // [2 · warps][16][2]
     int4* info;                                     // [units]: parts whose sums make up the unit (0: it is finished), first slot, first warp
@@ -558,7 +560,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     const uint32_t ring = base + warp * G::kWarpBytes;
     const uint32_t bars = base + G::kOffBars + 8u * warp * G::kStages;
     if (lane == 0) {
-        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, 1);
+        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, s == 0 && (p.flags & kFlagDropArrive) ? 2 : 1);
         fence_mbar_init_cluster();
     }
     griddep_wait();                          // launched early behind the kernel that may have written the cache or q
@@ -730,7 +732,7 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
         prefetch_tensor_map(&tmap_v);
     }
     if (lane == 0) {
-        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, 1);
+        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, s == 0 && (p.flags & kFlagDropArrive) ? 2 : 1);
         fence_mbar_init_cluster();
     }
     __syncwarp();

@@ -51,6 +51,7 @@ HK_TYPE_FP32 = 2
 
 HK_KV8_FEW_ROWS = 0x10
 HK_KV8_MANY_ROWS = 0x20
+HK_KV8_FAULT_DROP_ARRIVE = 0x40
 
 HK_FLAG_NONE = 0x0
 HK_FLAG_FAULT_DROP_ARRIVE = 0x1

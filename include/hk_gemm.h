@@ -505,9 +505,11 @@ hk_status hk_attention_kv8(const void* Q, int32_t type, const int64_t q_strides[
 
 /* The same with test controls. `flags`: which kernels run, HK_KV8_FEW_ROWS (whatever
  * the rows are) or HK_KV8_MANY_ROWS (refused for rows that they cannot take), 0: chosen by
- * shape. `timeout_ns` bounds each wait (0: 1 s). */
+ * shape; HK_KV8_FAULT_DROP_ARRIVE: an arrival is withheld, so that a bounded wait runs
+ * out. `timeout_ns` bounds each wait (0: 1 s). */
 #define HK_KV8_FEW_ROWS 0x10u
 #define HK_KV8_MANY_ROWS 0x20u
+#define HK_KV8_FAULT_DROP_ARRIVE 0x40u
 hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
                               const int32_t* block_table, int64_t table_stride, int64_t max_pages,
                               const int32_t* lengths, const int32_t* counts,

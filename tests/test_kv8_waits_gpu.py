@@ -18,7 +18,7 @@ CASES = [(MANY, 2, 2, 40, 300, 0), (FEW, 19, 8, 1, 150, 0), (FEW, 38, 8, 1, 150,
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("case", CASES, ids=["many", "block8", "block4", "block2", "block1", "cluster", "spread"])
-def test_a_load_that_never_comes_is_reported(hk, D, case):  # noqa: F811
+def test_an_arrival_that_never_comes_is_reported(hk, D, case):  # noqa: F811
     import torch
     form, B, H, T, n, wide = case
     rng = np.random.default_rng(B)
@@ -30,7 +30,7 @@ def test_a_load_that_never_comes_is_reported(hk, D, case):  # noqa: F811
         table = (w, torch.from_numpy(w).cuda())
     q = _tokens(rng, B, T, H * 4, D, torch.bfloat16, 1)
     for fill in (0, 0x7F, 0xFF):
-        _attend(hk, form, q, cache, table[1], lengths, fill=fill, timeout_ns=3_000_000, flags=hk.HK_KV8_FAULT_DROP_LOAD)
+        _attend(hk, form, q, cache, table[1], lengths, fill=fill, timeout_ns=3_000_000, flags=hk.HK_KV8_FAULT_DROP_ARRIVE)
         assert _status(hk) == hk.HK_ERR_TIMEOUT
         assert _status(hk) == hk.HK_OK
     _assert(hk, form, q, cache, table, lengths)

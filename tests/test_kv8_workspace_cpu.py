@@ -50,7 +50,7 @@ def test_either_form_can_be_asked_for(lib):  # noqa: F811
     assert _call(lib, c, wide, many, type=1) == h.HK_ERR_INVALID_ARG
     assert _call(lib, c, wide, many, O=P + 2) == h.HK_ERR_INVALID_ARG
     assert _call(lib, c, wide, few | many) == h.HK_ERR_INVALID_ARG
-    for other in (0x1, 0x2, 0x8, 0x100, 0x80000000):
+    for other in (0x1, 0x2, 0x8, 0x80, 0x100, 0x80000000):
         assert _call(lib, c, wide, other) == h.HK_ERR_INVALID_ARG
 
 
