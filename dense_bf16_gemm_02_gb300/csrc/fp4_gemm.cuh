@@ -128,8 +128,29 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ float global_alpha(const Fp4Params& p) {
-    return (p.ga != nullptr ? *p.ga : 1.0f) * (p.gb != nullptr ? *p.gb : 1.0f);
+// The global scales' product as two factors: the product and 1, unless it comes near the ends of fp32's range (a sum
+// times both may well be inside it); then its fraction with as much of its exponent as keeps a product with a sum
+// inside, and the rest of the exponent, which the sums are lifted by first.
+struct Alpha {
+    float mul, lift;
+    template <int kCount>
+    __device__ __forceinline__ void lift_sums(uint32_t (&v)[kCount]) const {
+        if (lift != 1.0f) {              // (the same in every thread)
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * lift);
+        }
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t sum) const { return __float_as_uint(__uint_as_float(sum) * mul); }
+};
+
+__device__ __forceinline__ Alpha global_alpha(const Fp4Params& p) {
+    const float a = p.ga != nullptr ? *p.ga : 1.0f, b = p.gb != nullptr ? *p.gb : 1.0f;
+    const float product = a * b;
+    if ((fabsf(product) >= 0x1p-80f && fabsf(product) <= 0x1p80f) || !isfinite(a) || !isfinite(b)) return Alpha{product, 1.0f};
+    int ea, eb;
+    const float fraction = frexpf(a, &ea) * frexpf(b, &eb);
+    const int e = ea + eb, near = max(-80, min(80, e));
+    return Alpha{ldexpf(fraction, near), ldexpf(1.0f, max(-149, min(127, e - near)))};
 }
 
 template <int kCols>
@@ -141,12 +162,12 @@ __device__ __forceinline__ void tmem_load_cols(uint32_t taddr, uint32_t (&v)[kCo
 
 // Sums of one feature and kStep tokens to their rows of C, as far as there are tokens.
 template <int kStep>
-__device__ __forceinline__ void store_tokens(uint16_t* dst, int64_t ldc, const uint32_t (&v)[kStep], float alpha, int tokens) {
+__device__ __forceinline__ void store_tokens(uint16_t* dst, int64_t ldc, uint32_t (&v)[kStep], const Alpha alpha, int tokens) {
+    alpha.lift_sums(v);
     uint32_t w[kStep / 2];
 #pragma unroll
     for (int i = 0; i < kStep / 2; ++i)
-        w[i] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(v[2 * i]) * alpha),
-                              __float_as_uint(__uint_as_float(v[2 * i + 1]) * alpha));
+        w[i] = pack_bf16x2_rn(alpha.of(v[2 * i]), alpha.of(v[2 * i + 1]));
     if (tokens >= kStep) {
 #pragma unroll
         for (int e = 0; e < kStep; ++e) dst[e * ldc] = static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]);
@@ -167,7 +188,7 @@ __device__ __forceinline__ void join_tokens(const Fp4Params& p, uint32_t base, i
     constexpr int kTokens = 16 / kParts;
     const int lane = static_cast<int>(lane_id());
     const int feature = tn * 128 + lane * 4;
-    const float alpha = global_alpha(p);
+    const Alpha alpha = global_alpha(p);
     uint32_t from[kParts];
 #pragma unroll
     for (int r = 0; r < kParts; ++r) from[r] = map_to_cta(base + static_cast<uint32_t>(lane) * 16u, static_cast<uint32_t>(r));
@@ -193,8 +214,10 @@ __device__ __forceinline__ void join_tokens(const Fp4Params& p, uint32_t base, i
             }
             if (!ok || t + 4 * i >= t1) continue;
             uint16_t* const dst = p.c + static_cast<int64_t>(tm * kTok + t + 4 * i) * p.ldc + feature;
-            const uint32_t w0 = pack_bf16x2_rn(__float_as_uint(sum.x * alpha), __float_as_uint(sum.y * alpha));
-            const uint32_t w1 = pack_bf16x2_rn(__float_as_uint(sum.z * alpha), __float_as_uint(sum.w * alpha));
+            uint32_t v[4] = {__float_as_uint(sum.x), __float_as_uint(sum.y), __float_as_uint(sum.z), __float_as_uint(sum.w)};
+            alpha.lift_sums(v);
+            const uint32_t w0 = pack_bf16x2_rn(alpha.of(v[0]), alpha.of(v[1]));
+            const uint32_t w1 = pack_bf16x2_rn(alpha.of(v[2]), alpha.of(v[3]));
             if (p.vec_c && feature + 4 <= p.N) {
                 *reinterpret_cast<uint2*>(dst) = make_uint2(w0, w1);
             } else {
@@ -374,7 +397,7 @@ gemm_fp4_single_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
         const int f_local = static_cast<int>(q * 32 + lane);
         const int feature = tn * G::kTileF + f_local;
         const uint32_t t_row = tmem_base + ((q * 32u) << 16);
-        const float alpha = global_alpha(p);
+        const Alpha alpha = global_alpha(p);
         // (columns of 32 tokens at a time, and no test or address of its own for each token where all of them are
         // inside C: one warp of a scheduler pays the latency of every instruction that depends on another)
         constexpr int kStep = kTok < 32 ? kTok : 32;
@@ -501,8 +524,9 @@ __device__ __forceinline__ void pair_unit(const Fp4Params& p, int u, int& tm, in
 // the last columns, since it bounds a row to 16 bytes only) a warp writes a row's
 // 32 columns at a time.
 __device__ __forceinline__ void store_sums(const Fp4Params& p, const void* tmap_c, uint32_t buf, const uint8_t* buf_ptr,
-                                           const uint32_t (&v)[32], float alpha, int row0, int col0) {
+                                           uint32_t (&v)[32], const Alpha alpha, int row0, int col0) {
     const uint32_t lane = lane_id();
+    alpha.lift_sums(v);
     if (row0 >= p.M || col0 >= p.N) return;          // (the same in every lane)
     if (lane == 0) bulk_wait_group_read<0>();        // the store before has read the buffer
     __syncwarp();
@@ -511,8 +535,7 @@ __device__ __forceinline__ void store_sums(const Fp4Params& p, const void* tmap_
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = pack_bf16x2_rn(__float_as_uint(__uint_as_float(v[8 * j + 2 * i]) * alpha),
-                                  __float_as_uint(__uint_as_float(v[8 * j + 2 * i + 1]) * alpha));
+            w[i] = pack_bf16x2_rn(alpha.of(v[8 * j + 2 * i]), alpha.of(v[8 * j + 2 * i + 1]));
         st_shared_v4(buf + lane * 64u + ((static_cast<uint32_t>(j) ^ ((lane >> 1) & 3u)) << 4), w[0], w[1], w[2], w[3]);
     }
     if (p.vec_c && (col0 + 32 <= p.N || p.N % 8 == 0)) {
@@ -706,7 +729,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_co
         // ----------------------------------------------------- epilogue --
         griddep_wait();                               // before C is written or the global scales are read
         const uint32_t q = warp & 3u;                 // TMEM lanes 32 q .. 32 q + 31
-        const float alpha = global_alpha(p);
+        const Alpha alpha = global_alpha(p);
         const uint32_t buf_addr = base + G::kOffStore + (warp - 2) * G::kStoreBytes;
         const uint8_t* const buf_ptr = smem + G::kOffStore + (warp - 2) * G::kStoreBytes;
         int local = 0;

@@ -56,3 +56,39 @@ def test_quantize_with_a_small_global_scale(hk, g, dtype):  # noqa: F811
         assert (ok | np.isnan(v)).all()
     torch.cuda.synchronize()
     assert hk.hk_gemm_last_device_status(torch.cuda.current_device()) == hk.HK_OK
+
+
+# products of global scales that fp32 does not hold, or barely, and sums that bring them back or do not
+PRODUCTS = [(1e-23, 1e-22, 0), (3e-39, 2e30, 0), (1.4e-45, 1e38, 0), (1e-20, 1e-19, 0), (2e-25, 2e-25, 0), (1e25, 1e9, 0),
+            (1e22, 3e17, 0), (1e22, 1e22, -8), (2e38, 1e-38, 0), (1e-30, 1e-30, 0), (1e30, 1e30, 0), (0.37, 1.9, 0), (1e-23, 1e-22, 8),
+            (1e-24, 1e-22, 8), (3e-30, 2e-18, 8), (1.4e-45, 1e0, 8)]
+
+
+@pytest.mark.parametrize("ga,gb,span", PRODUCTS)
+@pytest.mark.parametrize("M,split", [(3, 1), (3, 4), (100, 2), (300, 0)])
+def test_product_with_small_and_large_global_scales(hk, ga, gb, span, M, split):  # noqa: F811
+    """Tolerance: test_fp4_gpu.py's, and half a step of bf16's and fp32's smallest numbers (2^-134, 2^-149)."""
+    import torch
+    from test_fp4_gpu import _forced
+    N, K = 130, 2048
+    rng = np.random.default_rng(M)
+
+    def matrix(rows, g):
+        code = rng.integers(0, 16, (rows, K)).astype(np.uint8)
+        byte = rng.integers(0x28, 0x50, (rows, K // 16)).astype(np.uint8)
+        if span:
+            byte[:] = 1 if span < 0 else 0x7E                 # every block's scale E4M3's smallest, or its largest number
+        gt = torch.tensor([g], dtype=torch.float32, device="cuda")
+        m = hk.Fp4Matrix(torch.from_numpy(ref.pack(code)).cuda(), torch.from_numpy(ref.tile_scales(byte, K, "nvfp4")).cuda(),
+                         rows, K, "nvfp4", gt)
+        return m, ref.values(code, byte, "nvfp4", float(gt.double().item()))
+    (a, av), (b, bv) = matrix(M, ga), matrix(N, gb)
+    got = _forced(hk, a, b, 4 if split else 1, split).double().cpu().numpy()
+    want = av @ bv.T
+    tol = 2.0 ** -8 * np.abs(want) + (K * 2.0 ** -27 + 2.0 ** -22) * (np.abs(av) @ np.abs(bv).T) + 2.0 ** -134 + 2.0 ** -149
+    top = 2.0 ** 127 * (2 - 2.0 ** -8)                        # half a step above bf16's largest
+    huge = np.abs(want) > top * (1 + 2.0 ** -7)
+    near = ~huge & (np.abs(want) > top * (1 - 2.0 ** -7))      # may round to either
+    assert np.array_equal(got[huge], np.sign(want[huge]) * np.inf)
+    ok = np.abs(got - want) <= tol
+    assert (ok | huge | near).all(), (got[~(ok | huge | near)][:4], want[~(ok | huge | near)][:4])
