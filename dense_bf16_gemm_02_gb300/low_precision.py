@@ -17,6 +17,7 @@ rest what the two and the allocator cost each other in caches), a one-token prod
 """
 from __future__ import annotations
 
+import ctypes
 import operator
 import struct
 
@@ -324,8 +325,8 @@ def attention_kv8(q, cache: Kv8Cache, block_table, lengths, counts=None, causal=
         raise TypeError("q must be bfloat16 or float16")
     if scale is None:
         scale = 0.0
-    elif not scale:
-        raise ValueError("scale must not be 0")
+    elif not ctypes.c_float(scale).value:
+        raise ValueError("scale must not be 0, nor round to it in 32 bits")
     ld, pages = _table(block_table, B)
     _check_vector(lengths, "lengths", B)
     if counts is not None:

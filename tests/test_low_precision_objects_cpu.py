@@ -21,3 +21,15 @@ def test_a_quantised_matrix_keeps_its_tensors_and_sizes(name):
         setattr(q, name, 1)
     setattr(q, "_" + name, 7)
     assert getattr(q, name) == 7
+
+
+@pytest.mark.parametrize("scale", [0, 0.0, -0.0, 1e-50, -1e-60])
+def test_a_scale_that_is_0_in_32_bits_is_refused(scale, monkeypatch):
+    """(0 asks the entry point for its default, so it must not be what a small scale rounds to)"""
+    import torch
+
+    from dense_bf16_gemm_02_gb300 import Kv8Cache, low_precision
+    monkeypatch.setattr(low_precision, "_tokens_shape", lambda *a: (1, 1, 1, b""))
+    with pytest.raises(ValueError, match="scale"):
+        low_precision.attention_kv8(torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16), Kv8Cache.__new__(Kv8Cache), None, None,
+                                    scale=scale)
