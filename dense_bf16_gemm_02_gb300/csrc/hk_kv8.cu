@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <mutex>
 
 #include "../../include/hk_gemm.h"
@@ -572,6 +573,9 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if ((s = check_table(block_table, table_stride, max_pages, B, lengths, counts, cache->page_size)) != HK_OK) return s;
     if (!Q || !O || !q_strides || !o_strides) return fail(HK_ERR_INVALID_ARG, "null queries, output or strides");
     if (!aligned(Q, 2) || !aligned(O, 2) || !aligned(lse, 4)) return fail(HK_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    const int64_t sizes[3] = {B, T, Hq};
+    for (int i = 0; i < 3; ++i)
+        if (sizes[i] > 1 && std::llabs(o_strides[i]) < cache->head_dim) return fail(HK_ERR_INVALID_ARG, "the output's rows overlap");
     const int64_t group = Hq / cache->heads;
     if (T > kLimit / 16 / group || ceil_div(T * group, kRows) * (ceil_div(max_pages * cache->page_size, kTileKeys) + 1) > kLimit)
         return fail(HK_ERR_INVALID_ARG, "problem too large");

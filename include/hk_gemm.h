@@ -486,7 +486,7 @@ hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, const void* V,
  * of zeros and a log-sum-exp of -inf. `scale` must not be
  * negative; 0: 1/sqrt(head_dim).
  * Q and O are [B, T, Hq, head_dim] of `type` (bf16 or fp16), strides (b, t, head)
- * in elements, contiguous rows. lse, when not NULL: fp32 [B, T, Hq], natural
+ * in elements, contiguous rows (O's must not overlap). lse, when not NULL: fp32 [B, T, Hq], natural
  * log of the sum of exp(scale · q·k).
  * Many query rows per KV head (a prompt) run on the attention-forward kernel when Q
  * is bf16 with rows that are 16-byte aligned; fp16 and other rows run on the

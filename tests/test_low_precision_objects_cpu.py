@@ -33,3 +33,21 @@ def test_a_scale_that_is_0_in_32_bits_is_refused(scale, monkeypatch):
     with pytest.raises(ValueError, match="scale"):
         low_precision.attention_kv8(torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16), Kv8Cache.__new__(Kv8Cache), None, None,
                                     scale=scale)
+
+
+def test_an_output_whose_rows_overlap_is_refused():
+    import ctypes
+
+    from dense_bf16_gemm_02_gb300 import build, hk_gemm as h
+    build.build()
+    lib, P, I3 = h.load(), 1 << 20, ctypes.c_int64 * 3
+    cache = h.hk_kv8_cache(k_codes=P, v_codes=P, k_scale=P, v_scale=P, num_pages=4, heads=2, page_size=64, head_dim=64)
+
+    def call(strides, B=2, T=3, Hq=4):
+        return lib.hk_attention_kv8(P, 0, I3(768, 256, 64), ctypes.byref(cache), P, 4, 4, P, None, P, I3(*strides), None, B, T, Hq,
+                                    1, 0.0, P, 1 << 40, None)
+    for bad in ((0, 256, 64), (768, 0, 64), (768, 256, 0), (768, 256, 63), (768, -32, 64), (1, 256, 64)):
+        assert call(bad) == h.HK_ERR_INVALID_ARG, bad
+    for good in ((768, 256, 64), (64, 128, 384), (-768, 256, 64)):
+        assert call(good) != h.HK_ERR_INVALID_ARG, good
+    assert call((0, 256, 64), B=1) != h.HK_ERR_INVALID_ARG and call((64, 1, 128), B=2, T=1) != h.HK_ERR_INVALID_ARG
