@@ -45,22 +45,22 @@ FALLBACK_PEAKS = {"bf16_tflops": 1900.0, "bf16_tflops_sustained": 1700.0, "hbm_g
 # sources whose digest is given (the code of those sources, comments and
 # layout excluded).
 MEASURED_TRAFFIC = {
-    "gemm_8192": {"source_digest": "44f8f6e523fb0714", "bytes_per_launch": 1088810240 + 128326400},
+    "gemm_8192": {"source_digest": "7efc22286720fa41", "bytes_per_launch": 1088973312 + 127678464},
     # inputs smaller than L2 (warm): DRAM traffic is below the algorithmic bytes
-    "gemm_4096": {"source_digest": "44f8f6e523fb0714", "bytes_per_launch": 81987584 + 13967872},
-    "skinny_128x28672x8192": {"source_digest": "44f8f6e523fb0714", "bytes_per_launch": 471951104 + 3197184},
-    "fp8_gemm_8192": {"source_digest": "44f8f6e523fb0714", "bytes_per_launch": 345712640 + 117028608},
+    "gemm_4096": {"source_digest": "7efc22286720fa41", "bytes_per_launch": 82448640 + 14353408},
+    "skinny_128x28672x8192": {"source_digest": "7efc22286720fa41", "bytes_per_launch": 471995904 + 3211264},
+    "fp8_gemm_8192": {"source_digest": "7efc22286720fa41", "bytes_per_launch": 345696768 + 115882752},
     # the block-scaled GEMM kernel alone (the scale arrangement kernel moves ~8 MB more)
-    "mxfp8_gemm_8192": {"source_digest": "44f8f6e523fb0714", "bytes_per_launch": 358555648 + 116891904},
+    "mxfp8_gemm_8192": {"source_digest": "7efc22286720fa41", "bytes_per_launch": 359991296 + 116811776},
     # the GEMM kernel alone (the split-K reduction reads the fp32 partials and writes C)
-    "decode_64x8192x28672": {"source_digest": "44f8f6e523fb0714", "bytes_per_launch": 473500672 + 3272704},
+    "decode_64x8192x28672": {"source_digest": "7efc22286720fa41", "bytes_per_launch": 473500160 + 3192064},
     # one launch, no K split (the 256x112 pair): B read once, A and C
-    "decode_256x8192x8192": {"source_digest": "44f8f6e523fb0714", "bytes_per_launch": 138511104 + 3239680},
+    "decode_256x8192x8192": {"source_digest": "7efc22286720fa41", "bytes_per_launch": 138525184 + 3136512},
     # attention: captured at B2 (one launch); the B16 figure scales it by 8 (traffic grows with B)
-    "attn_gqa_b2_s4096_d128": {"source_digest": "dd1b44990baa0825", "bytes_per_launch": 199950848 + 110185984},
-    "attn_gqa_b16_s4096_d128": {"source_digest": "dd1b44990baa0825", "bytes_per_launch": 8 * (199950848 + 110185984)},
+    "attn_gqa_b2_s4096_d128": {"source_digest": "dd1b44990baa0825", "bytes_per_launch": 200624128 + 111305728},
+    "attn_gqa_b16_s4096_d128": {"source_digest": "dd1b44990baa0825", "bytes_per_launch": 8 * (200624128 + 111305728)},
     # D = 64 captured at the bench's own size (one launch)
-    "attn_gqa_b16_s4096_d64": {"source_digest": "dd1b44990baa0825", "bytes_per_launch": 2879983104 + 549222656},
+    "attn_gqa_b16_s4096_d64": {"source_digest": "dd1b44990baa0825", "bytes_per_launch": 2885150208 + 548860928},
 }
 
 

@@ -14,7 +14,7 @@
 // few tokens arrive per page, else eight warps. The new tokens of an item
 // stay in registers between the maximum and the rounding, so that they are read
 // once. A block does one item, so latency and the number of blocks on an SM
-// bound the kernel, and the issue of its instructions (70 % of the slots): the
+// bound the kernel, and the issue of its instructions (54 % of the slots): the
 // registers hold no more steps than a page needs, keys and values are in flight
 // together, both are asked for before the page's index is looked at, and what does
 // not depend on the data is known when it is compiled. 8 x 2048 tokens of 8 heads of

@@ -483,15 +483,19 @@ hk_status hk_kv8_append(const hk_kv8_cache* cache, const void* K, const void* V,
  * stands at position lengths[b] - n + t, n = counts[b] (NULL: T), and sees the
  * tokens up to it (the queries' own keys are in the cache); else it sees all
  * lengths[b]. A query that sees no token, and queries t >= counts[b], give a row
- * of zeros and a log-sum-exp of -inf. `scale` must not be
- * negative; 0: 1/sqrt(head_dim).
+ * of zeros and a log-sum-exp of -inf. A NaN among a token's values makes its
+ * dimension NaN in the queries that see the token and in no others. `scale` must not
+ * be negative; 0: 1/sqrt(head_dim).
  * Q and O are [B, T, Hq, head_dim] of `type` (bf16 or fp16), strides (b, t, head)
- * in elements, contiguous rows (O's must not overlap). lse, when not NULL: fp32 [B, T, Hq], natural
- * log of the sum of exp(scale · q·k).
+ * in elements, contiguous rows (O's must not overlap). lse, when not NULL: fp32
+ * [B, T, Hq], natural log of the sum of exp(scale · q·k).
  * Many query rows per KV head (a prompt) run on the attention-forward kernel when Q
  * is bf16 with rows that are 16-byte aligned; fp16 and other rows run on the
- * few-row kernel whatever their number (2048 tokens x 32 heads against 16384: 840 us
- * and 4180 us).
+ * few-row kernels whatever their number (2048 tokens x 64 heads of 128 against 16384: 806
+ * us and 4311 us).
+ * Scores, softmax sums and outputs are summed in fp32. Besides the rounding of O, the
+ * weights are rounded before they meet V: to f16 on the few-row kernels (2^-11 of a
+ * weight, down to 2^-29 of the row's largest), to bf16 on the many-row form (2^-8).
  * `workspace`: device memory of hk_attention_kv8_workspace_size(_ex) bytes, 256-byte
  * aligned, scratch of this call (calls that overlap on the GPU must not share
  * it). Asynchronous on `stream`; a bounded wait that runs out is reported by
