@@ -141,7 +141,8 @@ __device__ __forceinline__ Spread8<T> load_spread(const T* row, int64_t col, int
 
 // A global scale below 2^-60 is taken times 2^64 (kLift), and so is what meets it, so that s·g and its reciprocal
 // stay within fp32's normal numbers (for s·g < 2^-128 the reciprocal alone would be infinite). Powers of two:
-// every code and scale is the one that fp32 without a least exponent would give.
+// every code and scale is the one that fp32 without a least exponent would give. The kernels' loops are compiled
+// for both (one choice in the loop cost 18 % more instructions: 61.7 us for 57.6 at 16384 x 8192).
 constexpr float kSmallScale = 0x1p-60f;
 constexpr float kLift = 0x1p64f;
 
@@ -159,9 +160,9 @@ __device__ __forceinline__ void fill_reciprocals(float (&table)[128], float g) {
 }
 
 // Eight values of a block to codes; the block's scale byte. `six_g`, `per_six_g`:
-// 6·g and its reciprocal, both rounded to nearest; `lift`: kLift where g was lifted, else 1.
-template <int kFmt>
-__device__ __forceinline__ uint32_t quantize8(float (&v)[8], float six_g, float per_six_g, float lift, const float* reciprocals,
+// 6·g and its reciprocal, both rounded to nearest; kLifted: g was taken times kLift.
+template <int kFmt, bool kLifted>
+__device__ __forceinline__ uint32_t quantize8(float (&v)[8], float six_g, float per_six_g, const float* reciprocals,
                                               uint32_t& byte) {
     float m = amax3(v[0], v[1], v[2]);
     m = amax3(m, v[3], v[4]);
@@ -177,10 +178,10 @@ __device__ __forceinline__ uint32_t quantize8(float (&v)[8], float six_g, float 
     } else {
         // m / (6·g) to nearest by one correction of m · (1 / (6·g)) with its exact remainder (P. Markstein,
         // IBM J. Res. Dev. 34, 1990); where that leaves fp32's range the quotient is 0 or above 448 either way
-        if (lift != 1.0f) {              // (the same in every thread)
-            m = __fmul_rn(m, lift);
+        if constexpr (kLifted) {
+            m = __fmul_rn(m, kLift);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], lift);
+            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], kLift);
         }
         const float q0 = __fmul_rn(m, per_six_g);
         const float q = __fmaf_rn(__fmaf_rn(-q0, six_g, m), per_six_g, q0);
@@ -231,28 +232,12 @@ __device__ __forceinline__ Item item_of(uint64_t i, uint64_t items, uint32_t spa
     return Item{static_cast<int64_t>(row), static_cast<int64_t>(i - row * spans) * kSpanChunks};
 }
 
-// Block (32, kQuantWarps), every warp on items of its own: spans of the rows,
-// padding rows of the last scale tile included (their scales are 0).
-template <typename T, int kFmt>
-__global__ void __launch_bounds__(32 * kQuantWarps, 4)
-quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
-                const float* global_scale, uint32_t spans, int vec) {
-    __shared__ float staged[kQuantWarps][kChunkCols];
-    __shared__ float reciprocals[kFmt == kNvfp4 ? 128 : 1];
-    griddep_launch_dependents();
-    griddep_wait();                  // launched early behind the kernel that may have written x
+// Every warp on items of its own: spans of the rows, padding rows of the last scale tile included (their scales are 0).
+template <typename T, int kFmt, bool kLifted>
+__device__ __forceinline__ void quantize_items(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ld_codes,
+                                               uint8_t* scales, uint32_t spans, int vec, float* staged, const float* reciprocals,
+                                               float six_g, float per_six_g) {
     const uint32_t lane = threadIdx.x;
-    float six_g = 6.0f, per_six_g = 0.0f, lift = 1.0f;
-    if constexpr (kFmt == kNvfp4) {
-        float g = global_scale != nullptr ? *global_scale : 1.0f;
-        if (g < kSmallScale) {
-            lift = kLift;
-            g = __fmul_rn(g, kLift);
-        }
-        six_g = __fmul_rn(6.0f, g);
-        per_six_g = fminf(__fdiv_rn(1.0f, six_g), 3.4028235e38f);   // (finite: 0 times it is 0)
-        fill_reciprocals(reciprocals, g);
-    }
     const int64_t chunks = (cols + kChunkCols - 1) / kChunkCols;
     const int64_t whole = vec ? cols / kChunkCols : 0;     // chunks that are read 16 bytes at a time
     const int64_t code_cols = (cols + 31) / 32 * 32;
@@ -280,13 +265,13 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
             for (int i = 0; i < kSpanChunks; ++i) {
                 float v[8];
                 widen8<T>(raw[i], v);
-                *reinterpret_cast<uint32_t*>(out + i * (kChunkCols / 2)) = quantize8<kFmt>(v, six_g, per_six_g, lift, reciprocals, byte[i]);
+                *reinterpret_cast<uint32_t*>(out + i * (kChunkCols / 2)) = quantize8<kFmt, kLifted>(v, six_g, per_six_g, reciprocals, byte[i]);
             }
         } else {
             Spread8<T> raw[kSpanChunks];
 #pragma unroll
             for (int i = 0; i < kSpanChunks; ++i) raw[i] = load_spread<T>(src, (c0 + i) * kChunkCols, cols, lane);
-            float* const buf = staged[threadIdx.y];
+            float* const buf = staged;
 #pragma unroll
             for (int i = 0; i < kSpanChunks; ++i) {
                 __syncwarp();
@@ -295,7 +280,7 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
                 __syncwarp();
                 float v[8];
                 memcpy(v, buf + lane * 8, sizeof v);
-                const uint32_t packed = quantize8<kFmt>(v, six_g, per_six_g, lift, reciprocals, byte[i]);
+                const uint32_t packed = quantize8<kFmt, kLifted>(v, six_g, per_six_g, reciprocals, byte[i]);
                 if ((c0 + i) * kChunkCols + lane * 8 < code_cols)
                     *reinterpret_cast<uint32_t*>(dst + (c0 + i) * (kChunkCols / 2)) = packed;
             }
@@ -304,16 +289,44 @@ quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* co
     }
 }
 
+// Block (32, kQuantWarps).
+template <typename T, int kFmt>
+__global__ void __launch_bounds__(32 * kQuantWarps, 4)
+quantize_kernel(const T* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                const float* global_scale, uint32_t spans, int vec) {
+    __shared__ float staged[kQuantWarps][kChunkCols];
+    __shared__ float reciprocals[kFmt == kNvfp4 ? 128 : 1];
+    griddep_launch_dependents();
+    griddep_wait();                  // launched early behind the kernel that may have written x
+    if constexpr (kFmt == kNvfp4) {
+        float g = global_scale != nullptr ? *global_scale : 1.0f;
+        const bool small = g < kSmallScale;
+        if (small) g = __fmul_rn(g, kLift);
+        const float six_g = __fmul_rn(6.0f, g);
+        const float per_six_g = fminf(__fdiv_rn(1.0f, six_g), 3.4028235e38f);   // (finite: 0 times it is 0)
+        fill_reciprocals(reciprocals, g);
+        if (small)
+            quantize_items<T, kFmt, true>(x, rows, cols, ldx, codes, ld_codes, scales, spans, vec, staged[threadIdx.y], reciprocals,
+                                          six_g, per_six_g);
+        else
+            quantize_items<T, kFmt, false>(x, rows, cols, ldx, codes, ld_codes, scales, spans, vec, staged[threadIdx.y], reciprocals,
+                                           six_g, per_six_g);
+    } else {
+        quantize_items<T, kFmt, false>(x, rows, cols, ldx, codes, ld_codes, scales, spans, vec, staged[threadIdx.y], reciprocals, 6.0f,
+                                       0.0f);
+    }
+}
+
 // ----------------------------------------------------------- dequantise --
 
-// Eight codes times their scale (lifted, with `lower` 2^-64, or not, with 1), rounded once to T.
-template <typename T>
-__device__ __forceinline__ void dequantize8(uint32_t codes, float scale, float lower, T (&e)[8]) {
+// Eight codes times their scale, rounded once to T; kLifted: the scale was taken times kLift.
+template <typename T, bool kLifted>
+__device__ __forceinline__ void dequantize8(uint32_t codes, float scale, T (&e)[8]) {
     float v[8];
     unpack_e2m1x8(codes, v);
-    if (lower != 1.0f) {                 // (the same in every thread; v·scale does not fit fp32's normal numbers)
+    if constexpr (kLifted) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], scale), lower);
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], scale), 1.0f / kLift);
         scale = 1.0f;
     }
     const uint64_t s2 = f32x2(scale, scale);
@@ -332,19 +345,10 @@ __device__ __forceinline__ void dequantize8(uint32_t codes, float scale, float l
 }
 
 // y = code · (scale · g), rounded once to T.
-template <typename T, int kFmt>
-__global__ void __launch_bounds__(32 * kQuantWarps, 6)
-dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, const float* global_scale, int64_t rows,
-                  int64_t cols, T* y, int64_t ldy, uint32_t spans, int vec) {
-    __shared__ T staged[kQuantWarps][kChunkCols];
-    griddep_launch_dependents();
-    griddep_wait();                  // launched early behind the kernel that may have written the codes
+template <typename T, int kFmt, bool kLifted>
+__device__ __forceinline__ void dequantize_items(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, float g, int64_t rows,
+                                                 int64_t cols, T* y, int64_t ldy, uint32_t spans, int vec, T* staged) {
     const uint32_t lane = threadIdx.x;
-    float g = kFmt == kNvfp4 && global_scale != nullptr ? *global_scale : 1.0f, lower = 1.0f;
-    if (kFmt == kNvfp4 && g < kSmallScale) {
-        g = __fmul_rn(g, kLift);
-        lower = 1.0f / kLift;
-    }
     const int64_t chunks = (cols + kChunkCols - 1) / kChunkCols;
     const int64_t whole = vec ? cols / kChunkCols : 0;
     const int64_t code_cols = (cols + 31) / 32 * 32;
@@ -373,7 +377,7 @@ dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
 #pragma unroll
             for (int i = 0; i < kSpanChunks; ++i) {
                 T e[8];
-                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), kFmt == kNvfp4 ? lower : 1.0f, e);
+                dequantize8<T, kLifted>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
                 uint4 o[sizeof(T) / 2];
                 memcpy(o, e, sizeof o);
 #pragma unroll
@@ -389,12 +393,12 @@ dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
                     byte[i] = scale_at[i * kScaleStep];
                 }
             }
-            T* const buf = staged[threadIdx.y];
+            T* const buf = staged;
 #pragma unroll
             for (int i = 0; i < kSpanChunks; ++i) {
                 if (i >= n) break;
                 T e[8];
-                dequantize8<T>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), kFmt == kNvfp4 ? lower : 1.0f, e);
+                dequantize8<T, kLifted>(packed[i], kFmt == kNvfp4 ? scale_value<kFmt>(byte[i]) * g : scale_value<kFmt>(byte[i]), e);
                 __syncwarp();
                 memcpy(buf + lane * 8, e, sizeof e);
                 __syncwarp();
@@ -405,6 +409,21 @@ dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
             }
         }
     }
+}
+
+template <typename T, int kFmt>
+__global__ void __launch_bounds__(32 * kQuantWarps, 6)
+dequantize_kernel(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, const float* global_scale, int64_t rows,
+                  int64_t cols, T* y, int64_t ldy, uint32_t spans, int vec) {
+    __shared__ T staged[kQuantWarps][kChunkCols];
+    griddep_launch_dependents();
+    griddep_wait();                  // launched early behind the kernel that may have written the codes
+    const float g = kFmt == kNvfp4 && global_scale != nullptr ? *global_scale : 1.0f;
+    if (kFmt == kNvfp4 && g < kSmallScale)
+        dequantize_items<T, kFmt, kFmt == kNvfp4>(codes, ld_codes, scales, __fmul_rn(g, kLift), rows, cols, y, ldy, spans, vec,
+                                                  staged[threadIdx.y]);
+    else
+        dequantize_items<T, kFmt, false>(codes, ld_codes, scales, g, rows, cols, y, ldy, spans, vec, staged[threadIdx.y]);
 }
 
 }  // namespace fp4
