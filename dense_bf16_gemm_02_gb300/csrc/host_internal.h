@@ -15,9 +15,9 @@ namespace hk_host {
 // Records `msg` as the calling thread's last error and returns `s`.
 hk_status set_error(hk_status s, const char* msg);
 
-// The device status words ([0] error bits, [1] aborted launch id, [2] a cached
-// value was NaN, see kv8_prefill.cuh) shared by every one-shot entry point on
-// `device`; allocated on first use, four of them, as zeros.
+// The device status words ([0] error bits, [1] aborted launch id, [2] a count of
+// pages with NaN values, see kv8_prefill.cuh) shared by every one-shot entry point
+// on `device`; allocated on first use, four of them, as zeros.
 hk_status status_word(int device, uint32_t** out);
 
 // HK_OK when `device` is a compute capability 10.3 device (sets the error

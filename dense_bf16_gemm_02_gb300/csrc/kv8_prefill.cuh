@@ -17,9 +17,9 @@
 // tile spans few tokens (its causal edge wastes less).
 //
 // A value that is NaN would reach every row of a block of 128 tokens through weights of 0,
-// so the pass writes 0 in its place and notes that there was one; a last kernel, which
+// so the pass writes 0 in its place and counts the pages with one; a last kernel, which
 // otherwise ends at once (1.0 to 1.4 us of a call), then puts NaN into the rows that see
-// such a token.
+// such a token and takes its pages off the count.
 #pragma once
 
 #include <cstdint>
@@ -103,9 +103,9 @@ struct CachedItems {
     }
 };
 
-// The status word that says that a widened value was NaN, in this or an earlier call (it is never taken back: calls
-// on other streams may still be between the two kernels).
-constexpr int kNanSeen = 2;
+// The status word that counts widened pages (of a head and sequence) with NaN values, of all calls that are between
+// the pass and the kernel that takes them off again, on whatever stream. While it is 0 there is nothing to look for.
+constexpr int kNanPages = 2;
 
 struct WidenParams {
     const uint8_t* codes[2];       // keys, values
@@ -147,6 +147,7 @@ kv8_widen_kernel(const WidenParams p) {
     const int64_t dst = (static_cast<int64_t>(b) * p.Hkv + h) * p.rows + first;
     const int chunks = p.page_size * p.D / 16;
     const int chunk_shift = p.D == 128 ? 3 : 2;      // chunks of a token, as a shift
+    bool any_nan = false;
     for (int i = static_cast<int>(threadIdx.x); i < 2 * chunks; i += 256) {
         const int kv = i >= chunks ? 1 : 0;
         const int at = i - kv * chunks;
@@ -158,7 +159,7 @@ kv8_widen_kernel(const WidenParams p) {
             if (kv == 1) {
                 const uint32_t nan[4] = {nan_codes(w[0]), nan_codes(w[1]), nan_codes(w[2]), nan_codes(w[3])};
                 if (((nan[0] | nan[1]) | (nan[2] | nan[3])) != 0) {
-                    *reinterpret_cast<volatile uint32_t*>(p.status + kNanSeen) = 1u;
+                    any_nan = true;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) w[k] &= ~nan[k];
                 }
@@ -175,32 +176,42 @@ kv8_widen_kernel(const WidenParams p) {
         out[0] = make_uint4(o[0], o[1], o[2], o[3]);
         out[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    if (__syncthreads_or(any_nan) && threadIdx.x == 0) atomicAdd(p.status + kNanPages, 1u);
 }
 
 // After the attention kernel: NaN into every output that a NaN value belongs to; block (head, sequence). The first
 // token that holds a NaN, for each dimension, says which rows see one.
 static __global__ void __launch_bounds__(256)
 kv8_nan_values_kernel(const WidenParams w, const PrefillParams p) {
-    if (*reinterpret_cast<volatile uint32_t*>(w.status + kNanSeen) == 0u) return;
+    // (one thread looks: other blocks may take their pages off meanwhile, and a block goes or stays as a whole)
+    if (!__syncthreads_or(threadIdx.x == 0 && *reinterpret_cast<volatile uint32_t*>(w.status + kNanPages) != 0u)) return;
     __shared__ int first[128];
     const int h = static_cast<int>(blockIdx.x), b = static_cast<int>(blockIdx.y);
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
     const CachedItems::Seq s = CachedItems::seq(p, b);
     if (threadIdx.x < 128) first[threadIdx.x] = 0x7FFFFFFF;
     __syncthreads();
-    const int64_t chunks = static_cast<int64_t>(s.len) * (w.D / 16);      // 16 codes each
-    bool any = false;
-    for (int64_t i = threadIdx.x; i < chunks; i += 256) {
-        const int j = static_cast<int>(i / (w.D / 16)), d = static_cast<int>(i % (w.D / 16)) * 16;
-        const int64_t page = w.table[b * w.table_stride + j / w.page_size];
+    const int slots = (s.len + w.page_size - 1) / w.page_size, row_chunks = w.D / 16;
+    uint32_t pages = 0;                              // of this warp, with a NaN
+    for (int slot = static_cast<int>(warp); slot < slots; slot += 8) {
+        const int64_t page = w.table[b * w.table_stride + slot];
         if (page < 0 || page >= w.num_pages) continue;
-        const uint4 x = *reinterpret_cast<const uint4*>(w.codes[1] + ((page * w.Hkv + h) * w.page_size + j % w.page_size) * w.D + d);
-        const uint32_t nan[4] = {nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w)};
-        if (((nan[0] | nan[1]) | (nan[2] | nan[3])) == 0) continue;
-        any = true;
-        for (int k = 0; k < 16; ++k)
-            if (nan[k >> 2] >> (8 * (k & 3)) & 1u) atomicMin(&first[d + k], j);
+        const uint4* const codes = reinterpret_cast<const uint4*>(w.codes[1] + (page * w.Hkv + h) * w.page_size * w.D);
+        const int chunks = min(w.page_size, s.len - slot * w.page_size) * row_chunks;    // 16 codes each
+        bool any = false;
+#pragma unroll 4
+        for (int i = static_cast<int>(lane); i < chunks; i += 32) {
+            const uint4 x = codes[i];
+            const uint32_t nan[4] = {nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w)};
+            if (((nan[0] | nan[1]) | (nan[2] | nan[3])) == 0) continue;
+            any = true;
+            for (int k = 0; k < 16; ++k)
+                if (nan[k >> 2] >> (8 * (k & 3)) & 1u) atomicMin(&first[i % row_chunks * 16 + k], slot * w.page_size + i / row_chunks);
+        }
+        pages += __any_sync(0xffffffffu, any) ? 1u : 0u;
     }
-    if (!__syncthreads_or(any)) return;
+    if (lane == 0 && pages > 0) atomicSub(w.status + kNanPages, pages);
+    if (!__syncthreads_or(pages > 0)) return;
     const int64_t outputs = static_cast<int64_t>(s.count) * p.group * w.D;
     for (int64_t i = threadIdx.x; i < outputs; i += 256) {
         const int d = static_cast<int>(i % w.D), row = static_cast<int>(i / w.D);
