@@ -3,7 +3,10 @@ with its fused-epilogue (bias, activation, residual) and FP8 forms and the
 attention forward (MHA / GQA) built on the same tensor-core primitives; and the
 operators of a low-precision serving step: microscaled 4-bit matrices
 (``quantize_fp4``, ``dequantize_fp4``, ``gemm_fp4``) and a paged 8-bit key/value
-cache (``Kv8Cache``, ``kv8_append``, ``attention_kv8``).
+cache (``Kv8Cache``, ``kv8_append``, ``attention_kv8``); and those of a batch that
+shares its prompts: the pages that its sequences hold (``Kv8Pool``,
+``kv8_arrange``, ``kv8_compact``, ``kv8_copy_pages``) and the norm of each head's
+query and key with the rotation by its position (``qk_norm_rope``).
 
 The compute path is the CUDA library built from ``csrc/`` for sm_103a and
 reached through the C-ABI of ``include/hk_gemm.h``; this package is its
@@ -18,16 +21,23 @@ from .hk_gemm import (HK_ACT_GELU, HK_ACT_NONE, HK_ACT_RELU, HK_ACT_SILU, HK_ERR
                       HK_FP4_MXFP4, HK_FP4_NVFP4, HK_KV8_FAULT_DROP_ARRIVE, HK_KV8_FEW_ROWS, HK_KV8_MANY_ROWS,
                       HK_TYPE_BF16, HK_TYPE_FP16, HK_TYPE_FP32, hk_fp4_dequantize,
                       hk_attention_kv8, hk_attention_kv8_workspace_size, hk_fp4_quantize, hk_fp4_scales_size,
-                      hk_gemm_fp4, hk_gemm_fp4_ex, hk_kv8_append, hk_kv8_cache)
+                      hk_gemm_fp4, hk_gemm_fp4_ex, hk_kv8_append, hk_kv8_arrange, hk_kv8_arrange_workspace_size,
+                      hk_kv8_cache, hk_kv8_compact, hk_kv8_compact_workspace_size, hk_kv8_copy_pages, hk_kv8_pool,
+                      hk_qk_norm_rope)
 
 _LOW_PRECISION = ("Fp4Matrix", "quantize_fp4", "dequantize_fp4", "gemm_fp4", "Kv8Cache", "kv8_append", "attention_kv8")
+_SERVING = ("Kv8Pool", "kv8_arrange", "kv8_compact", "kv8_copy_pages", "qk_norm_rope")
 
 
 def __getattr__(name):
-    # the module that imports torch loads with the first use of one of its names
+    # the modules that import torch load with the first use of one of their names
     if name in _LOW_PRECISION:
         from . import low_precision
         globals().update({n: getattr(low_precision, n) for n in _LOW_PRECISION})
+        return globals()[name]
+    if name in _SERVING:
+        from . import serving
+        globals().update({n: getattr(serving, n) for n in _SERVING})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
@@ -42,5 +52,7 @@ __all__ = ["attention", "gemm", "Plan", "HKError", "load",
            "Fp4Matrix", "quantize_fp4", "dequantize_fp4", "gemm_fp4", "Kv8Cache", "kv8_append", "attention_kv8",
            "hk_kv8_cache", "hk_kv8_append", "hk_attention_kv8", "hk_attention_kv8_workspace_size",
            "hk_fp4_quantize", "hk_fp4_dequantize", "hk_fp4_scales_size", "hk_gemm_fp4", "hk_gemm_fp4_ex",
-           "HK_FP4_MXFP4", "HK_FP4_NVFP4", "HK_KV8_FAULT_DROP_ARRIVE", "HK_KV8_FEW_ROWS", "HK_KV8_MANY_ROWS",
+           "Kv8Pool", "kv8_arrange", "kv8_compact", "kv8_copy_pages", "qk_norm_rope", "hk_kv8_pool", "hk_kv8_arrange",
+           "hk_kv8_arrange_workspace_size", "hk_kv8_compact", "hk_kv8_compact_workspace_size", "hk_kv8_copy_pages",
+           "hk_qk_norm_rope", "HK_FP4_MXFP4", "HK_FP4_NVFP4", "HK_KV8_FAULT_DROP_ARRIVE", "HK_KV8_FEW_ROWS", "HK_KV8_MANY_ROWS",
            "HK_TYPE_BF16", "HK_TYPE_FP16", "HK_TYPE_FP32"]

@@ -7,8 +7,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <mutex>
 
@@ -16,91 +14,13 @@
 #include "host_internal.h"
 #include "kv8_append.cuh"
 #include "kv8_decode.cuh"
+#include "kv8_host.h"
 #include "kv8_prefill.cuh"
 
 namespace {
 
 using namespace hk::kv8;
-
-hk_status fail(hk_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-hk_status fail(hk_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    return hk_host::set_error(s, buf);
-}
-
-hk_status cuda_fail(hk_status s, const char* what, cudaError_t e) {
-    return fail(s, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;   // 1 s per bounded wait
-constexpr int kMaxDevices = 64;
-constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
-constexpr int kSms = 152;                               // the device's SMs: the workspace is sized without a device
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-constexpr int kMaxHeads = 65535;
-
-// (the sizes below stay within 64 bits for what passes; the tokens of a sequence, rounded up to a tile, within 31)
-bool cache_shape_ok(const hk_kv8_cache* c) {
-    return (c->head_dim == 64 || c->head_dim == 128) &&
-           (c->page_size == 16 || c->page_size == 32 || c->page_size == 64 || c->page_size == 128) && c->heads >= 1 &&
-           c->heads <= kMaxHeads && c->num_pages >= 1 && c->num_pages <= kLimit / c->heads;
-}
-bool table_width_ok(int64_t max_pages, int32_t page_size) { return max_pages >= 1 && max_pages <= (kLimit - 127) / page_size; }
-
-hk_status check_cache(const hk_kv8_cache* c) {
-    if (!c) return fail(HK_ERR_INVALID_ARG, "null cache");
-    if (c->head_dim != 64 && c->head_dim != 128)
-        return fail(HK_ERR_INVALID_ARG, "head dimension %d (supported: 64, 128)", (int)c->head_dim);
-    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
-        return fail(HK_ERR_INVALID_ARG, "page size %d (supported: 16, 32, 64, 128)", (int)c->page_size);
-    if (!cache_shape_ok(c))
-        return fail(HK_ERR_INVALID_ARG, "%lld pages of %d heads", (long long)c->num_pages, (int)c->heads);
-    if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return fail(HK_ERR_INVALID_ARG, "null cache pointer");
-    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
-        return fail(HK_ERR_MISALIGNED, "cache codes must be 16-byte aligned, scales 4-byte aligned");
-    return HK_OK;
-}
-
-hk_status check_table(const int32_t* table, int64_t stride, int64_t max_pages, int64_t B, const int32_t* lengths,
-                      const int32_t* counts, int32_t page_size) {
-    if (!table_width_ok(max_pages, page_size))
-        return fail(HK_ERR_INVALID_ARG, "a block table of %lld pages per sequence", (long long)max_pages);
-    if (stride < max_pages && B > 1) return fail(HK_ERR_INVALID_ARG, "block table rows overlap");
-    if (!table || !lengths) return fail(HK_ERR_INVALID_ARG, "null block table or lengths");
-    if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(counts, 4))
-        return fail(HK_ERR_MISALIGNED, "block table, lengths and counts must be 4-byte aligned");
-    return HK_OK;
-}
-
-hk_status current_device(int* device, int* sm_count) {
-    cudaError_t e = cudaGetDevice(device);
-    if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "cudaGetDevice", e);
-    if (*device < 0 || *device >= kMaxDevices) return fail(HK_ERR_INVALID_ARG, "device %d out of range", *device);
-    return hk_host::check_device(*device, sm_count);
-}
-
-// A launch that may begin while the kernel before it on the stream ends (the kernel waits for that end itself).
-template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*fn)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, args...);
-}
+using namespace hk_kv8;
 
 template <typename T, int kD, int kWarps>
 cudaError_t launch_append(const AppendParams& p, int steps, unsigned blocks, cudaStream_t st) {
@@ -115,22 +35,6 @@ template <typename T>
 cudaError_t launch_append(const AppendParams& p, int D, bool one_warp, int steps, unsigned blocks, cudaStream_t st) {
     if (D == 64) return one_warp ? launch_append<T, 64, 1>(p, steps, blocks, st) : launch_append<T, 64, 8>(p, steps, blocks, st);
     return one_warp ? launch_append<T, 128, 1>(p, steps, blocks, st) : launch_append<T, 128, 8>(p, steps, blocks, st);
-}
-
-int page_shift(int32_t page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
-
-// Codes of keys or values as [pages · heads, page_size, D] in boxes of up to 32 tokens of one head.
-hk_status encode_codes(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, const hk_kv8_cache* c) {
-    const cuuint64_t D = static_cast<cuuint64_t>(c->head_dim);
-    cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(c->page_size), static_cast<cuuint64_t>(c->num_pages) * c->heads};
-    cuuint64_t strides[2] = {D, D * c->page_size};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(std::min(c->page_size, kTileKeys)), 1};
-    cuuint32_t elem_strides[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, elem_strides,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(HK_ERR_INVALID_ARG, "encoding the tensor map of the cache failed (CUresult %d)", (int)r);
-    return HK_OK;
 }
 
 std::mutex g_setup_mutex;
@@ -516,10 +420,6 @@ size_t few_rows_bytes(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, i
     return decode_workspace(c, B, T, Hq).total;
 }
 
-bool rows_aligned(const void* ptr, const int64_t strides[3]) {
-    return aligned(ptr, 16) && strides[0] % 8 == 0 && strides[1] % 8 == 0 && strides[2] % 8 == 0;
-}
-
 // Can the tensor-core kernel run the call? It takes bf16 rows that TMA can read (aligned, and not one row for
 // several places) and writes 16 bytes at a time.
 bool many_rows_can(const void* Q, int32_t type, const int64_t q_strides[3], const void* O, const int64_t o_strides[3], int64_t B,
@@ -601,8 +501,8 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
         return prefill(Q, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse, B, T, Hq,
                        causal, scale_log2, workspace, status, flags, timeout_ns, enc, sms, st);
     CUtensorMap tk, tv;
-    if ((s = encode_codes(enc, &tk, cache->k_codes, cache)) != HK_OK) return s;
-    if ((s = encode_codes(enc, &tv, cache->v_codes, cache)) != HK_OK) return s;
+    if ((s = encode_codes(enc, &tk, cache->k_codes, cache, kTileKeys)) != HK_OK) return s;
+    if ((s = encode_codes(enc, &tv, cache->v_codes, cache, kTileKeys)) != HK_OK) return s;
 
     DecodeParams p = {};
     p.q_stride_b = q_strides[0];

@@ -249,14 +249,34 @@ __device__ __noinline__ uint2 edge_tile(uint32_t vb, int key0, int key_end, int 
     return found;
 }
 
-// One warp over tiles [first, last) of a unit (16 query rows rt of sequence b,
-// KV head h): the unnormalised output, maxima (log2 units) and this thread's
-// share of the sums. `ring`, `bars`: the warp's own stages and their barriers.
+// The 16 query rows rt of sequence b and KV head h: the pages that they read, and for each row where it lies,
+// whether it is a query at all, and how many tokens it sees.
+struct UnitRows {
+    const DecodeParams& p;
+    int b, h, rt;
+    const Sequence& seq;
+
+    __device__ __forceinline__ const int32_t* pages() const { return p.table + b * p.table_stride; }
+    __device__ __forceinline__ bool several() const { return p.T > 1; }      // can rows differ in what they see
+    template <typename T>
+    __device__ __forceinline__ const T* row(int r, bool& live, int& limit) const {
+        const int row = rt * kRows + r;
+        const int t = row / p.group;
+        live = t < seq.count;
+        // (rows past T are never stored and need no mask)
+        limit = t >= p.T ? 0x7FFFFFFF : !live ? 0 : p.causal ? max(0, seq.len - seq.count + t + 1) : seq.len;
+        return static_cast<const T*>(p.q) + b * p.q_stride_b + t * p.q_stride_t +
+               static_cast<int64_t>(h * p.group + row % p.group) * p.q_stride_h;
+    }
+};
+
+// One warp over tiles [first, last) of a unit (16 query rows, KV head h): the
+// unnormalised output, maxima (log2 units) and this thread's share of the sums. `ring`, `bars`: the warp's own stages and their barriers.
 // False when a wait gave up (the copies in flight are then still to be waited for).
-template <int kD, typename T, int kStages>
+template <int kD, typename T, int kStages, class Rows>
 __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k, const void* tmap_v, uint32_t ring, uint32_t bars,
-                                       int& fills, int& uses, int b, int h, int rt, const Sequence& seq, int key_end, int first,
-                                       int last, float (&o)[kD / 8][4], float (&m)[2], float (&l)[2]) {
+                                       int& fills, int& uses, const Rows& rows, int h, int key_end, int first, int last,
+                                       float (&o)[kD / 8][4], float (&m)[2], float (&l)[2]) {
     constexpr int kWords = kD / 16;          // 4-code words of a row that a thread holds (one K step each)
     constexpr int kNTiles = kD / 8;          // 8-column tiles of the output
     constexpr int kOwn = kD / 4;             // output columns of a thread
@@ -276,7 +296,7 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
     auto look_up = [&](Window& w, int tile0) {
         auto page_of = [&](int key) {
             if (key >= key_end) return -1;
-            const int32_t pg = p.table[b * p.table_stride + (key >> p.page_shift)];
+            const int32_t pg = rows.pages()[key >> p.page_shift];
             if (pg < 0 || pg >= p.num_pages) {
                 atomicOr(p.wait.status, kErrPage);
                 return -1;
@@ -340,13 +360,8 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
     int limit[2];                        // tokens the row sees
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int row = rt * kRows + static_cast<int>(g) + 8 * i;
-        const int t = row / p.group;
-        const bool live = t < seq.count;
-        // (rows past T are never stored and need no mask)
-        limit[i] = t >= p.T ? 0x7FFFFFFF : !live ? 0 : p.causal ? max(0, seq.len - seq.count + t + 1) : seq.len;
-        const T* const src = static_cast<const T*>(p.q) + b * p.q_stride_b + t * p.q_stride_t +
-                             static_cast<int64_t>(h * p.group + row % p.group) * p.q_stride_h;
+        bool live;
+        const T* const src = rows.template row<T>(static_cast<int>(g) + 8 * i, live, limit[i]);
         Raw8<T> rawq[kD / 32];
         uint32_t top = 0;
 #pragma unroll
@@ -406,7 +421,7 @@ __device__ __forceinline__ bool attend(const DecodeParams& p, const void* tmap_k
         const int key0 = tile * kTileKeys;
         const bool masked = key0 + kTileKeys > all_see;      // (all_see is at most key_end)
         if (masked) {
-            const uint2 found = edge_tile<kD>(vb, key0, key_end, limit[0], limit[1], p.T > 1);
+            const uint2 found = edge_tile<kD>(vb, key0, key_end, limit[0], limit[1], rows.several());
             nan_at[0] |= found.x;
             nan_at[1] |= found.y;
         }
@@ -615,7 +630,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         const int last = static_cast<int>(min(static_cast<int64_t>(unit_tiles), first + (end - at)));   // tiles [first, last)
 
         float o[kNTiles][4], m[2], l[2];
-        ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, b, h, rt, seq, key_end, first, last, o, m, l);
+        ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, UnitRows{p, b, h, rt, seq}, h, key_end, first,
+                                       last, o, m, l);
         if (!ok) break;
 
         // ---- finish the unit or leave its partial sums
@@ -754,7 +770,8 @@ kv8_decode_block_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid
         float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         if (first < last) {
             int fills = 0, uses = 0;
-            ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, b, h, rt, seq, key_end, first, last, o, m, l);
+            ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, UnitRows{p, b, h, rt, seq}, h, key_end, first,
+                                       last, o, m, l);
             if (ok) {
                 float* const part = reinterpret_cast<float*>(smem + warp * G::kWarpBytes);
 #pragma unroll

@@ -66,7 +66,8 @@ EXPORTED = (
     "hk_attention_fwd", "hk_attention_fwd_ex", "hk_gemm_mxfp8", "hk_gemm_mxfp8_ex", "hk_gemm_mxfp8_workspace_size",
     "hk_fp4_scales_size", "hk_fp4_quantize", "hk_fp4_dequantize", "hk_gemm_fp4", "hk_gemm_fp4_ex",
     "hk_kv8_append", "hk_attention_kv8", "hk_attention_kv8_ex", "hk_attention_kv8_workspace_size",
-    "hk_attention_kv8_workspace_size_ex",
+    "hk_attention_kv8_workspace_size_ex", "hk_kv8_arrange", "hk_kv8_arrange_workspace_size", "hk_kv8_compact",
+    "hk_kv8_compact_workspace_size", "hk_kv8_copy_pages", "hk_qk_norm_rope",
 )
 
 
@@ -95,6 +96,12 @@ class hk_kv8_cache(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class hk_kv8_pool(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("rows", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class HKError(RuntimeError):
@@ -190,6 +197,18 @@ def load() -> ctypes.CDLL:
         lib.hk_attention_kv8_workspace_size.restype = SZ
         lib.hk_attention_kv8_workspace_size_ex.argtypes = [P, I32, P, CP, I64, P, P, I64, I64, I64, U32]
         lib.hk_attention_kv8_workspace_size_ex.restype = SZ
+        lib.hk_kv8_arrange.argtypes = [P, P, P, P, P, I32, P, P, P, SZ, P]
+        lib.hk_kv8_arrange.restype = I32
+        lib.hk_kv8_compact.argtypes = [P, P, I32, P, P, SZ, P]
+        lib.hk_kv8_compact.restype = I32
+        for size in (lib.hk_kv8_arrange_workspace_size, lib.hk_kv8_compact_workspace_size):
+            size.argtypes = [P]
+            size.restype = SZ
+        lib.hk_kv8_copy_pages.argtypes = [P, P, I32, P, P, I64, P]
+        lib.hk_kv8_copy_pages.restype = I32
+        lib.hk_qk_norm_rope.argtypes = [P, P, P, P, P, P, P, P, I32, I64, I64, I64, I64, I64, P, P, I32, F, P, P, P, I32, P,
+                                        I64, I32, P]
+        lib.hk_qk_norm_rope.restype = I32
         _lib = lib
         return lib
 
@@ -310,6 +329,52 @@ def hk_attention_kv8(Q: int, type: int, q_strides, cache: hk_kv8_cache, block_ta
 
 def hk_attention_kv8_workspace_size(cache: hk_kv8_cache, B: int, T: int, Hq: int, max_pages: int) -> int:
     return int(load().hk_attention_kv8_workspace_size(ctypes.byref(cache), B, T, Hq, max_pages))
+
+
+def _cache_array(caches):
+    return (hk_kv8_cache * max(1, len(caches)))(*caches)
+
+
+def hk_kv8_arrange(pool: hk_kv8_pool, keep: int, room: int, parents: int = 0, caches=(), copies: int = 0, missing: int = 0,
+                   workspace: int = 0, workspace_bytes: int = 0, stream: int = 0) -> int:
+    """Arrange a pool's rows anew (caches: a sequence of hk_kv8_cache)."""
+    return load().hk_kv8_arrange(ctypes.byref(pool), keep, room, parents or None, _cache_array(caches), len(caches),
+                                 copies or None, missing, workspace or None, workspace_bytes, stream)
+
+
+def hk_kv8_arrange_workspace_size(pool: hk_kv8_pool) -> int:
+    return int(load().hk_kv8_arrange_workspace_size(ctypes.byref(pool)))
+
+
+def hk_kv8_compact(pool: hk_kv8_pool, caches=(), moved: int = 0, workspace: int = 0, workspace_bytes: int = 0,
+                   stream: int = 0) -> int:
+    """Move a pool's pages together."""
+    return load().hk_kv8_compact(ctypes.byref(pool), _cache_array(caches), len(caches), moved, workspace or None,
+                                 workspace_bytes, stream)
+
+
+def hk_kv8_compact_workspace_size(pool: hk_kv8_pool) -> int:
+    return int(load().hk_kv8_compact_workspace_size(ctypes.byref(pool)))
+
+
+def hk_kv8_copy_pages(dst, src, dst_pages: int, src_pages: int, n: int, stream: int = 0) -> int:
+    """Copy n listed pages of each cache of `src` to those of `dst` (sequences of hk_kv8_cache)."""
+    if len(dst) != len(src):
+        return HK_ERR_INVALID_ARG
+    return load().hk_kv8_copy_pages(_cache_array(dst), _cache_array(src), len(dst), dst_pages, src_pages, n, stream)
+
+
+def hk_qk_norm_rope(Q: int, q_strides, K: int, k_strides, QO: int, qo_strides, KO: int, ko_strides, type: int, B: int, T: int,
+                    Hq: int, Hk: int, D: int, q_weight: int = 0, k_weight: int = 0, weight_type: int = 2, eps: float = 1e-6,
+                    positions: int = 0, pos_strides=(0, 0, 0), sections=None, axes: int = 1, inv_freq: int = 0, pairs: int = 0,
+                    interleaved: int = 0, stream: int = 0) -> int:
+    """Norm of each head's query and key and the rotation by position (strides: sequences of three element strides)."""
+    I3 = ctypes.c_int64 * 3
+    return load().hk_qk_norm_rope(Q or None, I3(*q_strides), K or None, I3(*k_strides), QO or None, I3(*qo_strides), KO or None,
+                                  I3(*ko_strides), type, B, T, Hq, Hk, D, q_weight or None, k_weight or None, weight_type, eps,
+                                  positions or None, I3(*pos_strides),
+                                  (ctypes.c_int32 * axes)(*sections) if sections is not None else None, axes, inv_freq or None,
+                                  pairs, int(interleaved), stream)
 
 
 def hk_gemm_last_device_status(device: int) -> int:

@@ -1,0 +1,213 @@
+"""Torch conveniences over the entry points of ``include/hk_gemm.h`` for a batch
+that shares its prompts: the pages of the 8-bit cache that its sequences hold
+(``Kv8Pool``, ``kv8_arrange``, ``kv8_compact``, ``kv8_copy_pages``) and the norm of
+each head's query and key with the rotation by its position (``qk_norm_rope``).
+
+As in ``low_precision``, this is argument marshalling: every step runs in the CUDA
+library, on ``stream`` (default: torch's current stream), nothing is read back, and
+the tensors are on torch's current device.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import hk_gemm as _hk
+from .hk_gemm import HK_OK, HKError
+from .low_precision import Kv8Cache, _check_vector, _empty, _f32, _i32, _read_only, _row_stride, _stream, _strides, _type_code, _u8
+
+_pool_struct = struct.Struct("PPPqq4i").pack       # hk_kv8_pool
+
+
+class Kv8Pool:
+    """Which pages of an 8-bit cache (or of several alike: a model's layers) its sequences hold.
+
+    ``refs`` int32 [pages]: table entries that name each page (0: free);
+    ``table`` int32 [rows, max_pages]: the block table that kv8_append and
+    attention_kv8 take; ``held`` int32 [rows]: tokens whose pages a row has.
+    CUDA tensors; ``Kv8Pool.empty`` makes them, with nothing held. None of them can be
+    set to another tensor."""
+
+    __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref")
+    refs, table, held = (_read_only(n) for n in __slots__[:3])
+    pages, rows, max_pages, page_size = (_read_only(n) for n in __slots__[3:7])
+
+    def __init__(self, refs, table, held, page_size=64):
+        for t, dim in ((refs, 1), (table, 2), (held, 1)):
+            if not isinstance(t, torch.Tensor) or t.dtype != _i32 or not t.is_cuda or t.dim() != dim:
+                raise TypeError("refs and held must be 1-D, table 2-D int32 CUDA tensors")
+        if refs.get_device() != table.get_device() or held.get_device() != table.get_device():
+            raise ValueError("a pool's tensors must be on one device")
+        rows, max_pages = table.shape
+        if held.size(0) != rows:
+            raise ValueError(f"table has {rows} rows, held {held.size(0)}")
+        if not refs.is_contiguous() or not held.is_contiguous():
+            raise ValueError("refs and held must be contiguous")
+        self._refs, self._table, self._held = refs, table, held
+        self._pages, self._rows, self._max_pages, self._page_size = refs.size(0), rows, max_pages, page_size
+        self._ref = _pool_struct(refs.data_ptr(), table.data_ptr(), held.data_ptr(), refs.size(0), _row_stride(table, "table"),
+                                 rows, max_pages, page_size, 0)
+
+    @classmethod
+    def empty(cls, pages, rows, max_pages, page_size=64, device="cuda"):
+        """A pool of `pages` free pages and `rows` rows that hold nothing."""
+        return cls(torch.zeros(pages, dtype=_i32, device=device), torch.zeros(rows, max_pages, dtype=_i32, device=device),
+                   torch.zeros(rows, dtype=_i32, device=device), page_size)
+
+
+def _check_pool(pool):
+    if not isinstance(pool, Kv8Pool):
+        raise TypeError("pool must be a Kv8Pool")
+
+
+def _cache_refs(caches, name):
+    """The caches' structures side by side, as the entry points take them."""
+    if isinstance(caches, Kv8Cache):
+        caches = (caches,)
+    refs = []
+    for c in caches:
+        if not isinstance(c, Kv8Cache):
+            raise TypeError(f"{name} must be Kv8Caches")
+        refs.append(c._ref)
+    return b"".join(refs), len(refs)
+
+
+def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=None, stream=None):
+    """Arrange the pool's rows anew, all at once: row i becomes the first ``keep[i]``
+    tokens of what row ``parents[i]`` was (None: of its own), with pages for
+    ``room[i]`` tokens (None: keep). int32 CUDA tensors [rows].
+
+    room above what a row holds takes pages, keep below it cuts the row back (0 ends
+    it), another parent forks or reorders. Whole pages within keep are shared, the ones
+    that will be written are the row's own: copied in each of ``caches`` where they hold
+    tokens. Returns a 0-dim int32 tensor: 0; or the pages that lacked, or -1 for
+    arguments out of range, and then nothing was changed. What a call frees is free for the next
+    one. ``copies``: an int32 tensor [2, rows] that receives the copied pages and their
+    copies (-1: none). See hk_kv8_arrange."""
+    _check_pool(pool)
+    if room is None:
+        room = keep
+    _check_vector(keep, "keep", pool._rows)
+    _check_vector(room, "room", pool._rows)
+    if parents is not None:
+        _check_vector(parents, "parents", pool._rows)
+    if copies is not None and (not isinstance(copies, torch.Tensor) or copies.dtype != _i32 or not copies.is_cuda
+                               or tuple(copies.shape) != (2, pool._rows) or not copies.is_contiguous()):
+        raise TypeError("copies must be a contiguous int32 CUDA tensor [2, rows]")
+    refs, n = _cache_refs(caches, "caches")
+    lib = _hk.load()
+    size = lib.hk_kv8_arrange_workspace_size(pool._ref)
+    workspace = _empty(max(size, 1), _u8, keep, stream)
+    missing = _empty((), _i32, keep, stream)
+    st = lib.hk_kv8_arrange(pool._ref, keep.data_ptr(), room.data_ptr(), None if parents is None else parents.data_ptr(), refs, n,
+                            None if copies is None else copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(), size,
+                            _stream(stream, keep))
+    if st != HK_OK:
+        raise HKError(st, "hk_kv8_arrange")
+    return missing
+
+
+def kv8_compact(pool: Kv8Pool, caches=(), stream=None):
+    """Move the pool's pages in use to its first places, in each of ``caches`` and in
+    the table. Returns int32 [pages]: where each page is now, -1 where it was free. See
+    hk_kv8_compact."""
+    _check_pool(pool)
+    refs, n = _cache_refs(caches, "caches")
+    lib = _hk.load()
+    size = lib.hk_kv8_compact_workspace_size(pool._ref)
+    workspace = _empty(max(size, 1), _u8, pool._refs, stream)
+    moved = _empty(pool._pages, _i32, pool._refs, stream)
+    st = lib.hk_kv8_compact(pool._ref, refs, n, moved.data_ptr(), workspace.data_ptr(), size, _stream(stream, moved))
+    if st != HK_OK:
+        raise HKError(st, "hk_kv8_compact")
+    return moved
+
+
+def kv8_copy_pages(dst, src, dst_pages, src_pages, stream=None) -> None:
+    """Copy page ``src_pages[i]`` of each cache of ``src`` to page ``dst_pages[i]`` of
+    its counterpart in ``dst`` (one Kv8Cache or several; they may be the same ones): int32
+    CUDA tensors; -1 in both leaves the entry out. See hk_kv8_copy_pages."""
+    to, n = _cache_refs(dst, "dst")
+    of, m = _cache_refs(src, "src")
+    if n != m:
+        raise ValueError(f"{n} caches to copy to, {m} to copy from")
+    if not isinstance(src_pages, torch.Tensor) or src_pages.dim() != 1:
+        raise TypeError("src_pages must be a 1-D int32 CUDA tensor")
+    _check_vector(src_pages, "src_pages", src_pages.size(0))
+    _check_vector(dst_pages, "dst_pages", src_pages.size(0))
+    st = _hk.load().hk_kv8_copy_pages(to, of, n, dst_pages.data_ptr(), src_pages.data_ptr(), src_pages.size(0),
+                                      _stream(stream, src_pages))
+    if st != HK_OK:
+        raise HKError(st, "hk_kv8_copy_pages")
+
+
+def _heads(t, name, like):
+    """(B, T, heads, head_dim) and packed strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+        raise TypeError(f"{name} must be a CUDA tensor [B, T, heads, head_dim]")
+    if t.stride(3) != 1 and t.size(3) > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if like is not None and (t.dtype != like.dtype or t.shape[:2] != like.shape[:2] or t.shape[3] != like.shape[3]):
+        raise ValueError(f"{name} must have q's type, batch, tokens and head dimension")
+    return _strides(*t.stride()[:3])
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, sections=None, interleaved=False, out=None,
+                 stream=None):
+    """Norm of each head's query and key and the rotation by its token's position, in one
+    pass: x / sqrt(mean(x²) + eps) · weight, then the pairs (i, i + R/2) of the first R =
+    2 · len(inv_freq) elements (``interleaved``: (2i, 2i + 1)) turned by position · inv_freq[i].
+
+    q [B, T, Hq, D], k [B, T, Hk, D] (bf16, fp16 or fp32; any strides with contiguous rows),
+    ``positions`` int32 [B, T], or [axes, B, T] with ``sections``: the numbers of successive
+    pairs that turn by each axis. ``inv_freq`` float32 [R/2]. Weights [D] of q's type or
+    float32, both alike; None: 1. eps None: no norm. ``out``: (q', k') to write into, q and k
+    themselves among others. Returns (q', k'). See hk_qk_norm_rope."""
+    qs, ks = _heads(q, "q", None), _heads(k, "k", q)
+    code = _type_code(q, "q")
+    B, T, Hq, D = q.shape
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != _f32 or not inv_freq.is_cuda or inv_freq.dim() != 1 \
+            or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous 1-D float32 CUDA tensor")
+    if not isinstance(positions, torch.Tensor) or positions.dtype != _i32 or not positions.is_cuda or positions.dim() not in (2, 3):
+        raise TypeError("positions must be an int32 CUDA tensor [B, T] or [axes, B, T]")
+    if positions.shape[-2:] != q.shape[:2]:
+        raise ValueError(f"positions {tuple(positions.shape)} for {B} sequences of {T} tokens")
+    axes = positions.size(0) if positions.dim() == 3 else 1
+    if sections is not None:
+        if len(sections) != axes:
+            raise ValueError(f"{len(sections)} sections for {axes} position axes")
+        sections = (ctypes.c_int32 * axes)(*sections)
+    weight_code = code
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dim() != 1 or w.size(0) != D or not w.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous CUDA tensor [{D}]")
+        if w.dtype not in (q.dtype, _f32):
+            raise TypeError(f"{name} must be of q's type or float32")
+        weight_code = _type_code(w, name)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must be of one type")
+    if eps is None:
+        eps = -1.0
+    elif eps < 0:
+        raise ValueError("eps must not be negative (None: no norm)")
+    if out is None:
+        qo, ko = _empty(q.shape, q.dtype, q, stream), _empty(k.shape, k.dtype, k, stream)
+    else:
+        qo, ko = out
+    qos, kos = _heads(qo, "out", q), _heads(ko, "out", q)
+    if qo.shape != q.shape or ko.shape != k.shape:
+        raise ValueError("out must have q's and k's shapes")
+    pos = positions.stride() if axes > 1 or positions.dim() == 3 else (0, *positions.stride())
+    st = _hk.load().hk_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, qo.data_ptr(), qos, ko.data_ptr(), kos, code, B, T, Hq,
+                                    k.size(2), D, None if q_weight is None else q_weight.data_ptr(),
+                                    None if k_weight is None else k_weight.data_ptr(), weight_code, eps, positions.data_ptr(),
+                                    _strides(*pos), sections, axes, inv_freq.data_ptr(), inv_freq.size(0), 1 if interleaved else 0,
+                                    _stream(stream, q))
+    if st != HK_OK:
+        raise HKError(st, "hk_qk_norm_rope")
+    return qo, ko

@@ -536,6 +536,94 @@ size_t hk_attention_kv8_workspace_size_ex(const void* Q, int32_t type, const int
                                           const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq,
                                           uint32_t flags);
 
+/* ---------------------------------------------------------------------------
+ * Which pages of the cache a sequence holds: growing, cutting back, ending, forking and
+ * reordering sequences, and moving pages together. All of it runs on the device (nothing is
+ * read back, so that it may be captured in a graph).
+ *
+ * A pool goes with one or several caches of the same pages (a model's layers):
+ *   refs    int32 [num_pages]: how many table entries name each page; 0: it is free
+ *   table   int32 [rows, max_pages], table_stride elements between rows: the block table that
+ *           hk_kv8_append and hk_attention_kv8 read
+ *   held    int32 [rows]: tokens whose pages a row has, ceil(held / page_size) entries; entries
+ *           past them mean nothing
+ * An empty pool is refs and held of zeros. num_pages at most 2^30, rows · max_pages below 2^31. */
+typedef struct hk_kv8_pool {
+    int32_t* refs;
+    int32_t* table;
+    int32_t* held;
+    int64_t num_pages;
+    int64_t table_stride;
+    int32_t rows;
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t reserved;
+} hk_kv8_pool;
+
+/* Arrange the pool's rows anew, all at once: row i becomes the first keep[i] tokens of what row
+ * parents[i] was before the call (NULL: of its own), with pages for room[i] >= keep[i] tokens.
+ * keep, room, parents: int32 [rows] on the device. So
+ *   room[i] above what row i holds      takes pages (for tokens to come),
+ *   keep[i] below it                    cuts the row back; keep = room = 0 ends it,
+ *   parents[i] = j                      forks row j, or (for several rows) reorders them.
+ * Pages that are whole within keep[i] are shared with the parent. The pages above, into which
+ * tokens will be appended, belong to row i alone: it goes on in its parent's where it is the parent's
+ * heir (i itself where parents[i] = i; else, where the parent becomes another row's, the lowest
+ * row with that parent), no other entry names the page and no other row keeps it whole; else in free pages, the
+ * lowest ones first, in order of row and slot. Of a page that holds tokens of keep[i] the contents are copied
+ * in every one of the n_caches caches. keep[i] counts tokens that were appended, not
+ * only held: a page that counts as whole is not written again.
+ * Free are pages with refs = 0 before the call; what the call frees is free for the next one.
+ * *missing (device): 0, or the pages that lacked, or -1: a row's parent, tokens or page
+ * index is out of range (hk_gemm_last_device_status then reports HK_ERR_INVALID_ARG). Unless it is 0 nothing
+ * was changed. `copies` (device, or NULL): int32 [2, rows], each row's page that was copied and
+ * its copy, -1 where there is none (for other caches: hk_kv8_copy_pages).
+ * `workspace`: device memory of hk_kv8_arrange_workspace_size bytes, 256-byte aligned, scratch of
+ * this call. Asynchronous on `stream`, allocates nothing (but the status word, once). */
+hk_status hk_kv8_arrange(const hk_kv8_pool* pool, const int32_t* keep, const int32_t* room, const int32_t* parents,
+                         const hk_kv8_cache* caches, int32_t n_caches, int32_t* copies, int32_t* missing,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t hk_kv8_arrange_workspace_size(const hk_kv8_pool* pool);
+
+/* Move the U pages in use to the places [0, U): the k-th used page at U or above goes to the k-th free page
+ * below U, in every cache, in the table and in refs. moved: int32 [num_pages] on the device, where
+ * each page is now, -1 where it was free. A page index out of range in a row's entries stays as it is and
+ * hk_gemm_last_device_status reports HK_ERR_INVALID_ARG. Workspace and asynchrony as above. */
+hk_status hk_kv8_compact(const hk_kv8_pool* pool, const hk_kv8_cache* caches, int32_t n_caches, int32_t* moved,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t hk_kv8_compact_workspace_size(const hk_kv8_pool* pool);
+
+/* Copy page src_pages[i] of each src[j] to page dst_pages[i] of dst[j] (codes and scales), i < n, j <
+ * n_caches; entries of -1 in both lists are left out. dst[j] may be src[j] or another cache of the same heads,
+ * page size and head dimension (a larger pool); no page may be written twice or be read and written
+ * in one call. An index out of range is not followed and hk_gemm_last_device_status
+ * reports HK_ERR_INVALID_ARG. Asynchronous on `stream`. */
+hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, int32_t n_caches,
+                            const int32_t* dst_pages, const int32_t* src_pages, int64_t n, void* stream);
+
+/* The norm of each head's query and key and the rotation by its token's position, in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) · w;   (a, b) -> (a cos t - b sin t, a sin t + b cos t)
+ * over pairs i < `pairs` of y: (y[i], y[i + pairs]), or with `interleaved` (y[2i], y[2i + 1]); the
+ * elements from 2·pairs on are not turned. t = positions[axis(i)] · inv_freq[i]: pairs [0, sections[0]) turn by
+ * the first axis, the next sections[1] by the second, and so on (time, height, width; `sections` is a HOST
+ * array of `axes` numbers, 1 to 4, that add up to `pairs`; NULL with one axis).
+ * Q [B, T, Hq, D] and K [B, T, Hk, D] of `type` (bf16, fp16 or fp32), their outputs QO and KO, each with strides (b, t,
+ * head) in elements and contiguous rows; an output may be its input (then with its strides), else it must
+ * not overlap one, and its rows must not overlap. Hq or Hk 0 leaves that operand out. D a multiple of 8 up to
+ * 256, pairs a multiple of 8. q_weight, k_weight [D] of `type` or fp32 (weight_type), NULL: 1. eps < 0: no
+ * norm (and no weights). positions: int32 on the device with strides (axis, b, t) in elements;
+ * inv_freq: fp32 [pairs] on the device, of magnitude below 2^10 (above, bits of the angle are lost; not
+ * finite: NaN).
+ * The norm is summed in fp32, t is exact to 2^-31 of a turn whatever the position (for
+ * frequencies up to 1), and the result is rounded once.
+ * Asynchronous on `stream`, allocates nothing. */
+hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], const void* K, const int64_t k_strides[3],
+                          void* QO, const int64_t qo_strides[3], void* KO, const int64_t ko_strides[3], int32_t type,
+                          int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D, const void* q_weight,
+                          const void* k_weight, int32_t weight_type, float eps, const int32_t* positions,
+                          const int64_t pos_strides[3], const int32_t* sections, int32_t axes, const float* inv_freq,
+                          int64_t pairs, int32_t interleaved, void* stream);
+
 /* Static description of a status code. */
 const char* hk_status_string(hk_status status);
 
