@@ -5,8 +5,9 @@ operators of a low-precision serving step: microscaled 4-bit matrices
 (``quantize_fp4``, ``dequantize_fp4``, ``gemm_fp4``) and a paged 8-bit key/value
 cache (``Kv8Cache``, ``kv8_append``, ``attention_kv8``); and those of a batch that
 shares its prompts: the pages that its sequences hold (``Kv8Pool``,
-``kv8_arrange``, ``kv8_compact``, ``kv8_copy_pages``) and the norm of each head's
-query and key with the rotation by its position (``qk_norm_rope``).
+``kv8_arrange``, ``kv8_compact``, ``kv8_copy_pages``), the norm of each head's
+query and key with the rotation by its position (``qk_norm_rope``), and the
+attention that reads shared pages once (``attention_kv8_shared``).
 
 The compute path is the CUDA library built from ``csrc/`` for sm_103a and
 reached through the C-ABI of ``include/hk_gemm.h``; this package is its
@@ -23,10 +24,10 @@ from .hk_gemm import (HK_ACT_GELU, HK_ACT_NONE, HK_ACT_RELU, HK_ACT_SILU, HK_ERR
                       hk_attention_kv8, hk_attention_kv8_workspace_size, hk_fp4_quantize, hk_fp4_scales_size,
                       hk_gemm_fp4, hk_gemm_fp4_ex, hk_kv8_append, hk_kv8_arrange, hk_kv8_arrange_workspace_size,
                       hk_kv8_cache, hk_kv8_compact, hk_kv8_compact_workspace_size, hk_kv8_copy_pages, hk_kv8_pool,
-                      hk_qk_norm_rope)
+                      hk_qk_norm_rope, hk_attention_kv8_shared, hk_attention_kv8_shared_workspace_size)
 
 _LOW_PRECISION = ("Fp4Matrix", "quantize_fp4", "dequantize_fp4", "gemm_fp4", "Kv8Cache", "kv8_append", "attention_kv8")
-_SERVING = ("Kv8Pool", "kv8_arrange", "kv8_compact", "kv8_copy_pages", "qk_norm_rope")
+_SERVING = ("attention_kv8_shared", "Kv8Pool", "kv8_arrange", "kv8_compact", "kv8_copy_pages", "qk_norm_rope")
 
 
 def __getattr__(name):
@@ -54,5 +55,6 @@ __all__ = ["attention", "gemm", "Plan", "HKError", "load",
            "hk_fp4_quantize", "hk_fp4_dequantize", "hk_fp4_scales_size", "hk_gemm_fp4", "hk_gemm_fp4_ex",
            "Kv8Pool", "kv8_arrange", "kv8_compact", "kv8_copy_pages", "qk_norm_rope", "hk_kv8_pool", "hk_kv8_arrange",
            "hk_kv8_arrange_workspace_size", "hk_kv8_compact", "hk_kv8_compact_workspace_size", "hk_kv8_copy_pages",
-           "hk_qk_norm_rope", "HK_FP4_MXFP4", "HK_FP4_NVFP4", "HK_KV8_FAULT_DROP_ARRIVE", "HK_KV8_FEW_ROWS", "HK_KV8_MANY_ROWS",
+           "hk_qk_norm_rope", "attention_kv8_shared", "hk_attention_kv8_shared",
+           "hk_attention_kv8_shared_workspace_size", "HK_FP4_MXFP4", "HK_FP4_NVFP4", "HK_KV8_FAULT_DROP_ARRIVE", "HK_KV8_FEW_ROWS", "HK_KV8_MANY_ROWS",
            "HK_TYPE_BF16", "HK_TYPE_FP16", "HK_TYPE_FP32"]

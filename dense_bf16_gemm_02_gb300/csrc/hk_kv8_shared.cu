@@ -1,0 +1,260 @@
+// Host side of hk_attention_kv8_shared (include/hk_gemm.h): argument checks,
+// workspace and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
+#include <mutex>
+
+#include "../../include/hk_gemm.h"
+#include "host_internal.h"
+#include "kv8_host.h"
+#include "kv8_shared.cuh"
+#include "kv8_shared_mma.cuh"
+
+namespace {
+
+using namespace hk::kv8;
+using namespace hk_kv8;
+
+std::mutex g_setup_mutex;
+bool g_setup[kMaxDevices] = {};
+
+template <int kD, typename T>
+cudaError_t setup_one() {
+    return cudaFuncSetAttribute(kv8_shared_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedGeometry<kD>::kSmemBytes);
+}
+
+// (a split of registers that adds up to more than the launch has would wait for ever)
+template <int kD>
+cudaError_t setup_wide() {
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, kv8_shared_mma_kernel<kD>);
+    if (e == cudaSuccess && a.numRegs * kWideThreads < kWideRegisters) e = cudaErrorLaunchOutOfResources;
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kv8_shared_mma_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideGeometry<kD>::kSmemBytes);
+    return e;
+}
+
+hk_status setup(int device) {
+    std::lock_guard<std::mutex> lock(g_setup_mutex);
+    if (g_setup[device]) return HK_OK;
+    cudaError_t e = setup_one<64, __nv_bfloat16>();
+    if (e == cudaSuccess) e = setup_one<64, __half>();
+    if (e == cudaSuccess) e = setup_one<128, __nv_bfloat16>();
+    if (e == cudaSuccess) e = setup_one<128, __half>();
+    if (e == cudaSuccess) e = setup_wide<64>();
+    if (e == cudaSuccess) e = setup_wide<128>();
+    if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring the shared attention kernels", e);
+    g_setup[device] = true;
+    return HK_OK;
+}
+
+// Query rows per sequence and KV head from which a sequence fills the tensor-core kernel's tiles by itself: reading a
+// prefix once for several sequences saves nothing there, and the call is attention_kv8's.
+constexpr int64_t kOwnTileRows = 256;
+
+// Sequences of one launch: what the kernel plans for, and as many as keep the sums of whole units at 2^17 rows (two of
+// 64 MB at head dimension 128).
+int64_t launch_batch(int64_t B, int64_t T, int64_t Hq) {
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(B, kMaxShared), (int64_t(1) << 17) / (T * Hq)));
+}
+
+constexpr uint32_t kFormFlags = HK_KV8_FEW_ROWS | HK_KV8_MANY_ROWS;
+
+// Can the tensor-core kernel take the shared units? It reads 16-byte aligned bf16 rows and holds so many groups.
+bool wide_can(const void* Q, int32_t type, const int64_t q_strides[3], int64_t G) {
+    return type == HK_TYPE_BF16 && rows_aligned(Q, q_strides) && G <= kWideGroups;
+}
+
+// Does it? By the rows of a group.
+bool wide_pays(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, int64_t G) {
+    const int64_t rows = B * T * (Hq / c->heads) / G;
+    return rows > 32 && max_pages * c->page_size > 2048;
+}
+
+struct Workspace {
+    int64_t whole[2], slots, rows;   // rows of sums: of split units of 16 rows, of whole ones, of split units of 256 rows
+    int64_t shared_units;
+    size_t ml, info, shared_info, seqs, total;
+};
+
+Workspace workspace(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t G, bool wide) {
+    const int64_t n = launch_batch(B, T, Hq), group = Hq / c->heads;
+    const int64_t warps = 2 * kSms * kDecodeWarps;
+    Workspace w;
+    w.whole[0] = 2 * warps * kRows;
+    w.whole[1] = w.whole[0] + n * T * Hq;
+    w.slots = w.whole[1] + n * T * Hq;
+    w.rows = w.slots + (wide ? int64_t(2) * kSms * kWideRows : 0);
+    w.shared_units = n * T * group / kRows + std::min<int64_t>(G, kMaxShared) + 2;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.ml = up(static_cast<size_t>(w.rows * c->head_dim) * 4);
+    w.info = w.ml + up(static_cast<size_t>(w.rows) * 8);
+    w.shared_info = w.info + up(static_cast<size_t>(n * c->heads * ceil_div(T * group, kRows)) * sizeof(int4));
+    w.seqs = w.shared_info + up(static_cast<size_t>(c->heads * w.shared_units) * sizeof(int4));
+    w.total = w.seqs + up(static_cast<size_t>(n) * sizeof(int4));
+    return w;
+}
+
+bool shape_ok(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, int64_t G) {
+    return c && cache_shape_ok(c) && table_width_ok(max_pages, c->page_size) && B > 0 && B <= kLimit && T > 0 && Hq >= c->heads &&
+           Hq <= kLimit && Hq % c->heads == 0 && T <= kLimit / 16 / (Hq / c->heads) && G > 0 && G <= B;
+}
+
+bool on_its_own(const hk_kv8_cache* c, int64_t T, int64_t Hq) { return T * (Hq / c->heads) >= kOwnTileRows; }
+
+template <int kD, typename T>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const uint8_t* k_codes, const uint8_t* v_codes, const SharedParams& p,
+                   cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (p.wide_runs > 0)
+        e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads), WideGeometry<kD>::kSmemBytes, st,
+                         k_codes, v_codes, p);
+    if (e != cudaSuccess) return e;
+    e = launch_early(&kv8_shared_kernel<kD, T>, dim3(static_cast<unsigned>(p.warps / kDecodeWarps)), dim3(32 * kDecodeWarps),
+                                 SharedGeometry<kD>::kSmemBytes, st, tk, tv, p);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = int64_t(p.n) * p.T * p.Hq;
+    return launch_early(&kv8_shared_combine_kernel<kD, T>, dim3(static_cast<unsigned>(ceil_div(rows, 8))), dim3(256), 0, st, p);
+}
+
+}  // namespace
+
+extern "C" size_t hk_attention_kv8_shared_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
+                                                         int64_t max_pages, int64_t G) {
+    if (!shape_ok(cache, B, T, Hq, max_pages, G)) return 0;
+    if (on_its_own(cache, T, Hq)) return hk_attention_kv8_workspace_size(cache, B, T, Hq, max_pages);
+    return workspace(cache, B, T, Hq, G, G <= kWideGroups).total;
+}
+
+extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                                                const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                                                const int32_t* lengths, const int32_t* counts, const int32_t* groups,
+                                                const int32_t* shared, int64_t G, void* O, const int64_t o_strides[3], float* lse,
+                                                int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale, void* scratch,
+                                                size_t workspace_bytes, uint32_t flags, uint64_t timeout_ns, void* stream) {
+    hk_status s = check_cache(cache);
+    if (s != HK_OK) return s;
+    if ((flags & ~(kFormFlags | HK_KV8_FAULT_DROP_ARRIVE)) || (flags & kFormFlags) == kFormFlags) return fail(HK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if (type != HK_TYPE_BF16 && type != HK_TYPE_FP16) return fail(HK_ERR_INVALID_ARG, "element type %d (bf16 or fp16)", (int)type);
+    if (B < 0 || T < 0 || Hq < 0 || B > kLimit || T > kLimit || Hq > kLimit) return fail(HK_ERR_INVALID_ARG, "invalid size");
+    if (Hq % cache->heads) return fail(HK_ERR_INVALID_ARG, "Hq=%lld is not a multiple of the cache's %d heads", (long long)Hq, (int)cache->heads);
+    if (!std::isfinite(scale) || scale < 0.0f) return fail(HK_ERR_INVALID_ARG, "the scale must be finite and not negative");
+    if (B == 0 || T == 0 || Hq == 0) return HK_OK;
+    if (G < 1 || G > B) return fail(HK_ERR_INVALID_ARG, "%lld groups of %lld sequences", (long long)G, (long long)B);
+    if ((s = check_table(block_table, table_stride, max_pages, B, lengths, counts, cache->page_size)) != HK_OK) return s;
+    if (!groups || !shared) return fail(HK_ERR_INVALID_ARG, "null groups or shared tokens");
+    if (!aligned(groups, 4) || !aligned(shared, 4)) return fail(HK_ERR_MISALIGNED, "groups and shared tokens must be 4-byte aligned");
+    if (!Q || !O || !q_strides || !o_strides) return fail(HK_ERR_INVALID_ARG, "null queries, output or strides");
+    if (!aligned(Q, 2) || !aligned(O, 2) || !aligned(lse, 4)) return fail(HK_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    const int64_t sizes[3] = {B, T, Hq};
+    for (int i = 0; i < 3; ++i)
+        if (sizes[i] > 1 && std::llabs(o_strides[i]) < cache->head_dim) return fail(HK_ERR_INVALID_ARG, "the output's rows overlap");
+    if (!shape_ok(cache, B, T, Hq, max_pages, G)) return fail(HK_ERR_INVALID_ARG, "problem too large");
+    const int64_t group = Hq / cache->heads;
+    const size_t need = hk_attention_kv8_shared_workspace_size(cache, B, T, Hq, max_pages, G);
+    if (need > 0 && (!scratch || workspace_bytes < need))
+        return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, scratch ? workspace_bytes : size_t(0));
+    if (!aligned(scratch, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
+    if (on_its_own(cache, T, Hq))
+        return hk_attention_kv8_ex(Q, type, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse,
+                                   B, T, Hq, causal, scale, scratch, workspace_bytes, flags & ~kFormFlags, timeout_ns, stream);
+    if ((flags & HK_KV8_MANY_ROWS) && !wide_can(Q, type, q_strides, G))
+        return fail(HK_ERR_INVALID_ARG, "the tensor-core kernel takes bf16 queries with 16-byte aligned rows, and %d groups", kWideGroups);
+    const bool wide = flags & kFormFlags ? (flags & HK_KV8_MANY_ROWS) != 0
+                                         : wide_can(Q, type, q_strides, G) && wide_pays(cache, B, T, Hq, max_pages, G);
+    const int64_t batch = launch_batch(B, T, Hq), row_tiles = ceil_div(T * group, kRows);
+    // (tiles of one launch, at most: every sequence's own and every group's shared ones)
+    const int64_t unit_tiles = ceil_div(max_pages * cache->page_size, kTileKeys);
+    if (unit_tiles > kLimit / (cache->heads * (batch * (2 * row_tiles + 1) + std::min<int64_t>(G, kMaxShared))))
+        return fail(HK_ERR_INVALID_ARG, "problem too large");
+    int device = 0, sms = 0;
+    if ((s = current_device(&device, &sms)) != HK_OK) return s;
+    if ((s = setup(device)) != HK_OK) return s;
+    uint32_t* status = nullptr;
+    if ((s = hk_host::status_word(device, &status)) != HK_OK) return s;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    if ((s = hk_host::tensor_map_encoder(&enc)) != HK_OK) return s;
+    CUtensorMap tk, tv;
+    if ((s = encode_codes(enc, &tk, cache->k_codes, cache, kTileKeys)) != HK_OK) return s;
+    if ((s = encode_codes(enc, &tv, cache->v_codes, cache, kTileKeys)) != HK_OK) return s;
+
+    const Workspace w = workspace(cache, B, T, Hq, G, G <= kWideGroups);
+    char* const base = static_cast<char*>(scratch);
+    SharedParams p = {};
+    p.q = Q;
+    p.q_stride_b = q_strides[0];
+    p.q_stride_t = q_strides[1];
+    p.q_stride_h = q_strides[2];
+    p.o = O;
+    p.o_stride_b = o_strides[0];
+    p.o_stride_t = o_strides[1];
+    p.o_stride_h = o_strides[2];
+    p.vec_q = rows_aligned(Q, q_strides);
+    p.vec_o = rows_aligned(O, o_strides);
+    p.lse = lse;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.lengths = lengths;
+    p.counts = counts;
+    p.B = static_cast<int32_t>(B);
+    p.T = static_cast<int32_t>(T);
+    p.Hq = static_cast<int32_t>(Hq);
+    p.Hkv = cache->heads;
+    p.group = static_cast<int32_t>(group);
+    p.row_tiles = static_cast<int32_t>(row_tiles);
+    p.page_size = cache->page_size;
+    p.page_shift = page_shift(cache->page_size);
+    p.max_pages = static_cast<int32_t>(max_pages);
+    p.num_pages = cache->num_pages;
+    p.causal = causal ? 1 : 0;
+    p.scale_log2 = static_cast<float>(
+        1.4426950408889634 * (scale != 0.0f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->head_dim))));
+    p.flags = flags & HK_KV8_FAULT_DROP_ARRIVE ? kFlagDropArrive : 0u;
+    p.warps = 2 * std::min(sms, kSms) * kDecodeWarps;
+    p.part_o = reinterpret_cast<float*>(base);
+    p.part_ml = reinterpret_cast<float*>(base + w.ml);
+    p.info = reinterpret_cast<int4*>(base + w.info);
+    p.wait.status = status;
+    p.wait.timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
+    p.groups = groups;
+    p.shared = shared;
+    p.G = static_cast<int32_t>(G);
+    p.all = p.B;
+    p.whole[0] = w.whole[0];
+    p.whole[1] = w.whole[1];
+    p.shared_info = reinterpret_cast<int4*>(base + w.shared_info);
+    p.shared_units = static_cast<int32_t>(w.shared_units);
+    p.wide_runs = wide ? std::min(sms, kSms) : 0;
+    p.shared_slots = w.slots;
+    p.seqs = reinterpret_cast<int4*>(base + w.seqs);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    for (int64_t b0 = 0; b0 < B; b0 += batch) {       // (launches of one stream: they may share the workspace)
+        p.b0 = static_cast<int32_t>(b0);
+        p.n = static_cast<int32_t>(std::min<int64_t>(B - b0, batch));
+        p.wait.launch_id = hk_host::next_launch_id();
+        const bool half = type == HK_TYPE_FP16;
+        cudaError_t e;
+        const uint8_t *kc = static_cast<const uint8_t*>(cache->k_codes), *vc = static_cast<const uint8_t*>(cache->v_codes);
+        if (cache->head_dim == 64) e = half ? launch<64, __half>(tk, tv, kc, vc, p, st) : launch<64, __nv_bfloat16>(tk, tv, kc, vc, p, st);
+        else e = half ? launch<128, __half>(tk, tv, kc, vc, p, st) : launch<128, __nv_bfloat16>(tk, tv, kc, vc, p, st);
+        if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the shared attention", e);
+    }
+    return HK_OK;
+}
+
+extern "C" hk_status hk_attention_kv8_shared(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                                             const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                                             const int32_t* lengths, const int32_t* counts, const int32_t* groups,
+                                             const int32_t* shared, int64_t G, void* O, const int64_t o_strides[3], float* lse,
+                                             int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+    return hk_attention_kv8_shared_ex(Q, type, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, groups, shared,
+                                      G, O, o_strides, lse, B, T, Hq, causal, scale, workspace, workspace_bytes, 0u, 0u, stream);
+}

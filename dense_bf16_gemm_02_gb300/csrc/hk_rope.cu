@@ -51,7 +51,7 @@ hk_status check_operand(const void* in, const int64_t in_s[3], const void* out, 
 }
 
 template <typename T, int kLanes>
-cudaError_t launch(const RopeParams& p, bool interleaved, cudaStream_t st) {
+cudaError_t launch(const RopeParams& p, bool interleaved, bool vec, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>((p.warps + 7) / 8));
@@ -61,13 +61,16 @@ cudaError_t launch(const RopeParams& p, bool interleaved, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return interleaved ? cudaLaunchKernelEx(&cfg, &qk_norm_rope_kernel<T, kLanes, true>, p)
-                       : cudaLaunchKernelEx(&cfg, &qk_norm_rope_kernel<T, kLanes, false>, p);
+    auto* fn = interleaved ? (vec ? &qk_norm_rope_kernel<T, kLanes, true, true> : &qk_norm_rope_kernel<T, kLanes, true, false>)
+                           : (vec ? &qk_norm_rope_kernel<T, kLanes, false, true> : &qk_norm_rope_kernel<T, kLanes, false, false>);
+    return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 template <typename T>
-cudaError_t launch(const RopeParams& p, int lanes, bool interleaved, cudaStream_t st) {
-    return lanes == 8 ? launch<T, 8>(p, interleaved, st) : lanes == 16 ? launch<T, 16>(p, interleaved, st) : launch<T, 32>(p, interleaved, st);
+cudaError_t launch(const RopeParams& p, int lanes, bool interleaved, bool vec, cudaStream_t st) {
+    return lanes == 8    ? launch<T, 8>(p, interleaved, vec, st)
+           : lanes == 16 ? launch<T, 16>(p, interleaved, vec, st)
+                         : launch<T, 32>(p, interleaved, vec, st);
 }
 
 }  // namespace
@@ -146,10 +149,10 @@ extern "C" hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], 
     p.eps = eps;
     p.norm = eps >= 0.0f;
     p.weight_f32 = weight_type == HK_TYPE_FP32;
-    p.vec = vec;
     // as few row steps to a warp as leave the GPU full of warps, four (whose loads are in flight together) where there are enough
     const int lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;
-    const int64_t token_steps = (Hq + Hk + 32 / lanes - 1) / (32 / lanes);
+    for (int op = 0; op < 2; ++op) p.op_steps[op] = (p.heads[op] + 32 / lanes - 1) / (32 / lanes);
+    const int64_t token_steps = int64_t(p.op_steps[0]) + p.op_steps[1];
     const int64_t steps = std::min<int64_t>(token_steps, std::max<int64_t>(1, B * T * token_steps / (int64_t(kSms) * kWarpsPerSm)));
     p.shares = static_cast<int32_t>((token_steps + steps - 1) / steps);
     p.steps = static_cast<int32_t>((token_steps + p.shares - 1) / p.shares);
@@ -162,9 +165,9 @@ extern "C" hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], 
     if ((s = hk_host::check_device(device, &sms)) != HK_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (type) {
-        case HK_TYPE_BF16: e = launch<__nv_bfloat16>(p, lanes, interleaved != 0, st); break;
-        case HK_TYPE_FP16: e = launch<__half>(p, lanes, interleaved != 0, st); break;
-        default: e = launch<float>(p, lanes, interleaved != 0, st); break;
+        case HK_TYPE_BF16: e = launch<__nv_bfloat16>(p, lanes, interleaved != 0, vec, st); break;
+        case HK_TYPE_FP16: e = launch<__half>(p, lanes, interleaved != 0, vec, st); break;
+        default: e = launch<float>(p, lanes, interleaved != 0, vec, st); break;
     }
     return e == cudaSuccess ? HK_OK : fail(HK_ERR_LAUNCH, "launching the head norm and rotation: %s", cudaGetErrorString(e));
 }

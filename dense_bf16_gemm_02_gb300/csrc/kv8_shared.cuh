@@ -1,0 +1,409 @@
+// Attention of a few query rows per sequence over the paged 8-bit cache, for
+// sequences that begin with the same tokens in the same pages (answers to one prompt, requests
+// behind one system prompt): the shared pages are read once for all of them.
+//
+// A group is consecutive sequences whose first `shared` tokens lie in the pages that the
+// first one's table row names. Their query rows (sequences × tokens × the query heads of a KV
+// head) are stacked into units over those pages, and every sequence has units of its
+// own over its remaining tokens; with the running maxima m and sums l of both,
+//
+//   O = (O_1 2^(m_1 - m) + O_2 2^(m_2 - m)) / (l_1 2^(m_1 - m) + l_2 2^(m_2 - m)),  m = max(m_1, m_2)
+//
+// What is shared is rounded down to 128 tokens, so that it ends with a page and a tile; and
+// a sequence takes part only if all its queries see all of it (else its own units begin
+// at its first token, and its rows among the stacked ones are left unused): a shared unit
+// needs no masks, and no value of a token that a query does not see meets that query.
+//
+// Both kinds of units run as in kv8_decode.cuh: tiles of 32 tokens of all units in
+// one order, cut into equal runs, one per warp, whatever the lengths are; sums of units that
+// are split, and of sequences with a shared part, go through memory and are added up by a second
+// kernel, in order. Without a shared part a whole unit is finished at once.
+#pragma once
+
+#include "kv8_decode.cuh"
+
+namespace hk {
+namespace kv8 {
+
+constexpr int kMaxShared = 512;        // sequences, and groups, of one launch
+constexpr int kSharedStep = 128;       // tokens that what is shared is rounded down to
+
+template <int kD>
+struct SharedGeometry {
+    using G = DecodeGeometry<kD>;
+    static constexpr int kOffPrefix = kDecodeWarps * G::kWarpBytes;                   // tiles before each group's and sequence's
+    static constexpr int kOffGroups = kOffPrefix + (2 * kMaxShared + 1) * 4;          // first sequence of each group
+    static constexpr int kOffShared = kOffGroups + (kMaxShared + 1) * 4;              // shared tiles of each group
+    static constexpr int kOffStart = kOffShared + kMaxShared * 4;                     // first own tile of each sequence
+    static constexpr int kOffBars = (kOffStart + kMaxShared * 4 + 7) / 8 * 8;
+    static constexpr int kSmemBytes = kOffBars + kDecodeWarps * G::kStages * 8 + 1024;
+    static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two blocks per SM");
+};
+
+struct SharedParams : DecodeParams {
+    const int32_t* groups;         // [G + 1] first sequence of each group, B at the end
+    const int32_t* shared;         // [G] shared tokens
+    int32_t G, b0, n, all;         // groups; this launch: sequences [b0, b0 + n) of all
+    int64_t whole[2];              // rows of part_o and part_ml where the sums of whole units begin: shared, own
+    int4* shared_info;             // as info, of the units of the groups: [KV head][shared_units]
+    int32_t shared_units;
+    int32_t wide_runs;             // CTAs that work on the shared units of 256 rows (kv8_shared_mma.cuh); 0: units of 16 rows here
+    int64_t shared_slots;          // row of part_o and part_ml where the sums of split units of 256 rows begin
+    int4* seqs;                    // [n]: shared tiles, place of the group, its first sequence of this launch, queries
+};
+
+// Group of a launch: its sequences in it, and its shared tiles.
+struct Group {
+    int first, n, tiles;           // first sequence of the launch, counted from b0
+};
+
+__device__ __forceinline__ int shared_rows(const SharedParams& p, int n) { return n * p.T * p.group; }
+
+// Where the shared units of the group in place `j` with first sequence `first` begin in shared_info.
+__device__ __forceinline__ int shared_unit0(const SharedParams& p, int j, int first) { return shared_rows(p, first) / kRows + j; }
+
+// Tokens that the first query of a sequence sees (the fewest of its queries).
+__device__ __forceinline__ int least_seen(const SharedParams& p, const Sequence& s) {
+    if (s.count == 0) return 0;
+    return p.causal ? max(0, s.len - s.count + 1) : s.len;
+}
+
+// 16 stacked rows of a group: KV head h, rows [16 rt, 16 rt + 16).
+struct SharedRows {
+    const SharedParams& p;
+    int b, n, h, rt;               // first sequence of the group in this launch, and how many
+    const int32_t* table;          // of the group's first sequence
+
+    __device__ __forceinline__ const int32_t* pages() const { return table; }
+    __device__ __forceinline__ bool several() const { return false; }
+    template <typename T>
+    __device__ __forceinline__ const T* row(int r, bool& live, int& limit) const {
+        const int row = rt * kRows + r, per = p.T * p.group;
+        const int seq = row / per, rest = row - seq * per, t = rest / p.group;
+        live = seq < n;
+        limit = 0x7FFFFFFF;
+        return static_cast<const T*>(p.q) + (b + seq) * p.q_stride_b + t * p.q_stride_t +
+               static_cast<int64_t>(h * p.group + rest - t * p.group) * p.q_stride_h;
+    }
+};
+
+// What a launch's blocks all work out first: groups, shared and own tiles, and their sums. Returns the number of groups.
+template <int kThreads>
+__device__ __forceinline__ int plan_groups(const SharedParams& p, int32_t* first_of, int32_t* tiles_of_group, int32_t* start) {
+    const int t = static_cast<int>(threadIdx.x);
+    __shared__ int lowest;
+    if (t == 0) {
+        int lo = 0, hi = p.G - 1;            // the group of sequence b0
+        if (p.b0 > 0)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (p.groups[mid] <= p.b0) lo = mid; else hi = mid - 1;
+            }
+        lowest = lo;
+    }
+    __syncthreads();
+    const int g0 = lowest, groups = min(p.G - g0, kMaxShared);
+    const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+    for (int j = t; j <= groups; j += kThreads) {
+        int first = p.groups[g0 + j];
+        bool bad = (g0 + j == 0 && first != 0) || (g0 + j == p.G && first != p.all) || first < 0 || first > p.all;
+        int tiles = 0;
+        if (j < groups && !bad) {
+            const int next = p.groups[g0 + j + 1];
+            const int shared = p.shared[g0 + j];
+            bad = next <= first || next > p.all || shared < 0;
+            if (!bad && first < p.b0 + p.n) {
+                const int len = p.lengths[first];
+                const int64_t most = min(min(static_cast<int64_t>(shared), static_cast<int64_t>(len)), room);
+                tiles = static_cast<int>(max(static_cast<int64_t>(0), most)) / kSharedStep * (kSharedStep / kTileKeys);
+            }
+        }
+        if (bad) atomicOr(p.wait.status, kErrPage);
+        first_of[j] = first;
+        if (j < groups) tiles_of_group[j] = bad ? 0 : tiles;
+    }
+    __syncthreads();
+    for (int i = t; i < p.n; i += kThreads) {
+        const int b = p.b0 + i;
+        int lo = 0, hi = groups - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (first_of[mid] <= b) lo = mid; else hi = mid - 1;
+        }
+        const Sequence s = sequence(p, b);
+        const bool member = first_of[lo] >= 0 && first_of[lo] <= b && b < first_of[lo + 1];
+        const int tiles = member ? tiles_of_group[lo] : 0;
+        start[i] = tiles > 0 && least_seen(p, s) >= static_cast<int64_t>(tiles) * kTileKeys ? tiles : 0;
+        if (blockIdx.x == 0) p.seqs[i] = make_int4(start[i], lo, max(first_of[lo], p.b0) - p.b0, s.count);
+    }
+    __syncthreads();
+    return groups;
+}
+
+// Sequences of group `j` in this launch.
+__device__ __forceinline__ Group group_of(const SharedParams& p, const int32_t* first_of, const int32_t* tiles_of_group, int j) {
+    const int first = max(first_of[j], p.b0), end = min(first_of[j + 1], p.b0 + p.n);
+    return Group{first - p.b0, max(0, end - first), tiles_of_group[j]};
+}
+
+// Tiles of the unit of row tile rt of a sequence whose own part begins at tile `start`, of which there is one at least.
+__device__ __forceinline__ int own_tiles(int end, int start) { return max(1, (end + kTileKeys - 1) / kTileKeys - start); }
+
+template <int kD, typename T>
+__global__ void __launch_bounds__(32 * kDecodeWarps, 2)
+kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
+    using G = DecodeGeometry<kD>;
+    using S = SharedGeometry<kD>;
+    constexpr int kNTiles = kD / 8;
+    constexpr int kOwn = kD / 4;
+    constexpr int kThreads = 32 * kDecodeWarps;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw);
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    const uint32_t g = lane >> 2, c = lane & 3u;
+    const int self = static_cast<int>(blockIdx.x) * kDecodeWarps + static_cast<int>(warp);
+
+    griddep_launch_dependents();             // the combining kernel may be scheduled; it waits for this grid's end
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tmap_k);
+        prefetch_tensor_map(&tmap_v);
+    }
+    const uint32_t ring = base + warp * G::kWarpBytes;
+    const uint32_t bars = base + S::kOffBars + 8u * warp * G::kStages;
+    if (lane == 0) {
+        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, s == 0 && (p.flags & kFlagDropArrive) ? 2 : 1);
+        fence_mbar_init_cluster();
+    }
+    // launched early behind the kernel that may have written the cache or q; or behind the one for the shared units, beside which
+    // it may run (that one began when the kernels before it had ended), and for whose end it waits at its own
+    if (p.wide_runs == 0) griddep_wait();
+    int32_t* const prefix = reinterpret_cast<int32_t*>(smem + S::kOffPrefix);
+    int32_t* const first_of = reinterpret_cast<int32_t*>(smem + S::kOffGroups);
+    int32_t* const tiles_of_group = reinterpret_cast<int32_t*>(smem + S::kOffShared);
+    int32_t* const start = reinterpret_cast<int32_t*>(smem + S::kOffStart);
+    const int groups = plan_groups<kThreads>(p, first_of, tiles_of_group, start);
+    const int sections = groups + p.n;       // the groups' shared units, then the sequences' own
+    for (int i = static_cast<int>(threadIdx.x); i < sections; i += kThreads) {
+        int tiles = 0;
+        if (i < groups && p.wide_runs > 0) {
+            tiles = 0;
+        } else if (i < groups) {
+            const Group gr = group_of(p, first_of, tiles_of_group, i);
+            tiles = (shared_rows(p, gr.n) + kRows - 1) / kRows * gr.tiles;
+        } else {
+            const Sequence s = sequence(p, p.b0 + i - groups);
+            for (int rt = 0; rt < p.row_tiles; ++rt) tiles += own_tiles(row_tile_end(p, s, rt), start[i - groups]);
+        }
+        prefix[i + 1] = tiles * p.Hkv;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+        for (int i0 = 0; i0 < sections; i0 += 32) {
+            const int i = i0 + static_cast<int>(lane);
+            int inc = i < sections ? prefix[i + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (static_cast<int>(lane) >= d) inc += o;
+            }
+            if (i < sections) prefix[i + 1] = sum + inc;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+
+    const int total = prefix[sections];
+    const int per = (total + p.warps - 1) / p.warps;
+    const int begin = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(self) * per));
+    const int end = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(begin) + per));
+    bool ok = true;
+    int fills = 0, uses = 0;                 // ring stages filled and consumed so far
+
+    int at = begin, section = 0;
+    if (begin < end) {
+        int lo = 0, hi = sections - 1;       // the last section that begins at or before this run (those without tiles end there)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= begin) lo = mid; else hi = mid - 1;
+        }
+        section = lo;
+    }
+    while (at < end) {
+        // ---- the unit of tile `at`
+        while (prefix[section + 1] <= at) ++section;
+        const bool is_shared = section < groups;
+        int local = at - prefix[section];
+        const int head_tiles = (prefix[section + 1] - prefix[section]) / p.Hkv;
+        const int h = local / head_tiles;
+        local -= h * head_tiles;
+        const int i = section - groups, b = p.b0 + i;      // (of a sequence's own part)
+        Group gr = {0, 0, 0};
+        Sequence seq = {0, 0};
+        int rt = 0, unit_tiles, first, key_end, tile0 = 0;
+        if (is_shared) {
+            gr = group_of(p, first_of, tiles_of_group, section);
+            unit_tiles = gr.tiles;
+            rt = local / unit_tiles;
+            first = local - rt * unit_tiles;
+            key_end = unit_tiles * kTileKeys;
+        } else {
+            seq = sequence(p, b);
+            first = local;
+            tile0 = start[i];
+            while (first >= (unit_tiles = own_tiles(key_end = row_tile_end(p, seq, rt), tile0)) && rt + 1 < p.row_tiles) {
+                first -= unit_tiles;
+                ++rt;
+            }
+        }
+        const int last = min(unit_tiles, first + (end - at));   // tiles [first, last) of the unit
+
+        float o[kNTiles][4], m[2], l[2];
+        if (is_shared)
+            ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses,
+                                           SharedRows{p, p.b0 + gr.first, gr.n, h, rt, p.table + first_of[section] * p.table_stride}, h,
+                                           key_end, first, last, o, m, l);
+        else     // (a part that ends before it begins has one tile to see nothing in: no token is read)
+            ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, UnitRows{p, b, h, rt, seq}, h,
+                                           key_end > tile0 * kTileKeys ? key_end : 0, tile0 + first, tile0 + last, o, m, l);
+        if (!ok) break;
+
+        // ---- finish the unit or leave its sums
+        const bool whole = first == 0 && last == unit_tiles;
+        const int slot = 2 * self + (at == begin ? 0 : 1);
+        if (first == 0 && lane == 0) {       // this run holds the unit's first tile: it tells how the unit is made up
+            const int parts = whole ? 0 : (at + unit_tiles - 1) / per - at / per + 1;
+            const int4 record = make_int4(parts, slot, self, 0);
+            if (is_shared) p.shared_info[static_cast<int64_t>(h) * p.shared_units + shared_unit0(p, section, gr.first) + rt] = record;
+            else p.info[(static_cast<int64_t>(i) * p.Hkv + h) * p.row_tiles + rt] = record;
+        }
+        const bool finish = whole && !is_shared && tile0 == 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = static_cast<int>(g) + 8 * e, row = rt * kRows + r;
+            int s = i, rest = row;                                // sequence of the launch, row of it
+            if (is_shared) {
+                s = row / (p.T * p.group);
+                rest = row - s * (p.T * p.group);
+                if (s >= gr.n) continue;
+                s += gr.first;
+            }
+            const int t = rest / p.group, head = h * p.group + rest - t * p.group;
+            if (t >= p.T) continue;
+            float v[kOwn];
+            const bool any = l[e] > 0.0f || l[e] != l[e];        // (a row that sees nothing may hold NaN sums)
+            const float mul = !finish ? 1.0f : 1.0f / l[e];
+#pragma unroll
+            for (int j = 0; j < kNTiles; ++j) {
+                v[j] = any ? o[j][2 * e] * mul : 0.0f;
+                v[kNTiles + j] = any ? o[j][2 * e + 1] * mul : 0.0f;
+            }
+            const int64_t out_row = (static_cast<int64_t>(s) * p.T + t) * p.Hq + head;     // of the launch
+            if (finish) {
+                T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + c * kOwn;
+                store_row<T, kOwn>(dst, v, p.vec_o != 0);
+                if (p.lse != nullptr && c == 0)
+                    p.lse[static_cast<int64_t>(p.b0) * p.T * p.Hq + out_row] = any ? (m[e] + log2f(l[e])) * 0.69314718055994531f : -INFINITY;
+            } else {
+                const int64_t at_row = whole ? p.whole[is_shared ? 0 : 1] + out_row : static_cast<int64_t>(slot) * kRows + r;
+                float4* const dst = reinterpret_cast<float4*>(p.part_o + at_row * kD + c * kOwn);
+#pragma unroll
+                for (int k = 0; k < kOwn / 4; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                if (c == 0) {
+                    p.part_ml[2 * at_row] = any ? m[e] : -INFINITY;
+                    p.part_ml[2 * at_row + 1] = any ? l[e] : 0.0f;
+                }
+            }
+        }
+        at += last - first;
+    }
+    // abort: the copies in flight land before the block ends
+    if (!ok)
+        for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
+    if (p.wide_runs > 0) griddep_wait();
+}
+
+// Adds up what the kernel above left: grid (row of 16 · row_tiles, KV head, sequence) / 8 rows to a block, a warp to a row. A
+// row's parts are those of its shared unit, then those of its own: the maximum first, then the weighted sums, in order.
+template <int kD, typename T>
+__global__ void __launch_bounds__(256)
+kv8_shared_combine_kernel(const SharedParams p) {
+    constexpr int kVec = kD / 32;            // floats of a lane
+    constexpr int kBatch = 4;                // parts whose loads are in flight at a time
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t out_row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = static_cast<int>(lane_id());
+    if (out_row >= static_cast<int64_t>(p.n) * p.T * p.Hq) return;
+    const int head = static_cast<int>(out_row % p.Hq), t = static_cast<int>(out_row / p.Hq % p.T);
+    const int i = static_cast<int>(out_row / p.Hq / p.T), h = head / p.group;
+    const int row = t * p.group + head - h * p.group;
+    const int4 seq = __ldcg(p.seqs + i);     // (past L1: this grid may have started before the writes)
+    const int4 own = __ldcg(p.info + (static_cast<int64_t>(i) * p.Hkv + h) * p.row_tiles + row / kRows);
+    int4 shared = make_int4(0, 0, 0, 0);
+    int shared_row = 0;
+    const int unit_rows = p.wide_runs > 0 ? 256 : kRows;
+    if (seq.x > 0) {
+        shared_row = shared_rows(p, i - seq.z) + row;
+        shared = __ldcg(p.shared_info + static_cast<int64_t>(h) * p.shared_units + shared_unit0(p, seq.y, seq.z) + shared_row / unit_rows);
+    } else if (own.x == 0) {
+        return;                              // finished
+    }
+    // (a launch whose waits gave up leaves records unwritten: what they hold is no place to read from)
+    auto wrong = [&](const int4& x, int runs) { return x.x < 0 || (x.x > 0 && (x.y < 0 || x.y >= 2 * runs || x.z < 0 || x.x > runs - x.z)); };
+    if (wrong(own, p.warps) || wrong(shared, p.wide_runs > 0 ? p.wide_runs : p.warps)) return;
+    const int first_parts = seq.x > 0 ? max(shared.x, 1) : 0, parts = first_parts + max(own.x, 1);
+    auto row_of = [&](int k) {
+        const bool of_shared = k < first_parts;
+        const int4& x = of_shared ? shared : own;
+        const int part = of_shared ? k : k - first_parts;
+        if (x.x == 0) return p.whole[of_shared ? 0 : 1] + out_row;
+        const int64_t slot = part == 0 ? static_cast<int64_t>(x.y) : 2 * (static_cast<int64_t>(x.z) + part);
+        if (of_shared && p.wide_runs > 0) return p.shared_slots + slot * 256 + shared_row % 256;
+        return slot * kRows + (of_shared ? shared_row : row) % kRows;
+    };
+    float m = -INFINITY, l = 0.0f, acc[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[k] = 0.0f;
+    for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(p.part_ml + 2 * row_of(k)));
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int k0 = 0; k0 < parts; k0 += kBatch) {
+        float pm[kBatch], pl[kBatch], x[kBatch][kVec];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int64_t a = row_of(min(k0 + q, parts - 1));
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
+            pm[q] = ml.x;
+            pl[q] = ml.y;
+            if constexpr (kVec == 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * kD) + lane);
+                x[q][0] = f.x; x[q][1] = f.y; x[q][2] = f.z; x[q][3] = f.w;
+            } else {
+                const float2 f = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * kD) + lane);
+                x[q][0] = f.x; x[q][1] = f.y;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const bool counts = k0 + q < parts;
+            const float weight = !counts || pm[q] == -INFINITY ? 0.0f : ex2_approx(pm[q] - m);
+            l += !counts ? 0.0f : pm[q] == -INFINITY ? pl[q] : pl[q] * weight;       // (a NaN sum stays one)
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) acc[k] += x[q][k] * weight;
+        }
+    }
+    const bool any = t < seq.w && (l > 0.0f || l != l);      // (a row past the queries has stacked sums of what lies there)
+    const float mul = any ? 1.0f / l : 0.0f;
+    T* const dst = static_cast<T*>(p.o) + (p.b0 + i) * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + lane * kVec;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) dst[k] = from_float<T>(any ? acc[k] * mul : 0.0f);
+    if (p.lse != nullptr && lane == 0)
+        p.lse[static_cast<int64_t>(p.b0) * p.T * p.Hq + out_row] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace kv8
+}  // namespace hk

@@ -8,7 +8,7 @@
 // Every element is read once and written once: what bounds it is memory. A row
 // (one head of one token) is 8 elements each of 8, 16 or 32 lanes, so that a
 // warp's load is whole lines; a warp keeps to one token and takes `steps` times
-// 32 / lanes rows of it, so that the angles are worked out once for all of them:
+// 32 / lanes rows of its queries or keys, so that the angles are worked out once for all of them:
 // as few as leave every SM full of warps (a decoding step), up to all heads (a
 // prompt).
 //
@@ -43,10 +43,11 @@ struct RopeParams {
     int32_t section_end[kMaxAxes]; // pairs [.., section_end[a]) turn by axis a
     int32_t B, T, heads[2];        // heads of queries and keys
     int32_t D, half;               // R / 2
+    int32_t op_steps[2];           // row steps of a token's queries, of its keys
     int32_t steps, shares;         // row steps of a warp; warps of a token
     int64_t warps;
     float eps;
-    int32_t norm, weight_f32, vec;
+    int32_t norm, weight_f32;
 };
 
 // inv_freq / 2 pi as a fraction of 2^64 (whole turns dropped). The largest frequencies lose bits: 2^e costs e of them.
@@ -90,23 +91,37 @@ __device__ __forceinline__ void weights8(const RopeParams& p, int op, int d, flo
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float (&v)[8], bool vec) {
-    if (vec) {
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(pack_pair<T>(v[0], v[1]), pack_pair<T>(v[2], v[3]), pack_pair<T>(v[4], v[5]), pack_pair<T>(v[6], v[7]));
-        } else {
-            reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+// Eight elements of a row. kVec: 16 bytes at a time. No test around a load: the next one would wait for it.
+template <typename T, bool kVec>
+__device__ __forceinline__ Raw8<T> row8(const T* src) {
+    Raw8<T> r;
+    if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4*>(src)[i];
     } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = src[i];
+        memcpy(&r, e, sizeof r);
+    }
+    return r;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
+    if constexpr (!kVec) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) dst[k] = from_float<T>(v[k]);
+    } else if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(dst) =
+            make_uint4(pack_pair<T>(v[0], v[1]), pack_pair<T>(v[2], v[3]), pack_pair<T>(v[4], v[5]), pack_pair<T>(v[6], v[7]));
+    } else {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
 }
 
-template <typename T, int kLanes, bool kInterleaved>
+template <typename T, int kLanes, bool kInterleaved, bool kVec>
 __global__ void __launch_bounds__(256)
 qk_norm_rope_kernel(const RopeParams p) {
     constexpr int kRowsStep = 32 / kLanes;           // rows of a warp at a time
@@ -120,7 +135,6 @@ qk_norm_rope_kernel(const RopeParams p) {
     const int lane = static_cast<int>(lane_id());
     const int sub = lane % kLanes, d = 8 * sub;
     const bool live = d < p.D;
-    const int all = p.heads[0] + p.heads[1];
 
     // cos and sin of this lane's elements: of its 4 pairs (interleaved), or of the 8 pairs that it is one half of, four
     // of them worked out here and four by the lane that holds the other half
@@ -153,61 +167,65 @@ qk_norm_rope_kernel(const RopeParams p) {
             }
         }
     }
-    float wq[8], wk[8];
-    weights8<T>(p, 0, live ? d : 0, wq);
-    weights8<T>(p, 1, live ? d : 0, wk);
-
     const float inv_d = 1.0f / static_cast<float>(p.D);
     constexpr int kFlight = sizeof(T) == 2 ? 4 : 2;  // steps whose loads are in flight together
-    const int first = share * p.steps * kRowsStep, last = min(all, first + p.steps * kRowsStep);
-    for (int r0 = first; r0 < last; r0 += kFlight * kRowsStep) {
-        Raw8<T> raw[kFlight];
+    // steps [first, last) of the token's: its queries', then its keys'
+    int first = share * p.steps;
+    const int last = min(p.op_steps[0] + p.op_steps[1], first + p.steps);
+    while (first < last) {
+        const int op = first >= p.op_steps[0];
+        const int base = op ? p.op_steps[0] : 0, end = min(last, op ? last : p.op_steps[0]);
+        float w[8];
+        weights8<T>(p, op, live ? d : 0, w);
+        const T* const src = static_cast<const T*>(p.in[op]) + b * p.in_b[op] + t * p.in_t[op] + (live ? d : 0);
+        T* const dst = static_cast<T*>(p.out[op]) + b * p.out_b[op] + t * p.out_t[op] + d;
+        const int64_t in_h = p.in_h[op], out_h = p.out_h[op];
+        const int heads = p.heads[op];
+        for (int s0 = first; s0 < end; s0 += kFlight) {
+            const int r0 = (s0 - base) * kRowsStep + lane / kLanes;
+            Raw8<T> raw[kFlight];
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const int r = min(r0 + i * kRowsStep + lane / kLanes, last - 1);      // (past the end it is taken again and not stored)
-            const int op = r >= p.heads[0];
-            const T* const src = static_cast<const T*>(p.in[op]) + b * p.in_b[op] + t * p.in_t[op] + (op ? r - p.heads[0] : r) * p.in_h[op];
-            raw[i] = load8<T>(src, d, live ? p.D : 0, p.vec != 0);
-        }
+            for (int i = 0; i < kFlight; ++i)    // (past the end the last row is taken again and not stored)
+                raw[i] = row8<T, kVec>(src + min(r0 + min(i, end - 1 - s0) * kRowsStep, heads - 1) * in_h);
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const int r = r0 + i * kRowsStep + lane / kLanes;
-            const int op = r >= p.heads[0];
-            float y[8];
-            widen8<T>(raw[i], y);
-            if (p.norm) {
-                float sum = 0.0f;
+            for (int i = 0; i < kFlight; ++i) {
+                if (s0 + i >= end) break;
+                const int r = r0 + i * kRowsStep;
+                float y[8];
+                widen8<T>(raw[i], y);
+                if (p.norm) {
+                    float sum = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sum = fmaf(y[k], y[k], sum);
+                    for (int k = 0; k < 8; ++k) sum = fmaf(y[k], y[k], sum);
+                    if (!live) sum = 0.0f;
 #pragma unroll
-                for (int m = kLanes / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                const float mul = 1.0f / sqrtf(sum * inv_d + p.eps);
+                    for (int m = kLanes / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                    const float mul = rsqrtf(fmaf(sum, inv_d, p.eps));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] *= mul * (op ? wk[k] : wq[k]);
-            }
-            float z[8];
-            if constexpr (kInterleaved) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    z[2 * k] = y[2 * k] * c[k] - y[2 * k + 1] * s[k];
-                    z[2 * k + 1] = y[2 * k] * s[k] + y[2 * k + 1] * c[k];
+                    for (int k = 0; k < 8; ++k) y[k] *= mul * w[k];
                 }
-            } else {
+                float z[8];
+                if constexpr (kInterleaved) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float o = __shfl_sync(0xffffffffu, y[k], partner);
-                    z[k] = fmaf(o, s[k], y[k] * c[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        z[2 * k] = y[2 * k] * c[k] - y[2 * k + 1] * s[k];
+                        z[2 * k + 1] = y[2 * k] * s[k] + y[2 * k + 1] * c[k];
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float o = __shfl_sync(0xffffffffu, y[k], partner);
+                        z[k] = fmaf(o, s[k], y[k] * c[k]);
+                    }
                 }
-            }
-            if (!turns) {            // (not times 1 and 0: infinities)
+                if (!turns) {            // (not times 1 and 0: infinities)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) z[k] = y[k];
-            }
-            if (r < last && live) {
-                T* const dst = static_cast<T*>(p.out[op]) + b * p.out_b[op] + t * p.out_t[op] + (op ? r - p.heads[0] : r) * p.out_h[op] + d;
-                store8<T>(dst, z, p.vec != 0);
+                    for (int k = 0; k < 8; ++k) z[k] = y[k];
+                }
+                if (r < heads && live) store8<T, kVec>(dst + r * out_h, z);
             }
         }
+        first = end;
     }
 }
 

@@ -68,6 +68,7 @@ EXPORTED = (
     "hk_kv8_append", "hk_attention_kv8", "hk_attention_kv8_ex", "hk_attention_kv8_workspace_size",
     "hk_attention_kv8_workspace_size_ex", "hk_kv8_arrange", "hk_kv8_arrange_workspace_size", "hk_kv8_compact",
     "hk_kv8_compact_workspace_size", "hk_kv8_copy_pages", "hk_qk_norm_rope",
+    "hk_attention_kv8_shared", "hk_attention_kv8_shared_ex", "hk_attention_kv8_shared_workspace_size",
 )
 
 
@@ -209,6 +210,13 @@ def load() -> ctypes.CDLL:
         lib.hk_qk_norm_rope.argtypes = [P, P, P, P, P, P, P, P, I32, I64, I64, I64, I64, I64, P, P, I32, F, P, P, P, I32, P,
                                         I64, I32, P]
         lib.hk_qk_norm_rope.restype = I32
+        shared = [P, I32, P, CP, P, I64, I64, P, P, P, P, I64, P, P, P, I64, I64, I64, I32, F, P, SZ]
+        lib.hk_attention_kv8_shared.argtypes = [*shared, P]
+        lib.hk_attention_kv8_shared.restype = I32
+        lib.hk_attention_kv8_shared_ex.argtypes = [*shared, U32, U64, P]
+        lib.hk_attention_kv8_shared_ex.restype = I32
+        lib.hk_attention_kv8_shared_workspace_size.argtypes = [CP, I64, I64, I64, I64, I64]
+        lib.hk_attention_kv8_shared_workspace_size.restype = SZ
         _lib = lib
         return lib
 
@@ -329,6 +337,21 @@ def hk_attention_kv8(Q: int, type: int, q_strides, cache: hk_kv8_cache, block_ta
 
 def hk_attention_kv8_workspace_size(cache: hk_kv8_cache, B: int, T: int, Hq: int, max_pages: int) -> int:
     return int(load().hk_attention_kv8_workspace_size(ctypes.byref(cache), B, T, Hq, max_pages))
+
+
+def hk_attention_kv8_shared(Q: int, type: int, q_strides, cache: hk_kv8_cache, block_table: int, table_stride: int,
+                            max_pages: int, lengths: int, counts: int, groups: int, shared: int, G: int, O: int, o_strides,
+                            lse: int, B: int, T: int, Hq: int, causal: int = 1, scale: float = 0.0, workspace: int = 0,
+                            workspace_bytes: int = 0, stream: int = 0) -> int:
+    """hk_attention_kv8 for G groups of sequences whose first tokens lie in the same pages."""
+    I3 = ctypes.c_int64 * 3
+    return load().hk_attention_kv8_shared(Q, type, I3(*q_strides), ctypes.byref(cache), block_table, table_stride, max_pages,
+                                          lengths, counts or None, groups, shared, G, O, I3(*o_strides), lse or None, B, T, Hq,
+                                          int(causal), scale, workspace or None, workspace_bytes, stream)
+
+
+def hk_attention_kv8_shared_workspace_size(cache: hk_kv8_cache, B: int, T: int, Hq: int, max_pages: int, G: int) -> int:
+    return int(load().hk_attention_kv8_shared_workspace_size(ctypes.byref(cache), B, T, Hq, max_pages, G))
 
 
 def _cache_array(caches):

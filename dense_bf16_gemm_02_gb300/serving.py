@@ -1,7 +1,8 @@
 """Torch conveniences over the entry points of ``include/hk_gemm.h`` for a batch
 that shares its prompts: the pages of the 8-bit cache that its sequences hold
-(``Kv8Pool``, ``kv8_arrange``, ``kv8_compact``, ``kv8_copy_pages``) and the norm of
-each head's query and key with the rotation by its position (``qk_norm_rope``).
+(``Kv8Pool``, ``kv8_arrange``, ``kv8_compact``, ``kv8_copy_pages``), the norm of
+each head's query and key with the rotation by its position (``qk_norm_rope``), and
+the attention that reads shared pages once (``attention_kv8_shared``).
 
 As in ``low_precision``, this is argument marshalling: every step runs in the CUDA
 library, on ``stream`` (default: torch's current stream), nothing is read back, and
@@ -16,7 +17,8 @@ import torch
 
 from . import hk_gemm as _hk
 from .hk_gemm import HK_OK, HKError
-from .low_precision import Kv8Cache, _check_vector, _empty, _f32, _i32, _read_only, _row_stride, _stream, _strides, _type_code, _u8
+from .low_precision import (Kv8Cache, _check_vector, _empty, _f32, _i32, _read_only, _row_stride, _stream, _strides, _table,
+                            _tokens_shape, _type_code, _u8)
 
 _pool_struct = struct.Struct("PPPqq4i").pack       # hk_kv8_pool
 
@@ -211,3 +213,50 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     if st != HK_OK:
         raise HKError(st, "hk_qk_norm_rope")
     return qo, ko
+
+
+def attention_kv8_shared(q, cache: Kv8Cache, block_table, lengths, groups, shared, counts=None, causal=True, scale=None,
+                         return_lse=False, out=None, stream=None):
+    """attention_kv8 for a batch whose sequences begin with the same tokens in the same
+    pages: those are read once per group.
+
+    ``groups`` int32 [G + 1], strictly increasing from 0 to B: group g is the sequences
+    groups[g] to groups[g + 1] - 1; ``shared`` int32 [G]: their first so many tokens
+    lie in the pages that the table row of the group's first sequence names (as far as they fill
+    blocks of 128). CUDA tensors. Everything else as attention_kv8. See
+    hk_attention_kv8_shared."""
+    B, T, Hq, qs = _tokens_shape(q, "q", cache, False)
+    code = _type_code(q, "q")
+    if code == _hk.HK_TYPE_FP32:
+        raise TypeError("q must be bfloat16 or float16")
+    if scale is None:
+        scale = 0.0
+    elif not ctypes.c_float(scale).value:
+        raise ValueError("scale must not be 0, nor round to it in 32 bits")
+    ld, pages = _table(block_table, B)
+    _check_vector(lengths, "lengths", B)
+    if counts is not None:
+        _check_vector(counts, "counts", B)
+    if not isinstance(shared, torch.Tensor) or shared.dim() != 1:
+        raise TypeError("shared must be a 1-D int32 CUDA tensor")
+    G = shared.size(0)
+    _check_vector(shared, "shared", G)
+    _check_vector(groups, "groups", G + 1)
+    if out is None:
+        out = _empty((B, T, Hq, cache._head_dim), q.dtype, q, stream)
+        os = _strides(T * Hq * cache._head_dim, Hq * cache._head_dim, cache._head_dim)
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype != q.dtype or out.shape != q.shape:
+            raise ValueError("out must have q's shape and type")
+        os = _tokens_shape(out, "out", cache, False)[3]
+    lse = _empty((B, T, Hq), _f32, q, stream) if return_lse else None
+    lib = _hk.load()
+    size = lib.hk_attention_kv8_shared_workspace_size(cache._ref, B, T, Hq, pages, G)
+    workspace = _empty(size, _u8, q, stream) if size else None
+    st = lib.hk_attention_kv8_shared(q.data_ptr(), code, qs, cache._ref, block_table.data_ptr(), ld, pages, lengths.data_ptr(),
+                                     None if counts is None else counts.data_ptr(), groups.data_ptr(), shared.data_ptr(), G,
+                                     out.data_ptr(), os, None if lse is None else lse.data_ptr(), B, T, Hq, 1 if causal else 0,
+                                     scale, None if workspace is None else workspace.data_ptr(), size, _stream(stream, q))
+    if st != HK_OK:
+        raise HKError(st, "hk_attention_kv8_shared")
+    return (out, lse) if return_lse else out

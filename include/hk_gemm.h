@@ -280,7 +280,8 @@ hk_status hk_gemm_plan_device_status(hk_gemm_plan* plan);
 /* The same for the calls of the one-shot entry points (hk_gemm_bf16,
  * hk_gemm_bf16_epilogue, hk_gemm_bf16_fused, hk_gemm_fp8_e4m3, hk_gemm_mxfp8(_ex),
  * hk_attention_fwd(_ex), hk_gemm_bf16_noalloc, hk_gemm_fp4(_ex), hk_kv8_append,
- * hk_attention_kv8(_ex)) on `device`; HK_ERR_INVALID_ARG if a page index or a length
+ * hk_attention_kv8(_ex), hk_attention_kv8_shared(_ex), hk_kv8_arrange, hk_kv8_compact,
+ * hk_kv8_copy_pages) on `device`; HK_ERR_INVALID_ARG if a page index or a length
  * of a paged cache was out of range (and no wait ran out). */
 hk_status hk_gemm_last_device_status(int device);
 
@@ -600,6 +601,40 @@ size_t hk_kv8_compact_workspace_size(const hk_kv8_pool* pool);
  * reports HK_ERR_INVALID_ARG. Asynchronous on `stream`. */
 hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, int32_t n_caches,
                             const int32_t* dst_pages, const int32_t* src_pages, int64_t n, void* stream);
+
+/* Attention as hk_attention_kv8 for a batch whose sequences begin with the same tokens in the
+ * same pages (hk_kv8_arrange forks them so): the shared pages are read once per group.
+ * Group g < G is the sequences [groups[g], groups[g + 1]) of the batch (int32 [G + 1] on the device, from 0
+ * to B, strictly increasing); the first shared[g] tokens (int32 [G] on the device) of each of them
+ * lie in the pages that the table row of the group's first sequence names, as far as they fill whole blocks of
+ * 128 tokens; what is left of them is read from each sequence's own table row. shared[g] = 0, and groups of one sequence,
+ * are fine. The result is hk_attention_kv8's, but for the order of its fp32 sums. Not shared in
+ * fact, and read by a sequence itself, are tokens past the first sequence's length, and those of a
+ * sequence that has queries which do not see all of them. Groups out of order or range take no
+ * part (every sequence's tokens are its own) and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG.
+ * Many query rows per group run on a tensor-core kernel for what is shared when Q is bf16 with rows that are
+ * 16-byte aligned and there are up to 64 groups (weights rounded to bf16, 2^-8, before they meet V); else on the
+ * few-row kernels. From 256 rows of each sequence and KV head on the call is hk_attention_kv8's.
+ * `workspace`: device memory of hk_attention_kv8_shared_workspace_size bytes (up to 60 MB and 8 · head_dim bytes for
+ * each of up to 2^17 query rows), 256-byte aligned. Everything else as hk_attention_kv8. */
+hk_status hk_attention_kv8_shared(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                                  const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                                  const int32_t* lengths, const int32_t* counts, const int32_t* groups,
+                                  const int32_t* shared, int64_t G, void* O, const int64_t o_strides[3], float* lse,
+                                  int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* The same with test controls. `flags`: HK_KV8_FEW_ROWS (units of 16 query rows) or HK_KV8_MANY_ROWS (what is shared
+ * in units of 256 rows on the tensor-core kernel; refused for what it does not take), 0: chosen by shape;
+ * HK_KV8_FAULT_DROP_ARRIVE. `timeout_ns` bounds each wait (0: 1 s). */
+hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
+                                     const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                                     const int32_t* lengths, const int32_t* counts, const int32_t* groups,
+                                     const int32_t* shared, int64_t G, void* O, const int64_t o_strides[3], float* lse,
+                                     int64_t B, int64_t T, int64_t Hq, int32_t causal, float scale, void* workspace,
+                                     size_t workspace_bytes, uint32_t flags, uint64_t timeout_ns, void* stream);
+size_t hk_attention_kv8_shared_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq, int64_t max_pages,
+                                              int64_t G);
 
 /* The norm of each head's query and key and the rotation by its token's position, in one pass:
  *     y = x / sqrt(mean(x^2) + eps) · w;   (a, b) -> (a cos t - b sin t, a sin t + b cos t)
