@@ -77,7 +77,7 @@ bool wide_pays(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t 
 }
 
 struct Workspace {
-    int64_t whole[2], slots, rows;   // rows of sums: of split units of 16 rows, of whole ones, of split units of 256 rows
+    int64_t whole[2], slots, rows;   // rows of sums: of split units of 16 rows, of whole ones, of split units of 128 rows
     int64_t shared_units;
     size_t ml, info, shared_info, seqs, total;
 };
@@ -108,12 +108,12 @@ bool shape_ok(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t m
 bool on_its_own(const hk_kv8_cache* c, int64_t T, int64_t Hq) { return T * (Hq / c->heads) >= kOwnTileRows; }
 
 template <int kD, typename T>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const uint8_t* k_codes, const uint8_t* v_codes, const SharedParams& p,
-                   cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
+                   const SharedParams& p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     if (p.wide_runs > 0)
         e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads), WideGeometry<kD>::kSmemBytes, st,
-                         k_codes, v_codes, p);
+                         wide_k, wide_v, p);
     if (e != cudaSuccess) return e;
     e = launch_early(&kv8_shared_kernel<kD, T>, dim3(static_cast<unsigned>(p.warps / kDecodeWarps)), dim3(32 * kDecodeWarps),
                                  SharedGeometry<kD>::kSmemBytes, st, tk, tv, p);
@@ -182,6 +182,9 @@ extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, con
     CUtensorMap tk, tv;
     if ((s = encode_codes(enc, &tk, cache->k_codes, cache, kTileKeys)) != HK_OK) return s;
     if ((s = encode_codes(enc, &tv, cache->v_codes, cache, kTileKeys)) != HK_OK) return s;
+    CUtensorMap wk = tk, wv = tv;                    // whole pages at a time
+    if (wide && (s = encode_codes(enc, &wk, cache->k_codes, cache, cache->page_size)) != HK_OK) return s;
+    if (wide && (s = encode_codes(enc, &wv, cache->v_codes, cache, cache->page_size)) != HK_OK) return s;
 
     const Workspace w = workspace(cache, B, T, Hq, G, G <= kWideGroups);
     char* const base = static_cast<char*>(scratch);
@@ -241,9 +244,8 @@ extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, con
         p.wait.launch_id = hk_host::next_launch_id();
         const bool half = type == HK_TYPE_FP16;
         cudaError_t e;
-        const uint8_t *kc = static_cast<const uint8_t*>(cache->k_codes), *vc = static_cast<const uint8_t*>(cache->v_codes);
-        if (cache->head_dim == 64) e = half ? launch<64, __half>(tk, tv, kc, vc, p, st) : launch<64, __nv_bfloat16>(tk, tv, kc, vc, p, st);
-        else e = half ? launch<128, __half>(tk, tv, kc, vc, p, st) : launch<128, __nv_bfloat16>(tk, tv, kc, vc, p, st);
+        if (cache->head_dim == 64) e = half ? launch<64, __half>(tk, tv, wk, wv, p, st) : launch<64, __nv_bfloat16>(tk, tv, wk, wv, p, st);
+        else e = half ? launch<128, __half>(tk, tv, wk, wv, p, st) : launch<128, __nv_bfloat16>(tk, tv, wk, wv, p, st);
         if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the shared attention", e);
     }
     return HK_OK;

@@ -27,6 +27,7 @@ namespace kv8 {
 
 constexpr int kMaxShared = 512;        // sequences, and groups, of one launch
 constexpr int kSharedStep = 128;       // tokens that what is shared is rounded down to
+constexpr int kWideRows = 128;         // stacked rows of a unit on the tensor-core kernel
 
 template <int kD>
 struct SharedGeometry {
@@ -47,8 +48,8 @@ struct SharedParams : DecodeParams {
     int64_t whole[2];              // rows of part_o and part_ml where the sums of whole units begin: shared, own
     int4* shared_info;             // as info, of the units of the groups: [KV head][shared_units]
     int32_t shared_units;
-    int32_t wide_runs;             // CTAs that work on the shared units of 256 rows (kv8_shared_mma.cuh); 0: units of 16 rows here
-    int64_t shared_slots;          // row of part_o and part_ml where the sums of split units of 256 rows begin
+    int32_t wide_runs;             // CTAs that work on the shared units of 128 rows (kv8_shared_mma.cuh); 0: units of 16 rows here
+    int64_t shared_slots;          // row of part_o and part_ml where the sums of split units of 128 rows begin
     int4* seqs;                    // [n]: shared tiles, place of the group, its first sequence of this launch, queries
 };
 
@@ -345,7 +346,7 @@ kv8_shared_combine_kernel(const SharedParams p) {
     const int4 own = __ldcg(p.info + (static_cast<int64_t>(i) * p.Hkv + h) * p.row_tiles + row / kRows);
     int4 shared = make_int4(0, 0, 0, 0);
     int shared_row = 0;
-    const int unit_rows = p.wide_runs > 0 ? 256 : kRows;
+    const int unit_rows = p.wide_runs > 0 ? kWideRows : kRows;
     if (seq.x > 0) {
         shared_row = shared_rows(p, i - seq.z) + row;
         shared = __ldcg(p.shared_info + static_cast<int64_t>(h) * p.shared_units + shared_unit0(p, seq.y, seq.z) + shared_row / unit_rows);
@@ -362,7 +363,7 @@ kv8_shared_combine_kernel(const SharedParams p) {
         const int part = of_shared ? k : k - first_parts;
         if (x.x == 0) return p.whole[of_shared ? 0 : 1] + out_row;
         const int64_t slot = part == 0 ? static_cast<int64_t>(x.y) : 2 * (static_cast<int64_t>(x.z) + part);
-        if (of_shared && p.wide_runs > 0) return p.shared_slots + slot * 256 + shared_row % 256;
+        if (of_shared && p.wide_runs > 0) return p.shared_slots + slot * kWideRows + shared_row % kWideRows;
         return slot * kRows + (of_shared ? shared_row : row) % kRows;
     };
     float m = -INFINITY, l = 0.0f, acc[kVec];

@@ -2,24 +2,32 @@
 //
 // With 64 sequences of 8 query heads per KV head a shared token meets 512 rows: 4 · 512 · D
 // operations for 2 · D bytes, so the tensor cores bound the work and mma.sync with 16 rows
-// to a unit (each of which converts every tile again) is the wrong tool. Here a unit is 256 stacked rows
-// (two tiles of 128) of a group and KV head, and codes become bf16 once per unit: E4M3 times
-// a power of two is exact in it.
+// to a unit (each of which converts every tile again) is the wrong tool. Here a unit is 128 stacked rows
+// of a group and KV head: S = Q·Kᵀ (two buffers) and O += P·V in Tensor Memory on tcgen05.mma, P
+// in Tensor Memory too. All units' blocks of 128 tokens, in order, are cut into equal runs, one per
+// CTA, since a prefix has few units and many blocks: each run leaves unnormalised rows,
+// maxima and sums of its units in memory for the combining kernel.
 //
-// The schedule of a CTA is the attention-forward kernel's (attn_kernel.cuh): two softmax
-// warpgroups of one tile each, a thread to a row; one MMA-issuing warp per tile; S = Q·Kᵀ
-// and O += P·V in Tensor Memory; a ring of K and V blocks of 128 tokens. Two things differ. The
-// ring is filled by a converting warpgroup: it loads 16 codes per thread (the next block's loads are in
-// flight while this one's codes are converted), moves their bits to where bf16 has
-// them, multiplies by 2^120 (E4M3's exponent bias is 120 less; exact, subnormal codes
-// too) and by the page's scale, and writes the 128-byte-swizzled rows that
-// the MMAs read. And all units' blocks, in order, are cut into equal runs, one per CTA, since a
-// prefix has few units and many blocks: each run leaves unnormalised rows, maxima
-// and sums of its units in memory for the combining kernel.
+// A CTA: a producing warp streams the codes of K and V page by page (TMA) into a ring; two
+// converting warpgroups write them, as the 128-byte-swizzled rows that the MMAs read, into a second one; one thread
+// issues the MMAs; a softmax warpgroup has a thread to a row, as in attn_kernel.cuh. Conversion competes
+// with the softmax for the same pipes, so it is kept short. Keys become f16, two per
+// conversion instruction and exactly, and are met by queries in f16: a row is scaled by a power
+// of two as in kv8_decode.cuh (exact down to 2^-24 of its largest element). The pages'
+// scales do not touch them: a chain of the row's maximum is 16 columns, a page at least,
+// and takes the scale as a whole, and the exponential's multiply-add has it as its factor. Values become bf16
+// (f16 would not hold pages of different scales side by side): their bits are moved to where
+// bf16 has them and multiplied by 2^120 (E4M3's exponent bias is 120 less) times the scale,
+// exact, subnormal codes too. Weights meet them in bf16.
 //
-// Registers: 512 threads begin with 128 each; the softmax warpgroups take 184, the
-// converting one 96, the MMA-issuing warps (a warpgroup, two of them idle) 48.
+// Two tiles of 128 rows to a unit (so that a block is converted once for 256) took 10000 cycles a block: Q and P of
+// two tiles leave shared memory for two blocks in each ring, too few to hide a load and a conversion.
+//
+// Registers: 512 threads begin with 128 each; the softmax warpgroup takes 200, the
+// others 104.
 #pragma once
+
+#include <type_traits>
 
 #include "attn_kernel.cuh"
 #include "kv8_shared.cuh"
@@ -27,28 +35,50 @@
 namespace hk {
 namespace kv8 {
 
-constexpr int kWideRows = 256;         // stacked rows of a unit
 constexpr int kWideGroups = 64;        // groups of a call on this form
+constexpr int kWideBlock = 128;        // tokens of a block
 constexpr int kWideThreads = 512;
-constexpr int kWideSoftmaxWarps = 8;
-constexpr int kConvertThreads = 128;
-constexpr int kSoftmaxRegs = 168, kConvertRegs = 120, kIssueRegs = 56;
-constexpr int kWideRegisters = 256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs;
+constexpr int kWideIssueWarp = 4, kWideLoadWarp = 5, kWideConvertWarp = 8;      // after four softmax warps; eight convert
+constexpr int kConvertThreads = 256;
+constexpr int kSoftmaxRegs = 200, kConvertRegs = 104, kIssueRegs = 104;
+constexpr int kWideRegisters = 128 * kSoftmaxRegs + 256 * kConvertRegs + 128 * kIssueRegs;
 static_assert(kWideRegisters <= kWideThreads * 128, "registers of the launch");
 constexpr uint32_t kErrSoftmaxWait = 1u << 19;
 
 template <int kD>
 struct WideGeometry {
-    using A = attn::AttnGeometry<kD>;
-    static_assert(A::kRowSplit == 1, "a thread to a row");
-    static constexpr int kOffPlan = A::kOffXchg;                              // blocks, first sequence, blocks of each group
+    static constexpr int kChunkBytes = 128 * 128;                             // 128 rows of 64 16-bit elements
+    static constexpr int kTileBytes = kD / 64 * kChunkBytes;                  // Q, or a block of K or V
+    static constexpr int kSlots = kD == 128 ? 3 : 6;                          // K and V blocks in 16 bits
+    static constexpr int kRaw = kD == 128 ? 6 : 8;                            // and as codes
+    static constexpr int kRawBytes = kWideBlock * kD;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffKV = kTileBytes;
+    static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
+    static constexpr int kOffBars = kOffRaw + kRaw * kRawBytes;
+    // q_full, q_empty, p_full, o_done, s_full[2], s_free[2], kv_full and kv_empty of the slots, raw_full and raw_empty
+    static constexpr int kNumBars = 8 + 2 * kSlots + 2 * kRaw;
+    // factors of the values of 16 tokens each: [kRaw][2][8] bf16 pairs, whose product it is, and whether the second ones matter
+    static constexpr int kFactorBytes = 17 * 4;
+    static constexpr int kOffFactors = kOffBars + kNumBars * 8;
+    // scales of the keys of 16 tokens each, of the last kKeyScales blocks (no role is so far ahead of the softmax)
+    static constexpr int kKeyScales = 16;
+    static constexpr int kOffKeyScales = (kOffFactors + kRaw * kFactorBytes + 15) / 16 * 16;      // (read 16 bytes at a time)
+    static_assert(3 + (kSlots + kRaw + 1) / 2 < kKeyScales, "blocks ahead of the softmax");
+    static constexpr int kOffTmemHolder = kOffKeyScales + kKeyScales * 32;
+    static constexpr int kOffPlan = kOffTmemHolder + 16;                      // blocks, first sequence, blocks of each group
     static constexpr int kSmemBytes = kOffPlan + (3 * kWideGroups + 2) * 4 + 1024;
     static_assert(kSmemBytes <= attn::kSmemLimit, "shared memory");
+    static_assert(kOffRaw % 1024 == 0 && kOffKV % 1024 == 0 && kOffBars % 8 == 0 && kOffFactors % 4 == 0 && kOffKeyScales % 16 == 0, "alignment");
+    // TMEM columns: O (kD), S_0, S_1 (128 each), P (64: two bf16 per column)
+    static constexpr int kColO = 0, kColS = 128, kColP = 384, kTmemCols = 512;
+    static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128) & ~((7u << 7) | (7u << 10));     // A and B f16
+    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, kD) | (1u << 16);                    // B (V) MN-major
 };
 
 // A run's share of a unit: blocks [first, last) of `blocks` for rows from `row0` on.
 struct WidePiece {
-    int section, h, pair, first, last, blocks;
+    int section, h, tile, first, last, blocks;
     Group group;
     bool valid;
 };
@@ -70,43 +100,43 @@ struct WideWalk {
         w.blocks = blocks_of[section];
         const int first = max(first_of[section], p.b0), last_seq = min(first_of[section + 1], p.b0 + p.n);
         w.group = Group{first - p.b0, max(0, last_seq - first), w.blocks * (kSharedStep / kTileKeys)};
-        const int pairs = (shared_rows(p, w.group.n) + kWideRows - 1) / kWideRows;
+        const int tiles = (shared_rows(p, w.group.n) + kWideRows - 1) / kWideRows;
         int local = at - prefix[section];
         const int unit = local / w.blocks;
         w.first = local - unit * w.blocks;
-        w.h = unit / pairs;
-        w.pair = unit - w.h * pairs;
+        w.h = unit / tiles;
+        w.tile = unit - w.h * tiles;
         w.last = min(w.blocks, w.first + end - at);
         at += w.last - w.first;
         return w;
     }
 };
 
-template <int kD>
-__device__ __forceinline__ bool wide_has_second_tile(const SharedParams& p, const WidePiece& w) {
-    return shared_rows(p, w.group.n) > w.pair * kWideRows + kWideRows / 2;
+// a · b, of two bf16 each.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// Four codes to bf16 times `unit` (2^120) times `scale`, in two words of two.
-__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t unit, uint32_t scale) {
+// Four codes to bf16 times `factor` / 2^120, in two words of two.
+__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t factor) {
     const uint32_t h0 = __byte_perm(w, 0u, 0x1404), h1 = __byte_perm(w, 0u, 0x3424);     // each code in a high byte
-    uint32_t a = (h0 & 0x80008000u) | (h0 >> 4 & 0x07F007F0u), b = (h1 & 0x80008000u) | (h1 >> 4 & 0x07F007F0u);
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(unit));
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(unit));
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(scale));
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(scale));
-    return make_uint2(a, b);
+    const uint32_t a = (h0 & 0x80008000u) | (h0 >> 4 & 0x07F007F0u), b = (h1 & 0x80008000u) | (h1 >> 4 & 0x07F007F0u);
+    return make_uint2(mul_bf16x2(a, factor), mul_bf16x2(b, factor));
 }
 
 // bf16 NaN (0x7FFF) in the places of two NaN codes, the low ones of `nan` (0xFF each).
 __device__ __forceinline__ uint32_t nan_pair(uint32_t nan) { return __byte_perm(nan, 0u, 0x1100) & 0x7FFF7FFFu; }
 
-// wait_mbar_poll() without a call: a kernel that splits its registers may make none.
+// Bounded waits without a call: a kernel that splits its registers may make none. Those on the chain of S, softmax and P·V
+// poll; the others let the hardware suspend them.
+template <bool kSuspend>
 __device__ __forceinline__ bool wide_wait(const WaitCtx& c, uint32_t bar, uint32_t parity, uint32_t code) {
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_test_wait(bar, parity)) return true;
-        if ((it & 4095u) == 0) {
+        if (kSuspend ? mbar_try_wait_suspend(bar, parity, 20000) : mbar_test_wait(bar, parity)) return true;
+        if (kSuspend || (it & 4095u) == 0) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
             if (wait_aborted(c)) return false;
@@ -122,10 +152,8 @@ __device__ __forceinline__ bool wide_wait(const WaitCtx& c, uint32_t bar, uint32
 
 template <int kD>
 __global__ void __launch_bounds__(kWideThreads, 1)
-kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes, const SharedParams p) {
-    using G = attn::AttnGeometry<kD>;
+kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
     using W = WideGeometry<kD>;
-    constexpr int kTileQ = attn::kTileQ, kTiles = attn::kTiles, kBlockKV = attn::kBlockKV;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -133,38 +161,48 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
     const uint32_t warp = threadIdx.x >> 5;
     const uint32_t lane = lane_id();
 
-    const uint32_t q_full = base + G::kOffBars;
-    auto kv_full = [&](int s) { return base + G::kOffBars + 8u * (1 + s); };
-    auto kv_empty = [&](int s) { return base + G::kOffBars + 8u * (1 + G::kSlots + s); };
-    auto s_full = [&](int t) { return base + G::kOffBars + 8u * (1 + 2 * G::kSlots + t); };
-    auto s_free = [&](int t) { return base + G::kOffBars + 8u * (3 + 2 * G::kSlots + t); };
-    auto p_full = [&](int t) { return base + G::kOffBars + 8u * (5 + 2 * G::kSlots + t); };
-    auto o_done = [&](int t) { return base + G::kOffBars + 8u * (7 + 2 * G::kSlots + t); };
-    const uint32_t q_empty = base + G::kOffBars + 8u * (9 + 2 * G::kSlots);
-    auto p_smem = [&](int t) { return base + G::kOffP + static_cast<uint32_t>(t) * G::kPBytes; };
-    auto slot_addr = [&](int s) { return base + G::kOffKV + static_cast<uint32_t>(s) * G::kTileBytes; };
-    const uint32_t tmem_holder = base + G::kOffTmemHolder;
+    auto bar = [&](int i) { return base + W::kOffBars + 8u * static_cast<uint32_t>(i); };
+    const uint32_t q_full = bar(0), q_empty = bar(1), p_full = bar(2), o_done = bar(3);
+    auto s_full = [&](int i) { return bar(4 + i); };
+    auto s_free = [&](int i) { return bar(6 + i); };
+    auto kv_full = [&](int s) { return bar(8 + s); };
+    auto kv_empty = [&](int s) { return bar(8 + W::kSlots + s); };
+    auto raw_full = [&](int s) { return bar(8 + 2 * W::kSlots + s); };
+    auto raw_empty = [&](int s) { return bar(8 + 2 * W::kSlots + W::kRaw + s); };
+    auto slot_addr = [&](int s) { return base + W::kOffKV + static_cast<uint32_t>(s) * W::kTileBytes; };
+    auto raw_addr = [&](int s) { return base + W::kOffRaw + static_cast<uint32_t>(s) * W::kRawBytes; };
+    auto factor_addr = [&](int s) { return base + W::kOffFactors + static_cast<uint32_t>(s) * W::kFactorBytes; };
+    auto key_scale_addr = [&](int block) { return base + W::kOffKeyScales + static_cast<uint32_t>(block % W::kKeyScales) * 32u; };
+    const uint32_t tmem_holder = base + W::kOffTmemHolder;
     int32_t* const prefix = reinterpret_cast<int32_t*>(smem + W::kOffPlan);
     int32_t* const first_of = prefix + kWideGroups + 1;
     int32_t* const blocks_of = first_of + kWideGroups + 1;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, kConvertThreads / 32);
-        mbar_init(q_empty, kTiles);            // each tile's MMA issuer, once its last S of the piece is done
-        for (int s = 0; s < G::kSlots; ++s) {
-            mbar_init(kv_full(s), kConvertThreads / 32 + (s == 0 && (p.flags & kFlagDropArrive) ? 1 : 0));
-            mbar_init(kv_empty(s), kTiles);
+        mbar_init(q_full, 4);
+        mbar_init(q_empty, 1);                 // the last S of the piece is done
+        mbar_init(p_full, 128);
+        mbar_init(o_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(s_free(i), 128);
         }
-        for (int t = 0; t < kTiles; ++t) {
-            mbar_init(s_full(t), 1);
-            mbar_init(s_free(t), 4 * 32);
-            mbar_init(p_full(t), 4 * 32);
-            mbar_init(o_done(t), 1);
+        for (int s = 0; s < W::kSlots; ++s) {
+            mbar_init(kv_full(s), kConvertThreads / 32);
+            mbar_init(kv_empty(s), 1);
+        }
+        for (int s = 0; s < W::kRaw; ++s) {
+            mbar_init(raw_full(s), s == 0 && (p.flags & kFlagDropArrive) ? 2 : 1);
+            mbar_init(raw_empty(s), kConvertThreads / 32);
         }
         fence_mbar_init_cluster();
     }
-    if (warp == kWideSoftmaxWarps) {
-        tmem_alloc_one(tmem_holder, G::kTmemCols);
+    if (threadIdx.x == 32) {
+        prefetch_tensor_map(&tmap_k);
+        prefetch_tensor_map(&tmap_v);
+    }
+    if (warp == kWideIssueWarp) {
+        tmem_alloc_one(tmem_holder, W::kTmemCols);
         tmem_relinquish_one();
     }
     griddep_wait();                            // launched early behind the kernel that may have written the cache or q
@@ -211,7 +249,7 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + G::kOffTmemHolder);
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + W::kOffTmemHolder);
     const int ctas = static_cast<int>(gridDim.x), self = static_cast<int>(blockIdx.x);
     const int total = prefix[p.G], per = (total + ctas - 1) / ctas;
     WideWalk walk{p, prefix, first_of, blocks_of, 0, 0, 0};
@@ -219,91 +257,80 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
     walk.end = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(walk.at) + per));
     const int begin = walk.at;
     bool abort_seen = false;
-    auto wait_lane0 = [&](uint32_t bar, uint32_t parity, uint32_t code) {      // a warp's wait: lane 0 polls, all see it
+    // a warp's waits: lane 0 looks, all see
+    auto wait_warp = [&](uint32_t b, uint32_t parity, uint32_t code, auto suspend) {
         uint32_t ok = 0;
-        if (lane == 0) ok = wide_wait(p.wait, bar, parity, code) ? 1u : 0u;
+        if (lane == 0) ok = wide_wait<decltype(suspend)::value>(p.wait, b, parity, code) ? 1u : 0u;
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok) (void)mbar_test_wait(bar, parity);
+        if (ok) (void)mbar_test_wait(b, parity);
         __syncwarp();
         return ok != 0;
     };
+    constexpr std::integral_constant<bool, false> poll{};
+    constexpr std::integral_constant<bool, true> suspend{};
+    // position u of the order in which n blocks' K and V are used: K_0, (K_{j+1}, V_j)..., V_{n-1}
+    auto block_at = [](int u, int n, bool& is_k) {
+        is_k = u == 0 || ((u & 1) != 0 && u < 2 * n - 1);
+        return u == 2 * n - 1 ? n - 1 : is_k ? (u + 1) / 2 : u / 2 - 1;
+    };
 
-    if (warp >= 12) {
+    if (warp >= kWideConvertWarp) {
         // ------------------------------------------------ converting warps --
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
         constexpr int kTokenChunks = kD / 16;                          // 16-code pieces of a token
-        constexpr int kLoads = kBlockKV * kTokenChunks / kConvertThreads;
-        constexpr int kStepTokens = kConvertThreads / kTokenChunks;    // tokens between a thread's loads
-        const int ct = static_cast<int>(threadIdx.x) - 12 * 32;
-        const int chunk = ct % kTokenChunks, token = ct / kTokenChunks;
-        int slot = 0;
-        uint32_t ring_ph = 0;
-        int pieces = 0;
-        // pages and scales of the 32 pieces of 16 tokens of blocks [window, window + 4), one per lane
-        struct Window {
-            int page;
-            uint32_t ks, vs;       // scales as bf16 pairs
+        constexpr int kPieces = kWideBlock * kTokenChunks / kConvertThreads;
+        constexpr int kStepTokens = kConvertThreads / kTokenChunks;    // tokens between a thread's pieces
+        const int ct = static_cast<int>(threadIdx.x) - kWideConvertWarp * 32;
+        const uint32_t chunk = ct % kTokenChunks, token = ct / kTokenChunks;
+        int slot = 0, rs = 0;
+        uint32_t ring_ph = 0, raw_ph = 0;
+        // 16 columns of row `tok`: two 16-byte units of the 64-column half that they lie in; the halves' threads (which meet the
+        // same banks) write them in opposite order
+        auto put = [&](uint32_t tok, const uint32_t (&o)[8]) {
+            const uint32_t row = slot_addr(slot) + (chunk >> 2) * W::kChunkBytes + tok * 128u;
+            const uint32_t unit = 2u * (chunk & 3u), sw = tok & 7u;
+            const bool flip = (chunk >> 2) != 0;
+            const uint32_t lo = row + ((unit ^ sw) << 4), hi = row + (((unit + 1u) ^ sw) << 4);
+            st_shared_v4(flip ? hi : lo, flip ? o[4] : o[0], flip ? o[5] : o[1], flip ? o[6] : o[2], flip ? o[7] : o[3]);
+            st_shared_v4(flip ? lo : hi, flip ? o[0] : o[4], flip ? o[1] : o[5], flip ? o[2] : o[6], flip ? o[3] : o[7]);
         };
-        for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next(), ++pieces) {
-            const int32_t* const table = p.table + first_of[w.section] * p.table_stride;
-            auto look_up = [&](int block) {
-                Window x = {0, 0u, 0u};
-                const int key = block * kBlockKV + static_cast<int>(lane) * 16;
-                if (key < w.blocks * kBlockKV) {
-                    const int32_t pg = table[key >> p.page_shift];
-                    if (pg < 0 || pg >= p.num_pages) {
-                        atomicOr(p.wait.status, kErrPage);
-                    } else {
-                        x.page = pg;
-                        const int64_t ph = static_cast<int64_t>(pg) * p.Hkv + w.h;
-                        const uint32_t ks = __float_as_uint(p.k_scale[ph]) >> 16, vs = __float_as_uint(p.v_scale[ph]) >> 16;
-                        x.ks = ks | ks << 16;
-                        x.vs = vs | vs << 16;
-                    }
-                }
-                return x;
-            };
-            int window = w.first;
-            Window cur = look_up(window), ahead = look_up(window + 4);
-            auto load = [&](uint4 (&x)[kLoads], bool is_k, int block) {
-                const bool in_cur = block < window + 4;
-                const uint8_t* const codes = is_k ? k_codes : v_codes;
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int tok = token + i * kStepTokens;
-                    const int page = __shfl_sync(0xffffffffu, in_cur ? cur.page : ahead.page, (block - window & 3) * 8 + (tok >> 4));
-                    const int place = (block * kBlockKV + tok) & (p.page_size - 1);
-                    const int64_t row = ((static_cast<int64_t>(page) * p.Hkv + w.h) << p.page_shift) + place;
-                    x[i] = *reinterpret_cast<const uint4*>(codes + row * kD + 16 * chunk);
-                }
-            };
-            // position u of the consumption order: K_0, (K_{j+1}, V_j)..., V_{n-1}
-            const int n = w.last - w.first;
-            auto at_position = [&](int u, bool& is_k) {
-                if (u == 0) { is_k = true; return w.first; }
-                if (u == 2 * n - 1) { is_k = false; return w.last - 1; }
-                is_k = (u & 1) != 0;
-                return w.first + (is_k ? (u + 1) / 2 : u / 2 - 1);
-            };
-            auto convert = [&](const uint4 (&x)[kLoads], bool is_k, int block) {
-                const bool in_cur = block < window + 4;
-                const int s = slot;
-                const uint32_t parity = ring_ph ^ 1u;
-                if (++slot == G::kSlots) {
-                    slot = 0;
-                    ring_ph ^= 1u;
-                }
-                if (!wait_lane0(kv_empty(s), parity, kErrWaitRing)) return false;
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int tok = token + i * kStepTokens;
-                    const uint32_t mine = is_k ? (in_cur ? cur.ks : ahead.ks) : (in_cur ? cur.vs : ahead.vs);
-                    const uint32_t scale = __shfl_sync(0xffffffffu, mine, (block - window & 3) * 8 + (tok >> 4));
-                    const uint32_t words[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next()) {
+          const int n = w.last - w.first;
+          for (int u = 0; u < 2 * n; ++u) {
+            bool is_k;
+            block_at(u, n, is_k);
+            if (!wait_warp(raw_full(rs), raw_ph, kErrWaitData, poll) || !wait_warp(kv_empty(slot), ring_ph ^ 1u, kErrWaitRing, poll)) {
+                abort_seen = true;
+                break;
+            }
+            if (is_k) {
+#pragma unroll 2
+                for (int i = 0; i < kPieces; ++i) {
+                    const uint32_t tok = token + i * kStepTokens;
+                    const uint4 x = ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk));
+                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint2 v = codes_to_bf16(words[k], 0x7B807B80u, scale);
+                        o[2 * k] = e4m3x2_to_f16x2(words[k] & 0xFFFFu);
+                        o[2 * k + 1] = e4m3x2_to_f16x2(words[k] >> 16);
+                    }
+                    put(tok, o);
+                }
+            } else {
+                uint32_t second;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(second) : "r"(factor_addr(rs) + 64u));
+#pragma unroll 2
+                for (int i = 0; i < kPieces; ++i) {
+                    const uint32_t tok = token + i * kStepTokens;
+                    const uint4 x = ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk));
+                    uint32_t factor;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(factor) : "r"(factor_addr(rs) + 4u * (tok >> 4)));
+                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint2 v = codes_to_bf16(words[k], factor);
                         o[2 * k] = v.x;
                         o[2 * k + 1] = v.y;
                     }
@@ -311,191 +338,239 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
                     uint32_t carry = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) carry |= (words[k] & 0x7F7F7F7Fu) + 0x01010101u;
-                    if (carry & 0x80808080u) {
+                    if (((carry & 0x80808080u) | second) != 0) {
+                        uint32_t more;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(more) : "r"(factor_addr(rs) + 32u + 4u * (tok >> 4)));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t nan = nan_codes(words[k]);
-                            o[2 * k] |= nan_pair(nan);
-                            o[2 * k + 1] |= nan_pair(nan >> 16);
+                            o[2 * k] = mul_bf16x2(o[2 * k], more) | nan_pair(nan);
+                            o[2 * k + 1] = mul_bf16x2(o[2 * k + 1], more) | nan_pair(nan >> 16);
                         }
                     }
-                    // 16 columns of row `tok`: two 16-byte units of the 64-column half that they lie in; the halves' threads
-                    // (which meet the same banks) write them in opposite order
-                    const uint32_t row = slot_addr(s) + (chunk >> 2) * G::kChunkBytes + static_cast<uint32_t>(tok) * 128u;
-                    const uint32_t unit = 2u * (chunk & 3), sw = static_cast<uint32_t>(tok) & 7u, flip = chunk >> 2 & 1;
-                    const uint32_t first = row + (((unit + flip) ^ sw) << 4), second = row + (((unit + 1 - flip) ^ sw) << 4);
-                    if (flip) {
-                        st_shared_v4(first, o[4], o[5], o[6], o[7]);
-                        st_shared_v4(second, o[0], o[1], o[2], o[3]);
-                    } else {
-                        st_shared_v4(first, o[0], o[1], o[2], o[3]);
-                        st_shared_v4(second, o[4], o[5], o[6], o[7]);
-                    }
+                    put(tok, o);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(kv_full(s));
-                return true;
-            };
-            uint4 a[kLoads], b[kLoads];
-            load(a, true, w.first);
-            // ---- Q of this piece once both issuers have finished the previous one's S
-            if (pieces > 0 && !wait_lane0(q_empty, (pieces - 1) & 1, kErrWaitRing)) {
-                abort_seen = true;
-                break;
             }
-            {
-                constexpr int kRowUnits = kD / 8;
-                const int rows = shared_rows(p, w.group.n), per_seq = p.T * p.group;
-                const int tiles = wide_has_second_tile<kD>(p, w) ? 2 : 1;
-#pragma unroll 4
-                for (int i = ct; i < tiles * kTileQ * kRowUnits; i += kConvertThreads) {
-                    const int r = i / kRowUnits, unit = i % kRowUnits;
-                    const int row = w.pair * kWideRows + r;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < rows) {
-                        const int seq = row / per_seq, rest = row - seq * per_seq, t = rest / p.group;
-                        const uint16_t* const src = static_cast<const uint16_t*>(p.q) + (p.b0 + w.group.first + seq) * p.q_stride_b +
-                                                    t * p.q_stride_t + static_cast<int64_t>(w.h * p.group + rest - t * p.group) * p.q_stride_h;
-                        x = *reinterpret_cast<const uint4*>(src + 8 * unit);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(kv_full(slot));
+                mbar_arrive(raw_empty(rs));
+            }
+            if (++slot == W::kSlots) {
+                slot = 0;
+                ring_ph ^= 1u;
+            }
+            if (++rs == W::kRaw) {
+                rs = 0;
+                raw_ph ^= 1u;
+            }
+          }
+        }
+    } else if (warp >= kWideIssueWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == kWideLoadWarp) {
+            // ------------------------------------------ producing warp --
+            int rs = 0, key_block = 0;
+            uint32_t raw_ph = 0;
+            const int boxes = kWideBlock >> p.page_shift;                // pages of a block
+            for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next()) {
+                const int32_t* const table = p.table + first_of[w.section] * p.table_stride;
+                // pages (as rows of the tensor map) and scales of the 32 pieces of 16 tokens of blocks [window, window + 4), one
+                // per lane, and of the four blocks after those
+                struct Window {
+                    int row;
+                    float ks;
+                    uint32_t vs;           // exponent field of V's scale, a power of two
+                };
+                auto look_up = [&](int block) {
+                    Window x = {w.h, 0.0f, 0u};
+                    const int key = block * kWideBlock + static_cast<int>(lane) * 16;
+                    if (key < w.blocks * kWideBlock) {
+                        const int32_t pg = table[key >> p.page_shift];
+                        if (pg < 0 || pg >= p.num_pages) {
+                            atomicOr(p.wait.status, kErrPage);      // (scale 0: nothing of page 0, read in its place, comes through)
+                        } else {
+                            const int64_t ph = static_cast<int64_t>(pg) * p.Hkv + w.h;
+                            x = Window{static_cast<int>(ph), p.k_scale[ph], __float_as_uint(p.v_scale[ph]) >> 23 & 0xFFu};
+                        }
                     }
-                    const uint32_t tile = r / kTileQ, tr = r % kTileQ;
-                    st_shared_v4(base + G::kOffQ + tile * G::kTileBytes + (unit >> 3) * G::kChunkBytes + tr * 128u +
-                                     (((unit & 7u) ^ (tr & 7u)) << 4), x.x, x.y, x.z, x.w);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
-            }
-            // two positions at a time: one's loads are in flight while the other is converted
-            bool ok = true;
-            for (int u = 0; u < 2 * n && ok; u += 2) {
-                bool is_k0, is_k1, is_k2 = false;
-                const int b0 = at_position(u, is_k0), b1 = at_position(u + 1, is_k1);
-                load(b, is_k1, b1);
-                ok = convert(a, is_k0, b0);
-                if (!ok) break;
-                if (u + 2 < 2 * n) {
-                    const int b2 = at_position(u + 2, is_k2);
-                    // (V of a block follows K of the next: the window moves when both are past its first four blocks)
-                    if (min(b1, b2) >= window + 4) {
+                    return x;
+                };
+                int window = w.first;
+                Window cur = look_up(window), ahead = look_up(window + 4);
+                const int n = w.last - w.first;
+                for (int u = 0; u < 2 * n; ++u) {
+                    bool is_k;
+                    const int block = w.first + block_at(u, n, is_k);
+                    // (K runs a block ahead of V: the window moves with V)
+                    if (!is_k && block >= window + 4) {
                         window += 4;
                         cur = ahead;
                         ahead = look_up(window + 4);
                     }
-                    load(a, is_k2, b2);
+                    const bool in_cur = block < window + 4;
+                    const int at = (block - window & 3) * 8;
+                    const uint32_t mine = is_k ? __float_as_uint(in_cur ? cur.ks : ahead.ks) : (in_cur ? cur.vs : ahead.vs);
+                    const uint32_t scale = __shfl_sync(0xffffffffu, mine, at + (lane & 7u));
+                    if (!wait_warp(raw_empty(rs), raw_ph ^ 1u, kErrWaitRing, suspend)) {
+                        abort_seen = true;
+                        break;
+                    }
+                    if (is_k) {
+                        if (lane < 8)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(key_scale_addr(key_block) + 4u * lane), "r"(scale) : "memory");
+                        ++key_block;
+                    } else {
+                        // 2^120 · scale as a product of two, for bf16 holds nothing above 2^127 (no scale: 0)
+                        const uint32_t first = scale == 0 ? 0u : min(scale + 120u, 254u), rest = scale == 0 ? 127u : 127u + scale + 120u - first;
+                        const bool second = __any_sync(0xffffffffu, rest != 127u);
+                        if (lane < 8) {
+                            const uint32_t at8 = factor_addr(rs) + 4u * lane;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at8), "r"(first << 7 | first << 23) : "memory");
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at8 + 32u), "r"(rest << 7 | rest << 23) : "memory");
+                        }
+                        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 64u), "r"(second ? 1u : 0u) : "memory");
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(raw_full(rs), W::kRawBytes);
+                    for (int k = 0; k < boxes; ++k) {
+                        const int row = __shfl_sync(0xffffffffu, in_cur ? cur.row : ahead.row, at + (k << p.page_shift >> 4));
+                        if (lane == 0)
+                            tma_load_3d(raw_addr(rs) + static_cast<uint32_t>((k << p.page_shift) * kD), is_k ? &tmap_k : &tmap_v, 0, 0, row,
+                                        raw_full(rs));
+                    }
+                    if (++rs == W::kRaw) {
+                        rs = 0;
+                        raw_ph ^= 1u;
+                    }
                 }
-                ok = convert(b, is_k1, b1);
             }
-            if (!ok) abort_seen = true;
         }
-    } else if (warp >= kWideSoftmaxWarps) {
-        // ------------------------------------------- MMA issue, one warp per tile --
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        const int t = static_cast<int>(warp) - kWideSoftmaxWarps;
-        if (t < kTiles && lane == 0) {
-            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
+        // ------------------------------------------- MMA issue --
+        if (warp == kWideIssueWarp && lane == 0) {
+            auto wait = [&](uint32_t b, uint32_t parity, uint32_t code) {
                 if (abort_seen) return false;
-                if (!wide_wait(p.wait, bar, parity, code)) abort_seen = true;
+                if (!wide_wait<false>(p.wait, b, parity, code)) abort_seen = true;
                 return !abort_seen;
             };
-            int s0 = 0;              // ring slot of the piece's first position
-            uint32_t ph0 = 0;        // and its phase
-            auto kv_slot = [&](int u) { return (s0 + u) % G::kSlots; };
-            auto kv_parity = [&](int u) { return ph0 ^ static_cast<uint32_t>(((s0 + u) / G::kSlots) & 1); };
-            const uint32_t qa = base + G::kOffQ + t * G::kTileBytes;
-            const uint32_t s_tmem = tmem_base + G::kColS + t * kBlockKV;
-            const uint32_t o_tmem = tmem_base + G::kColO + t * kD;
-            const uint32_t pa = p_smem(t);
-            const uint32_t p_tmem = tmem_base + G::kColP + t * (kBlockKV / 2);
-            uint32_t jp = 0;
-            bool any_block = false;
+            int slot = 0;
+            uint32_t ring_ph = 0;
+            // the next position's block in 16 bits: its address once it is there, and the barrier that gives it back
+            auto take = [&](uint32_t& addr, uint32_t& back) {
+                if (!wait(kv_full(slot), ring_ph, kErrWaitData)) return false;
+                addr = slot_addr(slot);
+                back = kv_empty(slot);
+                if (++slot == W::kSlots) {
+                    slot = 0;
+                    ring_ph ^= 1u;
+                }
+                return true;
+            };
+            const uint32_t qa = base + W::kOffQ;
+            uint32_t nb = 0;             // blocks of S issued so far: buffer nb & 1, its phase nb / 2
+            uint32_t pv = 0;             // of P·V
             int pieces = 0;
             for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next(), ++pieces) {
-                const int n_all = w.last - w.first;
-                const int n = t == 0 || wide_has_second_tile<kD>(p, w) ? n_all : 0;
+                const int n = w.last - w.first;
                 if (!wait(q_full, pieces & 1, kErrWaitData)) break;
-                auto issue_s = [&](int j, int u) {
-                    if ((j > 0 || any_block) && !wait(s_free(t), jp ^ static_cast<uint32_t>((j - 1) & 1), kErrWaitAcc)) return false;
-                    if (!wait(kv_full(kv_slot(u)), kv_parity(u), kErrWaitData)) return false;
+                auto issue_s = [&](bool last) {
+                    uint32_t ka, back;
+                    if (nb >= 2 && !wait(s_free(nb & 1u), (nb / 2 - 1) & 1u, kErrWaitAcc)) return false;
+                    if (!take(ka, back)) return false;
                     tc_fence_after_sync();
-                    const uint32_t ka = slot_addr(kv_slot(u));
+                    const uint32_t s_tmem = tmem_base + W::kColS + (nb & 1u) * kWideBlock;
 #pragma unroll
                     for (int kk = 0; kk < kD / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * G::kChunkBytes + (kk & 3) * 32;
-                        mma_bf16_one(s_tmem, smem_desc_kmajor_sw128(qa + off), smem_desc_kmajor_sw128(ka + off), G::kIdescS,
-                                     kk > 0 ? 1u : 0u);
+                        const uint32_t off = (kk >> 2) * W::kChunkBytes + (kk & 3) * 32;
+                        mma_bf16_one(s_tmem, smem_desc_kmajor_sw128(qa + off), smem_desc_kmajor_sw128(ka + off), W::kIdescS, kk > 0 ? 1u : 0u);
                     }
-                    mma_commit_one(s_full(t));
-                    mma_commit_one(kv_empty(kv_slot(u)));
-                    if (j == n - 1) mma_commit_one(q_empty);
+                    mma_commit_one(s_full(nb & 1u));
+                    mma_commit_one(back);
+                    if (last) mma_commit_one(q_empty);
+                    ++nb;
                     return true;
                 };
-                if (n == 0) {
-                    mbar_arrive(q_empty);
-                } else if (issue_s(0, 0)) {
-                    for (int j = 0; j < n && !abort_seen; ++j) {
-                        if (j + 1 < n && !issue_s(j + 1, attn::pos_k(j + 1))) break;
-                        const int uv = attn::pos_v(j, n_all);
-                        if (!wait(kv_full(kv_slot(uv)), kv_parity(uv), kErrWaitData)) break;
-                        if (!wait(p_full(t), jp ^ static_cast<uint32_t>(j & 1), kErrWaitAcc)) break;
-                        tc_fence_after_sync();
-                        const uint32_t va = slot_addr(kv_slot(uv));
+                if (!issue_s(n == 1)) break;
+                for (int j = 0; j < n; ++j, ++pv) {
+                    if (j + 1 < n && !issue_s(j + 2 == n)) break;
+                    uint32_t va, back;
+                    if (!take(va, back) || !wait(p_full, pv & 1u, kErrWaitAcc)) break;
+                    tc_fence_after_sync();
 #pragma unroll
-                        for (int kk = 0; kk < kBlockKV / 16; ++kk) {
-                            const uint64_t vdesc = smem_desc_mnmajor(va + kk * 2048, 128, G::kChunkBytes);
-                            const uint32_t acc = (j == 0 && kk == 0) ? 0u : 1u;
-                            if constexpr (G::kPInTmem)
-                                mma_bf16_ts_one(o_tmem, p_tmem + kk * 8, vdesc, G::kIdescPV, acc);
-                            else
-                                mma_bf16_one(o_tmem, smem_desc_kmajor_sw128(pa + (kk >> 2) * G::kChunkBytes + (kk & 3) * 32), vdesc,
-                                             G::kIdescPV, acc);
-                        }
-                        mma_commit_one(o_done(t));
-                        mma_commit_one(kv_empty(kv_slot(uv)));
-                    }
+                    for (int kk = 0; kk < kWideBlock / 16; ++kk)
+                        mma_bf16_ts_one(tmem_base + W::kColO, tmem_base + W::kColP + kk * 8, smem_desc_mnmajor(va + kk * 2048, 128, W::kChunkBytes),
+                                        W::kIdescPV, (j == 0 && kk == 0) ? 0u : 1u);
+                    mma_commit_one(o_done);
+                    mma_commit_one(back);
                 }
-                // positions that this tile does not use: arrive once each has landed
-                auto release = [&](int u) {
-                    if (!wait(kv_full(kv_slot(u)), kv_parity(u), kErrWaitData)) return false;
-                    mbar_arrive(kv_empty(kv_slot(u)));
-                    return true;
-                };
-                for (int u = 0; n == 0 && u < 2 * n_all && !abort_seen; ++u)
-                    if (!release(u)) break;
-                ph0 ^= static_cast<uint32_t>(((s0 + 2 * n_all) / G::kSlots) & 1);
-                s0 = (s0 + 2 * n_all) % G::kSlots;
-                jp ^= static_cast<uint32_t>(n & 1);
-                any_block = any_block || n > 0;
             }
         }
     } else {
-        // ------------------------------------------ softmax warpgroups --
+        // ------------------------------------------ softmax warpgroup --
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        const int t = static_cast<int>(warp >> 2) & 1;
-        const uint32_t quarter = warp & 3u;
-        const int r = static_cast<int>(quarter * 32 + lane);
-        const uint32_t lane_off = (quarter * 32u) << 16;
-        const uint32_t s_addr = tmem_base + lane_off + G::kColS + t * kBlockKV;
-        const uint32_t o_addr = tmem_base + lane_off + G::kColO + t * kD;
-        const float c = p.scale_log2;
-        uint32_t jp = 0;
-        int done = begin;              // blocks of the run before this piece
+        const int r = static_cast<int>(threadIdx.x);
+        const uint32_t lane_off = (warp * 32u) << 16;
+        const uint32_t o_addr = tmem_base + lane_off + W::kColO;
+        const uint32_t p_addr = tmem_base + lane_off + W::kColP;
+        float c = 0.0f;                // of this row: its scale's other factor times that of the softmax
+        uint32_t nb = 0;               // blocks so far
+        int pieces = 0;
         for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next()) {
-            const int n_all = w.last - w.first;
-            const int n = t == 0 || wide_has_second_tile<kD>(p, w) ? n_all : 0;
-            const bool whole = n_all == w.blocks;
-            const int slot = 2 * self + (done == begin ? 0 : 1);
+            const int n = w.last - w.first, done = begin + static_cast<int>(nb);
+            const bool whole = n == w.blocks;
+            const int slot = 2 * self + (nb == 0 ? 0 : 1);
             if (w.first == 0 && threadIdx.x == 0) {     // this run holds the unit's first block: it tells how the unit is made up
                 const int parts = whole ? 0 : (done + w.blocks - 1) / per - done / per + 1;
-                p.shared_info[static_cast<int64_t>(w.h) * p.shared_units + shared_unit0(p, w.section, w.group.first) + w.pair] =
+                p.shared_info[static_cast<int64_t>(w.h) * p.shared_units + shared_unit0(p, w.section, w.group.first) + w.tile] =
                     make_int4(parts, slot, self, 0);
             }
-            done += n_all;
+            // ---- this thread's row of Q, once the previous piece's S are done
+            const int row = w.tile * kWideRows + r, per_seq = p.T * p.group;
+            const bool live = row < shared_rows(p, w.group.n);
+            const int seq = row / per_seq, rest = row - seq * per_seq, tok = rest / p.group;
+            const int head = w.h * p.group + rest - tok * p.group;
+            if (pieces > 0 && !wait_warp(q_empty, (pieces - 1) & 1, kErrSoftmaxWait, suspend)) {
+                abort_seen = true;
+                break;
+            }
+            {
+                const uint16_t* const src = static_cast<const uint16_t*>(p.q) + (p.b0 + w.group.first + seq) * p.q_stride_b +
+                                            tok * p.q_stride_t + head * p.q_stride_h;
+                Raw8<__nv_bfloat16> x[kD / 8];
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < kD / 8; ++k) x[k].w[0] = live ? reinterpret_cast<const uint4*>(src)[k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < kD / 8; ++k) {
+                    const uint32_t words[4] = {x[k].w[0].x, x[k].w[0].y, x[k].w[0].z, x[k].w[0].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, words[i] & 0x7FFF7FFFu);
+                }
+                top = max(top & 0xFFFFu, top >> 16);
+                // 2^(10 - floor(log2 of the largest)), kept a normal number; 1 for rows of zeros and rows with an infinity or NaN
+                int field = 127 + 10 - (static_cast<int>(top >> 7) - 127);
+                if (top == 0 || top >= 0x7F80u) field = 127;
+                field = min(max(field, 1), 253);
+                const float mul = __uint_as_float(static_cast<uint32_t>(field) << 23);
+                c = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * p.scale_log2;
+#pragma unroll
+                for (int k = 0; k < kD / 8; ++k) {
+                    float f[8];
+                    widen8<__nv_bfloat16>(x[k], f);
+                    st_shared_v4(base + W::kOffQ + (k >> 3) * W::kChunkBytes + r * 128u + (((k & 7u) ^ (r & 7u)) << 4),
+                                 pack_f16x2(f[0] * mul, f[1] * mul), pack_f16x2(f[2] * mul, f[3] * mul), pack_f16x2(f[4] * mul, f[5] * mul),
+                                 pack_f16x2(f[6] * mul, f[7] * mul));
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            ++pieces;
             float m = 0.0f, l = 0.0f;      // running maximum (log2 units) used for P, and sum of P
-            for (int j = 0; j < n; ++j) {
-                const uint32_t par = jp ^ static_cast<uint32_t>(j & 1);
-                if (!wait_lane0(s_full(t), par, kErrSoftmaxWait)) {
+            for (int j = 0; j < n; ++j, ++nb) {
+                const uint32_t s_addr = tmem_base + lane_off + W::kColS + (nb & 1u) * kWideBlock;
+                if (!wait_warp(s_full(nb & 1u), nb / 2 & 1u, kErrSoftmaxWait, poll)) {
                     abort_seen = true;
                     break;
                 }
@@ -507,7 +582,7 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
                 tmem_load_32cols_at<96>(s_addr + 96, v);
                 tmem_wait_ld();
                 tc_fence_before_sync();
-                mbar_arrive(s_free(t));    // S is in registers: the next block's may be computed
+                mbar_arrive(s_free(nb & 1u));    // S is in registers: the block after the next may be computed
                 float acc[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -517,8 +592,22 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
                     for (int e = 3; e < 15; e += 2) a = fmax3(a, __uint_as_float(v[e0 + e]), __uint_as_float(v[e0 + e + 1]));
                     acc[k] = fmaxf(a, __uint_as_float(v[e0 + 15]));
                 }
-                const float mx = fmax3(fmax3(acc[0], acc[1], acc[2]), fmax3(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
-                float m_blk = mx * c;
+                // each chain's 16 columns lie in one page: their factor
+                float cs[8];
+                {
+                    const uint32_t at8 = key_scale_addr(static_cast<int>(nb));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 x = ld_shared_v4(at8 + 16u * k);
+                        cs[4 * k] = c * __uint_as_float(x.x);
+                        cs[4 * k + 1] = c * __uint_as_float(x.y);
+                        cs[4 * k + 2] = c * __uint_as_float(x.z);
+                        cs[4 * k + 3] = c * __uint_as_float(x.w);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] *= cs[k];
+                float m_blk = fmax3(fmax3(acc[0], acc[1], acc[2]), fmax3(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
                 // (scores of -inf alone: any finite maximum makes their weights 0)
                 if (m_blk == -INFINITY) m_blk = j == 0 ? 0.0f : m;
                 float alpha = 1.0f;
@@ -529,12 +618,9 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
                     m = m_blk;
                     l *= alpha;
                 }
-                const uint64_t c2 = f32x2(c, c);
                 const uint64_t nm2 = f32x2(-m, -m);
                 uint64_t sum2[4] = {0, 0, 0, 0};
                 uint32_t pk[64];
-                constexpr bool kEarlyP = G::kPInTmem;
-                constexpr int kFirstPairs = kEarlyP ? 32 : 64;
                 auto rescale_o = [&]() {
                     if (__any_sync(0xffffffffu, alpha != 1.0f)) {
 #pragma unroll
@@ -549,7 +635,7 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
                     }
                 };
                 auto exp_pair = [&](int e) {
-                    const uint64_t x = ffma2(f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, nm2);
+                    const uint64_t x = ffma2(f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f32x2(cs[e >> 3], cs[e >> 3]), nm2);
                     float x0, x1;
                     f32x2_split(x, x0, x1);
                     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
@@ -557,63 +643,38 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
                     pk[e] = pack_bf16x2_rn(__float_as_uint(p0), __float_as_uint(p1));
                 };
 #pragma unroll
-                for (int e = 0; e < kFirstPairs; ++e) exp_pair(e);
-                const uint32_t p_addr = tmem_base + lane_off + G::kColP + t * (kBlockKV / 2);
-                if constexpr (kEarlyP) {
-                    if (j > 0 && !wait_lane0(o_done(t), par ^ 1u, kErrSoftmaxWait)) {
-                        abort_seen = true;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    rescale_o();
-                    tmem_store_32cols(p_addr, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+                for (int e = 0; e < 32; ++e) exp_pair(e);
+                // P·V of the previous block must be done before its P is overwritten and O rescaled; the first half of P is
+                // stored while the second is computed
+                if (j > 0 && !wait_warp(o_done, (nb - 1) & 1u, kErrSoftmaxWait, poll)) {
+                    abort_seen = true;
+                    break;
                 }
+                tc_fence_after_sync();
+                if (j > 0) rescale_o();
+                tmem_store_32cols(p_addr, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
 #pragma unroll
-                for (int e = kFirstPairs; e < 64; ++e) exp_pair(e);
+                for (int e = 32; e < 64; ++e) exp_pair(e);
                 {
                     const uint64_t s01 = fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3]));
                     float lo, hi;
                     f32x2_split(s01, lo, hi);
                     l += lo + hi;
                 }
-                if constexpr (kEarlyP) {
-                    tmem_store_32cols(p_addr + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
-                    tmem_wait_st();
-                } else {
-                    // P·V of the previous block must be done before its P is overwritten and O rescaled
-                    if (j > 0 && !wait_lane0(o_done(t), par ^ 1u, kErrSoftmaxWait)) {
-                        abort_seen = true;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    rescale_o();
-                    tmem_wait_st();
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const uint32_t row = p_smem(t) + hh * G::kChunkBytes + static_cast<uint32_t>(r) * 128u;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            st_shared_v4(row + ((static_cast<uint32_t>(x) ^ (static_cast<uint32_t>(r) & 7u)) << 4), pk[32 * hh + 4 * x],
-                                         pk[32 * hh + 4 * x + 1], pk[32 * hh + 4 * x + 2], pk[32 * hh + 4 * x + 3]);
-                    }
-                    fence_proxy_async_smem();
-                }
+                tmem_store_32cols(p_addr + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+                tmem_wait_st();
                 tc_fence_before_sync();
-                mbar_arrive(p_full(t));
+                mbar_arrive(p_full);
             }
             // ---- the row's sums, unnormalised (reading O here, before this warp publishes the next piece's first P,
             // orders these reads before the P·V that overwrites O)
-            if (!abort_seen && n > 0) {
-                if (!wait_lane0(o_done(t), jp ^ static_cast<uint32_t>((n - 1) & 1), kErrSoftmaxWait)) {
+            if (!abort_seen) {
+                if (!wait_warp(o_done, (nb - 1) & 1u, kErrSoftmaxWait, poll)) {
                     abort_seen = true;
                 } else {
                     tc_fence_after_sync();
-                    const int in_unit = t * kTileQ + r, row = w.pair * kWideRows + in_unit;
-                    const int per_seq = p.T * p.group;
-                    const bool live = row < shared_rows(p, w.group.n);
-                    const int seq = row / per_seq, rest = row - seq * per_seq, tok = rest / p.group;
-                    const int64_t out_row = (static_cast<int64_t>(w.group.first + seq) * p.T + tok) * p.Hq + w.h * p.group + rest - tok * p.group;
-                    const int64_t at_row = whole ? p.whole[0] + out_row : p.shared_slots + static_cast<int64_t>(slot) * kWideRows + in_unit;
+                    const int64_t out_row = (static_cast<int64_t>(w.group.first + seq) * p.T + tok) * p.Hq + head;
+                    const int64_t at_row = whole ? p.whole[0] + out_row : p.shared_slots + static_cast<int64_t>(slot) * kWideRows + r;
                     const bool any = l > 0.0f || l != l;
 #pragma unroll
                     for (int cc = 0; cc < kD / 32; ++cc) {
@@ -634,7 +695,6 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
                     tc_fence_before_sync();
                 }
             }
-            jp ^= static_cast<uint32_t>(n & 1);
         }
     }
 
@@ -644,9 +704,9 @@ kv8_shared_mma_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __rest
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kWideSoftmaxWarps) {
+    if (warp == kWideIssueWarp) {
         tc_fence_after_sync();
-        tmem_dealloc_one(tmem_base, G::kTmemCols);
+        tmem_dealloc_one(tmem_base, W::kTmemCols);
     }
 }
 

@@ -121,8 +121,19 @@ __device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
     }
 }
 
+// The words of eight elements that another lane holds.
+template <typename T>
+__device__ __forceinline__ Raw8<T> shuffle8(const Raw8<T>& r, int from) {
+    Raw8<T> o;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+        o.w[i] = make_uint4(__shfl_sync(0xffffffffu, r.w[i].x, from), __shfl_sync(0xffffffffu, r.w[i].y, from),
+                            __shfl_sync(0xffffffffu, r.w[i].z, from), __shfl_sync(0xffffffffu, r.w[i].w, from));
+    return o;
+}
+
 template <typename T, int kLanes, bool kInterleaved, bool kVec>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 qk_norm_rope_kernel(const RopeParams p) {
     constexpr int kRowsStep = 32 / kLanes;           // rows of a warp at a time
     griddep_launch_dependents();
@@ -175,8 +186,23 @@ qk_norm_rope_kernel(const RopeParams p) {
     while (first < last) {
         const int op = first >= p.op_steps[0];
         const int base = op ? p.op_steps[0] : 0, end = min(last, op ? last : p.op_steps[0]);
-        float w[8];
-        weights8<T>(p, op, live ? d : 0, w);
+        // an output is (x a + o b) / root: x the element, o the one that it is turned with, a and b weight times cos and sin
+        uint64_t a2[4], b2[4];
+        {
+            float w[8];
+            weights8<T>(p, op, live ? d : 0, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (kInterleaved) {
+                    a2[k] = f32x2(w[2 * k] * c[k], w[2 * k + 1] * c[k]);
+                    b2[k] = f32x2(-w[2 * k + 1] * s[k], w[2 * k] * s[k]);
+                } else {
+                    a2[k] = f32x2(w[2 * k] * c[2 * k], w[2 * k + 1] * c[2 * k + 1]);
+                    const float o0 = __shfl_sync(0xffffffffu, w[2 * k], partner), o1 = __shfl_sync(0xffffffffu, w[2 * k + 1], partner);
+                    b2[k] = f32x2(o0 * s[2 * k], o1 * s[2 * k + 1]);
+                }
+            }
+        }
         const T* const src = static_cast<const T*>(p.in[op]) + b * p.in_b[op] + t * p.in_t[op] + (live ? d : 0);
         T* const dst = static_cast<T*>(p.out[op]) + b * p.out_b[op] + t * p.out_t[op] + d;
         const int64_t in_h = p.in_h[op], out_h = p.out_h[op];
@@ -191,36 +217,33 @@ qk_norm_rope_kernel(const RopeParams p) {
             for (int i = 0; i < kFlight; ++i) {
                 if (s0 + i >= end) break;
                 const int r = r0 + i * kRowsStep;
-                float y[8];
+                float y[8], o[8];
                 widen8<T>(raw[i], y);
-                if (p.norm) {
-                    float sum = 0.0f;
+                uint64_t y2[4];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) sum = fmaf(y[k], y[k], sum);
-                    if (!live) sum = 0.0f;
+                for (int k = 0; k < 4; ++k) y2[k] = f32x2(y[2 * k], y[2 * k + 1]);
+                float mul = 1.0f;
+                if (p.norm) {
+                    const uint64_t q = ffma2(y2[3], y2[3], ffma2(y2[2], y2[2], ffma2(y2[1], y2[1], fmul2(y2[0], y2[0]))));
+                    float lo, hi;
+                    f32x2_split(q, lo, hi);
+                    float sum = live ? lo + hi : 0.0f;
 #pragma unroll
                     for (int m = kLanes / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                    const float mul = rsqrtf(fmaf(sum, inv_d, p.eps));
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] *= mul * w[k];
+                    mul = rsqrtf(fmaf(sum, inv_d, p.eps));
                 }
-                float z[8];
                 if constexpr (kInterleaved) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        z[2 * k] = y[2 * k] * c[k] - y[2 * k + 1] * s[k];
-                        z[2 * k + 1] = y[2 * k] * s[k] + y[2 * k + 1] * c[k];
-                    }
+                    for (int k = 0; k < 8; ++k) o[k] = y[k ^ 1];
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float o = __shfl_sync(0xffffffffu, y[k], partner);
-                        z[k] = fmaf(o, s[k], y[k] * c[k]);
-                    }
+                    widen8<T>(shuffle8<T>(raw[i], partner), o);
                 }
-                if (!turns) {            // (not times 1 and 0: infinities)
+                float z[8];
+                const uint64_t mul2 = f32x2(mul, mul);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) z[k] = y[k];
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t x = fmul2(y2[k], a2[k]), turned = ffma2(f32x2(o[2 * k], o[2 * k + 1]), b2[k], x);
+                    f32x2_split(fmul2(turns ? turned : x, mul2), z[2 * k], z[2 * k + 1]);      // (not plus 0 times an infinity)
                 }
                 if (r < heads && live) store8<T, kVec>(dst + r * out_h, z);
             }

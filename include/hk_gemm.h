@@ -625,7 +625,7 @@ hk_status hk_attention_kv8_shared(const void* Q, int32_t type, const int64_t q_s
                                   size_t workspace_bytes, void* stream);
 
 /* The same with test controls. `flags`: HK_KV8_FEW_ROWS (units of 16 query rows) or HK_KV8_MANY_ROWS (what is shared
- * in units of 256 rows on the tensor-core kernel; refused for what it does not take), 0: chosen by shape;
+ * in units of 128 rows on the tensor-core kernel; refused for what it does not take), 0: chosen by shape;
  * HK_KV8_FAULT_DROP_ARRIVE. `timeout_ns` bounds each wait (0: 1 s). */
 hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
                                      const int32_t* block_table, int64_t table_stride, int64_t max_pages,

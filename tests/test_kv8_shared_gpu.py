@@ -15,7 +15,7 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 
-FEW, MANY = 0x10, 0x20         # units of 16 rows, shared units of 256 rows
+FEW, MANY = 0x10, 0x20         # units of 16 rows, shared units of 128 rows
 FORMS = pytest.mark.parametrize("form", [FEW, MANY], ids=["few", "many"])
 
 
@@ -252,6 +252,9 @@ def test_pages_and_queries_of_very_different_size(form):
     q[1, 0, 3] *= 2.0 ** 20
     q[2, 0, 1] = 0
     _check(batch, q, _attend(batch, q, scale=2.0 ** -24, form=form), scale=2.0 ** -24, form=form)
+    batch = Batch([(1500, [40, 9, 100])], 2, 64, 32, scales=(2.0 ** 9, 2.0 ** 6, 2.0 ** 20, 2.0 ** -126))      # (bf16 ends at 2^127)
+    q = _q(batch.B, 1, 8, 64)
+    _check(batch, q, _attend(batch, q, scale=2.0 ** -26, form=form), scale=2.0 ** -26, form=form)
 
 
 @FORMS
