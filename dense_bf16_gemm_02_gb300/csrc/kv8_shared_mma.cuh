@@ -40,7 +40,7 @@ constexpr int kWideBlock = 128;        // tokens of a block
 constexpr int kWideThreads = 512;
 constexpr int kWideIssueWarp = 4, kWideLoadWarp = 5, kWideConvertWarp = 8;      // after four softmax warps; eight convert
 constexpr int kConvertThreads = 256;
-constexpr int kSoftmaxRegs = 200, kConvertRegs = 104, kIssueRegs = 104;
+constexpr int kSoftmaxRegs = 216, kConvertRegs = 96, kIssueRegs = 104;
 constexpr int kWideRegisters = 128 * kSoftmaxRegs + 256 * kConvertRegs + 128 * kIssueRegs;
 static_assert(kWideRegisters <= kWideThreads * 128, "registers of the launch");
 constexpr uint32_t kErrSoftmaxWait = 1u << 19;
@@ -121,8 +121,10 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 
 // Four codes to bf16 times `factor` / 2^120, in two words of two.
 __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t factor) {
-    const uint32_t h0 = __byte_perm(w, 0u, 0x1404), h1 = __byte_perm(w, 0u, 0x3424);     // each code in a high byte
-    const uint32_t a = (h0 & 0x80008000u) | (h0 >> 4 & 0x07F007F0u), b = (h1 & 0x80008000u) | (h1 >> 4 & 0x07F007F0u);
+    // each code in a low byte, four bits up (its exponent then ends at bit 10, where bf16's lowest four exponent bits do), and the
+    // sign from bit 11 to bit 15: x + 15 (x & 0x800). Half of it multiply-adds, which leaves the logic pipe free
+    const uint32_t l0 = __byte_perm(w, 0u, 0x4140) * 16u, l1 = __byte_perm(w, 0u, 0x4342) * 16u;
+    const uint32_t a = (l0 & 0x08000800u) * 15u + l0, b = (l1 & 0x08000800u) * 15u + l1;
     return make_uint2(mul_bf16x2(a, factor), mul_bf16x2(b, factor));
 }
 
@@ -257,14 +259,9 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
     walk.end = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(walk.at) + per));
     const int begin = walk.at;
     bool abort_seen = false;
-    // a warp's waits: lane 0 looks, all see
+    // a warp's waits
     auto wait_warp = [&](uint32_t b, uint32_t parity, uint32_t code, auto suspend) {
-        uint32_t ok = 0;
-        if (lane == 0) ok = wide_wait<decltype(suspend)::value>(p.wait, b, parity, code) ? 1u : 0u;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok) (void)mbar_test_wait(b, parity);
-        __syncwarp();
-        return ok != 0;
+        return __all_sync(0xffffffffu, wide_wait<decltype(suspend)::value>(p.wait, b, parity, code)) != 0;
     };
     constexpr std::integral_constant<bool, false> poll{};
     constexpr std::integral_constant<bool, true> suspend{};
@@ -281,18 +278,16 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
         constexpr int kPieces = kWideBlock * kTokenChunks / kConvertThreads;
         constexpr int kStepTokens = kConvertThreads / kTokenChunks;    // tokens between a thread's pieces
         const int ct = static_cast<int>(threadIdx.x) - kWideConvertWarp * 32;
-        const uint32_t chunk = ct % kTokenChunks, token = ct / kTokenChunks;
+        // eight threads whose 16-byte stores go together take 64 columns of two tokens, so that they meet no bank twice
+        constexpr int kHalves = kD / 64;
+        const uint32_t half = ct / 8 % kHalves, chunk = 4 * half + ct % 4, token = ct / (8 * kHalves) * 2 + ct / 4 % 2;
         int slot = 0, rs = 0;
         uint32_t ring_ph = 0, raw_ph = 0;
-        // 16 columns of row `tok`: two 16-byte units of the 64-column half that they lie in; the halves' threads (which meet the
-        // same banks) write them in opposite order
+        // 16 columns of row `tok`: two 16-byte units of the 64-column half that they lie in
         auto put = [&](uint32_t tok, const uint32_t (&o)[8]) {
-            const uint32_t row = slot_addr(slot) + (chunk >> 2) * W::kChunkBytes + tok * 128u;
-            const uint32_t unit = 2u * (chunk & 3u), sw = tok & 7u;
-            const bool flip = (chunk >> 2) != 0;
-            const uint32_t lo = row + ((unit ^ sw) << 4), hi = row + (((unit + 1u) ^ sw) << 4);
-            st_shared_v4(flip ? hi : lo, flip ? o[4] : o[0], flip ? o[5] : o[1], flip ? o[6] : o[2], flip ? o[7] : o[3]);
-            st_shared_v4(flip ? lo : hi, flip ? o[0] : o[4], flip ? o[1] : o[5], flip ? o[2] : o[6], flip ? o[3] : o[7]);
+            const uint32_t row = slot_addr(slot) + half * W::kChunkBytes + tok * 128u, unit = 2u * (chunk & 3u), sw = tok & 7u;
+            st_shared_v4(row + ((unit ^ sw) << 4), o[0], o[1], o[2], o[3]);
+            st_shared_v4(row + (((unit + 1u) ^ sw) << 4), o[4], o[5], o[6], o[7]);
         };
         for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next()) {
           const int n = w.last - w.first;
@@ -304,7 +299,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                 break;
             }
             if (is_k) {
-#pragma unroll 2
+#pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     const uint32_t tok = token + i * kStepTokens;
                     const uint4 x = ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk));
@@ -320,7 +315,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
             } else {
                 uint32_t second;
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(second) : "r"(factor_addr(rs) + 64u));
-#pragma unroll 2
+#pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     const uint32_t tok = token + i * kStepTokens;
                     const uint4 x = ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk));
