@@ -28,7 +28,7 @@ hk_status fail(hk_status s, const char* fmt, ...) {
 constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
 constexpr int kSms = 152;
 constexpr int64_t kMaxHeads = 65535;
-constexpr int kWarpsPerSm = 48;          // warps that a decoding step is spread over: registers allow some 48 to an SM
+constexpr int kWarpsPerSm = 24;          // warps that a call is spread over: as many as an SM holds
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -154,11 +154,12 @@ extern "C" hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], 
     for (int op = 0; op < 2; ++op) p.op_steps[op] = (p.heads[op] + 32 / lanes - 1) / (32 / lanes);
     const int64_t token_steps = int64_t(p.op_steps[0]) + p.op_steps[1];
     const int64_t steps = std::min<int64_t>(token_steps, std::max<int64_t>(1, B * T * token_steps / (int64_t(kSms) * kWarpsPerSm)));
-    p.shares = static_cast<int32_t>((token_steps + steps - 1) / steps);
-    p.steps = static_cast<int32_t>((token_steps + p.shares - 1) / p.shares);
-    p.shares = static_cast<int32_t>((token_steps + p.steps - 1) / p.steps);
-    p.warps = B * T * p.shares;
-    if (p.warps > kLimit * 8) return fail(HK_ERR_INVALID_ARG, "problem too large");
+    int64_t shares = (token_steps + steps - 1) / steps;
+    p.steps = static_cast<int32_t>((token_steps + shares - 1) / shares);
+    shares = (token_steps + p.steps - 1) / p.steps;
+    if (B * T > kLimit / shares) return fail(HK_ERR_INVALID_ARG, "problem too large");
+    p.shares = static_cast<uint32_t>(shares);
+    p.warps = static_cast<uint32_t>(B * T * shares);
     int device = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return fail(HK_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));

@@ -327,17 +327,21 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     if (p.wide_runs > 0) griddep_wait();
 }
 
-// Adds up what the kernel above left: grid (row of 16 · row_tiles, KV head, sequence) / 8 rows to a block, a warp to a row. A
-// row's parts are those of its shared unit, then those of its own: the maximum first, then the weighted sums, in order.
-template <int kD, typename T>
+// Adds up what the kernels above left: kSplit warps of a block to a row (eight where there are few rows, of many parts each),
+// of which each takes every kSplit-th part. A row's parts are those of its shared unit, then those of its own: the maximum over
+// all of them first, then the weighted sums, joined through shared memory in order.
+template <int kD, typename T, int kSplit>
 __global__ void __launch_bounds__(256)
 kv8_shared_combine_kernel(const SharedParams p) {
     constexpr int kVec = kD / 32;            // floats of a lane
     constexpr int kBatch = 4;                // parts whose loads are in flight at a time
+    __shared__ float joined[8][kD + 1];
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t out_row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int warp = static_cast<int>(threadIdx.x >> 5), share = warp % kSplit;
+    const int64_t out_row = static_cast<int64_t>(blockIdx.x) * (8 / kSplit) + warp / kSplit;
     const int lane = static_cast<int>(lane_id());
+    // (with several warps to a row a block has one row or whole rows: they leave together)
     if (out_row >= static_cast<int64_t>(p.n) * p.T * p.Hq) return;
     const int head = static_cast<int>(out_row % p.Hq), t = static_cast<int>(out_row / p.Hq % p.T);
     const int i = static_cast<int>(out_row / p.Hq / p.T), h = head / p.group;
@@ -372,11 +376,11 @@ kv8_shared_combine_kernel(const SharedParams p) {
     for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(p.part_ml + 2 * row_of(k)));
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    for (int k0 = 0; k0 < parts; k0 += kBatch) {
+    for (int k0 = share; k0 < parts; k0 += kBatch * kSplit) {
         float pm[kBatch], pl[kBatch], x[kBatch][kVec];
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int64_t a = row_of(min(k0 + q, parts - 1));
+            const int64_t a = row_of(min(k0 + q * kSplit, parts - 1));
             const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
             pm[q] = ml.x;
             pl[q] = ml.y;
@@ -390,11 +394,24 @@ kv8_shared_combine_kernel(const SharedParams p) {
         }
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const bool counts = k0 + q < parts;
+            const bool counts = k0 + q * kSplit < parts;
             const float weight = !counts || pm[q] == -INFINITY ? 0.0f : ex2_approx(pm[q] - m);
             l += !counts ? 0.0f : pm[q] == -INFINITY ? pl[q] : pl[q] * weight;       // (a NaN sum stays one)
 #pragma unroll
             for (int k = 0; k < kVec; ++k) acc[k] += x[q][k] * weight;
+        }
+    }
+    if constexpr (kSplit > 1) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) joined[warp][lane * kVec + k] = acc[k];
+        if (lane == 0) joined[warp][kD] = l;
+        named_barrier_sync(1 + warp / kSplit, 32 * kSplit);
+        if (share != 0) return;
+#pragma unroll
+        for (int w = 1; w < kSplit; ++w) {
+            l += joined[warp + w][kD];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) acc[k] += joined[warp + w][lane * kVec + k];
         }
     }
     const bool any = t < seq.w && (l > 0.0f || l != l);      // (a row past the queries has stacked sums of what lies there)

@@ -6,8 +6,8 @@
 // over the pairs (a, b) = (y_i, y_{i + R/2}) or (y_{2i}, y_{2i+1}) of the first R of D elements.
 //
 // Every element is read once and written once: what bounds it is memory. A row
-// (one head of one token) is 8 elements each of 8, 16 or 32 lanes, so that a
-// warp's load is whole lines; a warp keeps to one token and takes `steps` times
+// (one head of one token) is 8 elements each of 8, 16 or 32 lanes, four of each half of
+// the pairs, so that a pair is one lane's and a warp's load is whole lines; a warp keeps to one token and takes `steps` times
 // 32 / lanes rows of its queries or keys, so that the angles are worked out once for all of them:
 // as few as leave every SM full of warps (a decoding step), up to all heads (a
 // prompt).
@@ -22,6 +22,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "elements.cuh"
 #include "ptx.cuh"
@@ -44,8 +45,8 @@ struct RopeParams {
     int32_t B, T, heads[2];        // heads of queries and keys
     int32_t D, half;               // R / 2
     int32_t op_steps[2];           // row steps of a token's queries, of its keys
-    int32_t steps, shares;         // row steps of a warp; warps of a token
-    int64_t warps;
+    int32_t steps;                 // row steps of a warp
+    uint32_t shares, warps;        // warps of a token, of all
     float eps;
     int32_t norm, weight_f32;
 };
@@ -77,177 +78,185 @@ __device__ __forceinline__ void angle(const RopeParams& p, int pair, int64_t at,
     if (!isfinite(f)) c = s = NAN;
 }
 
+// Four consecutive elements of bf16, fp16 or fp32.
 template <typename T>
-__device__ __forceinline__ void weights8(const RopeParams& p, int op, int d, float (&w)[8]) {
-    if (p.weight[op] == nullptr) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = 1.0f;
-    } else if (p.weight_f32) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = static_cast<const float*>(p.weight[op])[d + k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = to_float(static_cast<const T*>(p.weight[op])[d + k]);
-    }
-}
+struct Raw4 {
+    uint32_t w[sizeof(T)];
+};
 
-// Eight elements of a row. kVec: 16 bytes at a time. No test around a load: the next one would wait for it.
+// kVec: in one access. No test around a load: the next one would wait for it.
 template <typename T, bool kVec>
-__device__ __forceinline__ Raw8<T> row8(const T* src) {
-    Raw8<T> r;
-    if constexpr (kVec) {
+__device__ __forceinline__ Raw4<T> load4(const T* src) {
+    Raw4<T> r;
+    if constexpr (!kVec) {
+        T e[4];
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4*>(src)[i];
-    } else {
-        T e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = src[i];
+        for (int i = 0; i < 4; ++i) e[i] = src[i];
         memcpy(&r, e, sizeof r);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(src);
+        r.w[0] = x.x; r.w[1] = x.y;
+    } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(src);
+        r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
     }
     return r;
 }
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void store8(T* dst, const float (&v)[8]) {
+__device__ __forceinline__ void store4(T* dst, const float (&v)[4]) {
     if constexpr (!kVec) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dst[k] = from_float<T>(v[k]);
+        for (int k = 0; k < 4; ++k) dst[k] = from_float<T>(v[k]);
     } else if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(dst) =
-            make_uint4(pack_pair<T>(v[0], v[1]), pack_pair<T>(v[2], v[3]), pack_pair<T>(v[4], v[5]), pack_pair<T>(v[6], v[7]));
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_pair<T>(v[0], v[1]), pack_pair<T>(v[2], v[3]));
     } else {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
     }
 }
 
-// The words of eight elements that another lane holds.
+// As two pairs.
 template <typename T>
-__device__ __forceinline__ Raw8<T> shuffle8(const Raw8<T>& r, int from) {
-    Raw8<T> o;
+__device__ __forceinline__ void pairs_of(const Raw4<T>& r, uint64_t (&v)[2]) {
+    T e[4];
+    memcpy(e, &r, sizeof r);
+    v[0] = f32x2(to_float(e[0]), to_float(e[1]));
+    v[1] = f32x2(to_float(e[2]), to_float(e[3]));
+}
+
+template <typename T>
+__device__ __forceinline__ void weights4(const RopeParams& p, int op, int e, float* w) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-        o.w[i] = make_uint4(__shfl_sync(0xffffffffu, r.w[i].x, from), __shfl_sync(0xffffffffu, r.w[i].y, from),
-                            __shfl_sync(0xffffffffu, r.w[i].z, from), __shfl_sync(0xffffffffu, r.w[i].w, from));
-    return o;
+    for (int k = 0; k < 4; ++k)
+        w[k] = p.weight[op] == nullptr ? 1.0f
+               : p.weight_f32          ? static_cast<const float*>(p.weight[op])[e + k]
+                                       : to_float(static_cast<const T*>(p.weight[op])[e + k]);
+}
+
+__device__ __forceinline__ uint64_t swap_pair(uint64_t x) {
+    float lo, hi;
+    f32x2_split(x, lo, hi);
+    return f32x2(hi, lo);
 }
 
 template <typename T, int kLanes, bool kInterleaved, bool kVec>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(256, 3)
 qk_norm_rope_kernel(const RopeParams p) {
     constexpr int kRowsStep = 32 / kLanes;           // rows of a warp at a time
+    constexpr int kFlight = sizeof(T) == 2 ? 4 : 2;  // steps whose loads are in flight together
     griddep_launch_dependents();
     griddep_wait();                  // launched early behind the kernel that may have written the queries and keys
-    const int64_t warp = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const uint32_t warp = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (warp >= p.warps) return;
-    const int64_t token = warp / p.shares;
+    const uint32_t token = warp / p.shares;
     const int share = static_cast<int>(warp - token * p.shares);
-    const int64_t b = token / p.T, t = token - b * p.T;
+    const int64_t b = token / static_cast<uint32_t>(p.T), t = token - static_cast<uint32_t>(b) * p.T;
     const int lane = static_cast<int>(lane_id());
-    const int sub = lane % kLanes, d = 8 * sub;
-    const bool live = d < p.D;
-
-    // cos and sin of this lane's elements: of its 4 pairs (interleaved), or of the 8 pairs that it is one half of, four
-    // of them worked out here and four by the lane that holds the other half
-    constexpr int kAngles = kInterleaved ? 4 : 8;
-    float c[kAngles], s[kAngles];
-    const int64_t at = b * p.pos_b + t * p.pos_t;
-    const bool turns = d < 2 * p.half;
-    const bool second = !kInterleaved && d >= p.half;
-    const int partner = kInterleaved || !turns ? lane : second ? lane - p.half / 8 : lane + p.half / 8;
-    {
-        const int pair0 = !turns ? 0 : kInterleaved ? d / 2 : second ? d - p.half : d;
-        float mc[4], ms[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            mc[k] = 1.0f;
-            ms[k] = 0.0f;
-            if (turns) angle(p, pair0 + (second ? 4 : 0) + k, at, mc[k], ms[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if constexpr (kInterleaved) {
-                c[k] = mc[k];
-                s[k] = ms[k];
-            } else {
-                const float oc = __shfl_sync(0xffffffffu, mc[k], partner), os = __shfl_sync(0xffffffffu, ms[k], partner);
-                c[k] = second ? oc : mc[k];
-                c[4 + k] = second ? mc[k] : oc;
-                s[k] = second ? os : -ms[k];                 // (the first half's sin with its sign)
-                s[4 + k] = second ? ms[k] : -os;
-            }
-        }
-    }
-    const float inv_d = 1.0f / static_cast<float>(p.D);
-    constexpr int kFlight = sizeof(T) == 2 ? 4 : 2;  // steps whose loads are in flight together
+    const int sub = lane % kLanes, my_row = lane / kLanes;
+    // This lane's elements: four from e0 and four from e1 on. Those of both halves of four pairs (or four whole pairs), for the
+    // pairs that turn; then what does not turn, eight in a row.
+    const int turning = p.half / 4;                  // lanes that turn pairs
+    const bool turns = sub < turning, live = 8 * sub < p.D;
+    const int e0 = !live ? 0 : kInterleaved || !turns ? 8 * sub : 4 * sub;
+    const int e1 = !live ? 0 : kInterleaved || !turns ? 8 * sub + 4 : 4 * sub + p.half;
     // steps [first, last) of the token's: its queries', then its keys'
     int first = share * p.steps;
     const int last = min(p.op_steps[0] + p.op_steps[1], first + p.steps);
+
+    float c[4], s[4];                // cos and sin of the four pairs
+    {
+        const int64_t at = b * p.pos_b + t * p.pos_t;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            c[k] = 1.0f;
+            s[k] = 0.0f;
+            if (turns) angle(p, 4 * sub + k, at, c[k], s[k]);
+        }
+    }
+    const float inv_d = 1.0f / static_cast<float>(p.D);
     while (first < last) {
         const int op = first >= p.op_steps[0];
         const int base = op ? p.op_steps[0] : 0, end = min(last, op ? last : p.op_steps[0]);
         // an output is (x a + o b) / root: x the element, o the one that it is turned with, a and b weight times cos and sin
-        uint64_t a2[4], b2[4];
+        uint64_t a2[4], b2[4];       // of e0's two pairs of elements, of e1's
         {
             float w[8];
-            weights8<T>(p, op, live ? d : 0, w);
+            weights4<T>(p, op, e0, w);
+            weights4<T>(p, op, e1, w + 4);
+            if constexpr (kInterleaved) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (kInterleaved) {
+                for (int k = 0; k < 4; ++k) {
                     a2[k] = f32x2(w[2 * k] * c[k], w[2 * k + 1] * c[k]);
                     b2[k] = f32x2(-w[2 * k + 1] * s[k], w[2 * k] * s[k]);
-                } else {
-                    a2[k] = f32x2(w[2 * k] * c[2 * k], w[2 * k + 1] * c[2 * k + 1]);
-                    const float o0 = __shfl_sync(0xffffffffu, w[2 * k], partner), o1 = __shfl_sync(0xffffffffu, w[2 * k + 1], partner);
-                    b2[k] = f32x2(o0 * s[2 * k], o1 * s[2 * k + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = 2 * k, j = 2 * k + 1;
+                    a2[k] = f32x2(w[i] * c[i], w[j] * c[j]);
+                    a2[2 + k] = f32x2(w[4 + i] * c[i], w[4 + j] * c[j]);
+                    b2[k] = f32x2(-w[4 + i] * s[i], -w[4 + j] * s[j]);
+                    b2[2 + k] = f32x2(w[i] * s[i], w[j] * s[j]);
                 }
             }
         }
-        const T* const src = static_cast<const T*>(p.in[op]) + b * p.in_b[op] + t * p.in_t[op] + (live ? d : 0);
-        T* const dst = static_cast<T*>(p.out[op]) + b * p.out_b[op] + t * p.out_t[op] + d;
-        const int64_t in_h = p.in_h[op], out_h = p.out_h[op];
         const int heads = p.heads[op];
-        for (int s0 = first; s0 < end; s0 += kFlight) {
-            const int r0 = (s0 - base) * kRowsStep + lane / kLanes;
-            Raw8<T> raw[kFlight];
+        const int64_t in_step = kRowsStep * p.in_h[op], out_step = kRowsStep * p.out_h[op];
+        int row = (first - base) * kRowsStep + my_row;
+        const T* const rows = static_cast<const T*>(p.in[op]) + b * p.in_b[op] + t * p.in_t[op];
+        const T* src = rows + row * p.in_h[op];          // (not read where it is none of the rows)
+        T* dst = static_cast<T*>(p.out[op]) + b * p.out_b[op] + t * p.out_t[op] + row * p.out_h[op];
+        // kFlight steps from s0 on; `whole`: all of them are there, and their rows
+        auto steps = [&](int s0, auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
+            Raw4<T> raw[kFlight][2];
+            const T* at = kWhole ? src : rows + min(row, heads - 1) * p.in_h[op];
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i)    // (past the end the last row is taken again and not stored)
-                raw[i] = row8<T, kVec>(src + min(r0 + min(i, end - 1 - s0) * kRowsStep, heads - 1) * in_h);
+            for (int i = 0; i < kFlight; ++i) {      // (past the end a row is taken again and not stored)
+                raw[i][0] = load4<T, kVec>(at + e0);
+                raw[i][1] = load4<T, kVec>(at + e1);
+                if (kWhole || row + (i + 1) * kRowsStep < heads) at += in_step;
+            }
+            src += kFlight * in_step;
 #pragma unroll
             for (int i = 0; i < kFlight; ++i) {
-                if (s0 + i >= end) break;
-                const int r = r0 + i * kRowsStep;
-                float y[8], o[8];
-                widen8<T>(raw[i], y);
-                uint64_t y2[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y2[k] = f32x2(y[2 * k], y[2 * k + 1]);
-                float mul = 1.0f;
+                if (!kWhole && s0 + i >= end) break;
+                uint64_t y[4];
+                pairs_of<T>(raw[i][0], *reinterpret_cast<uint64_t(*)[2]>(&y[0]));
+                pairs_of<T>(raw[i][1], *reinterpret_cast<uint64_t(*)[2]>(&y[2]));
+                uint64_t mul2 = f32x2(1.0f, 1.0f);
                 if (p.norm) {
-                    const uint64_t q = ffma2(y2[3], y2[3], ffma2(y2[2], y2[2], ffma2(y2[1], y2[1], fmul2(y2[0], y2[0]))));
+                    const uint64_t q = ffma2(y[3], y[3], ffma2(y[2], y[2], ffma2(y[1], y[1], fmul2(y[0], y[0]))));
                     float lo, hi;
                     f32x2_split(q, lo, hi);
                     float sum = live ? lo + hi : 0.0f;
 #pragma unroll
                     for (int m = kLanes / 2; m > 0; m /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                    mul = rsqrtf(fmaf(sum, inv_d, p.eps));
+                    const float mul = rsqrtf(fmaf(sum, inv_d, p.eps));
+                    mul2 = f32x2(mul, mul);
                 }
-                if constexpr (kInterleaved) {
+                uint64_t z[4];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = y[k ^ 1];
-                } else {
-                    widen8<T>(shuffle8<T>(raw[i], partner), o);
-                }
-                float z[8];
-                const uint64_t mul2 = f32x2(mul, mul);
+                for (int k = 0; k < 4; ++k) z[k] = fmul2(y[k], a2[k]);
+                if (turns) {                     // (not plus 0 times an infinity)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t x = fmul2(y2[k], a2[k]), turned = ffma2(f32x2(o[2 * k], o[2 * k + 1]), b2[k], x);
-                    f32x2_split(fmul2(turns ? turned : x, mul2), z[2 * k], z[2 * k + 1]);      // (not plus 0 times an infinity)
+                    for (int k = 0; k < 4; ++k) z[k] = ffma2(kInterleaved ? swap_pair(y[k]) : y[k ^ 2], b2[k], z[k]);
                 }
-                if (r < heads && live) store8<T, kVec>(dst + r * out_h, z);
+                float out[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f32x2_split(fmul2(z[k], mul2), out[2 * k], out[2 * k + 1]);
+                if (live && (kWhole || row < heads)) {
+                    store4<T, kVec>(dst + e0, *reinterpret_cast<const float(*)[4]>(&out[0]));
+                    store4<T, kVec>(dst + e1, *reinterpret_cast<const float(*)[4]>(&out[4]));
+                }
+                row += kRowsStep;
+                dst += out_step;
             }
-        }
+        };
+        const int whole = base + heads / kRowsStep;      // steps up to there have all their rows
+        int s0 = first;
+        for (; s0 + kFlight <= min(end, whole); s0 += kFlight) steps(s0, std::integral_constant<bool, true>{});
+        for (; s0 < end; s0 += kFlight) steps(s0, std::integral_constant<bool, false>{});
         first = end;
     }
 }

@@ -7,6 +7,10 @@ the attention that reads shared pages once (``attention_kv8_shared``).
 As in ``low_precision``, this is argument marshalling: every step runs in the CUDA
 library, on ``stream`` (default: torch's current stream), nothing is read back, and
 the tensors are on torch's current device.
+
+As there, the way through Python is kept short, since a decoding step's calls are a few
+microseconds of GPU time each: sizes and strides are taken once, small numbers go to the
+library as packed bytes, what a pool's calls need is worked out once per pool.
 """
 from __future__ import annotations
 
@@ -21,6 +25,8 @@ from .low_precision import (Kv8Cache, _check_vector, _empty, _f32, _i32, _read_o
                             _tokens_shape, _type_code, _u8)
 
 _pool_struct = struct.Struct("PPPqq4i").pack       # hk_kv8_pool
+_int32s = [struct.Struct(f"{n}i").pack for n in range(5)]
+_Tensor = torch.Tensor
 
 
 class Kv8Pool:
@@ -32,7 +38,7 @@ class Kv8Pool:
     CUDA tensors; ``Kv8Pool.empty`` makes them, with nothing held. None of them can be
     set to another tensor."""
 
-    __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref")
+    __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref", "_scratch")
     refs, table, held = (_read_only(n) for n in __slots__[:3])
     pages, rows, max_pages, page_size = (_read_only(n) for n in __slots__[3:7])
 
@@ -49,6 +55,7 @@ class Kv8Pool:
             raise ValueError("refs and held must be contiguous")
         self._refs, self._table, self._held = refs, table, held
         self._pages, self._rows, self._max_pages, self._page_size = refs.size(0), rows, max_pages, page_size
+        self._scratch = 0                    # bytes of an arrangement's workspace, once known
         self._ref = _pool_struct(refs.data_ptr(), table.data_ptr(), held.data_ptr(), refs.size(0), _row_stride(table, "table"),
                                  rows, max_pages, page_size, 0)
 
@@ -65,9 +72,9 @@ def _check_pool(pool):
 
 
 def _cache_refs(caches, name):
-    """The caches' structures side by side, as the entry points take them."""
+    """The caches' structures side by side, as the entry points take them, and their number."""
     if isinstance(caches, Kv8Cache):
-        caches = (caches,)
+        return caches._ref, 1
     refs = []
     for c in caches:
         if not isinstance(c, Kv8Cache):
@@ -89,19 +96,23 @@ def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=
     one. ``copies``: an int32 tensor [2, rows] that receives the copied pages and their
     copies (-1: none). See hk_kv8_arrange."""
     _check_pool(pool)
+    rows = pool._rows
+    _check_vector(keep, "keep", rows)
     if room is None:
         room = keep
-    _check_vector(keep, "keep", pool._rows)
-    _check_vector(room, "room", pool._rows)
+    else:
+        _check_vector(room, "room", rows)
     if parents is not None:
-        _check_vector(parents, "parents", pool._rows)
-    if copies is not None and (not isinstance(copies, torch.Tensor) or copies.dtype != _i32 or not copies.is_cuda
-                               or tuple(copies.shape) != (2, pool._rows) or not copies.is_contiguous()):
+        _check_vector(parents, "parents", rows)
+    if copies is not None and (not isinstance(copies, _Tensor) or copies.dtype != _i32 or not copies.is_cuda
+                               or tuple(copies.shape) != (2, rows) or not copies.is_contiguous()):
         raise TypeError("copies must be a contiguous int32 CUDA tensor [2, rows]")
-    refs, n = _cache_refs(caches, "caches")
+    refs, n = _cache_refs(caches, "caches") if caches else (None, 0)
     lib = _hk.load()
-    size = lib.hk_kv8_arrange_workspace_size(pool._ref)
-    workspace = _empty(max(size, 1), _u8, keep, stream)
+    size = pool._scratch
+    if not size:
+        size = pool._scratch = lib.hk_kv8_arrange_workspace_size(pool._ref)
+    workspace = _empty((size,), _u8, keep, stream)
     missing = _empty((), _i32, keep, stream)
     st = lib.hk_kv8_arrange(pool._ref, keep.data_ptr(), room.data_ptr(), None if parents is None else parents.data_ptr(), refs, n,
                             None if copies is None else copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(), size,
@@ -145,15 +156,23 @@ def kv8_copy_pages(dst, src, dst_pages, src_pages, stream=None) -> None:
         raise HKError(st, "hk_kv8_copy_pages")
 
 
-def _heads(t, name, like):
-    """(B, T, heads, head_dim) and packed strides."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+def _heads(t, name):
+    """Sizes and packed strides of [B, T, heads, head_dim]."""
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dim() != 4:
         raise TypeError(f"{name} must be a CUDA tensor [B, T, heads, head_dim]")
-    if t.stride(3) != 1 and t.size(3) > 1:
+    sb, st, sh, sd = t.stride()
+    shape = t.shape
+    if sd != 1 and shape[3] > 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
-    if like is not None and (t.dtype != like.dtype or t.shape[:2] != like.shape[:2] or t.shape[3] != like.shape[3]):
-        raise ValueError(f"{name} must have q's type, batch, tokens and head dimension")
-    return _strides(*t.stride()[:3])
+    return shape, _strides(sb, st, sh)
+
+
+def _rope_weight(w, name, dtype, D):
+    if not isinstance(w, _Tensor) or not w.is_cuda or w.dim() != 1 or w.size(0) != D or not w.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA tensor [{D}]")
+    if w.dtype != dtype and w.dtype != _f32:
+        raise TypeError(f"{name} must be of q's type or float32")
+    return w.data_ptr()
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, sections=None, interleaved=False, out=None,
@@ -167,49 +186,56 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     pairs that turn by each axis. ``inv_freq`` float32 [R/2]. Weights [D] of q's type or
     float32, both alike; None: 1. eps None: no norm. ``out``: (q', k') to write into, q and k
     themselves among others. Returns (q', k'). See hk_qk_norm_rope."""
-    qs, ks = _heads(q, "q", None), _heads(k, "k", q)
+    (B, T, Hq, D), qs = _heads(q, "q")
+    (kB, kT, Hk, kD), ks = _heads(k, "k")
+    dtype = q.dtype
     code = _type_code(q, "q")
-    B, T, Hq, D = q.shape
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != _f32 or not inv_freq.is_cuda or inv_freq.dim() != 1 \
+    if kB != B or kT != T or kD != D or k.dtype != dtype:
+        raise ValueError("k must have q's type, batch, tokens and head dimension")
+    if not isinstance(inv_freq, _Tensor) or inv_freq.dtype != _f32 or not inv_freq.is_cuda or inv_freq.dim() != 1 \
             or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous 1-D float32 CUDA tensor")
-    if not isinstance(positions, torch.Tensor) or positions.dtype != _i32 or not positions.is_cuda or positions.dim() not in (2, 3):
+    if not isinstance(positions, _Tensor) or positions.dtype != _i32 or not positions.is_cuda:
         raise TypeError("positions must be an int32 CUDA tensor [B, T] or [axes, B, T]")
-    if positions.shape[-2:] != q.shape[:2]:
-        raise ValueError(f"positions {tuple(positions.shape)} for {B} sequences of {T} tokens")
-    axes = positions.size(0) if positions.dim() == 3 else 1
+    shape, pos = positions.shape, positions.stride()
+    if len(shape) == 2:
+        axes, pos = 1, (0, *pos)
+    elif len(shape) == 3:
+        axes = shape[0]
+    else:
+        raise TypeError("positions must be an int32 CUDA tensor [B, T] or [axes, B, T]")
+    if shape[-1] != T or shape[-2] != B:
+        raise ValueError(f"positions {tuple(shape)} for {B} sequences of {T} tokens")
     if sections is not None:
-        if len(sections) != axes:
-            raise ValueError(f"{len(sections)} sections for {axes} position axes")
-        sections = (ctypes.c_int32 * axes)(*sections)
+        if len(sections) != axes or axes >= len(_int32s):
+            raise ValueError(f"{len(sections)} sections for {axes} position axes (at most 4)")
+        sections = _int32s[axes](*sections)
     weight_code = code
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is None:
-            continue
-        if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dim() != 1 or w.size(0) != D or not w.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous CUDA tensor [{D}]")
-        if w.dtype not in (q.dtype, _f32):
-            raise TypeError(f"{name} must be of q's type or float32")
-        weight_code = _type_code(w, name)
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TypeError("q_weight and k_weight must be of one type")
+    qw = kw = None
+    if q_weight is not None:
+        qw = _rope_weight(q_weight, "q_weight", dtype, D)
+        weight_code = _type_code(q_weight, "q_weight")
+    if k_weight is not None:
+        kw = _rope_weight(k_weight, "k_weight", dtype, D)
+        if q_weight is not None and k_weight.dtype != q_weight.dtype:
+            raise TypeError("q_weight and k_weight must be of one type")
+        weight_code = _type_code(k_weight, "k_weight")
     if eps is None:
         eps = -1.0
     elif eps < 0:
         raise ValueError("eps must not be negative (None: no norm)")
     if out is None:
-        qo, ko = _empty(q.shape, q.dtype, q, stream), _empty(k.shape, k.dtype, k, stream)
+        qo, ko = _empty((B, T, Hq, D), dtype, q, stream), _empty((B, T, Hk, D), dtype, q, stream)
+        row = Hq * D, Hk * D
+        qos, kos = _strides(T * row[0], row[0], D), _strides(T * row[1], row[1], D)
     else:
         qo, ko = out
-    qos, kos = _heads(qo, "out", q), _heads(ko, "out", q)
-    if qo.shape != q.shape or ko.shape != k.shape:
-        raise ValueError("out must have q's and k's shapes")
-    pos = positions.stride() if axes > 1 or positions.dim() == 3 else (0, *positions.stride())
-    st = _hk.load().hk_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, qo.data_ptr(), qos, ko.data_ptr(), kos, code, B, T, Hq,
-                                    k.size(2), D, None if q_weight is None else q_weight.data_ptr(),
-                                    None if k_weight is None else k_weight.data_ptr(), weight_code, eps, positions.data_ptr(),
-                                    _strides(*pos), sections, axes, inv_freq.data_ptr(), inv_freq.size(0), 1 if interleaved else 0,
-                                    _stream(stream, q))
+        (qshape, qos), (kshape, kos) = _heads(qo, "out"), _heads(ko, "out")
+        if qshape != q.shape or kshape != k.shape or qo.dtype != dtype or ko.dtype != dtype:
+            raise ValueError("out must have q's and k's shapes and type")
+    st = _hk.load().hk_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, qo.data_ptr(), qos, ko.data_ptr(), kos, code, B, T, Hq, Hk, D,
+                                    qw, kw, weight_code, eps, positions.data_ptr(), _strides(*pos), sections, axes,
+                                    inv_freq.data_ptr(), inv_freq.size(0), 1 if interleaved else 0, _stream(stream, q))
     if st != HK_OK:
         raise HKError(st, "hk_qk_norm_rope")
     return qo, ko
