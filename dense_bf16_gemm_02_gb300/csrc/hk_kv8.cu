@@ -133,13 +133,6 @@ int pack_shift_of(int64_t group) {
 // first load, sums go through memory: some 10) stays the same.
 constexpr int kBlockTiles = 32;
 
-// Warps of a block that has a unit to itself: as many as let one round of blocks hold all units.
-int block_warps(int64_t units) {
-    int warps = kBlockWarps;
-    while (warps > 1 && units > int64_t(kSms) * (kBlockWarps / warps)) warps /= 2;
-    return warps;
-}
-
 // Sequences that are brought to bf16 at a time: as many as fit 512 MB, one at least.
 constexpr int64_t kWidenBytes = int64_t(512) << 20;
 
@@ -416,7 +409,7 @@ bool attention_shape_ok(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq,
 size_t few_rows_bytes(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages) {
     const int64_t row_tiles = ceil_div(T * (Hq / c->heads), kRows);
     const int64_t units = decode_batch(B, c->heads, row_tiles) * c->heads * row_tiles;
-    if (ceil_div(max_pages * c->page_size, kTileKeys) <= block_warps(units) * kBlockTiles) return 0;
+    if (ceil_div(max_pages * c->page_size, kTileKeys) <= block_warps(units, kBlockWarps) * kBlockTiles) return 0;
     return decode_workspace(c, B, T, Hq).total;
 }
 
@@ -540,7 +533,7 @@ extern "C" hk_status hk_attention_kv8_ex(const void* Q, int32_t type, const int6
     if (units > kLimit) return fail(HK_ERR_INVALID_ARG, "problem too large");
     const int64_t unit_room = ceil_div(max_pages * p.page_size, kTileKeys);
     DecodePlan plan = {0, 1, static_cast<int>(std::min<int64_t>(2 * std::min(sms, kSms), ceil_div(units * unit_room, kDecodeWarps)))};
-    const int warps = block_warps(units);
+    const int warps = block_warps(units, kBlockWarps);
     // a cluster of blocks where one block to a unit leaves SMs idle, as long as its warps have half a tile each (8
     // units: 12 blocks, 32768 tokens 24.5 us; 8 blocks 30)
     if (warps == kBlockWarps)

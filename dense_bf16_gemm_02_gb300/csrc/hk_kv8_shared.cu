@@ -23,6 +23,12 @@ using namespace hk_kv8;
 std::mutex g_setup_mutex;
 bool g_setup[kMaxDevices] = {};
 
+template <int kD, int kWarps>
+cudaError_t setup_own() {
+    return cudaFuncSetAttribute(kv8_own_kernel<kD, __nv_bfloat16, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                BlockGeometry<kD, kWarps>::kSmemBytes);
+}
+
 template <int kD, typename T>
 cudaError_t setup_one() {
     return cudaFuncSetAttribute(kv8_shared_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SharedGeometry<kD>::kSmemBytes);
@@ -34,6 +40,10 @@ cudaError_t setup_wide() {
     cudaFuncAttributes a;
     cudaError_t e = cudaFuncGetAttributes(&a, kv8_shared_mma_kernel<kD>);
     if (e == cudaSuccess && a.numRegs * kWideThreads < kWideRegisters) e = cudaErrorLaunchOutOfResources;
+    if (e == cudaSuccess) e = setup_own<kD, 1>();
+    if (e == cudaSuccess) e = setup_own<kD, 2>();
+    if (e == cudaSuccess) e = setup_own<kD, 4>();
+    if (e == cudaSuccess) e = setup_own<kD, 8>();
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kv8_shared_mma_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideGeometry<kD>::kSmemBytes);
     return e;
@@ -56,6 +66,9 @@ hk_status setup(int device) {
 // Query rows per sequence and KV head from which a sequence fills the tensor-core kernel's tiles by itself: reading a
 // prefix once for several sequences saves nothing there, and the call is attention_kv8's.
 constexpr int64_t kOwnTileRows = 256;
+
+// Tiles per warp up to which a sequence's own unit is a block's, beside the tensor-core kernel (beyond, it is spread over the GPU).
+constexpr int kOwnTiles = 32;
 
 // Sequences of one launch: what the kernel plans for, and as many as keep the sums of whole units at 2^17 rows (two of
 // 64 MB at head dimension 128).
@@ -107,13 +120,34 @@ bool shape_ok(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t m
 
 bool on_its_own(const hk_kv8_cache* c, int64_t T, int64_t Hq) { return T * (Hq / c->heads) >= kOwnTileRows; }
 
+template <int kD, int kWarps>
+cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p, cudaStream_t st) {
+    return launch_early(&kv8_own_kernel<kD, __nv_bfloat16, kWarps>, dim3(static_cast<unsigned>(int64_t(p.n) * p.Hkv * p.row_tiles)),
+                        dim3(32 * kWarps), BlockGeometry<kD, kWarps>::kSmemBytes, st, tk, tv, p);
+}
+
+// The shared units on the tensor cores (a run of blocks to every SM), then the sequences' own ones.
+template <int kD>
+cudaError_t launch_wide(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
+                        SharedParams& p, cudaStream_t st) {
+    const int warps = block_warps(int64_t(p.n) * p.Hkv * p.row_tiles, kBlockWarps);
+    p.own_limit = warps * kOwnTiles;
+    const cudaError_t e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads),
+                                       WideGeometry<kD>::kSmemBytes, st, wide_k, wide_v, p);
+    if (e != cudaSuccess) return e;
+    switch (warps) {
+        case 1: return launch_own<kD, 1>(tk, tv, p, st);
+        case 2: return launch_own<kD, 2>(tk, tv, p, st);
+        case 4: return launch_own<kD, 4>(tk, tv, p, st);
+        default: return launch_own<kD, 8>(tk, tv, p, st);
+    }
+}
+
 template <int kD, typename T>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
-                   const SharedParams& p, cudaStream_t st) {
+                   SharedParams p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.wide_runs > 0)
-        e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads), WideGeometry<kD>::kSmemBytes, st,
-                         wide_k, wide_v, p);
+    if (p.wide_runs > 0) e = launch_wide<kD>(tk, tv, wide_k, wide_v, p, st);
     if (e != cudaSuccess) return e;
     e = launch_early(&kv8_shared_kernel<kD, T>, dim3(static_cast<unsigned>(p.warps / kDecodeWarps)), dim3(32 * kDecodeWarps),
                                  SharedGeometry<kD>::kSmemBytes, st, tk, tv, p);

@@ -117,4 +117,12 @@ inline bool rows_aligned(const void* ptr, const int64_t strides[3]) {
     return aligned(ptr, 16) && strides[0] % 8 == 0 && strides[1] % 8 == 0 && strides[2] % 8 == 0;
 }
 
+// Warps of a block that has a unit to itself, of at most `most`, which fill an SM: as many as let one round of blocks hold all
+// units.
+inline int block_warps(int64_t units, int most) {
+    int warps = most;
+    while (warps > 1 && units > int64_t(kSms) * (most / warps)) warps /= 2;
+    return warps;
+}
+
 }  // namespace hk_kv8

@@ -17,7 +17,10 @@
 // Both kinds of units run as in kv8_decode.cuh: tiles of 32 tokens of all units in
 // one order, cut into equal runs, one per warp, whatever the lengths are; sums of units that
 // are split, and of sequences with a shared part, go through memory and are added up by a second
-// kernel, in order. Without a shared part a whole unit is finished at once.
+// kernel, in order. Without a shared part a whole unit is finished at once. Where the shared units
+// run on the tensor-core kernel (kv8_shared_mma.cuh), what sequences have of their own is
+// mostly short, and a block to a unit is quicker: no plan over all lengths before the first load, and
+// the unit's warps load at the same time; only units of more than `own_limit` tiles are spread.
 #pragma once
 
 #include "kv8_decode.cuh"
@@ -48,6 +51,7 @@ struct SharedParams : DecodeParams {
     int64_t whole[2];              // rows of part_o and part_ml where the sums of whole units begin: shared, own
     int4* shared_info;             // as info, of the units of the groups: [KV head][shared_units]
     int32_t shared_units;
+    int32_t own_limit;             // a sequence's own units of up to so many tiles are blocks of kv8_own_kernel
     int32_t wide_runs;             // CTAs that work on the shared units of 128 rows (kv8_shared_mma.cuh); 0: units of 16 rows here
     int64_t shared_slots;          // row of part_o and part_ml where the sums of split units of 128 rows begin
     int4* seqs;                    // [n]: shared tiles, place of the group, its first sequence of this launch, queries
@@ -67,6 +71,23 @@ __device__ __forceinline__ int shared_unit0(const SharedParams& p, int j, int fi
 __device__ __forceinline__ int least_seen(const SharedParams& p, const Sequence& s) {
     if (s.count == 0) return 0;
     return p.causal ? max(0, s.len - s.count + 1) : s.len;
+}
+
+// Are a group's sequences and its shared tokens what they may be? (Where one group's are not, none shares anything: groups that
+// overlap would name more tiles than are counted.)
+__device__ __forceinline__ bool group_in_order(const SharedParams& p, int j, int first, int next, int shared) {
+    return first >= 0 && next > first && next <= p.all && shared >= 0 && (j > 0 || first == 0);
+}
+
+// Tiles of a group's shared part: what its first sequence, of `len` tokens, has of it, in whole steps.
+__device__ __forceinline__ int shared_tiles(const SharedParams& p, int shared, int len) {
+    const int64_t most = min(min(static_cast<int64_t>(shared), static_cast<int64_t>(len)), static_cast<int64_t>(p.max_pages) * p.page_size);
+    return static_cast<int>(max(static_cast<int64_t>(0), most)) / kSharedStep * (kSharedStep / kTileKeys);
+}
+
+// The tile that a sequence's own part begins at, in a group of so many shared tiles: it takes part if all its queries see them.
+__device__ __forceinline__ int own_start(const SharedParams& p, const Sequence& s, int tiles) {
+    return tiles > 0 && least_seen(p, s) >= static_cast<int64_t>(tiles) * kTileKeys ? tiles : 0;
 }
 
 // 16 stacked rows of a group: KV head h, rows [16 rt, 16 rt + 16).
@@ -104,26 +125,23 @@ __device__ __forceinline__ int plan_groups(const SharedParams& p, int32_t* first
     }
     __syncthreads();
     const int g0 = lowest, groups = min(p.G - g0, kMaxShared);
-    const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+    bool bad = false;
     for (int j = t; j <= groups; j += kThreads) {
-        int first = p.groups[g0 + j];
-        bool bad = (g0 + j == 0 && first != 0) || (g0 + j == p.G && first != p.all) || first < 0 || first > p.all;
-        int tiles = 0;
-        if (j < groups && !bad) {
-            const int next = p.groups[g0 + j + 1];
+        const int first = p.groups[g0 + j];
+        if (j < groups) {
             const int shared = p.shared[g0 + j];
-            bad = next <= first || next > p.all || shared < 0;
-            if (!bad && first < p.b0 + p.n) {
-                const int len = p.lengths[first];
-                const int64_t most = min(min(static_cast<int64_t>(shared), static_cast<int64_t>(len)), room);
-                tiles = static_cast<int>(max(static_cast<int64_t>(0), most)) / kSharedStep * (kSharedStep / kTileKeys);
-            }
+            const bool in_order = group_in_order(p, g0 + j, first, p.groups[g0 + j + 1], shared);
+            tiles_of_group[j] = in_order && first < p.b0 + p.n ? shared_tiles(p, shared, p.lengths[first]) : 0;
+            bad = bad || !in_order;
         }
-        if (bad) atomicOr(p.wait.status, kErrPage);
+        bad = bad || (g0 + j == p.G && first != p.all);
         first_of[j] = first;
-        if (j < groups) tiles_of_group[j] = bad ? 0 : tiles;
     }
-    __syncthreads();
+    if (bad) atomicOr(p.wait.status, kErrPage);
+    if (__syncthreads_or(bad)) {
+        for (int j = t; j < groups; j += kThreads) tiles_of_group[j] = 0;
+        __syncthreads();
+    }
     for (int i = t; i < p.n; i += kThreads) {
         const int b = p.b0 + i;
         int lo = 0, hi = groups - 1;
@@ -134,7 +152,7 @@ __device__ __forceinline__ int plan_groups(const SharedParams& p, int32_t* first
         const Sequence s = sequence(p, b);
         const bool member = first_of[lo] >= 0 && first_of[lo] <= b && b < first_of[lo + 1];
         const int tiles = member ? tiles_of_group[lo] : 0;
-        start[i] = tiles > 0 && least_seen(p, s) >= static_cast<int64_t>(tiles) * kTileKeys ? tiles : 0;
+        start[i] = own_start(p, s, tiles);
         if (blockIdx.x == 0) p.seqs[i] = make_int4(start[i], lo, max(first_of[lo], p.b0) - p.b0, s.count);
     }
     __syncthreads();
@@ -149,6 +167,12 @@ __device__ __forceinline__ Group group_of(const SharedParams& p, const int32_t* 
 
 // Tiles of the unit of row tile rt of a sequence whose own part begins at tile `start`, of which there is one at least.
 __device__ __forceinline__ int own_tiles(int end, int start) { return max(1, (end + kTileKeys - 1) / kTileKeys - start); }
+
+// Those of them that the spreading kernel works on.
+__device__ __forceinline__ int spread_tiles(const SharedParams& p, int end, int start) {
+    const int tiles = own_tiles(end, start);
+    return tiles > p.own_limit ? tiles : 0;
+}
 
 template <int kD, typename T>
 __global__ void __launch_bounds__(32 * kDecodeWarps, 2)
@@ -195,7 +219,7 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             tiles = (shared_rows(p, gr.n) + kRows - 1) / kRows * gr.tiles;
         } else {
             const Sequence s = sequence(p, p.b0 + i - groups);
-            for (int rt = 0; rt < p.row_tiles; ++rt) tiles += own_tiles(row_tile_end(p, s, rt), start[i - groups]);
+            for (int rt = 0; rt < p.row_tiles; ++rt) tiles += spread_tiles(p, row_tile_end(p, s, rt), start[i - groups]);
         }
         prefix[i + 1] = tiles * p.Hkv;
     }
@@ -255,7 +279,7 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             seq = sequence(p, b);
             first = local;
             tile0 = start[i];
-            while (first >= (unit_tiles = own_tiles(key_end = row_tile_end(p, seq, rt), tile0)) && rt + 1 < p.row_tiles) {
+            while (first >= (unit_tiles = spread_tiles(p, key_end = row_tile_end(p, seq, rt), tile0)) && rt + 1 < p.row_tiles) {
                 first -= unit_tiles;
                 ++rt;
             }
@@ -325,6 +349,146 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     if (!ok)
         for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
     if (p.wide_runs > 0) griddep_wait();
+}
+
+// A sequence's own part, a block to a unit (of up to own_limit tiles), whose warps share the tiles out and join their sums in
+// shared memory. For up to 64 groups, beside the tensor-core kernel (see there for the waits).
+template <int kD, typename T, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kBlockWarps / kWarps)
+kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
+    using G = DecodeGeometry<kD>;
+    using B = BlockGeometry<kD, kWarps>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ float warp_ml[kWarps][kRows][2];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (base - raw);
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    const uint32_t g = lane >> 2, c = lane & 3u;
+    const uint32_t ring = base + warp * G::kWarpBytes, bars = base + B::kOffBars + 8u * warp * G::kStages;
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tmap_k);
+        prefetch_tensor_map(&tmap_v);
+    }
+    if (lane == 0) {
+        for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, s == 0 && (p.flags & kFlagDropArrive) ? 2 : 1);
+        fence_mbar_init_cluster();
+    }
+    __syncwarp();
+    int unit = static_cast<int>(blockIdx.x);
+    const int rt = unit % p.row_tiles;
+    unit /= p.row_tiles;
+    const int h = unit % p.Hkv, i = unit / p.Hkv, b = p.b0 + i;
+    // ---- where the sequence's own part begins: its group is one lane's
+    int start = 0;
+    const Sequence seq = sequence(p, b);
+    {
+        int shared = 0, of = -1;
+        bool in_order = true;
+        for (int j0 = 0; j0 < p.G; j0 += 32) {
+            const int j = j0 + static_cast<int>(lane);
+            if (j >= p.G) continue;
+            const int first = p.groups[j], next = p.groups[j + 1], tokens = p.shared[j];
+            in_order = in_order && group_in_order(p, j, first, next, tokens) && (j + 1 < p.G || next == p.all);
+            if (first <= b && b < next) {
+                shared = tokens;
+                of = first;
+            }
+        }
+        const uint32_t who = __ballot_sync(0xffffffffu, of >= 0);
+        if (__all_sync(0xffffffffu, in_order) && who != 0) {
+            const int from = __ffs(static_cast<int>(who)) - 1;
+            of = __shfl_sync(0xffffffffu, of, from);
+            shared = __shfl_sync(0xffffffffu, shared, from);
+            start = own_start(p, seq, shared_tiles(p, shared, p.lengths[of]));
+        }
+    }
+    const int key_end = row_tile_end(p, seq, rt);
+    const int tiles = own_tiles(key_end, start);
+    const bool mine = tiles <= p.own_limit;
+    bool ok = true;
+    if (mine) {
+        float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        const int first = start + static_cast<int>(warp) * tiles / kWarps, last = start + static_cast<int>(warp + 1) * tiles / kWarps;
+        if (first < last && key_end > start * kTileKeys) {
+            int fills = 0, uses = 0;
+            ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, UnitRows{p, b, h, rt, seq}, h, key_end, first, last,
+                                           o, m, l);
+            if (ok) {
+                float* const part = reinterpret_cast<float*>(smem + warp * G::kWarpBytes);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float4* const dst = reinterpret_cast<float4*>(part + ((g + 8 * e) * 4 + c) * B::kPitch);
+#pragma unroll
+                    for (int k = 0; k < kD / 32; ++k) {
+                        dst[k] = make_float4(o[4 * k][2 * e], o[4 * k + 1][2 * e], o[4 * k + 2][2 * e], o[4 * k + 3][2 * e]);
+                        dst[kD / 32 + k] =
+                            make_float4(o[4 * k][2 * e + 1], o[4 * k + 1][2 * e + 1], o[4 * k + 2][2 * e + 1], o[4 * k + 3][2 * e + 1]);
+                    }
+                }
+            } else {                         // the copies in flight land before the block ends
+                for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
+            }
+        }
+        if (c == 0) {                        // (a warp without tiles has a maximum of -inf)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                warp_ml[warp][g + 8 * e][0] = ok ? m[e] : -INFINITY;
+                warp_ml[warp][g + 8 * e][1] = ok ? l[e] : 0.0f;
+            }
+        }
+    }
+    ok = !__syncthreads_or(!ok);
+    if (mine && threadIdx.x == 0) p.info[(static_cast<int64_t>(i) * p.Hkv + h) * p.row_tiles + rt] = make_int4(0, 0, 0, 0);
+    // 16 threads per row, kD / 16 columns each
+    constexpr int kCols = kD / 16;
+    const int col = static_cast<int>(threadIdx.x & 15u) * kCols;
+#pragma unroll 1
+    for (int r = static_cast<int>(threadIdx.x >> 4); mine && ok && r < kRows; r += 2 * kWarps) {
+        const int row = rt * kRows + r;
+        const int t = row / p.group, head = h * p.group + row % p.group;
+        if (t >= p.T) break;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][r][0]);
+        float l = 0.0f, acc[kCols];
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = warp_ml[w][r][0], lw = warp_ml[w][r][1];
+            if (mw > -INFINITY || lw != 0.0f) {  // (a row that a warp's tokens are all hidden from has left zeros)
+                const float weight = ex2_approx(mw - m);
+                l += lw * weight;
+                const float* const part =
+                    reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + (r * 4 + col / B::kOwn) * B::kPitch + col % B::kOwn;
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) acc[k] += part[k] * weight;
+            }
+        }
+        const bool any = l > 0.0f || l != l;
+        const int64_t out_row = (static_cast<int64_t>(i) * p.T + t) * p.Hq + head;     // of the launch
+        if (start > 0) {
+            const int64_t at_row = p.whole[1] + out_row;
+            float4* const dst = reinterpret_cast<float4*>(p.part_o + at_row * kD + col);
+#pragma unroll
+            for (int k = 0; k < kCols / 4; ++k)
+                dst[k] = make_float4(any ? acc[4 * k] : 0.0f, any ? acc[4 * k + 1] : 0.0f, any ? acc[4 * k + 2] : 0.0f, any ? acc[4 * k + 3] : 0.0f);
+            if (col == 0) {
+                p.part_ml[2 * at_row] = any ? m : -INFINITY;
+                p.part_ml[2 * at_row + 1] = any ? l : 0.0f;
+            }
+        } else {
+            const float mul = any ? 1.0f / l : 0.0f;
+            T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + col;
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) dst[k] = from_float<T>(any ? acc[k] * mul : 0.0f);
+            if (p.lse != nullptr && col == 0)
+                p.lse[static_cast<int64_t>(p.b0) * p.T * p.Hq + out_row] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+    }
+    griddep_wait();                          // (this grid may have run beside the one before it: its end is that one's too)
 }
 
 // Adds up what the kernels above left: kSplit warps of a block to a row (eight where there are few rows, of many parts each),

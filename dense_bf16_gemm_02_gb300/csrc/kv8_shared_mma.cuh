@@ -211,23 +211,24 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
     griddep_launch_dependents();               // (now: what follows on the stream may run beside this grid, see launch())
     // ---- the groups' blocks; the CTA's run
     {
-        const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
-        for (int j = static_cast<int>(threadIdx.x); j <= p.G; j += kWideThreads) {
+        bool bad = false;        // (what is out of order the spreading kernel reports)
+        static_assert(kWideGroups < kWideThreads, "a thread to a group");
+        const int j = static_cast<int>(threadIdx.x);
+        if (j <= p.G) {
             const int first = p.groups[j];
-            const bool in_order = first >= 0 && first <= p.all;
-            int blocks = 0;
-            if (j < p.G && in_order) {
-                const int next = p.groups[j + 1], shared = p.shared[j];
-                if (next > first && next <= p.all && shared >= 0) {      // (what is out of order the other kernel reports)
-                    const int len = p.lengths[first];
-                    const int64_t most = min(min(static_cast<int64_t>(shared), static_cast<int64_t>(len)), room);
-                    blocks = static_cast<int>(max(static_cast<int64_t>(0), most)) / kSharedStep;
-                }
-            }
             first_of[j] = first;
-            if (j < p.G) blocks_of[j] = blocks;
+            if (j < p.G) {
+                const int shared = p.shared[j];
+                bad = !group_in_order(p, j, first, p.groups[j + 1], shared);
+                blocks_of[j] = bad ? 0 : shared_tiles(p, shared, p.lengths[first]) / (kSharedStep / kTileKeys);
+            } else {
+                bad = first != p.all;
+            }
         }
-        __syncthreads();
+        if (__syncthreads_or(bad)) {
+            if (j < p.G) blocks_of[j] = 0;
+            __syncthreads();
+        }
         if (warp == 0) {
             int sum = 0;
             for (int j0 = 0; j0 < p.G; j0 += 32) {
@@ -406,12 +407,19 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                     }
                     const bool in_cur = block < window + 4;
                     const int at = (block - window & 3) * 8;
-                    const uint32_t mine = is_k ? __float_as_uint(in_cur ? cur.ks : ahead.ks) : (in_cur ? cur.vs : ahead.vs);
-                    const uint32_t scale = __shfl_sync(0xffffffffu, mine, at + (lane & 7u));
                     if (!wait_warp(raw_empty(rs), raw_ph ^ 1u, kErrWaitRing, suspend)) {
                         abort_seen = true;
                         break;
                     }
+                    // (the copies go out before the scales are waited for; the barrier's one arrival, which says what to expect, after)
+                    for (int k = 0; k < boxes; ++k) {
+                        const int row = __shfl_sync(0xffffffffu, in_cur ? cur.row : ahead.row, at + (k << p.page_shift >> 4));
+                        if (lane == 0)
+                            tma_load_3d(raw_addr(rs) + static_cast<uint32_t>((k << p.page_shift) * kD), is_k ? &tmap_k : &tmap_v, 0, 0, row,
+                                        raw_full(rs));
+                    }
+                    const uint32_t mine = is_k ? __float_as_uint(in_cur ? cur.ks : ahead.ks) : (in_cur ? cur.vs : ahead.vs);
+                    const uint32_t scale = __shfl_sync(0xffffffffu, mine, at + (lane & 7u));
                     if (is_k) {
                         if (lane < 8)
                             asm volatile("st.shared.b32 [%0], %1;" ::"r"(key_scale_addr(key_block) + 4u * lane), "r"(scale) : "memory");
@@ -429,12 +437,6 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(raw_full(rs), W::kRawBytes);
-                    for (int k = 0; k < boxes; ++k) {
-                        const int row = __shfl_sync(0xffffffffu, in_cur ? cur.row : ahead.row, at + (k << p.page_shift >> 4));
-                        if (lane == 0)
-                            tma_load_3d(raw_addr(rs) + static_cast<uint32_t>((k << p.page_shift) * kD), is_k ? &tmap_k : &tmap_v, 0, 0, row,
-                                        raw_full(rs));
-                    }
                     if (++rs == W::kRaw) {
                         rs = 0;
                         raw_ph ^= 1u;

@@ -610,8 +610,8 @@ hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, in
  * 128 tokens; what is left of them is read from each sequence's own table row. shared[g] = 0, and groups of one sequence,
  * are fine. The result is hk_attention_kv8's, but for the order of its fp32 sums. Not shared in
  * fact, and read by a sequence itself, are tokens past the first sequence's length, and those of a
- * sequence that has queries which do not see all of them. Groups out of order or range take no
- * part (every sequence's tokens are its own) and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG.
+ * sequence that has queries which do not see all of them. Where groups are out of order or range, every sequence
+ * reads all its tokens itself and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG.
  * Many query rows per group run on a tensor-core kernel for what is shared when Q is bf16 with rows that are
  * 16-byte aligned and there are up to 64 groups (weights rounded to bf16, 2^-8, before they meet V); else on the
  * few-row kernels. From 256 rows of each sequence and KV head on the call is hk_attention_kv8's.
