@@ -28,7 +28,8 @@ hk_status fail(hk_status s, const char* fmt, ...) {
 constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
 constexpr int kSms = 152;
 constexpr int64_t kMaxHeads = 65535;
-constexpr int kWarpsPerSm = 24;          // warps that a call is spread over: as many as an SM holds
+constexpr int64_t kWarpsPerSm = 24;      // warps that an SM holds
+constexpr int kAngleSteps = 8;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -149,14 +150,22 @@ extern "C" hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], 
     p.eps = eps;
     p.norm = eps >= 0.0f;
     p.weight_f32 = weight_type == HK_TYPE_FP32;
-    // as few row steps to a warp as leave the GPU full of warps, four (whose loads are in flight together) where there are enough
     const int lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;
     for (int op = 0; op < 2; ++op) p.op_steps[op] = (p.heads[op] + 32 / lanes - 1) / (32 / lanes);
     const int64_t token_steps = int64_t(p.op_steps[0]) + p.op_steps[1];
-    const int64_t steps = std::min<int64_t>(token_steps, std::max<int64_t>(1, B * T * token_steps / (int64_t(kSms) * kWarpsPerSm)));
-    int64_t shares = (token_steps + steps - 1) / steps;
+    // warps to a token: those whose rounds over the GPU take the least time, a warp's being its row steps and what its angles
+    // cost (some eight steps)
+    int64_t shares = 1, least = INT64_MAX;
+    for (int64_t rounds = 1; rounds <= 8; ++rounds) {
+        const int64_t s = std::max<int64_t>(1, std::min(token_steps, rounds * kSms * kWarpsPerSm / (B * T)));
+        const int64_t steps = (token_steps + s - 1) / s, warps = B * T * ((token_steps + steps - 1) / steps);
+        const int64_t time = (warps + kSms * kWarpsPerSm - 1) / (kSms * kWarpsPerSm) * (steps + kAngleSteps);
+        if (time < least) {
+            least = time;
+            shares = (token_steps + steps - 1) / steps;
+        }
+    }
     p.steps = static_cast<int32_t>((token_steps + shares - 1) / shares);
-    shares = (token_steps + p.steps - 1) / p.steps;
     if (B * T > kLimit / shares) return fail(HK_ERR_INVALID_ARG, "problem too large");
     p.shares = static_cast<uint32_t>(shares);
     p.warps = static_cast<uint32_t>(B * T * shares);

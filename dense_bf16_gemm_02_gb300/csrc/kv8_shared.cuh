@@ -109,22 +109,43 @@ struct SharedRows {
     }
 };
 
-// What a launch's blocks all work out first: groups, shared and own tiles, and their sums. Returns the number of groups.
+// Tiles of the unit of row tile rt of a sequence whose own part begins at tile `start`, of which there is one at least.
+__device__ __forceinline__ int own_tiles(int end, int start) { return max(1, (end + kTileKeys - 1) / kTileKeys - start); }
+
+// Those of them that the spreading kernel works on.
+__device__ __forceinline__ int spread_tiles(const SharedParams& p, int end, int start) {
+    const int tiles = own_tiles(end, start);
+    return tiles > p.own_limit ? tiles : 0;
+}
+
+// Sequences of group `j` in this launch.
+__device__ __forceinline__ Group group_of(const SharedParams& p, const int32_t* first_of, const int32_t* tiles_of_group, int j) {
+    const int first = max(first_of[j], p.b0), end = min(first_of[j + 1], p.b0 + p.n);
+    return Group{first - p.b0, max(0, end - first), tiles_of_group[j]};
+}
+
+// What the spreading kernel's blocks all work out first: groups, shared tiles, where the sequences' own parts begin, and (at
+// i + 1) the tiles of each section i: the groups' shared units, then the sequences' own. Returns the number of groups.
 template <int kThreads>
-__device__ __forceinline__ int plan_groups(const SharedParams& p, int32_t* first_of, int32_t* tiles_of_group, int32_t* start) {
+__device__ __forceinline__ int plan_sections(const SharedParams& p, int32_t* first_of, int32_t* tiles_of_group, int32_t* start, int32_t* prefix) {
     const int t = static_cast<int>(threadIdx.x);
     __shared__ int lowest;
-    if (t == 0) {
-        int lo = 0, hi = p.G - 1;            // the group of sequence b0
-        if (p.b0 > 0)
+    Sequence mine = {0, 0};                  // (asked for ahead of what the groups' loads are waited for)
+    if (t < p.n) mine = sequence(p, p.b0 + t);
+    int g0 = 0;
+    if (p.b0 > 0) {                          // the group of sequence b0
+        if (t == 0) {
+            int lo = 0, hi = p.G - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
                 if (p.groups[mid] <= p.b0) lo = mid; else hi = mid - 1;
             }
-        lowest = lo;
+            lowest = lo;
+        }
+        __syncthreads();
+        g0 = lowest;
     }
-    __syncthreads();
-    const int g0 = lowest, groups = min(p.G - g0, kMaxShared);
+    const int groups = min(p.G - g0, kMaxShared);
     bool bad = false;
     for (int j = t; j <= groups; j += kThreads) {
         const int first = p.groups[g0 + j];
@@ -142,6 +163,10 @@ __device__ __forceinline__ int plan_groups(const SharedParams& p, int32_t* first
         for (int j = t; j < groups; j += kThreads) tiles_of_group[j] = 0;
         __syncthreads();
     }
+    for (int j = t; j < groups; j += kThreads) {
+        const Group gr = group_of(p, first_of, tiles_of_group, j);
+        prefix[j + 1] = p.wide_runs > 0 ? 0 : (shared_rows(p, gr.n) + kRows - 1) / kRows * gr.tiles * p.Hkv;
+    }
     for (int i = t; i < p.n; i += kThreads) {
         const int b = p.b0 + i;
         int lo = 0, hi = groups - 1;
@@ -149,29 +174,17 @@ __device__ __forceinline__ int plan_groups(const SharedParams& p, int32_t* first
             const int mid = (lo + hi + 1) / 2;
             if (first_of[mid] <= b) lo = mid; else hi = mid - 1;
         }
-        const Sequence s = sequence(p, b);
+        const Sequence s = i == t ? mine : sequence(p, b);
         const bool member = first_of[lo] >= 0 && first_of[lo] <= b && b < first_of[lo + 1];
-        const int tiles = member ? tiles_of_group[lo] : 0;
-        start[i] = own_start(p, s, tiles);
-        if (blockIdx.x == 0) p.seqs[i] = make_int4(start[i], lo, max(first_of[lo], p.b0) - p.b0, s.count);
+        const int from = own_start(p, s, member ? tiles_of_group[lo] : 0);
+        start[i] = from;
+        if (blockIdx.x == 0) p.seqs[i] = make_int4(from, lo, max(first_of[lo], p.b0) - p.b0, s.count);
+        int tiles = 0;
+        for (int rt = 0; rt < p.row_tiles; ++rt) tiles += spread_tiles(p, row_tile_end(p, s, rt), from);
+        prefix[groups + i + 1] = tiles * p.Hkv;
     }
     __syncthreads();
     return groups;
-}
-
-// Sequences of group `j` in this launch.
-__device__ __forceinline__ Group group_of(const SharedParams& p, const int32_t* first_of, const int32_t* tiles_of_group, int j) {
-    const int first = max(first_of[j], p.b0), end = min(first_of[j + 1], p.b0 + p.n);
-    return Group{first - p.b0, max(0, end - first), tiles_of_group[j]};
-}
-
-// Tiles of the unit of row tile rt of a sequence whose own part begins at tile `start`, of which there is one at least.
-__device__ __forceinline__ int own_tiles(int end, int start) { return max(1, (end + kTileKeys - 1) / kTileKeys - start); }
-
-// Those of them that the spreading kernel works on.
-__device__ __forceinline__ int spread_tiles(const SharedParams& p, int end, int start) {
-    const int tiles = own_tiles(end, start);
-    return tiles > p.own_limit ? tiles : 0;
 }
 
 template <int kD, typename T>
@@ -208,22 +221,8 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     int32_t* const first_of = reinterpret_cast<int32_t*>(smem + S::kOffGroups);
     int32_t* const tiles_of_group = reinterpret_cast<int32_t*>(smem + S::kOffShared);
     int32_t* const start = reinterpret_cast<int32_t*>(smem + S::kOffStart);
-    const int groups = plan_groups<kThreads>(p, first_of, tiles_of_group, start);
+    const int groups = plan_sections<kThreads>(p, first_of, tiles_of_group, start, prefix);
     const int sections = groups + p.n;       // the groups' shared units, then the sequences' own
-    for (int i = static_cast<int>(threadIdx.x); i < sections; i += kThreads) {
-        int tiles = 0;
-        if (i < groups && p.wide_runs > 0) {
-            tiles = 0;
-        } else if (i < groups) {
-            const Group gr = group_of(p, first_of, tiles_of_group, i);
-            tiles = (shared_rows(p, gr.n) + kRows - 1) / kRows * gr.tiles;
-        } else {
-            const Sequence s = sequence(p, p.b0 + i - groups);
-            for (int rt = 0; rt < p.row_tiles; ++rt) tiles += spread_tiles(p, row_tile_end(p, s, rt), start[i - groups]);
-        }
-        prefix[i + 1] = tiles * p.Hkv;
-    }
-    __syncthreads();
     if (warp == 0) {
         int sum = 0;
         for (int i0 = 0; i0 < sections; i0 += 32) {

@@ -36,11 +36,14 @@ class Kv8Pool:
     ``table`` int32 [rows, max_pages]: the block table that kv8_append and
     attention_kv8 take; ``held`` int32 [rows]: tokens whose pages a row has.
     CUDA tensors; ``Kv8Pool.empty`` makes them, with nothing held. None of them can be
-    set to another tensor."""
+    set to another tensor. A pool also keeps the workspace of its arrangements (calls
+    on one pool follow one another anyway) and ``missing``, what the last one lacked."""
 
-    __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref", "_scratch")
+    __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref", "_workspace", "_missing",
+                 "_workspace_ptr", "_workspace_size", "_missing_ptr")
     refs, table, held = (_read_only(n) for n in __slots__[:3])
     pages, rows, max_pages, page_size = (_read_only(n) for n in __slots__[3:7])
+    missing = _read_only("_missing")
 
     def __init__(self, refs, table, held, page_size=64):
         for t, dim in ((refs, 1), (table, 2), (held, 1)):
@@ -55,9 +58,12 @@ class Kv8Pool:
             raise ValueError("refs and held must be contiguous")
         self._refs, self._table, self._held = refs, table, held
         self._pages, self._rows, self._max_pages, self._page_size = refs.size(0), rows, max_pages, page_size
-        self._scratch = 0                    # bytes of an arrangement's workspace, once known
         self._ref = _pool_struct(refs.data_ptr(), table.data_ptr(), held.data_ptr(), refs.size(0), _row_stride(table, "table"),
                                  rows, max_pages, page_size, 0)
+        size = _hk.load().hk_kv8_arrange_workspace_size(self._ref)
+        self._workspace = torch.empty(size, dtype=_u8, device=refs.device)
+        self._missing = torch.empty((), dtype=_i32, device=refs.device)
+        self._workspace_ptr, self._workspace_size, self._missing_ptr = self._workspace.data_ptr(), size, self._missing.data_ptr()
 
     @classmethod
     def empty(cls, pages, rows, max_pages, page_size=64, device="cuda"):
@@ -91,9 +97,9 @@ def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=
     room above what a row holds takes pages, keep below it cuts the row back (0 ends
     it), another parent forks or reorders. Whole pages within keep are shared, the ones
     that will be written are the row's own: copied in each of ``caches`` where they hold
-    tokens. Returns a 0-dim int32 tensor: 0; or the pages that lacked, or -1 for
-    arguments out of range, and then nothing was changed. What a call frees is free for the next
-    one. ``copies``: an int32 tensor [2, rows] that receives the copied pages and their
+    tokens. Returns ``pool.missing``, a 0-dim int32 tensor that the pool's next call
+    writes again: 0; or the pages that lacked, or -1 for arguments out of range, and then nothing was
+    changed. What a call frees is free for the next one. ``copies``: an int32 tensor [2, rows] that receives the copied pages and their
     copies (-1: none). See hk_kv8_arrange."""
     _check_pool(pool)
     rows = pool._rows
@@ -108,18 +114,12 @@ def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=
                                or tuple(copies.shape) != (2, rows) or not copies.is_contiguous()):
         raise TypeError("copies must be a contiguous int32 CUDA tensor [2, rows]")
     refs, n = _cache_refs(caches, "caches") if caches else (None, 0)
-    lib = _hk.load()
-    size = pool._scratch
-    if not size:
-        size = pool._scratch = lib.hk_kv8_arrange_workspace_size(pool._ref)
-    workspace = _empty((size,), _u8, keep, stream)
-    missing = _empty((), _i32, keep, stream)
-    st = lib.hk_kv8_arrange(pool._ref, keep.data_ptr(), room.data_ptr(), None if parents is None else parents.data_ptr(), refs, n,
-                            None if copies is None else copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(), size,
-                            _stream(stream, keep))
+    st = _hk.load().hk_kv8_arrange(pool._ref, keep.data_ptr(), room.data_ptr(), None if parents is None else parents.data_ptr(), refs,
+                                   n, None if copies is None else copies.data_ptr(), pool._missing_ptr, pool._workspace_ptr,
+                                   pool._workspace_size, _stream(stream, keep))
     if st != HK_OK:
         raise HKError(st, "hk_kv8_arrange")
-    return missing
+    return pool._missing
 
 
 def kv8_compact(pool: Kv8Pool, caches=(), stream=None):

@@ -112,7 +112,7 @@ def test_python_refusals(lib):
     with pytest.raises(TypeError):
         hk.kv8_copy_pages([z], [z], z, z)
     pool = hk.Kv8Pool.__new__(hk.Kv8Pool)
-    for name in ("refs", "table", "held", "pages", "rows", "max_pages", "page_size"):
+    for name in ("refs", "table", "held", "pages", "rows", "max_pages", "page_size", "missing"):
         with pytest.raises(AttributeError):
             setattr(pool, name, 1)
 

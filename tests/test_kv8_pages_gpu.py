@@ -98,7 +98,10 @@ def test_a_call_that_lacks_pages_changes_nothing():
     pool, caches = hk.Kv8Pool.empty(4, 3, 4, 16), _caches(1, 4, 16)
     assert hk.kv8_arrange(pool, _i32([0, 0, 0]), _i32([17, 1, 0]), caches=caches).item() == 0
     state = [t.clone() for t in (pool.refs, pool.table, pool.held, *_tensors(caches))]
-    assert hk.kv8_arrange(pool, _i32([17, 1, 1]), _i32([33, 1, 17]), _i32([0, 1, 1]), caches).item() == 2
+    lack = hk.kv8_arrange(pool, _i32([17, 1, 1]), _i32([33, 1, 17]), _i32([0, 1, 1]), caches)
+    assert lack.item() == 2 and lack is pool.missing
+    other = hk.Kv8Pool.empty(4, 3, 4, 16)
+    assert hk.kv8_arrange(other, _i32([0, 0, 0])).item() == 0 and lack.item() == 2
     assert all((a == b).all() for a, b in zip(state, (pool.refs, pool.table, pool.held, *_tensors(caches))))
     assert hk.kv8_arrange(pool, _i32([17, 0, 0])).item() == 0          # (room: keep)
     assert pool.refs.sum().item() == 2 and pool.held.tolist() == [17, 0, 0]
