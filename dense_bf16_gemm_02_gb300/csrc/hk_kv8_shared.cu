@@ -153,7 +153,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorM
                                  SharedGeometry<kD>::kSmemBytes, st, tk, tv, p);
     if (e != cudaSuccess) return e;
     const int64_t rows = int64_t(p.n) * p.T * p.Hq;
-    const int split = rows <= 8 * kSms ? 8 : rows <= 32 * kSms ? 2 : 1;
+    const int split = rows <= 16 * kSms ? 8 : rows <= 64 * kSms ? 2 : 1;       // (as many warps as are resident at a time)
     auto* fn = split == 8 ? &kv8_shared_combine_kernel<kD, T, 8> : split == 2 ? &kv8_shared_combine_kernel<kD, T, 2> : &kv8_shared_combine_kernel<kD, T, 1>;
     return launch_early(fn, dim3(static_cast<unsigned>(ceil_div(rows * split, 8))), dim3(256), 0, st, p);
 }

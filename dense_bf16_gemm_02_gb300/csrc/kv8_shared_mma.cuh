@@ -3,8 +3,8 @@
 // With 64 sequences of 8 query heads per KV head a shared token meets 512 rows: 4 · 512 · D
 // operations for 2 · D bytes, so the tensor cores bound the work and mma.sync with 16 rows
 // to a unit (each of which converts every tile again) is the wrong tool. Here a unit is 128 stacked rows
-// of a group and KV head: S = Q·Kᵀ (two buffers) and O += P·V in Tensor Memory on tcgen05.mma, P
-// in Tensor Memory too. All units' blocks of 128 tokens, in order, are cut into equal runs, one per
+// of a group and KV head: S = Q·Kᵀ (two buffers) and O += P·V in Tensor Memory on tcgen05.mma, P and
+// Q in Tensor Memory too (shared memory is what MMAs and conversion wait for). All units' blocks of 128 tokens, in order, are cut into equal runs, one per
 // CTA, since a prefix has few units and many blocks: each run leaves unnormalised rows,
 // maxima and sums of its units in memory for the combining kernel.
 //
@@ -48,12 +48,11 @@ constexpr uint32_t kErrSoftmaxWait = 1u << 19;
 template <int kD>
 struct WideGeometry {
     static constexpr int kChunkBytes = 128 * 128;                             // 128 rows of 64 16-bit elements
-    static constexpr int kTileBytes = kD / 64 * kChunkBytes;                  // Q, or a block of K or V
-    static constexpr int kSlots = kD == 128 ? 3 : 6;                          // K and V blocks in 16 bits
+    static constexpr int kTileBytes = kD / 64 * kChunkBytes;                  // a block of K or V
+    static constexpr int kSlots = kD == 128 ? 4 : 6;                          // K and V blocks in 16 bits
     static constexpr int kRaw = kD == 128 ? 6 : 8;                            // and as codes
     static constexpr int kRawBytes = kWideBlock * kD;
-    static constexpr int kOffQ = 0;
-    static constexpr int kOffKV = kTileBytes;
+    static constexpr int kOffKV = 0;
     static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
     static constexpr int kOffBars = kOffRaw + kRaw * kRawBytes;
     // q_full, q_empty, p_full, o_done, s_full[2], s_free[2], kv_full and kv_empty of the slots, raw_full and raw_empty
@@ -70,8 +69,9 @@ struct WideGeometry {
     static constexpr int kSmemBytes = kOffPlan + (3 * kWideGroups + 2) * 4 + 1024;
     static_assert(kSmemBytes <= attn::kSmemLimit, "shared memory");
     static_assert(kOffRaw % 1024 == 0 && kOffKV % 1024 == 0 && kOffBars % 8 == 0 && kOffFactors % 4 == 0 && kOffKeyScales % 16 == 0, "alignment");
-    // TMEM columns: O (kD), S_0, S_1 (128 each), P (64: two bf16 per column)
-    static constexpr int kColO = 0, kColS = 128, kColP = 384, kTmemCols = 512;
+    // TMEM columns: O (kD), S_0, S_1 (128 each), P (64: two bf16 per column), Q (kD / 2: two f16 per column)
+    static constexpr int kColO = 0, kColS = 128, kColP = 384, kColQ = 448, kTmemCols = 512;
+    static_assert(kColQ + kD / 2 <= kTmemCols, "TMEM");
     static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128) & ~((7u << 7) | (7u << 10));     // A and B f16
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, kD) | (1u << 16);                    // B (V) MN-major
 };
@@ -181,7 +181,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
     int32_t* const blocks_of = first_of + kWideGroups + 1;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 4);
+        mbar_init(q_full, 128);
         mbar_init(q_empty, 1);                 // the last S of the piece is done
         mbar_init(p_full, 128);
         mbar_init(o_done, 1);
@@ -445,62 +445,67 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
             }
         }
         // ------------------------------------------- MMA issue --
-        if (warp == kWideIssueWarp && lane == 0) {
-            auto wait = [&](uint32_t b, uint32_t parity, uint32_t code) {
-                if (abort_seen) return false;
-                if (!wide_wait<false>(p.wait, b, parity, code)) abort_seen = true;
-                return !abort_seen;
-            };
+        // (the warp as a whole, one elected lane issuing: descriptors then stay in uniform registers)
+        if (warp == kWideIssueWarp) {
             int slot = 0;
             uint32_t ring_ph = 0;
-            // the next position's block in 16 bits: its address once it is there, and the barrier that gives it back
-            auto take = [&](uint32_t& addr, uint32_t& back) {
-                if (!wait(kv_full(slot), ring_ph, kErrWaitData)) return false;
-                addr = slot_addr(slot);
-                back = kv_empty(slot);
+            // waits for the next position's block in 16 bits; its slot
+            auto take = [&](int& at) {
+                if (!wait_warp(kv_full(slot), ring_ph, kErrWaitData, poll)) return false;
+                at = slot;
                 if (++slot == W::kSlots) {
                     slot = 0;
                     ring_ph ^= 1u;
                 }
                 return true;
             };
-            const uint32_t qa = base + W::kOffQ;
             uint32_t nb = 0;             // blocks of S issued so far: buffer nb & 1, its phase nb / 2
             uint32_t pv = 0;             // of P·V
             int pieces = 0;
             for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next(), ++pieces) {
                 const int n = w.last - w.first;
-                if (!wait(q_full, pieces & 1, kErrWaitData)) break;
+                if (!wait_warp(q_full, pieces & 1, kErrWaitData, poll)) {
+                    abort_seen = true;
+                    break;
+                }
                 auto issue_s = [&](bool last) {
-                    uint32_t ka, back;
-                    if (nb >= 2 && !wait(s_free(nb & 1u), (nb / 2 - 1) & 1u, kErrWaitAcc)) return false;
-                    if (!take(ka, back)) return false;
+                    int at;
+                    if (nb >= 2 && !wait_warp(s_free(nb & 1u), (nb / 2 - 1) & 1u, kErrWaitAcc, poll)) return false;
+                    if (!take(at)) return false;
                     tc_fence_after_sync();
-                    const uint32_t s_tmem = tmem_base + W::kColS + (nb & 1u) * kWideBlock;
+                    if (elect_one()) {
+                        const uint32_t s_tmem = tmem_base + W::kColS + (nb & 1u) * kWideBlock, ka = slot_addr(at);
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * W::kChunkBytes + (kk & 3) * 32;
-                        mma_bf16_one(s_tmem, smem_desc_kmajor_sw128(qa + off), smem_desc_kmajor_sw128(ka + off), W::kIdescS, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < kD / 16; ++kk)
+                            mma_bf16_ts_one(s_tmem, tmem_base + W::kColQ + kk * 8,
+                                            smem_desc_kmajor_sw128(ka + (kk >> 2) * W::kChunkBytes + (kk & 3) * 32), W::kIdescS, kk > 0 ? 1u : 0u);
+                        mma_commit_one(s_full(nb & 1u));
+                        mma_commit_one(kv_empty(at));
+                        if (last) mma_commit_one(q_empty);
                     }
-                    mma_commit_one(s_full(nb & 1u));
-                    mma_commit_one(back);
-                    if (last) mma_commit_one(q_empty);
+                    __syncwarp();
                     ++nb;
                     return true;
                 };
-                if (!issue_s(n == 1)) break;
-                for (int j = 0; j < n; ++j, ++pv) {
-                    if (j + 1 < n && !issue_s(j + 2 == n)) break;
-                    uint32_t va, back;
-                    if (!take(va, back) || !wait(p_full, pv & 1u, kErrWaitAcc)) break;
+                bool ok = issue_s(n == 1);
+                for (int j = 0; ok && j < n; ++j, ++pv) {
+                    int at;
+                    ok = j + 1 == n || issue_s(j + 2 == n);
+                    ok = ok && take(at) && wait_warp(p_full, pv & 1u, kErrWaitAcc, poll);
+                    if (!ok) break;
                     tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t va = slot_addr(at);
 #pragma unroll
-                    for (int kk = 0; kk < kWideBlock / 16; ++kk)
-                        mma_bf16_ts_one(tmem_base + W::kColO, tmem_base + W::kColP + kk * 8, smem_desc_mnmajor(va + kk * 2048, 128, W::kChunkBytes),
-                                        W::kIdescPV, (j == 0 && kk == 0) ? 0u : 1u);
-                    mma_commit_one(o_done);
-                    mma_commit_one(back);
+                        for (int kk = 0; kk < kWideBlock / 16; ++kk)
+                            mma_bf16_ts_one(tmem_base + W::kColO, tmem_base + W::kColP + kk * 8, smem_desc_mnmajor(va + kk * 2048, 128, W::kChunkBytes),
+                                            W::kIdescPV, (j == 0 && kk == 0) ? 0u : 1u);
+                        mma_commit_one(o_done);
+                        mma_commit_one(kv_empty(at));
+                    }
+                    __syncwarp();
                 }
+                if (!ok) abort_seen = true;
             }
         }
     } else {
@@ -531,6 +536,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                 abort_seen = true;
                 break;
             }
+            tc_fence_after_sync();
             {
                 const uint16_t* const src = static_cast<const uint16_t*>(p.q) + (p.b0 + w.group.first + seq) * p.q_stride_b +
                                             tok * p.q_stride_t + head * p.q_stride_h;
@@ -552,17 +558,21 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                 const float mul = __uint_as_float(static_cast<uint32_t>(field) << 23);
                 c = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * p.scale_log2;
 #pragma unroll
-                for (int k = 0; k < kD / 8; ++k) {
-                    float f[8];
-                    widen8<__nv_bfloat16>(x[k], f);
-                    st_shared_v4(base + W::kOffQ + (k >> 3) * W::kChunkBytes + r * 128u + (((k & 7u) ^ (r & 7u)) << 4),
-                                 pack_f16x2(f[0] * mul, f[1] * mul), pack_f16x2(f[2] * mul, f[3] * mul), pack_f16x2(f[4] * mul, f[5] * mul),
-                                 pack_f16x2(f[6] * mul, f[7] * mul));
+                for (int k = 0; k < kD / 64; ++k) {
+                    uint32_t h[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float f[8];
+                        widen8<__nv_bfloat16>(x[8 * k + e], f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[4 * e + i] = pack_f16x2(f[2 * i] * mul, f[2 * i + 1] * mul);
+                    }
+                    tmem_store_32cols(tmem_base + lane_off + W::kColQ + 32 * k, h);
                 }
-                fence_proxy_async_smem();
+                tmem_wait_st();
+                tc_fence_before_sync();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            mbar_arrive(q_full);
             ++pieces;
             float m = 0.0f, l = 0.0f;      // running maximum (log2 units) used for P, and sum of P
             for (int j = 0; j < n; ++j, ++nb) {
