@@ -103,7 +103,7 @@ hk_status copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, int32_t n
         }
         // (a list whose length the host does not know: as many blocks as are resident at a time)
         const int64_t steps = int64_t(p.caches) * 2 * p.parts;
-        const int64_t blocks = std::min<int64_t>(n > kLimit / steps ? kLimit : n * steps, int64_t(kSms) * 8);
+        const int64_t blocks = std::min<int64_t>(n > kLimit / steps ? kLimit : ceil_div(n * steps, 8), int64_t(kSms) * 8);
         const cudaError_t e = launch_early(&kv8_copy_pages_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p);
         if (e != cudaSuccess) return cuda_fail(HK_ERR_LAUNCH, "launching the copy of pages", e);
     }
