@@ -152,6 +152,20 @@ PrefillWorkspace prefill_workspace(const hk_kv8_cache* c, int64_t B, int64_t max
     return w;
 }
 
+// Millionths of a microsecond per cached token of each form (figures at many_rows).
+double unit_cost(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq) {
+    return 35.0 * static_cast<double>(B) * c->heads * ceil_div(T * (Hq / c->heads), kRows);
+}
+
+double item_cost(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages) {
+    const int pack = pack_shift_of(Hq / c->heads);
+    const double seq_items = static_cast<double>(Hq >> pack) * ceil_div(T, (hk::attn::kTiles * hk::attn::kTileQ) >> pack);
+    const int64_t seqs = prefill_workspace(c, B, max_pages).seqs;
+    const double rounds = static_cast<double>(B / seqs) * std::ceil(static_cast<double>(seqs) * seq_items / kSms) +
+                          std::ceil(static_cast<double>(B % seqs) * seq_items / kSms);
+    return 13000.0 * rounds + 120.0 * static_cast<double>(B) * c->heads;
+}
+
 // Do the rows go to the tensor-core kernel? Both forms' time grows with the cached tokens; per token, in
 // millionths of a microsecond, measured (D 64 and 128, 2000 to 16000 tokens): 35 for each unit of 16 rows and KV
 // head, whatever their number, against 13000 for each round of 256-row items over the SMs and 120 for bringing
@@ -160,14 +174,7 @@ PrefillWorkspace prefill_workspace(const hk_kv8_cache* c, int64_t B, int64_t max
 // share a round: 64 sequences of up to 2048 tokens, 32 queries of 32 heads, take 230 us by units and 2112 us by
 // items with a table of 131072 tokens, 180 us by items with one of 2048.
 bool many_rows(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages) {
-    const int64_t group = Hq / c->heads;
-    const double units = static_cast<double>(B) * c->heads * ceil_div(T * group, kRows);
-    const int pack = pack_shift_of(group);
-    const double seq_items = static_cast<double>(Hq >> pack) * ceil_div(T, (hk::attn::kTiles * hk::attn::kTileQ) >> pack);
-    const int64_t seqs = prefill_workspace(c, B, max_pages).seqs;
-    const double rounds = static_cast<double>(B / seqs) * std::ceil(static_cast<double>(seqs) * seq_items / kSms) +
-                          std::ceil(static_cast<double>(B % seqs) * seq_items / kSms);
-    return 35.0 * units > 13000.0 * rounds + 120.0 * static_cast<double>(B) * c->heads;
+    return unit_cost(c, B, T, Hq) > item_cost(c, B, T, Hq, max_pages);
 }
 
 // Queries as [B, T, heads, D] in boxes of 64 columns × `pack` heads × 128 / pack tokens.
@@ -413,6 +420,10 @@ size_t few_rows_bytes(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, i
     return decode_workspace(c, B, T, Hq).total;
 }
 
+}  // namespace
+
+namespace hk_kv8 {
+
 // Can the tensor-core kernel run the call? It takes bf16 rows that TMA can read (aligned, and not one row for
 // several places) and writes 16 bytes at a time.
 bool many_rows_can(const void* Q, int32_t type, const int64_t q_strides[3], const void* O, const int64_t o_strides[3], int64_t B,
@@ -420,6 +431,16 @@ bool many_rows_can(const void* Q, int32_t type, const int64_t q_strides[3], cons
     return type == HK_TYPE_BF16 && rows_aligned(Q, q_strides) && rows_aligned(O, o_strides) && (B == 1 || q_strides[0] > 0) &&
            (T == 1 || q_strides[1] > 0) && (Hq == 1 || q_strides[2] > 0);
 }
+
+// (units at 25 millionths of a microsecond per cached token at head dimension 64, where both forms' order stays as it is)
+double attention_cost(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, bool many_can) {
+    if (many_can && many_rows(c, B, T, Hq, max_pages)) return item_cost(c, B, T, Hq, max_pages);
+    return unit_cost(c, B, T, Hq) * (c->head_dim == 64 ? 25.0 / 35.0 : 1.0);
+}
+
+}  // namespace hk_kv8
+
+namespace {
 
 constexpr uint32_t kFormFlags = HK_KV8_FEW_ROWS | HK_KV8_MANY_ROWS;
 

@@ -63,12 +63,11 @@ hk_status setup(int device) {
     return HK_OK;
 }
 
-// Query rows per sequence and KV head from which a sequence fills the tensor-core kernel's tiles by itself: reading a
-// prefix once for several sequences saves nothing there, and the call is attention_kv8's.
-constexpr int64_t kOwnTileRows = 256;
-
-// Tiles per warp up to which a sequence's own unit is a block's, beside the tensor-core kernel (beyond, it is spread over the GPU).
-constexpr int kOwnTiles = 32;
+// Tiles per warp up to which a sequence's own unit is a block's, beside the tensor-core kernel; beyond, it is spread over the
+// GPU: long ones among few would leave SMs idle, one long one among many would be waited for. Both sides (a block's, spread), 8 KV
+// heads, behind 8192 tokens, in microseconds: 64 sequences with 100 tokens of their own 53 and 59, with 1000 75 and 102, with
+// 4000 132 and 160; 4 sequences with 2000 37 and 41, with 4000 47 and 43, with 16000 112 and 77.
+constexpr int kOwnTiles = 32, kOwnTilesOfMany = 64;
 
 // Sequences of one launch: what the kernel plans for, and as many as keep the sums of whole units at 2^17 rows (two of
 // 64 MB at head dimension 128).
@@ -83,10 +82,35 @@ bool wide_can(const void* Q, int32_t type, const int64_t q_strides[3], int64_t G
     return type == HK_TYPE_BF16 && rows_aligned(Q, q_strides) && G <= kWideGroups;
 }
 
-// Does it? By the rows of a group.
-bool wide_pays(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, int64_t G) {
-    const int64_t rows = B * T * (Hq / c->heads) / G;
-    return rows > 32 && max_pages * c->page_size > 2048;
+// Who takes the call: attention_kv8 (every sequence reads all its tokens), the few-row kernels, or the tensor-core
+// kernel with the few-row ones beside it.
+enum Form { kOwn, kFew, kWide };
+
+// Query rows of a sequence and KV head from which attention_kv8's own tiles are full and it takes the call. Both sides
+// (tensor-core kernel here, attention_kv8), 8 KV heads of 128, in microseconds: 1024 rows, 8 sequences behind 2048, 8192 and
+// 32768 tokens 260 and 108, 483 and 294, 1417 and 1523; 512 rows 141 and 69, 253 and 180, 714 and 1515.
+constexpr int64_t kOwnTileRows = 1024;
+
+// By an estimate of the three times in microseconds, with the table's width for the lengths (which the host does not know) and
+// all of it shared. Per token, in millionths: what attention_kv8 takes, against 55 (head dimension 64: 30) for a unit of 16
+// stacked rows and 85 (65) for one of 128; 8, 18 and 25 for a call of one token, and a thousandth for every row that is joined.
+// Measured (attention_kv8, units of 16, of 128 rows; 8 KV heads of 128, 8 query heads each, one group of sequences with
+// 200 tokens of their own): 8 behind 2048 tokens 13.6, 24.3, 27.4; 8 behind 8192 29.2, 31.9, 30.8; 16 behind 8192 53, 49, 37;
+// 64 behind 2048 54, 72, 40; 64 behind 32768 546, 459, 115. 32 KV heads of a query head each: 16 behind 1024 30, 26, 32;
+// 16 behind 16384 285, 65, 72; 64 behind 16384 1086, 184, 99. Head dimension 64, fp16: 48 in 6 groups behind 4096 55 and 46;
+// 64 of 16 query heads behind 4096 (their own tiles are full) 43 and 54. Between the measured points it errs where two are near:
+// 4 behind 32768 take 52 by attention_kv8, which is chosen, and 42 by units of 128.
+Form choose(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, int64_t G, bool wide, bool many) {
+    const int64_t group = Hq / c->heads;
+    if (T * group >= kOwnTileRows || launch_batch(B, T, Hq) < 2) return kOwn;
+    const double room = 1e-6 * static_cast<double>(max_pages * c->page_size), rows = static_cast<double>(B * T * group) / G;
+    const double join = 1e-3 * static_cast<double>(B * T) * Hq, groups = static_cast<double>(G) * c->heads;
+    const bool d64 = c->head_dim == 64;
+    const double own_us = 8.0 + room * attention_cost(c, B, T, Hq, max_pages, many);
+    const double few_us = 18.0 + join + room * (d64 ? 30.0 : 55.0) * groups * std::ceil(rows / kRows);
+    const double wide_us = 25.0 + join + room * (d64 ? 65.0 : 85.0) * groups * std::ceil(rows / kWideRows);
+    if (wide && wide_us < std::min(own_us, few_us)) return kWide;
+    return few_us < own_us ? kFew : kOwn;
 }
 
 struct Workspace {
@@ -118,8 +142,6 @@ bool shape_ok(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t m
            Hq <= kLimit && Hq % c->heads == 0 && T <= kLimit / 16 / (Hq / c->heads) && G > 0 && G <= B;
 }
 
-bool on_its_own(const hk_kv8_cache* c, int64_t T, int64_t Hq) { return T * (Hq / c->heads) >= kOwnTileRows; }
-
 template <int kD, int kWarps>
 cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p, cudaStream_t st) {
     return launch_early(&kv8_own_kernel<kD, __nv_bfloat16, kWarps>, dim3(static_cast<unsigned>(int64_t(p.n) * p.Hkv * p.row_tiles)),
@@ -130,8 +152,9 @@ cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const Share
 template <int kD>
 cudaError_t launch_wide(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
                         SharedParams& p, cudaStream_t st) {
-    const int warps = block_warps(int64_t(p.n) * p.Hkv * p.row_tiles, kBlockWarps);
-    p.own_limit = warps * kOwnTiles;
+    const int64_t units = int64_t(p.n) * p.Hkv * p.row_tiles;
+    const int warps = block_warps(units, kBlockWarps);
+    p.own_limit = warps * (units >= kSms ? kOwnTilesOfMany : kOwnTiles);
     const cudaError_t e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads),
                                        WideGeometry<kD>::kSmemBytes, st, wide_k, wide_v, p);
     if (e != cudaSuccess) return e;
@@ -163,8 +186,12 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorM
 extern "C" size_t hk_attention_kv8_shared_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                          int64_t max_pages, int64_t G) {
     if (!shape_ok(cache, B, T, Hq, max_pages, G)) return 0;
-    if (on_its_own(cache, T, Hq)) return hk_attention_kv8_workspace_size(cache, B, T, Hq, max_pages);
-    return workspace(cache, B, T, Hq, G, G <= kWideGroups).total;
+    // (whatever the queries' type and alignment, and for every form that the flags ask for)
+    size_t own = 0;
+    for (int i = 0; i < 4; ++i)
+        if (choose(cache, B, T, Hq, max_pages, G, (i & 1) && G <= kWideGroups, i & 2) == kOwn)
+            own = hk_attention_kv8_workspace_size(cache, B, T, Hq, max_pages);
+    return std::max(own, T * (Hq / cache->heads) < kOwnTileRows ? workspace(cache, B, T, Hq, G, G <= kWideGroups).total : size_t(0));
 }
 
 extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
@@ -196,13 +223,17 @@ extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, con
     if (need > 0 && (!scratch || workspace_bytes < need))
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, scratch ? workspace_bytes : size_t(0));
     if (!aligned(scratch, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
-    if (on_its_own(cache, T, Hq))
-        return hk_attention_kv8_ex(Q, type, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse,
-                                   B, T, Hq, causal, scale, scratch, workspace_bytes, flags & ~kFormFlags, timeout_ns, stream);
     if ((flags & HK_KV8_MANY_ROWS) && !wide_can(Q, type, q_strides, G))
         return fail(HK_ERR_INVALID_ARG, "the tensor-core kernel takes bf16 queries with 16-byte aligned rows, and %d groups", kWideGroups);
-    const bool wide = flags & kFormFlags ? (flags & HK_KV8_MANY_ROWS) != 0
-                                         : wide_can(Q, type, q_strides, G) && wide_pays(cache, B, T, Hq, max_pages, G);
+    if ((flags & kFormFlags) && T * group >= kOwnTileRows)
+        return fail(HK_ERR_INVALID_ARG, "%lld query rows of a sequence and KV head: attention_kv8's", (long long)(T * group));
+    const Form form = flags & HK_KV8_MANY_ROWS ? kWide : flags & HK_KV8_FEW_ROWS ? kFew
+                                               : choose(cache, B, T, Hq, max_pages, G, wide_can(Q, type, q_strides, G),
+                                                        many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq));
+    if (form == kOwn)
+        return hk_attention_kv8_ex(Q, type, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse,
+                                   B, T, Hq, causal, scale, scratch, workspace_bytes, flags & ~kFormFlags, timeout_ns, stream);
+    const bool wide = form == kWide;
     const int64_t batch = launch_batch(B, T, Hq), row_tiles = ceil_div(T * group, kRows);
     // (tiles of one launch, at most: every sequence's own and every group's shared ones)
     const int64_t unit_tiles = ceil_div(max_pages * cache->page_size, kTileKeys);

@@ -125,4 +125,10 @@ inline int block_warps(int64_t units, int most) {
     return warps;
 }
 
+// hk_attention_kv8's form for many rows: can it run the call? And what that entry point takes per token of a sequence's
+// table, in millionths of a microsecond (hk_kv8.cu).
+bool many_rows_can(const void* Q, int32_t type, const int64_t q_strides[3], const void* O, const int64_t o_strides[3], int64_t B,
+                   int64_t T, int64_t Hq);
+double attention_cost(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, bool many_can);
+
 }  // namespace hk_kv8

@@ -605,18 +605,19 @@ hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, in
 /* Attention as hk_attention_kv8 for a batch whose sequences begin with the same tokens in the
  * same pages (hk_kv8_arrange forks them so): the shared pages are read once per group.
  * Group g < G is the sequences [groups[g], groups[g + 1]) of the batch (int32 [G + 1] on the device, from 0
- * to B, strictly increasing); the first shared[g] tokens (int32 [G] on the device) of each of them
- * lie in the pages that the table row of the group's first sequence names, as far as they fill whole blocks of
- * 128 tokens; what is left of them is read from each sequence's own table row. shared[g] = 0, and groups of one sequence,
- * are fine. The result is hk_attention_kv8's, but for the order of its fp32 sums. Not shared in
+ * to B, strictly increasing); the first shared[g] tokens (int32 [G] on the device) of each of them lie in the same pages,
+ * which every sequence's own table row names too. They are read once, by the first sequence's row, as far as they fill whole
+ * blocks of 128 tokens. shared[g] = 0, and groups of one sequence, are fine. The result is hk_attention_kv8's, but for the
+ * order of its fp32 sums (and the rounding of weights, below). Not shared in
  * fact, and read by a sequence itself, are tokens past the first sequence's length, and those of a
  * sequence that has queries which do not see all of them. Where groups are out of order or range, every sequence
  * reads all its tokens itself and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG.
- * Many query rows per group run on a tensor-core kernel for what is shared when Q is bf16 with rows that are
- * 16-byte aligned and there are up to 64 groups (weights rounded to bf16, 2^-8, before they meet V); else on the
- * few-row kernels. From 256 rows of each sequence and KV head on the call is hk_attention_kv8's.
- * `workspace`: device memory of hk_attention_kv8_shared_workspace_size bytes (up to 60 MB and 8 · head_dim bytes for
- * each of up to 2^17 query rows), 256-byte aligned. Everything else as hk_attention_kv8. */
+ * By the sizes that the host knows the call runs on a tensor-core kernel for what is shared (Q bf16 with rows that are
+ * 16-byte aligned, up to 64 groups; weights are rounded to bf16, 2^-8, before they meet V), on few-row kernels, or, where
+ * reading everything for each sequence costs less (few sequences, short tables, 1024 query rows of a sequence and KV head or
+ * more), as hk_attention_kv8, which does not look at the groups.
+ * `workspace`: device memory of hk_attention_kv8_shared_workspace_size bytes (up to 44 MB and 8 · head_dim bytes for
+ * each of up to 2^17 query rows, or what hk_attention_kv8 needs), 256-byte aligned. Everything else as hk_attention_kv8. */
 hk_status hk_attention_kv8_shared(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
                                   const int32_t* block_table, int64_t table_stride, int64_t max_pages,
                                   const int32_t* lengths, const int32_t* counts, const int32_t* groups,
@@ -625,7 +626,7 @@ hk_status hk_attention_kv8_shared(const void* Q, int32_t type, const int64_t q_s
                                   size_t workspace_bytes, void* stream);
 
 /* The same with test controls. `flags`: HK_KV8_FEW_ROWS (units of 16 query rows) or HK_KV8_MANY_ROWS (what is shared
- * in units of 128 rows on the tensor-core kernel; refused for what it does not take), 0: chosen by shape;
+ * in units of 128 rows on the tensor-core kernel); each is refused for what it does not take. 0: chosen by shape;
  * HK_KV8_FAULT_DROP_ARRIVE. `timeout_ns` bounds each wait (0: 1 s). */
 hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
                                      const int32_t* block_table, int64_t table_stride, int64_t max_pages,

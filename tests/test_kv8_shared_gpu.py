@@ -27,7 +27,7 @@ def _possible(form, dtype="bf16", groups=1):
 
 def _i32(x):
     import torch
-    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    return x if isinstance(x, torch.Tensor) else torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
 
 
 class Batch:
@@ -113,7 +113,7 @@ def _strides(t):
 
 
 def _attend(batch, q, counts=None, causal=True, scale=0.0, form=0, out=None, fill=0xFF, flags=0, timeout_ns=0, shared=None,
-            offsets=None, lengths=None):
+            offsets=None, lengths=None, wait=True):
     """(o, lse) through the entry point with controls; the workspace is full of `fill` before."""
     import torch
     import dense_bf16_gemm_02_gb300 as hk
@@ -131,7 +131,8 @@ def _attend(batch, q, counts=None, causal=True, scale=0.0, form=0, out=None, fil
         offsets.data_ptr(), shared.data_ptr(), len(shared), out.data_ptr(), _strides(out), lse.data_ptr(), B, T, Hq,
         1 if causal else 0, scale, workspace.data_ptr(), size, form | flags, timeout_ns, torch.cuda.current_stream().cuda_stream)
     assert st == hk.HK_OK, hk.hk_gemm_last_error_string()
-    torch.cuda.synchronize()
+    if wait:
+        torch.cuda.synchronize()
     return out, lse
 
 
@@ -341,30 +342,55 @@ def test_repeats_exactly_on_streams_and_in_graphs(form):
     for fill in (0, 0x7F, 0xFF):
         b, lb = _attend(batch, q, form=form, fill=fill)
         assert torch.equal(a, b) and torch.equal(la, lb)
-    args = (q, batch.cache, batch.table, _i32(batch.lengths), _i32(batch.offsets), _i32(batch.shared))
-    a, la = hk.attention_kv8_shared(*args, return_lse=True)
+    n, offsets, shared = _i32(batch.lengths), _i32(batch.offsets), _i32(batch.shared)
+    same = dict(form=form, lengths=n, offsets=offsets, shared=shared, wait=False)
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
-    out = torch.empty_like(q)
-    c = hk.attention_kv8_shared(*args, stream=stream, out=out)
+    with torch.cuda.stream(stream):
+        c, _ = _attend(batch, q, **same)
     stream.synchronize()
-    assert c is out and torch.equal(a, c)
+    assert torch.equal(a, c)
     graphs = []
     for _ in range(2):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            d, ld = hk.attention_kv8_shared(*args, return_lse=True)
-        graphs.append((graph, d, ld))
+            got = _attend(batch, q, **same)
+        graphs.append((graph, *got))
     for graph, _, _ in graphs:
         graph.replay()
     for _, d, ld in graphs:
         assert torch.equal(a, d) and torch.equal(la, ld)
     # other lengths and another sharing in the captured call: all of it is read on the device
-    args[3][0] = 1800
-    args[5][0] = 1000
+    n[0] = 1800
+    shared[0] = 1000
     graphs[0][0].replay()
     batch.lengths[0] = 1800
     _check(batch, q, graphs[0][1:], form=form)
+    assert _status() == hk.HK_OK
+
+
+def test_python_on_streams_and_in_graphs():
+    """A size that each form takes by itself."""
+    import torch
+    import dense_bf16_gemm_02_gb300 as hk
+    for groups, H, group, D in (([(200, [5, 9])], 2, 4, 64), ([(2000, [3] * 64)], 4, 1, 64), ([(6000, [40] * 48)], 8, 8, 128)):
+        batch = Batch(groups, H, D, 64)
+        q = _q(batch.B, 1, H * group, D)
+        args = (q, batch.cache, batch.table, _i32(batch.lengths), _i32(batch.offsets), _i32(batch.shared))
+        a, la = hk.attention_kv8_shared(*args, return_lse=True)
+        _check(batch, q, (a, la))
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        out = torch.empty_like(q)
+        c = hk.attention_kv8_shared(*args, stream=stream, out=out)
+        stream.synchronize()
+        assert c is out and torch.equal(a, c)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            d, ld = hk.attention_kv8_shared(*args, return_lse=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, d) and torch.equal(la, ld)
     assert _status() == hk.HK_OK
 
 
@@ -381,21 +407,33 @@ def test_an_arrival_that_never_comes_is_reported(form, D):
     _check(batch, q, _attend(batch, q, form=form), form=form)
 
 
-@pytest.mark.parametrize("T,dtype", [(40, "bf16"), (40, "fp16"), (257, "bf16")])
-def test_many_queries_of_each_sequence(T, dtype):
-    """From 256 query rows of a KV head on, the call is attention_kv8's."""
+@FORMS
+@pytest.mark.parametrize("T,group,dtype", [(40, 8, "bf16"), (63, 16, "bf16"), (40, 8, "fp16"), (341, 3, "bf16")])
+def test_many_queries_of_each_sequence(form, T, group, dtype):
+    _possible(form, dtype)
+    batch = Batch([(1300, [T, T + 9, T + 100]), (500, [T, T + 1])], 2, 64, 32)
+    q = _q(batch.B, T, 2 * group, 64, dtype)
+    _check(batch, q, _attend(batch, q, form=form), form=form)
+    counts = [T, 1, T // 2, 0, T - 1]
+    _check(batch, q, _attend(batch, q, counts, form=form), counts, form=form)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("T,dtype,tokens", [(1, "bf16", 300), (1, "fp16", 300), (128, "bf16", 300), (128, "fp16", 300)])
+def test_small_calls_and_many_queries_are_attention_kv8s(T, dtype, tokens):
+    """Where reading everything again costs less than joining, and from 1024 rows of a sequence and KV head on."""
     import torch
     import dense_bf16_gemm_02_gb300 as hk
-    batch = Batch([(300, [T, T + 9])], 1, 64, 32)
+    batch = Batch([(tokens, [T, T + 9])], 1, 64, 32)
     q = _q(batch.B, T, 8, 64, dtype)
     got = _attend(batch, q)
     _check(batch, q, got)
-    if T * 8 >= 256:
-        o, lse = hk.attention_kv8(q, batch.cache, batch.table, _i32(batch.lengths), return_lse=True)
-        assert torch.equal(o, got[0]) and torch.equal(lse, got[1])
+    o, lse = hk.attention_kv8(q, batch.cache, batch.table, _i32(batch.lengths), return_lse=True)
+    assert torch.equal(o, got[0]) and torch.equal(lse, got[1])
 
 
-def test_cache_beyond_32_bit_offsets():
+@FORMS
+def test_cache_beyond_32_bit_offsets(form):
     import torch
     import dense_bf16_gemm_02_gb300 as hk
     small = Batch([(1024, [40, 9, 100])], 8, 128, 128, scales=(0.0625,))
@@ -405,10 +443,10 @@ def test_cache_beyond_32_bit_offsets():
     for a, b in zip((small.cache.k, small.cache.v, small.cache.k_scale, small.cache.v_scale), (big.k, big.v, big.k_scale, big.v_scale)):
         b[move:] = a
     q = _q(small.B, 1, 64, 128)
-    want = _attend(small, q)
+    want = _attend(small, q, form=form)
     small.cache, small.table = big, torch.where(small.table >= 0, small.table + move, small.table)
     small.np_table = np.where(small.np_table >= 0, small.np_table + move, small.np_table)
-    got = _attend(small, q)
+    got = _attend(small, q, form=form)
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
