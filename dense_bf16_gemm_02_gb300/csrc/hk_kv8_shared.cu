@@ -148,15 +148,24 @@ cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const Share
                         dim3(32 * kWarps), BlockGeometry<kD, kWarps>::kSmemBytes, st, tk, tv, p);
 }
 
-// The shared units on the tensor cores (a run of blocks to every SM), then the sequences' own ones.
+template <int kD, typename T>
+cudaError_t launch_spread(const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p, cudaStream_t st) {
+    return launch_early(&kv8_shared_kernel<kD, T>, dim3(static_cast<unsigned>(p.warps / kDecodeWarps)), dim3(32 * kDecodeWarps),
+                        SharedGeometry<kD>::kSmemBytes, st, tk, tv, p);
+}
+
+// Long own parts over the GPU, the shared units on the tensor cores (a run of blocks to every SM), then the other own parts
+// and the output: the last of them beside the last of the shared units, whose SMs do not all end at a time.
 template <int kD>
 cudaError_t launch_wide(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
                         SharedParams& p, cudaStream_t st) {
     const int64_t units = int64_t(p.n) * p.Hkv * p.row_tiles;
     const int warps = block_warps(units, kBlockWarps);
     p.own_limit = warps * (units >= kSms ? kOwnTilesOfMany : kOwnTiles);
-    const cudaError_t e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads),
-                                       WideGeometry<kD>::kSmemBytes, st, wide_k, wide_v, p);
+    cudaError_t e = launch_spread<kD, __nv_bfloat16>(tk, tv, p, st);
+    if (e == cudaSuccess)
+        e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads),
+                         WideGeometry<kD>::kSmemBytes, st, wide_k, wide_v, p);
     if (e != cudaSuccess) return e;
     switch (warps) {
         case 1: return launch_own<kD, 1>(tk, tv, p, st);
@@ -169,11 +178,8 @@ cudaError_t launch_wide(const CUtensorMap& tk, const CUtensorMap& tv, const CUte
 template <int kD, typename T>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
                    SharedParams p, cudaStream_t st) {
-    cudaError_t e = cudaSuccess;
-    if (p.wide_runs > 0) e = launch_wide<kD>(tk, tv, wide_k, wide_v, p, st);
-    if (e != cudaSuccess) return e;
-    e = launch_early(&kv8_shared_kernel<kD, T>, dim3(static_cast<unsigned>(p.warps / kDecodeWarps)), dim3(32 * kDecodeWarps),
-                                 SharedGeometry<kD>::kSmemBytes, st, tk, tv, p);
+    if (p.wide_runs > 0) return launch_wide<kD>(tk, tv, wide_k, wide_v, p, st);
+    const cudaError_t e = launch_spread<kD, T>(tk, tv, p, st);
     if (e != cudaSuccess) return e;
     const int64_t rows = int64_t(p.n) * p.T * p.Hq;
     const int split = rows <= 16 * kSms ? 8 : rows <= 64 * kSms ? 2 : 1;       // (as many warps as are resident at a time)

@@ -64,7 +64,8 @@ struct Group {
 
 __device__ __forceinline__ int shared_rows(const SharedParams& p, int n) { return n * p.T * p.group; }
 
-// Where the shared units of the group in place `j` with first sequence `first` begin in shared_info.
+// Where the shared units of the group in place `j` (of the launch's groups; for units of 128 rows, of all) with first sequence
+// `first` begin in shared_info.
 __device__ __forceinline__ int shared_unit0(const SharedParams& p, int j, int first) { return shared_rows(p, first) / kRows + j; }
 
 // Tokens that the first query of a sequence sees (the fewest of its queries).
@@ -203,7 +204,7 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     const uint32_t g = lane >> 2, c = lane & 3u;
     const int self = static_cast<int>(blockIdx.x) * kDecodeWarps + static_cast<int>(warp);
 
-    griddep_launch_dependents();             // the combining kernel may be scheduled; it waits for this grid's end
+    griddep_launch_dependents();             // the next kernel may be scheduled; it waits for this grid's end
     if (threadIdx.x == 0) {
         prefetch_tensor_map(&tmap_k);
         prefetch_tensor_map(&tmap_v);
@@ -214,9 +215,7 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         for (int s = 0; s < G::kStages; ++s) mbar_init(bars + 8u * s, s == 0 && (p.flags & kFlagDropArrive) ? 2 : 1);
         fence_mbar_init_cluster();
     }
-    // launched early behind the kernel that may have written the cache or q; or behind the one for the shared units, beside which
-    // it may run (that one began when the kernels before it had ended), and for whose end it waits at its own
-    if (p.wide_runs == 0) griddep_wait();
+    griddep_wait();                          // launched early behind the kernel that may have written the cache or q
     int32_t* const prefix = reinterpret_cast<int32_t*>(smem + S::kOffPrefix);
     int32_t* const first_of = reinterpret_cast<int32_t*>(smem + S::kOffGroups);
     int32_t* const tiles_of_group = reinterpret_cast<int32_t*>(smem + S::kOffShared);
@@ -347,11 +346,124 @@ kv8_shared_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     // abort: the copies in flight land before the block ends
     if (!ok)
         for (; uses < fills; ++uses) wait_mbar_drain(bars + 8u * (uses % G::kStages), (uses / G::kStages) & 1);
-    if (p.wide_runs > 0) griddep_wait();
 }
 
-// A sequence's own part, a block to a unit (of up to own_limit tiles), whose warps share the tiles out and join their sums in
-// shared memory. For up to 64 groups, beside the tensor-core kernel (see there for the waits).
+// Sums in memory that make up 16 rows of a sequence and KV head: those of its own part, where the spreading kernel left it, and
+// those of the stacked rows' units of 128, of which the 16 rows may lie in two.
+struct RowParts {
+    const SharedParams& p;
+    int64_t out_row0;              // of the launch, of query token 0 and the KV head's first query head
+    int row0;                      // rt * 16
+    int4 own;                      // record of the own part; own_parts 0: it is in shared memory
+    int own_parts;
+    int4 shared0, shared1;         // records of the stacked rows' units, the second from row `cut` on
+    int cut, stacked0;             // stacked row of row 0; -1: nothing shared
+
+    __device__ __forceinline__ int4 unit(int r) const {
+        const bool before = r < cut;
+        return make_int4(before ? shared0.x : shared1.x, before ? shared0.y : shared1.y, before ? shared0.z : shared1.z, 0);
+    }
+    __device__ __forceinline__ int64_t out_row(int r) const {
+        const int row = row0 + r, t = row / p.group;
+        return out_row0 + static_cast<int64_t>(t) * p.Hq + (row - t * p.group);
+    }
+    __device__ __forceinline__ int parts(int r) const { return own_parts + (stacked0 >= 0 ? max(unit(r).x, 1) : 0); }
+    // The row of part_o and part_ml of part k.
+    __device__ __forceinline__ int64_t at(int r, int k) const {
+        const bool mine = k < own_parts;
+        const int4 u = unit(r);
+        const int4 x = make_int4(mine ? own.x : u.x, mine ? own.y : u.y, mine ? own.z : u.z, 0);
+        if (x.x == 0) return (mine ? p.whole[1] : p.whole[0]) + out_row(r);
+        const int part = mine ? k : k - own_parts;
+        const int64_t slot = part == 0 ? static_cast<int64_t>(x.y) : 2 * (static_cast<int64_t>(x.z) + part);
+        return mine ? slot * kRows + r : p.shared_slots + slot * kWideRows + (stacked0 + r) % kWideRows;
+    }
+};
+
+// Adds parts k = warp, warp + kWarps, ... of each of the first `rows` rows to what the warp holds of them: sums in
+// shared memory at `part` (rows of four times kPitch), maxima and sums in `ml`. Four rows and four parts at a time, since
+// each trip to memory takes longer than what is done with what it brings.
+template <int kD, int kWarps, int kPitch>
+__device__ __forceinline__ void add_parts(const RowParts& in, int rows, int warp, float* part, float (*ml)[2]) {
+    constexpr int kVec = kD / 32, kAtATime = 4;
+    const int lane = static_cast<int>(lane_id());
+    const SharedParams& p = in.p;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kAtATime) {
+        float acc[kAtATime][kVec], m[kAtATime], l[kAtATime];
+        int n[kAtATime], most = 0;
+#pragma unroll
+        for (int q = 0; q < kAtATime; ++q) {
+            const int r = min(r0 + q, rows - 1);
+            n[q] = in.parts(r);
+            most = max(most, n[q]);
+            m[q] = ml[r][0];
+            l[q] = ml[r][1];
+            const bool have = m[q] > -INFINITY || l[q] != 0.0f;      // (else nothing has been written at `part`)
+            const float* const src = part + (r * 4 + lane / 8) * kPitch + lane % 8 * kVec;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) acc[q][v] = have ? src[v] : 0.0f;
+        }
+#pragma unroll 1
+        for (int k0 = warp; k0 < most; k0 += kAtATime * kWarps) {
+            float2 f[kAtATime][kAtATime];
+            float x[kAtATime][kAtATime][kVec];
+#pragma unroll
+            for (int u = 0; u < kAtATime; ++u)
+#pragma unroll
+                for (int q = 0; q < kAtATime; ++q) {
+                    if (k0 + u * kWarps >= most) continue;
+                    const int64_t a = in.at(min(r0 + q, rows - 1), min(k0 + u * kWarps, n[q] - 1));
+                    f[u][q] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
+                    if constexpr (kVec == 4) {
+                        const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * kD) + lane);
+                        x[u][q][0] = o.x; x[u][q][1] = o.y; x[u][q][2] = o.z; x[u][q][3] = o.w;
+                    } else {
+                        const float2 o = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * kD) + lane);
+                        x[u][q][0] = o.x; x[u][q][1] = o.y;
+                    }
+                }
+#pragma unroll
+            for (int q = 0; q < kAtATime; ++q) {
+                float top = m[q];
+#pragma unroll
+                for (int u = 0; u < kAtATime; ++u)
+                    if (k0 + u * kWarps < n[q]) top = fmaxf(top, f[u][q].x);
+                // (a maximum of -inf has a sum of 0, or of NaN, which stays one)
+                const float before = m[q] == -INFINITY ? 1.0f : ex2_approx(m[q] - top);
+                m[q] = top;
+                l[q] *= before;
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) acc[q][v] *= before;
+#pragma unroll
+                for (int u = 0; u < kAtATime; ++u) {
+                    if (k0 + u * kWarps >= n[q]) continue;
+                    const float weight = f[u][q].x == -INFINITY ? 0.0f : ex2_approx(f[u][q].x - top);
+                    l[q] += f[u][q].x == -INFINITY ? f[u][q].y : f[u][q].y * weight;
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v) acc[q][v] += x[u][q][v] * weight;
+                }
+            }
+        }
+        __syncwarp();                        // every lane has read the rows' sums
+#pragma unroll
+        for (int q = 0; q < kAtATime; ++q) {
+            if (r0 + q >= rows) break;
+            float* const dst = part + ((r0 + q) * 4 + lane / 8) * kPitch + lane % 8 * kVec;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) dst[v] = acc[q][v];
+            if (lane == 0) {
+                ml[r0 + q][0] = m[q];
+                ml[r0 + q][1] = l[q];
+            }
+        }
+    }
+}
+
+// What a sequence has of its own, and its output, a block to a unit, beside the tensor-core kernel (for up to 64 groups; see
+// there for the waits): the warps share out the tiles of an own part of up to own_limit, and then the sums that the
+// tensor-core kernel left of its rows (and those of a longer own part, which the first kernel has spread over the GPU), and join theirs in shared memory. A kernel for the joining alone, with the own parts' sums through memory, made a call
+// for 64 sequences behind 16384 tokens 81 us instead of 78, for 16 of 4 queries behind 8192 53 instead of 47.
 template <int kD, typename T, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, kBlockWarps / kWarps)
 kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
@@ -379,8 +491,8 @@ kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
     const int rt = unit % p.row_tiles;
     unit /= p.row_tiles;
     const int h = unit % p.Hkv, i = unit / p.Hkv, b = p.b0 + i;
-    // ---- where the sequence's own part begins: its group is one lane's
-    int start = 0;
+    // ---- where the sequence's own part begins, and where its stacked rows lie: its group is one lane's
+    int start = 0, place = 0, first_of = 0;
     const Sequence seq = sequence(p, b);
     {
         int shared = 0, of = -1;
@@ -393,6 +505,7 @@ kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             if (first <= b && b < next) {
                 shared = tokens;
                 of = first;
+                place = j;
             }
         }
         const uint32_t who = __ballot_sync(0xffffffffu, of >= 0);
@@ -400,22 +513,24 @@ kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             const int from = __ffs(static_cast<int>(who)) - 1;
             of = __shfl_sync(0xffffffffu, of, from);
             shared = __shfl_sync(0xffffffffu, shared, from);
+            place = __shfl_sync(0xffffffffu, place, from);
+            first_of = max(of - p.b0, 0);
             start = own_start(p, seq, shared_tiles(p, shared, p.lengths[of]));
         }
     }
     const int key_end = row_tile_end(p, seq, rt);
     const int tiles = own_tiles(key_end, start);
     const bool mine = tiles <= p.own_limit;
+    float* const part = reinterpret_cast<float*>(smem + warp * G::kWarpBytes);
     bool ok = true;
-    if (mine) {
+    {
         float o[kD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         const int first = start + static_cast<int>(warp) * tiles / kWarps, last = start + static_cast<int>(warp + 1) * tiles / kWarps;
-        if (first < last && key_end > start * kTileKeys) {
+        if (mine && first < last && key_end > start * kTileKeys) {
             int fills = 0, uses = 0;
             ok = attend<kD, T, G::kStages>(p, &tmap_k, &tmap_v, ring, bars, fills, uses, UnitRows{p, b, h, rt, seq}, h, key_end, first, last,
                                            o, m, l);
             if (ok) {
-                float* const part = reinterpret_cast<float*>(smem + warp * G::kWarpBytes);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float4* const dst = reinterpret_cast<float4*>(part + ((g + 8 * e) * 4 + c) * B::kPitch);
@@ -437,14 +552,35 @@ kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                 warp_ml[warp][g + 8 * e][1] = ok ? l[e] : 0.0f;
             }
         }
+        __syncwarp();
+    }
+    // ---- what the kernels before left of these rows
+    griddep_wait();                          // (this grid may have run beside those before it)
+    const int live = min(max(seq.count * p.group - rt * kRows, 0), kRows);       // rows that are queries
+    int4 own = make_int4(0, 0, 0, 0);
+    if (!mine) own = __ldcg(p.info + (static_cast<int64_t>(i) * p.Hkv + h) * p.row_tiles + rt);      // (past L1: written meanwhile)
+    const bool finished = !mine && start == 0 && own.x == 0;
+    if (ok && live > 0 && (start > 0 || !mine) && !finished) {
+        const int stacked0 = start > 0 ? shared_rows(p, i - first_of) + rt * kRows : -1;
+        RowParts in = {p, static_cast<int64_t>(i) * p.T * p.Hq + h * p.group, rt * kRows, own, mine ? 0 : max(own.x, 1),
+                       make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0), kRows, stacked0};
+        if (start > 0) {
+            const int4* const records = p.shared_info + static_cast<int64_t>(h) * p.shared_units + shared_unit0(p, place, first_of);
+            in.shared0 = __ldcg(records + stacked0 / kWideRows);
+            in.shared1 = __ldcg(records + (stacked0 + live - 1) / kWideRows);
+            in.cut = kWideRows - stacked0 % kWideRows;
+        }
+        // (a launch whose waits gave up leaves records unwritten: what they hold is no place to read from)
+        auto wrong = [&](const int4& x, int runs) { return x.x < 0 || (x.x > 0 && (x.y < 0 || x.y >= 2 * runs || x.z < 0 || x.x > runs - x.z)); };
+        if (wrong(own, p.warps) || wrong(in.shared0, p.wide_runs) || wrong(in.shared1, p.wide_runs)) ok = false;
+        else add_parts<kD, kWarps, B::kPitch>(in, live, static_cast<int>(warp), part, warp_ml[warp]);
     }
     ok = !__syncthreads_or(!ok);
-    if (mine && threadIdx.x == 0) p.info[(static_cast<int64_t>(i) * p.Hkv + h) * p.row_tiles + rt] = make_int4(0, 0, 0, 0);
     // 16 threads per row, kD / 16 columns each
     constexpr int kCols = kD / 16;
     const int col = static_cast<int>(threadIdx.x & 15u) * kCols;
 #pragma unroll 1
-    for (int r = static_cast<int>(threadIdx.x >> 4); mine && ok && r < kRows; r += 2 * kWarps) {
+    for (int r = static_cast<int>(threadIdx.x >> 4); !finished && ok && r < kRows; r += 2 * kWarps) {
         const int row = rt * kRows + r;
         const int t = row / p.group, head = h * p.group + row % p.group;
         if (t >= p.T) break;
@@ -460,34 +596,20 @@ kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             if (mw > -INFINITY || lw != 0.0f) {  // (a row that a warp's tokens are all hidden from has left zeros)
                 const float weight = ex2_approx(mw - m);
                 l += lw * weight;
-                const float* const part =
+                const float* const src =
                     reinterpret_cast<const float*>(smem + w * G::kWarpBytes) + (r * 4 + col / B::kOwn) * B::kPitch + col % B::kOwn;
 #pragma unroll
-                for (int k = 0; k < kCols; ++k) acc[k] += part[k] * weight;
+                for (int k = 0; k < kCols; ++k) acc[k] += src[k] * weight;
             }
         }
-        const bool any = l > 0.0f || l != l;
-        const int64_t out_row = (static_cast<int64_t>(i) * p.T + t) * p.Hq + head;     // of the launch
-        if (start > 0) {
-            const int64_t at_row = p.whole[1] + out_row;
-            float4* const dst = reinterpret_cast<float4*>(p.part_o + at_row * kD + col);
+        const bool any = r < live && (l > 0.0f || l != l);
+        const float mul = any ? 1.0f / l : 0.0f;
+        T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + col;
 #pragma unroll
-            for (int k = 0; k < kCols / 4; ++k)
-                dst[k] = make_float4(any ? acc[4 * k] : 0.0f, any ? acc[4 * k + 1] : 0.0f, any ? acc[4 * k + 2] : 0.0f, any ? acc[4 * k + 3] : 0.0f);
-            if (col == 0) {
-                p.part_ml[2 * at_row] = any ? m : -INFINITY;
-                p.part_ml[2 * at_row + 1] = any ? l : 0.0f;
-            }
-        } else {
-            const float mul = any ? 1.0f / l : 0.0f;
-            T* const dst = static_cast<T*>(p.o) + b * p.o_stride_b + t * p.o_stride_t + head * p.o_stride_h + col;
-#pragma unroll
-            for (int k = 0; k < kCols; ++k) dst[k] = from_float<T>(any ? acc[k] * mul : 0.0f);
-            if (p.lse != nullptr && col == 0)
-                p.lse[static_cast<int64_t>(p.b0) * p.T * p.Hq + out_row] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        }
+        for (int k = 0; k < kCols; ++k) dst[k] = from_float<T>(any ? acc[k] * mul : 0.0f);
+        if (p.lse != nullptr && col == 0)
+            p.lse[(static_cast<int64_t>(b) * p.T + t) * p.Hq + head] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
-    griddep_wait();                          // (this grid may have run beside the one before it: its end is that one's too)
 }
 
 // Adds up what the kernels above left: kSplit warps of a block to a row (eight where there are few rows, of many parts each),
@@ -513,16 +635,15 @@ kv8_shared_combine_kernel(const SharedParams p) {
     const int4 own = __ldcg(p.info + (static_cast<int64_t>(i) * p.Hkv + h) * p.row_tiles + row / kRows);
     int4 shared = make_int4(0, 0, 0, 0);
     int shared_row = 0;
-    const int unit_rows = p.wide_runs > 0 ? kWideRows : kRows;
     if (seq.x > 0) {
         shared_row = shared_rows(p, i - seq.z) + row;
-        shared = __ldcg(p.shared_info + static_cast<int64_t>(h) * p.shared_units + shared_unit0(p, seq.y, seq.z) + shared_row / unit_rows);
+        shared = __ldcg(p.shared_info + static_cast<int64_t>(h) * p.shared_units + shared_unit0(p, seq.y, seq.z) + shared_row / kRows);
     } else if (own.x == 0) {
         return;                              // finished
     }
     // (a launch whose waits gave up leaves records unwritten: what they hold is no place to read from)
-    auto wrong = [&](const int4& x, int runs) { return x.x < 0 || (x.x > 0 && (x.y < 0 || x.y >= 2 * runs || x.z < 0 || x.x > runs - x.z)); };
-    if (wrong(own, p.warps) || wrong(shared, p.wide_runs > 0 ? p.wide_runs : p.warps)) return;
+    auto wrong = [&](const int4& x) { return x.x < 0 || (x.x > 0 && (x.y < 0 || x.y >= 2 * p.warps || x.z < 0 || x.x > p.warps - x.z)); };
+    if (wrong(own) || wrong(shared)) return;
     const int first_parts = seq.x > 0 ? max(shared.x, 1) : 0, parts = first_parts + max(own.x, 1);
     auto row_of = [&](int k) {
         const bool of_shared = k < first_parts;
@@ -530,7 +651,6 @@ kv8_shared_combine_kernel(const SharedParams p) {
         const int part = of_shared ? k : k - first_parts;
         if (x.x == 0) return p.whole[of_shared ? 0 : 1] + out_row;
         const int64_t slot = part == 0 ? static_cast<int64_t>(x.y) : 2 * (static_cast<int64_t>(x.z) + part);
-        if (of_shared && p.wide_runs > 0) return p.shared_slots + slot * kWideRows + shared_row % kWideRows;
         return slot * kRows + (of_shared ? shared_row : row) % kRows;
     };
     float m = -INFINITY, l = 0.0f, acc[kVec];

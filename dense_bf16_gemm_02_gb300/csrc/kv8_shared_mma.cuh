@@ -207,7 +207,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
         tmem_alloc_one(tmem_holder, W::kTmemCols);
         tmem_relinquish_one();
     }
-    griddep_wait();                            // launched early behind the kernel that may have written the cache or q
+    griddep_wait();                            // launched early behind the spreading kernel, which waits for what wrote the cache or q
     griddep_launch_dependents();               // (now: what follows on the stream may run beside this grid, see launch())
     // ---- the groups' blocks; the CTA's run
     {

@@ -252,9 +252,11 @@ def test_many_sequences_and_groups(form):
     assert batch.B > 1024 and len(groups) > 512
     _check(batch, q, _attend(batch, q, form=form & FEW), form=FEW)
     assert _status() == 0
-    batch = Batch([(640, [3] * 700)], 1, 64, 64)
-    q = _q(batch.B, 1, 2, 64)
-    _check(batch, q, _attend(batch, q, form=form), form=form)
+    for groups in ([(640, [3] * 700)], [(640, [3] * 300), (0, [9]), (300, [7] * 280), (400, [5, 2500] * 60)]):
+        batch = Batch(groups, 1, 64, 64)
+        q = _q(batch.B, 1, 2, 64)
+        _check(batch, q, _attend(batch, q, form=form), form=form)
+    assert _status() == 0
 
 
 @FORMS
