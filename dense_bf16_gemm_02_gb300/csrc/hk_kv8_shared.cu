@@ -23,9 +23,9 @@ using namespace hk_kv8;
 std::mutex g_setup_mutex;
 bool g_setup[kMaxDevices] = {};
 
-template <int kD, int kWarps>
+template <int kD, typename T, int kWarps>
 cudaError_t setup_own() {
-    return cudaFuncSetAttribute(kv8_own_kernel<kD, __nv_bfloat16, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kv8_own_kernel<kD, T, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 BlockGeometry<kD, kWarps>::kSmemBytes);
 }
 
@@ -35,17 +35,17 @@ cudaError_t setup_one() {
 }
 
 // (a split of registers that adds up to more than the launch has would wait for ever)
-template <int kD>
+template <int kD, typename T>
 cudaError_t setup_wide() {
     cudaFuncAttributes a;
-    cudaError_t e = cudaFuncGetAttributes(&a, kv8_shared_mma_kernel<kD>);
+    cudaError_t e = cudaFuncGetAttributes(&a, kv8_shared_mma_kernel<kD, T>);
     if (e == cudaSuccess && a.numRegs * kWideThreads < kWideRegisters) e = cudaErrorLaunchOutOfResources;
-    if (e == cudaSuccess) e = setup_own<kD, 1>();
-    if (e == cudaSuccess) e = setup_own<kD, 2>();
-    if (e == cudaSuccess) e = setup_own<kD, 4>();
-    if (e == cudaSuccess) e = setup_own<kD, 8>();
+    if (e == cudaSuccess) e = setup_own<kD, T, 1>();
+    if (e == cudaSuccess) e = setup_own<kD, T, 2>();
+    if (e == cudaSuccess) e = setup_own<kD, T, 4>();
+    if (e == cudaSuccess) e = setup_own<kD, T, 8>();
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kv8_shared_mma_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideGeometry<kD>::kSmemBytes);
+        e = cudaFuncSetAttribute(kv8_shared_mma_kernel<kD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideGeometry<kD>::kSmemBytes);
     return e;
 }
 
@@ -56,8 +56,10 @@ hk_status setup(int device) {
     if (e == cudaSuccess) e = setup_one<64, __half>();
     if (e == cudaSuccess) e = setup_one<128, __nv_bfloat16>();
     if (e == cudaSuccess) e = setup_one<128, __half>();
-    if (e == cudaSuccess) e = setup_wide<64>();
-    if (e == cudaSuccess) e = setup_wide<128>();
+    if (e == cudaSuccess) e = setup_wide<64, __nv_bfloat16>();
+    if (e == cudaSuccess) e = setup_wide<64, __half>();
+    if (e == cudaSuccess) e = setup_wide<128, __nv_bfloat16>();
+    if (e == cudaSuccess) e = setup_wide<128, __half>();
     if (e != cudaSuccess) return cuda_fail(HK_ERR_CUDA, "configuring the shared attention kernels", e);
     g_setup[device] = true;
     return HK_OK;
@@ -77,9 +79,9 @@ int64_t launch_batch(int64_t B, int64_t T, int64_t Hq) {
 
 constexpr uint32_t kFormFlags = HK_KV8_FEW_ROWS | HK_KV8_MANY_ROWS;
 
-// Can the tensor-core kernel take the shared units? It reads 16-byte aligned bf16 rows and holds so many groups.
-bool wide_can(const void* Q, int32_t type, const int64_t q_strides[3], int64_t G) {
-    return type == HK_TYPE_BF16 && rows_aligned(Q, q_strides) && G <= kWideGroups;
+// Can the tensor-core kernel take the shared units? It reads 16-byte aligned rows and holds so many groups.
+bool wide_can(const void* Q, const int64_t q_strides[3], int64_t G) {
+    return rows_aligned(Q, q_strides) && G <= kWideGroups;
 }
 
 // Who takes the call: attention_kv8 (every sequence reads all its tokens), the few-row kernels, or the tensor-core
@@ -142,9 +144,9 @@ bool shape_ok(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t m
            Hq <= kLimit && Hq % c->heads == 0 && T <= kLimit / 16 / (Hq / c->heads) && G > 0 && G <= B;
 }
 
-template <int kD, int kWarps>
+template <int kD, typename T, int kWarps>
 cudaError_t launch_own(const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p, cudaStream_t st) {
-    return launch_early(&kv8_own_kernel<kD, __nv_bfloat16, kWarps>, dim3(static_cast<unsigned>(int64_t(p.n) * p.Hkv * p.row_tiles)),
+    return launch_early(&kv8_own_kernel<kD, T, kWarps>, dim3(static_cast<unsigned>(int64_t(p.n) * p.Hkv * p.row_tiles)),
                         dim3(32 * kWarps), BlockGeometry<kD, kWarps>::kSmemBytes, st, tk, tv, p);
 }
 
@@ -156,29 +158,29 @@ cudaError_t launch_spread(const CUtensorMap& tk, const CUtensorMap& tv, const Sh
 
 // Long own parts over the GPU, the shared units on the tensor cores (a run of blocks to every SM), then the other own parts
 // and the output: the last of them beside the last of the shared units, whose SMs do not all end at a time.
-template <int kD>
+template <int kD, typename T>
 cudaError_t launch_wide(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
                         SharedParams& p, cudaStream_t st) {
     const int64_t units = int64_t(p.n) * p.Hkv * p.row_tiles;
     const int warps = block_warps(units, kBlockWarps);
     p.own_limit = warps * (units >= kSms ? kOwnTilesOfMany : kOwnTiles);
-    cudaError_t e = launch_spread<kD, __nv_bfloat16>(tk, tv, p, st);
+    cudaError_t e = launch_spread<kD, T>(tk, tv, p, st);
     if (e == cudaSuccess)
-        e = launch_early(&kv8_shared_mma_kernel<kD>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads),
+        e = launch_early(&kv8_shared_mma_kernel<kD, T>, dim3(static_cast<unsigned>(p.wide_runs)), dim3(kWideThreads),
                          WideGeometry<kD>::kSmemBytes, st, wide_k, wide_v, p);
     if (e != cudaSuccess) return e;
     switch (warps) {
-        case 1: return launch_own<kD, 1>(tk, tv, p, st);
-        case 2: return launch_own<kD, 2>(tk, tv, p, st);
-        case 4: return launch_own<kD, 4>(tk, tv, p, st);
-        default: return launch_own<kD, 8>(tk, tv, p, st);
+        case 1: return launch_own<kD, T, 1>(tk, tv, p, st);
+        case 2: return launch_own<kD, T, 2>(tk, tv, p, st);
+        case 4: return launch_own<kD, T, 4>(tk, tv, p, st);
+        default: return launch_own<kD, T, 8>(tk, tv, p, st);
     }
 }
 
 template <int kD, typename T>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& wide_k, const CUtensorMap& wide_v,
                    SharedParams p, cudaStream_t st) {
-    if (p.wide_runs > 0) return launch_wide<kD>(tk, tv, wide_k, wide_v, p, st);
+    if (p.wide_runs > 0) return launch_wide<kD, T>(tk, tv, wide_k, wide_v, p, st);
     const cudaError_t e = launch_spread<kD, T>(tk, tv, p, st);
     if (e != cudaSuccess) return e;
     const int64_t rows = int64_t(p.n) * p.T * p.Hq;
@@ -229,12 +231,12 @@ extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, con
     if (need > 0 && (!scratch || workspace_bytes < need))
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, scratch ? workspace_bytes : size_t(0));
     if (!aligned(scratch, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
-    if ((flags & HK_KV8_MANY_ROWS) && !wide_can(Q, type, q_strides, G))
-        return fail(HK_ERR_INVALID_ARG, "the tensor-core kernel takes bf16 queries with 16-byte aligned rows, and %d groups", kWideGroups);
+    if ((flags & HK_KV8_MANY_ROWS) && !wide_can(Q, q_strides, G))
+        return fail(HK_ERR_INVALID_ARG, "the tensor-core kernel takes queries with 16-byte aligned rows, and %d groups", kWideGroups);
     if ((flags & kFormFlags) && T * group >= kOwnTileRows)
         return fail(HK_ERR_INVALID_ARG, "%lld query rows of a sequence and KV head: attention_kv8's", (long long)(T * group));
     const Form form = flags & HK_KV8_MANY_ROWS ? kWide : flags & HK_KV8_FEW_ROWS ? kFew
-                                               : choose(cache, B, T, Hq, max_pages, G, wide_can(Q, type, q_strides, G),
+                                               : choose(cache, B, T, Hq, max_pages, G, wide_can(Q, q_strides, G),
                                                         many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq));
     if (form == kOwn)
         return hk_attention_kv8_ex(Q, type, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse,

@@ -4,27 +4,30 @@
 // operations for 2 · D bytes, so the tensor cores bound the work and mma.sync with 16 rows
 // to a unit (each of which converts every tile again) is the wrong tool. Here a unit is 128 stacked rows
 // of a group and KV head: S = Q·Kᵀ (two buffers) and O += P·V in Tensor Memory on tcgen05.mma, P and
-// Q in Tensor Memory too (shared memory is what MMAs and conversion wait for). All units' blocks of 128 tokens, in order, are cut into equal runs, one per
-// CTA, since a prefix has few units and many blocks: each run leaves unnormalised rows,
-// maxima and sums of its units in memory for the combining kernel.
+// Q in Tensor Memory too (shared memory is what MMAs and conversion wait for). All units' blocks of
+// 128 tokens, in order, are cut into equal runs, one per CTA, since a prefix has few units and many blocks: each run
+// leaves unnormalised rows, maxima and sums of its units in memory, which kv8_own_kernel adds up.
 //
-// A CTA: a producing warp streams the codes of K and V page by page (TMA) into a ring; two
-// converting warpgroups write them, as the 128-byte-swizzled rows that the MMAs read, into a second one; one thread
+// A CTA: a producing warp streams the codes of K and V page by page (TMA) into a ring; eight
+// converting warps write them, as the 128-byte-swizzled f16 rows that the MMAs read, into a second one; one thread
 // issues the MMAs; a softmax warpgroup has a thread to a row, as in attn_kernel.cuh. Conversion competes
-// with the softmax for the same pipes, so it is kept short. Keys become f16, two per
+// with the softmax for the same pipes, so it is kept short: codes become f16, two per
 // conversion instruction and exactly, and are met by queries in f16: a row is scaled by a power
 // of two as in kv8_decode.cuh (exact down to 2^-24 of its largest element). The pages'
-// scales do not touch them: a chain of the row's maximum is 16 columns, a page at least,
-// and takes the scale as a whole, and the exponential's multiply-add has it as its factor. Values become bf16
-// (f16 would not hold pages of different scales side by side): their bits are moved to where
-// bf16 has them and multiplied by 2^120 (E4M3's exponent bias is 120 less) times the scale,
-// exact, subnormal codes too. Weights meet them in bf16.
+// scales do not touch the keys: a chain of the row's maximum is 16 columns, a page at least,
+// and takes the scale as a whole, and the exponential's multiply-add has it as its factor. Those of the
+// values, powers of two, become factors within a block: O is in units of the largest scale of values that the
+// unit's run has seen, and a page's values are multiplied by what its scale is of it, down to 2^-14, exactly. Blocks with
+// pages below that, or 2^7 above the first block's unit, have values and weights in bf16 (each code's bits
+// moved to where bf16 has them, times 2^120, which E4M3's exponent bias is less): f16 weights hold down to 2^-31 of the largest, and
+// values that are much larger than others would make what lies below count.
 //
-// Two tiles of 128 rows to a unit (so that a block is converted once for 256) took 10000 cycles a block: Q and P of
-// two tiles leave shared memory for two blocks in each ring, too few to hide a load and a conversion.
-//
-// Registers: 512 threads begin with 128 each; the softmax warpgroup takes 200, the
-// others 104.
+// Measured: 60 us for 64 sequences of 64 query heads (8 KV heads of 128) behind 16384 tokens, 180 us for 128 behind 32768
+// (780 TFLOP/s, 0.41 of the 1917 measured for large GEMMs; tensor pipe 32 % busy, DRAM 6 %): some 2900 cycles for a
+// block of 128 x 128, of which the MMAs take 1080 and the softmax warps 2000 and waits, and some 14 us to
+// start, fill and drain. Two tiles of 128 rows to a unit (so that a block is converted once for 256)
+// took 10000 cycles a block: Q and P of two tiles leave shared memory for two blocks in each ring, too few to hide a
+// load and a conversion. Values in bf16 throughout were as fast, with weights of 2^-8 instead of 2^-11.
 #pragma once
 
 #include <type_traits>
@@ -43,6 +46,7 @@ constexpr int kConvertThreads = 256;
 constexpr int kSoftmaxRegs = 216, kConvertRegs = 96, kIssueRegs = 104;
 constexpr int kWideRegisters = 128 * kSoftmaxRegs + 256 * kConvertRegs + 128 * kIssueRegs;
 static_assert(kWideRegisters <= kWideThreads * 128, "registers of the launch");
+constexpr float kWideShift = 7.0f;      // weights are 2^7 times what the running maximum makes them (2^15 at most): f16 holds them down to 2^-31
 constexpr uint32_t kErrSoftmaxWait = 1u << 19;
 
 template <int kD>
@@ -57,23 +61,25 @@ struct WideGeometry {
     static constexpr int kOffBars = kOffRaw + kRaw * kRawBytes;
     // q_full, q_empty, p_full, o_done, s_full[2], s_free[2], kv_full and kv_empty of the slots, raw_full and raw_empty
     static constexpr int kNumBars = 8 + 2 * kSlots + 2 * kRaw;
-    // factors of the values of 16 tokens each: [kRaw][2][8] bf16 pairs, whose product it is, and whether the second ones matter
-    static constexpr int kFactorBytes = 17 * 4;
+    // factors of the values of 16 tokens each: [kRaw][8] pairs, and whether they are f16
+    static constexpr int kFactorBytes = 9 * 4;
     static constexpr int kOffFactors = kOffBars + kNumBars * 8;
-    // scales of the keys of 16 tokens each, of the last kKeyScales blocks (no role is so far ahead of the softmax)
-    static constexpr int kKeyScales = 16;
-    static constexpr int kOffKeyScales = (kOffFactors + kRaw * kFactorBytes + 15) / 16 * 16;      // (read 16 bytes at a time)
-    static_assert(3 + (kSlots + kRaw + 1) / 2 < kKeyScales, "blocks ahead of the softmax");
-    static constexpr int kOffTmemHolder = kOffKeyScales + kKeyScales * 32;
+    // of the last kScales blocks (no role is so far ahead of the softmax): scales of the keys of 16 tokens each; whether the values
+    // are f16, what O is multiplied by before the block, and the unit of O
+    static constexpr int kScales = 16, kScaleBytes = 48;
+    static constexpr int kOffScales = (kOffFactors + kRaw * kFactorBytes + 15) / 16 * 16;         // (read 16 bytes at a time)
+    static_assert(3 + (kSlots + kRaw + 1) / 2 < kScales, "blocks ahead of the softmax");
+    static constexpr int kOffTmemHolder = kOffScales + kScales * kScaleBytes;
     static constexpr int kOffPlan = kOffTmemHolder + 16;                      // blocks, first sequence, blocks of each group
     static constexpr int kSmemBytes = kOffPlan + (3 * kWideGroups + 2) * 4 + 1024;
     static_assert(kSmemBytes <= attn::kSmemLimit, "shared memory");
-    static_assert(kOffRaw % 1024 == 0 && kOffKV % 1024 == 0 && kOffBars % 8 == 0 && kOffFactors % 4 == 0 && kOffKeyScales % 16 == 0, "alignment");
+    static_assert(kOffRaw % 1024 == 0 && kOffKV % 1024 == 0 && kOffBars % 8 == 0 && kOffFactors % 4 == 0 && kOffScales % 16 == 0, "alignment");
     // TMEM columns: O (kD), S_0, S_1 (128 each), P (64: two bf16 per column), Q (kD / 2: two f16 per column)
     static constexpr int kColO = 0, kColS = 128, kColP = 384, kColQ = 448, kTmemCols = 512;
     static_assert(kColQ + kD / 2 <= kTmemCols, "TMEM");
     static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128) & ~((7u << 7) | (7u << 10));     // A and B f16
-    static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, kD) | (1u << 16);                    // B (V) MN-major
+    static constexpr uint32_t kIdescPVWide = idesc_bf16_f32(128, kD) | (1u << 16);                // B (V) MN-major
+    static constexpr uint32_t kIdescPV = kIdescPVWide & ~((7u << 7) | (7u << 10));                // A and B f16
 };
 
 // A run's share of a unit: blocks [first, last) of `blocks` for rows from `row0` on.
@@ -119,6 +125,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Four codes to bf16 times `factor` / 2^120, in two words of two.
 __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, uint32_t factor) {
     // each code in a low byte, four bits up (its exponent then ends at bit 10, where bf16's lowest four exponent bits do), and the
@@ -152,7 +164,7 @@ __device__ __forceinline__ bool wide_wait(const WaitCtx& c, uint32_t bar, uint32
     }
 }
 
-template <int kD>
+template <int kD, typename T>
 __global__ void __launch_bounds__(kWideThreads, 1)
 kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
     using W = WideGeometry<kD>;
@@ -174,7 +186,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
     auto slot_addr = [&](int s) { return base + W::kOffKV + static_cast<uint32_t>(s) * W::kTileBytes; };
     auto raw_addr = [&](int s) { return base + W::kOffRaw + static_cast<uint32_t>(s) * W::kRawBytes; };
     auto factor_addr = [&](int s) { return base + W::kOffFactors + static_cast<uint32_t>(s) * W::kFactorBytes; };
-    auto key_scale_addr = [&](int block) { return base + W::kOffKeyScales + static_cast<uint32_t>(block % W::kKeyScales) * 32u; };
+    auto scales_addr = [&](int block) { return base + W::kOffScales + static_cast<uint32_t>(block % W::kScales * W::kScaleBytes); };
     const uint32_t tmem_holder = base + W::kOffTmemHolder;
     int32_t* const prefix = reinterpret_cast<int32_t*>(smem + W::kOffPlan);
     int32_t* const first_of = prefix + kWideGroups + 1;
@@ -291,77 +303,84 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
             st_shared_v4(row + (((unit + 1u) ^ sw) << 4), o[4], o[5], o[6], o[7]);
         };
         for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next()) {
-          const int n = w.last - w.first;
-          for (int u = 0; u < 2 * n; ++u) {
-            bool is_k;
-            block_at(u, n, is_k);
-            if (!wait_warp(raw_full(rs), raw_ph, kErrWaitData, poll) || !wait_warp(kv_empty(slot), ring_ph ^ 1u, kErrWaitRing, poll)) {
-                abort_seen = true;
-                break;
-            }
-            if (is_k) {
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const uint32_t tok = token + i * kStepTokens;
-                    const uint4 x = ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk));
-                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = e4m3x2_to_f16x2(words[k] & 0xFFFFu);
-                        o[2 * k + 1] = e4m3x2_to_f16x2(words[k] >> 16);
-                    }
-                    put(tok, o);
+            const int n = w.last - w.first;
+            for (int u = 0; u < 2 * n; ++u) {
+                bool is_k;
+                block_at(u, n, is_k);
+                if (!wait_warp(raw_full(rs), raw_ph, kErrWaitData, poll) || !wait_warp(kv_empty(slot), ring_ph ^ 1u, kErrWaitRing, poll)) {
+                    abort_seen = true;
+                    break;
                 }
-            } else {
-                uint32_t second;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(second) : "r"(factor_addr(rs) + 64u));
+                if (is_k) {
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const uint32_t tok = token + i * kStepTokens;
-                    const uint4 x = ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk));
-                    uint32_t factor;
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(factor) : "r"(factor_addr(rs) + 4u * (tok >> 4)));
-                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint2 v = codes_to_bf16(words[k], factor);
-                        o[2 * k] = v.x;
-                        o[2 * k + 1] = v.y;
-                    }
-                    // a code 0x7F or 0xFF is the only one whose magnitude carries into its sign bit when 1 is added
-                    uint32_t carry = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) carry |= (words[k] & 0x7F7F7F7Fu) + 0x01010101u;
-                    if (((carry & 0x80808080u) | second) != 0) {
-                        uint32_t more;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(more) : "r"(factor_addr(rs) + 32u + 4u * (tok >> 4)));
+                    for (int i = 0; i < kPieces; ++i) {
+                        const uint32_t tok = token + i * kStepTokens;
+                        const uint4 x = ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk));
+                        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t o[8];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t nan = nan_codes(words[k]);
-                            o[2 * k] = mul_bf16x2(o[2 * k], more) | nan_pair(nan);
-                            o[2 * k + 1] = mul_bf16x2(o[2 * k + 1], more) | nan_pair(nan >> 16);
+                            o[2 * k] = e4m3x2_to_f16x2(words[k] & 0xFFFFu);
+                            o[2 * k + 1] = e4m3x2_to_f16x2(words[k] >> 16);
+                        }
+                        put(tok, o);
+                    }
+                } else {
+                    uint32_t half_values;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(half_values) : "r"(factor_addr(rs) + 32u));
+                    auto codes_of = [&](uint32_t tok) { return ld_shared_v4(raw_addr(rs) + chunk_offset<kD>(tok, chunk)); };
+                    auto factor_of = [&](uint32_t tok) {
+                        uint32_t factor;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(factor) : "r"(factor_addr(rs) + 4u * (tok >> 4)));
+                        return factor;
+                    };
+                    if (half_values != 0) {
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            const uint32_t tok = token + i * kStepTokens, factor = factor_of(tok);
+                            const uint4 x = codes_of(tok);
+                            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                o[2 * k] = mul_f16x2(e4m3x2_to_f16x2(words[k] & 0xFFFFu), factor);
+                                o[2 * k + 1] = mul_f16x2(e4m3x2_to_f16x2(words[k] >> 16), factor);
+                            }
+                            put(tok, o);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < kPieces; ++i) {
+                            const uint32_t tok = token + i * kStepTokens, factor = factor_of(tok);
+                            const uint4 x = codes_of(tok);
+                            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint2 v = codes_to_bf16(words[k], factor);
+                                const uint32_t nan = nan_codes(words[k]);
+                                o[2 * k] = v.x | nan_pair(nan);
+                                o[2 * k + 1] = v.y | nan_pair(nan >> 16);
+                            }
+                            put(tok, o);
                         }
                     }
-                    put(tok, o);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(kv_full(slot));
+                    mbar_arrive(raw_empty(rs));
+                }
+                if (++slot == W::kSlots) {
+                    slot = 0;
+                    ring_ph ^= 1u;
+                }
+                if (++rs == W::kRaw) {
+                    rs = 0;
+                    raw_ph ^= 1u;
                 }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(kv_full(slot));
-                mbar_arrive(raw_empty(rs));
-            }
-            if (++slot == W::kSlots) {
-                slot = 0;
-                ring_ph ^= 1u;
-            }
-            if (++rs == W::kRaw) {
-                rs = 0;
-                raw_ph ^= 1u;
-            }
-          }
         }
     } else if (warp >= kWideIssueWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -395,6 +414,10 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                 };
                 int window = w.first;
                 Window cur = look_up(window), ahead = look_up(window + 4);
+                // the unit of O from each block on, as an exponent field: the largest scale of values so far; and whether the block's
+                // values are f16 in it (of this block and the one before: K runs a block ahead of V)
+                uint32_t unit = 1, unit_before = 1, unit_first = 0;
+                bool half_values = true, half_before = true;
                 const int n = w.last - w.first;
                 for (int u = 0; u < 2 * n; ++u) {
                     bool is_k;
@@ -418,22 +441,30 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                             tma_load_3d(raw_addr(rs) + static_cast<uint32_t>((k << p.page_shift) * kD), is_k ? &tmap_k : &tmap_v, 0, 0, row,
                                         raw_full(rs));
                     }
-                    const uint32_t mine = is_k ? __float_as_uint(in_cur ? cur.ks : ahead.ks) : (in_cur ? cur.vs : ahead.vs);
-                    const uint32_t scale = __shfl_sync(0xffffffffu, mine, at + (lane & 7u));
+                    const uint32_t vs = __shfl_sync(0xffffffffu, in_cur ? cur.vs : ahead.vs, at + (lane & 7u));
                     if (is_k) {
-                        if (lane < 8)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(key_scale_addr(key_block) + 4u * lane), "r"(scale) : "memory");
+                        const float ks = __shfl_sync(0xffffffffu, in_cur ? cur.ks : ahead.ks, at + (lane & 7u));
+                        unit_before = unit;
+                        half_before = half_values;
+                        unit = max(unit, __reduce_max_sync(0xffffffffu, vs));
+                        if (unit_first == 0) unit_first = unit;
+                        // (2^-14 times the smallest code is two of f16's smallest steps; and weights that f16 does not
+                        // hold are to matter nowhere, which much larger values than those before would make them)
+                        half_values = __all_sync(0xffffffffu, vs == 0 || vs + 14u >= unit) != 0 && unit <= unit_first + 7u;
+                        if (lane < 8) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales_addr(key_block) + 4u * lane), "f"(ks) : "memory");
+                        if (lane == 0)
+                            st_shared_v4(scales_addr(key_block) + 32u, half_values ? 1u : 0u,
+                                         unit - unit_before < 127u ? 127u - (unit - unit_before) << 23 : 0u, unit << 23, 0u);
                         ++key_block;
                     } else {
-                        // 2^120 · scale as a product of two, for bf16 holds nothing above 2^127 (no scale: 0)
-                        const uint32_t first = scale == 0 ? 0u : min(scale + 120u, 254u), rest = scale == 0 ? 127u : 127u + scale + 120u - first;
-                        const bool second = __any_sync(0xffffffffu, rest != 127u);
-                        if (lane < 8) {
-                            const uint32_t at8 = factor_addr(rs) + 4u * lane;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at8), "r"(first << 7 | first << 23) : "memory");
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at8 + 32u), "r"(rest << 7 | rest << 23) : "memory");
-                        }
-                        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 64u), "r"(second ? 1u : 0u) : "memory");
+                        // 2^(scale - unit), in bf16 times 2^120 (no scale: 0)
+                        const bool last = block + 1 == w.last;
+                        const uint32_t below = (last ? unit : unit_before) - vs;
+                        const bool half_now = last ? half_values : half_before;
+                        const uint32_t f = vs == 0 ? 0u : half_now ? (15u - below) << 10 : below < 247u ? (247u - below) << 7 : 0u;
+                        if (lane < 8)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 4u * lane), "r"(f | f << 16) : "memory");
+                        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 32u), "r"(half_now ? 1u : 0u) : "memory");
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(raw_full(rs), W::kRawBytes);
@@ -491,15 +522,24 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                 for (int j = 0; ok && j < n; ++j, ++pv) {
                     int at;
                     ok = j + 1 == n || issue_s(j + 2 == n);
-                    ok = ok && take(at) && wait_warp(p_full, pv & 1u, kErrWaitAcc, poll);
+                    ok = ok && take(at);
+                    // (read before what the next softmax waits for)
+                    uint32_t half_values;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(half_values) : "r"(scales_addr(static_cast<int>(pv)) + 32u));
+                    half_values = __reduce_or_sync(0xffffffffu, half_values);
+                    ok = ok && wait_warp(p_full, pv & 1u, kErrWaitAcc, poll);
                     if (!ok) break;
                     tc_fence_after_sync();
                     if (elect_one()) {
                         const uint32_t va = slot_addr(at);
+                        auto issue_pv = [&](uint32_t idesc) {
 #pragma unroll
-                        for (int kk = 0; kk < kWideBlock / 16; ++kk)
-                            mma_bf16_ts_one(tmem_base + W::kColO, tmem_base + W::kColP + kk * 8, smem_desc_mnmajor(va + kk * 2048, 128, W::kChunkBytes),
-                                            W::kIdescPV, (j == 0 && kk == 0) ? 0u : 1u);
+                            for (int kk = 0; kk < kWideBlock / 16; ++kk)
+                                mma_bf16_ts_one(tmem_base + W::kColO, tmem_base + W::kColP + kk * 8, smem_desc_mnmajor(va + kk * 2048, 128, W::kChunkBytes),
+                                                idesc, (j == 0 && kk == 0) ? 0u : 1u);
+                        };
+                        if (half_values != 0) issue_pv(W::kIdescPV);
+                        else issue_pv(W::kIdescPVWide);
                         mma_commit_one(o_done);
                         mma_commit_one(kv_empty(at));
                     }
@@ -540,7 +580,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
             {
                 const uint16_t* const src = static_cast<const uint16_t*>(p.q) + (p.b0 + w.group.first + seq) * p.q_stride_b +
                                             tok * p.q_stride_t + head * p.q_stride_h;
-                Raw8<__nv_bfloat16> x[kD / 8];
+                Raw8<T> x[kD / 8];
                 uint32_t top = 0;
 #pragma unroll
                 for (int k = 0; k < kD / 8; ++k) x[k].w[0] = live ? reinterpret_cast<const uint4*>(src)[k] : make_uint4(0, 0, 0, 0);
@@ -551,9 +591,13 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                     for (int i = 0; i < 4; ++i) top = __vmaxu2(top, words[i] & 0x7FFF7FFFu);
                 }
                 top = max(top & 0xFFFFu, top >> 16);
+                if constexpr (std::is_same<T, __half>::value)
+                    top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+                else
+                    top <<= 16;
                 // 2^(10 - floor(log2 of the largest)), kept a normal number; 1 for rows of zeros and rows with an infinity or NaN
-                int field = 127 + 10 - (static_cast<int>(top >> 7) - 127);
-                if (top == 0 || top >= 0x7F80u) field = 127;
+                int field = 127 + 10 - (static_cast<int>(top >> 23) - 127);
+                if (top == 0 || top >= 0x7F800000u) field = 127;
                 field = min(max(field, 1), 253);
                 const float mul = __uint_as_float(static_cast<uint32_t>(field) << 23);
                 c = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * p.scale_log2;
@@ -563,7 +607,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         float f[8];
-                        widen8<__nv_bfloat16>(x[8 * k + e], f);
+                        widen8<T>(x[8 * k + e], f);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) h[4 * e + i] = pack_f16x2(f[2 * i] * mul, f[2 * i + 1] * mul);
                     }
@@ -575,6 +619,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
             mbar_arrive(q_full);
             ++pieces;
             float m = 0.0f, l = 0.0f;      // running maximum (log2 units) used for P, and sum of P
+            float o_unit = 1.0f;           // of O
             for (int j = 0; j < n; ++j, ++nb) {
                 const uint32_t s_addr = tmem_base + lane_off + W::kColS + (nb & 1u) * kWideBlock;
                 if (!wait_warp(s_full(nb & 1u), nb / 2 & 1u, kErrSoftmaxWait, poll)) {
@@ -600,9 +645,14 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                     acc[k] = fmaxf(a, __uint_as_float(v[e0 + 15]));
                 }
                 // each chain's 16 columns lie in one page: their factor
-                float cs[8];
+                float cs[8], to_unit;
+                bool half_values;
                 {
-                    const uint32_t at8 = key_scale_addr(static_cast<int>(nb));
+                    const uint32_t at8 = scales_addr(static_cast<int>(nb));
+                    const uint4 y = ld_shared_v4(at8 + 32u);
+                    half_values = y.x != 0;
+                    to_unit = j > 0 ? __uint_as_float(y.y) : 1.0f;
+                    o_unit = __uint_as_float(y.z);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const uint4 x = ld_shared_v4(at8 + 16u * k);
@@ -625,18 +675,19 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                     m = m_blk;
                     l *= alpha;
                 }
-                const uint64_t nm2 = f32x2(-m, -m);
+                const uint64_t nm2 = f32x2(kWideShift - m, kWideShift - m);
                 uint64_t sum2[4] = {0, 0, 0, 0};
                 uint32_t pk[64];
                 auto rescale_o = [&]() {
-                    if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+                    const float by = alpha * to_unit;
+                    if (__any_sync(0xffffffffu, by != 1.0f)) {
 #pragma unroll
                         for (int cc = 0; cc < kD / 32; ++cc) {
                             uint32_t o[32];
                             tmem_load_32cols(o_addr + 32 * cc, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
                             tmem_store_32cols(o_addr + 32 * cc, o);
                         }
                     }
@@ -647,10 +698,21 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                     f32x2_split(x, x0, x1);
                     const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                     sum2[e & 3] = fadd2(sum2[e & 3], f32x2(p0, p1));
-                    pk[e] = pack_bf16x2_rn(__float_as_uint(p0), __float_as_uint(p1));
+                    v[2 * e] = __float_as_uint(p0);
+                    v[2 * e + 1] = __float_as_uint(p1);
+                };
+                auto pack_half = [&](int e0) {
+                    if (half_values) {
+#pragma unroll
+                        for (int e = e0; e < e0 + 32; ++e) pk[e] = pack_f16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                    } else {
+#pragma unroll
+                        for (int e = e0; e < e0 + 32; ++e) pk[e] = pack_bf16x2_rn(v[2 * e], v[2 * e + 1]);
+                    }
                 };
 #pragma unroll
                 for (int e = 0; e < 32; ++e) exp_pair(e);
+                pack_half(0);
                 // P·V of the previous block must be done before its P is overwritten and O rescaled; the first half of P is
                 // stored while the second is computed
                 if (j > 0 && !wait_warp(o_done, (nb - 1) & 1u, kErrSoftmaxWait, poll)) {
@@ -662,6 +724,7 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                 tmem_store_32cols(p_addr, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
 #pragma unroll
                 for (int e = 32; e < 64; ++e) exp_pair(e);
+                pack_half(32);
                 {
                     const uint64_t s01 = fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3]));
                     float lo, hi;
@@ -683,6 +746,9 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                     const int64_t out_row = (static_cast<int64_t>(w.group.first + seq) * p.T + tok) * p.Hq + head;
                     const int64_t at_row = whole ? p.whole[0] + out_row : p.shared_slots + static_cast<int64_t>(slot) * kWideRows + r;
                     const bool any = l > 0.0f || l != l;
+                    // in units of the power of two in l, so that sums of values that fp32 holds are values that it holds
+                    const int field = static_cast<int>(__float_as_uint(l) >> 23), exponent = l > 0.0f && field < 255 ? field - 127 : 0;
+                    const float less = __uint_as_float(static_cast<uint32_t>(min(max(127 - exponent, 1), 254)) << 23), by = o_unit * less;
 #pragma unroll
                     for (int cc = 0; cc < kD / 32; ++cc) {
                         uint32_t o[32];
@@ -690,14 +756,15 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
                         tmem_wait_ld();
                         if (live) {
 #pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * by) : 0u;
+#pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                st_global_v4(p.part_o + at_row * kD + 32 * cc + 4 * e, any ? o[4 * e] : 0u, any ? o[4 * e + 1] : 0u,
-                                             any ? o[4 * e + 2] : 0u, any ? o[4 * e + 3] : 0u);
+                                st_global_v4(p.part_o + at_row * kD + 32 * cc + 4 * e, o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     }
                     if (live) {
-                        p.part_ml[2 * at_row] = any ? m : -INFINITY;
-                        p.part_ml[2 * at_row + 1] = any ? l : 0.0f;
+                        p.part_ml[2 * at_row] = any ? m - kWideShift + static_cast<float>(exponent) : -INFINITY;
+                        p.part_ml[2 * at_row + 1] = any ? l * less : 0.0f;
                     }
                     tc_fence_before_sync();
                 }

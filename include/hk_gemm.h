@@ -608,12 +608,13 @@ hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, in
  * to B, strictly increasing); the first shared[g] tokens (int32 [G] on the device) of each of them lie in the same pages,
  * which every sequence's own table row names too. They are read once, by the first sequence's row, as far as they fill whole
  * blocks of 128 tokens. shared[g] = 0, and groups of one sequence, are fine. The result is hk_attention_kv8's, but for the
- * order of its fp32 sums (and the rounding of weights, below). Not shared in
+ * order of its fp32 sums (and, for the tensor-core kernel, the rounding of weights where pages' scales of values differ by
+ * more than 2^7: to bf16, 2^-8, instead of f16, 2^-11). Not shared in
  * fact, and read by a sequence itself, are tokens past the first sequence's length, and those of a
  * sequence that has queries which do not see all of them. Where groups are out of order or range, every sequence
  * reads all its tokens itself and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG.
- * By the sizes that the host knows the call runs on a tensor-core kernel for what is shared (Q bf16 with rows that are
- * 16-byte aligned, up to 64 groups; weights are rounded to bf16, 2^-8, before they meet V), on few-row kernels, or, where
+ * By the sizes that the host knows the call runs on a tensor-core kernel for what is shared (rows of Q that are
+ * 16-byte aligned, up to 64 groups), on few-row kernels, or, where
  * reading everything for each sequence costs less (few sequences, short tables, 1024 query rows of a sequence and KV head or
  * more), as hk_attention_kv8, which does not look at the groups.
  * `workspace`: device memory of hk_attention_kv8_shared_workspace_size bytes (up to 44 MB and 8 · head_dim bytes for

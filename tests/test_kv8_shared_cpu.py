@@ -39,7 +39,7 @@ def test_refusals(lib):
     assert at(G=0) == INV and at(G=5) == INV and at(groups=None) == INV and at(shared=None) == INV
     assert at(groups=A + 2) == MIS and at(shared=A + 1) == MIS
     assert at(scale=float("nan")) == INV and at(scale=-1.0) == INV and at(flags=1) == INV
-    assert at(flags=0x30) == INV and at(flags=0x20, type=1) == INV and at(flags=0x20, Q=A + 2) == INV
+    assert at(flags=0x30) == INV and at(flags=0x20, Q=A + 2) == INV
     assert at(flags=0x20, B=130, G=65) == INV                    # more groups than the tensor-core kernel plans for
     assert at(Q=None) == INV and at(O=None) == INV and at(qs=None) == INV and at(os=None) == INV
     assert at(table=None) == INV and at(lengths=None) == INV and at(pages=0) == INV and at(stride=2) == INV
