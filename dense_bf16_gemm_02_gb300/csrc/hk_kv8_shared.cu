@@ -189,7 +189,24 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorM
     return launch_early(fn, dim3(static_cast<unsigned>(ceil_div(rows * split, 8))), dim3(256), 0, st, p);
 }
 
+// The form of a call.
+Form form_of(uint32_t flags, const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* c, int64_t max_pages,
+             const void* O, const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq, int64_t G) {
+    if (flags & kFormFlags) return flags & HK_KV8_MANY_ROWS ? kWide : kFew;
+    return choose(c, B, T, Hq, max_pages, G, wide_can(Q, q_strides, G), many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq));
+}
+
 }  // namespace
+
+extern "C" size_t hk_attention_kv8_shared_workspace_size_ex(const void* Q, int32_t type, const int64_t q_strides[3],
+                                                            const hk_kv8_cache* cache, int64_t max_pages, const void* O,
+                                                            const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq, int64_t G,
+                                                            uint32_t flags) {
+    if (!shape_ok(cache, B, T, Hq, max_pages, G) || !q_strides || !o_strides) return 0;
+    const Form form = form_of(flags, Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq, G);
+    return form == kOwn ? hk_attention_kv8_workspace_size_ex(Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq, 0)
+                        : workspace(cache, B, T, Hq, G, form == kWide).total;
+}
 
 extern "C" size_t hk_attention_kv8_shared_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                          int64_t max_pages, int64_t G) {
@@ -227,7 +244,7 @@ extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, con
         if (sizes[i] > 1 && std::llabs(o_strides[i]) < cache->head_dim) return fail(HK_ERR_INVALID_ARG, "the output's rows overlap");
     if (!shape_ok(cache, B, T, Hq, max_pages, G)) return fail(HK_ERR_INVALID_ARG, "problem too large");
     const int64_t group = Hq / cache->heads;
-    const size_t need = hk_attention_kv8_shared_workspace_size(cache, B, T, Hq, max_pages, G);
+    const size_t need = hk_attention_kv8_shared_workspace_size_ex(Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq, G, flags);
     if (need > 0 && (!scratch || workspace_bytes < need))
         return fail(HK_ERR_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, scratch ? workspace_bytes : size_t(0));
     if (!aligned(scratch, 256)) return fail(HK_ERR_WORKSPACE, "the workspace must be 256-byte aligned");
@@ -235,9 +252,7 @@ extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, con
         return fail(HK_ERR_INVALID_ARG, "the tensor-core kernel takes queries with 16-byte aligned rows, and %d groups", kWideGroups);
     if ((flags & kFormFlags) && T * group >= kOwnTileRows)
         return fail(HK_ERR_INVALID_ARG, "%lld query rows of a sequence and KV head: attention_kv8's", (long long)(T * group));
-    const Form form = flags & HK_KV8_MANY_ROWS ? kWide : flags & HK_KV8_FEW_ROWS ? kFew
-                                               : choose(cache, B, T, Hq, max_pages, G, wide_can(Q, q_strides, G),
-                                                        many_rows_can(Q, type, q_strides, O, o_strides, B, T, Hq));
+    const Form form = form_of(flags, Q, type, q_strides, cache, max_pages, O, o_strides, B, T, Hq, G);
     if (form == kOwn)
         return hk_attention_kv8_ex(Q, type, q_strides, cache, block_table, table_stride, max_pages, lengths, counts, O, o_strides, lse,
                                    B, T, Hq, causal, scale, scratch, workspace_bytes, flags & ~kFormFlags, timeout_ns, stream);
@@ -261,7 +276,7 @@ extern "C" hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, con
     if (wide && (s = encode_codes(enc, &wk, cache->k_codes, cache, cache->page_size)) != HK_OK) return s;
     if (wide && (s = encode_codes(enc, &wv, cache->v_codes, cache, cache->page_size)) != HK_OK) return s;
 
-    const Workspace w = workspace(cache, B, T, Hq, G, G <= kWideGroups);
+    const Workspace w = workspace(cache, B, T, Hq, G, wide);
     char* const base = static_cast<char*>(scratch);
     SharedParams p = {};
     p.q = Q;

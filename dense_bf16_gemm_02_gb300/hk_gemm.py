@@ -69,6 +69,7 @@ EXPORTED = (
     "hk_attention_kv8_workspace_size_ex", "hk_kv8_arrange", "hk_kv8_arrange_workspace_size", "hk_kv8_compact",
     "hk_kv8_compact_workspace_size", "hk_kv8_copy_pages", "hk_qk_norm_rope",
     "hk_attention_kv8_shared", "hk_attention_kv8_shared_ex", "hk_attention_kv8_shared_workspace_size",
+    "hk_attention_kv8_shared_workspace_size_ex",
 )
 
 
@@ -217,6 +218,8 @@ def load() -> ctypes.CDLL:
         lib.hk_attention_kv8_shared_ex.restype = I32
         lib.hk_attention_kv8_shared_workspace_size.argtypes = [CP, I64, I64, I64, I64, I64]
         lib.hk_attention_kv8_shared_workspace_size.restype = SZ
+        lib.hk_attention_kv8_shared_workspace_size_ex.argtypes = [P, I32, P, CP, I64, P, P, I64, I64, I64, I64, U32]
+        lib.hk_attention_kv8_shared_workspace_size_ex.restype = SZ
         _lib = lib
         return lib
 

@@ -277,7 +277,7 @@ def attention_kv8_shared(q, cache: Kv8Cache, block_table, lengths, groups, share
         os = _tokens_shape(out, "out", cache, False)[3]
     lse = _empty((B, T, Hq), _f32, q, stream) if return_lse else None
     lib = _hk.load()
-    size = lib.hk_attention_kv8_shared_workspace_size(cache._ref, B, T, Hq, pages, G)
+    size = lib.hk_attention_kv8_shared_workspace_size_ex(q.data_ptr(), code, qs, cache._ref, pages, out.data_ptr(), os, B, T, Hq, G, 0)
     workspace = _empty(size, _u8, q, stream) if size else None
     st = lib.hk_attention_kv8_shared(q.data_ptr(), code, qs, cache._ref, block_table.data_ptr(), ld, pages, lengths.data_ptr(),
                                      None if counts is None else counts.data_ptr(), groups.data_ptr(), shared.data_ptr(), G,

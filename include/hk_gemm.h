@@ -637,6 +637,11 @@ hk_status hk_attention_kv8_shared_ex(const void* Q, int32_t type, const int64_t 
                                      size_t workspace_bytes, uint32_t flags, uint64_t timeout_ns, void* stream);
 size_t hk_attention_kv8_shared_workspace_size(const hk_kv8_cache* cache, int64_t B, int64_t T, int64_t Hq, int64_t max_pages,
                                               int64_t G);
+/* Bytes that the call with these arguments needs, and asks for (as hk_attention_kv8_workspace_size_ex). */
+size_t hk_attention_kv8_shared_workspace_size_ex(const void* Q, int32_t type, const int64_t q_strides[3],
+                                                 const hk_kv8_cache* cache, int64_t max_pages, const void* O,
+                                                 const int64_t o_strides[3], int64_t B, int64_t T, int64_t Hq, int64_t G,
+                                                 uint32_t flags);
 
 /* The norm of each head's query and key and the rotation by its token's position, in one pass:
  *     y = x / sqrt(mean(x^2) + eps) · w;   (a, b) -> (a cos t - b sin t, a sin t + b cos t)

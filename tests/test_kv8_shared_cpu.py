@@ -48,7 +48,8 @@ def test_refusals(lib):
     assert at(Q=A + 1) == MIS and at(O=A + 1) == MIS and at(lse=A + 2) == MIS and at(counts=A + 1) == MIS
     c = _cache()
     for T in (1, 100, 300):                  # (1024 rows of a sequence and more: what attention_kv8 needs)
-        need = h.hk_attention_kv8_shared_workspace_size(c, 4, T, 8, 4000, 2)
+        need = lib.hk_attention_kv8_shared_workspace_size_ex(A, 0, S3, ctypes.byref(c), 4000, A, S3, 4, T, 8, 2, 0)
+        assert 0 < need <= h.hk_attention_kv8_shared_workspace_size(c, 4, T, 8, 4000, 2)
         assert at(T=T, pages=4000, stride=4000, wsb=need - 1) == WS and at(T=T, pages=4000, stride=4000, ws=None) == WS
         assert at(T=T, pages=4000, stride=4000, ws=A + 128) == WS
     assert h.hk_attention_kv8_shared_workspace_size(c, 4, 300, 8, 4000, 2) == h.hk_attention_kv8_workspace_size(c, 4, 300, 8, 4000)
@@ -58,8 +59,11 @@ def test_refusals(lib):
         for pages in (1, 5, 40, 400, 4000):
             for B, G in ((1, 1), (4, 1), (64, 1), (64, 64), (700, 3)):
                 need = h.hk_attention_kv8_shared_workspace_size(c, B, T, 8, pages, G)
-                few = lib.hk_attention_kv8_workspace_size_ex(A, 1, S3, ctypes.byref(c), pages, A, S3, B, T, 8, 0)
-                assert need >= few
+                for type, at_q in ((0, A), (0, A + 2), (1, A), (1, A + 2)):
+                    for flags in (0, 0x10, 0x20)[: 3 if at_q == A else 2]:
+                        assert lib.hk_attention_kv8_shared_workspace_size_ex(at_q, type, S3, ctypes.byref(c), pages, A, S3, B, T, 8, G,
+                                                                             flags) <= need
+    assert lib.hk_attention_kv8_shared_workspace_size_ex(A, 0, S3, ctypes.byref(c), 4, A, S3, 2, 1, 8, 1, 0) == 0      # a small call
     for args in ((0, 1, 8, 4, 1), (4, 1, 7, 4, 1), (4, 1, 8, 4, 5), (4, 1, 8, 4, 0), (4, 1, 8, 0, 1)):
         assert h.hk_attention_kv8_shared_workspace_size(c, *args) == 0
     # (bounded by the rows of a launch, whatever the batch is)
