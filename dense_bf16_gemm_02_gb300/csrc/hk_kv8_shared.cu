@@ -184,7 +184,9 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorM
     const cudaError_t e = launch_spread<kD, T>(tk, tv, p, st);
     if (e != cudaSuccess) return e;
     const int64_t rows = int64_t(p.n) * p.T * p.Hq;
-    const int split = rows <= 16 * kSms ? 8 : rows <= 64 * kSms ? 2 : 1;       // (as many warps as are resident at a time)
+    // Warps to a row of the joining kernel, eight, two and one measured, calls in microseconds: 32 rows 20.1, 23.8, 29.8; 512 34.9,
+    // 37.0, 38.6; 1176 43.5, 42.5, 45.0; 2048 93, 83, 85; 8192 180, 159, 153.
+    const int split = rows <= 6 * kSms ? 8 : rows <= 24 * kSms ? 2 : 1;
     auto* fn = split == 8 ? &kv8_shared_combine_kernel<kD, T, 8> : split == 2 ? &kv8_shared_combine_kernel<kD, T, 2> : &kv8_shared_combine_kernel<kD, T, 1>;
     return launch_early(fn, dim3(static_cast<unsigned>(ceil_div(rows * split, 8))), dim3(256), 0, st, p);
 }

@@ -29,6 +29,8 @@ constexpr int64_t kLimit = (int64_t(1) << 31) - 1;
 constexpr int kSms = 152;
 constexpr int64_t kMaxHeads = 65535;
 constexpr int64_t kWarpsPerSm = 24;      // warps that an SM holds
+// A warp's angles, in steps of its rows. Counted as nothing, as 8 steps, as more than anything (a warp to a token): 500 tokens
+// of 72 heads of 128 in bf16 take 19.0, 7.6, 7.7 us, 2000 tokens 24.5, 19.4, 21.6, 5003 of 48 heads 40.3, 29.6, 30.0.
 constexpr int kAngleSteps = 8;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -153,8 +155,7 @@ extern "C" hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], 
     const int lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;
     for (int op = 0; op < 2; ++op) p.op_steps[op] = (p.heads[op] + 32 / lanes - 1) / (32 / lanes);
     const int64_t token_steps = int64_t(p.op_steps[0]) + p.op_steps[1];
-    // warps to a token: those whose rounds over the GPU take the least time, a warp's being its row steps and what its angles
-    // cost (some eight steps)
+    // warps to a token: those whose rounds over the GPU take the least time, a warp's being its row steps and its angles
     int64_t shares = 1, least = INT64_MAX;
     for (int64_t rounds = 1; rounds <= 8; ++rounds) {
         const int64_t s = std::max<int64_t>(1, std::min(token_steps, rounds * kSms * kWarpsPerSm / (B * T)));

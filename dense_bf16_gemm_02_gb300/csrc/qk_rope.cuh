@@ -19,6 +19,11 @@
 // position modulo 2^64 that is the fraction of a turn to within 2^-33 whatever
 // the position is (whole turns fall out at the top), for a handful of integer
 // multiplications; its top 32 bits, signed, go to fp32 and to sincospi.
+//
+// Measured: 16384 tokens of 72 heads of 128 in bf16 106 us, 5.7 TB/s read and written, 0.84 of a copy's rate (half the issue slots
+// are taken; a test at each load, which made the loads wait for one another, took 256 us, 64-bit divisions to find rows 135, clamped
+// row numbers instead of whole steps first and a rest 122); 5003 of 48 heads in fp16 28 us; 64 of 72 heads 5 us, a launch and
+// two trips to memory.
 #pragma once
 
 #include <cstdint>
