@@ -8,7 +8,7 @@
 // 128 tokens, in order, are cut into equal runs, one per CTA, since a prefix has few units and many blocks: each run
 // leaves unnormalised rows, maxima and sums of its units in memory, which kv8_own_kernel adds up.
 //
-// A CTA: a producing warp streams the codes of K and V page by page (TMA) into a ring; eight
+// A CTA: two producing warps stream the codes of K and V page by page (TMA) into a ring; eight
 // converting warps write them, as the 128-byte-swizzled f16 rows that the MMAs read, into a second one; one thread
 // issues the MMAs; a softmax warpgroup has a thread to a row, as in attn_kernel.cuh. Conversion competes
 // with the softmax for the same pipes, so it is kept short: codes become f16, two per
@@ -41,7 +41,7 @@ namespace kv8 {
 constexpr int kWideGroups = 64;        // groups of a call on this form
 constexpr int kWideBlock = 128;        // tokens of a block
 constexpr int kWideThreads = 512;
-constexpr int kWideIssueWarp = 4, kWideLoadWarp = 5, kWideConvertWarp = 8;      // after four softmax warps; eight convert
+constexpr int kWideIssueWarp = 4, kWideLoadWarp = 5, kWideConvertWarp = 8;      // after four softmax warps; two load, eight convert
 constexpr int kConvertThreads = 256;
 constexpr int kSoftmaxRegs = 216, kConvertRegs = 96, kIssueRegs = 104;
 constexpr int kWideRegisters = 128 * kSoftmaxRegs + 256 * kConvertRegs + 128 * kIssueRegs;
@@ -384,90 +384,83 @@ kv8_shared_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_c
         }
     } else if (warp >= kWideIssueWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == kWideLoadWarp) {
-            // ------------------------------------------ producing warp --
+        if (warp == kWideLoadWarp || warp == kWideLoadWarp + 1) {
+            // ------------------------------------- producing warps: one for K, one for V --
+            const bool of_k = warp == kWideLoadWarp;
             int rs = 0, key_block = 0;
             uint32_t raw_ph = 0;
             const int boxes = kWideBlock >> p.page_shift;                // pages of a block
             for (WidePiece w = walk.next(); w.valid && !abort_seen; w = walk.next()) {
                 const int32_t* const table = p.table + first_of[w.section] * p.table_stride;
                 // pages (as rows of the tensor map) and scales of the 32 pieces of 16 tokens of blocks [window, window + 4), one
-                // per lane, and of the four blocks after those
+                // per lane; those of the next four blocks, whose loads are then under way, and the pages of the four after them
                 struct Window {
                     int row;
                     float ks;
-                    uint32_t vs;           // exponent field of V's scale, a power of two
+                    uint32_t vs;           // V's scale, a power of two
                 };
-                auto look_up = [&](int block) {
-                    Window x = {w.h, 0.0f, 0u};
+                auto page_of = [&](int block) {
                     const int key = block * kWideBlock + static_cast<int>(lane) * 16;
-                    if (key < w.blocks * kWideBlock) {
-                        const int32_t pg = table[key >> p.page_shift];
-                        if (pg < 0 || pg >= p.num_pages) {
-                            atomicOr(p.wait.status, kErrPage);      // (scale 0: nothing of page 0, read in its place, comes through)
-                        } else {
-                            const int64_t ph = static_cast<int64_t>(pg) * p.Hkv + w.h;
-                            x = Window{static_cast<int>(ph), p.k_scale[ph], __float_as_uint(p.v_scale[ph]) >> 23 & 0xFFu};
-                        }
-                    }
-                    return x;
+                    return key < w.blocks * kWideBlock ? table[key >> p.page_shift] : 0;
+                };
+                auto look_up = [&](int pg) {
+                    const bool good = pg >= 0 && pg < p.num_pages;
+                    if (!good) atomicOr(p.wait.status, kErrPage);        // (scale 0: nothing of page 0, read in its place, comes through)
+                    const int64_t ph = static_cast<int64_t>(good ? pg : 0) * p.Hkv + w.h;
+                    return Window{static_cast<int>(ph), good && of_k ? p.k_scale[ph] : 0.0f, good ? __float_as_uint(p.v_scale[ph]) : 0u};
                 };
                 int window = w.first;
-                Window cur = look_up(window), ahead = look_up(window + 4);
+                int page = page_of(window), page_ahead = page_of(window + 4);
+                Window cur = look_up(page), ahead = look_up(page_ahead);
+                page = page_of(window + 8);
                 // the unit of O from each block on, as an exponent field: the largest scale of values so far; and whether the block's
-                // values are f16 in it (of this block and the one before: K runs a block ahead of V)
-                uint32_t unit = 1, unit_before = 1, unit_first = 0;
-                bool half_values = true, half_before = true;
+                // values are f16 in it
+                uint32_t unit = 1, unit_first = 0;
                 const int n = w.last - w.first;
                 for (int u = 0; u < 2 * n; ++u) {
                     bool is_k;
                     const int block = w.first + block_at(u, n, is_k);
-                    // (K runs a block ahead of V: the window moves with V)
-                    if (!is_k && block >= window + 4) {
-                        window += 4;
-                        cur = ahead;
-                        ahead = look_up(window + 4);
-                    }
-                    const bool in_cur = block < window + 4;
-                    const int at = (block - window & 3) * 8;
-                    if (!wait_warp(raw_empty(rs), raw_ph ^ 1u, kErrWaitRing, suspend)) {
-                        abort_seen = true;
-                        break;
-                    }
-                    // (the copies go out before the scales are waited for; the barrier's one arrival, which says what to expect, after)
-                    for (int k = 0; k < boxes; ++k) {
-                        const int row = __shfl_sync(0xffffffffu, in_cur ? cur.row : ahead.row, at + (k << p.page_shift >> 4));
-                        if (lane == 0)
-                            tma_load_3d(raw_addr(rs) + static_cast<uint32_t>((k << p.page_shift) * kD), is_k ? &tmap_k : &tmap_v, 0, 0, row,
-                                        raw_full(rs));
-                    }
-                    const uint32_t vs = __shfl_sync(0xffffffffu, in_cur ? cur.vs : ahead.vs, at + (lane & 7u));
-                    if (is_k) {
-                        const float ks = __shfl_sync(0xffffffffu, in_cur ? cur.ks : ahead.ks, at + (lane & 7u));
-                        unit_before = unit;
-                        half_before = half_values;
+                    if (is_k == of_k) {
+                        if (block >= window + 4) {
+                            window += 4;
+                            cur = ahead;
+                            ahead = look_up(page);
+                            page = page_of(window + 8);
+                        }
+                        const int at = (block - window) * 8;
+                        if (!wait_warp(raw_empty(rs), raw_ph ^ 1u, kErrWaitRing, suspend)) {
+                            abort_seen = true;
+                            break;
+                        }
+                        // (the copies go out before the scales are waited for; the barrier's one arrival, which says what to expect, after)
+                        const int row = __shfl_sync(0xffffffffu, cur.row, at + (static_cast<int>(lane) % boxes << p.page_shift >> 4));
+                        if (static_cast<int>(lane) < boxes)
+                            tma_load_3d(raw_addr(rs) + (lane << p.page_shift) * kD, is_k ? &tmap_k : &tmap_v, 0, 0, row, raw_full(rs));
+                        const uint32_t vs = __shfl_sync(0xffffffffu, cur.vs, at + (lane & 7u)) >> 23 & 0xFFu;
+                        const uint32_t unit_before = unit;
                         unit = max(unit, __reduce_max_sync(0xffffffffu, vs));
                         if (unit_first == 0) unit_first = unit;
                         // (2^-14 times the smallest code is two of f16's smallest steps; and weights that f16 does not
                         // hold are to matter nowhere, which much larger values than those before would make them)
-                        half_values = __all_sync(0xffffffffu, vs == 0 || vs + 14u >= unit) != 0 && unit <= unit_first + 7u;
-                        if (lane < 8) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales_addr(key_block) + 4u * lane), "f"(ks) : "memory");
-                        if (lane == 0)
-                            st_shared_v4(scales_addr(key_block) + 32u, half_values ? 1u : 0u,
-                                         unit - unit_before < 127u ? 127u - (unit - unit_before) << 23 : 0u, unit << 23, 0u);
-                        ++key_block;
-                    } else {
-                        // 2^(scale - unit), in bf16 times 2^120 (no scale: 0)
-                        const bool last = block + 1 == w.last;
-                        const uint32_t below = (last ? unit : unit_before) - vs;
-                        const bool half_now = last ? half_values : half_before;
-                        const uint32_t f = vs == 0 ? 0u : half_now ? (15u - below) << 10 : below < 247u ? (247u - below) << 7 : 0u;
-                        if (lane < 8)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 4u * lane), "r"(f | f << 16) : "memory");
-                        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 32u), "r"(half_now ? 1u : 0u) : "memory");
+                        const bool half_values = __all_sync(0xffffffffu, vs == 0 || vs + 14u >= unit) != 0 && unit <= unit_first + 7u;
+                        if (is_k) {
+                            const float ks = __shfl_sync(0xffffffffu, cur.ks, at + (lane & 7u));
+                            if (lane < 8) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales_addr(key_block) + 4u * lane), "f"(ks) : "memory");
+                            if (lane == 0)
+                                st_shared_v4(scales_addr(key_block) + 32u, half_values ? 1u : 0u,
+                                             unit - unit_before < 127u ? 127u - (unit - unit_before) << 23 : 0u, unit << 23, 0u);
+                            ++key_block;
+                        } else {
+                            // 2^(scale - unit), in bf16 times 2^120 (no scale: 0)
+                            const uint32_t below = unit - vs;
+                            const uint32_t f = vs == 0 ? 0u : half_values ? (15u - below) << 10 : below < 247u ? (247u - below) << 7 : 0u;
+                            if (lane < 8)
+                                asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 4u * lane), "r"(f | f << 16) : "memory");
+                            if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(factor_addr(rs) + 32u), "r"(half_values ? 1u : 0u) : "memory");
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_expect_tx(raw_full(rs), W::kRawBytes);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(raw_full(rs), W::kRawBytes);
                     if (++rs == W::kRaw) {
                         rs = 0;
                         raw_ph ^= 1u;
