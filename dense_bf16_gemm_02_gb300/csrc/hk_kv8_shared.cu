@@ -96,11 +96,11 @@ constexpr int64_t kOwnTileRows = 1024;
 // By an estimate of the three times in microseconds, with the table's width for the lengths (which the host does not know) and
 // all of it shared: a call of one token, every row that is joined, and every token of the table, of which attention_kv8 takes what
 // attention_cost says (and a tenth for lengths that do not divide evenly), units of 16 stacked rows 48 millionths each (head
-// dimension 64: 30), units of 128 rows 85 (65).
+// dimension 64: 30), units of 128 rows 75 (55).
 // Measured (attention_kv8, units of 16, of 128 rows; 8 KV heads of 128, 8 query heads each, one group of sequences with
-// 300 tokens of their own): 8 behind 2048 tokens 14, 25, 29; 8 behind 8192 30, 32, 32; 16 behind 8192 52, 48, 37;
-// 64 behind 2048 56, 68, 41; 64 behind 32768 549, 413, 117. 32 KV heads of a query head each: 16 behind 500 20, 23, 33;
-// 16 behind 8192 153, 53, 53; 16 behind 32768 561, 88, 111. Head dimension 64: 16 behind 2048 14, 23, 26; 16 behind 8192 40, 34, 30;
+// 300 tokens of their own): 8 behind 2048 tokens 14, 25, 30; 8 behind 8192 30, 32, 33; 16 behind 8192 52, 47, 36;
+// 64 behind 2048 56, 67, 42; 64 behind 32768 548, 409, 107. 32 KV heads of a query head each: 16 behind 500 20, 22, 32;
+// 16 behind 8192 153, 54, 54; 16 behind 32768 560, 87, 102. Head dimension 64: 16 behind 2048 14, 22, 26; 16 behind 8192 40, 34, 29;
 // 64 of 16 query heads behind 4096 (their own tiles are full) 43, 54. It errs where two are near: 4 behind 32768 52, 50, 44.
 Form choose(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, int64_t G, bool wide, bool many) {
     const int64_t group = Hq / c->heads;
@@ -110,7 +110,7 @@ Form choose(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max
     const bool d64 = c->head_dim == 64;
     const double own_us = 8.0 + 1.1 * room * attention_cost(c, B, T, Hq, max_pages, many);
     const double few_us = (d64 ? 15.0 + 0.002 * rows : 18.0 + 0.006 * rows) + room * (d64 ? 30.0 : 48.0) * groups * std::ceil(stacked / kRows);
-    const double wide_us = (d64 ? 25.0 : 30.0) + 0.001 * rows + room * (d64 ? 65.0 : 85.0) * groups * std::ceil(stacked / kWideRows);
+    const double wide_us = (d64 ? 25.0 : 30.0) + 0.001 * rows + room * (d64 ? 55.0 : 75.0) * groups * std::ceil(stacked / kWideRows);
     if (wide && wide_us < std::min(own_us, few_us)) return kWide;
     return few_us < own_us ? kFew : kOwn;
 }

@@ -22,12 +22,16 @@
 // moved to where bf16 has them, times 2^120, which E4M3's exponent bias is less): f16 weights hold down to 2^-31 of the largest, and
 // values that are much larger than others would make what lies below count.
 //
-// Measured: 60 us for 64 sequences of 64 query heads (8 KV heads of 128) behind 16384 tokens, 180 us for 128 behind 32768
-// (780 TFLOP/s, 0.41 of the 1917 measured for large GEMMs; tensor pipe 32 % busy, DRAM 6 %): some 2900 cycles for a
-// block of 128 x 128, of which the MMAs take 1080 and the softmax warps 2000 and waits, and some 14 us to
-// start, fill and drain. Two tiles of 128 rows to a unit (so that a block is converted once for 256)
+// Measured: 56 us for 64 sequences of 64 query heads (8 KV heads of 128) behind 16384 tokens, 153 us for 128 behind 32768
+// (914 TFLOP/s, 0.48 of the 1917 measured for large GEMMs; tensor pipe 37 % busy, DRAM 6 %): some 2300 cycles for a
+// block of 128 x 128, of which the MMAs take 1080, and some 20 us to start, fill and drain. With conversions, exponentials,
+// packing and maxima all left out it is 1950, with the MMAs too 1800: what is left is the chain from S through the softmax's loads and
+// stores of Tensor Memory to P·V. One producing warp, which waited for each look-up of pages, bound it at 2900. What was tried (us of a
+// call, 64 behind 16384 and 128 behind 32768, with 77 and 208 as it is): two threads to a row, which tell
+// each other their maxima 81 and 216; converting warps of K and V apart, with rings of their own 82 and 211; every
+// code loaded before the first one is converted 80 and 214. Two tiles of 128 rows to a unit (so that a block is converted once for 256)
 // took 10000 cycles a block: Q and P of two tiles leave shared memory for two blocks in each ring, too few to hide a
-// load and a conversion. Values in bf16 throughout were as fast, with weights of 2^-8 instead of 2^-11.
+// load and a conversion.
 #pragma once
 
 #include <type_traits>
