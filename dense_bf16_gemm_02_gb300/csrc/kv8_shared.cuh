@@ -17,8 +17,9 @@
 // Both kinds of units run as in kv8_decode.cuh: tiles of 32 tokens of all units in
 // one order, cut into equal runs, one per warp, whatever the lengths are; sums of units that
 // are split, and of sequences with a shared part, go through memory and are added up by a second
-// kernel, in order. Without a shared part a whole unit is finished at once. Where the shared units
-// run on the tensor-core kernel (kv8_shared_mma.cuh), what sequences have of their own is
+// kernel, in order. Without a shared part a whole unit is finished at once. Tiles bound it: 16 rows by 32 tokens
+// some 1 us of a warp whatever its rows hold, 45 sequences in 6 groups behind 5003 tokens (28/4 heads of 64, fp16) 33 to 39 us.
+// Where the shared units run on the tensor-core kernel (kv8_shared_mma.cuh), what sequences have of their own is
 // mostly short, and a block to a unit is quicker: no plan over all lengths before the first load, and
 // the unit's warps load at the same time; only units of more than `own_limit` tiles are spread.
 #pragma once
@@ -460,10 +461,12 @@ __device__ __forceinline__ void add_parts(const RowParts& in, int rows, int warp
     }
 }
 
-// What a sequence has of its own, and its output, a block to a unit, beside the tensor-core kernel (for up to 64 groups; see
-// there for the waits): the warps share out the tiles of an own part of up to own_limit, and then the sums that the
-// tensor-core kernel left of its rows (and those of a longer own part, which the first kernel has spread over the GPU), and join theirs in shared memory. A kernel for the joining alone, with the own parts' sums through memory, made a call
-// for 16 sequences of 4 queries behind 8192 53 instead of 47.
+// What a sequence has of its own, and its output, a block to a unit, behind the tensor-core kernel and beside its last blocks (for
+// up to 64 groups): the warps share out the tiles of an own part of up to own_limit, then the sums that the
+// tensor-core kernel left of its rows (and those of a longer own part, which the first kernel has spread over the GPU), and
+// join theirs in shared memory. 26 us for 64 sequences of 512 tokens (8 KV heads of 128, 34 MB: 20 of it the tiles, in a row of
+// trips to memory, 6 the joining). A kernel for the joining alone, with the own parts' sums through memory, made a call for 16
+// sequences of 4 queries behind 8192 tokens 53 us instead of 47.
 template <int kD, typename T, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, kBlockWarps / kWarps)
 kv8_own_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
