@@ -563,7 +563,7 @@ typedef struct hk_kv8_pool {
 
 /* Arrange the pool's rows anew, all at once: row i becomes the first keep[i] tokens of what row
  * parents[i] was before the call (NULL: of its own), with pages for room[i] >= keep[i] tokens.
- * keep, room, parents: int32 [rows] on the device. So
+ * keep, room, parents: int32 [rows] on the device (keep and room may be held itself). So
  *   room[i] above what row i holds      takes pages (for tokens to come),
  *   keep[i] below it                    cuts the row back; keep = room = 0 ends it,
  *   parents[i] = j                      forks row j, or (for several rows) reorders them.

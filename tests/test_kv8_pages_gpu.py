@@ -259,3 +259,75 @@ def test_wrong_shapes_are_refused():
     with pytest.raises(hk.HKError):
         hk.kv8_arrange(hk.Kv8Pool(pool.refs, pool.table, pool.held, 24), three)
     assert pool.refs.sum().item() == 0 and torch.cuda.is_available()
+
+
+@pytest.mark.parametrize("rows,width,page", [(5, 700, 16), (40, 6, 64), (1, 3, 128)])
+def test_what_the_rows_hold_as_an_argument(rows, width, page):
+    """keep or room may be the pool's own tensor, which the call writes."""
+    import torch
+    import dense_bf16_gemm_02_gb300 as hk
+    rng = random.Random(rows * width)
+    pages = rows * width + 3
+    pool = hk.Kv8Pool.empty(pages, rows, width, page_size=page)
+    refs, table, held = [0] * pages, [[0] * width for _ in range(rows)], [0] * rows
+    caches = _caches(1, pages, page)
+    even = [rng.randrange(1, width * page // 2)] * rows
+    calls = [("keep", even, None)]
+    for _ in range(6):
+        calls += [("keep", [rng.randrange(0, 3 * page) for _ in range(rows)], None), ("room", None, None)]
+    for how, more, _ in calls:
+        if how == "keep":                    # all that is held, and room for more
+            keep, room = list(held), [min(width * page, h + m) for h, m in zip(held, more)]
+            missing = hk.kv8_arrange(pool, pool.held, _i32(room), caches=caches)
+        else:                                # part of it, with as much room as before
+            keep, room = [rng.randrange(0, h + 1) for h in held], list(held)
+            missing = hk.kv8_arrange(pool, _i32(keep), pool.held, caches=caches)
+        refs, table, held, _, lack = ref.arrange(refs, table, held, keep, room, None, page)
+        assert missing.item() == lack == 0
+        assert pool.refs.tolist() == refs and pool.held.tolist() == held
+        _same_rows(pool.table.tolist(), table, held, page)
+    parents = list(range(rows))[::-1]
+    room = [max(held)] * rows
+    assert hk.kv8_arrange(pool, _i32([0] * rows), _i32(room)).item() == 0
+    refs, table, held, _, _ = ref.arrange(refs, table, held, [0] * rows, room, None, page)
+    missing = hk.kv8_arrange(pool, pool.held, pool.held, parents=_i32(parents), caches=caches)
+    refs, table, held, _, lack = ref.arrange(refs, table, held, list(held), list(held), parents, page)
+    assert missing.item() == lack and pool.refs.tolist() == refs
+    _same_rows(pool.table.tolist(), table, held, page)
+    assert _status_ok()
+
+
+def test_two_captured_calls_of_one_pool():
+    """Graphs that were captured before either ran, replayed in turn: they share the pool's workspace."""
+    import torch
+    import dense_bf16_gemm_02_gb300 as hk
+    pages, rows, width, page = 400, 20, 12, 16
+    pool = hk.Kv8Pool.empty(pages, rows, width, page_size=page)
+    caches = _caches(2, pages, page)
+    keep, room = _i32([0] * rows), _i32([0] * rows)
+    back, parents = _i32([0] * rows), _i32(list(range(rows)))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.graph(graphs[0]):
+        hk.kv8_arrange(pool, keep, room, caches=caches)
+    with torch.cuda.graph(graphs[1]):
+        hk.kv8_arrange(pool, back, back, parents=parents, caches=caches)
+    refs, table, held = [0] * pages, [[0] * width for _ in range(rows)], [0] * rows
+    rng = random.Random(7)
+    for _ in range(12):
+        k = [rng.randrange(0, h + 1) for h in held]
+        r = [min(width * page, x + rng.randrange(0, 40)) for x in k]
+        keep.copy_(_i32(k))
+        room.copy_(_i32(r))
+        graphs[0].replay()
+        refs, table, held, _, lack = ref.arrange(refs, table, held, k, r, None, page)
+        assert lack == 0 and pool.missing.item() == 0
+        p = [rng.randrange(rows) for _ in range(rows)]
+        b = [rng.randrange(0, held[x] + 1) for x in p]
+        back.copy_(_i32(b))
+        parents.copy_(_i32(p))
+        graphs[1].replay()
+        refs, table, held, _, lack = ref.arrange(refs, table, held, b, b, p, page)
+        assert pool.missing.item() == lack == 0
+        assert pool.refs.tolist() == refs and pool.held.tolist() == held
+        _same_rows(pool.table.tolist(), table, held, page)
+    assert _status_ok()
