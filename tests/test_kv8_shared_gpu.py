@@ -375,6 +375,37 @@ def test_repeats_exactly_on_streams_and_in_graphs(form):
     assert _status() == hk.HK_OK
 
 
+@FORMS
+def test_two_calls_at_once(form):
+    """Calls on two streams, and a GEMM on a third, beside one another."""
+    import torch
+    import dense_bf16_gemm_02_gb300 as hk
+    jobs = []
+    for seed, (groups, H, group, D) in enumerate((([(3000, [50] * 20)], 4, 8, 128), ([(900, [7, 2000, 60]), (1300, [5] * 30)], 2, 4, 64))):
+        batch = Batch(groups, H, D, 64, seed=seed)
+        q = _q(batch.B, 1, H * group, D)
+        same = dict(form=form, lengths=_i32(batch.lengths), offsets=_i32(batch.offsets), shared=_i32(batch.shared), wait=False)
+        jobs.append((batch, q, same, _attend(batch, q, form=form)))
+    a = torch.randn(2048, 2048, device="cuda").to(torch.bfloat16)
+    product = hk.gemm(a, a)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for (batch, q, same, _), stream in zip(jobs, streams):
+            with torch.cuda.stream(stream):
+                got.append(_attend(batch, q, **same))
+        with torch.cuda.stream(streams[2]):
+            got.append(hk.gemm(a, a))
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        if i % 3 == 2:
+            assert torch.equal(x, product)
+        else:
+            assert torch.equal(x[0], jobs[i % 3][3][0]) and torch.equal(x[1], jobs[i % 3][3][1])
+    assert _status() == hk.HK_OK
+
+
 def test_python_on_streams_and_in_graphs():
     """A size that each form takes by itself."""
     import torch
