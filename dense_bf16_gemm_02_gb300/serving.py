@@ -27,6 +27,7 @@ from .low_precision import (Kv8Cache, _check_vector, _empty, _f32, _i32, _read_o
 _pool_struct = struct.Struct("PPPqq4i").pack       # hk_kv8_pool
 _int32s = [struct.Struct(f"{n}i").pack for n in range(5)]
 _Tensor = torch.Tensor
+_is_capturing = torch.cuda.is_current_stream_capturing
 
 
 class Kv8Pool:
@@ -37,13 +38,13 @@ class Kv8Pool:
     attention_kv8 take; ``held`` int32 [rows]: tokens whose pages a row has.
     CUDA tensors; ``Kv8Pool.empty`` makes them, with nothing held. None of them can be
     set to another tensor. A pool also keeps the workspace of its arrangements (calls
-    on one pool follow one another anyway) and ``missing``, what the last one lacked."""
+    on one pool follow one another anyway) and ``missing``, what the last one lacked that
+    was not captured in a graph."""
 
     __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref", "_workspace", "_missing",
-                 "_workspace_ptr", "_workspace_size", "_missing_ptr")
+                 "_workspace_ptr", "_workspace_size")
     refs, table, held = (_read_only(n) for n in __slots__[:3])
     pages, rows, max_pages, page_size = (_read_only(n) for n in __slots__[3:7])
-    missing = _read_only("_missing")
 
     def __init__(self, refs, table, held, page_size=64):
         for t, dim in ((refs, 1), (table, 2), (held, 1)):
@@ -62,14 +63,20 @@ class Kv8Pool:
                                  rows, max_pages, page_size, 0)
         size = _hk.load().hk_kv8_arrange_workspace_size(self._ref)
         self._workspace = torch.empty(size, dtype=_u8, device=refs.device)
-        self._missing = torch.empty((), dtype=_i32, device=refs.device)
-        self._workspace_ptr, self._workspace_size, self._missing_ptr = self._workspace.data_ptr(), size, self._missing.data_ptr()
+        self._workspace_ptr, self._workspace_size = self._workspace.data_ptr(), size
+        self._missing = None
 
     @classmethod
     def empty(cls, pages, rows, max_pages, page_size=64, device="cuda"):
         """A pool of `pages` free pages and `rows` rows that hold nothing."""
         return cls(torch.zeros(pages, dtype=_i32, device=device), torch.zeros(rows, max_pages, dtype=_i32, device=device),
                    torch.zeros(rows, dtype=_i32, device=device), page_size)
+
+    @property
+    def missing(self):
+        if self._missing is None:            # (no call so far)
+            self._missing = torch.zeros((), dtype=_i32, device=self._refs.device)
+        return self._missing
 
 
 def _check_pool(pool):
@@ -97,9 +104,9 @@ def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=
     room above what a row holds takes pages, keep below it cuts the row back (0 ends
     it), another parent forks or reorders. Whole pages within keep are shared, the ones
     that will be written are the row's own: copied in each of ``caches`` where they hold
-    tokens. Returns ``pool.missing``, a 0-dim int32 tensor that the pool's next call
-    writes again: 0; or the pages that lacked, or -1 for arguments out of range, and then nothing was
-    changed. What a call frees is free for the next one. ``copies``: an int32 tensor [2, rows] that receives the copied pages and their
+    tokens. Returns a 0-dim int32 tensor of its own: 0; or the pages that lacked, or -1 for
+    arguments out of range, and then nothing was changed. What a call frees is free for the next
+    one. ``copies``: an int32 tensor [2, rows] that receives the copied pages and their
     copies (-1: none). See hk_kv8_arrange."""
     _check_pool(pool)
     rows = pool._rows
@@ -114,12 +121,15 @@ def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=
                                or tuple(copies.shape) != (2, rows) or not copies.is_contiguous()):
         raise TypeError("copies must be a contiguous int32 CUDA tensor [2, rows]")
     refs, n = _cache_refs(caches, "caches") if caches else (None, 0)
+    missing = _empty((), _i32, keep, stream)
     st = _hk.load().hk_kv8_arrange(pool._ref, keep.data_ptr(), room.data_ptr(), None if parents is None else parents.data_ptr(), refs,
-                                   n, None if copies is None else copies.data_ptr(), pool._missing_ptr, pool._workspace_ptr,
+                                   n, None if copies is None else copies.data_ptr(), missing.data_ptr(), pool._workspace_ptr,
                                    pool._workspace_size, _stream(stream, keep))
     if st != HK_OK:
         raise HKError(st, "hk_kv8_arrange")
-    return pool._missing
+    if not _is_capturing():
+        pool._missing = missing
+    return missing
 
 
 def kv8_compact(pool: Kv8Pool, caches=(), stream=None):
