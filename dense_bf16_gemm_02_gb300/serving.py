@@ -27,7 +27,7 @@ from .low_precision import (Kv8Cache, _check_vector, _empty, _f32, _i32, _read_o
 _pool_struct = struct.Struct("PPPqq4i").pack       # hk_kv8_pool
 _int32s = [struct.Struct(f"{n}i").pack for n in range(5)]
 _Tensor = torch.Tensor
-_is_capturing = torch.cuda.is_current_stream_capturing
+_is_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 class Kv8Pool:
@@ -37,12 +37,12 @@ class Kv8Pool:
     ``table`` int32 [rows, max_pages]: the block table that kv8_append and
     attention_kv8 take; ``held`` int32 [rows]: tokens whose pages a row has.
     CUDA tensors; ``Kv8Pool.empty`` makes them, with nothing held. None of them can be
-    set to another tensor. A pool also keeps the workspace of its arrangements (calls
-    on one pool follow one another anyway) and ``missing``, what the last one lacked that
-    was not captured in a graph."""
+    set to another tensor. The object itself may be dropped while work on its tensors is under way or
+    captured (the tensors have to live, as any that a kernel works on). ``missing``: what the last
+    arrangement lacked that was not captured in a graph."""
 
-    __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref", "_workspace", "_missing",
-                 "_workspace_ptr", "_workspace_size")
+    __slots__ = ("_refs", "_table", "_held", "_pages", "_rows", "_max_pages", "_page_size", "_ref", "_missing", "_workspace",
+                 "_workspace_stream", "_workspace_size")
     refs, table, held = (_read_only(n) for n in __slots__[:3])
     pages, rows, max_pages, page_size = (_read_only(n) for n in __slots__[3:7])
 
@@ -61,10 +61,8 @@ class Kv8Pool:
         self._pages, self._rows, self._max_pages, self._page_size = refs.size(0), rows, max_pages, page_size
         self._ref = _pool_struct(refs.data_ptr(), table.data_ptr(), held.data_ptr(), refs.size(0), _row_stride(table, "table"),
                                  rows, max_pages, page_size, 0)
-        size = _hk.load().hk_kv8_arrange_workspace_size(self._ref)
-        self._workspace = torch.empty(size, dtype=_u8, device=refs.device)
-        self._workspace_ptr, self._workspace_size = self._workspace.data_ptr(), size
-        self._missing = None
+        self._workspace_size = _hk.load().hk_kv8_arrange_workspace_size(self._ref)
+        self._missing = self._workspace = self._workspace_stream = None
 
     @classmethod
     def empty(cls, pages, rows, max_pages, page_size=64, device="cuda"):
@@ -122,12 +120,23 @@ def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=
         raise TypeError("copies must be a contiguous int32 CUDA tensor [2, rows]")
     refs, n = _cache_refs(caches, "caches") if caches else (None, 0)
     missing = _empty((), _i32, keep, stream)
+    raw, captured = _stream(stream, keep), _is_capturing()
+    # The pool keeps a workspace for the stream that it is used on: calls there follow one another, and when the pool is dropped
+    # the memory is free for what comes after them on that stream. For another stream, or in a graph, which may
+    # run when the pool is gone, it is the call's own.
+    if stream is None and not captured and pool._workspace_stream in (None, raw):
+        workspace = pool._workspace
+        if workspace is None:
+            workspace = pool._workspace = _empty(pool._workspace_size, _u8, keep, None)
+            pool._workspace_stream = raw
+    else:
+        workspace = _empty(pool._workspace_size, _u8, keep, stream)
     st = _hk.load().hk_kv8_arrange(pool._ref, keep.data_ptr(), room.data_ptr(), None if parents is None else parents.data_ptr(), refs,
-                                   n, None if copies is None else copies.data_ptr(), missing.data_ptr(), pool._workspace_ptr,
-                                   pool._workspace_size, _stream(stream, keep))
+                                   n, None if copies is None else copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(),
+                                   pool._workspace_size, raw)
     if st != HK_OK:
         raise HKError(st, "hk_kv8_arrange")
-    if not _is_capturing():
+    if not captured:
         pool._missing = missing
     return missing
 
