@@ -124,8 +124,9 @@ extern "C" hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], 
     p.in[1] = K;
     p.out[0] = QO;
     p.out[1] = KO;
-    p.weight[0] = q_weight;
-    p.weight[1] = k_weight;
+    p.norm = eps >= 0.0f;
+    p.weight[0] = p.norm ? q_weight : nullptr;       // (the weights are the norm's)
+    p.weight[1] = p.norm ? k_weight : nullptr;
     const int64_t* strides[4] = {q_strides, k_strides, qo_strides, ko_strides};
     for (int op = 0; op < 2; ++op) {
         if ((op ? Hk : Hq) == 0) continue;
@@ -150,7 +151,6 @@ extern "C" hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], 
     p.D = static_cast<int32_t>(D);
     p.half = static_cast<int32_t>(pairs);
     p.eps = eps;
-    p.norm = eps >= 0.0f;
     p.weight_f32 = weight_type == HK_TYPE_FP32;
     const int lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32;
     for (int op = 0; op < 2; ++op) p.op_steps[op] = (p.heads[op] + 32 / lanes - 1) / (32 / lanes);

@@ -203,7 +203,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     q [B, T, Hq, D], k [B, T, Hk, D] (bf16, fp16 or fp32; any strides with contiguous rows),
     ``positions`` int32 [B, T], or [axes, B, T] with ``sections``: the numbers of successive
     pairs that turn by each axis. ``inv_freq`` float32 [R/2]. Weights [D] of q's type or
-    float32, both alike; None: 1. eps None: no norm. ``out``: (q', k') to write into, q and k
+    float32, both alike; None: 1. eps None: no norm and no weights. ``out``: (q', k') to write into, q and k
     themselves among others. Returns (q', k'). See hk_qk_norm_rope."""
     (B, T, Hq, D), qs = _heads(q, "q")
     (kB, kT, Hk, kD), ks = _heads(k, "k")

@@ -653,7 +653,7 @@ size_t hk_attention_kv8_shared_workspace_size_ex(const void* Q, int32_t type, co
  * head) in elements and contiguous rows; an output may be its input (then with its strides), else it must
  * not overlap one, and its rows must not overlap. Hq or Hk 0 leaves that operand out. D a multiple of 8 up to
  * 256, pairs a multiple of 8. q_weight, k_weight [D] of `type` or fp32 (weight_type), NULL: 1. eps < 0: no
- * norm (and no weights). positions: int32 on the device with strides (axis, b, t) in elements;
+ * norm and no weights (they are not read). positions: int32 on the device with strides (axis, b, t) in elements;
  * inv_freq: fp32 [pairs] on the device, of magnitude below 2^10 (above, bits of the angle are lost; not
  * finite: NaN).
  * The norm is summed in fp32, t is exact to 2^-31 of a turn whatever the position (for
