@@ -160,7 +160,18 @@ __device__ __forceinline__ int plan_sections(const SharedParams& p, int32_t* fir
         bad = bad || (g0 + j == p.G && first != p.all);
         first_of[j] = first;
     }
+    auto off = [&](int j) {                  // (of groups that this launch does not plan for)
+        const int next = p.groups[j + 1];
+        return !group_in_order(p, j, p.groups[j], next, p.shared[j]) || (j + 1 == p.G && next != p.all);
+    };
+    // The kernels for units of 128 rows and for own parts look at every group, and what is shared has to be the same to all three.
+    // Groups that are too many for that are looked at once, a part by each block of the first launch, so as to be reported.
+    if (p.wide_runs > 0)
+        for (int j = t; j < g0; j += kThreads) bad = bad || off(j);
     if (bad) atomicOr(p.wait.status, kErrPage);
+    if (p.b0 == 0)
+        for (int64_t j = groups + static_cast<int64_t>(blockIdx.x) * kThreads + t; j < p.G; j += static_cast<int64_t>(gridDim.x) * kThreads)
+            if (off(static_cast<int>(j))) atomicOr(p.wait.status, kErrPage);
     if (__syncthreads_or(bad)) {
         for (int j = t; j < groups; j += kThreads) tiles_of_group[j] = 0;
         __syncthreads();

@@ -611,8 +611,9 @@ hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, in
  * order of its fp32 sums (and, for the tensor-core kernel, the rounding of weights where pages' scales of values differ by
  * more than 2^7: to bf16, 2^-8, instead of f16, 2^-11). Not shared in
  * fact, and read by a sequence itself, are tokens past the first sequence's length, and those of a
- * sequence that has queries which do not see all of them. Where groups are out of order or range, every sequence
- * reads all its tokens itself and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG.
+ * sequence that has queries which do not see all of them. Where groups are out of order or range, sequences
+ * read all their tokens themselves (but, in a batch of several launches, those of few-row launches whose own groups
+ * are in order) and hk_gemm_last_device_status reports HK_ERR_INVALID_ARG.
  * By the sizes that the host knows the call runs on a tensor-core kernel for what is shared (rows of Q that are
  * 16-byte aligned, up to 64 groups), on few-row kernels, or, where
  * reading everything for each sequence costs less (few sequences, short tables, 1024 query rows of a sequence and KV head or
