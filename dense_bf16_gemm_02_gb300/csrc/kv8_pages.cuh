@@ -452,7 +452,7 @@ kv8_copy_pages_kernel(const CopyParams p) {
         const int64_t entry = steps <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(item) / per_entry) : item / per_entry;
         uint32_t rest = static_cast<uint32_t>(item - entry * per_entry);
         const int32_t src = __ldcg(p.src + entry), dst = __ldcg(p.dst + entry);
-        if (src < 0 && dst < 0) continue;
+        if (src == -1 && dst == -1) continue;
         if (src < 0 || src >= p.src_pages || dst < 0 || dst >= p.dst_pages) {
             if (lane == 0) atomicOr(p.status, kErrPage);
             continue;
