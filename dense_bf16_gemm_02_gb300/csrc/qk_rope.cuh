@@ -16,9 +16,9 @@
 // (position 10^6: an error of 0.06 radians). Here the frequency is taken as the
 // turns per position, inv_freq / 2 pi, in fixed point with 64 bits behind the
 // point: 24 bits of mantissa times a 64-bit 1 / 2 pi, shifted. Times the
-// position modulo 2^64 that is the fraction of a turn to within 2^-33 whatever
-// the position is (whole turns fall out at the top), for a handful of integer
-// multiplications; its top 32 bits, signed, go to fp32 and to sincospi.
+// position modulo 2^64 that is the fraction of a turn to within 2^-32.4 whatever
+// the position is (for frequencies up to 1; whole turns fall out at the top), for a handful of integer
+// multiplications; its top 32 bits, signed, go to fp32, which rounds them by up to 2^-26 of a turn, and to sincospi.
 //
 // Measured: 16384 tokens of 72 heads of 128 in bf16 106 us, 5.7 TB/s read and written, 0.84 of a copy's rate (half the issue slots
 // are taken; a test at each load, which made the loads wait for one another, took 256 us, 64-bit divisions to find rows 135, clamped

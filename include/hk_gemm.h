@@ -657,7 +657,8 @@ size_t hk_attention_kv8_shared_workspace_size_ex(const void* Q, int32_t type, co
  * norm and no weights (they are not read). positions: int32 on the device with strides (axis, b, t) in elements;
  * inv_freq: fp32 [pairs] on the device, of magnitude below 2^10 (above, bits of the angle are lost; not
  * finite: NaN).
- * The norm is summed in fp32, t is exact to 2^-31 of a turn whatever the position (for
+ * The norm is summed in fp32 (elements whose squares pass its range, above 10^19, make a row of zeros), t is
+ * reduced to 2^-31 of a turn and then rounded to fp32, at most 2^-25.9 of a turn off whatever the position (for
  * frequencies up to 1), and the result is rounded once.
  * Asynchronous on `stream`, allocates nothing. */
 hk_status hk_qk_norm_rope(const void* Q, const int64_t q_strides[3], const void* K, const int64_t k_strides[3],
