@@ -21,12 +21,13 @@ import torch
 
 from . import hk_gemm as _hk
 from .hk_gemm import HK_OK, HKError
-from .low_precision import (Kv8Cache, _check_vector, _empty, _f32, _i32, _read_only, _row_stride, _stream, _strides, _table,
+from .low_precision import (Kv8Cache, _check_vector, _empty, _f32, _i32, _raw_stream, _read_only, _row_stride, _stream, _strides, _table,
                             _tokens_shape, _type_code, _u8)
 
 _pool_struct = struct.Struct("PPPqq4i").pack       # hk_kv8_pool
 _int32s = [struct.Struct(f"{n}i").pack for n in range(5)]
 _Tensor = torch.Tensor
+_verdicts = {}       # (device, stream) -> what is left of the last 64
 _is_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
@@ -94,6 +95,20 @@ def _cache_refs(caches, name):
     return b"".join(refs), len(refs)
 
 
+def _verdict(like, raw):
+    """A 0-dim int32 tensor that no call has had before, on the device's current stream `raw`. Made 64 at a time: a tensor made
+    between launches costs its call 5 us on the GPU's host (as much as the launches), one of 64 less than one."""
+    key = like.get_device(), raw
+    try:
+        return _verdicts[key].pop()
+    except (KeyError, IndexError):
+        with torch.inference_mode(False):    # (an ordinary tensor wherever the first of them is asked for)
+            some = list(torch.empty(64, dtype=_i32, device=like.device).unbind())
+        verdict = some.pop()
+        _verdicts[key] = some
+        return verdict
+
+
 def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=None, stream=None):
     """Arrange the pool's rows anew, all at once: row i becomes the first ``keep[i]``
     tokens of what row ``parents[i]`` was (None: of its own), with pages for
@@ -119,18 +134,24 @@ def kv8_arrange(pool: Kv8Pool, keep, room=None, parents=None, caches=(), copies=
                                or tuple(copies.shape) != (2, rows) or not copies.is_contiguous()):
         raise TypeError("copies must be a contiguous int32 CUDA tensor [2, rows]")
     refs, n = _cache_refs(caches, "caches") if caches else (None, 0)
-    missing = _empty((), _i32, keep, stream)
-    raw, captured = _stream(stream, keep), _is_capturing()
     # The pool keeps a workspace for the stream that it is used on: calls there follow one another, and when the pool is dropped
-    # the memory is free for what comes after them on that stream. For another stream, or in a graph, which may
+    # the memory is free for what comes after them on that stream. For a stream that is given, or in a graph, which may
     # run when the pool is gone, it is the call's own.
-    if stream is None and not captured and pool._workspace_stream in (None, raw):
-        workspace = pool._workspace
-        if workspace is None:
-            workspace = pool._workspace = _empty(pool._workspace_size, _u8, keep, None)
-            pool._workspace_stream = raw
+    if stream is None:
+        raw = _raw_stream(keep.get_device())
+        captured = raw != 0 and _is_capturing()          # (the default stream cannot be)
     else:
-        workspace = _empty(pool._workspace_size, _u8, keep, stream)
+        raw = int(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            captured = _is_capturing()
+    if stream is None and not captured:
+        missing, workspace = _verdict(keep, raw), pool._workspace
+        if workspace is None or pool._workspace_stream != raw:
+            workspace = _empty(pool._workspace_size, _u8, keep, None)
+            if pool._workspace is None:
+                pool._workspace, pool._workspace_stream = workspace, raw
+    else:
+        missing, workspace = _empty((), _i32, keep, stream), _empty(pool._workspace_size, _u8, keep, stream)
     st = _hk.load().hk_kv8_arrange(pool._ref, keep.data_ptr(), room.data_ptr(), None if parents is None else parents.data_ptr(), refs,
                                    n, None if copies is None else copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(),
                                    pool._workspace_size, raw)

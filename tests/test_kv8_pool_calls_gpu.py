@@ -52,3 +52,21 @@ def test_a_pool_says_what_its_last_call_lacked():
         hk.kv8_arrange(other, _i32([0]))
         assert pool.missing is got and got.item() == lack
         hk.kv8_arrange(pool, _i32([0]))
+
+
+@pytest.mark.parametrize("inference", [False, True])
+def test_verdicts_are_each_calls_own(inference):
+    """More calls than verdicts are made at a time, on two streams, all of them kept."""
+    import torch
+    import dense_bf16_gemm_02_gb300 as hk
+    side, got = torch.cuda.Stream(), []
+    for i in range(200):
+        with torch.inference_mode(inference), torch.cuda.stream(side if i % 3 == 0 else torch.cuda.current_stream()):
+            pool = hk.Kv8Pool.empty(4, 1, 300, 16)
+            got.append(hk.kv8_arrange(pool, _i32([0]), _i32([16 * (4 + i)])))
+    torch.cuda.synchronize()
+    assert len({t.data_ptr() for t in got}) == 200
+    assert [t.item() for t in got] == list(range(200))
+    got[0].add_(5)                                       # (ordinary tensors, wherever they come from)
+    got[1].add_(got[0])
+    assert got[1].item() == 6 and [t.item() for t in got[2:]] == list(range(2, 200))
