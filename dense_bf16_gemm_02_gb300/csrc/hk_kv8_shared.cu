@@ -90,7 +90,8 @@ enum Form { kOwn, kFew, kWide };
 
 // Query rows of a sequence and KV head from which attention_kv8's own tiles are full and it takes the call. Both sides
 // (tensor-core kernel here, attention_kv8), 8 KV heads of 128, in microseconds: 1024 rows, 8 sequences behind 2048, 8192 and
-// 32768 tokens 260 and 108, 483 and 294, 1417 and 1523; 512 rows 141 and 69, 253 and 180, 714 and 1515.
+// 32768 tokens 260 and 108, 483 and 294, 1417 and 1523; 512 rows 141 and 69, 253 and 180, 714 and 1515. All in bf16: fp16 rows are then
+// attention_kv8's few-row kernels', which take several times as long (include/hk_gemm.h), and were not measured against this form.
 constexpr int64_t kOwnTileRows = 1024;
 
 // By an estimate of the three times in microseconds, with the table's width for the lengths (which the host does not know) and
@@ -101,7 +102,9 @@ constexpr int64_t kOwnTileRows = 1024;
 // 300 tokens of their own): 8 behind 2048 tokens 14, 25, 30; 8 behind 8192 30, 32, 33; 16 behind 8192 52, 47, 36;
 // 64 behind 2048 56, 67, 42; 64 behind 32768 548, 409, 107. 32 KV heads of a query head each: 16 behind 500 20, 22, 32;
 // 16 behind 8192 153, 54, 54; 16 behind 32768 560, 87, 102. Head dimension 64: 16 behind 2048 14, 22, 26; 16 behind 8192 40, 34, 29;
-// 64 of 16 query heads behind 4096 (their own tiles are full) 43, 54. It errs where two are near: 4 behind 32768 52, 50, 44.
+// 64 of 16 query heads behind 4096 (their own tiles are full) 43, 54. It errs where two are near: 4 behind 32768 52, 50, 44 (it
+// takes the second). All in bf16 with aligned rows and tables as wide as the sequences: fp16 and other rows go by the same figures, and where
+// the table is much wider the estimates are of more tokens than there are (8 behind 2048 tokens in a table of 131072: the third, 30 for 14).
 Form choose(const hk_kv8_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_pages, int64_t G, bool wide, bool many) {
     const int64_t group = Hq / c->heads;
     if (T * group >= kOwnTileRows || launch_batch(B, T, Hq) < 2) return kOwn;

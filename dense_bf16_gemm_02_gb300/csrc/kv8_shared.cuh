@@ -18,7 +18,8 @@
 // one order, cut into equal runs, one per warp, whatever the lengths are; sums of units that
 // are split, and of sequences with a shared part, go through memory and are added up by a second
 // kernel, in order. Without a shared part a whole unit is finished at once. Tiles bound it: 16 rows by 32 tokens
-// some 1 us of a warp whatever its rows hold, 45 sequences in 6 groups behind 5003 tokens (28/4 heads of 64, fp16) 33 to 39 us.
+// some 1 us of a warp whatever its rows hold, 45 sequences in 6 groups behind 5003 tokens (28/4 heads of 64, fp16) 33 to 39 us
+// (255 registers a thread; at head dimension 128 the compiler spills 64 bytes).
 // Where the shared units run on the tensor-core kernel (kv8_shared_mma.cuh), what sequences have of their own is
 // mostly short, and a block to a unit is quicker: no plan over all lengths before the first load, and
 // the unit's warps load at the same time; only units of more than `own_limit` tiles are spread.

@@ -20,10 +20,13 @@
 // unit's run has seen, and a page's values are multiplied by what its scale is of it, down to 2^-14, exactly. Blocks with
 // pages below that, or 2^7 above the first block's unit, have values and weights in bf16 (each code's bits
 // moved to where bf16 has them, times 2^120, which E4M3's exponent bias is less): f16 weights hold down to 2^-31 of the largest, and
-// values that are much larger than others would make what lies below count.
+// values that are much larger than others would make what lies below count. They have their 11 bits down to 2^-21 of it (kv8_decode.cuh,
+// whose maximum is never behind: 2^-29), since a maximum that may be 2^8 behind leaves 2^7 for the shift: with 2^4 and 2^11, which would
+// hold 2^-25, 64 sequences behind 16384 tokens take 75 us (75) and 128 behind 32768 207 (205), with 2^2 and 2^13 77 and 210.
+// At the launch's 128 registers a thread the compiler spills 46 bytes.
 //
 // Measured: 56 us for 64 sequences of 64 query heads (8 KV heads of 128) behind 16384 tokens, 153 us for 128 behind 32768
-// (914 TFLOP/s, 0.48 of the 1917 measured for large GEMMs; tensor pipe 37 % busy, DRAM 6 %): some 2300 cycles for a
+// (898 TFLOP/s, 0.47 of the 1917 measured for large GEMMs; tensor pipe 37 % busy, DRAM 6 %): some 2300 cycles for a
 // block of 128 x 128, of which the MMAs take 1080, and some 20 us to start, fill and drain. With conversions, exponentials,
 // packing and maxima all left out it is 1950, with the MMAs too 1800: what is left is the chain from S through the softmax's loads and
 // stores of Tensor Memory to P·V. One producing warp, which waited for each look-up of pages, bound it at 2900. What was tried (us of a

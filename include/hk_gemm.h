@@ -608,8 +608,9 @@ hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, in
  * to B, strictly increasing); the first shared[g] tokens (int32 [G] on the device) of each of them lie in the same pages,
  * which every sequence's own table row names too. They are read once, by the first sequence's row, as far as they fill whole
  * blocks of 128 tokens. shared[g] = 0, and groups of one sequence, are fine. The result is hk_attention_kv8's, but for the
- * order of its fp32 sums (and, for the tensor-core kernel, the rounding of weights where pages' scales of values differ by
- * more than 2^7: to bf16, 2^-8, instead of f16, 2^-11). Not shared in
+ * order of its fp32 sums and, on the tensor-core kernel, the rounding of weights: in f16 they are 2^-11 of a weight down to 2^-21
+ * of the row's largest so far, and 2^-32 of that below (2^-29 and 2^-40 in hk_attention_kv8); where pages' scales of values
+ * differ by more than 2^7 they are bf16, 2^-8, for fp16 queries too. Not shared in
  * fact, and read by a sequence itself, are tokens past the first sequence's length, and those of a
  * sequence that has queries which do not see all of them. Where groups are out of order or range, sequences
  * read all their tokens themselves (but, in a batch of several launches, those of few-row launches whose own groups
@@ -617,7 +618,9 @@ hk_status hk_kv8_copy_pages(const hk_kv8_cache* dst, const hk_kv8_cache* src, in
  * By the sizes that the host knows the call runs on a tensor-core kernel for what is shared (rows of Q that are
  * 16-byte aligned, up to 64 groups), on few-row kernels, or, where
  * reading everything for each sequence costs less (few sequences, short tables, 1024 query rows of a sequence and KV head or
- * more), as hk_attention_kv8, which does not look at the groups.
+ * more), as hk_attention_kv8, which does not look at the groups. The table's width stands for the lengths there: a table much wider than
+ * the sequences can make a small call take the form of a large one. A launch of up to 512 sequences counts its tiles of 32 tokens
+ * (sequences · KV heads · what the table has room for) in 31 bits; a wider table is HK_ERR_INVALID_ARG.
  * `workspace`: device memory of hk_attention_kv8_shared_workspace_size bytes (up to 44 MB and 8 · head_dim bytes for
  * each of up to 2^17 query rows, or what hk_attention_kv8 needs), 256-byte aligned. Everything else as hk_attention_kv8. */
 hk_status hk_attention_kv8_shared(const void* Q, int32_t type, const int64_t q_strides[3], const hk_kv8_cache* cache,
